@@ -18,3 +18,8 @@ from ._binding import (  # noqa: F401
     gq_norm_finish, gq_norm_partial, gq_philox4x32_10, gq_quantize,
     gq_quantize_codes, gq_quantize_sum, gq_quantize_ws, gq_reduce_codes, gq_selftest_wait_timeout,
     gq_status_string, gq_workspace, gq_workspace_bytes, lib, library_path)
+from ._activations import (  # noqa: F401
+    ACT_NEAREST, ACT_RANDOM, GELU_ERF, GELU_TANH, Act8, gq_act_dequantize, gq_act_exp_pitch,
+    gq_act_quantize, gq_gelu_backward, gq_gelu_forward, gq_layernorm_backward,
+    gq_layernorm_forward, gq_layernorm_workspace_bytes, gq_linear_wgrad,
+    gq_linear_wgrad_workspace_bytes)

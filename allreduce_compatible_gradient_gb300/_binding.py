@@ -79,6 +79,19 @@ def lib() -> ctypes.CDLL:
         "gq_exp_dequantize": (ci, [vp, i64, vp, ci, i64, vp, ci, vp]),
         "gq_status_string": (ctypes.c_char_p, [ci]),
         "gq_debug_status": (ci, []),
+        "gq_act_exp_pitch": (i64, [i64]),
+        "gq_act_quantize": (ci, [vp, ci, i64, i64, i64, ci, u64, u64, vp, vp, vp]),
+        "gq_act_dequantize": (ci, [vp, vp, i64, i64, vp, ci, i64, vp]),
+        "gq_layernorm_forward": (ci, [vp, ci, i64, i64, i64, vp, vp, ci, ctypes.c_float, vp, i64, vp,
+                                      vp, ci, u64, u64, vp, vp, vp]),
+        "gq_layernorm_workspace_bytes": (sz, [i64, i64]),
+        "gq_layernorm_backward": (ci, [vp, ci, i64, i64, i64, vp, ci, vp, vp, vp, vp, i64, vp, vp,
+                                       i64, vp, vp, ci, vp, sz, vp]),
+        "gq_gelu_forward": (ci, [vp, ci, i64, i64, i64, ci, vp, i64, ci, u64, u64, vp, vp, vp]),
+        "gq_gelu_backward": (ci, [vp, ci, i64, i64, i64, vp, vp, ci, vp, i64, vp, i64, vp]),
+        "gq_linear_wgrad_workspace_bytes": (sz, [vp, ci, i64, i64, i64, i64]),
+        "gq_linear_wgrad": (ci, [vp, ci, i64, i64, i64, vp, vp, i64, vp, vp, vp, ci, i64, vp, vp, sz,
+                                 vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

@@ -1,10 +1,11 @@
 """Compile the CUDA library (csrc/*.cu over csrc/gq_kernels.cuh) into libgq.so, in-tree.
 
-Five translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
-gradient type and scheme) compiled in parallel with one -gencode (sm_103a), then linked with the
-static CUDA runtime: the library depends on nothing but the driver at load time.  -fmad=false
-keeps every fp32 operation a separately rounded IEEE operation (the rounding decisions must be
-bit-identical to their definition).
+Eight translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
+gradient type and scheme; the activation kernels) compiled in parallel with one -gencode
+(sm_103a), then linked with the static CUDA runtime: the library depends on nothing but the driver
+at load time.  -fmad=false keeps every fp32 operation of the gradient path a separately rounded
+IEEE operation (its rounding decisions must be bit-identical to their definition); the activation
+units are compiled with contraction, and spell out the roundings that their codes depend on.
 """
 from __future__ import annotations
 
@@ -17,7 +18,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 UNITS = ["gq.cu", "gq_quant_f32_l.cu", "gq_quant_f32_e.cu", "gq_quant_bf16_l.cu",
-         "gq_quant_bf16_e.cu"]
+         "gq_quant_bf16_e.cu", "gq_act.cu", "gq_layernorm.cu", "gq_wgrad.cu"]
+CONTRACTED = {"gq_act.cu", "gq_layernorm.cu", "gq_wgrad.cu"}
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgq.so")
 # the same library with the kernels' bounds checks compiled in (-DGQ_DEBUG)
@@ -38,7 +40,8 @@ def nvcc() -> str:
 
 
 def compile_command(unit: str, obj: str, extra=()) -> list:
-    return [nvcc(), ARCH, "-O3", "-lineinfo", "-fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
+    fmad = "-fmad=true" if unit in CONTRACTED else "-fmad=false"
+    return [nvcc(), ARCH, "-O3", "-lineinfo", fmad, "-std=c++17", "-Xcompiler", "-fPIC",
             "-I" + os.path.join(ROOT, "include"), *extra, "-c", "-o", obj,
             os.path.join(CSRC, unit)]
 

@@ -1,0 +1,344 @@
+// gq_act.cuh -- device and host pieces shared by the activation kernels (gq_act.cu,
+// gq_layernorm.cu, gq_wgrad.cu): element access, the 8-bit block format and its two roundings.
+//
+// Format: a row of `cols` elements is cut into blocks of 32 columns.  A block with largest
+// magnitude a has the exponent byte E = min{ E >= 1 : a <= 127 * 2^(E - 127) }, 255 if it holds
+// a NaN, an infinity or a magnitude above 127 * 2^121 (its codes are then 0 and it reads back as
+// NaN: 0 * 2^128); an element stands for code * 2^(E - 127).  A power-of-two step costs at most one bit against a free step
+// (the code of the block's largest element lies in 64..127) and makes every value, 7 bits times
+// a power of two, exact in bf16: what reads a checkpoint rounds nothing.
+#pragma once
+#include "gq.h"
+#include "gq_host.cuh"
+#include "gq_kernels.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace gqa {
+
+constexpr int kBlk = 32;         // columns of one exponent
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+// Random words of a launch: the Philox round keys of the seed, and the step.
+struct Rng {
+    uint32_t rk[20];
+    uint32_t step_lo, step_hi;
+};
+
+inline Rng make_rng(uint64_t seed, uint64_t step) {
+    Rng r;
+    const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    for (int i = 0; i < 10; ++i) {
+        r.rk[2 * i] = k0 + static_cast<uint32_t>(i) * 0x9E3779B9u;
+        r.rk[2 * i + 1] = k1 + static_cast<uint32_t>(i) * 0xBB67AE85u;
+    }
+    r.step_lo = static_cast<uint32_t>(step);
+    r.step_hi = static_cast<uint32_t>(step >> 32);
+    return r;
+}
+
+inline int64_t code_pitch(int64_t cols) { return (cols + 31) / 32 * 32; }
+inline int64_t exp_pitch(int64_t cols) { return ((cols + 31) / 32 + 15) / 16 * 16; }
+
+// n / d for n < 2^31 by a multiplication: m = ceil(2^(31 + l) / d), l = ceil(log2 d) >= 1; the
+// excess m d - 2^(31 + l) is below 2^l, so its contribution n * excess stays below 2^(31 + l).
+struct Div {
+    uint32_t d, m, s;
+};
+inline Div make_div(uint32_t d) {  // d >= 2
+    uint32_t l = 1;
+    while ((uint64_t(1) << l) < d) ++l;
+    return Div{d, static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t quot(uint32_t n, const Div& v) { return __umulhi(n, v.m) >> v.s; }
+
+// ---- elements ------------------------------------------------------------------------------
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float up(float v) { return v; }
+__device__ __forceinline__ float up(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void down(float v, float& o) { o = v; }
+__device__ __forceinline__ void down(float v, bf16& o) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void down(float v, __half& o) { o = __float2half_rn(v); }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bf16) {
+    __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&t);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+    __half2 t = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&t);
+}
+
+// 32 bytes in one access (sm_100 and later), or two 16-byte ones where rows are only 16-byte
+// aligned.
+template <int ALIGN>
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
+    if constexpr (ALIGN == 32) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(static_cast<const uint4*>(p));
+        const uint4 b = __ldg(static_cast<const uint4*>(p) + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+}
+template <int ALIGN>
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+    if constexpr (ALIGN == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// V consecutive elements starting at column c of the row at p, widened to fp32; columns at and
+// past `cols` read as 0.  V = 1: one element.  V = 8 or 16: p + c is ALIGN-byte aligned.
+template <typename T, int V, int ALIGN>
+__device__ __forceinline__ void load(const T* p, int64_t c, int64_t cols, float (&v)[V]) {
+    if constexpr (V > 1) {
+        if (c + V <= cols) {
+            if constexpr (sizeof(T) == 4) {
+                if constexpr (V * 4 >= 32) {
+#pragma unroll
+                    for (int k = 0; k < V / 8; ++k) {
+                        uint32_t w[8];
+                        ld32<ALIGN>(p + c + 8 * k, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[8 * k + i] = __uint_as_float(w[i]);
+                    }
+                }
+            } else if constexpr (V == 16) {
+                uint32_t w[8];
+                ld32<ALIGN>(p + c, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            } else {
+                const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + c));
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = c + i < cols ? up(p[c + i]) : 0.0f;
+}
+
+template <typename T, int V, int ALIGN>
+__device__ __forceinline__ void store(T* p, int64_t c, int64_t cols, const float (&v)[V]) {
+    if constexpr (V > 1) {
+        if (c + V <= cols) {
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int k = 0; k < V / 8; ++k) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * k + i]);
+                    st32<ALIGN>(p + c + 8 * k, w);
+                }
+            } else if constexpr (V == 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], T());
+                st32<ALIGN>(p + c, w);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], T());
+                *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (c + i < cols) down(v[i], p[c + i]);
+}
+
+// ---- the 8-bit block format ----------------------------------------------------------------
+
+// Largest magnitude of the 32-column block that 32 / V neighbouring lanes hold, as fp32 bits
+// (which order like the magnitudes, with NaN above infinity).  Every lane of the warp calls it.
+template <int V>
+__device__ __forceinline__ uint32_t block_top(const float (&v)[V]) {
+    uint32_t m = __float_as_uint(v[0]) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    if constexpr (V == 1) {
+        m = __reduce_max_sync(kFull, m);
+    } else {
+#pragma unroll
+        for (int o = 1; o < kBlk / V; o *= 2) m = max(m, __shfl_xor_sync(kFull, m, o));
+    }
+    return m;
+}
+
+// The exponent byte: with a = 1.f * 2^k, a <= 127 * 2^(k - 6) iff 1.f <= 127 / 64, that is iff
+// the fraction field is at most 0x7E0000; adding 0x1FFFF carries into the exponent otherwise.
+__device__ __forceinline__ uint32_t exp_byte(uint32_t top) {
+    const int e = static_cast<int>((top + 0x1FFFFu) >> 23) - 6;
+    return top > 0x7F7E0000u ? 255u : static_cast<uint32_t>(max(e, 1));
+}
+// 2^(127 - E): exact, normal for 1 <= E <= 248 (the largest that a block not marked has).
+__device__ __forceinline__ float inv_step(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+// 2^(E - 127); infinity for E = 255.
+__device__ __forceinline__ float step_of(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Bytes B of a, b, c, d as one word.
+template <int B>
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    constexpr uint32_t sel = B | ((4 + B) << 4);
+    return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
+}
+
+// Codes of V elements (V = 1: in the low byte).  Nearest: x / step + 1.5 * 2^23 leaves the integer
+// nearest to x / step, ties to even, in the low byte (one rounding, the product is exact).
+// Random: x / step * 2^16 + 1.5 * 2^24 keeps 128 + x / step in units of 2^-15 in the fraction;
+// doubled and increased by the 16-bit random number, bits 16..23 hold floor(128 + x / step + u).
+// c is the element's column (a multiple of V), row its row.
+template <int V, bool RANDOM>
+__device__ __forceinline__ void codes_of(const float (&v)[V], uint32_t e, uint32_t row, uint32_t c,
+                                         const Rng& rng, uint32_t (&w)[(V + 3) / 4]) {
+    const float inv = inv_step(e);
+    uint32_t t[V];
+    if constexpr (RANDOM) {
+#pragma unroll
+        for (int g = 0; g < (V + 7) / 8; ++g) {
+            const uint4 r = gq::philox4x32_10_rk(
+                make_uint4((c >> 3) + g, row, rng.step_lo, rng.step_hi), rng.rk);
+            const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+            if constexpr (V == 1) {
+                const uint32_t q = (c & 4) ? ((c & 2) ? r.w : r.z) : ((c & 2) ? r.y : r.x);
+                const uint32_t h = (c & 1) ? q >> 16 : q & 0xFFFFu;
+                t[0] = (__float_as_uint(__fmaf_rn(v[0] * inv, 65536.0f, 25165824.0f)) << 1) + h;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t h = (i & 1) ? word[i >> 1] >> 16 : word[i >> 1] & 0xFFFFu;
+                    t[8 * g + i] = (__float_as_uint(__fmaf_rn(v[8 * g + i] * inv, 65536.0f,
+                                                              25165824.0f)) << 1) + h;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = __float_as_uint(__fmaf_rn(v[i], inv, 12582912.0f));
+    }
+    constexpr int B = RANDOM ? 2 : 0;
+    constexpr uint32_t flip = RANDOM ? 0x80808080u : 0u;
+    if constexpr (V == 1) {
+        w[0] = ((t[0] >> (8 * B)) ^ flip) & 0xFFu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            w[i] = gather_bytes<B>(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]) ^ flip;
+    }
+    if (e == 255u) {
+#pragma unroll
+        for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0u;
+    }
+}
+
+// Quantises the V elements at column c of `row` and writes their codes, and the block's exponent
+// byte from its first lane.  Called by every lane of the warp; lanes with live = false (past the
+// last row) only take part in the reduction.  Columns past cols hold 0 and have code 0.
+template <int V, bool RANDOM>
+__device__ __forceinline__ void save(const float (&v)[V], bool live, uint32_t row, uint32_t c,
+                                     int64_t pitch, int64_t epitch, const Rng& rng, int8_t* codes,
+                                     uint8_t* exps) {
+    const uint32_t e = exp_byte(block_top<V>(v));
+    uint32_t w[(V + 3) / 4];
+    codes_of<V, RANDOM>(v, e, row, c, rng, w);
+    if (!live) return;
+    int8_t* p = codes + static_cast<int64_t>(row) * pitch + c;
+    if constexpr (V == 16)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (V == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+        *p = static_cast<int8_t>(w[0]);
+    if ((c & (kBlk - 1)) == 0)
+        exps[static_cast<int64_t>(row) * epitch + (c >> 5)] = static_cast<uint8_t>(e);
+}
+
+// What V codes stand for.  A code byte plus 128 in the low byte of the fp32 number 2^23 gives
+// 2^23 + 128 + code without a conversion instruction.
+template <int V>
+__device__ __forceinline__ void values_of(const uint32_t (&w)[(V + 3) / 4], uint32_t e,
+                                          float (&v)[V]) {
+    const float s = step_of(e);
+    if constexpr (V == 1) {
+        v[0] = static_cast<float>(static_cast<int8_t>(w[0])) * s;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const uint32_t u = w[i] ^ 0x80808080u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[4 * i + k] =
+                    (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + k)) - 8388736.0f) * s;
+        }
+    }
+}
+
+// The V saved values at column c of a row whose codes and exponents begin at p and pe.
+template <int V>
+__device__ __forceinline__ void saved(const int8_t* p, const uint8_t* pe, int64_t c,
+                                      float (&v)[V]) {
+    uint32_t w[(V + 3) / 4];
+    if constexpr (V == 16) {
+        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p + c));
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+    } else if constexpr (V == 8) {
+        const uint2 t = __ldg(reinterpret_cast<const uint2*>(p + c));
+        w[0] = t.x; w[1] = t.y;
+    } else {
+        w[0] = static_cast<uint8_t>(p[c]);
+    }
+    values_of<V>(w, pe[c >> 5], v);
+}
+
+// ---- host checks ---------------------------------------------------------------------------
+
+inline bool mult(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline int elt_bytes(int dtype) { return dtype == GQ_F32 ? 4 : 2; }
+inline bool in_type(int dtype) { return dtype == GQ_F32 || dtype == GQ_BF16; }
+
+// A rows x cols matrix whose rows are ld elements apart, of an element type already checked.
+inline bool matrix_ok(const void* p, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+    if (rows == 0) return true;
+    return p && mult(p, elt_bytes(dtype)) && ld >= cols;
+}
+inline bool size_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols < (int64_t(1) << 31) - 32;
+}
+// Codes and exponent bytes: 16-byte aligned (their row pitches are multiples of 16 bytes).
+inline bool saved_ok(const void* codes, const void* exps) {
+    return codes && exps && mult(codes, 16) && mult(exps, 16);
+}
+// Widest alignment (32, 16 or 0 bytes) that every row start of the matrix has.
+inline int row_align(const void* p, int dtype, int64_t rows, int64_t ld) {
+    const int64_t step = rows > 1 ? ld * elt_bytes(dtype) : 0;
+    if (mult(p, 32) && step % 32 == 0) return 32;
+    return mult(p, 16) && step % 16 == 0 ? 16 : 0;
+}
+
+}  // namespace gqa

@@ -1,0 +1,686 @@
+// gq_wgrad.cu -- weight and bias gradient of a linear layer whose input was kept as an 8-bit
+// checkpoint (C ABI in include/gq.h).
+//
+//   dW[o, i] = sum_t dy[t, o] X[t, i],   X = V  or  V scale + shift (a layer norm's affine part)
+//            = scale[i] (dy^T V)[o, i] + shift[i] db[o],   db[o] = sum_t dy[t, o]
+//
+// with V the values of the checkpoint.  They are exact in bf16, so the tensor cores see the
+// checkpoint itself: dy^T V is a product of bf16 matrices with fp32 accumulation, and the affine
+// part is applied to the finished sums.  fp32 gradients are cut into three bf16 parts (8 + 8 + 8
+// bits, exact), laid one after another along t.
+//
+// One persistent block per SM computes tiles of (128 MH) outs x BN columns:
+//   warp 0      TMA loads of dy (64 tokens x 64 outs per box, 128-byte swizzle, outs contiguous)
+//   warp 1      one thread issues tcgen05.mma, accumulators in TMEM
+//   warps 2-9   read codes and exponents from global memory into registers one stage ahead, widen
+//               them to bf16 in shared memory in the layout of the other operand, and store
+//               finished tiles from TMEM
+// Both operands are contiguous along their outer dimension ("MN-major"), so neither is transposed.
+// The k range of all tiles is one list of 64-token steps, cut into equal contiguous shares, one
+// per block: a tile that two or more blocks share leaves fp32 partial tiles in the workspace,
+// which join_kernel adds in a fixed order.
+#include "gq_act.cuh"
+
+#include <cuda.h>
+
+using namespace gqa;
+
+namespace {
+
+constexpr int kTok = 64;              // tokens per step
+constexpr int kConvWarps = 8;         // warps 2..9
+constexpr int kWThreads = 64 + 32 * kConvWarps;
+constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
+
+template <int MH, int BN> struct Tile {
+    static constexpr int kOuts = 128 * MH;
+    static constexpr int kABytes = kOuts * kTok * 2;
+    static constexpr int kBBytes = BN * kTok * 2;
+    static constexpr int kStages = (kABytes + kBBytes) * 3 <= 200 * 1024
+                                       ? ((kABytes + kBBytes) * 6 <= 200 * 1024 ? 6 : 3) : 2;
+    static constexpr int kCols = MH * BN;  // TMEM columns: a power of two >= 32
+    static constexpr int kSmem = kStages * (kABytes + kBBytes) + 1024;
+};
+
+struct WArgs {
+    int64_t rows, outs, cols, pitch, epitch, ldw;
+    const int8_t* codes;
+    const uint8_t* exps;
+    const float* scale;   // nullable, with shift
+    const float* shift;
+    const float* db;
+    void* dw;
+    int out_f32;
+    int vec;              // dw rows are 16-byte aligned
+    float* partial;
+    int64_t ktok;         // tokens of one part, rounded up to whole steps, in steps
+    int ksteps;           // steps of a tile: parts * ktok
+    int tiles_m, tiles_n;
+    int64_t units;        // tiles * ksteps
+};
+
+// ---- tcgen05 -------------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory descriptor of an operand that is contiguous along its outer dimension, 128-byte
+// swizzle: rows of 64 elements (one token each, 128 bytes), 8 tokens every 1,024 bytes (stride
+// offset), the next 64 outer elements kChunk bytes on (leading offset).
+__device__ __forceinline__ uint64_t operand(uint32_t smem) {
+    return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) |
+           (static_cast<uint64_t>(kChunk >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// fp32 accumulator, bf16 operands, both contiguous along their outer dimension, M = 128, N = BN.
+template <int BN> struct Instruction {
+    static constexpr uint32_t value = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                                      (static_cast<uint32_t>(BN >> 3) << 17) | (128u >> 4 << 24);
+};
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Two codes (the low bytes of the halves of p, 0x43 above them) times a power of two.  0x43cc is
+// 128 + (c & 127) if c's sign bit is taken out, and 0x4300 or 0x4380, 128 or 256, from the sign
+// bit alone: their difference is the code, and the product is exact.
+__device__ __forceinline__ uint32_t widen2(uint32_t p, __nv_bfloat162 s) {
+    uint32_t a = p & 0xFF7FFF7Fu, b = p & 0xFF80FF80u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                     *reinterpret_cast<__nv_bfloat162*>(&b));
+    const __nv_bfloat162 r = __hmul2(d, s);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The contiguous steps [u0, u1) of a block.
+struct Share {
+    int64_t u0, u1;
+    __device__ __forceinline__ Share(int64_t units, int block, int blocks) {
+        u0 = units * block / blocks;
+        u1 = units * (block + 1) / blocks;
+    }
+};
+
+// Row o0 + r of a tile's output or partial tile: 32 columns from TMEM.
+template <typename O>
+__device__ __forceinline__ void put(O* p, int64_t i, int64_t cols, int vec, const float (&v)[32]) {
+    if (vec && i + 32 <= cols) {
+        if constexpr (sizeof(O) == 4) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                reinterpret_cast<float4*>(p + i)[k] =
+                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                reinterpret_cast<uint4*>(p + i)[k] =
+                    make_uint4(pack2(v[8 * k], v[8 * k + 1], bf16()),
+                               pack2(v[8 * k + 2], v[8 * k + 3], bf16()),
+                               pack2(v[8 * k + 4], v[8 * k + 5], bf16()),
+                               pack2(v[8 * k + 6], v[8 * k + 7], bf16()));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (i + k < cols) down(v[k], p[i + k]);
+    }
+}
+
+template <int MH, int BN>
+__global__ void __launch_bounds__(kWThreads, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const WArgs a) {
+    using Cfg = Tile<MH, BN>;
+    constexpr int S = Cfg::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ alignas(8) uint64_t full_a[S], full_b[S], empty[S], acc_full, acc_empty, drain;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto a_stage = [&](int s) { return base + s * Cfg::kABytes; };
+    auto b_stage = [&](int s) { return base + S * Cfg::kABytes + s * Cfg::kBBytes; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            gq::mbar_init(gq::smem_u32(&full_a[s]), 1u);
+            gq::mbar_init(gq::smem_u32(&full_b[s]), kConvWarps);
+            gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
+        }
+        gq::mbar_init(gq::smem_u32(&acc_full), 1u);
+        gq::mbar_init(gq::smem_u32(&acc_empty), kConvWarps);
+        gq::mbar_init(gq::smem_u32(&drain), 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(gq::smem_u32(&tmem_slot), Cfg::kCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Share share(a.units, blockIdx.x, gridDim.x);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            bool ok = true;
+            for (int64_t u = share.u0; u < share.u1 && ok; ++u, ++n) {
+                const int s = n % S;
+                if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                if (!ok) break;
+                const int tile = static_cast<int>(u / a.ksteps), k = static_cast<int>(u % a.ksteps);
+                const uint32_t bar = gq::smem_u32(&full_a[s]);
+                gq::mbar_arrive_expect_tx(bar, Cfg::kABytes);
+                const int o0 = (tile % a.tiles_m) * Cfg::kOuts;
+#pragma unroll
+                for (int c = 0; c < 2 * MH; ++c)
+                    tma_load(a_stage(s) + c * kChunk, &dy_map, o0 + 64 * c, k * kTok, bar);
+            }
+            // nothing of this block's is in flight when it ends, whatever the others did
+            for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
+                gq::mbar_wait(gq::smem_u32(&full_a[j % S]), (j / S) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t n = 0, seg = 0;
+            bool ok = true;
+            for (int64_t u = share.u0; u < share.u1 && ok;) {
+                const int k = static_cast<int>(u % a.ksteps);
+                const int64_t end = min(share.u1, u - k + a.ksteps);
+                if (seg > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (seg - 1) & 1);
+                fence_after();
+                for (bool first = true; u < end && ok; ++u, ++n, first = false) {
+                    const int s = n % S;
+                    ok = gq::mbar_wait(gq::smem_u32(&full_a[s]), (n / S) & 1) &&
+                         gq::mbar_wait(gq::smem_u32(&full_b[s]), (n / S) & 1);
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTok / 16; ++kk) {
+                        const uint64_t b = operand(b_stage(s) + kk * 2048);
+#pragma unroll
+                        for (int h = 0; h < MH; ++h)
+                            mma_bf16(tmem + h * BN, operand(a_stage(s) + h * 2 * kChunk + kk * 2048), b,
+                                     Instruction<BN>::value, !first || kk > 0);
+                    }
+                    mma_commit(gq::smem_u32(&empty[s]));
+                }
+                if (ok) mma_commit(gq::smem_u32(&acc_full));
+                ++seg;
+            }
+            if (!ok) {  // let what was issued finish before TMEM is given back
+                mma_commit(gq::smem_u32(&drain));
+                gq::mbar_wait(gq::smem_u32(&drain), 0);
+            }
+        }
+    } else {
+        const int ct = threadIdx.x - 64;
+        constexpr int kPer = BN * kTok / 16 / (32 * kConvWarps);  // 16-code pieces per thread
+        constexpr int kRowPieces = BN / 16;
+        uint4 w[kPer];
+        uint32_t e[kPer];
+        auto fetch = [&](int64_t u) {
+            const int tile = static_cast<int>(u / a.ksteps), k = static_cast<int>(u % a.ksteps);
+            const int64_t t0 = (k % a.ktok) * kTok;
+            const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int q = ct + j * 32 * kConvWarps;
+                const int64_t t = t0 + q / kRowPieces, i = i0 + (q % kRowPieces) * 16;
+                const bool in = t < a.rows && i < a.pitch;
+                w[j] = in ? __ldg(reinterpret_cast<const uint4*>(a.codes + t * a.pitch + i))
+                          : make_uint4(0, 0, 0, 0);
+                e[j] = in ? __ldg(a.exps + t * a.epitch + (i >> 5)) : 0u;
+            }
+        };
+        uint32_t n = 0, seg = 0;
+        bool ok = true;
+        if (share.u0 < share.u1) fetch(share.u0);
+        for (int64_t u = share.u0; u < share.u1;) {
+            const int k0 = static_cast<int>(u % a.ksteps);
+            const int tile = static_cast<int>(u / a.ksteps);
+            const int64_t end = min(share.u1, u - k0 + a.ksteps);
+            const bool whole = k0 == 0 && end - u == a.ksteps;
+            for (; u < end; ++u, ++n) {
+                const int s = n % S;
+                uint4 cw[kPer];
+                uint32_t ce[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
+                if (u + 1 < share.u1) fetch(u + 1);
+                if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) continue;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int q = ct + j * 32 * kConvWarps;
+                    const int t = q / kRowPieces, c = q % kRowPieces;  // token, 16-column piece
+                    const uint32_t sc = ce[j] << 7 | ce[j] << 23;
+                    const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
+                    const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        o[2 * m] = widen2(__byte_perm(in[m], 0x43434343u, 0x4140), sv);
+                        o[2 * m + 1] = widen2(__byte_perm(in[m], 0x43434343u, 0x4342), sv);
+                    }
+                    // 16-byte unit v of row t of a 64-column chunk sits at unit v ^ (t mod 8)
+                    const uint32_t row = b_stage(s) + (c >> 2) * kChunk + t * 128;
+                    const uint32_t v0 = (2 * (c & 3)) ^ (t & 7);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + v0 * 16),
+                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (v0 ^ 1) * 16),
+                                 "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full_b[s]));
+            }
+            // the finished tile: 4 warps take the 128 lanes of TMEM, the two groups of 4 share
+            // the halves (or, with one half, its columns)
+            if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
+            ok = __all_sync(kFull, ok);
+            fence_after();
+            const int quad = warp & 3, group = (warp - 2) >> 2;
+            const int h = MH == 2 ? group : 0;
+            const int c0 = MH == 2 ? 0 : group * (BN / 2), c1 = MH == 2 ? BN : c0 + BN / 2;
+            const int r = h * 128 + quad * 32 + lane;
+            const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * Cfg::kOuts + r;
+            const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
+            float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) *
+                                          (Cfg::kOuts * BN) + static_cast<int64_t>(r) * BN;
+            const float dbo = whole && a.shift && o < a.outs ? a.db[o] : 0.0f;
+            for (int c = c0; c < c1; c += 32) {
+                uint32_t acc[32];
+                if (ok) {
+                    tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * BN + c, acc);
+                } else {  // a wait gave up: the tile is marked, not left as it was
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) acc[k] = 0x7FFFFFFFu;
+                }
+                float v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
+                if (!whole) {
+                    put<float>(part, c, BN, 1, v);
+                    continue;
+                }
+                if (o >= a.outs || i0 + c >= a.cols) continue;
+                if (a.scale) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int64_t i = i0 + c + k;
+                        if (i < a.cols) v[k] = v[k] * __ldg(a.scale + i);
+                    }
+                }
+                if (a.shift) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int64_t i = i0 + c + k;
+                        if (i < a.cols) v[k] = fmaf(dbo, __ldg(a.shift + i), v[k]);
+                    }
+                }
+                if (a.out_f32)
+                    put(static_cast<float*>(a.dw) + o * a.ldw, i0 + c, a.cols, a.vec, v);
+                else
+                    put(static_cast<bf16*>(a.dw) + o * a.ldw, i0 + c, a.cols, a.vec, v);
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) gq::mbar_arrive(gq::smem_u32(&acc_empty));
+            ++seg;
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, Cfg::kCols);
+}
+
+// Adds the partial tiles of every tile that more than one block worked on, in block order.
+// blockIdx.x = tile, blockIdx.y = a share of its rows; thread = 4 columns.
+template <int MH, int BN>
+__global__ void __launch_bounds__(256) join_kernel(const WArgs a, int blocks) {
+    constexpr int kOuts = Tile<MH, BN>::kOuts;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * a.ksteps;
+    const int64_t last = first + a.ksteps - 1;
+    auto owner = [&](int64_t u) {  // the block whose share holds step u
+        int64_t b = u * blocks / a.units;
+        while (b + 1 < blocks && a.units * (b + 1) / blocks <= u) ++b;
+        while (b > 0 && a.units * b / blocks > u) --b;
+        return b;
+    };
+    const int64_t b0 = owner(first), b1 = owner(last);
+    if (b0 == b1) return;  // stored by its one block
+    const int64_t om = static_cast<int64_t>(blockIdx.x % a.tiles_m) * kOuts;
+    const int64_t im = static_cast<int64_t>(blockIdx.x / a.tiles_m) * BN;
+    constexpr int kQuads = BN / 4;
+    const int rows = kOuts / gridDim.y;
+    for (int q = threadIdx.x; q < rows * kQuads; q += 256) {
+        const int r = blockIdx.y * rows + q / kQuads, c = (q % kQuads) * 4;
+        const int64_t o = om + r, i = im + c;
+        if (o >= a.outs || i >= a.cols) continue;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t b = b0; b <= b1; ++b) {
+            // a share that begins at the tile's first step is in slot 1, any other in slot 0
+            const int64_t u0 = a.units * b / blocks;
+            const int slot = u0 <= first ? 1 : 0;
+            const float4 p = *reinterpret_cast<const float4*>(
+                a.partial + (b * 2 + slot) * (kOuts * BN) + static_cast<int64_t>(r) * BN + c);
+            v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+        }
+        const float dbo = a.shift ? a.db[o] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k >= a.cols) break;
+            if (a.scale) v[k] *= a.scale[i + k];
+            if (a.shift) v[k] = fmaf(dbo, a.shift[i + k], v[k]);
+            if (a.out_f32)
+                static_cast<float*>(a.dw)[o * a.ldw + i + k] = v[k];
+            else
+                static_cast<bf16*>(a.dw)[o * a.ldw + i + k] = __float2bfloat16_rn(v[k]);
+        }
+    }
+}
+
+// dy as the TMA needs it: rows of `pitch` bf16 (a multiple of 8), `tokens` per part (whole steps),
+// zeros behind the last row.  fp32 is cut into three parts of 8 bits each by truncation, whose
+// sum is the number itself; an infinity or a NaN stays in the first.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    pack_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs, bf16* out,
+                int64_t pitch, int64_t tokens) {
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (o >= pitch) return;
+    for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
+        const bool in = t < rows && o < outs;
+        if constexpr (sizeof(T) == 2) {
+            out[t * pitch + o] = in ? dy[t * ld + o] : __float2bfloat16_rn(0.0f);
+        } else {
+            float v = in ? dy[t * ld + o] : 0.0f;
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint32_t top = __float_as_uint(v) & 0xFFFF0000u;
+                const bool special = (top & 0x7F800000u) == 0x7F800000u;
+                const bool nan = (__float_as_uint(v) & 0x7FFFFFFFu) > 0x7F800000u;
+                reinterpret_cast<uint16_t*>(out)[(p * tokens + t) * pitch + o] =
+                    static_cast<uint16_t>(nan ? 0x7FFFu : top >> 16);
+                v = special ? 0.0f : v - __uint_as_float(top);
+            }
+        }
+    }
+}
+
+// Column sums of dy: thread = V columns, 8 rows at a time per block, partial[blockIdx.y][outs].
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+    bias_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
+                float* __restrict__ partial) {
+    __shared__ float tile[8][32 * V];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * V;
+    float s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 0.0f;
+    if (c < outs) {
+#pragma unroll 4
+        for (int64_t t = static_cast<int64_t>(blockIdx.y) * 8 + y; t < rows;
+             t += static_cast<int64_t>(gridDim.y) * 8) {
+            float v[V];
+            load<T, V, 16>(dy + t * ld, c, outs, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] += v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) tile[y][x * V + i] = s[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+        const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * V + i;
+        if (col < outs) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += tile[k][i];
+            partial[blockIdx.y * outs + col] = v;
+        }
+    }
+}
+__global__ void __launch_bounds__(256)
+    bias_sum_kernel(const float* __restrict__ partial, int parts, int64_t outs, float* db) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+    __shared__ float tile[8][32];
+    float s = 0.0f;
+    if (c < outs) {
+#pragma unroll 4
+        for (int p = threadIdx.x >> 5; p < parts; p += 8) s += partial[p * outs + c];
+    }
+    tile[threadIdx.x >> 5][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (threadIdx.x < 32 && c < outs) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += tile[k][threadIdx.x];
+        db[c] = v;
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+struct WPlan {
+    bool big;            // 256 x 256 tiles, else 128 x 128
+    bool pack;
+    int parts;           // bf16 parts of dy
+    int64_t ktok, ksteps, tiles_m, tiles_n, units, pitch;
+    int blocks, shares;  // of the main kernel; of the bias sums
+    size_t pack_off, bias_off, db_off, bytes;
+};
+
+WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t ld, int64_t cols) {
+    WPlan p;
+    const int sms = gqh::sm_count();
+    p.parts = dtype == GQ_F32 ? 3 : 1;
+    p.pack = dtype == GQ_F32 || row_align(dy, dtype, rows, ld) == 0;
+    p.ktok = (rows + kTok - 1) / kTok;
+    p.ksteps = p.ktok * p.parts;
+    const int64_t big = ((outs + 255) / 256) * ((cols + 255) / 256) * p.ksteps;
+    p.big = big >= 16 * sms && outs > 128 && cols > 128;
+    const int side = p.big ? 256 : 128;
+    p.tiles_m = (outs + side - 1) / side;
+    p.tiles_n = (cols + side - 1) / side;
+    p.units = p.tiles_m * p.tiles_n * p.ksteps;
+    // a block's share is worth its partial tile's trip through memory from about 4 steps on
+    int64_t blocks = (p.units + 3) / 4;
+    if (blocks < p.tiles_m * p.tiles_n) blocks = p.tiles_m * p.tiles_n;
+    p.blocks = static_cast<int>(blocks < sms ? blocks : sms);
+    p.pitch = (outs + 7) / 8 * 8;
+    int64_t sh = (rows + 63) / 64;
+    p.shares = static_cast<int>(sh < 64 ? (sh < 1 ? 1 : sh) : 64);
+    auto up256 = [](size_t v) { return (v + 255) / 256 * 256; };
+    p.pack_off = up256(static_cast<size_t>(p.blocks) * 2 * side * side * sizeof(float));
+    p.bias_off = p.pack_off +
+                 (p.pack ? up256(static_cast<size_t>(p.ksteps) * kTok * p.pitch * 2) : 0);
+    p.db_off = p.bias_off + up256(static_cast<size_t>(p.shares) * outs * sizeof(float));
+    p.bytes = p.db_off + up256(static_cast<size_t>(outs) * sizeof(float));
+    return p;
+}
+
+bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
+    // 32-bit TMA coordinates: tokens of three parts, and outs
+    return size_ok(rows, cols) && rows < (int64_t(1) << 29) && outs >= 1 &&
+           outs < (int64_t(1) << 30) && cols < (int64_t(1) << 30) &&
+           ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 31);
+}
+
+template <int MH, int BN>
+gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int blocks, cudaStream_t st) {
+    using Cfg = Tile<MH, BN>;
+    auto k = wgrad_kernel<MH, BN>;
+    gqh::blocks_per_sm(k, Cfg::kSmem, kWThreads);  // raises the shared-memory limit once
+    k<<<blocks, kWThreads, Cfg::kSmem, st>>>(map, a);
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+    // every tile is whole when the shares are whole numbers of tiles
+    if (tiles % blocks != 0) {
+        const dim3 grid(static_cast<unsigned>(tiles), MH == 2 ? 16 : 8);
+        join_kernel<MH, BN><<<grid, 256, 0, st>>>(a, blocks);
+    }
+    return gqh::launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gq_linear_wgrad_workspace_bytes(const void *dy, int dtype, int64_t rows, int64_t outs,
+                                       int64_t lddy, int64_t cols) {
+    if (!in_type(dtype) || !wgrad_sizes(rows, outs, cols)) return 0;
+    if (rows == 0) return 16;
+    return wgrad_plan(dy, dtype, rows, outs, lddy, cols).bytes;
+}
+
+gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
+                          const int8_t *codes, const uint8_t *exps, int64_t cols,
+                          const float *scale, const float *shift, void *dw, int out_dtype,
+                          int64_t lddw, float *dbias, void *ws, size_t ws_bytes, void *stream) {
+    if (!in_type(dtype) || !in_type(out_dtype) || !wgrad_sizes(rows, outs, cols))
+        return GQ_ERR_INVALID;
+    if (!matrix_ok(dw, out_dtype, outs, cols, lddw) || !matrix_ok(dy, dtype, rows, outs, lddy))
+        return GQ_ERR_INVALID;
+    if (!mult(scale, 4) || !mult(shift, 4) || !mult(dbias, 4)) return GQ_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // sums over no tokens
+        const size_t elt = elt_bytes(out_dtype);
+        if (cudaMemset2DAsync(dw, lddw * elt, 0, cols * elt, outs, st) != cudaSuccess)
+            return GQ_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, outs * sizeof(float), st) != cudaSuccess)
+            return GQ_ERR_CUDA;
+        return GQ_OK;
+    }
+    if (!saved_ok(codes, exps)) return GQ_ERR_INVALID;
+    const WPlan p = wgrad_plan(dy, dtype, rows, outs, lddy, cols);
+    if (!ws || !mult(ws, 16) || ws_bytes < p.bytes) return GQ_ERR_WORKSPACE;
+    EncodeFn encode = encode_fn();
+    if (!encode) return GQ_ERR_CUDA;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    float* db = dbias ? dbias : reinterpret_cast<float*>(w + p.db_off);
+
+    const void* src = dy;
+    int64_t src_ld = lddy, src_rows = rows, src_outs = outs;
+    if (p.pack) {
+        bf16* out = reinterpret_cast<bf16*>(w + p.pack_off);
+        const int64_t tokens = p.ktok * kTok;
+        const dim3 grid(static_cast<unsigned>((p.pitch + 255) / 256),
+                        static_cast<unsigned>(tokens < 4096 ? tokens : 4096));
+        if (dtype == GQ_F32)
+            pack_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(dy), lddy, rows, outs,
+                                                     out, p.pitch, tokens);
+        else
+            pack_kernel<bf16><<<grid, 256, 0, st>>>(static_cast<const bf16*>(dy), lddy, rows, outs,
+                                                    out, p.pitch, tokens);
+        src = out;
+        src_ld = p.pitch;
+        src_rows = tokens * p.parts;
+        src_outs = p.pitch;
+    }
+    if (dbias || shift) {
+        float* part = reinterpret_cast<float*>(w + p.bias_off);
+        const bool vec = row_align(dy, dtype, rows, lddy) != 0;
+        const int v = vec ? 8 : 1;
+        const dim3 grid(static_cast<unsigned>((outs + 32 * v - 1) / (32 * v)), p.shares);
+        if (dtype == GQ_F32) {
+            const float* g = static_cast<const float*>(dy);
+            if (vec) bias_kernel<float, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+            else bias_kernel<float, 1><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+        } else {
+            const bf16* g = static_cast<const bf16*>(dy);
+            if (vec) bias_kernel<bf16, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+            else bias_kernel<bf16, 1><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+        }
+        bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.shares, outs,
+                                                                                db);
+    }
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(src_outs), static_cast<cuuint64_t>(src_rows)};
+    // one row's stride is not used, but has to be a multiple of 16 bytes like any other
+    const cuuint64_t strides[1] = {src_rows > 1 ? static_cast<cuuint64_t>(src_ld) * 2
+                                                : (static_cast<cuuint64_t>(src_outs) * 2 + 15) / 16 * 16};
+    const cuuint32_t box[2] = {64, kTok}, one[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(src), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return GQ_ERR_CUDA;
+
+    WArgs a;
+    a.rows = rows; a.outs = outs; a.cols = cols;
+    a.pitch = code_pitch(cols); a.epitch = exp_pitch(cols); a.ldw = lddw;
+    a.codes = codes; a.exps = exps;
+    a.scale = scale; a.shift = shift; a.db = db;
+    a.dw = dw; a.out_f32 = out_dtype == GQ_F32;
+    a.vec = row_align(dw, out_dtype, outs, lddw) != 0;
+    a.partial = static_cast<float*>(ws);
+    a.ktok = p.ktok; a.ksteps = static_cast<int>(p.ksteps);
+    a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
+    a.units = p.units;
+    return p.big ? launch_wgrad<2, 256>(map, a, p.blocks, st) : launch_wgrad<1, 128>(map, a, p.blocks, st);
+}
+
+}  // extern "C"

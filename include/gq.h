@@ -437,6 +437,115 @@ gq_status gq_exp_dequantize(const int8_t *codes, int64_t d, const float *norm_de
 gq_status gq_selftest_wait_timeout(void *ws, size_t ws_bytes, uint64_t limit_ns,
                                    unsigned long long *elapsed_dev, void *stream);
 
+/*
+ * ---- Activations of a training step kept in 8 bits ------------------------------------------
+ *
+ * The calls below keep what a forward pass leaves for the backward pass as an 8-bit checkpoint,
+ * and compute the backward pass from it.  They have no counterpart in the paper, which quantises
+ * gradients: they extend its unbiased rounding to the activations from which those gradients are
+ * computed, with the same random words.
+ *
+ * A checkpoint of a rows x cols matrix is two arrays in device memory, 16-byte aligned:
+ *   codes  int8,  rows of gq_code_pitch(cols) = round_up(cols, 32) bytes; padding codes are 0;
+ *   exps   uint8, rows of gq_act_exp_pitch(cols) = round_up(ceil(cols / 32), 16) bytes; bytes
+ *          behind the last block of a row are not written.
+ * Element (i, j) stands for codes[i][j] * 2^(E - 127), E = exps[i][j / 32] the smallest value >= 1
+ * with 127 * 2^(E - 127) >= the largest magnitude of the 32 columns of its block.  A block that
+ * holds a NaN, an infinity or a magnitude above 127 * 2^121 has E = 255 and zero codes and reads
+ * back as NaN.  Magnitudes below 2^-126 keep at most that step.  Values are exact in bf16.
+ * Rounding of x / 2^(E - 127):
+ *   GQ_ACT_NEAREST  to the nearest integer, ties to even (seed and step are not used);
+ *   GQ_ACT_RANDOM   floor(P / 2^16 + H / 2^16), P = 2^16 x / 2^(E - 127) rounded to the nearest
+ *                   even integer and H the high 16 bits of the random word of element (i, j) of
+ *                   gq_quantize (key seed, worker i, step): unbiased but for the rounding of P,
+ *                   which is below 2^-16 of a step.
+ *
+ * Matrices: GQ_F32 or GQ_BF16, element-aligned, rows ld >= cols elements apart (16-byte aligned
+ * rows take the wide loads).  0 <= rows < 2^31, 1 <= cols < 2^31 - 32; with rows = 0 nothing is read
+ * and sums over rows are written as 0.  Outputs may not overlap inputs.  All sums are fp32, in a
+ * fixed order: results repeat bit for bit on the same GPU.
+ */
+#define GQ_ACT_NEAREST 0
+#define GQ_ACT_RANDOM 1
+
+/* Row pitch of the exponent array in bytes; 0 if cols < 1. */
+int64_t gq_act_exp_pitch(int64_t cols);
+
+/* Checkpoint of x. */
+gq_status gq_act_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                          int rounding, uint64_t seed, uint64_t step, int8_t *codes,
+                          uint8_t *exps, void *stream);
+
+/* The values of a checkpoint as out_dtype (exact in GQ_F32 and GQ_BF16; GQ_F16 rounds to nearest
+ * even and overflows to infinity). */
+gq_status gq_act_dequantize(const int8_t *codes, const uint8_t *exps, int64_t rows, int64_t cols,
+                            void *out, int out_dtype, int64_t ldout, void *stream);
+
+/*
+ * Layer norm: y = xh w + b with xh = (x - mean) rstd, mean and variance over a row, rstd =
+ * 1 / sqrt(variance + eps), eps >= 0.  weight and bias (nullable, wdtype GQ_F32 or GQ_BF16, cols
+ * elements) are 1 and 0 where absent.  y has x's type.  mean, rstd: fp32, rows elements.  codes and
+ * exps (both or neither) receive the checkpoint of xh, from which gq_layernorm_backward and, with
+ * scale = weight and shift = bias, gq_linear_wgrad of the following linear layer are computed:
+ * one byte per element kept for both.
+ */
+gq_status gq_layernorm_forward(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               const void *weight, const void *bias, int wdtype, float eps, void *y,
+                               int64_t ldy, float *mean, float *rstd, int rounding, uint64_t seed,
+                               uint64_t step, int8_t *codes, uint8_t *exps, void *stream);
+
+/*
+ * Its backward pass: dx = rstd (w dy - mean(w dy) - xh mean(w dy xh)), dweight = sum over the rows
+ * of dy xh, dbias = sum over the rows of dy.  xh is read from the checkpoint (codes and exps, with
+ * x = mean = NULL) or computed from x, mean and rstd (codes = exps = NULL); anything else is
+ * GQ_ERR_INVALID.  dx has dy's type; dweight and dbias (nullable) are of gdtype (GQ_F32 or GQ_BF16).
+ * ws: gq_layernorm_workspace_bytes(rows, cols) bytes, 16-byte aligned, contents irrelevant (else
+ * GQ_ERR_WORKSPACE).
+ */
+size_t gq_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t cols, int64_t lddy,
+                                const void *weight, int wdtype, const float *rstd,
+                                const int8_t *codes, const uint8_t *exps, const void *x,
+                                int64_t ldx, const float *mean, void *dx, int64_t lddx,
+                                void *dweight, void *dbias, int gdtype, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* GELU u Phi(u): with the normal distribution function (GQ_GELU_ERF), or with
+ * (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) / 2 in its place (GQ_GELU_TANH). */
+#define GQ_GELU_ERF 0
+#define GQ_GELU_TANH 1
+
+/* h = gelu(u), of u's type; codes and exps (both or neither) receive the checkpoint of u. */
+gq_status gq_gelu_forward(const void *u, int dtype, int64_t rows, int64_t cols, int64_t ldu,
+                          int form, void *h, int64_t ldh, int rounding, uint64_t seed,
+                          uint64_t step, int8_t *codes, uint8_t *exps, void *stream);
+
+/* du = dh gelu'(u) with u read from its checkpoint, of dh's type; h (nullable) receives gelu(u)
+ * again, the next linear layer's input, so that the forward pass need not keep it. */
+gq_status gq_gelu_backward(const void *dh, int dtype, int64_t rows, int64_t cols, int64_t lddh,
+                           const int8_t *codes, const uint8_t *exps, int form, void *du,
+                           int64_t lddu, void *h, int64_t ldh, void *stream);
+
+/*
+ * Weight and bias gradient of a linear layer y = X W^T + b whose input X (rows x cols) is the
+ * checkpoint's values V, or V scale + shift (each nullable, fp32, cols elements):
+ *   dw[o][i] = sum over the rows t of dy[t][o] X[t][i]   (outs x cols, out_dtype GQ_F32 or GQ_BF16,
+ *                                                        rows lddw apart)
+ *   dbias[o] = sum over the rows t of dy[t][o]           (nullable, fp32)
+ * dy: rows x outs.  Products of bf16 matrices with fp32 accumulation on the tensor cores; V is
+ * exact in bf16, and an fp32 dy takes part as three bf16 matrices whose sum it is, so that nothing
+ * is rounded before the accumulation.  rows < 2^29, outs and cols < 2^30.  ws:
+ * gq_linear_wgrad_workspace_bytes(...) bytes for the same dy (its alignment counts), 16-byte
+ * aligned, contents irrelevant (else GQ_ERR_WORKSPACE).  A bounded wait that gives up (about a
+ * second; a broken kernel only) leaves NaN in the tiles concerned.
+ */
+size_t gq_linear_wgrad_workspace_bytes(const void *dy, int dtype, int64_t rows, int64_t outs,
+                                       int64_t lddy, int64_t cols);
+gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
+                          const int8_t *codes, const uint8_t *exps, int64_t cols,
+                          const float *scale, const float *shift, void *dw, int out_dtype,
+                          int64_t lddw, float *dbias, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
