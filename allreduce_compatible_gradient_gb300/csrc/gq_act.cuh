@@ -173,6 +173,42 @@ __device__ __forceinline__ void store(T* p, int64_t c, int64_t cols, const float
         if (c + i < cols) down(v[i], p[c + i]);
 }
 
+// ---- pairs of fp32 -------------------------------------------------------------------------
+// One instruction on two fp32 numbers (sm_100 and later), each rounded as its scalar form: what
+// bounds these kernels beside memory is the number of instructions issued.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    float x, y;
+    split(a, x, y);
+    return x + y;
+}
+
 // ---- the 8-bit block format ----------------------------------------------------------------
 
 // Largest magnitude of the 32-column block that 32 / V neighbouring lanes hold, as fp32 bits
@@ -277,6 +313,112 @@ __device__ __forceinline__ void save(const float (&v)[V], bool live, uint32_t ro
         *p = static_cast<int8_t>(w[0]);
     if ((c & (kBlk - 1)) == 0)
         exps[static_cast<int64_t>(row) * epitch + (c >> 5)] = static_cast<uint8_t>(e);
+}
+
+// The same for 8 columns held as pairs: largest magnitude of the lane's 8 and of the block's 4
+// lanes.  Maxima of floating-point numbers pass over a NaN, so `plain` says that there is none
+// (and no infinity); otherwise the bits are compared.
+__device__ __forceinline__ uint32_t block_top8(const F2 (&h)[4], bool plain) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(h[i], v[2 * i], v[2 * i + 1]);
+    uint32_t m;
+    if (plain) {
+        float a = fmaxf(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+        for (int i = 2; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+        m = __float_as_uint(a);
+    } else {
+        m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    m = max(m, __shfl_xor_sync(kFull, m, 1));
+    return max(m, __shfl_xor_sync(kFull, m, 2));
+}
+
+// Codes of 8 columns; r: their Philox call (not read when rounding to nearest).
+template <bool RANDOM>
+__device__ __forceinline__ uint2 codes8(const F2 (&h)[4], uint32_t e, const uint4& r) {
+    const F2 inv = f2(inv_step(e));
+    uint32_t t[8];
+    const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        if constexpr (RANDOM) {
+            split(fma2(mul2(h[i], inv), f2(65536.0f), f2(25165824.0f)), a, b);
+            t[2 * i] = (__float_as_uint(a) << 1) + (word[i] & 0xFFFFu);
+            t[2 * i + 1] = (__float_as_uint(b) << 1) + (word[i] >> 16);
+        } else {
+            split(fma2(h[i], inv, f2(12582912.0f)), a, b);
+            t[2 * i] = __float_as_uint(a);
+            t[2 * i + 1] = __float_as_uint(b);
+        }
+    }
+    constexpr int B = RANDOM ? 2 : 0;
+    constexpr uint32_t flip = RANDOM ? 0x80808080u : 0u;
+    uint2 w = make_uint2(gather_bytes<B>(t[0], t[1], t[2], t[3]) ^ flip,
+                         gather_bytes<B>(t[4], t[5], t[6], t[7]) ^ flip);
+    if (e == 255u) w = make_uint2(0u, 0u);
+    return w;
+}
+
+// The values of 8 codes as pairs.
+__device__ __forceinline__ void values8(uint2 w, uint32_t e, F2 (&v)[4]) {
+    const F2 s = f2(step_of(e)), off = f2(-8388736.0f);
+    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t q = u[i >> 1];
+        const int k = 2 * (i & 1);
+        v[i] = mul2(add2(f2(__uint_as_float(__byte_perm(q, 0x4B000000u, 0x7650 + k)),
+                            __uint_as_float(__byte_perm(q, 0x4B000000u, 0x7651 + k))), off), s);
+    }
+}
+
+// 8 elements as loaded (bf16: 4 words, fp32: 8), and as pairs of fp32.
+template <typename T> struct Raw8 {
+    uint32_t w[sizeof(T) * 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p, int64_t c, int64_t cols) {
+    Raw8<T> r;
+    if (c + 8 <= cols) {
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + c) + k);
+            r.w[4 * k] = a.x; r.w[4 * k + 1] = a.y; r.w[4 * k + 2] = a.z; r.w[4 * k + 3] = a.w;
+        }
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? up(p[c + i]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) r.w[i] = __float_as_uint(v[i]);
+            else if (i & 1) r.w[i / 2] |= __float_as_uint(v[i]) & 0xFFFF0000u;
+            else r.w[i / 2] = __float_as_uint(v[i]) >> 16;
+        }
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void pairs(const Raw8<T>& r, F2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+            v[i] = f2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+        else
+            v[i] = f2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int64_t c, int64_t cols, const F2 (&v)[4]) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
+    store<T, 8, 16>(p, c, cols, o);
 }
 
 // What V codes stand for.  A code byte plus 128 in the low byte of the fp32 number 2^23 gives

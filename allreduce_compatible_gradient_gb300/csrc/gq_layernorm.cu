@@ -6,12 +6,14 @@
 //             db = sum_rows dy
 //
 // Both are bound by memory.  A row stays in registers between its reductions, so it is read
-// once: a warp holds a row of up to 1,024 columns (32 per lane), a block of 128 to 512 threads
-// a longer one; what does not fit the registers is read again (from L2, mostly).  The backward
-// pass keeps dw and db of its threads' columns in registers over all the rows of a block and
-// leaves one partial row per block in the workspace; a second kernel adds those in a fixed order,
-// so that results do not depend on timing.  All sums are fp32.
+// once (see "rows held by fixed threads"); the generic kernels at the top take unaligned rows and
+// rows of more than 8,192 columns, and read again what does not fit their registers (from L2,
+// mostly).  The backward pass keeps dw and db of its threads' columns in registers over all the
+// rows of a block and leaves one partial row per block in the workspace; a second kernel adds
+// those in a fixed order, so that results do not depend on timing.  All sums are fp32.
 #include "gq_act.cuh"
+
+#include <mutex>
 
 using namespace gqa;
 
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
         }
     }
     row_sum<WARP>(sq, buf[1], threads);
-    const float rstd = 1.0f / sqrtf(sq[0] * s.inv_cols + eps);
+    const float rstd = 1.0f / sqrtf(__fmul_rn(sq[0], s.inv_cols) + eps);
     if (t == 0) {
         mean_out[row] = mean;
         rstd_out[row] = rstd;
@@ -371,9 +373,267 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
+// ---- rows held by fixed threads ------------------------------------------------------------
+// The form for 16-byte aligned rows of up to 8,192 columns.  A group of tpr threads (whole warps,
+// cols / 8 or cols / 16 of them) walks over rows; thread t has the same 8 columns of every row (two
+// such pieces where VPT = 2), so that weights, the backward sums and the column part of the random
+// words stay in registers, and the next row is on its way while this one is worked on.
+
+struct Groups {
+    int wpr;     // warps per row
+    int groups;  // rows at a time per block
+};
+
+__device__ __forceinline__ void group_sync(int group, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+}
+
+// Sums over a group's threads.  `buf` must not be written again before the group has passed another
+// barrier: calls alternate between two.
+__device__ __forceinline__ float group_sum(float v, float* buf, int warp_in_row, const Groups& g,
+                                           int group) {
+    v = warp_sum(v);
+    if (g.wpr == 1) return v;
+    const int lane = threadIdx.x & 31;
+    float* mine = buf + group * g.wpr;
+    if (lane == 0) mine[warp_in_row] = v;
+    group_sync(group, g.wpr * 32);
+    if (g.wpr <= 4) {
+        v = mine[0];
+        for (int k = 1; k < g.wpr; ++k) v += mine[k];
+        return v;
+    }
+    return warp_sum(lane < g.wpr ? mine[lane] : 0.0f);
+}
+// Two sums at once: the halves of the warp take one each after the first exchange.
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2* buf, int warp_in_row,
+                                             const Groups& g, int group) {
+    const int lane = threadIdx.x & 31;
+    const bool upper = lane & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(kFull, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if (g.wpr == 1) return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
+    float2* mine = buf + group * g.wpr;
+    if ((lane & 15) == 0) reinterpret_cast<float*>(mine + warp_in_row)[lane >> 4] = v;
+    group_sync(group, g.wpr * 32);
+    if (g.wpr <= 4) {
+        float2 r = mine[0];
+        for (int k = 1; k < g.wpr; ++k) {
+            r.x += mine[k].x;
+            r.y += mine[k].y;
+        }
+        return r;
+    }
+    const float2 r = lane < g.wpr ? mine[lane] : make_float2(0.0f, 0.0f);
+    return make_float2(warp_sum(r.x), warp_sum(r.y));
+}
+
+__device__ __forceinline__ void vec8(const void* p, int wide, float none, int64_t c, int64_t cols,
+                                     F2 (&v)[4]) {
+    float t[8];
+    vec_of<8>(p, wide, none, c, cols, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(t[2 * i], t[2 * i + 1]);
+}
+
+template <typename T, int VPT, int RND, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
+    forward_rows(const T* __restrict__ x, int64_t ldx, Shape s, Groups g, Affine af, float eps,
+                 T* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
+                 float* __restrict__ rstd_out, int8_t* __restrict__ codes,
+                 uint8_t* __restrict__ exps, Rng rng) {
+    __shared__ float buf[2][16];
+    const int warp = threadIdx.x >> 5, group = warp / g.wpr, wr = warp % g.wpr;
+    const int t = wr * 32 + (threadIdx.x & 31), tpr = g.wpr * 32;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * g.groups;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + group;
+    if (row >= s.rows) return;  // whole groups
+    int64_t c[VPT];
+    F2 w[VPT][4], b[VPT][4];
+    gq::PhiloxGroup pg[VPT];
+    Raw8<T> next[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        c[k] = static_cast<int64_t>(k * tpr + t) * 8;
+        vec8(af.w, af.wide, 1.0f, c[k], s.cols, w[k]);
+        vec8(af.b, af.wide, 0.0f, c[k], s.cols, b[k]);
+        if constexpr (RND == 1)
+            pg[k] = gq::philox_group(static_cast<uint32_t>(c[k] >> 3), rng.step_lo, rng.step_hi, rng.rk);
+        next[k] = raw8(x + row * ldx, c[k], s.cols);
+    }
+    for (; row < s.rows; row += stride) {
+        F2 v[VPT][4];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            pairs(next[k], v[k]);
+            if (row + stride < s.rows) next[k] = raw8(x + (row + stride) * ldx, c[k], s.cols);
+        }
+        F2 sum = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = add2(sum, v[k][i]);
+        const float mean = group_sum(sum2(sum), buf[0], wr, g, group) * s.inv_cols;
+        F2 sq = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (c[k] + 8 <= s.cols) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], f2(-mean));
+            } else {  // nothing is subtracted behind the last column
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[k][i] = add2(v[k][i], f2(c[k] + 2 * i < s.cols ? -mean : 0.0f,
+                                               c[k] + 2 * i + 1 < s.cols ? -mean : 0.0f));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
+        }
+        // not contracted with the sum: y is the same with and without a checkpoint
+        const float var = __fmul_rn(group_sum(sum2(sq), buf[1], wr, g, group), s.inv_cols);
+        const float rstd = 1.0f / sqrtf(var + eps);
+        if (t == 0) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
+        const F2 rs = f2(rstd);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k][i] = mul2(v[k][i], rs);
+            if constexpr (RND >= 0) {
+                const float inf = __uint_as_float(0x7F800000u);
+                const uint32_t e = exp_byte(block_top8(v[k], var < inf && rstd < inf));
+                uint4 r = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (RND == 1)
+                    r = gq::philox_row(pg[k], static_cast<uint32_t>(row), rng.step_lo, rng.rk);
+                if (c[k] < s.pitch) {
+                    *reinterpret_cast<uint2*>(codes + row * s.pitch + c[k]) =
+                        codes8<RND == 1>(v[k], e, r);
+                    if ((c[k] & 31) == 0)
+                        exps[row * s.epitch + (c[k] >> 5)] = static_cast<uint8_t>(e);
+                }
+            }
+            if (c[k] < s.cols) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = fma2(v[k][i], w[k][i], b[k][i]);
+                store8(y + row * ldy, c[k], s.cols, v[k]);
+            }
+        }
+    }
+}
+
+// The block's rows' sums of dy xh and dy go to partial[block][0 and 1][cols].
+template <typename T, int VPT, bool CODES, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
+    backward_rows(const T* __restrict__ dy, int64_t lddy, Shape s, Groups g, const void* w, int wide,
+                  const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx, int64_t lddx,
+                  float* __restrict__ partial) {
+    __shared__ float2 buf[2][16];
+    extern __shared__ float shared_cols[];  // 2 x cols, with more than one group
+    const int warp = threadIdx.x >> 5, group = warp / g.wpr, wr = warp % g.wpr;
+    const int t = wr * 32 + (threadIdx.x & 31), tpr = g.wpr * 32;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * g.groups;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + group;
+    int64_t c[VPT];
+    F2 wv[VPT][4], aw[VPT][4], ab[VPT][4];
+    Raw8<T> ng[VPT], nx[CODES ? 1 : VPT];
+    uint2 nc[CODES ? VPT : 1];
+    uint32_t ne[CODES ? VPT : 1];
+    float nrstd = 0.0f, nmean = 0.0f;
+    auto fetch = [&](int64_t r) {
+        nrstd = __ldg(rstd_in + r);
+        if constexpr (!CODES) nmean = __ldg(src.mean + r);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            ng[k] = raw8(dy + r * lddy, c[k], s.cols);
+            if constexpr (CODES) {
+                const bool in = c[k] < s.pitch;
+                nc[k] = in ? __ldg(reinterpret_cast<const uint2*>(src.codes + r * s.pitch + c[k]))
+                           : make_uint2(0u, 0u);
+                ne[k] = in ? __ldg(src.exps + r * s.epitch + (c[k] >> 5)) : 1u;
+            } else {
+                nx[k] = raw8(src.x + r * src.ldx, c[k], s.cols);
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        c[k] = static_cast<int64_t>(k * tpr + t) * 8;
+        vec8(w, wide, 1.0f, c[k], s.cols, wv[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = f2(0.0f);
+    }
+    if (row < s.rows) fetch(row);
+    int flip = 0;
+    for (; row < s.rows; row += stride, flip ^= 1) {
+        F2 gv[VPT][4], h[VPT][4];
+        const float rstd = nrstd, mean = nmean;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            pairs(ng[k], gv[k]);
+            if constexpr (CODES) {
+                values8(nc[k], ne[k], h[k]);
+            } else {
+                // columns behind the last have x = 0 and dy = 0: their xh is not 0, but every
+                // use of it is multiplied by that dy or not stored
+                pairs(nx[k], h[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[k][i] = mul2(add2(h[k][i], f2(-mean)), f2(rstd));
+            }
+        }
+        if (row + stride < s.rows) fetch(row + stride);
+        F2 c1 = f2(0.0f), c2 = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                aw[k][i] = fma2(gv[k][i], h[k][i], aw[k][i]);
+                ab[k][i] = add2(ab[k][i], gv[k][i]);
+                gv[k][i] = mul2(gv[k][i], wv[k][i]);
+                c1 = add2(c1, gv[k][i]);
+                c2 = fma2(gv[k][i], h[k][i], c2);
+            }
+        const float2 m = group_sum2(sum2(c1), sum2(c2), buf[flip], wr, g, group);
+        // dx = rstd g - (rstd mean2) xh - rstd mean1
+        const F2 rs = f2(rstd), m1 = f2(-m.x * s.inv_cols * rstd), m2 = f2(-m.y * s.inv_cols * rstd);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (c[k] >= s.cols) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                gv[k][i] = fma2(gv[k][i], rs, fma2(h[k][i], m2, m1));
+            store8(dx + row * lddx, c[k], s.cols, gv[k]);
+        }
+    }
+    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * s.cols;
+    float* out = g.groups > 1 ? shared_cols : pw;
+    for (int q = 0; q < g.groups; ++q) {  // the groups add up their columns one after another
+        if (group == q) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t col = c[k] + i;
+                    if (col < s.cols) {
+                        float a[2], d[2];
+                        split(aw[k][i / 2], a[0], a[1]);
+                        split(ab[k][i / 2], d[0], d[1]);
+                        out[col] = (q ? out[col] : 0.0f) + a[i & 1];
+                        out[s.cols + col] = (q ? out[s.cols + col] : 0.0f) + d[i & 1];
+                    }
+                }
+        }
+        if (g.groups > 1) __syncthreads();
+    }
+    if (g.groups > 1)
+        for (int64_t i = threadIdx.x; i < 2 * s.cols; i += blockDim.x) pw[i] = shared_cols[i];
+}
+
 // ---- host ----------------------------------------------------------------------------------
 
-constexpr int64_t kRegCols8 = 8192;  // columns that the backward block holds (V = 8: 512 x 2 x 8)
+constexpr int64_t kHeldCols = 8192;  // columns of the held form: 512 threads x 2 x 8
 
 int threads_for(int64_t cols, int per_thread, int least, int most) {
     int t = least;
@@ -381,123 +641,173 @@ int threads_for(int64_t cols, int per_thread, int least, int most) {
     return t;
 }
 
-template <typename T, int V, int VPT, bool WARP>
-gq_status forward_run(const T* x, int64_t ldx, const Shape& s, const Affine& af, float eps, T* y,
-                      int64_t ldy, float* mean, float* rstd, int8_t* codes, uint8_t* exps, int rnd,
-                      const Rng& rng, cudaStream_t st) {
-    const int threads = WARP ? 256 : threads_for(s.cols, V * VPT, 128, 512);
-    const int64_t blocks = WARP ? (s.rows + kWarpRows - 1) / kWarpRows : s.rows;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (rnd == GQ_ACT_RANDOM)
-        forward_kernel<T, V, VPT, 1, WARP><<<grid, threads, 0, st>>>(x, ldx, s, af, eps, y, ldy, mean,
-                                                                     rstd, codes, exps, rng);
-    else if (rnd == GQ_ACT_NEAREST)
-        forward_kernel<T, V, VPT, 0, WARP><<<grid, threads, 0, st>>>(x, ldx, s, af, eps, y, ldy, mean,
-                                                                     rstd, codes, exps, rng);
-    else
-        forward_kernel<T, V, VPT, -1, WARP><<<grid, threads, 0, st>>>(x, ldx, s, af, eps, y, ldy, mean,
-                                                                      rstd, codes, exps, rng);
-    return gqh::launch_status();
+// Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.
+struct Held {
+    Groups g;
+    int vpt, threads;
+};
+inline Held held_for(int64_t cols) {
+    Held h;
+    h.vpt = cols <= 4096 ? 1 : 2;
+    h.g.wpr = static_cast<int>((cols + 256 * h.vpt - 1) / (256 * h.vpt));
+    h.g.groups = h.g.wpr < 8 ? 8 / h.g.wpr : 1;
+    h.threads = 32 * h.g.wpr * h.g.groups;
+    return h;
+}
+
+// One wave of resident blocks, or fewer where the rows run out.  The query is remembered by kernel
+// and block size (more shared memory than a launch asks for is never assumed: `smem` is rounded up
+// to the largest that this block size uses).
+template <typename K>
+int wave(K kernel, int threads, size_t smem, int64_t units) {
+    struct Entry {
+        const void* fn;
+        int dev, threads, blocks;
+    };
+    static std::mutex mu;
+    static Entry table[256];
+    static int used = 0;
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    int dev = 0, nb = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        for (int i = 0; i < used && nb == 0; ++i)
+            if (table[i].fn == fn && table[i].dev == dev && table[i].threads == threads)
+                nb = table[i].blocks;
+        if (nb == 0) {
+            const size_t room = smem ? 2 * 1024 * sizeof(float) : 0;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, threads, room) != cudaSuccess ||
+                nb < 1)
+                nb = 1;
+            if (used < 256) table[used++] = Entry{fn, dev, threads, nb};
+        }
+    }
+    const int64_t full = static_cast<int64_t>(nb) * gqh::sm_count();
+    return static_cast<int>(units < full ? units : full);
 }
 
 template <typename T>
-gq_status forward_any(const T* x, int64_t ldx, const Shape& s, const Affine& af, float eps, T* y,
-                      int64_t ldy, float* mean, float* rstd, int8_t* codes, uint8_t* exps, int rnd,
-                      const Rng& rng, bool vec, cudaStream_t st) {
-#define GQA_FWD(V, VPT, WARP) \
-    forward_run<T, V, VPT, WARP>(x, ldx, s, af, eps, y, ldy, mean, rstd, codes, exps, rnd, rng, st)
-    if (vec) {
-        if (s.cols <= 256) return GQA_FWD(8, 1, true);
-        if (s.cols <= 512) return GQA_FWD(8, 2, true);
-        if (s.cols <= 1024) return GQA_FWD(8, 4, true);
-        return GQA_FWD(8, 4, false);
-    }
-    if (s.cols <= 256) return GQA_FWD(1, 8, true);
-    return GQA_FWD(1, 8, false);
-#undef GQA_FWD
-}
-
-// Partial rows of the backward pass: blocks of its main kernel (SUMS), or row shares of the
-// column kernel.
-struct Plan {
-    int parts;
-    int threads;   // of the main kernel
-    bool warp, sums;
-    int vpt;
+struct ForwardCall {
+    const T* x;
+    int64_t ldx;
+    Shape s;
+    Affine af;
+    float eps;
+    T* y;
+    int64_t ldy;
+    float *mean, *rstd;
+    int8_t* codes;
+    uint8_t* exps;
+    Rng rng;
+    cudaStream_t st;
 };
 
-inline Plan backward_plan(int64_t rows, int64_t cols, bool vec) {
-    Plan p;
-    const int sms = gqh::sm_count();
-    if (vec) {
-        p.warp = cols <= 1024;
-        p.sums = cols <= kRegCols8;
-        p.vpt = p.warp ? (cols <= 256 ? 1 : cols <= 512 ? 2 : 4) : 2;
-        p.threads = p.warp ? 256 : threads_for(cols, 16, 128, 512);
-    } else {
-        p.warp = cols <= 256;
-        p.sums = cols <= 4096;
-        p.vpt = 8;
-        p.threads = p.warp ? 256 : threads_for(cols, 8, 128, 512);
-    }
-    const int64_t units = p.warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
-    const int64_t full = static_cast<int64_t>(sms) * (p.threads <= 256 ? 2 : 1);
-    p.parts = static_cast<int>(units < full ? units : full);
-    if (!p.sums) {
-        const int64_t share = (rows + 63) / 64;
-        p.parts = static_cast<int>(share < 64 ? share : 64);
-    }
-    if (p.parts < 1) p.parts = 1;
-    return p;
+template <typename T, int V, int VPT, int RND, bool WARP>
+gq_status forward_generic(const ForwardCall<T>& a) {
+    const int threads = WARP ? 256 : threads_for(a.s.cols, V * VPT, 128, 512);
+    const int64_t blocks = WARP ? (a.s.rows + kWarpRows - 1) / kWarpRows : a.s.rows;
+    forward_kernel<T, V, VPT, RND, WARP><<<static_cast<unsigned>(blocks), threads, 0, a.st>>>(
+        a.x, a.ldx, a.s, a.af, a.eps, a.y, a.ldy, a.mean, a.rstd, a.codes, a.exps, a.rng);
+    return gqh::launch_status();
 }
-
-template <typename T, int V, int VPT, bool WARP, bool SUMS>
-gq_status backward_run(const T* dy, int64_t lddy, const Shape& s, const void* w, int wide,
-                       const float* rstd, const Source<T>& src, T* dx, int64_t lddx, float* partial,
-                       const Plan& p, cudaStream_t st) {
-    const size_t smem = WARP ? 2 * s.cols * sizeof(float) : 0;
-    const unsigned grid = static_cast<unsigned>(SUMS ? p.parts : s.rows);
-    if (src.codes)
-        backward_kernel<T, V, VPT, true, WARP, SUMS><<<grid, p.threads, smem, st>>>(
-            dy, lddy, s, w, wide, rstd, src, dx, lddx, partial);
-    else
-        backward_kernel<T, V, VPT, false, WARP, SUMS><<<grid, p.threads, smem, st>>>(
-            dy, lddy, s, w, wide, rstd, src, dx, lddx, partial);
+template <typename T, int VPT, int RND, int MOST>
+gq_status forward_held(const ForwardCall<T>& a, const Held& h) {
+    auto k = forward_rows<T, VPT, RND, MOST>;
+    const int grid = wave(k, h.threads, 0, (a.s.rows + h.g.groups - 1) / h.g.groups);
+    k<<<grid, h.threads, 0, a.st>>>(a.x, a.ldx, a.s, h.g, a.af, a.eps, a.y, a.ldy, a.mean, a.rstd,
+                                    a.codes, a.exps, a.rng);
     return gqh::launch_status();
 }
 
+template <typename T, int RND>
+gq_status forward_any(const ForwardCall<T>& a, bool vec) {
+    if (!vec) return a.s.cols <= 256 ? forward_generic<T, 1, 8, RND, true>(a)
+                                     : forward_generic<T, 1, 8, RND, false>(a);
+    if (a.s.cols > kHeldCols) return forward_generic<T, 8, 4, RND, false>(a);
+    const Held h = held_for(a.s.cols);
+    if (h.threads <= 256) return forward_held<T, 1, RND, 256>(a, h);
+    return h.vpt == 1 ? forward_held<T, 1, RND, 512>(a, h) : forward_held<T, 2, RND, 512>(a, h);
+}
+
+// Partial rows of the backward pass: at most one per block of its main kernel, or the row shares
+// of the column kernel.
+constexpr int kMostParts = 1024;
+enum Form { kHeld, kScalarWarp, kScalar, kLong };  // kLong: rows that no block holds
+inline Form backward_form(int64_t cols, bool vec) {
+    if (vec) return cols <= kHeldCols ? kHeld : kLong;
+    return cols <= 256 ? kScalarWarp : cols <= 4096 ? kScalar : kLong;
+}
+
 template <typename T>
-gq_status backward_any(const T* dy, int64_t lddy, const Shape& s, const void* w, int wide,
-                       const float* rstd, const Source<T>& src, T* dx, int64_t lddx, void* dw,
-                       void* db, int gdtype, float* partial, bool vec, cudaStream_t st) {
-    const Plan p = backward_plan(s.rows, s.cols, vec);
-    gq_status r;
-#define GQA_BWD(V, VPT, WARP, SUMS) \
-    backward_run<T, V, VPT, WARP, SUMS>(dy, lddy, s, w, wide, rstd, src, dx, lddx, partial, p, st)
-    if (vec)
-        r = p.warp ? (p.vpt == 1   ? GQA_BWD(8, 1, true, true)
-                      : p.vpt == 2 ? GQA_BWD(8, 2, true, true)
-                                   : GQA_BWD(8, 4, true, true))
-                   : (p.sums ? GQA_BWD(8, 2, false, true) : GQA_BWD(8, 2, false, false));
-    else
-        r = p.warp ? GQA_BWD(1, 8, true, true)
-                   : (p.sums ? GQA_BWD(1, 8, false, true) : GQA_BWD(1, 8, false, false));
-#undef GQA_BWD
-    if (r != GQ_OK || (!dw && !db)) return r;
-    if (!p.sums) {
-        const dim3 grid(static_cast<unsigned>((s.cols + 255) / 256), static_cast<unsigned>(p.parts));
-        if (src.codes)
-            columns_kernel<T, true><<<grid, 256, 0, st>>>(dy, lddy, s, rstd, src, partial);
-        else
-            columns_kernel<T, false><<<grid, 256, 0, st>>>(dy, lddy, s, rstd, src, partial);
+struct BackwardCall {
+    const T* dy;
+    int64_t lddy;
+    Shape s;
+    const void* w;
+    int wide;
+    const float* rstd;
+    Source<T> src;
+    T* dx;
+    int64_t lddx;
+    float* partial;
+    cudaStream_t st;
+};
+
+template <typename T, int VPT, bool CODES, int MOST>
+int backward_held(const BackwardCall<T>& a, const Held& h) {
+    const size_t smem = h.g.groups > 1 ? 2 * a.s.cols * sizeof(float) : 0;
+    auto k = backward_rows<T, VPT, CODES, MOST>;
+    int grid = wave(k, h.threads, smem, (a.s.rows + h.g.groups - 1) / h.g.groups);
+    if (grid > kMostParts) grid = kMostParts;
+    k<<<grid, h.threads, smem, a.st>>>(a.dy, a.lddy, a.s, h.g, a.w, a.wide, a.rstd, a.src, a.dx, a.lddx,
+                                       a.partial);
+    return grid;
+}
+template <typename T, int V, int VPT, bool CODES, bool WARP, bool SUMS>
+int backward_generic(const BackwardCall<T>& a) {
+    const int threads = WARP ? 256 : threads_for(a.s.cols, V * VPT, 128, 512);
+    const size_t smem = WARP ? 2 * a.s.cols * sizeof(float) : 0;
+    auto k = backward_kernel<T, V, VPT, CODES, WARP, SUMS>;
+    const int64_t units = WARP ? (a.s.rows + kWarpRows - 1) / kWarpRows : a.s.rows;
+    int64_t grid = SUMS ? wave(k, threads, smem, units) : units;
+    if (SUMS && grid > kMostParts) grid = kMostParts;
+    k<<<static_cast<unsigned>(grid), threads, smem, a.st>>>(a.dy, a.lddy, a.s, a.w, a.wide, a.rstd, a.src,
+                                                           a.dx, a.lddx, a.partial);
+    return static_cast<int>(grid);
+}
+
+template <typename T, bool CODES>
+gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype, bool vec) {
+    const int64_t cols = a.s.cols;
+    const Form form = backward_form(cols, vec);
+    int parts;
+    if (form == kHeld) {
+        const Held h = held_for(cols);
+        parts = h.threads <= 256 ? backward_held<T, 1, CODES, 256>(a, h)
+                : h.vpt == 1     ? backward_held<T, 1, CODES, 512>(a, h)
+                                 : backward_held<T, 2, CODES, 512>(a, h);
+    } else if (form == kScalarWarp) {
+        parts = backward_generic<T, 1, 8, CODES, true, true>(a);
+    } else if (form == kScalar) {
+        parts = backward_generic<T, 1, 8, CODES, false, true>(a);
+    } else {
+        if (vec) backward_generic<T, 8, 2, CODES, false, false>(a);
+        else backward_generic<T, 1, 8, CODES, false, false>(a);
+        parts = static_cast<int>((a.s.rows + 63) / 64 < 64 ? (a.s.rows + 63) / 64 : 64);
+        const dim3 grid(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(parts));
+        if (dw || db)
+            columns_kernel<T, CODES><<<grid, 256, 0, a.st>>>(a.dy, a.lddy, a.s, a.rstd, a.src, a.partial);
     }
-    const unsigned grid = static_cast<unsigned>((2 * s.cols + 31) / 32);
-    if (gdtype == GQ_F32)
-        sum_kernel<float><<<grid, dim3(32, kSumRows), 0, st>>>(
-            partial, p.parts, s.cols, static_cast<float*>(dw), static_cast<float*>(db));
-    else
-        sum_kernel<bf16><<<grid, dim3(32, kSumRows), 0, st>>>(
-            partial, p.parts, s.cols, static_cast<bf16*>(dw), static_cast<bf16*>(db));
+    if (dw || db) {
+        const unsigned grid = static_cast<unsigned>((2 * cols + 31) / 32);
+        if (gdtype == GQ_F32)
+            sum_kernel<float><<<grid, dim3(32, kSumRows), 0, a.st>>>(
+                a.partial, parts, cols, static_cast<float*>(dw), static_cast<float*>(db));
+        else
+            sum_kernel<bf16><<<grid, dim3(32, kSumRows), 0, a.st>>>(
+                a.partial, parts, cols, static_cast<bf16*>(dw), static_cast<bf16*>(db));
+    }
     return gqh::launch_status();
 }
 
@@ -510,8 +820,8 @@ extern "C" {
 size_t gq_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
     if (!size_ok(rows, cols)) return 0;
     if (rows == 0) return 16;
-    const int a = backward_plan(rows, cols, true).parts, b = backward_plan(rows, cols, false).parts;
-    return static_cast<size_t>(a > b ? a : b) * 2 * static_cast<size_t>(cols) * sizeof(float);
+    return static_cast<size_t>(rows < kMostParts ? rows : kMostParts) * 2 *
+           static_cast<size_t>(cols) * sizeof(float);
 }
 
 gq_status gq_layernorm_forward(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
@@ -527,18 +837,21 @@ gq_status gq_layernorm_forward(const void *x, int dtype, int64_t rows, int64_t c
     if (rows == 0) return GQ_OK;
     if (!mean || !rstd || !mult(mean, 4) || !mult(rstd, 4)) return GQ_ERR_INVALID;
     if ((codes || exps) && !saved_ok(codes, exps)) return GQ_ERR_INVALID;
-    const int rnd = codes ? rounding : -1;
     const bool vec = row_align(x, dtype, rows, ldx) && row_align(y, dtype, rows, ldy) &&
                      mult(weight, 16) && mult(bias, 16);
     const Shape s = shape_of(rows, cols);
     const Affine af{weight, bias, wdtype == GQ_F32};
     const Rng rng = make_rng(seed, step);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == GQ_F32)
-        return forward_any(static_cast<const float*>(x), ldx, s, af, eps, static_cast<float*>(y), ldy,
-                           mean, rstd, codes, exps, rnd, rng, vec, st);
-    return forward_any(static_cast<const bf16*>(x), ldx, s, af, eps, static_cast<bf16*>(y), ldy, mean,
-                       rstd, codes, exps, rnd, rng, vec, st);
+    auto run = [&](auto elt) {
+        using T = decltype(elt);
+        const ForwardCall<T> a{static_cast<const T*>(x), ldx, s, af, eps, static_cast<T*>(y), ldy, mean,
+                               rstd, codes, exps, rng, st};
+        return !codes                         ? forward_any<T, -1>(a, vec)
+               : rounding == GQ_ACT_NEAREST ? forward_any<T, 0>(a, vec)
+                                            : forward_any<T, 1>(a, vec);
+    };
+    return dtype == GQ_F32 ? run(float()) : run(bf16());
 }
 
 gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t cols, int64_t lddy,
@@ -572,15 +885,15 @@ gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t
     const bool vec = row_align(dy, dtype, rows, lddy) && row_align(dx, dtype, rows, lddx) &&
                      mult(weight, 16) && (from_codes || row_align(x, dtype, rows, ldx));
     const Shape s = shape_of(rows, cols);
-    float* partial = static_cast<float*>(ws);
-    if (dtype == GQ_F32) {
-        const Source<float> src{codes, exps, static_cast<const float*>(x), ldx, mean};
-        return backward_any(static_cast<const float*>(dy), lddy, s, weight, wdtype == GQ_F32, rstd, src,
-                            static_cast<float*>(dx), lddx, dweight, dbias, gdtype, partial, vec, st);
-    }
-    const Source<bf16> src{codes, exps, static_cast<const bf16*>(x), ldx, mean};
-    return backward_any(static_cast<const bf16*>(dy), lddy, s, weight, wdtype == GQ_F32, rstd, src,
-                        static_cast<bf16*>(dx), lddx, dweight, dbias, gdtype, partial, vec, st);
+    auto run = [&](auto elt) {
+        using T = decltype(elt);
+        const BackwardCall<T> a{static_cast<const T*>(dy), lddy, s, weight, wdtype == GQ_F32, rstd,
+                                Source<T>{codes, exps, static_cast<const T*>(x), ldx, mean},
+                                static_cast<T*>(dx), lddx, static_cast<float*>(ws), st};
+        return from_codes ? backward_any<T, true>(a, dweight, dbias, gdtype, vec)
+                          : backward_any<T, false>(a, dweight, dbias, gdtype, vec);
+    };
+    return dtype == GQ_F32 ? run(float()) : run(bf16());
 }
 
 }  // extern "C"
