@@ -7,7 +7,7 @@
 //
 // Both are bound by memory.  A row stays in registers between its reductions, so it is read
 // once (see "rows held by fixed threads"); the generic kernels at the top take unaligned rows and
-// rows of more than 8,192 columns, and read again what does not fit their registers (from L2,
+// rows of more columns than a block holds, and read again what does not fit their registers (from L2,
 // mostly).  The backward pass keeps dw and db of its threads' columns in registers over all the
 // rows of a block and leaves one partial row per block in the workspace; a second kernel adds
 // those in a fixed order, so that results do not depend on timing.  All sums are fp32.
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
         }
     }
     row_sum<WARP>(sq, buf[1], threads);
-    const float rstd = 1.0f / sqrtf(__fmul_rn(sq[0], s.inv_cols) + eps);
+    const float rstd = rsqrtf(__fmul_rn(sq[0], s.inv_cols) + eps);  // within 2 units
     if (t == 0) {
         mean_out[row] = mean;
         rstd_out[row] = rstd;
@@ -374,60 +374,61 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---- rows held by fixed threads ------------------------------------------------------------
-// The form for 16-byte aligned rows of up to 8,192 columns.  A group of tpr threads (whole warps,
-// cols / 8 or cols / 16 of them) walks over rows; thread t has the same 8 columns of every row (two
-// such pieces where VPT = 2), so that weights, the backward sums and the column part of the random
-// words stay in registers, and the next row is on its way while this one is worked on.
+// The form for 16-byte aligned rows of up to 8,192 columns, a multiple of 8.  A group of 32 wpr
+// threads (whole warps, 16 columns per thread as two pieces of 8; 8 columns up to 256) walks over
+// rows; a thread has the same columns of every row, so that weights, the backward sums and the column
+// part of the random words stay in registers, and the next rows are on their way while one is worked
+// on.  What bounds it is the number of instructions per row beside its elements' own: 16 columns per
+// thread instead of 8 took the backward pass at 65,536 x 1,024 bf16 from 75 to 65 us; no branches
+// depend on the thread either: a thread behind the last column works on copies of the first columns
+// with weights and masks of 0, and only its stores are left out.
 
 struct Groups {
     int wpr;     // warps per row
     int groups;  // rows at a time per block
 };
 
-__device__ __forceinline__ void group_sync(int group, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-}
+// Warps per row, as far as the reductions differ by it.
+enum Wide { kOne = 1, kFour = 4, kMany = 16 };
 
-// Sums over a group's threads.  `buf` must not be written again before the group has passed another
-// barrier: calls alternate between two.
-__device__ __forceinline__ float group_sum(float v, float* buf, int warp_in_row, const Groups& g,
-                                           int group) {
-    v = warp_sum(v);
-    if (g.wpr == 1) return v;
+// Sums of N values (1 or 2) over a group's threads.  `mine`: the group's slots, N per warp, room for
+// 4 warps at least (unused ones hold 0), 16-byte aligned.  They must not be written again before the
+// group has passed another barrier: calls alternate between two sets.
+template <int W, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* mine, int wr, int wpr, int group) {
     const int lane = threadIdx.x & 31;
-    float* mine = buf + group * g.wpr;
-    if (lane == 0) mine[warp_in_row] = v;
-    group_sync(group, g.wpr * 32);
-    if (g.wpr <= 4) {
-        v = mine[0];
-        for (int k = 1; k < g.wpr; ++k) v += mine[k];
-        return v;
-    }
-    return warp_sum(lane < g.wpr ? mine[lane] : 0.0f);
-}
-// Two sums at once: the halves of the warp take one each after the first exchange.
-__device__ __forceinline__ float2 group_sum2(float a, float b, float2* buf, int warp_in_row,
-                                             const Groups& g, int group) {
-    const int lane = threadIdx.x & 31;
-    const bool upper = lane & 16;
-    float v = (upper ? b : a) + __shfl_xor_sync(kFull, upper ? a : b, 16);
+    if constexpr (N == 2) {  // the halves of the warp take one each after the first exchange
+        const bool upper = lane & 16;
+        float x = (upper ? v[1] : v[0]) + __shfl_xor_sync(kFull, upper ? v[0] : v[1], 16);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if (g.wpr == 1) return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
-    float2* mine = buf + group * g.wpr;
-    if ((lane & 15) == 0) reinterpret_cast<float*>(mine + warp_in_row)[lane >> 4] = v;
-    group_sync(group, g.wpr * 32);
-    if (g.wpr <= 4) {
-        float2 r = mine[0];
-        for (int k = 1; k < g.wpr; ++k) {
-            r.x += mine[k].x;
-            r.y += mine[k].y;
+        for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if constexpr (W == kOne) {
+            v[0] = __shfl_sync(kFull, x, 0);
+            v[1] = __shfl_sync(kFull, x, 16);
+            return;
         }
-        return r;
+        if ((lane & 15) == 0) mine[2 * wr + (lane >> 4)] = x;
+    } else {
+        v[0] = warp_sum(v[0]);
+        if constexpr (W == kOne) return;
+        if (lane == 0) mine[wr] = v[0];
     }
-    const float2 r = lane < g.wpr ? mine[lane] : make_float2(0.0f, 0.0f);
-    return make_float2(warp_sum(r.x), warp_sum(r.y));
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+    if constexpr (W == kFour) {
+        const float4 p = reinterpret_cast<const float4*>(mine)[0];
+        if constexpr (N == 2) {
+            const float4 q = reinterpret_cast<const float4*>(mine)[1];
+            v[0] = (p.x + p.z) + (q.x + q.z);
+            v[1] = (p.y + p.w) + (q.y + q.w);
+        } else {
+            v[0] = (p.x + p.y) + (p.z + p.w);
+        }
+    } else if constexpr (W == kMany) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < wpr ? mine[N * lane + k] : 0.0f);
+    }
 }
+constexpr int kSlots = 32;  // per set and value: 8 groups x 4 slots, or 1 group of up to 16 warps
 
 __device__ __forceinline__ void vec8(const void* p, int wide, float none, int64_t c, int64_t cols,
                                      F2 (&v)[4]) {
@@ -437,67 +438,138 @@ __device__ __forceinline__ void vec8(const void* p, int wide, float none, int64_
     for (int i = 0; i < 4; ++i) v[i] = f2(t[2 * i], t[2 * i + 1]);
 }
 
-template <typename T, int VPT, int RND, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
-    forward_rows(const T* __restrict__ x, int64_t ldx, Shape s, Groups g, Affine af, float eps,
-                 T* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
-                 float* __restrict__ rstd_out, int8_t* __restrict__ codes,
-                 uint8_t* __restrict__ exps, Rng rng) {
-    __shared__ float buf[2][16];
-    const int warp = threadIdx.x >> 5, group = warp / g.wpr, wr = warp % g.wpr;
-    const int t = wr * 32 + (threadIdx.x & 31), tpr = g.wpr * 32;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * g.groups;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + group;
-    if (row >= s.rows) return;  // whole groups
-    int64_t c[VPT];
-    F2 w[VPT][4], b[VPT][4];
+// Copies in flight: every thread brings what it will read itself to its own places in shared
+// memory, kDepth - 1 rows ahead, so that no thread waits for another's copy.
+constexpr int kDepth = 4;
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() {  // all but the last kDepth - 1 groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+}
+__device__ __forceinline__ void copy_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// 8 elements of a thread in a slot: planes of 16 bytes per thread.
+template <typename T> struct Ring {
+    static constexpr int kPieces = sizeof(T) / 2;
+    static __device__ __forceinline__ void fetch(uint32_t to, uint32_t plane, const T* p) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            copy_async<16>(to + i * plane, reinterpret_cast<const uint8_t*>(p) + 16 * i);
+    }
+    static __device__ __forceinline__ void read(const uint8_t* at, uint32_t plane, F2 (&v)[4]) {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint4 a = *reinterpret_cast<const uint4*>(at + i * plane);
+            r.w[4 * i] = a.x; r.w[4 * i + 1] = a.y; r.w[4 * i + 2] = a.z; r.w[4 * i + 3] = a.w;
+        }
+        pairs(r, v);
+    }
+};
+
+// p + row * ld elements, in one multiplication: rows and pitches fit 32 bits each (checked on the
+// host for the pitches).
+template <typename P>
+__device__ __forceinline__ P* row_of(P* p, uint32_t row, uint32_t ld_bytes) {
+    return reinterpret_cast<P*>(reinterpret_cast<uintptr_t>(p) + static_cast<uint64_t>(row) * ld_bytes);
+}
+
+// What a launch of the held form is made for.
+struct HeldArgs {
+    uint32_t rows, stride;  // stride: rows at a time of the whole grid
+    uint32_t cols, pitch, epitch;
+    uint32_t in, in2, out;  // bytes from one row to the next
+    int wpr, groups;
+    float inv_cols;
+};
+
+template <typename T, int VPT, int RND, int W, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
+    forward_rows(const T* __restrict__ x, HeldArgs a, Affine af, float eps, T* __restrict__ y,
+                 float* __restrict__ mean_out, float* __restrict__ rstd_out,
+                 int8_t* __restrict__ codes, uint8_t* __restrict__ exps, Rng rng) {
+    __shared__ alignas(16) float buf[2][kSlots];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int warp = threadIdx.x >> 5;
+    const int group = W == kMany ? 0 : warp / a.wpr, wr = warp - group * a.wpr;
+    const uint32_t t = wr * 32 + (threadIdx.x & 31), apart = a.wpr * 256;
+    for (int i = threadIdx.x; i < 2 * kSlots; i += blockDim.x) (&buf[0][0])[i] = 0.0f;
+    __syncthreads();
+    uint32_t row = blockIdx.x * a.groups + group;
+    if (row >= a.rows) return;  // whole groups
+    float* const slots = &buf[0][W == kFour ? group * 4 : 0];
+    bool in[VPT], padded[VPT];  // columns of the matrix; of the codes
+    uint32_t col[VPT];
+    F2 w[VPT][4], b[VPT][4], mask[VPT];
     gq::PhiloxGroup pg[VPT];
-    Raw8<T> next[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        c[k] = static_cast<int64_t>(k * tpr + t) * 8;
-        vec8(af.w, af.wide, 1.0f, c[k], s.cols, w[k]);
-        vec8(af.b, af.wide, 0.0f, c[k], s.cols, b[k]);
+        const uint32_t c = k * apart + t * 8;
+        in[k] = c < a.cols;
+        padded[k] = c < a.pitch;
+        col[k] = in[k] ? c : 0u;
+        mask[k] = f2(in[k] ? 1.0f : 0.0f);
+        vec8(af.w, af.wide, 1.0f, c, a.cols, w[k]);
+        vec8(af.b, af.wide, 0.0f, c, a.cols, b[k]);
         if constexpr (RND == 1)
-            pg[k] = gq::philox_group(static_cast<uint32_t>(c[k] >> 3), rng.step_lo, rng.step_hi, rng.rk);
-        next[k] = raw8(x + row * ldx, c[k], s.cols);
+            pg[k] = gq::philox_group(c >> 3, rng.step_lo, rng.step_hi, rng.rk);
     }
-    for (; row < s.rows; row += stride) {
-        F2 v[VPT][4];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            pairs(next[k], v[k]);
-            if (row + stride < s.rows) next[k] = raw8(x + (row + stride) * ldx, c[k], s.cols);
-        }
-        F2 sum = f2(0.0f);
+    constexpr int P = Ring<T>::kPieces;
+    const uint32_t plane = blockDim.x * 16, slot_bytes = plane * VPT * P;
+    const uint32_t base = gq::smem_u32(ring) + threadIdx.x * 16;
+    uint32_t ahead = row, turn = 0;
+    auto fetch = [&]() {  // (the last row again where there is none)
+        const T* p = row_of(x, min(ahead, a.rows - 1), a.in);
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
+            Ring<T>::fetch(base + (turn & (kDepth - 1)) * slot_bytes + k * P * plane, plane, p + col[k]);
+        copy_commit();
+        ahead += a.stride;
+        ++turn;
+    };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum = add2(sum, v[k][i]);
-        const float mean = group_sum(sum2(sum), buf[0], wr, g, group) * s.inv_cols;
+    for (int d = 0; d < kDepth - 1; ++d) fetch();
+    for (; row < a.rows; row += a.stride) {
+        F2 v[VPT][4];
+        fetch();
+        copy_wait();
+        F2 sum = f2(0.0f);
+        const uint8_t* slot = ring + (turn & (kDepth - 1)) * slot_bytes + threadIdx.x * 16;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            Ring<T>::read(slot + k * P * plane, plane, v[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = fma2(v[k][i], mask[k], sum);
+        }
+        float m[1] = {sum2(sum)};
+        group_sum<W>(m, slots, wr, a.wpr, group);
+        const float mean = m[0] * a.inv_cols;
         F2 sq = f2(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            if (c[k] + 8 <= s.cols) {
+            const F2 less = mul2(mask[k], f2(-mean));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], f2(-mean));
-            } else {  // nothing is subtracted behind the last column
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[k][i] = add2(v[k][i], f2(c[k] + 2 * i < s.cols ? -mean : 0.0f,
-                                               c[k] + 2 * i + 1 < s.cols ? -mean : 0.0f));
+            for (int i = 0; i < 4; ++i) {
+                v[k][i] = fma2(v[k][i], mask[k], less);
+                sq = fma2(v[k][i], v[k][i], sq);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
         }
+        float q[1] = {sum2(sq)};
+        group_sum<W>(q, slots + kSlots, wr, a.wpr, group);
         // not contracted with the sum: y is the same with and without a checkpoint
-        const float var = __fmul_rn(group_sum(sum2(sq), buf[1], wr, g, group), s.inv_cols);
-        const float rstd = 1.0f / sqrtf(var + eps);
+        const float var = __fmul_rn(q[0], a.inv_cols);
+        const float rstd = rsqrtf(var + eps);
         if (t == 0) {
             mean_out[row] = mean;
             rstd_out[row] = rstd;
         }
         const F2 rs = f2(rstd);
+        T* py = row_of(y, row, a.out);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
 #pragma unroll
@@ -506,87 +578,109 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
                 const float inf = __uint_as_float(0x7F800000u);
                 const uint32_t e = exp_byte(block_top8(v[k], var < inf && rstd < inf));
                 uint4 r = make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (RND == 1)
-                    r = gq::philox_row(pg[k], static_cast<uint32_t>(row), rng.step_lo, rng.rk);
-                if (c[k] < s.pitch) {
-                    *reinterpret_cast<uint2*>(codes + row * s.pitch + c[k]) =
-                        codes8<RND == 1>(v[k], e, r);
-                    if ((c[k] & 31) == 0)
-                        exps[row * s.epitch + (c[k] >> 5)] = static_cast<uint8_t>(e);
+                if constexpr (RND == 1) r = gq::philox_row(pg[k], row, rng.step_lo, rng.rk);
+                const uint2 cc = codes8<RND == 1>(v[k], e, r);
+                const uint32_t c = k * apart + t * 8;
+                if (padded[k]) {
+                    *reinterpret_cast<uint2*>(row_of(codes, row, a.pitch) + c) = cc;
+                    if ((t & 3) == 0) row_of(exps, row, a.epitch)[c >> 5] = static_cast<uint8_t>(e);
                 }
             }
-            if (c[k] < s.cols) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][i] = fma2(v[k][i], w[k][i], b[k][i]);
-                store8(y + row * ldy, c[k], s.cols, v[k]);
-            }
+            for (int i = 0; i < 4; ++i) v[k][i] = fma2(v[k][i], w[k][i], b[k][i]);
+            if (in[k]) store8(py + col[k], 0, 8, v[k]);
         }
     }
+    copy_all();
 }
 
 // The block's rows' sums of dy xh and dy go to partial[block][0 and 1][cols].
-template <typename T, int VPT, bool CODES, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
-    backward_rows(const T* __restrict__ dy, int64_t lddy, Shape s, Groups g, const void* w, int wide,
-                  const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx, int64_t lddx,
+template <typename T, int VPT, bool CODES, int W, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
+    backward_rows(const T* __restrict__ dy, HeldArgs a, const void* w, int wide,
+                  const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx,
                   float* __restrict__ partial) {
-    __shared__ float2 buf[2][16];
-    extern __shared__ float shared_cols[];  // 2 x cols, with more than one group
-    const int warp = threadIdx.x >> 5, group = warp / g.wpr, wr = warp % g.wpr;
-    const int t = wr * 32 + (threadIdx.x & 31), tpr = g.wpr * 32;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * g.groups;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + group;
-    int64_t c[VPT];
+    __shared__ alignas(16) float buf[2][2 * kSlots];
+    extern __shared__ __align__(16) uint8_t ring[];  // afterwards 2 x cols sums, with several groups
+    const int warp = threadIdx.x >> 5;
+    const int group = W == kMany ? 0 : warp / a.wpr, wr = warp - group * a.wpr;
+    const uint32_t t = wr * 32 + (threadIdx.x & 31), apart = a.wpr * 256;
+    for (int i = threadIdx.x; i < 4 * kSlots; i += blockDim.x) (&buf[0][0])[i] = 0.0f;
+    __syncthreads();
+    float* const slots = &buf[0][W == kFour ? group * 8 : 0];
+    bool in[VPT];
+    uint32_t col[VPT];
     F2 wv[VPT][4], aw[VPT][4], ab[VPT][4];
-    Raw8<T> ng[VPT], nx[CODES ? 1 : VPT];
-    uint2 nc[CODES ? VPT : 1];
-    uint32_t ne[CODES ? VPT : 1];
-    float nrstd = 0.0f, nmean = 0.0f;
-    auto fetch = [&](int64_t r) {
-        nrstd = __ldg(rstd_in + r);
-        if constexpr (!CODES) nmean = __ldg(src.mean + r);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            ng[k] = raw8(dy + r * lddy, c[k], s.cols);
-            if constexpr (CODES) {
-                const bool in = c[k] < s.pitch;
-                nc[k] = in ? __ldg(reinterpret_cast<const uint2*>(src.codes + r * s.pitch + c[k]))
-                           : make_uint2(0u, 0u);
-                ne[k] = in ? __ldg(src.exps + r * s.epitch + (c[k] >> 5)) : 1u;
-            } else {
-                nx[k] = raw8(src.x + r * src.ldx, c[k], s.cols);
-            }
-        }
-    };
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        c[k] = static_cast<int64_t>(k * tpr + t) * 8;
-        vec8(w, wide, 1.0f, c[k], s.cols, wv[k]);
+        const uint32_t c = k * apart + t * 8;
+        in[k] = c < a.cols;
+        col[k] = in[k] ? c : 0u;
+        vec8(w, wide, 1.0f, c, a.cols, wv[k]);
+        if (!in[k]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wv[k][i] = f2(0.0f);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = f2(0.0f);
     }
-    if (row < s.rows) fetch(row);
-    int flip = 0;
-    for (; row < s.rows; row += stride, flip ^= 1) {
-        F2 gv[VPT][4], h[VPT][4];
-        const float rstd = nrstd, mean = nmean;
+    // a slot: dy's planes of 16 bytes per thread, then x's or those of 8 and 4 for the checkpoint (4
+    // exponent bytes, of which one is this thread's)
+    constexpr int P = Ring<T>::kPieces;
+    const uint32_t n = blockDim.x, tid = threadIdx.x, plane = n * 16;
+    const uint32_t second = plane * VPT * P, third = second + VPT * n * 8;
+    const uint32_t slot_bytes = CODES ? third + VPT * n * 4 : 2 * second;
+    const uint32_t base = gq::smem_u32(ring);
+    uint32_t row = blockIdx.x * a.groups + group, ahead = row, turn = 0;
+    auto fetch = [&]() {  // (the last row again where there is none)
+        const uint32_t r = min(ahead, a.rows - 1), to = base + (turn & (kDepth - 1)) * slot_bytes;
+        const T* p = row_of(dy, r, a.in);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            pairs(ng[k], gv[k]);
+            Ring<T>::fetch(to + k * P * plane + tid * 16, plane, p + col[k]);
             if constexpr (CODES) {
-                values8(nc[k], ne[k], h[k]);
+                copy_async<8>(to + second + (k * n + tid) * 8, row_of(src.codes, r, a.pitch) + col[k]);
+                copy_async<4>(to + third + (k * n + tid) * 4,
+                              row_of(src.exps, r, a.epitch) + col[k] / 128 * 4);
             } else {
-                // columns behind the last have x = 0 and dy = 0: their xh is not 0, but every
-                // use of it is multiplied by that dy or not stored
-                pairs(nx[k], h[k]);
+                Ring<T>::fetch(to + second + k * P * plane + tid * 16, plane,
+                               row_of(src.x, r, a.in2) + col[k]);
+            }
+        }
+        copy_commit();
+        ahead += a.stride;
+        ++turn;
+    };
+    float nrstd = 0.0f, nmean = 0.0f;
+    if (row < a.rows) {
+#pragma unroll
+        for (int d = 0; d < kDepth - 1; ++d) fetch();
+        nrstd = __ldg(rstd_in + row);
+        if constexpr (!CODES) nmean = __ldg(src.mean + row);
+    }
+    float* set = slots;
+    for (; row < a.rows; row += a.stride) {
+        F2 gv[VPT][4], h[VPT][4];
+        const float rstd = nrstd, mean = nmean;
+        const uint32_t next = min(row + a.stride, a.rows - 1);
+        nrstd = __ldg(rstd_in + next);
+        if constexpr (!CODES) nmean = __ldg(src.mean + next);
+        fetch();
+        copy_wait();
+        const uint8_t* slot = ring + (turn & (kDepth - 1)) * slot_bytes;
+        F2 c1 = f2(0.0f), c2 = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            Ring<T>::read(slot + k * P * plane + tid * 16, plane, gv[k]);
+            if constexpr (CODES) {
+                const uint2 q = *reinterpret_cast<const uint2*>(slot + second + (k * n + tid) * 8);
+                const uint32_t e4 = *reinterpret_cast<const uint32_t*>(slot + third + (k * n + tid) * 4);
+                values8(q, e4 >> (col[k] / 32 % 4 * 8) & 0xFFu, h[k]);
+            } else {
+                Ring<T>::read(slot + second + k * P * plane + tid * 16, plane, h[k]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[k][i] = mul2(add2(h[k][i], f2(-mean)), f2(rstd));
             }
-        }
-        if (row + stride < s.rows) fetch(row + stride);
-        F2 c1 = f2(0.0f), c2 = f2(0.0f);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 aw[k][i] = fma2(gv[k][i], h[k][i], aw[k][i]);
@@ -595,40 +689,53 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? 3 : 1)
                 c1 = add2(c1, gv[k][i]);
                 c2 = fma2(gv[k][i], h[k][i], c2);
             }
-        const float2 m = group_sum2(sum2(c1), sum2(c2), buf[flip], wr, g, group);
+        }
+        float m[2] = {sum2(c1), sum2(c2)};
+        group_sum<W>(m, set, wr, a.wpr, group);
+        set = slots + (set == slots ? 2 * kSlots : 0);
         // dx = rstd g - (rstd mean2) xh - rstd mean1
-        const F2 rs = f2(rstd), m1 = f2(-m.x * s.inv_cols * rstd), m2 = f2(-m.y * s.inv_cols * rstd);
+        const float by = -a.inv_cols * rstd;
+        const F2 rs = f2(rstd), m1 = f2(m[0] * by), m2 = f2(m[1] * by);
+        T* p = row_of(dx, row, a.out);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            if (c[k] >= s.cols) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 gv[k][i] = fma2(gv[k][i], rs, fma2(h[k][i], m2, m1));
-            store8(dx + row * lddx, c[k], s.cols, gv[k]);
+            if (in[k]) store8(p + col[k], 0, 8, gv[k]);
         }
     }
-    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * s.cols;
-    float* out = g.groups > 1 ? shared_cols : pw;
-    for (int q = 0; q < g.groups; ++q) {  // the groups add up their columns one after another
-        if (group == q) {
+    copy_all();
+    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    float* shared_cols = reinterpret_cast<float*>(ring);
+    float* out = a.groups > 1 ? shared_cols : pw;
+    for (int q = 0; q < a.groups; ++q) {  // the groups add up their columns one after another
+        if (a.groups > 1) __syncthreads();
+        if (group != q) continue;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            if (!in[k]) continue;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t col = c[k] + i;
-                    if (col < s.cols) {
-                        float a[2], d[2];
-                        split(aw[k][i / 2], a[0], a[1]);
-                        split(ab[k][i / 2], d[0], d[1]);
-                        out[col] = (q ? out[col] : 0.0f) + a[i & 1];
-                        out[s.cols + col] = (q ? out[s.cols + col] : 0.0f) + d[i & 1];
-                    }
+            for (int z = 0; z < 4; ++z) {  // 4 columns of dw, 4 more, the same of db
+                const F2 lo = z < 2 ? aw[k][2 * z] : ab[k][2 * z - 4];
+                const F2 hi = z < 2 ? aw[k][2 * z + 1] : ab[k][2 * z - 3];
+                float4 v;
+                split(lo, v.x, v.y);
+                split(hi, v.z, v.w);
+                float4* at = reinterpret_cast<float4*>(out + (z < 2 ? 0u : a.cols) + col[k] + (z & 1) * 4);
+                if (q > 0) {
+                    const float4 u = *at;
+                    v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
                 }
+                *at = v;
+            }
         }
-        if (g.groups > 1) __syncthreads();
     }
-    if (g.groups > 1)
-        for (int64_t i = threadIdx.x; i < 2 * s.cols; i += blockDim.x) pw[i] = shared_cols[i];
+    if (a.groups > 1) {
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < a.cols / 2; i += blockDim.x)
+            reinterpret_cast<float4*>(pw)[i] = reinterpret_cast<const float4*>(shared_cols)[i];
+    }
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -641,31 +748,59 @@ int threads_for(int64_t cols, int per_thread, int least, int most) {
     return t;
 }
 
-// Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.
+inline bool held_ok(int64_t cols, int64_t ld_bytes) {
+    return cols <= kHeldCols && cols % 8 == 0 && ld_bytes < (int64_t(1) << 32);
+}
+
+// Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.  With
+// fewer rows than two per SM a block takes one at a time: there is nothing to share, and the sums
+// need not be put together within the block.
 struct Held {
-    Groups g;
-    int vpt, threads;
+    int vpt, threads, wpr, groups;
 };
-inline Held held_for(int64_t cols) {
+inline Held held_for(int64_t rows, int64_t cols) {
     Held h;
-    h.vpt = cols <= 4096 ? 1 : 2;
-    h.g.wpr = static_cast<int>((cols + 256 * h.vpt - 1) / (256 * h.vpt));
-    h.g.groups = h.g.wpr < 8 ? 8 / h.g.wpr : 1;
-    h.threads = 32 * h.g.wpr * h.g.groups;
+    h.vpt = cols <= 256 ? 1 : 2;
+    h.wpr = static_cast<int>((cols + 256 * h.vpt - 1) / (256 * h.vpt));
+    h.groups = h.wpr <= 4 && rows > 2 * gqh::sm_count() ? 8 / h.wpr : 1;
+    h.threads = 32 * h.wpr * h.groups;
     return h;
+}
+inline HeldArgs held_args(const Held& h, int grid, const Shape& s, int64_t in, int64_t in2, int64_t out) {
+    HeldArgs a;
+    a.rows = static_cast<uint32_t>(s.rows);
+    a.stride = static_cast<uint32_t>(grid * h.groups);
+    a.cols = static_cast<uint32_t>(s.cols);
+    a.pitch = static_cast<uint32_t>(s.pitch);
+    a.epitch = static_cast<uint32_t>(s.epitch);
+    a.in = static_cast<uint32_t>(in);
+    a.in2 = static_cast<uint32_t>(in2);
+    a.out = static_cast<uint32_t>(out);
+    a.wpr = h.wpr;
+    a.groups = h.groups;
+    a.inv_cols = s.inv_cols;
+    return a;
+}
+// run.template operator()<VPT, W, MOST>() for a shape of the held form
+template <typename F> auto held_switch(const Held& h, F run) {
+    if (h.vpt == 1) return run.template operator()<1, kOne, 256>();
+    if (h.wpr == 1) return run.template operator()<2, kOne, 256>();
+    if (h.wpr <= 4) return run.template operator()<2, kFour, 256>();
+    if (h.wpr <= 8) return run.template operator()<2, kMany, 256>();
+    return run.template operator()<2, kMany, 512>();
 }
 
 // One wave of resident blocks, or fewer where the rows run out.  The query is remembered by kernel
-// and block size (more shared memory than a launch asks for is never assumed: `smem` is rounded up
-// to the largest that this block size uses).
+// and shared memory, which a kernel's block size determines; the kernel's limit on it is raised.
 template <typename K>
 int wave(K kernel, int threads, size_t smem, int64_t units) {
     struct Entry {
         const void* fn;
         int dev, threads, blocks;
+        size_t smem;
     };
     static std::mutex mu;
-    static Entry table[256];
+    static Entry table[512];
     static int used = 0;
     const void* fn = reinterpret_cast<const void*>(kernel);
     int dev = 0, nb = 0;
@@ -673,14 +808,17 @@ int wave(K kernel, int threads, size_t smem, int64_t units) {
     {
         std::lock_guard<std::mutex> lock(mu);
         for (int i = 0; i < used && nb == 0; ++i)
-            if (table[i].fn == fn && table[i].dev == dev && table[i].threads == threads)
+            if (table[i].fn == fn && table[i].dev == dev && table[i].threads == threads &&
+                table[i].smem == smem)
                 nb = table[i].blocks;
         if (nb == 0) {
-            const size_t room = smem ? 2 * 1024 * sizeof(float) : 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, threads, room) != cudaSuccess ||
+            if (smem > 32 * 1024)
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     227 * 1024 - 4096);
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, threads, smem) != cudaSuccess ||
                 nb < 1)
                 nb = 1;
-            if (used < 256) table[used++] = Entry{fn, dev, threads, nb};
+            if (used < 512) table[used++] = Entry{fn, dev, threads, nb, smem};
         }
     }
     const int64_t full = static_cast<int64_t>(nb) * gqh::sm_count();
@@ -711,31 +849,38 @@ gq_status forward_generic(const ForwardCall<T>& a) {
         a.x, a.ldx, a.s, a.af, a.eps, a.y, a.ldy, a.mean, a.rstd, a.codes, a.exps, a.rng);
     return gqh::launch_status();
 }
-template <typename T, int VPT, int RND, int MOST>
-gq_status forward_held(const ForwardCall<T>& a, const Held& h) {
-    auto k = forward_rows<T, VPT, RND, MOST>;
-    const int grid = wave(k, h.threads, 0, (a.s.rows + h.g.groups - 1) / h.g.groups);
-    k<<<grid, h.threads, 0, a.st>>>(a.x, a.ldx, a.s, h.g, a.af, a.eps, a.y, a.ldy, a.mean, a.rstd,
-                                    a.codes, a.exps, a.rng);
-    return gqh::launch_status();
-}
+template <typename T, int RND> struct ForwardHeld {
+    const ForwardCall<T>& a;
+    const Held& h;
+    template <int VPT, int W, int MOST> gq_status operator()() const {
+        auto k = forward_rows<T, VPT, RND, W, MOST>;
+        const size_t smem = static_cast<size_t>(kDepth) * h.threads * VPT * 8 * sizeof(T);
+        const int grid = wave(k, h.threads, smem, (a.s.rows + h.groups - 1) / h.groups);
+        const HeldArgs ha = held_args(h, grid, a.s, a.ldx * sizeof(T), 0, a.ldy * sizeof(T));
+        k<<<grid, h.threads, smem, a.st>>>(a.x, ha, a.af, a.eps, a.y, a.mean, a.rstd, a.codes, a.exps,
+                                           a.rng);
+        return gqh::launch_status();
+    }
+};
 
 template <typename T, int RND>
 gq_status forward_any(const ForwardCall<T>& a, bool vec) {
     if (!vec) return a.s.cols <= 256 ? forward_generic<T, 1, 8, RND, true>(a)
                                      : forward_generic<T, 1, 8, RND, false>(a);
-    if (a.s.cols > kHeldCols) return forward_generic<T, 8, 4, RND, false>(a);
-    const Held h = held_for(a.s.cols);
-    if (h.threads <= 256) return forward_held<T, 1, RND, 256>(a, h);
-    return h.vpt == 1 ? forward_held<T, 1, RND, 512>(a, h) : forward_held<T, 2, RND, 512>(a, h);
+    if (!held_ok(a.s.cols, (a.ldx > a.ldy ? a.ldx : a.ldy) * sizeof(T)))
+        return forward_generic<T, 8, 4, RND, false>(a);
+    const Held h = held_for(a.s.rows, a.s.cols);
+    return held_switch(h, ForwardHeld<T, RND>{a, h});
 }
 
 // Partial rows of the backward pass: at most one per block of its main kernel, or the row shares
 // of the column kernel.
 constexpr int kMostParts = 1024;
 enum Form { kHeld, kScalarWarp, kScalar, kLong };  // kLong: rows that no block holds
-inline Form backward_form(int64_t cols, bool vec) {
-    if (vec) return cols <= kHeldCols ? kHeld : kLong;
+inline Form backward_form(int64_t cols, int64_t ld_bytes, bool vec, size_t elt) {
+    // (the ring of fp32 rows of more than 4,096 columns would pass the shared memory)
+    if (vec && held_ok(cols, ld_bytes) && (elt == 2 || cols <= kHeldCols / 2)) return kHeld;
+    if (vec && cols > kHeldCols / 2) return kLong;
     return cols <= 256 ? kScalarWarp : cols <= 4096 ? kScalar : kLong;
 }
 
@@ -754,16 +899,26 @@ struct BackwardCall {
     cudaStream_t st;
 };
 
-template <typename T, int VPT, bool CODES, int MOST>
-int backward_held(const BackwardCall<T>& a, const Held& h) {
-    const size_t smem = h.g.groups > 1 ? 2 * a.s.cols * sizeof(float) : 0;
-    auto k = backward_rows<T, VPT, CODES, MOST>;
-    int grid = wave(k, h.threads, smem, (a.s.rows + h.g.groups - 1) / h.g.groups);
-    if (grid > kMostParts) grid = kMostParts;
-    k<<<grid, h.threads, smem, a.st>>>(a.dy, a.lddy, a.s, h.g, a.w, a.wide, a.rstd, a.src, a.dx, a.lddx,
-                                       a.partial);
-    return grid;
-}
+template <typename T, bool CODES> struct BackwardHeld {
+    const BackwardCall<T>& a;
+    const Held& h;
+    template <int VPT, int W, int MOST> int operator()() const {
+        if constexpr (MOST == 512 && sizeof(T) == 4) {
+            return 0;  // not reached: backward_form
+        } else {
+            // (also room for 2 x cols sums: 64 bytes per thread and piece at least)
+            const size_t smem = static_cast<size_t>(kDepth) * h.threads * VPT *
+                                (CODES ? 8 * sizeof(T) + 12 : 16 * sizeof(T));
+            auto k = backward_rows<T, VPT, CODES, W, MOST>;
+            int grid = wave(k, h.threads, smem, (a.s.rows + h.groups - 1) / h.groups);
+            if (grid > kMostParts) grid = kMostParts;
+            const HeldArgs ha = held_args(h, grid, a.s, a.lddy * sizeof(T), a.src.ldx * sizeof(T),
+                                          a.lddx * sizeof(T));
+            k<<<grid, h.threads, smem, a.st>>>(a.dy, ha, a.w, a.wide, a.rstd, a.src, a.dx, a.partial);
+            return grid;
+        }
+    }
+};
 template <typename T, int V, int VPT, bool CODES, bool WARP, bool SUMS>
 int backward_generic(const BackwardCall<T>& a) {
     const int threads = WARP ? 256 : threads_for(a.s.cols, V * VPT, 128, 512);
@@ -780,13 +935,13 @@ int backward_generic(const BackwardCall<T>& a) {
 template <typename T, bool CODES>
 gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype, bool vec) {
     const int64_t cols = a.s.cols;
-    const Form form = backward_form(cols, vec);
+    int64_t ld = a.lddy > a.lddx ? a.lddy : a.lddx;
+    if (a.src.ldx > ld) ld = a.src.ldx;
+    const Form form = backward_form(cols, ld * sizeof(T), vec, sizeof(T));
     int parts;
     if (form == kHeld) {
-        const Held h = held_for(cols);
-        parts = h.threads <= 256 ? backward_held<T, 1, CODES, 256>(a, h)
-                : h.vpt == 1     ? backward_held<T, 1, CODES, 512>(a, h)
-                                 : backward_held<T, 2, CODES, 512>(a, h);
+        const Held h = held_for(a.s.rows, cols);
+        parts = held_switch(h, BackwardHeld<T, CODES>{a, h});
     } else if (form == kScalarWarp) {
         parts = backward_generic<T, 1, 8, CODES, true, true>(a);
     } else if (form == kScalar) {
