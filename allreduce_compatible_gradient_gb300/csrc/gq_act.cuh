@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 namespace gqa {
 
@@ -173,6 +174,29 @@ __device__ __forceinline__ void store(T* p, int64_t c, int64_t cols, const float
         if (c + i < cols) down(v[i], p[c + i]);
 }
 
+// ---- copies in flight ----------------------------------------------------------------------
+// Every thread brings what it will read itself to its own places in shared memory, kDepth - 1 rows
+// ahead, so that no thread waits for another's copy: about 70 KB in flight per SM where latency
+// times bandwidth asks for 36, without a register for it.
+constexpr int kDepth = 4;
+// Through L1: a thread's 32 bytes are two copies, and past L1 (cp.async.cg) each would fetch the
+// 32-byte sector that they share (32,768 x 4,096 bf16 to codes: 95 us so, 64 us through L1).
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last D - 1 groups have landed.
+template <int D = kDepth> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+}
+__device__ __forceinline__ void copy_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// `bytes` of 16 (0..16), the rest zeros.
+__device__ __forceinline__ void copy_part(uint32_t to, const void* from, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+
 // ---- pairs of fp32 -------------------------------------------------------------------------
 // One instruction on two fp32 numbers (sm_100 and later), each rounded as its scalar form: what
 // bounds these kernels beside memory is the number of instructions issued.
@@ -245,76 +269,6 @@ __device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_
     return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
 }
 
-// Codes of V elements (V = 1: in the low byte).  Nearest: x / step + 1.5 * 2^23 leaves the integer
-// nearest to x / step, ties to even, in the low byte (one rounding, the product is exact).
-// Random: x / step * 2^16 + 1.5 * 2^24 keeps 128 + x / step in units of 2^-15 in the fraction;
-// doubled and increased by the 16-bit random number, bits 16..23 hold floor(128 + x / step + u).
-// c is the element's column (a multiple of V), row its row.
-template <int V, bool RANDOM>
-__device__ __forceinline__ void codes_of(const float (&v)[V], uint32_t e, uint32_t row, uint32_t c,
-                                         const Rng& rng, uint32_t (&w)[(V + 3) / 4]) {
-    const float inv = inv_step(e);
-    uint32_t t[V];
-    if constexpr (RANDOM) {
-#pragma unroll
-        for (int g = 0; g < (V + 7) / 8; ++g) {
-            const uint4 r = gq::philox4x32_10_rk(
-                make_uint4((c >> 3) + g, row, rng.step_lo, rng.step_hi), rng.rk);
-            const uint32_t word[4] = {r.x, r.y, r.z, r.w};
-            if constexpr (V == 1) {
-                const uint32_t q = (c & 4) ? ((c & 2) ? r.w : r.z) : ((c & 2) ? r.y : r.x);
-                const uint32_t h = (c & 1) ? q >> 16 : q & 0xFFFFu;
-                t[0] = (__float_as_uint(__fmaf_rn(v[0] * inv, 65536.0f, 25165824.0f)) << 1) + h;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t h = (i & 1) ? word[i >> 1] >> 16 : word[i >> 1] & 0xFFFFu;
-                    t[8 * g + i] = (__float_as_uint(__fmaf_rn(v[8 * g + i] * inv, 65536.0f,
-                                                              25165824.0f)) << 1) + h;
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = __float_as_uint(__fmaf_rn(v[i], inv, 12582912.0f));
-    }
-    constexpr int B = RANDOM ? 2 : 0;
-    constexpr uint32_t flip = RANDOM ? 0x80808080u : 0u;
-    if constexpr (V == 1) {
-        w[0] = ((t[0] >> (8 * B)) ^ flip) & 0xFFu;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-            w[i] = gather_bytes<B>(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]) ^ flip;
-    }
-    if (e == 255u) {
-#pragma unroll
-        for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0u;
-    }
-}
-
-// Quantises the V elements at column c of `row` and writes their codes, and the block's exponent
-// byte from its first lane.  Called by every lane of the warp; lanes with live = false (past the
-// last row) only take part in the reduction.  Columns past cols hold 0 and have code 0.
-template <int V, bool RANDOM>
-__device__ __forceinline__ void save(const float (&v)[V], bool live, uint32_t row, uint32_t c,
-                                     int64_t pitch, int64_t epitch, const Rng& rng, int8_t* codes,
-                                     uint8_t* exps) {
-    const uint32_t e = exp_byte(block_top<V>(v));
-    uint32_t w[(V + 3) / 4];
-    codes_of<V, RANDOM>(v, e, row, c, rng, w);
-    if (!live) return;
-    int8_t* p = codes + static_cast<int64_t>(row) * pitch + c;
-    if constexpr (V == 16)
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else if constexpr (V == 8)
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else
-        *p = static_cast<int8_t>(w[0]);
-    if ((c & (kBlk - 1)) == 0)
-        exps[static_cast<int64_t>(row) * epitch + (c >> 5)] = static_cast<uint8_t>(e);
-}
-
 // The same for 8 columns held as pairs: largest magnitude of the lane's 8 and of the block's 4
 // lanes.  Maxima of floating-point numbers pass over a NaN, so `plain` says that there is none
 // (and no infinity); otherwise the bits are compared.
@@ -362,6 +316,66 @@ __device__ __forceinline__ uint2 codes8(const F2 (&h)[4], uint32_t e, const uint
                          gather_bytes<B>(t[4], t[5], t[6], t[7]) ^ flip);
     if (e == 255u) w = make_uint2(0u, 0u);
     return w;
+}
+
+// Codes of V elements (V = 1: in the low byte).  Nearest: x / step + 1.5 * 2^23 leaves the integer
+// nearest to x / step, ties to even, in the low byte (one rounding, the product is exact).
+// Random: x / step * 2^16 + 1.5 * 2^24 keeps 128 + x / step in units of 2^-15 in the fraction;
+// doubled and increased by the 16-bit random number, bits 16..23 hold floor(128 + x / step + u).
+// c is the element's column (a multiple of V), row its row; pg the part of the random words
+// that depends on the columns (V = 16: of two calls).
+template <int V, bool RANDOM>
+__device__ __forceinline__ void codes_of(const float (&v)[V], uint32_t e, uint32_t row, uint32_t c,
+                                         const Rng& rng, const gq::PhiloxGroup (&pg)[(V + 7) / 8],
+                                         uint32_t (&w)[(V + 3) / 4]) {
+    const float inv = inv_step(e);
+    if constexpr (V == 1) {
+        if constexpr (RANDOM) {
+            const uint4 r = gq::philox_row(pg[0], row, rng.step_lo, rng.rk);
+            const uint32_t q = (c & 4) ? ((c & 2) ? r.w : r.z) : ((c & 2) ? r.y : r.x);
+            const uint32_t t = (__float_as_uint(__fmaf_rn(v[0] * inv, 65536.0f, 25165824.0f)) << 1) +
+                               ((c & 1) ? q >> 16 : q & 0xFFFFu);
+            w[0] = ((t >> 16) ^ 0x80u) & 0xFFu;
+        } else {
+            w[0] = __float_as_uint(__fmaf_rn(v[0], inv, 12582912.0f)) & 0xFFu;
+        }
+        if (e == 255u) w[0] = 0u;
+    } else {
+#pragma unroll
+        for (int g = 0; g < V / 8; ++g) {
+            F2 h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = f2(v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
+            uint4 r = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (RANDOM) r = gq::philox_row(pg[g], row, rng.step_lo, rng.rk);
+            const uint2 q = codes8<RANDOM>(h, e, r);
+            w[2 * g] = q.x;
+            w[2 * g + 1] = q.y;
+        }
+    }
+}
+
+// Quantises the V elements at column c of `row` and writes their codes, and the block's exponent
+// byte from its first lane.  Called by every lane of the warp; lanes with live = false (past the
+// last row) only take part in the reduction.  Columns past cols hold 0 and have code 0.
+template <int V, bool RANDOM>
+__device__ __forceinline__ void save(const float (&v)[V], bool live, uint32_t row, uint32_t c,
+                                     int64_t pitch, int64_t epitch, const Rng& rng,
+                                     const gq::PhiloxGroup (&pg)[(V + 7) / 8], int8_t* codes,
+                                     uint8_t* exps) {
+    const uint32_t e = exp_byte(block_top<V>(v));
+    uint32_t w[(V + 3) / 4];
+    codes_of<V, RANDOM>(v, e, row, c, rng, pg, w);
+    if (!live) return;
+    int8_t* p = codes + static_cast<int64_t>(row) * pitch + c;
+    if constexpr (V == 16)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (V == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+        *p = static_cast<int8_t>(w[0]);
+    if ((c & (kBlk - 1)) == 0)
+        exps[static_cast<int64_t>(row) * epitch + (c >> 5)] = static_cast<uint8_t>(e);
 }
 
 // The values of 8 codes as pairs.
@@ -458,6 +472,12 @@ __device__ __forceinline__ void saved(const int8_t* p, const uint8_t* pe, int64_
     values_of<V>(w, pe[c >> 5], v);
 }
 
+// p + row * ld elements, in one multiplication: rows and their distance in bytes fit 32 bits each.
+template <typename P>
+__device__ __forceinline__ P* row_of(P* p, uint32_t row, uint32_t ld_bytes) {
+    return reinterpret_cast<P*>(reinterpret_cast<uintptr_t>(p) + static_cast<uint64_t>(row) * ld_bytes);
+}
+
 // ---- host checks ---------------------------------------------------------------------------
 
 inline bool mult(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -481,6 +501,39 @@ inline int row_align(const void* p, int dtype, int64_t rows, int64_t ld) {
     const int64_t step = rows > 1 ? ld * elt_bytes(dtype) : 0;
     if (mult(p, 32) && step % 32 == 0) return 32;
     return mult(p, 16) && step % 16 == 0 ? 16 : 0;
+}
+
+// Blocks of a kernel that are resident on the whole GPU.  The query is remembered; the kernel's limit
+// on shared memory is raised first where it asks for much.
+template <typename K> int64_t resident_blocks(K kernel, int threads, size_t smem) {
+    struct Entry {
+        const void* fn;
+        int dev, threads, blocks;
+        size_t smem;
+    };
+    static std::mutex mu;
+    static Entry table[512];
+    static int used = 0;
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    int dev = 0, nb = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        for (int i = 0; i < used && nb == 0; ++i)
+            if (table[i].fn == fn && table[i].dev == dev && table[i].threads == threads &&
+                table[i].smem == smem)
+                nb = table[i].blocks;
+        if (nb == 0) {
+            if (smem > 32 * 1024)
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     227 * 1024 - 4096);
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, threads, smem) != cudaSuccess ||
+                nb < 1)
+                nb = 1;
+            if (used < 512) table[used++] = Entry{fn, dev, threads, nb, smem};
+        }
+    }
+    return static_cast<int64_t>(nb) * gqh::sm_count();
 }
 
 }  // namespace gqa

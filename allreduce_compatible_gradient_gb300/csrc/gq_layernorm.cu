@@ -13,8 +13,6 @@
 // those in a fixed order, so that results do not depend on timing.  All sums are fp32.
 #include "gq_act.cuh"
 
-#include <mutex>
-
 using namespace gqa;
 
 namespace {
@@ -141,8 +139,13 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = z[i] * rstd;
         if constexpr (RND >= 0)
+        {
+            gq::PhiloxGroup pg[1];
+            if constexpr (RND == 1)
+                pg[0] = gq::philox_group(static_cast<uint32_t>(c >> 3), rng.step_lo, rng.step_hi, rng.rk);
             save<V, RND == 1>(z, c < s.pitch, static_cast<uint32_t>(row), static_cast<uint32_t>(c),
-                              s.pitch, s.epitch, rng, codes, exps);
+                              s.pitch, s.epitch, rng, pg, codes, exps);
+        }
         if (c < s.cols) {
             float w[V], b[V];
             vec_of<V>(af.w, af.wide, 1.0f, c, s.cols, w);
@@ -438,21 +441,6 @@ __device__ __forceinline__ void vec8(const void* p, int wide, float none, int64_
     for (int i = 0; i < 4; ++i) v[i] = f2(t[2 * i], t[2 * i + 1]);
 }
 
-// Copies in flight: every thread brings what it will read itself to its own places in shared
-// memory, kDepth - 1 rows ahead, so that no thread waits for another's copy.
-constexpr int kDepth = 4;
-template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_wait() {  // all but the last kDepth - 1 groups have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-}
-__device__ __forceinline__ void copy_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // 8 elements of a thread in a slot: planes of 16 bytes per thread.
 template <typename T> struct Ring {
     static constexpr int kPieces = sizeof(T) / 2;
@@ -471,13 +459,6 @@ template <typename T> struct Ring {
         pairs(r, v);
     }
 };
-
-// p + row * ld elements, in one multiplication: rows and pitches fit 32 bits each (checked on the
-// host for the pitches).
-template <typename P>
-__device__ __forceinline__ P* row_of(P* p, uint32_t row, uint32_t ld_bytes) {
-    return reinterpret_cast<P*>(reinterpret_cast<uintptr_t>(p) + static_cast<uint64_t>(row) * ld_bytes);
-}
 
 // What a launch of the held form is made for.
 struct HeldArgs {
@@ -790,40 +771,8 @@ template <typename F> auto held_switch(const Held& h, F run) {
     return run.template operator()<2, kMany, 512>();
 }
 
-// One wave of resident blocks, or fewer where the rows run out.  The query is remembered by kernel
-// and shared memory, which a kernel's block size determines; the kernel's limit on it is raised.
-template <typename K>
-int wave(K kernel, int threads, size_t smem, int64_t units) {
-    struct Entry {
-        const void* fn;
-        int dev, threads, blocks;
-        size_t smem;
-    };
-    static std::mutex mu;
-    static Entry table[512];
-    static int used = 0;
-    const void* fn = reinterpret_cast<const void*>(kernel);
-    int dev = 0, nb = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        for (int i = 0; i < used && nb == 0; ++i)
-            if (table[i].fn == fn && table[i].dev == dev && table[i].threads == threads &&
-                table[i].smem == smem)
-                nb = table[i].blocks;
-        if (nb == 0) {
-            if (smem > 32 * 1024)
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     227 * 1024 - 4096);
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, threads, smem) != cudaSuccess ||
-                nb < 1)
-                nb = 1;
-            if (used < 512) table[used++] = Entry{fn, dev, threads, nb, smem};
-        }
-    }
-    const int64_t full = static_cast<int64_t>(nb) * gqh::sm_count();
-    return static_cast<int>(units < full ? units : full);
-}
+// One wave of resident blocks, or fewer where the rows run out.
+int wave(int64_t resident, int64_t units) { return static_cast<int>(units < resident ? units : resident); }
 
 template <typename T>
 struct ForwardCall {
@@ -855,7 +804,7 @@ template <typename T, int RND> struct ForwardHeld {
     template <int VPT, int W, int MOST> gq_status operator()() const {
         auto k = forward_rows<T, VPT, RND, W, MOST>;
         const size_t smem = static_cast<size_t>(kDepth) * h.threads * VPT * 8 * sizeof(T);
-        const int grid = wave(k, h.threads, smem, (a.s.rows + h.groups - 1) / h.groups);
+        const int grid = wave(resident_blocks(k, h.threads, smem), (a.s.rows + h.groups - 1) / h.groups);
         const HeldArgs ha = held_args(h, grid, a.s, a.ldx * sizeof(T), 0, a.ldy * sizeof(T));
         k<<<grid, h.threads, smem, a.st>>>(a.x, ha, a.af, a.eps, a.y, a.mean, a.rstd, a.codes, a.exps,
                                            a.rng);
@@ -910,7 +859,7 @@ template <typename T, bool CODES> struct BackwardHeld {
             const size_t smem = static_cast<size_t>(kDepth) * h.threads * VPT *
                                 (CODES ? 8 * sizeof(T) + 12 : 16 * sizeof(T));
             auto k = backward_rows<T, VPT, CODES, W, MOST>;
-            int grid = wave(k, h.threads, smem, (a.s.rows + h.groups - 1) / h.groups);
+            int grid = wave(resident_blocks(k, h.threads, smem), (a.s.rows + h.groups - 1) / h.groups);
             if (grid > kMostParts) grid = kMostParts;
             const HeldArgs ha = held_args(h, grid, a.s, a.lddy * sizeof(T), a.src.ldx * sizeof(T),
                                           a.lddx * sizeof(T));
@@ -925,7 +874,7 @@ int backward_generic(const BackwardCall<T>& a) {
     const size_t smem = WARP ? 2 * a.s.cols * sizeof(float) : 0;
     auto k = backward_kernel<T, V, VPT, CODES, WARP, SUMS>;
     const int64_t units = WARP ? (a.s.rows + kWarpRows - 1) / kWarpRows : a.s.rows;
-    int64_t grid = SUMS ? wave(k, threads, smem, units) : units;
+    int64_t grid = SUMS ? wave(resident_blocks(k, threads, smem), units) : units;
     if (SUMS && grid > kMostParts) grid = kMostParts;
     k<<<static_cast<unsigned>(grid), threads, smem, a.st>>>(a.dy, a.lddy, a.s, a.w, a.wide, a.rstd, a.src,
                                                            a.dx, a.lddx, a.partial);
