@@ -12,9 +12,10 @@
 // One persistent block per SM computes tiles of (128 MH) outs x BN columns:
 //   warp 0      TMA loads of dy (64 tokens x 64 outs per box, 128-byte swizzle, outs contiguous)
 //   warp 1      one thread issues tcgen05.mma, accumulators in TMEM
-//   warps 2-9   read codes and exponents from global memory into registers one stage ahead, widen
+//   the others  read codes and exponents from global memory into registers one turn ahead, widen
 //               them to bf16 in shared memory in the layout of the other operand, and store
-//               finished tiles from TMEM
+//               finished tiles from TMEM; two teams take turns at the steps, so that the latency
+//               of a load or of a barrier is that of two steps' time
 // Both operands are contiguous along their outer dimension ("MN-major"), so neither is transposed.
 // The k range of all tiles is one list of 64-token steps, cut into equal contiguous shares, one
 // per block: a tile that two or more blocks share leaves fp32 partial tiles in the workspace,
@@ -28,7 +29,9 @@ using namespace gqa;
 namespace {
 
 constexpr int kTok = 64;              // tokens per step
-constexpr int kConvWarps = 8;         // warps 2..9
+constexpr int kConvWarps = 16;        // warps 2..17, in
+constexpr int kTeams = 2;             // teams that take turns at the steps
+constexpr int kTeam = 32 * kConvWarps / kTeams;  // threads of a team
 constexpr int kWThreads = 64 + 32 * kConvWarps;
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
 
@@ -136,12 +139,31 @@ __device__ __forceinline__ uint32_t widen2(uint32_t p, __nv_bfloat162 s) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The contiguous steps [u0, u1) of a block.
+// The contiguous steps [u0, u1) of a block, and a place in them: a tile, and a step of that tile.  The
+// place moves on by counting; a 64-bit division per step and thread had cost a third of the issue
+// slots.
 struct Share {
     int64_t u0, u1;
     __device__ __forceinline__ Share(int64_t units, int block, int blocks) {
         u0 = units * block / blocks;
         u1 = units * (block + 1) / blocks;
+    }
+};
+struct At {
+    int64_t left;  // steps of the share from here on
+    int tile, k;
+    __device__ __forceinline__ At(const Share& s, int ksteps)
+        : left(s.u1 - s.u0), tile(static_cast<int>(s.u0 / ksteps)), k(static_cast<int>(s.u0 % ksteps)) {}
+    __device__ __forceinline__ void next(int ksteps) {
+        --left;
+        if (++k == ksteps) {
+            k = 0;
+            ++tile;
+        }
+    }
+    // steps of the tile at hand that are in the share
+    __device__ __forceinline__ int segment(int ksteps) const {
+        return static_cast<int>(min(left, static_cast<int64_t>(ksteps - k)));
     }
 };
 
@@ -186,7 +208,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             gq::mbar_init(gq::smem_u32(&full_a[s]), 1u);
-            gq::mbar_init(gq::smem_u32(&full_b[s]), kConvWarps);
+            gq::mbar_init(gq::smem_u32(&full_b[s]), kConvWarps / kTeams);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
@@ -205,17 +227,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane == 0) {
             uint32_t n = 0;
             bool ok = true;
-            for (int64_t u = share.u0; u < share.u1 && ok; ++u, ++n) {
+            for (At at(share, a.ksteps); at.left > 0 && ok; at.next(a.ksteps), ++n) {
                 const int s = n % S;
                 if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                 if (!ok) break;
-                const int tile = static_cast<int>(u / a.ksteps), k = static_cast<int>(u % a.ksteps);
                 const uint32_t bar = gq::smem_u32(&full_a[s]);
                 gq::mbar_arrive_expect_tx(bar, Cfg::kABytes);
-                const int o0 = (tile % a.tiles_m) * Cfg::kOuts;
+                const int o0 = (at.tile % a.tiles_m) * Cfg::kOuts;
 #pragma unroll
                 for (int c = 0; c < 2 * MH; ++c)
-                    tma_load(a_stage(s) + c * kChunk, &dy_map, o0 + 64 * c, k * kTok, bar);
+                    tma_load(a_stage(s) + c * kChunk, &dy_map, o0 + 64 * c, at.k * kTok, bar);
             }
             // nothing of this block's is in flight when it ends, whatever the others did
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
@@ -225,8 +246,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane == 0) {
             uint32_t n = 0, seg = 0;
             bool ok = true;
-            for (int64_t u = share.u0; u < share.u1 && ok;) {
-                const int k = static_cast<int>(u % a.ksteps);
+            int k = static_cast<int>(share.u0 % a.ksteps);
+            for (int64_t u = share.u0; u < share.u1 && ok; k = 0) {
                 const int64_t end = min(share.u1, u - k + a.ksteps);
                 if (seg > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (seg - 1) & 1);
                 fence_after();
@@ -255,47 +276,74 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
         }
     } else {
-        const int ct = threadIdx.x - 64;
-        constexpr int kPer = BN * kTok / 16 / (32 * kConvWarps);  // 16-code pieces per thread
+        const int team = (threadIdx.x - 64) / kTeam, ct = (threadIdx.x - 64) % kTeam;
+        constexpr int kPer = BN * kTok / 16 / kTeam;  // 16-code pieces per thread and step
         constexpr int kRowPieces = BN / 16;
+        // this thread's pieces of a step: every kTokStep-th token, the same 16 columns
+        static_assert(kTeam % kRowPieces == 0, "a thread keeps its columns");
+        const int col = (ct % kRowPieces) * 16, tok = ct / kRowPieces;
+        constexpr int kTokStep = kTeam / kRowPieces;
         uint4 w[kPer];
         uint32_t e[kPer];
-        auto fetch = [&](int64_t u) {
-            const int tile = static_cast<int>(u / a.ksteps), k = static_cast<int>(u % a.ksteps);
-            const int64_t t0 = (k % a.ktok) * kTok;
-            const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int q = ct + j * 32 * kConvWarps;
-                const int64_t t = t0 + q / kRowPieces, i = i0 + (q % kRowPieces) * 16;
-                const bool in = t < a.rows && i < a.pitch;
-                w[j] = in ? __ldg(reinterpret_cast<const uint4*>(a.codes + t * a.pitch + i))
-                          : make_uint4(0, 0, 0, 0);
-                e[j] = in ? __ldg(a.exps + t * a.epitch + (i >> 5)) : 0u;
+        At ahead(share, a.ksteps);
+        int part = ahead.k % static_cast<int>(a.ktok);  // step within the part of dy
+        const int8_t* pc = nullptr;   // codes and exponents of the thread's first piece of the
+        const uint8_t* pe = nullptr;  // step `ahead`
+        bool in_cols = false;
+        const int rows_left = static_cast<int>(min(a.rows - tok, int64_t(1) << 30));
+        auto place = [&]() {
+            const int64_t i = static_cast<int64_t>(ahead.tile / a.tiles_m) * BN + col;
+            const int64_t t = static_cast<int64_t>(part) * kTok + tok;
+            in_cols = i < a.pitch;
+            pc = a.codes + t * a.pitch + i;
+            pe = a.exps + t * a.epitch + (i >> 5);
+        };
+        auto advance = [&]() {
+            ahead.next(a.ksteps);
+            if (++part == a.ktok || ahead.k == 0) {  // a part of dy, or a tile, begins
+                part = 0;
+                place();
+            } else {
+                pc += kTok * a.pitch;
+                pe += kTok * a.epitch;
             }
         };
+        auto fetch = [&]() {  // the step `ahead`, and on to the team's next
+            const int left = rows_left - part * kTok;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const bool in = in_cols && j * kTokStep < left;
+                w[j] = in ? __ldg(reinterpret_cast<const uint4*>(pc + j * kTokStep * a.pitch))
+                          : make_uint4(0, 0, 0, 0);
+                e[j] = in ? __ldg(pe + j * kTokStep * a.epitch) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < kTeams; ++j) advance();
+        };
+        place();
+        for (int j = 0; j < team; ++j) advance();
+        if (ahead.left > 0) fetch();
         uint32_t n = 0, seg = 0;
         bool ok = true;
-        if (share.u0 < share.u1) fetch(share.u0);
-        for (int64_t u = share.u0; u < share.u1;) {
-            const int k0 = static_cast<int>(u % a.ksteps);
-            const int tile = static_cast<int>(u / a.ksteps);
-            const int64_t end = min(share.u1, u - k0 + a.ksteps);
-            const bool whole = k0 == 0 && end - u == a.ksteps;
-            for (; u < end; ++u, ++n) {
+        At at(share, a.ksteps);
+        while (at.left > 0) {
+            const int steps = at.segment(a.ksteps), tile = at.tile;
+            const bool whole = at.k == 0 && steps == a.ksteps, from_first = at.k == 0;
+            for (int z = 0; z < steps; ++z, ++n) {
+                at.next(a.ksteps);
+                if (static_cast<int>(n % kTeams) != team) continue;
                 const int s = n % S;
                 uint4 cw[kPer];
                 uint32_t ce[kPer];
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
-                if (u + 1 < share.u1) fetch(u + 1);
+                if (ahead.left > 0) fetch();
                 if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                 ok = __all_sync(kFull, ok);
                 if (!ok) continue;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
-                    const int q = ct + j * 32 * kConvWarps;
-                    const int t = q / kRowPieces, c = q % kRowPieces;  // token, 16-column piece
+                    const int t = tok + j * kTokStep, c = col / 16;  // token, 16-column piece
                     const uint32_t sc = ce[j] << 7 | ce[j] << 23;
                     const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
                     const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
@@ -319,18 +367,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 __syncwarp();
                 if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full_b[s]));
             }
-            // the finished tile: 4 warps take the 128 lanes of TMEM, the two groups of 4 share
-            // the halves (or, with one half, its columns)
+            // the finished tile: 4 warps take the 128 lanes of TMEM, the groups of 4 share the columns
             if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
             ok = __all_sync(kFull, ok);
             fence_after();
             const int quad = warp & 3, group = (warp - 2) >> 2;
-            const int h = MH == 2 ? group : 0;
-            const int c0 = MH == 2 ? 0 : group * (BN / 2), c1 = MH == 2 ? BN : c0 + BN / 2;
+            constexpr int kGroups = kConvWarps / 4, kShare = MH * BN / kGroups;
+            const int h = group * kShare / BN, c0 = group * kShare % BN, c1 = c0 + kShare;
             const int r = h * 128 + quad * 32 + lane;
             const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * Cfg::kOuts + r;
             const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
-            float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) *
+            float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (from_first ? 1 : 0)) *
                                           (Cfg::kOuts * BN) + static_cast<int64_t>(r) * BN;
             const float dbo = whole && a.shift && o < a.outs ? a.db[o] : 0.0f;
             for (int c = c0; c < c1; c += 32) {
