@@ -9,17 +9,25 @@
 // part is applied to the finished sums.  fp32 gradients are cut into three bf16 parts (8 + 8 + 8
 // bits, exact), laid one after another along t.
 //
-// One persistent block per SM computes tiles of (128 MH) outs x BN columns:
+// Persistent blocks compute tiles of outs x columns; a large tile (512 x 256) belongs to a pair of
+// blocks, each with 256 of its outs (two accumulators of 128 x 256, all of TMEM) and 128 of its columns
+// as operands, on which one tcgen05.mma of both tensor cores works.  In each block:
 //   warp 0      TMA loads of dy (64 tokens x 64 outs per box, 128-byte swizzle, outs contiguous)
-//   warp 1      one thread issues tcgen05.mma, accumulators in TMEM
+//   warp 1      one thread (of the pair's first block) issues tcgen05.mma, accumulators in TMEM
 //   the others  read codes and exponents from global memory into registers one turn ahead, widen
 //               them to bf16 in shared memory in the layout of the other operand, and store
 //               finished tiles from TMEM; two teams take turns at the steps, so that the latency
 //               of a load or of a barrier is that of two steps' time
 // Both operands are contiguous along their outer dimension ("MN-major"), so neither is transposed.
-// The k range of all tiles is one list of 64-token steps, cut into equal contiguous shares, one
-// per block: a tile that two or more blocks share leaves fp32 partial tiles in the workspace,
-// which join_kernel adds in a fixed order.
+// Why pairs: shared memory moves 128 bytes per cycle, and one block with a 256 x 256 tile asks for 160
+// (operands 96, dy's arrival 32, the widened codes 32): it ran at 74 % of the MMA rate.  A pair shares
+// the widened codes, and asks for 112.
+//
+// The steps (64 tokens) of all tiles are one list, cut into equal contiguous shares, one per block or
+// pair: a tile that two or more of them work on leaves fp32 partial tiles in the workspace, which
+// join_kernel adds in a fixed order.  The tensor cores' fp32 accumulation rounds each sum of 16 products
+// towards zero or nearly so, an error that grows with the length of the chain (7.8e-6 of the result's
+// norm over 16,384 tokens): a chain ends after kChain steps, and the rest is added to it in fp32 outside.
 #include "gq_act.cuh"
 
 #include <cuda.h>
@@ -29,21 +37,27 @@ using namespace gqa;
 namespace {
 
 constexpr int kTok = 64;              // tokens per step
+constexpr int kChain = 128;           // steps of one accumulation
 constexpr int kConvWarps = 16;        // warps 2..17, in
 constexpr int kTeams = 2;             // teams that take turns at the steps
 constexpr int kTeam = 32 * kConvWarps / kTeams;  // threads of a team
 constexpr int kWThreads = 64 + 32 * kConvWarps;
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
 
-template <int MH, int BN> struct Tile {
-    static constexpr int kOuts = 128 * MH;
+// CG blocks work on a tile, each on MH x 128 of its outs; BN columns, BN / CG widened by each block.
+template <int CG_, int MH_, int BN_> struct Tile {
+    static constexpr int CG = CG_, MH = MH_, BN = BN_;
+    static constexpr int kOuts = 128 * MH;            // of a block
+    static constexpr int kRows = kOuts * CG;          // of the tile
+    static constexpr int kOwn = BN / CG;              // columns widened by a block
     static constexpr int kABytes = kOuts * kTok * 2;
-    static constexpr int kBBytes = BN * kTok * 2;
-    static constexpr int kStages = (kABytes + kBBytes) * 3 <= 200 * 1024
-                                       ? ((kABytes + kBBytes) * 6 <= 200 * 1024 ? 6 : 3) : 2;
-    static constexpr int kCols = MH * BN;  // TMEM columns: a power of two >= 32
+    static constexpr int kBBytes = kOwn * kTok * 2;
+    static constexpr int kStages = 192 * 1024 / (kABytes + kBBytes);
+    static constexpr int kCols = MH * BN;             // TMEM columns: a power of two >= 32
     static constexpr int kSmem = kStages * (kABytes + kBBytes) + 1024;
 };
+using Large = Tile<2, 2, 256>;
+using Small = Tile<1, 1, 128>;
 
 struct WArgs {
     int64_t rows, outs, cols, pitch, epitch, ldw;
@@ -54,7 +68,7 @@ struct WArgs {
     const float* db;
     void* dw;
     int out_f32;
-    int vec;              // dw rows are 16-byte aligned
+    int vec;              // dw rows are 32-, 16- or 0-byte aligned
     float* partial;
     int64_t ktok;         // tokens of one part, rounded up to whole steps, in steps
     int ksteps;           // steps of a tile: parts * ktok
@@ -63,27 +77,70 @@ struct WArgs {
 };
 
 // ---- tcgen05 -------------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+#define GQA_CG(CG, one, two, ...)                     \
+    do {                                              \
+        if constexpr ((CG) == 1) asm volatile(one __VA_ARGS__); \
+        else asm volatile(two __VA_ARGS__);           \
+    } while (0)
+template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t cols) {
+    GQA_CG(CG, "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;",
+           "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;",
+           ::"r"(smem), "r"(cols) : "memory");
+    GQA_CG(CG, "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;",
+           "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;", ::);
 }
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+template <int CG> __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    GQA_CG(CG, "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;",
+           "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;", ::"r"(addr), "r"(cols));
 }
+template <int CG>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
+    GQA_CG(CG,
+           "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+           "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}",
+           "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+           "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}",
+           ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
+// Arrives on this barrier of every block of the tile when the MMAs issued so far are done.
+template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+// The pair: this block's rank, an arrival on the same barrier in the first block, and a barrier of both
+// blocks.  What an arrival announces are operands in shared memory, made visible to the tensor cores
+// by a proxy fence or written by the TMA, and registers read from TMEM, ordered by a tcgen05 fence; no
+// thread of the other block reads them with ordinary loads, so the arrival is not a release at cluster
+// scope (which waits for every store of the thread: 1,600 cycles, most of a step).
+template <int CG> __device__ __forceinline__ uint32_t pair_rank() {
+    uint32_t r = 0;
+    if constexpr (CG == 2) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+template <int CG> __device__ __forceinline__ void arrive_first(uint32_t bar) {
+    if constexpr (CG == 1) {
+        gq::mbar_arrive(bar);
+    } else {
+        uint32_t there;
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(bar));
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
+    }
+}
+template <int CG> __device__ __forceinline__ void pair_sync() {
+    if constexpr (CG == 2) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
 }
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -113,10 +170,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t smem) {
            (static_cast<uint64_t>(kChunk >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// fp32 accumulator, bf16 operands, both contiguous along their outer dimension, M = 128, N = BN.
-template <int BN> struct Instruction {
+// fp32 accumulator, bf16 operands, both contiguous along their outer dimension, M = 128 per block.
+template <int CG, int BN> struct Instruction {
     static constexpr uint32_t value = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                                      (static_cast<uint32_t>(BN >> 3) << 17) | (128u >> 4 << 24);
+                                      (static_cast<uint32_t>(BN >> 3) << 17) | ((128u * CG) >> 4 << 24);
 };
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -167,61 +224,85 @@ struct At {
     }
 };
 
-// Row o0 + r of a tile's output or partial tile: 32 columns from TMEM.
-template <typename O>
-__device__ __forceinline__ void put(O* p, int64_t i, int64_t cols, int vec, const float (&v)[32]) {
-    if (vec && i + 32 <= cols) {
-        if constexpr (sizeof(O) == 4) {
+template <typename O> __device__ __forceinline__ void tail(O* p, int left, const float (&w)[8]) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                reinterpret_cast<float4*>(p + i)[k] =
-                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    for (int k = 0; k < 8; ++k)
+        if (k < left) down(w[k], p[k]);
+}
+
+// N consecutive columns of a row of dw from fp32 sums: times scale, plus db shift, rounded.
+template <int N>
+__device__ __forceinline__ void finish(const WArgs& a, int64_t o, int64_t i, float (&v)[N]) {
+    if (o >= a.outs || i >= a.cols) return;
+    if (a.scale) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i + k < a.cols) v[k] = v[k] * __ldg(a.scale + i + k);
+    }
+    if (a.shift) {
+        const float d = __ldg(a.db + o);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i + k < a.cols) v[k] = fmaf(d, __ldg(a.shift + i + k), v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+        const float w[8] = {v[k], v[k + 1], v[k + 2], v[k + 3], v[k + 4], v[k + 5], v[k + 6], v[k + 7]};
+        const int left = static_cast<int>(min(a.cols - i - k, int64_t(8)));
+        if (a.out_f32) {
+            float* p = static_cast<float*>(a.dw) + o * a.ldw + i + k;
+            if (a.vec == 32) store<float, 8, 32>(p, 0, left, w);
+            else if (a.vec) store<float, 8, 16>(p, 0, left, w);
+            else tail(p, left, w);
         } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                reinterpret_cast<uint4*>(p + i)[k] =
-                    make_uint4(pack2(v[8 * k], v[8 * k + 1], bf16()),
-                               pack2(v[8 * k + 2], v[8 * k + 3], bf16()),
-                               pack2(v[8 * k + 4], v[8 * k + 5], bf16()),
-                               pack2(v[8 * k + 6], v[8 * k + 7], bf16()));
+            bf16* p = static_cast<bf16*>(a.dw) + o * a.ldw + i + k;
+            if (a.vec) store<bf16, 8, 16>(p, 0, left, w);
+            else tail(p, left, w);
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            if (i + k < cols) down(v[k], p[i + k]);
     }
 }
 
-template <int MH, int BN>
+// Where a partial tile keeps 8 columns of a row: blocks of 32 rows x 32 columns, in which the 32 rows'
+// 32 bytes of the same 8 columns lie side by side, so that a warp with a row per lane writes and reads
+// 1,024 bytes in a row.
+template <int BN> __device__ __forceinline__ int64_t partial_at(int row, int col) {
+    return static_cast<int64_t>((row >> 5) * (BN / 32) + (col >> 5)) * 1024 + (col >> 3 & 3) * 256 +
+           (row & 31) * 8;
+}
+
+template <typename C>
 __global__ void __launch_bounds__(kWThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const WArgs a) {
-    using Cfg = Tile<MH, BN>;
-    constexpr int S = Cfg::kStages;
+    constexpr int CG = C::CG, MH = C::MH, BN = C::BN, S = C::kStages;
     extern __shared__ uint8_t raw[];
-    __shared__ alignas(8) uint64_t full_a[S], full_b[S], empty[S], acc_full, acc_empty, drain;
+    // full: everything of a step is there (in the pair's first block); full_a: the second block's dy
+    __shared__ alignas(8) uint64_t full[S], full_a[S], empty[S], acc_full, acc_empty, drain;
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto a_stage = [&](int s) { return base + s * Cfg::kABytes; };
-    auto b_stage = [&](int s) { return base + S * Cfg::kABytes + s * Cfg::kBBytes; };
+    const uint32_t rank = pair_rank<CG>();
+    auto a_stage = [&](int s) { return base + s * C::kABytes; };
+    auto b_stage = [&](int s) { return base + S * C::kABytes + s * C::kBBytes; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
+            // the widening warps of a team in each block, and each block's dy
+            gq::mbar_init(gq::smem_u32(&full[s]), CG * (kConvWarps / kTeams + 1));
             gq::mbar_init(gq::smem_u32(&full_a[s]), 1u);
-            gq::mbar_init(gq::smem_u32(&full_b[s]), kConvWarps / kTeams);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
-        gq::mbar_init(gq::smem_u32(&acc_empty), kConvWarps);
+        gq::mbar_init(gq::smem_u32(&acc_empty), CG * kConvWarps);
         gq::mbar_init(gq::smem_u32(&drain), 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc(gq::smem_u32(&tmem_slot), Cfg::kCols);
+    if (warp == 1) tmem_alloc<CG>(gq::smem_u32(&tmem_slot), C::kCols);
     fence_before();
     __syncthreads();
+    pair_sync<CG>();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const Share share(a.units, blockIdx.x, gridDim.x);
+    const Share share(a.units, blockIdx.x / CG, gridDim.x / CG);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -231,30 +312,28 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 const int s = n % S;
                 if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                 if (!ok) break;
-                const uint32_t bar = gq::smem_u32(&full_a[s]);
-                gq::mbar_arrive_expect_tx(bar, Cfg::kABytes);
-                const int o0 = (at.tile % a.tiles_m) * Cfg::kOuts;
+                const uint32_t bar = gq::smem_u32(rank == 0 ? &full[s] : &full_a[s]);
+                gq::mbar_arrive_expect_tx(bar, C::kABytes);
+                const int o0 = (at.tile % a.tiles_m) * C::kRows + static_cast<int>(rank) * C::kOuts;
 #pragma unroll
                 for (int c = 0; c < 2 * MH; ++c)
                     tma_load(a_stage(s) + c * kChunk, &dy_map, o0 + 64 * c, at.k * kTok, bar);
             }
             // nothing of this block's is in flight when it ends, whatever the others did
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
-                gq::mbar_wait(gq::smem_u32(&full_a[j % S]), (j / S) & 1);
+                gq::mbar_wait(gq::smem_u32(rank == 0 ? &full[j % S] : &full_a[j % S]), (j / S) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             uint32_t n = 0, seg = 0;
             bool ok = true;
-            int k = static_cast<int>(share.u0 % a.ksteps);
-            for (int64_t u = share.u0; u < share.u1 && ok; k = 0) {
-                const int64_t end = min(share.u1, u - k + a.ksteps);
+            for (At at(share, a.ksteps); at.left > 0 && ok; ++seg) {
+                const int steps = min(at.segment(a.ksteps), kChain);
                 if (seg > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (seg - 1) & 1);
                 fence_after();
-                for (bool first = true; u < end && ok; ++u, ++n, first = false) {
+                for (int z = 0; z < steps && ok; ++z, ++n) {
                     const int s = n % S;
-                    ok = gq::mbar_wait(gq::smem_u32(&full_a[s]), (n / S) & 1) &&
-                         gq::mbar_wait(gq::smem_u32(&full_b[s]), (n / S) & 1);
+                    ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
                     if (!ok) break;
                     fence_after();
 #pragma unroll
@@ -262,23 +341,31 @@ __global__ void __launch_bounds__(kWThreads, 1)
                         const uint64_t b = operand(b_stage(s) + kk * 2048);
 #pragma unroll
                         for (int h = 0; h < MH; ++h)
-                            mma_bf16(tmem + h * BN, operand(a_stage(s) + h * 2 * kChunk + kk * 2048), b,
-                                     Instruction<BN>::value, !first || kk > 0);
+                            mma_bf16<CG>(tmem + h * BN,
+                                         operand(a_stage(s) + h * 2 * kChunk + kk * 2048), b,
+                                         Instruction<CG, BN>::value, z > 0 || kk > 0);
                     }
-                    mma_commit(gq::smem_u32(&empty[s]));
+                    mma_commit<CG>(gq::smem_u32(&empty[s]));
+                    at.next(a.ksteps);
                 }
-                if (ok) mma_commit(gq::smem_u32(&acc_full));
-                ++seg;
+                if (ok) mma_commit<CG>(gq::smem_u32(&acc_full));
             }
             if (!ok) {  // let what was issued finish before TMEM is given back
-                mma_commit(gq::smem_u32(&drain));
+                mma_commit<CG>(gq::smem_u32(&drain));
                 gq::mbar_wait(gq::smem_u32(&drain), 0);
+            }
+        } else if (lane == 0) {  // the second block: tells the first that its dy has arrived
+            uint32_t n = 0;
+            bool ok = true;
+            for (At at(share, a.ksteps); at.left > 0 && ok; at.next(a.ksteps), ++n) {
+                ok = gq::mbar_wait(gq::smem_u32(&full_a[n % S]), (n / S) & 1);
+                if (ok) arrive_first<CG>(gq::smem_u32(&full[n % S]));
             }
         }
     } else {
         const int team = (threadIdx.x - 64) / kTeam, ct = (threadIdx.x - 64) % kTeam;
-        constexpr int kPer = BN * kTok / 16 / kTeam;  // 16-code pieces per thread and step
-        constexpr int kRowPieces = BN / 16;
+        constexpr int kPer = C::kOwn * kTok / 16 / kTeam;  // 16-code pieces per thread and step
+        constexpr int kRowPieces = C::kOwn / 16;
         // this thread's pieces of a step: every kTokStep-th token, the same 16 columns
         static_assert(kTeam % kRowPieces == 0, "a thread keeps its columns");
         const int col = (ct % kRowPieces) * 16, tok = ct / kRowPieces;
@@ -292,7 +379,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         bool in_cols = false;
         const int rows_left = static_cast<int>(min(a.rows - tok, int64_t(1) << 30));
         auto place = [&]() {
-            const int64_t i = static_cast<int64_t>(ahead.tile / a.tiles_m) * BN + col;
+            const int64_t i = static_cast<int64_t>(ahead.tile / a.tiles_m) * BN + rank * C::kOwn + col;
             const int64_t t = static_cast<int64_t>(part) * kTok + tok;
             in_cols = i < a.pitch;
             pc = a.codes + t * a.pitch + i;
@@ -327,149 +414,145 @@ __global__ void __launch_bounds__(kWThreads, 1)
         bool ok = true;
         At at(share, a.ksteps);
         while (at.left > 0) {
-            const int steps = at.segment(a.ksteps), tile = at.tile;
-            const bool whole = at.k == 0 && steps == a.ksteps, from_first = at.k == 0;
-            for (int z = 0; z < steps; ++z, ++n) {
-                at.next(a.ksteps);
-                if (static_cast<int>(n % kTeams) != team) continue;
-                const int s = n % S;
-                uint4 cw[kPer];
-                uint32_t ce[kPer];
+            const int tile = at.tile;
+            int left = at.segment(a.ksteps);
+            const bool whole = at.k == 0 && left == a.ksteps, from_first = at.k == 0;
+            for (bool first = true; left > 0; first = false, ++seg) {  // the chains of the segment
+                const int steps = min(left, kChain);
+                left -= steps;
+                for (int z = 0; z < steps; ++z, ++n) {
+                    at.next(a.ksteps);
+                    if (static_cast<int>(n % kTeams) != team) continue;
+                    const int s = n % S;
+                    uint4 cw[kPer];
+                    uint32_t ce[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
-                if (ahead.left > 0) fetch();
-                if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                    for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
+                    if (ahead.left > 0) fetch();
+                    if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) continue;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        const int t = tok + j * kTokStep, c = col / 16;  // token, 16-column piece
+                        const uint32_t sc = ce[j] << 7 | ce[j] << 23;
+                        const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
+                        const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            o[2 * m] = widen2(__byte_perm(in[m], 0x43434343u, 0x4140), sv);
+                            o[2 * m + 1] = widen2(__byte_perm(in[m], 0x43434343u, 0x4342), sv);
+                        }
+                        // 16-byte unit v of row t of a 64-column chunk sits at unit v ^ (t mod 8)
+                        const uint32_t row = b_stage(s) + (c >> 2) * kChunk + t * 128;
+                        const uint32_t v0 = (2 * (c & 3)) ^ (t & 7);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + v0 * 16),
+                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (v0 ^ 1) * 16),
+                                     "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                     : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) arrive_first<CG>(gq::smem_u32(&full[s]));
+                }
+                // the chain's sums: 4 warps take the 128 lanes of TMEM, the groups of 4 share the
+                // columns
+                if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
                 ok = __all_sync(kFull, ok);
-                if (!ok) continue;
+                fence_after();
+                const int quad = warp & 3, group = (warp - 2) >> 2;
+                constexpr int kGroups = kConvWarps / 4, kShare = MH * BN / kGroups;
+                const int h = group * kShare / BN, c0 = group * kShare % BN;
+                const int r = static_cast<int>(rank) * C::kOuts + h * 128 + quad * 32 + lane;
+                const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * C::kRows + r;
+                const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
+                float* part_tile = a.partial + (static_cast<int64_t>(blockIdx.x / CG) * 2 +
+                                                (from_first ? 1 : 0)) * (C::kRows * BN);
+                const bool last = whole && left == 0;
+#pragma unroll 1
+                for (int c = c0; c < c0 + kShare; c += 32) {
+                    uint32_t acc[32];
+                    if (ok) {
+                        tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * BN + c, acc);
+                    } else {  // a wait gave up: the tile is marked, not left as it was
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int t = tok + j * kTokStep, c = col / 16;  // token, 16-column piece
-                    const uint32_t sc = ce[j] << 7 | ce[j] << 23;
-                    const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
-                    const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        o[2 * m] = widen2(__byte_perm(in[m], 0x43434343u, 0x4140), sv);
-                        o[2 * m + 1] = widen2(__byte_perm(in[m], 0x43434343u, 0x4342), sv);
+                        for (int k = 0; k < 32; ++k) acc[k] = 0x7FFFFFFFu;
                     }
-                    // 16-byte unit v of row t of a 64-column chunk sits at unit v ^ (t mod 8)
-                    const uint32_t row = b_stage(s) + (c >> 2) * kChunk + t * 128;
-                    const uint32_t v0 = (2 * (c & 3)) ^ (t & 7);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + v0 * 16),
-                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (v0 ^ 1) * 16),
-                                 "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                 : "memory");
+                    float v[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
+                    float* p = part_tile + partial_at<BN>(r, c);
+                    if (!first) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 x = reinterpret_cast<const float4*>(p + 256 * k)[0];
+                            const float4 y = reinterpret_cast<const float4*>(p + 256 * k)[1];
+                            v[8 * k] += x.x; v[8 * k + 1] += x.y; v[8 * k + 2] += x.z; v[8 * k + 3] += x.w;
+                            v[8 * k + 4] += y.x; v[8 * k + 5] += y.y; v[8 * k + 6] += y.z; v[8 * k + 7] += y.w;
+                        }
+                    }
+                    if (last) {
+                        finish(a, o, i0 + c, v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[8 * k + j]);
+                            st32<32>(p + 256 * k, u);
+                        }
+                    }
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fence_before();
                 __syncwarp();
-                if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full_b[s]));
+                if (lane == 0) arrive_first<CG>(gq::smem_u32(&acc_empty));
             }
-            // the finished tile: 4 warps take the 128 lanes of TMEM, the groups of 4 share the columns
-            if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
-            ok = __all_sync(kFull, ok);
-            fence_after();
-            const int quad = warp & 3, group = (warp - 2) >> 2;
-            constexpr int kGroups = kConvWarps / 4, kShare = MH * BN / kGroups;
-            const int h = group * kShare / BN, c0 = group * kShare % BN, c1 = c0 + kShare;
-            const int r = h * 128 + quad * 32 + lane;
-            const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * Cfg::kOuts + r;
-            const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
-            float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (from_first ? 1 : 0)) *
-                                          (Cfg::kOuts * BN) + static_cast<int64_t>(r) * BN;
-            const float dbo = whole && a.shift && o < a.outs ? a.db[o] : 0.0f;
-            for (int c = c0; c < c1; c += 32) {
-                uint32_t acc[32];
-                if (ok) {
-                    tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * BN + c, acc);
-                } else {  // a wait gave up: the tile is marked, not left as it was
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) acc[k] = 0x7FFFFFFFu;
-                }
-                float v[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
-                if (!whole) {
-                    put<float>(part, c, BN, 1, v);
-                    continue;
-                }
-                if (o >= a.outs || i0 + c >= a.cols) continue;
-                if (a.scale) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int64_t i = i0 + c + k;
-                        if (i < a.cols) v[k] = v[k] * __ldg(a.scale + i);
-                    }
-                }
-                if (a.shift) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int64_t i = i0 + c + k;
-                        if (i < a.cols) v[k] = fmaf(dbo, __ldg(a.shift + i), v[k]);
-                    }
-                }
-                if (a.out_f32)
-                    put(static_cast<float*>(a.dw) + o * a.ldw, i0 + c, a.cols, a.vec, v);
-                else
-                    put(static_cast<bf16*>(a.dw) + o * a.ldw, i0 + c, a.cols, a.vec, v);
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) gq::mbar_arrive(gq::smem_u32(&acc_empty));
-            ++seg;
         }
     }
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free(tmem, Cfg::kCols);
+    pair_sync<CG>();  // neither block's memory is in use any more
+    if (warp == 1) tmem_free<CG>(tmem, C::kCols);
+    pair_sync<CG>();
 }
 
-// Adds the partial tiles of every tile that more than one block worked on, in block order.
-// blockIdx.x = tile, blockIdx.y = a share of its rows; thread = 4 columns.
-template <int MH, int BN>
-__global__ void __launch_bounds__(256) join_kernel(const WArgs a, int blocks) {
-    constexpr int kOuts = Tile<MH, BN>::kOuts;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * a.ksteps;
-    const int64_t last = first + a.ksteps - 1;
-    auto owner = [&](int64_t u) {  // the block whose share holds step u
-        int64_t b = u * blocks / a.units;
-        while (b + 1 < blocks && a.units * (b + 1) / blocks <= u) ++b;
-        while (b > 0 && a.units * b / blocks > u) --b;
-        return b;
-    };
-    const int64_t b0 = owner(first), b1 = owner(last);
-    if (b0 == b1) return;  // stored by its one block
-    const int64_t om = static_cast<int64_t>(blockIdx.x % a.tiles_m) * kOuts;
-    const int64_t im = static_cast<int64_t>(blockIdx.x / a.tiles_m) * BN;
-    constexpr int kQuads = BN / 4;
-    const int rows = kOuts / gridDim.y;
-    for (int q = threadIdx.x; q < rows * kQuads; q += 256) {
-        const int r = blockIdx.y * rows + q / kQuads, c = (q % kQuads) * 4;
-        const int64_t o = om + r, i = im + c;
-        if (o >= a.outs || i >= a.cols) continue;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t b = b0; b <= b1; ++b) {
-            // a share that begins at the tile's first step is in slot 1, any other in slot 0
-            const int64_t u0 = a.units * b / blocks;
-            const int slot = u0 <= first ? 1 : 0;
-            const float4 p = *reinterpret_cast<const float4*>(
-                a.partial + (b * 2 + slot) * (kOuts * BN) + static_cast<int64_t>(r) * BN + c);
-            v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
-        }
-        const float dbo = a.shift ? a.db[o] : 0.0f;
+// Adds the partial tiles of every tile that more than one share has a part of, in the shares' order.
+// blockIdx.x = tile; thread = 8 columns of a row, 32 rows of the same columns per warp.
+template <typename C> __global__ void __launch_bounds__(256) join_kernel(const WArgs a, int shares) {
+    constexpr int BN = C::BN;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * a.ksteps, last = first + a.ksteps - 1;
+    __shared__ int owners[2];
+    if (threadIdx.x < 2) {  // the share that holds the tile's first step, and its last
+        const int64_t u = threadIdx.x ? last : first;
+        int64_t b = u * shares / a.units;
+        while (b + 1 < shares && a.units * (b + 1) / shares <= u) ++b;
+        while (b > 0 && a.units * b / shares > u) --b;
+        // a share that begins at the tile's first step keeps it in slot 1, any other in slot 0
+        owners[threadIdx.x] = static_cast<int>(2 * b + (a.units * b / shares <= first ? 1 : 0));
+    }
+    __syncthreads();
+    const int b0 = owners[0], b1 = owners[1];
+    if (b0 / 2 == b1 / 2) return;  // stored by its one share
+    constexpr int kPieces = C::kRows * BN / 8;
+#pragma unroll 1
+    for (int q = blockIdx.y * 256 + threadIdx.x; q < kPieces; q += gridDim.y * 256) {
+        // q counts rows of 32, then the four 8-column pieces of a 32-column block, then blocks
+        const int r = (q >> 7) / (BN / 32) * 32 + (q & 31);
+        const int c = (q >> 7) % (BN / 32) * 32 + (q >> 5 & 3) * 8;
+        float v[8] = {};
+#pragma unroll 2
+        for (int b = b0; b <= b1; b = (b | 1) + 1) {  // slot b0, then slot 0 of the shares after it
+            uint32_t w[8];
+            ld32<32>(a.partial + static_cast<int64_t>(b) * (C::kRows * BN) + partial_at<BN>(r, c), w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (i + k >= a.cols) break;
-            if (a.scale) v[k] *= a.scale[i + k];
-            if (a.shift) v[k] = fmaf(dbo, a.shift[i + k], v[k]);
-            if (a.out_f32)
-                static_cast<float*>(a.dw)[o * a.ldw + i + k] = v[k];
-            else
-                static_cast<bf16*>(a.dw)[o * a.ldw + i + k] = __float2bfloat16_rn(v[k]);
+            for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[k]);
         }
+        finish(a, static_cast<int64_t>(blockIdx.x % a.tiles_m) * C::kRows + r,
+               static_cast<int64_t>(blockIdx.x / a.tiles_m) * BN + c, v);
     }
 }
 
@@ -574,11 +657,11 @@ EncodeFn encode_fn() {
 }
 
 struct WPlan {
-    bool big;            // 256 x 256 tiles, else 128 x 128
+    bool big;            // pairs of blocks on 512 x 256 tiles, else 128 x 128
     bool pack;
     int parts;           // bf16 parts of dy
     int64_t ktok, ksteps, tiles_m, tiles_n, units, pitch;
-    int blocks, shares;  // of the main kernel; of the bias sums
+    int shares, bias_shares;  // of the steps; of the rows in the bias sums
     size_t pack_off, bias_off, db_off, bytes;
 };
 
@@ -589,25 +672,26 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.pack = dtype == GQ_F32 || row_align(dy, dtype, rows, ld) == 0;
     p.ktok = (rows + kTok - 1) / kTok;
     p.ksteps = p.ktok * p.parts;
-    const int64_t big = ((outs + 255) / 256) * ((cols + 255) / 256) * p.ksteps;
-    p.big = big >= 16 * sms && outs > 128 && cols > 128;
-    const int side = p.big ? 256 : 128;
-    p.tiles_m = (outs + side - 1) / side;
-    p.tiles_n = (cols + side - 1) / side;
+    const int64_t big = ((outs + 511) / 512) * ((cols + 255) / 256) * p.ksteps;
+    p.big = big >= 8 * sms && outs > 256 && cols > 128;
+    const int rows_of = p.big ? Large::kRows : Small::kRows, cols_of = p.big ? Large::BN : Small::BN;
+    p.tiles_m = (outs + rows_of - 1) / rows_of;
+    p.tiles_n = (cols + cols_of - 1) / cols_of;
     p.units = p.tiles_m * p.tiles_n * p.ksteps;
-    // a block's share is worth its partial tile's trip through memory from about 4 steps on
-    int64_t blocks = (p.units + 3) / 4;
-    if (blocks < p.tiles_m * p.tiles_n) blocks = p.tiles_m * p.tiles_n;
-    p.blocks = static_cast<int>(blocks < sms ? blocks : sms);
+    // a share is worth its partial tile's trip through memory from about 4 steps on
+    const int most = p.big ? sms / 2 : sms;
+    int64_t shares = (p.units + 3) / 4;
+    if (shares < p.tiles_m * p.tiles_n) shares = p.tiles_m * p.tiles_n;
+    p.shares = static_cast<int>(shares < most ? shares : most);
     p.pitch = (outs + 7) / 8 * 8;
     int64_t sh = (rows + 63) / 64;
-    p.shares = static_cast<int>(sh < 64 ? (sh < 1 ? 1 : sh) : 64);
+    p.bias_shares = static_cast<int>(sh < 64 ? (sh < 1 ? 1 : sh) : 64);
     auto up256 = [](size_t v) { return (v + 255) / 256 * 256; };
-    p.pack_off = up256(static_cast<size_t>(p.blocks) * 2 * side * side * sizeof(float));
+    p.pack_off = up256(static_cast<size_t>(p.shares) * 2 * rows_of * cols_of * sizeof(float));
     p.bias_off = p.pack_off +
                  (p.pack ? up256(static_cast<size_t>(p.ksteps) * kTok * p.pitch * 2) : 0);
-    p.db_off = p.bias_off + up256(static_cast<size_t>(p.shares) * outs * sizeof(float));
-    p.bytes = p.db_off + up256(static_cast<size_t>(outs) * sizeof(float));
+    p.db_off = p.bias_off + up256(static_cast<size_t>(p.bias_shares) * outs * sizeof(float));
+    p.bytes = p.db_off + up256(static_cast<size_t>(outs) * sizeof(float)) + 256;  // to align the start
     return p;
 }
 
@@ -618,17 +702,26 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
            ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 31);
 }
 
-template <int MH, int BN>
-gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int blocks, cudaStream_t st) {
-    using Cfg = Tile<MH, BN>;
-    auto k = wgrad_kernel<MH, BN>;
-    gqh::blocks_per_sm(k, Cfg::kSmem, kWThreads);  // raises the shared-memory limit once
-    k<<<blocks, kWThreads, Cfg::kSmem, st>>>(map, a);
+template <typename C>
+gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, cudaStream_t st) {
+    auto k = wgrad_kernel<C>;
+    gqh::blocks_per_sm(k, C::kSmem, kWThreads);  // raises the shared-memory limit once
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(shares * C::CG));
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute pair;
+    pair.id = cudaLaunchAttributeClusterDimension;
+    pair.val.clusterDim.x = C::CG;
+    pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+    cfg.attrs = &pair;
+    cfg.numAttrs = C::CG > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, k, map, a) != cudaSuccess) return GQ_ERR_CUDA;
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
-    // every tile is whole when the shares are whole numbers of tiles
-    if (tiles % blocks != 0) {
-        const dim3 grid(static_cast<unsigned>(tiles), MH == 2 ? 16 : 8);
-        join_kernel<MH, BN><<<grid, 256, 0, st>>>(a, blocks);
+    if (tiles % shares != 0) {  // otherwise every share is a whole number of tiles
+        const dim3 grid(static_cast<unsigned>(tiles), C::CG == 2 ? 32 : 8);
+        join_kernel<C><<<grid, 256, 0, st>>>(a, shares);
     }
     return gqh::launch_status();
 }
@@ -667,7 +760,7 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     if (!ws || !mult(ws, 16) || ws_bytes < p.bytes) return GQ_ERR_WORKSPACE;
     EncodeFn encode = encode_fn();
     if (!encode) return GQ_ERR_CUDA;
-    uint8_t* w = static_cast<uint8_t*>(ws);
+    uint8_t* w = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 255) / 256 * 256);
     float* db = dbias ? dbias : reinterpret_cast<float*>(w + p.db_off);
 
     const void* src = dy;
@@ -692,7 +785,7 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
         float* part = reinterpret_cast<float*>(w + p.bias_off);
         const bool vec = row_align(dy, dtype, rows, lddy) != 0;
         const int v = vec ? 8 : 1;
-        const dim3 grid(static_cast<unsigned>((outs + 32 * v - 1) / (32 * v)), p.shares);
+        const dim3 grid(static_cast<unsigned>((outs + 32 * v - 1) / (32 * v)), p.bias_shares);
         if (dtype == GQ_F32) {
             const float* g = static_cast<const float*>(dy);
             if (vec) bias_kernel<float, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
@@ -702,7 +795,7 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
             if (vec) bias_kernel<bf16, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
             else bias_kernel<bf16, 1><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
         }
-        bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.shares, outs,
+        bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.bias_shares, outs,
                                                                                 db);
     }
     CUtensorMap map;
@@ -722,12 +815,12 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     a.codes = codes; a.exps = exps;
     a.scale = scale; a.shift = shift; a.db = db;
     a.dw = dw; a.out_f32 = out_dtype == GQ_F32;
-    a.vec = row_align(dw, out_dtype, outs, lddw) != 0;
-    a.partial = static_cast<float*>(ws);
+    a.vec = row_align(dw, out_dtype, outs, lddw);
+    a.partial = reinterpret_cast<float*>(w);
     a.ktok = p.ktok; a.ksteps = static_cast<int>(p.ksteps);
     a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
     a.units = p.units;
-    return p.big ? launch_wgrad<2, 256>(map, a, p.blocks, st) : launch_wgrad<1, 128>(map, a, p.blocks, st);
+    return p.big ? launch_wgrad<Large>(map, a, p.shares, st) : launch_wgrad<Small>(map, a, p.shares, st);
 }
 
 }  // extern "C"
