@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kTok = 64;              // tokens per step
 constexpr int kChain = 128;           // steps of one accumulation
-constexpr int kConvWarps = 16;        // warps 2..17, in
+constexpr int kConvWarps = 8;         // warps 2..9, in
 constexpr int kTeams = 2;             // teams that take turns at the steps
 constexpr int kTeam = 32 * kConvWarps / kTeams;  // threads of a team
 constexpr int kWThreads = 64 + 32 * kConvWarps;
@@ -207,10 +207,11 @@ struct Share {
     }
 };
 struct At {
-    int64_t left;  // steps of the share from here on
+    int left;  // steps of the share from here on
     int tile, k;
     __device__ __forceinline__ At(const Share& s, int ksteps)
-        : left(s.u1 - s.u0), tile(static_cast<int>(s.u0 / ksteps)), k(static_cast<int>(s.u0 % ksteps)) {}
+        : left(static_cast<int>(s.u1 - s.u0)), tile(static_cast<int>(s.u0 / ksteps)),
+          k(static_cast<int>(s.u0 % ksteps)) {}
     __device__ __forceinline__ void next(int ksteps) {
         --left;
         if (++k == ksteps) {
@@ -219,8 +220,15 @@ struct At {
         }
     }
     // steps of the tile at hand that are in the share
-    __device__ __forceinline__ int segment(int ksteps) const {
-        return static_cast<int>(min(left, static_cast<int64_t>(ksteps - k)));
+    __device__ __forceinline__ int segment(int ksteps) const { return min(left, ksteps - k); }
+    // `steps` more, which stay in the tile or end it
+    __device__ __forceinline__ void skip(int steps, int ksteps) {
+        left -= steps;
+        k += steps;
+        if (k == ksteps) {
+            k = 0;
+            ++tile;
+        }
     }
 };
 
@@ -366,9 +374,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int team = (threadIdx.x - 64) / kTeam, ct = (threadIdx.x - 64) % kTeam;
         constexpr int kPer = C::kOwn * kTok / 16 / kTeam;  // 16-code pieces per thread and step
         constexpr int kRowPieces = C::kOwn / 16;
-        // this thread's pieces of a step: every kTokStep-th token, the same 16 columns
-        static_assert(kTeam % kRowPieces == 0, "a thread keeps its columns");
-        const int col = (ct % kRowPieces) * 16, tok = ct / kRowPieces;
+        // this thread's pieces of a step: every kTokStep-th token, the same 16 columns.  Eight lanes
+        // that store together hold 64 columns of two tokens, whose swizzles differ in the last bit: 8
+        // different bank groups (128 columns of one token would be 4 groups twice).
+        static_assert(kRowPieces == 8, "the bits of ct below");
+        const int col = ((ct & 3) | (ct >> 1 & 4)) * 16, tok = (ct >> 2 & 1) | (ct >> 4 << 1);
         constexpr int kTokStep = kTeam / kRowPieces;
         uint4 w[kPer];
         uint32_t e[kPer];
@@ -385,14 +395,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
             pc = a.codes + t * a.pitch + i;
             pe = a.exps + t * a.epitch + (i >> 5);
         };
-        auto advance = [&]() {
-            ahead.next(a.ksteps);
-            if (++part == a.ktok || ahead.k == 0) {  // a part of dy, or a tile, begins
-                part = 0;
+        // on by `steps` (at most kTeams)
+        auto advance = [&](int steps) {
+            if (ahead.k + steps < a.ksteps && part + steps < a.ktok) {
+                ahead.left -= steps;
+                ahead.k += steps;
+                part += steps;
+                pc += steps * (kTok * a.pitch);
+                pe += steps * (kTok * a.epitch);
+            } else {  // a part of dy, or a tile, begins
+                for (int j = 0; j < steps; ++j) {
+                    ahead.next(a.ksteps);
+                    if (++part == a.ktok) part = 0;
+                }
                 place();
-            } else {
-                pc += kTok * a.pitch;
-                pe += kTok * a.epitch;
             }
         };
         auto fetch = [&]() {  // the step `ahead`, and on to the team's next
@@ -404,11 +420,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
                           : make_uint4(0, 0, 0, 0);
                 e[j] = in ? __ldg(pe + j * kTokStep * a.epitch) : 0u;
             }
-#pragma unroll
-            for (int j = 0; j < kTeams; ++j) advance();
+            advance(kTeams);
         };
         place();
-        for (int j = 0; j < team; ++j) advance();
+        if (team > 0) advance(team);
         if (ahead.left > 0) fetch();
         uint32_t n = 0, seg = 0;
         bool ok = true;
@@ -420,9 +435,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
             for (bool first = true; left > 0; first = false, ++seg) {  // the chains of the segment
                 const int steps = min(left, kChain);
                 left -= steps;
-                for (int z = 0; z < steps; ++z, ++n) {
-                    at.next(a.ksteps);
-                    if (static_cast<int>(n % kTeams) != team) continue;
+                at.skip(steps, a.ksteps);
+                const uint32_t end = n + steps;
+                for (n += (team - n) % kTeams; n < end; n += kTeams) {
                     const int s = n % S;
                     uint4 cw[kPer];
                     uint32_t ce[kPer];
@@ -458,11 +473,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     __syncwarp();
                     if (lane == 0) arrive_first<CG>(gq::smem_u32(&full[s]));
                 }
+                n = end;
                 // the chain's sums: 4 warps take the 128 lanes of TMEM, the groups of 4 share the
                 // columns
-                if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
-                ok = __all_sync(kFull, ok);
-                fence_after();
                 const int quad = warp & 3, group = (warp - 2) >> 2;
                 constexpr int kGroups = kConvWarps / 4, kShare = MH * BN / kGroups;
                 const int h = group * kShare / BN, c0 = group * kShare % BN;
@@ -472,6 +485,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 float* part_tile = a.partial + (static_cast<int64_t>(blockIdx.x / CG) * 2 +
                                                 (from_first ? 1 : 0)) * (C::kRows * BN);
                 const bool last = whole && left == 0;
+                float4 x[8];  // what the chains before left of the next 32 columns, on its way
+                auto before = [&](int c) {
+                    const float* p = part_tile + partial_at<BN>(r, c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        x[k] = reinterpret_cast<const float4*>(p + 256 * (k >> 1))[k & 1];
+                };
+                if (!first) before(c0);
+                if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
+                ok = __all_sync(kFull, ok);
+                fence_after();
 #pragma unroll 1
                 for (int c = c0; c < c0 + kShare; c += 32) {
                     uint32_t acc[32];
@@ -484,19 +508,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     float v[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
-                    float* p = part_tile + partial_at<BN>(r, c);
                     if (!first) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 x = reinterpret_cast<const float4*>(p + 256 * k)[0];
-                            const float4 y = reinterpret_cast<const float4*>(p + 256 * k)[1];
-                            v[8 * k] += x.x; v[8 * k + 1] += x.y; v[8 * k + 2] += x.z; v[8 * k + 3] += x.w;
-                            v[8 * k + 4] += y.x; v[8 * k + 5] += y.y; v[8 * k + 6] += y.z; v[8 * k + 7] += y.w;
+                        for (int k = 0; k < 8; ++k) {
+                            v[4 * k] += x[k].x; v[4 * k + 1] += x[k].y;
+                            v[4 * k + 2] += x[k].z; v[4 * k + 3] += x[k].w;
                         }
+                        if (c + 32 < c0 + kShare) before(c + 32);
                     }
                     if (last) {
                         finish(a, o, i0 + c, v);
                     } else {
+                        float* p = part_tile + partial_at<BN>(r, c);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t u[8];
@@ -699,7 +722,9 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
     // 32-bit TMA coordinates: tokens of three parts, and outs
     return size_ok(rows, cols) && rows < (int64_t(1) << 29) && outs >= 1 &&
            outs < (int64_t(1) << 30) && cols < (int64_t(1) << 30) &&
-           ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 31);
+           ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 31) &&
+           // steps of a share, in 32 bits
+           static_cast<double>(rows) * outs * cols < 1e17;
 }
 
 template <typename C>
