@@ -38,15 +38,17 @@ namespace {
 
 constexpr int kTok = 64;              // tokens per step
 constexpr int kChain = 128;           // steps of one accumulation
-constexpr int kConvWarps = 8;         // warps 2..9, in
-constexpr int kTeams = 2;             // teams that take turns at the steps
-constexpr int kTeam = 32 * kConvWarps / kTeams;  // threads of a team
-constexpr int kWThreads = 64 + 32 * kConvWarps;
+constexpr int kTeams = 2;             // teams of widening warps that take turns at the steps
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
 
 // CG blocks work on a tile, each on MH x 128 of its outs; BN columns, BN / CG widened by each block.
-template <int CG_, int MH_, int BN_> struct Tile {
+// WARPS widening warps: 8 keep up with both (16 leave 96 registers each, and gained nothing: 600 cycles
+// of a small tile's step are its operands' way through shared memory).
+template <int CG_, int MH_, int BN_, int WARPS> struct Tile {
     static constexpr int CG = CG_, MH = MH_, BN = BN_;
+    static constexpr int kConv = WARPS;               // warps 2 .. WARPS + 1
+    static constexpr int kTeam = 32 * WARPS / kTeams; // threads of a team
+    static constexpr int kThreads = 64 + 32 * WARPS;
     static constexpr int kOuts = 128 * MH;            // of a block
     static constexpr int kRows = kOuts * CG;          // of the tile
     static constexpr int kOwn = BN / CG;              // columns widened by a block
@@ -56,8 +58,8 @@ template <int CG_, int MH_, int BN_> struct Tile {
     static constexpr int kCols = MH * BN;             // TMEM columns: a power of two >= 32
     static constexpr int kSmem = kStages * (kABytes + kBBytes) + 1024;
 };
-using Large = Tile<2, 2, 256>;
-using Small = Tile<1, 1, 128>;
+using Large = Tile<2, 2, 256, 8>;
+using Small = Tile<1, 1, 128, 8>;
 
 struct WArgs {
     int64_t rows, outs, cols, pitch, epitch, ldw;
@@ -68,12 +70,14 @@ struct WArgs {
     const float* db;
     void* dw;
     int out_f32;
-    int vec;              // dw rows are 32-, 16- or 0-byte aligned
     float* partial;
     int64_t ktok;         // tokens of one part, rounded up to whole steps, in steps
     int ksteps;           // steps of a tile: parts * ktok
     int tiles_m, tiles_n;
-    int64_t units;        // tiles * ksteps
+    int64_t units;        // tiles * ksteps, in
+    int64_t base;         // shares of base steps, one more in the first `rest`
+    int rest;
+    int fast;             // whole 32-byte pieces of dw, and of scale and shift, are aligned
 };
 
 // ---- tcgen05 -------------------------------------------------------------------------------
@@ -196,22 +200,27 @@ __device__ __forceinline__ uint32_t widen2(uint32_t p, __nv_bfloat162 s) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The contiguous steps [u0, u1) of a block, and a place in them: a tile, and a step of that tile.  The
-// place moves on by counting; a 64-bit division per step and thread had cost a third of the issue
-// slots.
-struct Share {
-    int64_t u0, u1;
-    __device__ __forceinline__ Share(int64_t units, int block, int blocks) {
-        u0 = units * block / blocks;
-        u1 = units * (block + 1) / blocks;
-    }
-};
+// The contiguous steps of a share (the first `rest` shares have one more), and a place in them: a tile,
+// and a step of that tile.  The place moves on by counting; a 64-bit division per step and thread had
+// cost a third of the issue slots, and even one per thread is felt by a call of a few steps.
+__device__ __forceinline__ int64_t share_begin(const WArgs& a, int share) {
+    return a.base * share + min(share, a.rest);
+}
 struct At {
     int left;  // steps of the share from here on
     int tile, k;
-    __device__ __forceinline__ At(const Share& s, int ksteps)
-        : left(static_cast<int>(s.u1 - s.u0)), tile(static_cast<int>(s.u0 / ksteps)),
-          k(static_cast<int>(s.u0 % ksteps)) {}
+    __device__ __forceinline__ At(const WArgs& a, int share)
+        : left(static_cast<int>(a.base) + (share < a.rest ? 1 : 0)) {
+        const int64_t u = share_begin(a, share);
+        if (a.units <= INT32_MAX) {
+            const uint32_t v = static_cast<uint32_t>(u);
+            tile = static_cast<int>(v / static_cast<uint32_t>(a.ksteps));
+            k = static_cast<int>(v % static_cast<uint32_t>(a.ksteps));
+        } else {
+            tile = static_cast<int>(u / a.ksteps);
+            k = static_cast<int>(u % a.ksteps);
+        }
+    }
     __device__ __forceinline__ void next(int ksteps) {
         --left;
         if (++k == ksteps) {
@@ -232,41 +241,61 @@ struct At {
     }
 };
 
-template <typename O> __device__ __forceinline__ void tail(O* p, int left, const float (&w)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (k < left) down(w[k], p[k]);
+// 8 columns of a row of dw from fp32 sums, element by element: the last columns, and rows that are
+// not aligned.  Kept out of the kernels' straight path, whose instructions a short call fetches cold.
+__device__ __noinline__ void finish_slow(const WArgs& a, int64_t o, int64_t i, const float (&v)[8]) {
+    for (int k = 0; k < 8 && i + k < a.cols; ++k) {
+        float x = v[k];
+        if (a.scale) x = x * a.scale[i + k];
+        if (a.shift) x = fmaf(a.db[o], a.shift[i + k], x);
+        if (a.out_f32) static_cast<float*>(a.dw)[o * a.ldw + i + k] = x;
+        else static_cast<bf16*>(a.dw)[o * a.ldw + i + k] = __float2bfloat16_rn(x);
+    }
 }
-
-// N consecutive columns of a row of dw from fp32 sums: times scale, plus db shift, rounded.
+// N columns (a multiple of 8) of row o from column i on: the sums times scale, plus db shift, rounded.
 template <int N>
 __device__ __forceinline__ void finish(const WArgs& a, int64_t o, int64_t i, float (&v)[N]) {
     if (o >= a.outs || i >= a.cols) return;
-    if (a.scale) {
+    if (a.fast && i + N <= a.cols) {
+        if (a.scale) {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (i + k < a.cols) v[k] = v[k] * __ldg(a.scale + i + k);
-    }
-    if (a.shift) {
-        const float d = __ldg(a.db + o);
+            for (int k = 0; k < N; k += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.scale + i + k));
+                v[k] *= f.x; v[k + 1] *= f.y; v[k + 2] *= f.z; v[k + 3] *= f.w;
+            }
+        }
+        if (a.shift) {
+            const float d = __ldg(a.db + o);
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (i + k < a.cols) v[k] = fmaf(d, __ldg(a.shift + i + k), v[k]);
+            for (int k = 0; k < N; k += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.shift + i + k));
+                v[k] = fmaf(d, f.x, v[k]); v[k + 1] = fmaf(d, f.y, v[k + 1]);
+                v[k + 2] = fmaf(d, f.z, v[k + 2]); v[k + 3] = fmaf(d, f.w, v[k + 3]);
+            }
+        }
+        if (a.out_f32) {
+            float* p = static_cast<float*>(a.dw) + o * a.ldw + i;
+#pragma unroll
+            for (int k = 0; k < N; k += 8) {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[k + j]);
+                st32<32>(p + k, u);
+            }
+        } else {
+            bf16* p = static_cast<bf16*>(a.dw) + o * a.ldw + i;
+#pragma unroll
+            for (int k = 0; k < N; k += 8)
+                *reinterpret_cast<uint4*>(p + k) =
+                    make_uint4(pack2(v[k], v[k + 1], bf16()), pack2(v[k + 2], v[k + 3], bf16()),
+                               pack2(v[k + 4], v[k + 5], bf16()), pack2(v[k + 6], v[k + 7], bf16()));
+        }
+        return;
     }
 #pragma unroll
     for (int k = 0; k < N; k += 8) {
         const float w[8] = {v[k], v[k + 1], v[k + 2], v[k + 3], v[k + 4], v[k + 5], v[k + 6], v[k + 7]};
-        const int left = static_cast<int>(min(a.cols - i - k, int64_t(8)));
-        if (a.out_f32) {
-            float* p = static_cast<float*>(a.dw) + o * a.ldw + i + k;
-            if (a.vec == 32) store<float, 8, 32>(p, 0, left, w);
-            else if (a.vec) store<float, 8, 16>(p, 0, left, w);
-            else tail(p, left, w);
-        } else {
-            bf16* p = static_cast<bf16*>(a.dw) + o * a.ldw + i + k;
-            if (a.vec) store<bf16, 8, 16>(p, 0, left, w);
-            else tail(p, left, w);
-        }
+        finish_slow(a, o, i + k, w);
     }
 }
 
@@ -279,7 +308,7 @@ template <int BN> __device__ __forceinline__ int64_t partial_at(int row, int col
 }
 
 template <typename C>
-__global__ void __launch_bounds__(kWThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const WArgs a) {
     constexpr int CG = C::CG, MH = C::MH, BN = C::BN, S = C::kStages;
     extern __shared__ uint8_t raw[];
@@ -295,12 +324,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             // the widening warps of a team in each block, and each block's dy
-            gq::mbar_init(gq::smem_u32(&full[s]), CG * (kConvWarps / kTeams + 1));
+            gq::mbar_init(gq::smem_u32(&full[s]), CG * (C::kConv / kTeams + 1));
             gq::mbar_init(gq::smem_u32(&full_a[s]), 1u);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
-        gq::mbar_init(gq::smem_u32(&acc_empty), CG * kConvWarps);
+        gq::mbar_init(gq::smem_u32(&acc_empty), CG * C::kConv);
         gq::mbar_init(gq::smem_u32(&drain), 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -310,13 +339,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
     pair_sync<CG>();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const Share share(a.units, blockIdx.x / CG, gridDim.x / CG);
+    const int share = blockIdx.x / CG;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t n = 0;
             bool ok = true;
-            for (At at(share, a.ksteps); at.left > 0 && ok; at.next(a.ksteps), ++n) {
+            for (At at(a, share); at.left > 0 && ok; at.next(a.ksteps), ++n) {
                 const int s = n % S;
                 if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                 if (!ok) break;
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane == 0 && rank == 0) {
             uint32_t n = 0, seg = 0;
             bool ok = true;
-            for (At at(share, a.ksteps); at.left > 0 && ok; ++seg) {
+            for (At at(a, share); at.left > 0 && ok; ++seg) {
                 const int steps = min(at.segment(a.ksteps), kChain);
                 if (seg > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (seg - 1) & 1);
                 fence_after();
@@ -365,24 +394,24 @@ __global__ void __launch_bounds__(kWThreads, 1)
         } else if (lane == 0) {  // the second block: tells the first that its dy has arrived
             uint32_t n = 0;
             bool ok = true;
-            for (At at(share, a.ksteps); at.left > 0 && ok; at.next(a.ksteps), ++n) {
+            for (At at(a, share); at.left > 0 && ok; at.next(a.ksteps), ++n) {
                 ok = gq::mbar_wait(gq::smem_u32(&full_a[n % S]), (n / S) & 1);
                 if (ok) arrive_first<CG>(gq::smem_u32(&full[n % S]));
             }
         }
     } else {
-        const int team = (threadIdx.x - 64) / kTeam, ct = (threadIdx.x - 64) % kTeam;
-        constexpr int kPer = C::kOwn * kTok / 16 / kTeam;  // 16-code pieces per thread and step
+        const int team = (threadIdx.x - 64) / C::kTeam, ct = (threadIdx.x - 64) % C::kTeam;
+        constexpr int kPer = C::kOwn * kTok / 16 / C::kTeam;  // 16-code pieces per thread and step
         constexpr int kRowPieces = C::kOwn / 16;
         // this thread's pieces of a step: every kTokStep-th token, the same 16 columns.  Eight lanes
         // that store together hold 64 columns of two tokens, whose swizzles differ in the last bit: 8
         // different bank groups (128 columns of one token would be 4 groups twice).
         static_assert(kRowPieces == 8, "the bits of ct below");
         const int col = ((ct & 3) | (ct >> 1 & 4)) * 16, tok = (ct >> 2 & 1) | (ct >> 4 << 1);
-        constexpr int kTokStep = kTeam / kRowPieces;
+        constexpr int kTokStep = C::kTeam / kRowPieces;
         uint4 w[kPer];
         uint32_t e[kPer];
-        At ahead(share, a.ksteps);
+        At ahead(a, share);
         int part = ahead.k % static_cast<int>(a.ktok);  // step within the part of dy
         const int8_t* pc = nullptr;   // codes and exponents of the thread's first piece of the
         const uint8_t* pe = nullptr;  // step `ahead`
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (ahead.left > 0) fetch();
         uint32_t n = 0, seg = 0;
         bool ok = true;
-        At at(share, a.ksteps);
+        At at(a, share);
         while (at.left > 0) {
             const int tile = at.tile;
             int left = at.segment(a.ksteps);
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 // the chain's sums: 4 warps take the 128 lanes of TMEM, the groups of 4 share the
                 // columns
                 const int quad = warp & 3, group = (warp - 2) >> 2;
-                constexpr int kGroups = kConvWarps / 4, kShare = MH * BN / kGroups;
+                constexpr int kGroups = C::kConv / 4, kShare = MH * BN / kGroups;
                 const int h = group * kShare / BN, c0 = group * kShare % BN;
                 const int r = static_cast<int>(rank) * C::kOuts + h * 128 + quad * 32 + lane;
                 const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * C::kRows + r;
@@ -545,17 +574,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
 // Adds the partial tiles of every tile that more than one share has a part of, in the shares' order.
 // blockIdx.x = tile; thread = 8 columns of a row, 32 rows of the same columns per warp.
-template <typename C> __global__ void __launch_bounds__(256) join_kernel(const WArgs a, int shares) {
+template <typename C> __global__ void __launch_bounds__(256) join_kernel(const WArgs a) {
     constexpr int BN = C::BN;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * a.ksteps, last = first + a.ksteps - 1;
     __shared__ int owners[2];
     if (threadIdx.x < 2) {  // the share that holds the tile's first step, and its last
         const int64_t u = threadIdx.x ? last : first;
-        int64_t b = u * shares / a.units;
-        while (b + 1 < shares && a.units * (b + 1) / shares <= u) ++b;
-        while (b > 0 && a.units * b / shares > u) --b;
+        const int64_t longer = (a.base + 1) * a.rest;  // steps of the shares that have one more
+        const int64_t b = u < longer ? u / (a.base + 1) : a.rest + (u - longer) / a.base;
         // a share that begins at the tile's first step keeps it in slot 1, any other in slot 0
-        owners[threadIdx.x] = static_cast<int>(2 * b + (a.units * b / shares <= first ? 1 : 0));
+        owners[threadIdx.x] = static_cast<int>(2 * b + (share_begin(a, static_cast<int>(b)) <= first ? 1 : 0));
     }
     __syncthreads();
     const int b0 = owners[0], b1 = owners[1];
@@ -607,23 +635,34 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Column sums of dy: thread = V columns, 8 rows at a time per block, partial[blockIdx.y][outs].
+// Column sums of dy: thread = V columns, 32 rows at a time per block; partial[blockIdx.y][outs], or db
+// itself where one block row does.
 template <typename T, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     bias_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
                 float* __restrict__ partial) {
-    __shared__ float tile[8][32 * V];
+    __shared__ float tile[32][32 * V + 1];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * V;
     float s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 0.0f;
     if (c < outs) {
-#pragma unroll 4
-        for (int64_t t = static_cast<int64_t>(blockIdx.y) * 8 + y; t < rows;
-             t += static_cast<int64_t>(gridDim.y) * 8) {
+        const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
+        const T* p = dy + (static_cast<int64_t>(blockIdx.y) * 32 + y) * ld;
+        int64_t left = rows - (static_cast<int64_t>(blockIdx.y) * 32 + y);
+        for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
+            float v[4][V];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load<T, V, 16>(p + k * stride * ld, c, outs, v[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] += v[k][i];
+        }
+        for (; left > 0; left -= stride, p += stride * ld) {
             float v[V];
-            load<T, V, 16>(dy + t * ld, c, outs, v);
+            load<T, V, 16>(p, c, outs, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) s[i] += v[i];
         }
@@ -631,14 +670,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < V; ++i) tile[y][x * V + i] = s[i];
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * V; i += 256) {
-        const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * V + i;
-        if (col < outs) {
-            float v = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v += tile[k][i];
-            partial[blockIdx.y * outs + col] = v;
-        }
+    for (int i = 0; i < V; ++i) {  // a warp adds up a column
+        const int col = y * V + i;
+        const float t = tile[x][col];
+        float v = t;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+        const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 * V + col;
+        if (x == 0 && out < outs) partial[blockIdx.y * outs + out] = v;
     }
 }
 __global__ void __launch_bounds__(256)
@@ -695,20 +735,43 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.pack = dtype == GQ_F32 || row_align(dy, dtype, rows, ld) == 0;
     p.ktok = (rows + kTok - 1) / kTok;
     p.ksteps = p.ktok * p.parts;
-    const int64_t big = ((outs + 511) / 512) * ((cols + 255) / 256) * p.ksteps;
-    p.big = big >= 8 * sms && outs > 256 && cols > 128;
+    // Small or large tiles, and how many shares: the smallest of the times that the steps, a launch's
+    // ends and the partial tiles take, in microseconds as measured (a step of a 512 x 256 tile 0.55, of
+    // a 128 x 128 tile 0.36; splitting tiles costs 12 or 6 more: 4096 x 4096 x 16384 takes 338 us in
+    // large tiles and 783 in small ones, 768 x 768 x 384 takes 14.5 us in 54 shares, 8.3 in 36 whole tiles).
+    double best = 0.0;
+    for (int large = 0; large < 2; ++large) {
+        const int rows_of = large ? Large::kRows : Small::kRows, cols_of = large ? Large::BN : Small::BN;
+        const int64_t tiles = ((outs + rows_of - 1) / rows_of) * ((cols + cols_of - 1) / cols_of);
+        const int64_t most = large ? sms / 2 : sms;
+        const double step = large ? 0.55 : 0.36, ends = large ? 4.0 : 3.0, split = large ? 12.0 : 6.0;
+        auto consider = [&](int64_t shares, double steps, bool whole) {
+            const double t = ends + steps * step + (whole ? 0.0 : split);
+            if (best == 0.0 || t < best) {
+                best = t;
+                p.big = large != 0;
+                p.shares = static_cast<int>(shares);
+            }
+        };
+        if (tiles <= most) {
+            consider(tiles, static_cast<double>(p.ksteps), true);
+            const int64_t q = most / tiles;  // shares per tile, none of which crosses tiles
+            if (q > 1 && p.ksteps >= 2 * q)
+                consider(tiles * q, static_cast<double>((p.ksteps + q - 1) / q), false);
+        }
+        const double even = static_cast<double>(tiles) * p.ksteps / most;
+        if (even >= 4.0) consider(most, even + 2.0, tiles % most == 0);
+    }
     const int rows_of = p.big ? Large::kRows : Small::kRows, cols_of = p.big ? Large::BN : Small::BN;
     p.tiles_m = (outs + rows_of - 1) / rows_of;
     p.tiles_n = (cols + cols_of - 1) / cols_of;
     p.units = p.tiles_m * p.tiles_n * p.ksteps;
-    // a share is worth its partial tile's trip through memory from about 4 steps on
-    const int most = p.big ? sms / 2 : sms;
-    int64_t shares = (p.units + 3) / 4;
-    if (shares < p.tiles_m * p.tiles_n) shares = p.tiles_m * p.tiles_n;
-    p.shares = static_cast<int>(shares < most ? shares : most);
     p.pitch = (outs + 7) / 8 * 8;
-    int64_t sh = (rows + 63) / 64;
-    p.bias_shares = static_cast<int>(sh < 64 ? (sh < 1 ? 1 : sh) : 64);
+    // sums of dy: up to 1,024 rows in one go, else one wave of blocks (two per SM)
+    const int64_t groups = (outs + 255) / 256;
+    int64_t sh = rows <= 1024 ? 1 : groups < 2 * sms ? 2 * sms / groups : 1;
+    if (sh > (rows + 127) / 128) sh = (rows + 127) / 128;
+    p.bias_shares = static_cast<int>(sh);
     auto up256 = [](size_t v) { return (v + 255) / 256 * 256; };
     p.pack_off = up256(static_cast<size_t>(p.shares) * 2 * rows_of * cols_of * sizeof(float));
     p.bias_off = p.pack_off +
@@ -730,10 +793,10 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
 template <typename C>
 gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, cudaStream_t st) {
     auto k = wgrad_kernel<C>;
-    gqh::blocks_per_sm(k, C::kSmem, kWThreads);  // raises the shared-memory limit once
+    gqh::blocks_per_sm(k, C::kSmem, C::kThreads);  // raises the shared-memory limit once
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(shares * C::CG));
-    cfg.blockDim = dim3(kWThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute pair;
@@ -746,7 +809,7 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, cudaS
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
     if (tiles % shares != 0) {  // otherwise every share is a whole number of tiles
         const dim3 grid(static_cast<unsigned>(tiles), C::CG == 2 ? 32 : 8);
-        join_kernel<C><<<grid, 256, 0, st>>>(a, shares);
+        join_kernel<C><<<grid, 256, 0, st>>>(a);
     }
     return gqh::launch_status();
 }
@@ -807,21 +870,22 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
         src_outs = p.pitch;
     }
     if (dbias || shift) {
-        float* part = reinterpret_cast<float*>(w + p.bias_off);
+        float* part = p.bias_shares > 1 ? reinterpret_cast<float*>(w + p.bias_off) : db;
         const bool vec = row_align(dy, dtype, rows, lddy) != 0;
         const int v = vec ? 8 : 1;
         const dim3 grid(static_cast<unsigned>((outs + 32 * v - 1) / (32 * v)), p.bias_shares);
         if (dtype == GQ_F32) {
             const float* g = static_cast<const float*>(dy);
-            if (vec) bias_kernel<float, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
-            else bias_kernel<float, 1><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+            if (vec) bias_kernel<float, 8><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
+            else bias_kernel<float, 1><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
         } else {
             const bf16* g = static_cast<const bf16*>(dy);
-            if (vec) bias_kernel<bf16, 8><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
-            else bias_kernel<bf16, 1><<<grid, 256, 0, st>>>(g, lddy, rows, outs, part);
+            if (vec) bias_kernel<bf16, 8><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
+            else bias_kernel<bf16, 1><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
         }
-        bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.bias_shares, outs,
-                                                                                db);
+        if (p.bias_shares > 1)
+            bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.bias_shares,
+                                                                                    outs, db);
     }
     CUtensorMap map;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(src_outs), static_cast<cuuint64_t>(src_rows)};
@@ -840,11 +904,12 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     a.codes = codes; a.exps = exps;
     a.scale = scale; a.shift = shift; a.db = db;
     a.dw = dw; a.out_f32 = out_dtype == GQ_F32;
-    a.vec = row_align(dw, out_dtype, outs, lddw);
+    a.fast = row_align(dw, out_dtype, outs, lddw) >= (a.out_f32 ? 32 : 16) && mult(scale, 16) && mult(shift, 16);
     a.partial = reinterpret_cast<float*>(w);
     a.ktok = p.ktok; a.ksteps = static_cast<int>(p.ksteps);
     a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
     a.units = p.units;
+    a.base = p.units / p.shares; a.rest = static_cast<int>(p.units % p.shares);
     return p.big ? launch_wgrad<Large>(map, a, p.shares, st) : launch_wgrad<Small>(map, a, p.shares, st);
 }
 
