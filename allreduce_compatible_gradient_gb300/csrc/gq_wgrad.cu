@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 float* part_tile = a.partial + (static_cast<int64_t>(blockIdx.x / CG) * 2 +
                                                 (from_first ? 1 : 0)) * (C::kRows * BN);
                 const bool last = whole && left == 0;
+                if (last && a.shift) gq::pdl_wait();  // db, if the sums of dy still run
                 float4 x[8];  // what the chains before left of the next 32 columns, on its way
                 auto before = [&](int c) {
                     const float* p = part_tile + partial_at<BN>(r, c);
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
         }
     }
+    gq::pdl_wait();
     __syncwarp();
     fence_before();
     __syncthreads();
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(1024)
     bias_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
                 float* __restrict__ partial) {
     __shared__ float tile[32][32 * V + 1];
+    gq::pdl_launch_dependents();  // what follows waits for these sums where it reads them
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * V;
     float s[V];
@@ -651,14 +654,35 @@ __global__ void __launch_bounds__(1024)
         const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
         const T* p = dy + (static_cast<int64_t>(blockIdx.y) * 32 + y) * ld;
         int64_t left = rows - (static_cast<int64_t>(blockIdx.y) * 32 + y);
-        for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
-            float v[4][V];
+        if constexpr (V == 8) {
+            // (the test for the last columns is outside, so that the loads are issued together)
+            if (c + V <= outs) {
+                for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
+                    Raw8<T> r[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) load<T, V, 16>(p + k * stride * ld, c, outs, v[k]);
+                    for (int k = 0; k < 4; ++k) r[k] = raw8(p + k * stride * ld + c, 0, 8);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
+                        F2 v[4];
+                        pairs(r[k], v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[i] += v[k][i];
+                        for (int i = 0; i < 4; ++i) {
+                            float x, y2;
+                            split(v[i], x, y2);
+                            s[2 * i] += x;
+                            s[2 * i + 1] += y2;
+                        }
+                    }
+                }
+            }
+        } else {
+            for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = up(p[k * stride * ld + c]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[0] += v[k];
+            }
         }
         for (; left > 0; left -= stride, p += stride * ld) {
             float v[V];
@@ -685,6 +709,8 @@ __global__ void __launch_bounds__(256)
     bias_sum_kernel(const float* __restrict__ partial, int parts, int64_t outs, float* db) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
     __shared__ float tile[8][32];
+    gq::pdl_launch_dependents();
+    gq::pdl_wait();
     float s = 0.0f;
     if (c < outs) {
 #pragma unroll 4
@@ -767,9 +793,9 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.tiles_n = (cols + cols_of - 1) / cols_of;
     p.units = p.tiles_m * p.tiles_n * p.ksteps;
     p.pitch = (outs + 7) / 8 * 8;
-    // sums of dy: up to 1,024 rows in one go, else one wave of blocks (two per SM)
+    // sums of dy: up to 512 rows in one go, else one wave of blocks (one per SM)
     const int64_t groups = (outs + 255) / 256;
-    int64_t sh = rows <= 1024 ? 1 : groups < 2 * sms ? 2 * sms / groups : 1;
+    int64_t sh = rows <= 512 ? 1 : groups < sms ? sms / groups : 1;
     if (sh > (rows + 127) / 128) sh = (rows + 127) / 128;
     p.bias_shares = static_cast<int>(sh);
     auto up256 = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -790,8 +816,10 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
            static_cast<double>(rows) * outs * cols < 1e17;
 }
 
+// after_bias: the launch before this one on the stream is of the sums of dy, which the kernel waits for
+// only where it reads them; what came before those is done when it starts.
 template <typename C>
-gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, cudaStream_t st) {
+gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool after_bias, cudaStream_t st) {
     auto k = wgrad_kernel<C>;
     gqh::blocks_per_sm(k, C::kSmem, C::kThreads);  // raises the shared-memory limit once
     cudaLaunchConfig_t cfg = {};
@@ -799,12 +827,14 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, cudaS
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute pair;
-    pair.id = cudaLaunchAttributeClusterDimension;
-    pair.val.clusterDim.x = C::CG;
-    pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
-    cfg.attrs = &pair;
-    cfg.numAttrs = C::CG > 1 ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = after_bias ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C::CG > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, k, map, a) != cudaSuccess) return GQ_ERR_CUDA;
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
     if (tiles % shares != 0) {  // otherwise every share is a whole number of tiles
@@ -883,9 +913,20 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
             if (vec) bias_kernel<bf16, 8><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
             else bias_kernel<bf16, 1><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
         }
-        if (p.bias_shares > 1)
-            bias_sum_kernel<<<static_cast<unsigned>((outs + 31) / 32), 256, 0, st>>>(part, p.bias_shares,
-                                                                                    outs, db);
+        if (p.bias_shares > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>((outs + 31) / 32));
+            cfg.blockDim = dim3(256);
+            cfg.stream = st;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(part), p.bias_shares,
+                                   outs, db) != cudaSuccess)
+                return GQ_ERR_CUDA;
+        }
     }
     CUtensorMap map;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(src_outs), static_cast<cuuint64_t>(src_rows)};
@@ -910,7 +951,9 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
     a.units = p.units;
     a.base = p.units / p.shares; a.rest = static_cast<int>(p.units % p.shares);
-    return p.big ? launch_wgrad<Large>(map, a, p.shares, st) : launch_wgrad<Small>(map, a, p.shares, st);
+    const bool after_bias = dbias || shift;
+    return p.big ? launch_wgrad<Large>(map, a, p.shares, after_bias, st)
+                 : launch_wgrad<Small>(map, a, p.shares, after_bias, st);
 }
 
 }  // extern "C"
