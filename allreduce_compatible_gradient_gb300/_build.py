@@ -1,4 +1,5 @@
-"""Compile the CUDA library (csrc/*.cu over csrc/gq_kernels.cuh) into libgq.so, in-tree.
+"""Compile the CUDA library (csrc/*.cu over csrc/gq_kernels.cuh) into libgq.so, in-tree, and the
+extension module through which Python calls its activation operators (csrc/gq_native.cpp).
 
 Eight translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
 gradient type and scheme; the activation kernels) compiled in parallel with one -gencode
@@ -24,6 +25,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgq.so")
 # the same library with the kernels' bounds checks compiled in (-DGQ_DEBUG)
 DEBUG_LIB = os.path.join(PKG, "libgq_debug.so")
+NATIVE = os.path.join(CSRC, "gq_native.cpp")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -50,6 +52,37 @@ def link_command(objs: list, out: str) -> list:
     return [nvcc(), ARCH, "-shared", "-o", out, *objs]
 
 
+def native_path() -> str:
+    """The extension module of this Python and torch (gq_native.cpp)."""
+    import torch
+
+    tag = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, "gq_native_%s.so" % tag)
+
+
+def native_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return ["g++", "-O2", "-fPIC", "-shared", "-std=c++%d" % (20 if _torch_wants_cxx20() else 17),
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            *["-isystem" + d for d in include_paths()], "-isystem" + cuda,
+            "-isystem" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+            NATIVE, "-o", out, "-L" + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch",
+            "-lc10_cuda", "-lc10"]
+
+
+def _torch_wants_cxx20() -> bool:
+    import torch
+
+    major, minor = (int("".join(c for c in v if c.isdigit())) for v in torch.__version__.split(".")[:2])
+    return (major, minor) >= (2, 10)
+
+
 def is_stale(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
@@ -59,8 +92,27 @@ def is_stale(lib: str = LIB) -> bool:
 
 def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Build libgq.so (debug: libgq_debug.so, with -DGQ_DEBUG) if missing or older than its
-    sources; return its path."""
+    sources, and beside it the extension module of the activation operators; return the library's
+    path."""
     lib = DEBUG_LIB if debug else LIB
+    native = native_path()
+    building = None
+    if not debug and (force or not os.path.exists(native) or any(
+            os.path.getmtime(f) > os.path.getmtime(native)
+            for f in (NATIVE, os.path.join(ROOT, "include", "gq.h")))):
+        made = native + ".tmp.%d" % os.getpid()
+        building = subprocess.Popen(native_command(made))
+    try:
+        _build_cuda(lib, force, verbose, debug)
+    finally:
+        if building is not None and building.wait() == 0:
+            os.replace(made, native)
+    if building is not None and building.returncode != 0:
+        raise subprocess.CalledProcessError(building.returncode, "g++")
+    return lib
+
+
+def _build_cuda(lib: str, force: bool, verbose: bool, debug: bool) -> None:
     if force or is_stale(lib):
         os.makedirs(OBJ_DIR, exist_ok=True)
         extra = (("-Xptxas", "-v") if verbose else ()) + (("-DGQ_DEBUG",) if debug else ())
@@ -78,4 +130,3 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
             for f in objs + [tmp]:
                 if os.path.exists(f):
                     os.remove(f)
-    return lib
