@@ -37,7 +37,7 @@ using namespace gqa;
 namespace {
 
 constexpr int kTok = 64;              // tokens per step
-constexpr int kChain = 128;           // steps of one accumulation
+constexpr int kChain = 96;            // steps of one accumulation
 constexpr int kTeams = 2;             // teams of widening warps that take turns at the steps
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
 
