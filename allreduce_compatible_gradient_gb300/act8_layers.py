@@ -1,0 +1,76 @@
+"""Transformer layers that keep their activations in 8 bits (torch modules over the activation
+operators): layer norm + linear, GELU + linear, and the pre-norm MLP block made of the two.
+
+Parameters are fp32; activations and their gradients are bf16 (or fp32).  The forward pass keeps one
+8-bit checkpoint per normalised input and one per GELU input, and nothing else of their size: the
+checkpoint of the normalised rows serves both the layer norm's backward pass and the weight gradient
+of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.
+Checkpoints are rounded at random without bias, with the random words of (seed, step, row, column)
+that gq_quantize uses for gradients; every layer has a seed of its own.
+"""
+from __future__ import annotations
+
+import torch
+from torch import nn
+
+from . import _activations as ops
+
+
+class _NormLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step):
+        rows = x.reshape(-1, x.shape[-1])
+        y, _, rstd, act = ops.gq_layernorm_forward(rows, norm_weight, norm_bias, eps, seed=seed, step=step)
+        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd)
+        ctx.act, ctx.shape = act, x.shape
+        out = torch.nn.functional.linear(y, weight.to(y.dtype), bias.to(y.dtype))
+        return out.view(*x.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    def backward(ctx, dout):
+        norm_weight, norm_bias, weight, rstd = ctx.saved_tensors
+        d = dout.reshape(-1, dout.shape[-1])
+        dweight, dbias = ops.gq_linear_wgrad(d, ctx.act, scale=norm_weight, shift=norm_bias)
+        dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=ctx.act)
+        return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None
+
+
+class _GeluLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, u, weight, bias, approximate, seed, step):
+        rows = u.reshape(-1, u.shape[-1])
+        h, act = ops.gq_gelu_forward(rows, approximate=approximate, seed=seed, step=step)
+        ctx.save_for_backward(weight)
+        ctx.act, ctx.approximate, ctx.shape = act, approximate, u.shape
+        out = torch.nn.functional.linear(h, weight.to(h.dtype), bias.to(h.dtype))
+        return out.view(*u.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    def backward(ctx, dout):
+        weight, = ctx.saved_tensors
+        d = dout.reshape(-1, dout.shape[-1])
+        du, h = ops.gq_gelu_backward(d @ weight.to(d.dtype), ctx.act, approximate=ctx.approximate,
+                                     need_output=True)
+        dweight = (d.t() @ h).float()
+        return du.view(ctx.shape), dweight, d.float().sum(0), None, None, None
+
+
+class MlpBlock8(nn.Module):
+    """x + W2 gelu(W1 norm(x) + b1) + b2 with 8-bit checkpoints.  `step` numbers the training steps:
+    set it before each forward pass, so that every step rounds with words of its own."""
+
+    def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
+                 seed: int = 0, device=None):
+        super().__init__()
+        self.norm_weight = nn.Parameter(torch.ones(width, device=device))
+        self.norm_bias = nn.Parameter(torch.zeros(width, device=device))
+        self.w1 = nn.Parameter(torch.randn(hidden, width, device=device) * width ** -0.5)
+        self.b1 = nn.Parameter(torch.zeros(hidden, device=device))
+        self.w2 = nn.Parameter(torch.randn(width, hidden, device=device) * hidden ** -0.5)
+        self.b2 = nn.Parameter(torch.zeros(width, device=device))
+        self.approximate, self.eps, self.seed, self.step = approximate, eps, seed, 0
+
+    def forward(self, x):
+        u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps,
+                              2 * self.seed, self.step)
+        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, 2 * self.seed + 1, self.step)

@@ -199,3 +199,73 @@ def test_argument_checks_of_the_bucket_and_rank_entry_points(lib):
     assert lib.gq_dequantize_to(vp(fake), vp(fake), 1, 8, 2, 64, vp(fake + 2), 1, None) == 1
     assert lib.gq_allreduce_mean_to(vp(fake), 0, 2, 64, 0, 0, 1, 8, 1, 1, vp(fake), -1, None,
                                     None, vp(fake), ws_bytes, None) == 1
+
+
+def test_argument_checks_of_the_activation_entry_points(lib):
+    """Checkpoints, layer norm, GELU and the weight gradient refuse bad arguments before any device
+    call; workspace queries answer without one."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("fake pointers: run only where no GPU can be reached")
+    from allreduce_compatible_gradient_gb300 import _binding
+    L = _binding.lib()
+    fake = 1 << 20
+
+    def quant(x=fake, dt=0, rows=4, cols=64, ld=64, rnd=0, codes=fake, exps=fake):
+        return L.gq_act_quantize(x, dt, rows, cols, ld, rnd, 0, 0, codes, exps, None)
+    assert quant(rows=0) == 0                     # nothing to do: no device call
+    for bad in (dict(x=None), dict(x=fake + 2), dict(dt=2), dict(rows=-1), dict(cols=0), dict(ld=63),
+                dict(rnd=2), dict(codes=None), dict(codes=fake + 8), dict(exps=None), dict(exps=fake + 8),
+                dict(rows=1 << 31), dict(cols=(1 << 31) - 32)):
+        assert quant(**bad) == 1, bad
+
+    def dequant(codes=fake, exps=fake, out=fake, dt=1, ld=64):
+        return L.gq_act_dequantize(codes, exps, 4, 64, out, dt, ld, None)
+    for bad in (dict(codes=None), dict(exps=fake + 4), dict(out=None), dict(out=fake + 1), dict(dt=3),
+                dict(ld=10)):
+        assert dequant(**bad) == 1, bad
+
+    def forward(x=fake, dt=0, w=None, wdt=0, eps=1e-5, y=fake, mean=fake, rstd=fake, rnd=0, codes=None,
+                exps=None):
+        return L.gq_layernorm_forward(x, dt, 4, 64, 64, w, None, wdt, eps, y, 64, mean, rstd, rnd, 0, 0,
+                                      codes, exps, None)
+    for bad in (dict(x=None), dict(dt=2), dict(w=fake + 1), dict(wdt=2), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(y=None), dict(mean=None), dict(rstd=fake + 2), dict(rnd=3),
+                dict(codes=fake), dict(exps=fake)):
+        assert forward(**bad) == 1, bad
+
+    need = L.gq_layernorm_workspace_bytes(4, 64)
+    assert need == 4 * 2 * 64 * 4 and L.gq_layernorm_workspace_bytes(-1, 64) == 0
+    assert L.gq_layernorm_workspace_bytes(10 ** 6, 64) == 1024 * 2 * 64 * 4
+
+    def backward(rstd=fake, codes=fake, exps=fake, x=None, mean=None, gdt=0, dw=fake, ws=fake, n=need):
+        return L.gq_layernorm_backward(fake, 0, 4, 64, 64, None, 0, rstd, codes, exps, x, 64, mean, fake,
+                                       64, dw, None, gdt, ws, n, None)
+    for bad in (dict(rstd=None), dict(codes=None), dict(x=fake), dict(x=fake, codes=None, exps=None),
+                dict(codes=None, exps=None), dict(gdt=2), dict(dw=fake + 2)):
+        assert backward(**bad) == 1, bad
+    assert backward(ws=None) == 7 and backward(n=need - 1) == 7 and backward(ws=fake + 8) == 7
+
+    def gelu(u=fake, dt=0, form=0, h=fake, codes=fake, exps=fake):
+        return L.gq_gelu_forward(u, dt, 4, 64, 64, form, h, 64, 0, 0, 0, codes, exps, None)
+    for bad in (dict(u=None), dict(dt=2), dict(form=2), dict(h=None), dict(codes=None), dict(exps=None)):
+        assert gelu(**bad) == 1, bad
+    for bad in (dict(form=-1), dict(du=None), dict(h=fake + 1), dict(codes=None)):
+        a = dict(form=0, du=fake, h=None, codes=fake, **{}) | bad
+        assert L.gq_gelu_backward(fake, 0, 4, 64, 64, a["codes"], fake, a["form"], a["du"], 64, a["h"], 64,
+                                  None) == 1, bad
+
+    def ws_bytes(dt=1, rows=384, outs=768, ld=768, cols=768, dy=fake):
+        return L.gq_linear_wgrad_workspace_bytes(dy, dt, rows, outs, ld, cols)
+    assert ws_bytes() > 0 and ws_bytes(dt=2) == 0 and ws_bytes(outs=0) == 0 and ws_bytes(rows=1 << 29) == 0
+    assert ws_bytes(dt=0) > ws_bytes() and ws_bytes(ld=771) > ws_bytes()  # room for packed copies
+
+    def wgrad(dy=fake, dt=1, lddy=768, codes=fake, scale=None, dw=fake, odt=0, lddw=768, db=None, ws=fake,
+              n=ws_bytes()):
+        return L.gq_linear_wgrad(dy, dt, 384, 768, lddy, codes, fake, 768, scale, None, dw, odt, lddw, db,
+                                 ws, n, None)
+    for bad in (dict(dy=None), dict(dt=2), dict(lddy=767), dict(codes=None), dict(codes=fake + 8),
+                dict(scale=fake + 2), dict(dw=None), dict(odt=2), dict(lddw=10), dict(db=fake + 1)):
+        assert wgrad(**bad) == 1, bad
+    assert wgrad(ws=None) == 7 and wgrad(n=100) == 7
+    assert [L.gq_act_exp_pitch(c) for c in (0, 1, 512, 513)] == [0, 16, 16, 32]

@@ -79,6 +79,10 @@ def near(got, want, tol, dtype):
     assert (d <= tol).all(), (d.max(), (d / tol).max())
 
 
+# more rows than two per SM: several rows at a time per block (one to four warps each), and one row of
+# up to 16 warps
+WALKED = [(400, 512), (700, 1024), (320, 768), (350, 4096), (310, 8192), (400, 200)]
+
 SHAPES = [(1, 1), (1, 31), (3, 32), (2, 33), (5, 7), (33, 100), (4, 255), (9, 256), (7, 257),
           (17, 512), (3, 1000), (130, 768), (19, 1024), (2, 1025), (5, 2048), (3, 4100), (2, 8192),
           (1, 8200), (2, 17000), (1, 40001)]
@@ -162,7 +166,7 @@ def affine(torch, cols, kind, seed):
 
 @pytest.mark.parametrize("extra,kind", [(0, "f32"), (3, "bf16"), (8, "none")])
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + WALKED)
 def test_layernorm_forward(gq, torch, rows, cols, dtype, extra, kind):
     x, xv = tensor(torch, inputs(rows, cols, 3 * rows + cols) + 0.7, dtype, extra)
     w, b, wv, bv = affine(torch, cols, kind, cols)
@@ -198,7 +202,7 @@ def test_layernorm_forward(gq, torch, rows, cols, dtype, extra, kind):
 @pytest.mark.parametrize("source", ["codes", "input"])
 @pytest.mark.parametrize("extra,kind,gtype", [(0, "f32", "f32"), (3, "bf16", "bf16"), (8, "none", "f32")])
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("rows,cols", SHAPES + [(700, 96), (333, 1030), (300, 9000)])
+@pytest.mark.parametrize("rows,cols", SHAPES + WALKED + [(700, 96), (333, 1030), (300, 9000)])
 def test_layernorm_backward(gq, torch, rows, cols, dtype, extra, kind, gtype, source):
     x, xv = tensor(torch, inputs(rows, cols, 5 * rows + cols) + 0.3, dtype, extra)
     dy, dyv = tensor(torch, inputs(rows, cols, 7 * rows + cols, 1e-2), dtype, extra)
@@ -388,6 +392,40 @@ def test_linear_wgrad_large_tiles(gq, torch, rows, outs, cols):
     assert torch.equal(dw, again)
 
 
+@pytest.mark.parametrize("rows,outs,cols,dtype,out,affine_part", [
+    (4096, 1024, 4096, "bf16", "f32", True), (3001, 1030, 2050, "bf16", "bf16", True),
+    (16384, 520, 777, "bf16", "f32", False), (2500, 2048, 1500, "f32", "f32", True),
+    (20000, 700, 300, "f32", "bf16", False), (7000, 600, 4096, "bf16", "f32", False)])
+def test_linear_wgrad_pairs(gq, torch, rows, outs, cols, dtype, out, affine_part):
+    """Sizes for pairs of blocks (512 x 256 tiles): several chains, shares that cross tiles, last tiles
+    of fewer outs and columns, three parts of an fp32 gradient; against a 64-bit product."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((rows, cols), generator=g, device="cuda")
+    dy = (torch.randn((rows, outs), generator=g, device="cuda") * 1e-2).to(types(torch, dtype))
+    act = gq.gq_act_quantize(x)
+    v = gq.gq_act_dequantize(act, out_dtype=torch.float32).double()
+    scale = shift = None
+    s64 = torch.ones(cols, device="cuda", dtype=torch.float64)
+    h64 = torch.zeros_like(s64)
+    if affine_part:
+        scale, shift = (1 + 0.3 * torch.randn(cols, generator=g, device="cuda"),
+                        torch.randn(cols, generator=g, device="cuda"))
+        s64, h64 = scale.double(), shift.double()
+    dw, db = gq.gq_linear_wgrad(dy, act, scale=scale, shift=shift, out_dtype=types(torch, out))
+    d = dy.double()
+    want = (d.t() @ v) * s64 + torch.outer(d.sum(0), h64)
+    steps = 3 * rows if dtype == "f32" else rows
+    bias = d.abs().sum(0)
+    tolb = (rows + 40) * U * bias
+    tol = ((steps / 16 + 32) * 2.0 ** -22 + 4 * U) * (d.abs().t() @ v.abs()) * s64.abs() + \
+        torch.outer(tolb + 4 * U * bias, h64.abs()) + \
+        (2.0 ** -8 if out == "bf16" else U) * want.abs()
+    assert ((dw.double() - want).abs() <= tol).all()
+    assert ((db.double() - d.sum(0)).abs() <= tolb).all()
+    again, _ = gq.gq_linear_wgrad(dy, act, scale=scale, shift=shift, out_dtype=types(torch, out))
+    assert torch.equal(dw, again)
+
+
 def test_linear_wgrad_special_values(gq, torch):
     """A NaN block of the checkpoint reaches its columns only; an infinite gradient its row only."""
     x = np.random.default_rng(0).standard_normal((70, 96)).astype(np.float32)
@@ -404,6 +442,134 @@ def test_linear_wgrad_special_values(gq, torch):
         assert np.isfinite(others).all()
         assert not np.isfinite(w[3]).any()
         assert np.isinf(host(db)[3]) and np.isfinite(np.delete(host(db), 3)).all()
+
+
+# ---- large offsets, guard bands --------------------------------------------------------------
+
+def test_offsets_past_32_bits(gq, torch):
+    """2.4e9 elements (4.8 GB of bf16): the last rows equal a call of their own on the same rows."""
+    rows, cols, tail = 590_000, 4096, 64
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[:tail].normal_()
+    x[tail:-tail].zero_()
+    x[-tail:].normal_()
+    last = x[-tail:].clone()
+    act = gq.gq_act_quantize(x)
+    part = gq.gq_act_quantize(last)
+    assert torch.equal(act.codes[-tail:], part.codes)
+    v = gq.gq_act_dequantize(act)
+    assert torch.equal(v[-tail:], gq.gq_act_dequantize(part))
+    del v
+    y, mean, rstd, ln = gq.gq_layernorm_forward(x)
+    py, _, prstd, pln = gq.gq_layernorm_forward(last)
+    assert torch.equal(y[-tail:], py) and torch.equal(rstd[-tail:], prstd)
+    assert torch.equal(ln.codes[-tail:], pln.codes)
+    del y, act
+    dx, dw, db = gq.gq_layernorm_backward(x, None, rstd, act=ln)
+    pdx, _, _ = gq.gq_layernorm_backward(last, None, prstd, act=pln)
+    assert torch.equal(dx[-tail:], pdx)
+    want = x[:tail].double().sum(0) + last.double().sum(0)
+    assert torch.allclose(db.double(), want, atol=1e-3)
+    del dx
+    du = gq.gq_gelu_backward(x, ln)
+    assert torch.equal(du[-tail:], gq.gq_gelu_backward(last, pln))
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 33), (5, 100), (40, 1000), (7, 1024), (320, 520), (2, 8200)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_guard_bands(gq, torch, rows, cols, dtype):
+    """Through the C interface, with rows of outputs further apart than their length: nothing outside
+    the outputs' own elements is written."""
+    L = gq.lib()
+    t = torch.float32 if dtype == 0 else torch.bfloat16
+    gap, mark = 24, 123.0
+
+    def banded(n, m):
+        full = torch.full((n + 2, m + gap), mark, dtype=t, device="cuda")
+        return full, full[1:-1, :m], m + gap
+
+    def intact(full, m):
+        inner = full[1:-1]
+        return bool((full[0] == mark).all() and (full[-1] == mark).all() and (inner[:, m:] == mark).all())
+
+    def banded_bytes(n, m):
+        full = torch.full((n * m + 512,), 77, dtype=torch.uint8, device="cuda")
+        return full, full[256:256 + n * m]
+
+    st = torch.cuda.current_stream().cuda_stream
+    pitch, epitch = gq.gq_code_pitch(cols), gq.gq_act_exp_pitch(cols)
+    x = torch.randn((rows, cols), device="cuda").to(t)
+    cf, c = banded_bytes(rows, pitch)
+    ef, e = banded_bytes(rows, epitch)
+    yf, y, ldy = banded(rows, cols)
+    stats = torch.full((4 * rows,), mark, device="cuda")
+    for rounding in (0, 1):
+        assert L.gq_layernorm_forward(x.data_ptr(), dtype, rows, cols, cols, None, None, 0, 1e-5,
+                                      y.data_ptr(), ldy, stats[rows:].data_ptr(),
+                                      stats[2 * rows:].data_ptr(), rounding, 1, 1, c.data_ptr(),
+                                      e.data_ptr(), st) == 0
+        assert L.gq_act_quantize(x.data_ptr(), dtype, rows, cols, cols, rounding, 1, 1, c.data_ptr(),
+                                 e.data_ptr(), st) == 0
+    assert intact(yf, cols)
+    assert (stats[:rows] == mark).all() and (stats[3 * rows:] == mark).all()
+    yf, y, ldy = banded(rows, cols)
+    assert L.gq_gelu_forward(x.data_ptr(), dtype, rows, cols, cols, 0, y.data_ptr(), ldy, 0, 0, 0,
+                             c.data_ptr(), e.data_ptr(), st) == 0
+    assert intact(yf, cols)
+    for full in (cf, ef):
+        assert (full[:256] == 77).all() and (full[-256:] == 77).all()
+    of, o, ldo = banded(rows, cols)
+    assert L.gq_act_dequantize(c.data_ptr(), e.data_ptr(), rows, cols, o.data_ptr(), dtype, ldo, st) == 0
+    assert intact(of, cols)
+    of, o, ldo = banded(rows, cols)
+    hf, h, ldh = banded(rows, cols)
+    assert L.gq_gelu_backward(x.data_ptr(), dtype, rows, cols, cols, c.data_ptr(), e.data_ptr(), 1,
+                              o.data_ptr(), ldo, h.data_ptr(), ldh, st) == 0
+    assert intact(of, cols) and intact(hf, cols)
+    rstd = torch.ones(rows, device="cuda")
+    n = L.gq_layernorm_workspace_bytes(rows, cols)
+    wf, w = banded_bytes(1, n)
+    of, o, ldo = banded(rows, cols)
+    dw = torch.full((3, cols), mark, device="cuda")
+    assert L.gq_layernorm_backward(x.data_ptr(), dtype, rows, cols, cols, None, 0, rstd.data_ptr(),
+                                   c.data_ptr(), e.data_ptr(), None, 0, None, o.data_ptr(), ldo,
+                                   dw[1].data_ptr(), None, 0, w.data_ptr(), n, st) == 0
+    assert intact(of, cols) and (dw[0] == mark).all() and (dw[2] == mark).all()
+    assert (wf[:256] == 77).all() and (wf[-256:] == 77).all()
+    outs = 70
+    dy = torch.randn((rows, outs), device="cuda").to(t)
+    n = L.gq_linear_wgrad_workspace_bytes(dy.data_ptr(), dtype, rows, outs, outs, cols)
+    wf, w = banded_bytes(1, n)
+    of, o, ldo = banded(outs, cols)
+    db = torch.full((3, outs), mark, device="cuda")
+    assert L.gq_linear_wgrad(dy.data_ptr(), dtype, rows, outs, outs, c.data_ptr(), e.data_ptr(), cols,
+                             None, None, o.data_ptr(), dtype, ldo, db[1].data_ptr(), w.data_ptr(), n,
+                             st) == 0
+    assert intact(of, cols) and (db[0] == mark).all() and (db[2] == mark).all()
+    assert (wf[:256] == 77).all() and (wf[-256:] == 77).all()
+
+
+def test_graph_capture(gq, torch):
+    """A captured training step over the operators replays to the same bits."""
+    x = torch.randn((256, 512), device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn((256, 384), device="cuda", dtype=torch.bfloat16)
+    w, b = torch.ones(512, device="cuda"), torch.zeros(512, device="cuda")
+
+    def step():
+        y, _, rstd, act = gq.gq_layernorm_forward(x, w, b, seed=1, step=2)
+        dw, db = gq.gq_linear_wgrad(dy, act, scale=w, shift=b)
+        h, ga = gq.gq_gelu_forward(y)
+        return [y, dw, db, h, *gq.gq_layernorm_backward(gq.gq_gelu_backward(h, ga), w, rstd, act=act)]
+    want = step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for t in got:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)
 
 
 # ---- streams, empty inputs, refusals -------------------------------------------------------
