@@ -294,8 +294,12 @@ __device__ __forceinline__ void finish(const WArgs& a, int64_t o, int64_t i, flo
     }
 #pragma unroll
     for (int k = 0; k < N; k += 8) {
-        const float w[8] = {v[k], v[k + 1], v[k + 2], v[k + 3], v[k + 4], v[k + 5], v[k + 6], v[k + 7]};
-        finish_slow(a, o, i + k, w);
+        float w[8] = {v[k], v[k + 1], v[k + 2], v[k + 3], v[k + 4], v[k + 5], v[k + 6], v[k + 7]};
+        if constexpr (N > 8) {
+            if (i + k < a.cols) finish(a, o, i + k, w);
+        } else {
+            finish_slow(a, o, i + k, w);
+        }
     }
 }
 
@@ -597,63 +601,84 @@ template <typename C> __global__ void __launch_bounds__(256) join_kernel(const W
         const int r = (q >> 7) / (BN / 32) * 32 + (q & 31);
         const int c = (q >> 7) % (BN / 32) * 32 + (q >> 5 & 3) * 8;
         float v[8] = {};
-#pragma unroll 2
-        for (int b = b0; b <= b1; b = (b | 1) + 1) {  // slot b0, then slot 0 of the shares after it
-            uint32_t w[8];
-            ld32<32>(a.partial + static_cast<int64_t>(b) * (C::kRows * BN) + partial_at<BN>(r, c), w);
+        const float* p = a.partial + partial_at<BN>(r, c);
+        for (int b = b0; b <= b1;) {  // slot b0, then slot 0 of the shares after it; four in flight
+            uint32_t w[4][8];
+            int n = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[k]);
+            for (int j = 0; j < 4; ++j) {
+                if (b <= b1) {
+                    ld32<32>(p + static_cast<int64_t>(b) * (C::kRows * BN), w[j]);
+                    b = (b | 1) + 1;
+                    n = j + 1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j < n) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[j][k]);
+                }
+            }
         }
         finish(a, static_cast<int64_t>(blockIdx.x % a.tiles_m) * C::kRows + r,
                static_cast<int64_t>(blockIdx.x / a.tiles_m) * BN + c, v);
     }
 }
 
-// dy as the TMA needs it: rows of `pitch` bf16 (a multiple of 8), `tokens` per part (whole steps),
-// zeros behind the last row.  fp32 is cut into three parts of 8 bits each by truncation, whose
-// sum is the number itself; an infinity or a NaN stays in the first.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    pack_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs, bf16* out,
-                int64_t pitch, int64_t tokens) {
-    const int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (o >= pitch) return;
-    for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
-        const bool in = t < rows && o < outs;
-        if constexpr (sizeof(T) == 2) {
-            out[t * pitch + o] = in ? dy[t * ld + o] : __float2bfloat16_rn(0.0f);
-        } else {
-            float v = in ? dy[t * ld + o] : 0.0f;
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                const uint32_t top = __float_as_uint(v) & 0xFFFF0000u;
-                const bool special = (top & 0x7F800000u) == 0x7F800000u;
-                const bool nan = (__float_as_uint(v) & 0x7FFFFFFFu) > 0x7F800000u;
-                reinterpret_cast<uint16_t*>(out)[(p * tokens + t) * pitch + o] =
-                    static_cast<uint16_t>(nan ? 0x7FFFu : top >> 16);
-                v = special ? 0.0f : v - __uint_as_float(top);
-            }
-        }
-    }
-}
-
-// Column sums of dy: thread = V columns, 32 rows at a time per block; partial[blockIdx.y][outs], or db
-// itself where one block row does.
-template <typename T, int V>
+// One pass over dy, 32 rows at a time per block, thread = V columns:
+// - its column sums (partial not null): partial[blockIdx.y][outs], or db itself where one block row does;
+// - PACK: dy as the TMA needs it: rows of `pitch` bf16 (a multiple of 8), `tokens` per part (whole
+//   steps), zeros behind the last row and column.  fp32 is cut into three parts of 8 bits each by
+//   truncation, whose sum is the number itself; an infinity or a NaN stays in the first.
+template <typename T, int V, bool PACK>
 __global__ void __launch_bounds__(1024)
     bias_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
-                float* __restrict__ partial) {
+                float* __restrict__ partial, bf16* __restrict__ out, int64_t pitch, int64_t tokens) {
     __shared__ float tile[32][32 * V + 1];
-    gq::pdl_launch_dependents();  // what follows waits for these sums where it reads them
+    if constexpr (!PACK) gq::pdl_launch_dependents();  // what follows waits where it reads the sums
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * V;
     float s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 0.0f;
-    if (c < outs) {
-        const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
-        const T* p = dy + (static_cast<int64_t>(blockIdx.y) * 32 + y) * ld;
-        int64_t left = rows - (static_cast<int64_t>(blockIdx.y) * 32 + y);
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32 + y;
+    if constexpr (PACK) {
+        if (c < pitch) {
+#pragma unroll 2
+            for (int64_t t = t0; t < tokens; t += stride) {
+                float v[V];
+                if (t < rows) {
+                    load<T, V, 16>(dy + t * ld, c, outs, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+                }
+                uint32_t top[V];
+#pragma unroll
+                for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        if (p == 0) s[i] += v[i];
+                        const uint32_t bits = __float_as_uint(v[i]);
+                        top[i] = (bits & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FFF0000u : bits & 0xFFFF0000u;
+                        const bool special = (bits & 0x7F800000u) == 0x7F800000u;
+                        v[i] = special ? 0.0f : v[i] - __uint_as_float(top[i]);
+                    }
+                    bf16* to = out + (p * tokens + t) * pitch + c;
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint4*>(to) =
+                            make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3],
+                                       top[4] >> 16 | top[5], top[6] >> 16 | top[7]);
+                    else
+                        *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(top[0] >> 16);
+                }
+            }
+        }
+    } else if (c < outs) {
+        const T* p = dy + t0 * ld;
+        int64_t left = rows - t0;
         if constexpr (V == 8) {
             // (the test for the last columns is outside, so that the loads are issued together)
             if (c + V <= outs) {
@@ -675,14 +700,6 @@ __global__ void __launch_bounds__(1024)
                     }
                 }
             }
-        } else {
-            for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
-                float v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = up(p[k * stride * ld + c]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[0] += v[k];
-            }
         }
         for (; left > 0; left -= stride, p += stride * ld) {
             float v[V];
@@ -691,18 +708,18 @@ __global__ void __launch_bounds__(1024)
             for (int i = 0; i < V; ++i) s[i] += v[i];
         }
     }
+    if (!partial) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) tile[y][x * V + i] = s[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < V; ++i) {  // a warp adds up a column
         const int col = y * V + i;
-        const float t = tile[x][col];
-        float v = t;
+        float v = tile[x][col];
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-        const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 * V + col;
-        if (x == 0 && out < outs) partial[blockIdx.y * outs + out] = v;
+        const int64_t to = static_cast<int64_t>(blockIdx.x) * 32 * V + col;
+        if (x == 0 && to < outs) partial[blockIdx.y * outs + to] = v;
     }
 }
 __global__ void __launch_bounds__(256)
@@ -723,6 +740,23 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int k = 0; k < 8; ++k) v += tile[k][threadIdx.x];
         db[c] = v;
+    }
+}
+
+// dw from finished fp32 sums in rows of `ld`: for a dw whose rows are not aligned, which the main kernel
+// could only store element by element.
+__global__ void __launch_bounds__(256)
+    finish_kernel(const WArgs a, const float* __restrict__ sums, int64_t ld) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.cols) return;
+    const float f = a.scale ? a.scale[i] : 1.0f, g = a.shift ? a.shift[i] : 0.0f;
+#pragma unroll 4
+    for (int64_t o = blockIdx.y; o < a.outs; o += gridDim.y) {
+        float x = sums[o * ld + i];
+        if (a.scale) x = x * f;
+        if (a.shift) x = fmaf(a.db[o], g, x);
+        if (a.out_f32) static_cast<float*>(a.dw)[o * a.ldw + i] = x;
+        else static_cast<bf16*>(a.dw)[o * a.ldw + i] = __float2bfloat16_rn(x);
     }
 }
 
@@ -751,7 +785,8 @@ struct WPlan {
     int parts;           // bf16 parts of dy
     int64_t ktok, ksteps, tiles_m, tiles_n, units, pitch;
     int shares, bias_shares;  // of the steps; of the rows in the bias sums
-    size_t pack_off, bias_off, db_off, bytes;
+    size_t pack_off, bias_off, db_off, sums_off, bytes;
+    int64_t sums_ld;     // of the fp32 sums for a dw with unaligned rows (0: none)
 };
 
 WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t ld, int64_t cols) {
@@ -782,8 +817,9 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
         if (tiles <= most) {
             consider(tiles, static_cast<double>(p.ksteps), true);
             const int64_t q = most / tiles;  // shares per tile, none of which crosses tiles
-            if (q > 1 && p.ksteps >= 2 * q)
-                consider(tiles * q, static_cast<double>((p.ksteps + q - 1) / q), false);
+            // (adding the partial tiles takes about 0.15 us for each of a tile's)
+            for (int64_t k = 2; k <= q && p.ksteps >= 2 * k; k = k < 8 ? k + 1 : k * 5 / 4)
+                consider(tiles * k, static_cast<double>((p.ksteps + k - 1) / k) + 0.15 * k / step, false);
         }
         const double even = static_cast<double>(tiles) * p.ksteps / most;
         if (even >= 4.0) consider(most, even + 2.0, tiles % most == 0);
@@ -793,17 +829,22 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.tiles_n = (cols + cols_of - 1) / cols_of;
     p.units = p.tiles_m * p.tiles_n * p.ksteps;
     p.pitch = (outs + 7) / 8 * 8;
-    // sums of dy: up to 512 rows in one go, else one wave of blocks (one per SM)
-    const int64_t groups = (outs + 255) / 256;
-    int64_t sh = rows <= 512 ? 1 : groups < sms ? sms / groups : 1;
-    if (sh > (rows + 127) / 128) sh = (rows + 127) / 128;
+    // the pass over dy: up to 512 rows in one go if there are only sums to take, else one wave of blocks
+    // (one per SM)
+    const int64_t groups = row_align(dy, dtype, rows, ld) ? (outs + 255) / 256 : (outs + 31) / 32;
+    int64_t sh = rows <= 512 && !p.pack ? 1 : groups < sms ? sms / groups : 1;
+    const int64_t rows_each = p.pack ? 32 : 128;
+    if (sh > (rows + rows_each - 1) / rows_each) sh = (rows + rows_each - 1) / rows_each;
     p.bias_shares = static_cast<int>(sh);
     auto up256 = [](size_t v) { return (v + 255) / 256 * 256; };
     p.pack_off = up256(static_cast<size_t>(p.shares) * 2 * rows_of * cols_of * sizeof(float));
     p.bias_off = p.pack_off +
                  (p.pack ? up256(static_cast<size_t>(p.ksteps) * kTok * p.pitch * 2) : 0);
     p.db_off = p.bias_off + up256(static_cast<size_t>(p.bias_shares) * outs * sizeof(float));
-    p.bytes = p.db_off + up256(static_cast<size_t>(outs) * sizeof(float)) + 256;  // to align the start
+    p.sums_off = p.db_off + up256(static_cast<size_t>(outs) * sizeof(float));
+    p.sums_ld = cols % 8 ? (cols + 7) / 8 * 8 : 0;
+    p.bytes = p.sums_off + up256(static_cast<size_t>(outs) * p.sums_ld * sizeof(float)) + 256;  // to align
+                                                                                               // the start
     return p;
 }
 
@@ -816,10 +857,10 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
            static_cast<double>(rows) * outs * cols < 1e17;
 }
 
-// after_bias: the launch before this one on the stream is of the sums of dy, which the kernel waits for
-// only where it reads them; what came before those is done when it starts.
+// early: the launch before this one on the stream is of the sums of dy, which the kernel waits for only
+// where it reads them; what came before those is done when it starts.
 template <typename C>
-gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool after_bias, cudaStream_t st) {
+gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool early, cudaStream_t st) {
     auto k = wgrad_kernel<C>;
     gqh::blocks_per_sm(k, C::kSmem, C::kThreads);  // raises the shared-memory limit once
     cudaLaunchConfig_t cfg = {};
@@ -829,7 +870,7 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool 
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = after_bias ? 1 : 0;
+    attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = C::CG;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -883,37 +924,26 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
 
     const void* src = dy;
     int64_t src_ld = lddy, src_rows = rows, src_outs = outs;
-    if (p.pack) {
-        bf16* out = reinterpret_cast<bf16*>(w + p.pack_off);
+    const bool sums = dbias || shift;
+    if (p.pack || sums) {
+        float* part = !sums ? nullptr : p.bias_shares > 1 ? reinterpret_cast<float*>(w + p.bias_off) : db;
         const int64_t tokens = p.ktok * kTok;
-        const dim3 grid(static_cast<unsigned>((p.pitch + 255) / 256),
-                        static_cast<unsigned>(tokens < 4096 ? tokens : 4096));
-        if (dtype == GQ_F32)
-            pack_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(dy), lddy, rows, outs,
-                                                     out, p.pitch, tokens);
-        else
-            pack_kernel<bf16><<<grid, 256, 0, st>>>(static_cast<const bf16*>(dy), lddy, rows, outs,
-                                                    out, p.pitch, tokens);
-        src = out;
-        src_ld = p.pitch;
-        src_rows = tokens * p.parts;
-        src_outs = p.pitch;
-    }
-    if (dbias || shift) {
-        float* part = p.bias_shares > 1 ? reinterpret_cast<float*>(w + p.bias_off) : db;
+        bf16* out = p.pack ? reinterpret_cast<bf16*>(w + p.pack_off) : nullptr;
         const bool vec = row_align(dy, dtype, rows, lddy) != 0;
-        const int v = vec ? 8 : 1;
-        const dim3 grid(static_cast<unsigned>((outs + 32 * v - 1) / (32 * v)), p.bias_shares);
+        const int64_t cols_of = 32 * (vec ? 8 : 1), across = p.pack ? p.pitch : outs;
+        const dim3 grid(static_cast<unsigned>((across + cols_of - 1) / cols_of), p.bias_shares);
+#define GQA_SUMS(T, V, PACK)                                                                         \
+    bias_kernel<T, V, PACK><<<grid, 1024, 0, st>>>(static_cast<const T*>(dy), lddy, rows, outs, part, out, \
+                                                   p.pitch, tokens)
         if (dtype == GQ_F32) {
-            const float* g = static_cast<const float*>(dy);
-            if (vec) bias_kernel<float, 8><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
-            else bias_kernel<float, 1><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
+            if (vec) GQA_SUMS(float, 8, true); else GQA_SUMS(float, 1, true);
+        } else if (p.pack) {
+            GQA_SUMS(bf16, 1, true);
         } else {
-            const bf16* g = static_cast<const bf16*>(dy);
-            if (vec) bias_kernel<bf16, 8><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
-            else bias_kernel<bf16, 1><<<grid, 1024, 0, st>>>(g, lddy, rows, outs, part);
+            GQA_SUMS(bf16, 8, false);  // aligned: else it would be packed
         }
-        if (p.bias_shares > 1) {
+#undef GQA_SUMS
+        if (sums && p.bias_shares > 1) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>((outs + 31) / 32));
             cfg.blockDim = dim3(256);
@@ -926,6 +956,12 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
             if (cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(part), p.bias_shares,
                                    outs, db) != cudaSuccess)
                 return GQ_ERR_CUDA;
+        }
+        if (p.pack) {
+            src = out;
+            src_ld = p.pitch;
+            src_rows = tokens * p.parts;
+            src_outs = p.pitch;
         }
     }
     CUtensorMap map;
@@ -951,9 +987,23 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
     a.units = p.units;
     a.base = p.units / p.shares; a.rest = static_cast<int>(p.units % p.shares);
-    const bool after_bias = dbias || shift;
-    return p.big ? launch_wgrad<Large>(map, a, p.shares, after_bias, st)
-                 : launch_wgrad<Small>(map, a, p.shares, after_bias, st);
+    const WArgs wanted = a;
+    float* raw = p.sums_ld && !a.fast ? reinterpret_cast<float*>(w + p.sums_off) : nullptr;
+    if (raw) {  // aligned fp32 sums first, padding columns among them (their codes are 0)
+        a.scale = a.shift = nullptr;
+        a.dw = raw;
+        a.ldw = a.cols = p.sums_ld;
+        a.out_f32 = a.fast = 1;
+    }
+    // a packed dy has to be there before the main kernel starts; sums alone only where it reads them
+    const bool early = sums && !p.pack;
+    const gq_status r = p.big ? launch_wgrad<Large>(map, a, p.shares, early, st)
+                              : launch_wgrad<Small>(map, a, p.shares, early, st);
+    if (r != GQ_OK || !raw) return r;
+    const dim3 grid(static_cast<unsigned>((cols + 255) / 256),
+                    static_cast<unsigned>(outs < 16384 ? (outs + 3) / 4 : 4096));
+    finish_kernel<<<grid, 256, 0, st>>>(wanted, raw, p.sums_ld);
+    return gqh::launch_status();
 }
 
 }  // extern "C"
