@@ -1,7 +1,7 @@
 """Compile the CUDA library (csrc/*.cu over csrc/gq_kernels.cuh) into libgq.so, in-tree, and the
 extension module through which Python calls its activation operators (csrc/gq_native.cpp).
 
-Eight translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
+Nine translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
 gradient type and scheme; the activation kernels) compiled in parallel with one -gencode
 (sm_103a), then linked with the static CUDA runtime: the library depends on nothing but the driver
 at load time.  -fmad=false keeps every fp32 operation of the gradient path a separately rounded
@@ -19,8 +19,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 UNITS = ["gq.cu", "gq_quant_f32_l.cu", "gq_quant_f32_e.cu", "gq_quant_bf16_l.cu",
-         "gq_quant_bf16_e.cu", "gq_act.cu", "gq_layernorm.cu", "gq_wgrad.cu"]
-CONTRACTED = {"gq_act.cu", "gq_layernorm.cu", "gq_wgrad.cu"}
+         "gq_quant_bf16_e.cu", "gq_act.cu", "gq_layernorm_fwd.cu", "gq_layernorm_bwd.cu",
+         "gq_wgrad.cu"]
+CONTRACTED = {"gq_act.cu", "gq_layernorm_fwd.cu", "gq_layernorm_bwd.cu", "gq_wgrad.cu"}
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgq.so")
 # the same library with the kernels' bounds checks compiled in (-DGQ_DEBUG)

@@ -1,0 +1,470 @@
+// gq_layernorm_bwd.cu -- layer norm backward, from an 8-bit checkpoint of the normalised rows or from x.
+//
+// dw and db of a thread's columns stay in its registers over all the rows of its block; every block
+// leaves one partial row in the workspace, and a second kernel adds those in a fixed order, so that
+// results do not depend on timing.
+#include "gq_layernorm.cuh"
+
+using namespace gqa;
+
+namespace {
+
+constexpr int kSumRows = 32;   // threads that share a column of the partial rows
+
+// What the backward pass reads the normalised row from: its checkpoint, or x with the row's mean
+// and rstd.
+template <typename T> struct Source {
+    const int8_t* codes;
+    const uint8_t* exps;
+    const T* x;
+    int64_t ldx;
+    const float* mean;
+};
+
+template <typename T, int V, bool CODES>
+__device__ __forceinline__ void hat_of(const Source<T>& src, const Shape& s, int64_t row, float mean,
+                                       float rstd, int64_t c, float (&v)[V]) {
+    if constexpr (CODES) {
+        if (c < s.pitch) {
+            saved<V>(src.codes + row * s.pitch, src.exps + row * s.epitch, c, v);
+            if (c + V > s.cols) {  // a block marked 255 reads as NaN in the padding too
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (c + i >= s.cols) v[i] = 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        }
+    } else {
+        load<T, V, 16>(src.x + row * src.ldx, c, s.cols, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = c + i < s.cols ? (v[i] - mean) * rstd : 0.0f;
+    }
+}
+
+// dx of rows of more columns than the held form takes: a block per row.
+template <typename T, int V, int VPT, bool CODES>
+__global__ void __launch_bounds__(512)
+    backward_kernel(const T* __restrict__ dy, int64_t lddy, Shape s, const void* w, int wide,
+                    const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx,
+                    int64_t lddx) {
+    __shared__ float buf[32][2];
+    const int threads = blockDim.x, t = threadIdx.x;
+    const int64_t step = static_cast<int64_t>(threads) * V;
+    const int64_t beyond = step * VPT, row = blockIdx.x;
+
+    const T* dyr = dy + row * lddy;
+    T* dxr = dx + row * lddx;
+    const float rstd = rstd_in[row];
+    const float mean = CODES ? 0.0f : src.mean[row];
+    float g[VPT][V], h[VPT][V];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        load<T, V, 16>(dyr, k * step + t * V, s.cols, g[k]);
+        hat_of<T, V, CODES>(src, s, row, mean, rstd, k * step + t * V, h[k]);
+    }
+    float c[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        float wv[V];
+        vec_of<V>(w, wide, 1.0f, k * step + t * V, s.cols, wv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            g[k][i] *= wv[i];
+            c[0] += g[k][i];
+            c[1] = fmaf(g[k][i], h[k][i], c[1]);
+        }
+    }
+    for (int64_t col = beyond + t * V; col < s.cols; col += step) {
+        float a[V], b[V], wv[V];
+        load<T, V, 16>(dyr, col, s.cols, a);
+        hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
+        vec_of<V>(w, wide, 1.0f, col, s.cols, wv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] *= wv[i];
+            c[0] += a[i];
+            c[1] = fmaf(a[i], b[i], c[1]);
+        }
+    }
+    row_sum(c, buf, threads);
+    const float c1 = c[0] * s.inv_cols, c2 = c[1] * s.inv_cols;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int64_t col = k * step + t * V;
+        if (col < s.cols) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                g[k][i] = (g[k][i] - fmaf(h[k][i], c2, c1)) * rstd;
+            store<T, V, 16>(dxr, col, s.cols, g[k]);
+        }
+    }
+    for (int64_t col = beyond + t * V; col < s.cols; col += step) {
+        float a[V], b[V], wv[V];
+        load<T, V, 16>(dyr, col, s.cols, a);
+        hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
+        vec_of<V>(w, wide, 1.0f, col, s.cols, wv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = (a[i] * wv[i] - fmaf(b[i], c2, c1)) * rstd;
+        store<T, V, 16>(dxr, col, s.cols, a);
+    }
+}
+
+// Column sums for rows that do not fit the registers: thread = column, blockIdx.y = a share of
+// the rows; partial[blockIdx.y][0 and 1][cols].
+template <typename T, bool CODES>
+__global__ void __launch_bounds__(256)
+    columns_kernel(const T* __restrict__ dy, int64_t lddy, Shape s,
+                   const float* __restrict__ rstd_in, Source<T> src, float* __restrict__ partial) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (col >= s.cols) return;
+    float aw = 0.0f, ab = 0.0f;
+#pragma unroll 4
+    for (int64_t row = blockIdx.y; row < s.rows; row += gridDim.y) {
+        const float g = up(dy[row * lddy + col]);
+        float h[1];
+        hat_of<T, 1, CODES>(src, s, row, CODES ? 0.0f : src.mean[row], rstd_in[row], col, h);
+        aw = fmaf(g, h[0], aw);
+        ab += g;
+    }
+    float* p = partial + static_cast<int64_t>(blockIdx.y) * 2 * s.cols + col;
+    p[0] = aw;
+    p[s.cols] = ab;
+}
+
+// Adds the partial rows: 32 columns x 32 shares of the rows per block.
+template <typename G>
+__global__ void __launch_bounds__(1024)
+    sum_kernel(const float* __restrict__ partial, int parts, int64_t cols, G* __restrict__ dw,
+               G* __restrict__ db) {
+    __shared__ float tile[kSumRows][33];
+    gq::pdl_wait();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    float a = 0.0f;
+    if (col < 2 * cols) {
+#pragma unroll 8
+        for (int p = threadIdx.y; p < parts; p += kSumRows) a += partial[p * 2 * cols + col];
+    }
+    tile[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    const float total = warp_sum(tile[threadIdx.x][threadIdx.y]);
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && out < 2 * cols) {
+        if (out < cols) {
+            if (dw) down(total, dw[out]);
+        } else if (db) {
+            down(total, db[out - cols]);
+        }
+    }
+}
+
+// The block's rows' sums of dy xh and dy go to partial[block][0 and 1][cols].
+template <typename T, bool ALIGNED, int VPT, bool CODES, int W, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
+    backward_rows(const T* __restrict__ dy, HeldArgs a, const void* w, int wide,
+                  const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx,
+                  float* __restrict__ partial) {
+    gq::pdl_launch_dependents();  // sum_kernel, which waits for this one's end before it reads
+    __shared__ alignas(16) float buf[2][2 * kSlots];
+    extern __shared__ __align__(16) uint8_t ring[];  // afterwards 2 x cols sums, with several groups
+    const int warp = threadIdx.x >> 5;
+    const int group = W == kMany ? 0 : warp / a.wpr, wr = warp - group * a.wpr;
+    const uint32_t t = wr * 32 + (threadIdx.x & 31), apart = a.wpr * 256;
+    for (int i = threadIdx.x; i < 4 * kSlots; i += blockDim.x) (&buf[0][0])[i] = 0.0f;
+    __syncthreads();
+    float* const slots = &buf[0][W == kFour ? group * 8 : 0];
+    bool in[VPT];
+    uint32_t col[VPT];
+    int left[VPT];  // elements of the row from col on
+    F2 wv[VPT][4], aw[VPT][4], ab[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const uint32_t c = k * apart + t * 8;
+        in[k] = c < a.cols;
+        col[k] = in[k] ? c : 0u;
+        left[k] = static_cast<int>(a.cols - col[k]);
+        vec8<ALIGNED>(w, wide, 1.0f, c, a.cols, wv[k]);
+        if (!in[k]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wv[k][i] = f2(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = f2(0.0f);
+    }
+    // a slot: dy's planes of 16 bytes per thread, then x's or those of 8 and 4 for the checkpoint (4
+    // exponent bytes, of which one is this thread's)
+    using R = Ring<T, ALIGNED>;
+    constexpr int P = R::kPieces, D = R::kSlots;
+    const uint32_t n = blockDim.x, tid = threadIdx.x, plane = n * 16;
+    const uint32_t second = plane * VPT * P, third = second + VPT * n * 8;
+    const uint32_t slot_bytes = CODES ? third + VPT * n * 4 : 2 * second;
+    const uint32_t base = gq::smem_u32(ring);
+    uint32_t row = blockIdx.x * a.groups + group, ahead = row, turn = 0;
+    auto fetch = [&]() {  // (the last row again where there is none)
+        const uint32_t r = min(ahead, a.rows - 1), to = base + (turn & (D - 1)) * slot_bytes;
+        const T* p = row_of(dy, r, a.in);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            R::fetch(to + k * P * plane + tid * 16, plane, p + col[k], left[k]);
+            if constexpr (CODES) {
+                copy_async<8>(to + second + (k * n + tid) * 8, row_of(src.codes, r, a.pitch) + col[k]);
+                copy_async<4>(to + third + (k * n + tid) * 4,
+                              row_of(src.exps, r, a.epitch) + col[k] / 128 * 4);
+            } else {
+                R::fetch(to + second + k * P * plane + tid * 16, plane,
+                         row_of(src.x, r, a.in2) + col[k], left[k]);
+            }
+        }
+        copy_commit();
+        ahead += a.stride;
+        ++turn;
+    };
+    float* square = reinterpret_cast<float*>(ring + D * slot_bytes) + warp * kSquare;
+    float nrstd = 0.0f, nmean = 0.0f;
+    if (row < a.rows) {
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) fetch();
+        nrstd = __ldg(rstd_in + row);
+        if constexpr (!CODES) nmean = __ldg(src.mean + row);
+    }
+    float* set = slots;
+    for (; row < a.rows; row += a.stride) {
+        F2 gv[VPT][4], h[VPT][4];
+        const float rstd = nrstd, mean = nmean;
+        const uint32_t next = min(row + a.stride, a.rows - 1);
+        nrstd = __ldg(rstd_in + next);
+        if constexpr (!CODES) nmean = __ldg(src.mean + next);
+        fetch();
+        copy_wait<D>();
+        const uint8_t* slot = ring + (turn & (D - 1)) * slot_bytes;
+        F2 c1 = f2(0.0f), c2 = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            R::read(slot + k * P * plane + tid * 16, plane, row_of(dy, row, a.in) + col[k], left[k], gv[k]);
+            if constexpr (CODES) {
+                const uint2 q = *reinterpret_cast<const uint2*>(slot + second + (k * n + tid) * 8);
+                const uint32_t e4 = *reinterpret_cast<const uint32_t*>(slot + third + (k * n + tid) * 4);
+                values8(q, e4 >> (col[k] / 32 % 4 * 8) & 0xFFu, h[k]);
+            } else {
+                R::read(slot + second + k * P * plane + tid * 16, plane,
+                        row_of(src.x, row, a.in2) + col[k], left[k], h[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[k][i] = mul2(add2(h[k][i], f2(-mean)), f2(rstd));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                aw[k][i] = fma2(gv[k][i], h[k][i], aw[k][i]);
+                ab[k][i] = add2(ab[k][i], gv[k][i]);
+                gv[k][i] = mul2(gv[k][i], wv[k][i]);
+                c1 = add2(c1, gv[k][i]);
+                c2 = fma2(gv[k][i], h[k][i], c2);
+            }
+        }
+        float m[2] = {sum2(c1), sum2(c2)};
+        group_sum<W>(m, set, wr, a.wpr, group);
+        set = slots + (set == slots ? 2 * kSlots : 0);
+        // dx = rstd g - (rstd mean2) xh - rstd mean1
+        const float by = -a.inv_cols * rstd;
+        const F2 rs = f2(rstd), m1 = f2(m[0] * by), m2 = f2(m[1] * by);
+        T* p = row_of(dx, row, a.out);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                gv[k][i] = fma2(gv[k][i], rs, fma2(h[k][i], m2, m1));
+            put8<T, ALIGNED>(p, col[k], in[k], k * apart + wr * 256, a.cols, square, gv[k]);
+        }
+    }
+    copy_all();
+    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    float* shared_cols = reinterpret_cast<float*>(ring);
+    float* out = a.groups > 1 ? shared_cols : pw;
+    for (int q = 0; q < a.groups; ++q) {  // the groups add up their columns one after another
+        if (a.groups > 1) __syncthreads();
+        if (group != q) continue;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (!in[k]) continue;
+            if constexpr (!ALIGNED) {
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    float u[2], d[2];
+                    split(aw[k][z / 2], u[0], u[1]);
+                    split(ab[k][z / 2], d[0], d[1]);
+                    if (z >= left[k]) continue;
+                    float* at = out + col[k] + z;
+                    at[0] = (q > 0 ? at[0] : 0.0f) + u[z & 1];
+                    at[a.cols] = (q > 0 ? at[a.cols] : 0.0f) + d[z & 1];
+                }
+            } else {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {  // 4 columns of dw, 4 more, the same of db
+                    const F2 lo = z < 2 ? aw[k][2 * z] : ab[k][2 * z - 4];
+                    const F2 hi = z < 2 ? aw[k][2 * z + 1] : ab[k][2 * z - 3];
+                    float4 v;
+                    split(lo, v.x, v.y);
+                    split(hi, v.z, v.w);
+                    float4* at = reinterpret_cast<float4*>(out + (z < 2 ? 0u : a.cols) + col[k] + (z & 1) * 4);
+                    if (q > 0) {
+                        const float4 u = *at;
+                        v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+                    }
+                    *at = v;
+                }
+            }
+        }
+    }
+    if (a.groups > 1) {
+        __syncthreads();
+        if constexpr (ALIGNED) {
+            for (uint32_t i = threadIdx.x; i < a.cols / 2; i += blockDim.x)
+                reinterpret_cast<float4*>(pw)[i] = reinterpret_cast<const float4*>(shared_cols)[i];
+        } else {
+            for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) pw[i] = shared_cols[i];
+        }
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+// Partial rows: at most one per block of the main kernel, or the row shares of the column kernel.
+constexpr int kMostParts = 1024;
+
+template <typename T>
+struct BackwardCall {
+    const T* dy;
+    int64_t lddy;
+    Shape s;
+    const void* w;
+    int wide;
+    const float* rstd;
+    Source<T> src;
+    T* dx;
+    int64_t lddx;
+    float* partial;
+    cudaStream_t st;
+};
+
+template <typename T, bool ALIGNED, bool CODES> struct BackwardHeld {
+    const BackwardCall<T>& a;
+    const Held& h;
+    template <int VPT, int W, int MOST> int operator()() const {
+        if constexpr (MOST == 512 && sizeof(T) == 4) {
+            return 0;  // not reached: such rows take the long form
+        } else {
+            using R = Ring<T, ALIGNED>;
+            // (also room for 2 x cols sums: 56 bytes per thread and piece at least)
+            const size_t smem = static_cast<size_t>(R::kSlots) * h.threads * VPT *
+                                    (CODES ? 16 * R::kPieces + 12 : 32 * R::kPieces) +
+                                (ALIGNED ? 0 : h.threads / 32 * kSquare * sizeof(float));
+            auto k = backward_rows<T, ALIGNED, VPT, CODES, W, MOST>;
+            int grid = wave(resident_blocks(k, h.threads, smem), (a.s.rows + h.groups - 1) / h.groups);
+            if (grid > kMostParts) grid = kMostParts;
+            const HeldArgs ha = held_args(h, grid, a.s, a.lddy * sizeof(T), a.src.ldx * sizeof(T),
+                                          a.lddx * sizeof(T));
+            k<<<grid, h.threads, smem, a.st>>>(a.dy, ha, a.w, a.wide, a.rstd, a.src, a.dx, a.partial);
+            return grid;
+        }
+    }
+};
+template <typename T, int V, int VPT, bool CODES> void backward_generic(const BackwardCall<T>& a) {
+    const int threads = threads_for(a.s.cols, V * VPT, 128, 512);
+    backward_kernel<T, V, VPT, CODES><<<static_cast<unsigned>(a.s.rows), threads, 0, a.st>>>(
+        a.dy, a.lddy, a.s, a.w, a.wide, a.rstd, a.src, a.dx, a.lddx);
+}
+
+template <typename T, bool CODES>
+gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype, bool vec) {
+    const int64_t cols = a.s.cols;
+    int64_t ld = a.lddy > a.lddx ? a.lddy : a.lddx;
+    if (a.src.ldx > ld) ld = a.src.ldx;
+    int parts;
+    // (the ring of fp32 rows of more than 4,096 columns would pass the shared memory)
+    if (held_ok(cols, ld * sizeof(T)) && (sizeof(T) == 2 || cols <= kHeldCols / 2)) {
+        const Held h = held_for(a.s.rows, cols);
+        parts = vec && cols % 8 == 0 ? held_switch(h, BackwardHeld<T, true, CODES>{a, h})
+                                     : held_switch(h, BackwardHeld<T, false, CODES>{a, h});
+    } else {
+        if (vec) backward_generic<T, 8, 2, CODES>(a);
+        else backward_generic<T, 1, 8, CODES>(a);
+        parts = static_cast<int>((a.s.rows + 63) / 64 < 64 ? (a.s.rows + 63) / 64 : 64);
+        const dim3 grid(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(parts));
+        if (dw || db)
+            columns_kernel<T, CODES><<<grid, 256, 0, a.st>>>(a.dy, a.lddy, a.s, a.rstd, a.src, a.partial);
+    }
+    if (cudaPeekAtLastError() == cudaSuccess && (dw || db)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>((2 * cols + 31) / 32));
+        cfg.blockDim = dim3(32, kSumRows);
+        cfg.stream = a.st;
+        cudaLaunchAttribute attr;  // its launch overlaps the main kernel's end
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const float* partial = a.partial;
+        const cudaError_t e =
+            gdtype == GQ_F32 ? cudaLaunchKernelEx(&cfg, sum_kernel<float>, partial, parts, cols,
+                                                  static_cast<float*>(dw), static_cast<float*>(db))
+                             : cudaLaunchKernelEx(&cfg, sum_kernel<bf16>, partial, parts, cols,
+                                                  static_cast<bf16*>(dw), static_cast<bf16*>(db));
+        if (e != cudaSuccess) return GQ_ERR_CUDA;
+    }
+    return gqh::launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gq_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (!size_ok(rows, cols)) return 0;
+    if (rows == 0) return 16;
+    return static_cast<size_t>(rows < kMostParts ? rows : kMostParts) * 2 *
+           static_cast<size_t>(cols) * sizeof(float);
+}
+
+gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t cols, int64_t lddy,
+                                const void *weight, int wdtype, const float *rstd,
+                                const int8_t *codes, const uint8_t *exps, const void *x,
+                                int64_t ldx, const float *mean, void *dx, int64_t lddx,
+                                void *dweight, void *dbias, int gdtype, void *ws, size_t ws_bytes,
+                                void *stream) {
+    if (!in_type(dtype) || !in_type(wdtype) || !in_type(gdtype) || !size_ok(rows, cols))
+        return GQ_ERR_INVALID;
+    if (!matrix_ok(dy, dtype, rows, cols, lddy) || !matrix_ok(dx, dtype, rows, cols, lddx))
+        return GQ_ERR_INVALID;
+    if (!vector_ok(weight, wdtype) || !vector_ok(dweight, gdtype) || !vector_ok(dbias, gdtype))
+        return GQ_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // sums over no rows
+        const size_t n = static_cast<size_t>(cols) * elt_bytes(gdtype);
+        if (dweight && cudaMemsetAsync(dweight, 0, n, st) != cudaSuccess) return GQ_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, n, st) != cudaSuccess) return GQ_ERR_CUDA;
+        return GQ_OK;
+    }
+    if (!rstd || !mult(rstd, 4)) return GQ_ERR_INVALID;
+    // exactly one source of the normalised rows
+    const bool from_codes = codes || exps;
+    if (from_codes == (x != nullptr)) return GQ_ERR_INVALID;
+    if (from_codes && !saved_ok(codes, exps)) return GQ_ERR_INVALID;
+    if (!from_codes && (!mean || !mult(mean, 4) || !matrix_ok(x, dtype, rows, cols, ldx)))
+        return GQ_ERR_INVALID;
+    if (!ws || !mult(ws, 16) || ws_bytes < gq_layernorm_workspace_bytes(rows, cols))
+        return GQ_ERR_WORKSPACE;
+    const bool vec = row_align(dy, dtype, rows, lddy) && row_align(dx, dtype, rows, lddx) &&
+                     mult(weight, 16) && (from_codes || row_align(x, dtype, rows, ldx));
+    const Shape s = shape_of(rows, cols);
+    auto run = [&](auto elt) {
+        using T = decltype(elt);
+        const BackwardCall<T> a{static_cast<const T*>(dy), lddy, s, weight, wdtype == GQ_F32, rstd,
+                                Source<T>{codes, exps, static_cast<const T*>(x), ldx, mean},
+                                static_cast<T*>(dx), lddx, static_cast<float*>(ws), st};
+        return from_codes ? backward_any<T, true>(a, dweight, dbias, gdtype, vec)
+                          : backward_any<T, false>(a, dweight, dbias, gdtype, vec);
+    };
+    return dtype == GQ_F32 ? run(float()) : run(bf16());
+}
+
+}  // extern "C"
