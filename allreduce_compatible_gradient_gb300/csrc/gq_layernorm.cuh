@@ -18,7 +18,8 @@ namespace gqa {
 struct Affine {
     const void* w;
     const void* b;
-    int wide;  // fp32
+    int wide;     // fp32
+    int aligned;  // to 16 bytes
 };
 template <int V>
 __device__ __forceinline__ void vec_of(const void* p, int wide, float none, int64_t c,
@@ -116,11 +117,10 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* mine, int wr, in
 constexpr int kSlots = 32;  // per set and value: 8 groups x 4 slots, or 1 group of up to 16 warps
 
 // 8 entries of a per-column vector, 0 behind the last column.
-template <bool ALIGNED>
-__device__ __forceinline__ void vec8(const void* p, int wide, float none, int64_t c, int64_t cols,
-                                     F2 (&v)[4]) {
+__device__ __forceinline__ void vec8(const void* p, int wide, int aligned, float none, int64_t c,
+                                     int64_t cols, F2 (&v)[4]) {
     float t[8];
-    if constexpr (ALIGNED) {
+    if (aligned) {
         vec_of<8>(p, wide, none, c, cols, t);
     } else {
 #pragma unroll

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         float wv[V];
-        vec_of<V>(w, wide, 1.0f, k * step + t * V, s.cols, wv);
+        vec_of<V>(w, wide & 1, 1.0f, k * step + t * V, s.cols, wv);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             g[k][i] *= wv[i];
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(512)
         float a[V], b[V], wv[V];
         load<T, V, 16>(dyr, col, s.cols, a);
         hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
-        vec_of<V>(w, wide, 1.0f, col, s.cols, wv);
+        vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             a[i] *= wv[i];
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(512)
         float a[V], b[V], wv[V];
         load<T, V, 16>(dyr, col, s.cols, a);
         hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
-        vec_of<V>(w, wide, 1.0f, col, s.cols, wv);
+        vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
 #pragma unroll
         for (int i = 0; i < V; ++i) a[i] = (a[i] * wv[i] - fmaf(b[i], c2, c1)) * rstd;
         store<T, V, 16>(dxr, col, s.cols, a);
@@ -159,6 +159,10 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
+// Slots of a block's ring: 2 for rows of fp32 that take 512 threads, whose 4 would pass the shared memory.
+template <typename T, bool ALIGNED, int MOST>
+constexpr int slots_of = sizeof(T) == 4 && MOST == 512 ? 2 : Ring<T, ALIGNED>::kSlots;
+
 // The block's rows' sums of dy xh and dy go to partial[block][0 and 1][cols].
 template <typename T, bool ALIGNED, int VPT, bool CODES, int W, int MOST>
 __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
         in[k] = c < a.cols;
         col[k] = in[k] ? c : 0u;
         left[k] = static_cast<int>(a.cols - col[k]);
-        vec8<ALIGNED>(w, wide, 1.0f, c, a.cols, wv[k]);
+        vec8(w, wide & 1, wide >> 1, 1.0f, c, a.cols, wv[k]);
         if (!in[k]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) wv[k][i] = f2(0.0f);
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
     // a slot: dy's planes of 16 bytes per thread, then x's or those of 8 and 4 for the checkpoint (4
     // exponent bytes, of which one is this thread's)
     using R = Ring<T, ALIGNED>;
-    constexpr int P = R::kPieces, D = R::kSlots;
+    constexpr int P = R::kPieces, D = slots_of<T, ALIGNED, MOST>;
     const uint32_t n = blockDim.x, tid = threadIdx.x, plane = n * 16;
     const uint32_t second = plane * VPT * P, third = second + VPT * n * 8;
     const uint32_t slot_bytes = CODES ? third + VPT * n * 4 : 2 * second;
@@ -337,7 +341,7 @@ struct BackwardCall {
     int64_t lddy;
     Shape s;
     const void* w;
-    int wide;
+    int wide;  // 1: fp32, 2: 16-byte aligned
     const float* rstd;
     Source<T> src;
     T* dx;
@@ -350,22 +354,18 @@ template <typename T, bool ALIGNED, bool CODES> struct BackwardHeld {
     const BackwardCall<T>& a;
     const Held& h;
     template <int VPT, int W, int MOST> int operator()() const {
-        if constexpr (MOST == 512 && sizeof(T) == 4) {
-            return 0;  // not reached: such rows take the long form
-        } else {
-            using R = Ring<T, ALIGNED>;
-            // (also room for 2 x cols sums: 56 bytes per thread and piece at least)
-            const size_t smem = static_cast<size_t>(R::kSlots) * h.threads * VPT *
-                                    (CODES ? 16 * R::kPieces + 12 : 32 * R::kPieces) +
-                                (ALIGNED ? 0 : h.threads / 32 * kSquare * sizeof(float));
-            auto k = backward_rows<T, ALIGNED, VPT, CODES, W, MOST>;
-            int grid = wave(resident_blocks(k, h.threads, smem), (a.s.rows + h.groups - 1) / h.groups);
-            if (grid > kMostParts) grid = kMostParts;
-            const HeldArgs ha = held_args(h, grid, a.s, a.lddy * sizeof(T), a.src.ldx * sizeof(T),
-                                          a.lddx * sizeof(T));
-            k<<<grid, h.threads, smem, a.st>>>(a.dy, ha, a.w, a.wide, a.rstd, a.src, a.dx, a.partial);
-            return grid;
-        }
+        using R = Ring<T, ALIGNED>;
+        // (also room for 2 x cols sums: 56 bytes per thread and piece at least)
+        const size_t smem = static_cast<size_t>(slots_of<T, ALIGNED, MOST>) * h.threads * VPT *
+                                (CODES ? 16 * R::kPieces + 12 : 32 * R::kPieces) +
+                            (ALIGNED ? 0 : h.threads / 32 * kSquare * sizeof(float));
+        auto k = backward_rows<T, ALIGNED, VPT, CODES, W, MOST>;
+        int grid = wave(resident_blocks(k, h.threads, smem), (a.s.rows + h.groups - 1) / h.groups);
+        if (grid > kMostParts) grid = kMostParts;
+        const HeldArgs ha = held_args(h, grid, a.s, a.lddy * sizeof(T), a.src.ldx * sizeof(T),
+                                      a.lddx * sizeof(T));
+        k<<<grid, h.threads, smem, a.st>>>(a.dy, ha, a.w, a.wide, a.rstd, a.src, a.dx, a.partial);
+        return grid;
     }
 };
 template <typename T, int V, int VPT, bool CODES> void backward_generic(const BackwardCall<T>& a) {
@@ -380,15 +380,14 @@ gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype,
     int64_t ld = a.lddy > a.lddx ? a.lddy : a.lddx;
     if (a.src.ldx > ld) ld = a.src.ldx;
     int parts;
-    // (the ring of fp32 rows of more than 4,096 columns would pass the shared memory)
-    if (held_ok(cols, ld * sizeof(T)) && (sizeof(T) == 2 || cols <= kHeldCols / 2)) {
+    if (held_ok(cols, ld * sizeof(T))) {
         const Held h = held_for(a.s.rows, cols);
         parts = vec && cols % 8 == 0 ? held_switch(h, BackwardHeld<T, true, CODES>{a, h})
                                      : held_switch(h, BackwardHeld<T, false, CODES>{a, h});
     } else {
         if (vec) backward_generic<T, 8, 2, CODES>(a);
         else backward_generic<T, 1, 8, CODES>(a);
-        parts = static_cast<int>((a.s.rows + 63) / 64 < 64 ? (a.s.rows + 63) / 64 : 64);
+        parts = static_cast<int>((a.s.rows + 7) / 8 < 64 ? (a.s.rows + 7) / 8 : 64);
         const dim3 grid(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(parts));
         if (dw || db)
             columns_kernel<T, CODES><<<grid, 256, 0, a.st>>>(a.dy, a.lddy, a.s, a.rstd, a.src, a.partial);
@@ -458,7 +457,8 @@ gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t
     const Shape s = shape_of(rows, cols);
     auto run = [&](auto elt) {
         using T = decltype(elt);
-        const BackwardCall<T> a{static_cast<const T*>(dy), lddy, s, weight, wdtype == GQ_F32, rstd,
+        const BackwardCall<T> a{static_cast<const T*>(dy), lddy, s, weight,
+                                (wdtype == GQ_F32) + 2 * mult(weight, 16), rstd,
                                 Source<T>{codes, exps, static_cast<const T*>(x), ldx, mean},
                                 static_cast<T*>(dx), lddx, static_cast<float*>(ws), st};
         return from_codes ? backward_any<T, true>(a, dweight, dbias, gdtype, vec)

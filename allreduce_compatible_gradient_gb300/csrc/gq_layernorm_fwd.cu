@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
         for (int i = 0; i < (ALIGNED ? 1 : 4); ++i)
             mask[k][i] = f2(c + 2 * i < a.cols ? 1.0f : 0.0f,
                             c + 2 * i + (ALIGNED ? 0 : 1) < a.cols ? 1.0f : 0.0f);
-        vec8<ALIGNED>(af.w, af.wide, 1.0f, c, a.cols, w[k]);
-        vec8<ALIGNED>(af.b, af.wide, 0.0f, c, a.cols, b[k]);
+        vec8(af.w, af.wide, af.aligned, 1.0f, c, a.cols, w[k]);
+        vec8(af.b, af.wide, af.aligned, 0.0f, c, a.cols, b[k]);
         if constexpr (RND == 1)
             pg[k] = gq::philox_group(c >> 3, rng.step_lo, rng.step_hi, rng.rk);
     }
@@ -279,10 +279,9 @@ gq_status gq_layernorm_forward(const void *x, int dtype, int64_t rows, int64_t c
     if (rows == 0) return GQ_OK;
     if (!mean || !rstd || !mult(mean, 4) || !mult(rstd, 4)) return GQ_ERR_INVALID;
     if ((codes || exps) && !saved_ok(codes, exps)) return GQ_ERR_INVALID;
-    const bool vec = row_align(x, dtype, rows, ldx) && row_align(y, dtype, rows, ldy) &&
-                     mult(weight, 16) && mult(bias, 16);
+    const Affine af{weight, bias, wdtype == GQ_F32, mult(weight, 16) && mult(bias, 16)};
+    const bool vec = row_align(x, dtype, rows, ldx) && row_align(y, dtype, rows, ldy) && af.aligned;
     const Shape s = shape_of(rows, cols);
-    const Affine af{weight, bias, wdtype == GQ_F32};
     const Rng rng = make_rng(seed, step);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto run = [&](auto elt) {

@@ -646,33 +646,40 @@ __global__ void __launch_bounds__(1024)
     const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32 + y;
     if constexpr (PACK) {
         if (c < pitch) {
-#pragma unroll 2
-            for (int64_t t = t0; t < tokens; t += stride) {
-                float v[V];
-                if (t < rows) {
-                    load<T, V, 16>(dy + t * ld, c, outs, v);
-                } else {
+            constexpr int B = V == 1 ? 8 : 2;  // rows whose loads are issued together
+            for (int64_t t = t0; t < tokens; t += B * stride) {
+                float v[B][V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-                }
-                uint32_t top[V];
+                for (int k = 0; k < B; ++k) {
+                    if (t + k * stride < rows) {
+                        load<T, V, 16>(dy + (t + k * stride) * ld, c, outs, v[k]);
+                    } else {
 #pragma unroll
-                for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        if (p == 0) s[i] += v[i];
-                        const uint32_t bits = __float_as_uint(v[i]);
-                        top[i] = (bits & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FFF0000u : bits & 0xFFFF0000u;
-                        const bool special = (bits & 0x7F800000u) == 0x7F800000u;
-                        v[i] = special ? 0.0f : v[i] - __uint_as_float(top[i]);
+                        for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
                     }
-                    bf16* to = out + (p * tokens + t) * pitch + c;
-                    if constexpr (V == 8)
-                        *reinterpret_cast<uint4*>(to) =
-                            make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3],
-                                       top[4] >> 16 | top[5], top[6] >> 16 | top[7]);
-                    else
-                        *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(top[0] >> 16);
+                }
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    if (t + k * stride >= tokens) break;
+                    uint32_t top[V];
+#pragma unroll
+                    for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            if (p == 0) s[i] += v[k][i];
+                            const uint32_t bits = __float_as_uint(v[k][i]);
+                            top[i] = (bits & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FFF0000u : bits & 0xFFFF0000u;
+                            const bool special = (bits & 0x7F800000u) == 0x7F800000u;
+                            v[k][i] = special ? 0.0f : v[k][i] - __uint_as_float(top[i]);
+                        }
+                        bf16* to = out + (p * tokens + t + k * stride) * pitch + c;
+                        if constexpr (V == 8)
+                            *reinterpret_cast<uint4*>(to) =
+                                make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3],
+                                           top[4] >> 16 | top[5], top[6] >> 16 | top[7]);
+                        else
+                            *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(top[0] >> 16);
+                    }
                 }
             }
         }
@@ -830,9 +837,10 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.units = p.tiles_m * p.tiles_n * p.ksteps;
     p.pitch = (outs + 7) / 8 * 8;
     // the pass over dy: up to 512 rows in one go if there are only sums to take, else one wave of blocks
-    // (one per SM)
+    // (one per SM, two where dy is packed)
     const int64_t groups = row_align(dy, dtype, rows, ld) ? (outs + 255) / 256 : (outs + 31) / 32;
-    int64_t sh = rows <= 512 && !p.pack ? 1 : groups < sms ? sms / groups : 1;
+    const int64_t wave = p.pack ? 2 * sms : sms;
+    int64_t sh = rows <= 512 && !p.pack ? 1 : groups < wave ? wave / groups : 1;
     const int64_t rows_each = p.pack ? 32 : 128;
     if (sh > (rows + rows_each - 1) / rows_each) sh = (rows + rows_each - 1) / rows_each;
     p.bias_shares = static_cast<int>(sh);
