@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kTok = 64;              // tokens per step
 constexpr int kChain = 96;            // steps of one accumulation
+constexpr int kEarly = 2;             // steps widened for the next chain before one's sums are stored
 constexpr int kTeams = 2;             // teams of widening warps that take turns at the steps
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
 
@@ -55,6 +56,7 @@ template <int CG_, int MH_, int BN_, int WARPS> struct Tile {
     static constexpr int kABytes = kOuts * kTok * 2;
     static constexpr int kBBytes = kOwn * kTok * 2;
     static constexpr int kStages = 192 * 1024 / (kABytes + kBBytes);
+    static_assert(kEarly <= kStages, "a chain's ends are in shared memory at once");
     static constexpr int kCols = MH * BN;             // TMEM columns: a power of two >= 32
     static constexpr int kSmem = kStages * (kABytes + kBBytes) + 1024;
 };
@@ -74,8 +76,9 @@ struct WArgs {
     int64_t ktok;         // tokens of one part, rounded up to whole steps, in steps
     int ksteps;           // steps of a tile: parts * ktok
     int tiles_m, tiles_n;
-    int64_t units;        // tiles * ksteps, in
-    int64_t base;         // shares of base steps, one more in the first `rest`
+    int shares, own;      // blocks or pairs at work; whole tiles that each has to itself
+    int64_t units;        // steps of the remaining tiles, in
+    int64_t base;         // pieces of base steps, one more in the first `rest` shares
     int rest;
     int fast;             // whole 32-byte pieces of dw, and of scale and shift, are aligned
 };
@@ -200,8 +203,9 @@ __device__ __forceinline__ uint32_t widen2(uint32_t p, __nv_bfloat162 s) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The contiguous steps of a share (the first `rest` shares have one more), and a place in them: a tile,
-// and a step of that tile.  The place moves on by counting; a 64-bit division per step and thread had
+// A place in a share's steps: a tile, and a step of that tile.  First come `own` whole tiles (share,
+// share + shares, ...), then a contiguous piece of the remaining tiles' steps (of the first `rest`
+// shares one step longer).  The place moves on by counting; a 64-bit division per step and thread had
 // cost a third of the issue slots, and even one per thread is felt by a call of a few steps.
 __device__ __forceinline__ int64_t share_begin(const WArgs& a, int share) {
     return a.base * share + min(share, a.rest);
@@ -209,8 +213,15 @@ __device__ __forceinline__ int64_t share_begin(const WArgs& a, int share) {
 struct At {
     int left;  // steps of the share from here on
     int tile, k;
+    int own;   // whole tiles from this one on
     __device__ __forceinline__ At(const WArgs& a, int share)
-        : left(static_cast<int>(a.base) + (share < a.rest ? 1 : 0)) {
+        : left(a.own * a.ksteps + static_cast<int>(a.base) + (share < a.rest ? 1 : 0)), own(a.own) {
+        tile = share;
+        k = 0;
+        if (own == 0) split(a, share);
+    }
+    // to the piece of the tiles that several shares work on
+    __device__ __forceinline__ void split(const WArgs& a, int share) {
         const int64_t u = share_begin(a, share);
         if (a.units <= INT32_MAX) {
             const uint32_t v = static_cast<uint32_t>(u);
@@ -220,26 +231,32 @@ struct At {
             tile = static_cast<int>(u / a.ksteps);
             k = static_cast<int>(u % a.ksteps);
         }
+        tile += a.own * a.shares;
     }
-    __device__ __forceinline__ void next(int ksteps) {
-        --left;
-        if (++k == ksteps) {
-            k = 0;
-            ++tile;
-        }
-    }
-    // steps of the tile at hand that are in the share
-    __device__ __forceinline__ int segment(int ksteps) const { return min(left, ksteps - k); }
     // `steps` more, which stay in the tile or end it
-    __device__ __forceinline__ void skip(int steps, int ksteps) {
+    __device__ __forceinline__ void skip(const WArgs& a, int steps) {
         left -= steps;
         k += steps;
-        if (k == ksteps) {
-            k = 0;
-            ++tile;
-        }
+        if (k < a.ksteps) return;
+        k = 0;
+        if (own == 0) ++tile;
+        else if (--own > 0) tile += a.shares;
+        else split(a, tile - (a.own - 1) * a.shares);
     }
+    __device__ __forceinline__ void next(const WArgs& a) { skip(a, 1); }
+    // steps of the tile at hand that are in the share
+    __device__ __forceinline__ int segment(const WArgs& a) const { return min(left, a.ksteps - k); }
 };
+
+// Steps of the next chain of a segment with `left` steps.  The first chains of neighbouring shares are of
+// different lengths, where the number of chains leaves the room, so that not all of them store their
+// sums at the same time.
+__device__ __forceinline__ int chain_steps(int left, bool first, int share) {
+    if (left <= kChain) return left;
+    if (!first) return kChain;
+    const int room = (left + kChain - 1) / kChain * kChain - left;
+    return kChain - room * (share & 7) / 8;
+}
 
 // 8 columns of a row of dw from fp32 sums, element by element: the last columns, and rows that are
 // not aligned.  Kept out of the kernels' straight path, whose instructions a short call fetches cold.
@@ -317,7 +334,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     constexpr int CG = C::CG, MH = C::MH, BN = C::BN, S = C::kStages;
     extern __shared__ uint8_t raw[];
     // full: everything of a step is there (in the pair's first block); full_a: the second block's dy
-    __shared__ alignas(8) uint64_t full[S], full_a[S], empty[S], acc_full, acc_empty, drain;
+    __shared__ alignas(8) uint64_t full[S], full_a[S], empty[S], acc_full[MH], acc_empty[MH], drain;
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -332,8 +349,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             gq::mbar_init(gq::smem_u32(&full_a[s]), 1u);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
-        gq::mbar_init(gq::smem_u32(&acc_full), 1u);
-        gq::mbar_init(gq::smem_u32(&acc_empty), CG * C::kConv);
+        for (int h = 0; h < MH; ++h) {
+            gq::mbar_init(gq::smem_u32(&acc_full[h]), 1u);
+            gq::mbar_init(gq::smem_u32(&acc_empty[h]), CG * C::kConv);
+        }
         gq::mbar_init(gq::smem_u32(&drain), 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -349,13 +368,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (lane == 0) {
             uint32_t n = 0;
             bool ok = true;
-            for (At at(a, share); at.left > 0 && ok; at.next(a.ksteps), ++n) {
+            for (At at(a, share); at.left > 0 && ok; at.next(a), ++n) {
                 const int s = n % S;
                 if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                 if (!ok) break;
                 const uint32_t bar = gq::smem_u32(rank == 0 ? &full[s] : &full_a[s]);
                 gq::mbar_arrive_expect_tx(bar, C::kABytes);
-                const int o0 = (at.tile % a.tiles_m) * C::kRows + static_cast<int>(rank) * C::kOuts;
+                const int o0 = (at.tile / a.tiles_n) * C::kRows + static_cast<int>(rank) * C::kOuts;
 #pragma unroll
                 for (int c = 0; c < 2 * MH; ++c)
                     tma_load(a_stage(s) + c * kChunk, &dy_map, o0 + 64 * c, at.k * kTok, bar);
@@ -367,29 +386,67 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             uint32_t n = 0, seg = 0;
-            bool ok = true;
-            for (At at(a, share); at.left > 0 && ok; ++seg) {
-                const int steps = min(at.segment(a.ksteps), kChain);
-                if (seg > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (seg - 1) & 1);
+            bool ok = true, first = true;
+            auto wait_full = [&](uint32_t m) {
+                if (ok) ok = gq::mbar_wait(gq::smem_u32(&full[m % S]), (m / S) & 1);
                 fence_after();
-                for (int z = 0; z < steps && ok; ++z, ++n) {
-                    const int s = n % S;
-                    ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
-                    if (!ok) break;
-                    fence_after();
+            };
+            auto issue = [&](uint32_t m, int h, bool add) {  // step m on accumulator h
+                const int s = m % S;
 #pragma unroll
-                    for (int kk = 0; kk < kTok / 16; ++kk) {
-                        const uint64_t b = operand(b_stage(s) + kk * 2048);
-#pragma unroll
-                        for (int h = 0; h < MH; ++h)
-                            mma_bf16<CG>(tmem + h * BN,
-                                         operand(a_stage(s) + h * 2 * kChunk + kk * 2048), b,
-                                         Instruction<CG, BN>::value, z > 0 || kk > 0);
-                    }
-                    mma_commit<CG>(gq::smem_u32(&empty[s]));
-                    at.next(a.ksteps);
+                for (int kk = 0; kk < kTok / 16; ++kk)
+                    mma_bf16<CG>(tmem + h * BN, operand(a_stage(s) + h * 2 * kChunk + kk * 2048),
+                                 operand(b_stage(s) + kk * 2048), Instruction<CG, BN>::value,
+                                 add || kk > 0);
+            };
+            auto wait_empty = [&](int h) {
+                if (seg > 0 && ok) ok = gq::mbar_wait(gq::smem_u32(&acc_empty[h]), (seg - 1) & 1);
+                fence_after();
+            };
+            for (At at(a, share); at.left > 0 && ok; ++seg) {
+                const int left = at.segment(a), steps = chain_steps(left, first, share);
+                at.skip(a, steps);
+                first = steps == left;
+                // With two accumulators a chain's first and last kEarly steps run on the first one, then
+                // on the second: each works on while the other's sums are stored.
+                const int head = MH > 1 ? min(steps, kEarly) : 0, tail = MH > 1 ? min(steps - head, kEarly) : 0;
+                const uint32_t from = n, back = n + steps - tail, end = n + steps;
+                wait_empty(0);
+                for (; n < from + head && ok; ++n) {
+                    wait_full(n);
+                    if (ok) issue(n, 0, n > from);
                 }
-                if (ok) mma_commit<CG>(gq::smem_u32(&acc_full));
+                if constexpr (MH > 1) {
+                    if (tail == 0 && ok) mma_commit<CG>(gq::smem_u32(&acc_full[0]));
+                    wait_empty(1);
+                    if (ok) {
+                        for (n = from; n < from + head; ++n) {
+                            issue(n, 1, n > from);
+                            mma_commit<CG>(gq::smem_u32(&empty[n % S]));
+                        }
+                    }
+                }
+                for (; n < back && ok; ++n) {
+                    wait_full(n);
+                    if (!ok) break;
+#pragma unroll
+                    for (int h = 0; h < MH; ++h) issue(n, h, n > from);
+                    mma_commit<CG>(gq::smem_u32(&empty[n % S]));
+                }
+                for (; n < end && ok; ++n) {
+                    wait_full(n);
+                    if (ok) issue(n, 0, true);
+                }
+                if (ok && (MH == 1 || tail > 0)) mma_commit<CG>(gq::smem_u32(&acc_full[0]));
+                if constexpr (MH > 1) {
+                    if (ok) {
+                        for (uint32_t m = back; m < end; ++m) {
+                            issue(m, 1, true);
+                            mma_commit<CG>(gq::smem_u32(&empty[m % S]));
+                        }
+                        mma_commit<CG>(gq::smem_u32(&acc_full[1]));
+                    }
+                }
             }
             if (!ok) {  // let what was issued finish before TMEM is given back
                 mma_commit<CG>(gq::smem_u32(&drain));
@@ -398,7 +455,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         } else if (lane == 0) {  // the second block: tells the first that its dy has arrived
             uint32_t n = 0;
             bool ok = true;
-            for (At at(a, share); at.left > 0 && ok; at.next(a.ksteps), ++n) {
+            for (At at(a, share); at.left > 0 && ok; at.next(a), ++n) {
                 ok = gq::mbar_wait(gq::smem_u32(&full_a[n % S]), (n / S) & 1);
                 if (ok) arrive_first<CG>(gq::smem_u32(&full[n % S]));
             }
@@ -422,7 +479,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         bool in_cols = false;
         const int rows_left = static_cast<int>(min(a.rows - tok, int64_t(1) << 30));
         auto place = [&]() {
-            const int64_t i = static_cast<int64_t>(ahead.tile / a.tiles_m) * BN + rank * C::kOwn + col;
+            const int64_t i = static_cast<int64_t>(ahead.tile % a.tiles_n) * BN + rank * C::kOwn + col;
             const int64_t t = static_cast<int64_t>(part) * kTok + tok;
             in_cols = i < a.pitch;
             pc = a.codes + t * a.pitch + i;
@@ -437,10 +494,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 pc += steps * (kTok * a.pitch);
                 pe += steps * (kTok * a.epitch);
             } else {  // a part of dy, or a tile, begins
-                for (int j = 0; j < steps; ++j) {
-                    ahead.next(a.ksteps);
-                    if (++part == a.ktok) part = 0;
-                }
+                for (int j = 0; j < steps; ++j) ahead.next(a);
+                part = ahead.k % static_cast<int>(a.ktok);
                 place();
             }
         };
@@ -458,114 +513,121 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         place();
         if (team > 0) advance(team);
         if (ahead.left > 0) fetch();
-        uint32_t n = 0, seg = 0;
+        uint32_t n = team, end = 0, seg = 0;
         bool ok = true;
         At at(a, share);
+        const uint32_t total = at.left;
+        auto widen = [&](uint32_t to) {  // the team's steps below `to`
+            for (; n < to; n += kTeams) {
+                const int s = n % S;
+                uint4 cw[kPer];
+                uint32_t ce[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
+                if (ahead.left > 0) fetch();
+                if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) continue;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int t = tok + j * kTokStep, c = col / 16;  // token, 16-column piece
+                    const uint32_t sc = ce[j] << 7 | ce[j] << 23;
+                    const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
+                    const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        o[2 * m] = widen2(__byte_perm(in[m], 0x43434343u, 0x4140), sv);
+                        o[2 * m + 1] = widen2(__byte_perm(in[m], 0x43434343u, 0x4342), sv);
+                    }
+                    // 16-byte unit v of row t of a 64-column chunk sits at unit v ^ (t mod 8)
+                    const uint32_t row = b_stage(s) + (c >> 2) * kChunk + t * 128;
+                    const uint32_t v0 = (2 * (c & 3)) ^ (t & 7);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + v0 * 16),
+                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (v0 ^ 1) * 16),
+                                 "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_first<CG>(gq::smem_u32(&full[s]));
+            }
+        };
         while (at.left > 0) {
             const int tile = at.tile;
-            int left = at.segment(a.ksteps);
+            int left = at.segment(a);
             const bool whole = at.k == 0 && left == a.ksteps, from_first = at.k == 0;
             for (bool first = true; left > 0; first = false, ++seg) {  // the chains of the segment
-                const int steps = min(left, kChain);
+                const int steps = chain_steps(left, first, share);
                 left -= steps;
-                at.skip(steps, a.ksteps);
-                const uint32_t end = n + steps;
-                for (n += (team - n) % kTeams; n < end; n += kTeams) {
-                    const int s = n % S;
-                    uint4 cw[kPer];
-                    uint32_t ce[kPer];
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) { cw[j] = w[j]; ce[j] = e[j]; }
-                    if (ahead.left > 0) fetch();
-                    if (n >= S && ok) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) continue;
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const int t = tok + j * kTokStep, c = col / 16;  // token, 16-column piece
-                        const uint32_t sc = ce[j] << 7 | ce[j] << 23;
-                        const __nv_bfloat162 sv = *reinterpret_cast<const __nv_bfloat162*>(&sc);
-                        const uint32_t in[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            o[2 * m] = widen2(__byte_perm(in[m], 0x43434343u, 0x4140), sv);
-                            o[2 * m + 1] = widen2(__byte_perm(in[m], 0x43434343u, 0x4342), sv);
-                        }
-                        // 16-byte unit v of row t of a 64-column chunk sits at unit v ^ (t mod 8)
-                        const uint32_t row = b_stage(s) + (c >> 2) * kChunk + t * 128;
-                        const uint32_t v0 = (2 * (c & 3)) ^ (t & 7);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + v0 * 16),
-                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (v0 ^ 1) * 16),
-                                     "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) arrive_first<CG>(gq::smem_u32(&full[s]));
-                }
-                n = end;
+                at.skip(a, steps);
+                end += steps;
+                widen(end);
                 // the chain's sums: 4 warps take the 128 lanes of TMEM, the groups of 4 share the
                 // columns
                 const int quad = warp & 3, group = (warp - 2) >> 2;
-                constexpr int kGroups = C::kConv / 4, kShare = MH * BN / kGroups;
-                const int h = group * kShare / BN, c0 = group * kShare % BN;
-                const int r = static_cast<int>(rank) * C::kOuts + h * 128 + quad * 32 + lane;
-                const int64_t o = static_cast<int64_t>(tile % a.tiles_m) * C::kRows + r;
-                const int64_t i0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
+                constexpr int kShare = BN / (C::kConv / 4);
+                const int c0 = group * kShare;
+                const int64_t i0 = static_cast<int64_t>(tile % a.tiles_n) * BN;
                 float* part_tile = a.partial + (static_cast<int64_t>(blockIdx.x / CG) * 2 +
                                                 (from_first ? 1 : 0)) * (C::kRows * BN);
                 const bool last = whole && left == 0;
                 if (last && a.shift) gq::pdl_wait();  // db, if the sums of dy still run
-                float4 x[8];  // what the chains before left of the next 32 columns, on its way
-                auto before = [&](int c) {
-                    const float* p = part_tile + partial_at<BN>(r, c);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        x[k] = reinterpret_cast<const float4*>(p + 256 * (k >> 1))[k & 1];
-                };
-                if (!first) before(c0);
-                if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), seg & 1);
-                ok = __all_sync(kFull, ok);
-                fence_after();
 #pragma unroll 1
-                for (int c = c0; c < c0 + kShare; c += 32) {
-                    uint32_t acc[32];
-                    if (ok) {
-                        tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * BN + c, acc);
-                    } else {  // a wait gave up: the tile is marked, not left as it was
+                for (int h = 0; h < MH; ++h) {
+                    const int r = static_cast<int>(rank) * C::kOuts + h * 128 + quad * 32 + lane;
+                    const int64_t o = static_cast<int64_t>(tile / a.tiles_n) * C::kRows + r;
+                    float4 x[8];  // what the chains before left of the next 32 columns, on its way
+                    auto before = [&](int c) {
+                        const float* p = part_tile + partial_at<BN>(r, c);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) acc[k] = 0x7FFFFFFFu;
-                    }
-                    float v[32];
+                        for (int k = 0; k < 8; ++k)
+                            x[k] = reinterpret_cast<const float4*>(p + 256 * (k >> 1))[k & 1];
+                    };
+                    if (!first) before(c0);
+                    if (h == MH - 1) widen(min(end + kEarly, total));
+                    if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full[h]), seg & 1);
+                    ok = __all_sync(kFull, ok);
+                    fence_after();
+#pragma unroll 1
+                    for (int c = c0; c < c0 + kShare; c += 32) {
+                        uint32_t acc[32];
+                        if (ok) {
+                            tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * BN + c, acc);
+                        } else {  // a wait gave up: the tile is marked, not left as it was
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
-                    if (!first) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            v[4 * k] += x[k].x; v[4 * k + 1] += x[k].y;
-                            v[4 * k + 2] += x[k].z; v[4 * k + 3] += x[k].w;
+                            for (int k = 0; k < 32; ++k) acc[k] = 0x7FFFFFFFu;
                         }
-                        if (c + 32 < c0 + kShare) before(c + 32);
-                    }
-                    if (last) {
-                        finish(a, o, i0 + c, v);
-                    } else {
-                        float* p = part_tile + partial_at<BN>(r, c);
+                        float v[32];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t u[8];
+                        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(acc[k]);
+                        if (!first) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[8 * k + j]);
-                            st32<32>(p + 256 * k, u);
+                            for (int k = 0; k < 8; ++k) {
+                                v[4 * k] += x[k].x; v[4 * k + 1] += x[k].y;
+                                v[4 * k + 2] += x[k].z; v[4 * k + 3] += x[k].w;
+                            }
+                            if (c + 32 < c0 + kShare) before(c + 32);
+                        }
+                        if (last) {
+                            finish(a, o, i0 + c, v);
+                        } else {
+                            float* p = part_tile + partial_at<BN>(r, c);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t u[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[8 * k + j]);
+                                st32<32>(p + 256 * k, u);
+                            }
                         }
                     }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_first<CG>(gq::smem_u32(&acc_empty[h]));
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first<CG>(gq::smem_u32(&acc_empty));
             }
         }
     }
@@ -579,10 +641,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 }
 
 // Adds the partial tiles of every tile that more than one share has a part of, in the shares' order.
-// blockIdx.x = tile; thread = 8 columns of a row, 32 rows of the same columns per warp.
+// blockIdx.x = tile after the shares' own; thread = 8 columns of a row, 32 rows of the same columns per warp.
 template <typename C> __global__ void __launch_bounds__(256) join_kernel(const WArgs a) {
     constexpr int BN = C::BN;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * a.ksteps, last = first + a.ksteps - 1;
+    const int tile = a.own * a.shares + static_cast<int>(blockIdx.x);
     __shared__ int owners[2];
     if (threadIdx.x < 2) {  // the share that holds the tile's first step, and its last
         const int64_t u = threadIdx.x ? last : first;
@@ -621,8 +684,8 @@ template <typename C> __global__ void __launch_bounds__(256) join_kernel(const W
                 }
             }
         }
-        finish(a, static_cast<int64_t>(blockIdx.x % a.tiles_m) * C::kRows + r,
-               static_cast<int64_t>(blockIdx.x / a.tiles_m) * BN + c, v);
+        finish(a, static_cast<int64_t>(tile / a.tiles_n) * C::kRows + r,
+               static_cast<int64_t>(tile % a.tiles_n) * BN + c, v);
     }
 }
 
@@ -790,7 +853,7 @@ struct WPlan {
     bool big;            // pairs of blocks on 512 x 256 tiles, else 128 x 128
     bool pack;
     int parts;           // bf16 parts of dy
-    int64_t ktok, ksteps, tiles_m, tiles_n, units, pitch;
+    int64_t ktok, ksteps, tiles_m, tiles_n, pitch;
     int shares, bias_shares;  // of the steps; of the rows in the bias sums
     size_t pack_off, bias_off, db_off, sums_off, bytes;
     int64_t sums_ld;     // of the fp32 sums for a dw with unaligned rows (0: none)
@@ -834,7 +897,6 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     const int rows_of = p.big ? Large::kRows : Small::kRows, cols_of = p.big ? Large::BN : Small::BN;
     p.tiles_m = (outs + rows_of - 1) / rows_of;
     p.tiles_n = (cols + cols_of - 1) / cols_of;
-    p.units = p.tiles_m * p.tiles_n * p.ksteps;
     p.pitch = (outs + 7) / 8 * 8;
     // the pass over dy: up to 512 rows in one go if there are only sums to take, else one wave of blocks
     // (one per SM, two where dy is packed)
@@ -868,11 +930,11 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
 // early: the launch before this one on the stream is of the sums of dy, which the kernel waits for only
 // where it reads them; what came before those is done when it starts.
 template <typename C>
-gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool early, cudaStream_t st) {
+gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, bool early, cudaStream_t st) {
     auto k = wgrad_kernel<C>;
     gqh::blocks_per_sm(k, C::kSmem, C::kThreads);  // raises the shared-memory limit once
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(shares * C::CG));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.shares * C::CG));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
@@ -885,9 +947,8 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, int shares, bool 
     cfg.attrs = attr;
     cfg.numAttrs = C::CG > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, k, map, a) != cudaSuccess) return GQ_ERR_CUDA;
-    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
-    if (tiles % shares != 0) {  // otherwise every share is a whole number of tiles
-        const dim3 grid(static_cast<unsigned>(tiles), C::CG == 2 ? 32 : 8);
+    if (a.units > 0) {  // tiles that several shares work on
+        const dim3 grid(static_cast<unsigned>(a.units / a.ksteps), C::CG == 2 ? 32 : 8);
         join_kernel<C><<<grid, 256, 0, st>>>(a);
     }
     return gqh::launch_status();
@@ -993,8 +1054,11 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     a.partial = reinterpret_cast<float*>(w);
     a.ktok = p.ktok; a.ksteps = static_cast<int>(p.ksteps);
     a.tiles_m = static_cast<int>(p.tiles_m); a.tiles_n = static_cast<int>(p.tiles_n);
-    a.units = p.units;
-    a.base = p.units / p.shares; a.rest = static_cast<int>(p.units % p.shares);
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    a.shares = p.shares;
+    a.own = static_cast<int>(tiles / p.shares);
+    a.units = tiles % p.shares * p.ksteps;
+    a.base = a.units / p.shares; a.rest = static_cast<int>(a.units % p.shares);
     const WArgs wanted = a;
     float* raw = p.sums_ld && !a.fast ? reinterpret_cast<float*>(w + p.sums_off) : nullptr;
     if (raw) {  // aligned fp32 sums first, padding columns among them (their codes are 0)
@@ -1005,8 +1069,8 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     }
     // a packed dy has to be there before the main kernel starts; sums alone only where it reads them
     const bool early = sums && !p.pack;
-    const gq_status r = p.big ? launch_wgrad<Large>(map, a, p.shares, early, st)
-                              : launch_wgrad<Small>(map, a, p.shares, early, st);
+    const gq_status r = p.big ? launch_wgrad<Large>(map, a, early, st)
+                              : launch_wgrad<Small>(map, a, early, st);
     if (r != GQ_OK || !raw) return r;
     const dim3 grid(static_cast<unsigned>((cols + 255) / 256),
                     static_cast<unsigned>(outs < 16384 ? (outs + 3) / 4 : 4096));
