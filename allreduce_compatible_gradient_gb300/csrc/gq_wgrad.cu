@@ -750,22 +750,24 @@ __global__ void __launch_bounds__(1024)
         const T* p = dy + t0 * ld;
         int64_t left = rows - t0;
         if constexpr (V == 8) {
-            // (the test for the last columns is outside, so that the loads are issued together)
+            // (the test for the last columns is outside, and rows that are not there are read as the
+            // first and left out, so that the loads are issued together)
             if (c + V <= outs) {
-                for (; left > 3 * stride; left -= 4 * stride, p += 4 * stride * ld) {
-                    Raw8<T> r[4];
+                constexpr int B = 8;
+                for (; left > 0; left -= B * stride, p += B * stride * ld) {
+                    Raw8<T> r[B];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = raw8(p + k * stride * ld + c, 0, 8);
+                    for (int k = 0; k < B; ++k) r[k] = raw8(p + (left > k * stride ? k * stride * ld : 0) + c, 0, 8);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < B; ++k) {
                         F2 v[4];
                         pairs(r[k], v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float x, y2;
                             split(v[i], x, y2);
-                            s[2 * i] += x;
-                            s[2 * i + 1] += y2;
+                            s[2 * i] += left > k * stride ? x : 0.0f;
+                            s[2 * i + 1] += left > k * stride ? y2 : 0.0f;
                         }
                     }
                 }
