@@ -417,6 +417,37 @@ __device__ __forceinline__ Raw8<T> raw8(const T* p, int64_t c, int64_t cols) {
     }
     return r;
 }
+// 8 elements out of the words of the 16-byte granules that hold them: the first is m bytes behind the
+// first granule's start (0 where ALIGNED); `left` of them are wanted, the others read as 0.
+template <typename T, bool ALIGNED, int N>
+__device__ __forceinline__ Raw8<T> shifted(uint32_t (&r)[N], uint32_t m, int left) {
+    constexpr int W = 2 * sizeof(T);
+    if constexpr (!ALIGNED) {
+#pragma unroll
+        for (int i = 0; i < W + 2; ++i) r[i] = (m & 8u) ? r[i + 2] : r[i];
+#pragma unroll
+        for (int i = 0; i < W + 1; ++i) r[i] = (m & 4u) ? r[i + 1] : r[i];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], (m & 2u) * 8u);
+        }
+    }
+    if (left < 8) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                if (i >= left) r[i] = 0u;
+            } else {
+                if (2 * i >= left) r[i] = 0u;
+                else if (2 * i + 1 >= left) r[i] &= 0xFFFFu;
+            }
+        }
+    }
+    Raw8<T> w;
+#pragma unroll
+    for (int i = 0; i < W; ++i) w.w[i] = r[i];
+    return w;
+}
 template <typename T>
 __device__ __forceinline__ void pairs(const Raw8<T>& r, F2 (&v)[4]) {
 #pragma unroll

@@ -155,39 +155,14 @@ template <typename T, bool ALIGNED> struct Ring {
     }
     static __device__ __forceinline__ void read(const uint8_t* at, uint32_t plane, const T* p, int left,
                                                 F2 (&v)[4]) {
-        constexpr int W = 2 * sizeof(T);
         uint32_t r[4 * kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const uint4 a = *reinterpret_cast<const uint4*>(at + i * plane);
             r[4 * i] = a.x; r[4 * i + 1] = a.y; r[4 * i + 2] = a.z; r[4 * i + 3] = a.w;
         }
-        if constexpr (!ALIGNED) {
-            const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-#pragma unroll
-            for (int i = 0; i < W + 2; ++i) r[i] = (m & 8u) ? r[i + 2] : r[i];
-#pragma unroll
-            for (int i = 0; i < W + 1; ++i) r[i] = (m & 4u) ? r[i + 1] : r[i];
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int i = 0; i < W; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], (m & 2u) * 8u);
-            }
-            if (left < 8) {
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    if constexpr (sizeof(T) == 4) {
-                        if (i >= left) r[i] = 0u;
-                    } else {
-                        if (2 * i >= left) r[i] = 0u;
-                        else if (2 * i + 1 >= left) r[i] &= 0xFFFFu;
-                    }
-                }
-            }
-        }
-        Raw8<T> w;
-#pragma unroll
-        for (int i = 0; i < W; ++i) w.w[i] = r[i];
-        pairs(w, v);
+        const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+        pairs(shifted<T, ALIGNED>(r, m, ALIGNED ? 8 : left), v);
     }
 };
 

@@ -80,6 +80,7 @@ struct WArgs {
     int64_t units;        // steps of the remaining tiles, in
     int64_t base;         // pieces of base steps, one more in the first `rest` shares
     int rest;
+    int packed;           // dy is what pack_kernel wrote
     int fast;             // whole 32-byte pieces of dw, and of scale and shift, are aligned
 };
 
@@ -368,6 +369,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (lane == 0) {
             uint32_t n = 0;
             bool ok = true;
+            if (a.packed) gq::pdl_wait();  // dy is the launch before's work
             for (At at(a, share); at.left > 0 && ok; at.next(a), ++n) {
                 const int s = n % S;
                 if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
@@ -657,140 +659,166 @@ template <typename C> __global__ void __launch_bounds__(256) join_kernel(const W
     __syncthreads();
     const int b0 = owners[0], b1 = owners[1];
     if (b0 / 2 == b1 / 2) return;  // stored by its one share
-    constexpr int kPieces = C::kRows * BN / 8;
-#pragma unroll 1
-    for (int q = blockIdx.y * 256 + threadIdx.x; q < kPieces; q += gridDim.y * 256) {
-        // q counts rows of 32, then the four 8-column pieces of a 32-column block, then blocks
-        const int r = (q >> 7) / (BN / 32) * 32 + (q & 31);
-        const int c = (q >> 7) % (BN / 32) * 32 + (q >> 5 & 3) * 8;
-        float v[8] = {};
-        const float* p = a.partial + partial_at<BN>(r, c);
-        for (int b = b0; b <= b1;) {  // slot b0, then slot 0 of the shares after it; four in flight
-            uint32_t w[4][8];
-            int n = 0;
+    // q counts rows of 32, then the four 8-column pieces of a 32-column block, then blocks
+    const int q = blockIdx.y * 256 + threadIdx.x;
+    const int r = (q >> 7) / (BN / 32) * 32 + (q & 31);
+    const int c = (q >> 7) % (BN / 32) * 32 + (q >> 5 & 3) * 8;
+    float v[8] = {};
+    const float* p = a.partial + partial_at<BN>(r, c);
+    for (int b = b0; b <= b1;) {  // slot b0, then slot 0 of the shares after it; four in flight
+        uint32_t w[4][8];
+        int n = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (b <= b1) {
-                    ld32<32>(p + static_cast<int64_t>(b) * (C::kRows * BN), w[j]);
-                    b = (b | 1) + 1;
-                    n = j + 1;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j < n) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[j][k]);
-                }
+        for (int j = 0; j < 4; ++j) {
+            if (b <= b1) {
+                ld32<32>(p + static_cast<int64_t>(b) * (C::kRows * BN), w[j]);
+                b = (b | 1) + 1;
+                n = j + 1;
             }
         }
-        finish(a, static_cast<int64_t>(tile / a.tiles_n) * C::kRows + r,
-               static_cast<int64_t>(tile % a.tiles_n) * BN + c, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < n) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[j][k]);
+            }
+        }
     }
+    finish(a, static_cast<int64_t>(tile / a.tiles_n) * C::kRows + r,
+           static_cast<int64_t>(tile % a.tiles_n) * BN + c, v);
 }
 
-// One pass over dy, 32 rows at a time per block, thread = V columns:
-// - its column sums (partial not null): partial[blockIdx.y][outs], or db itself where one block row does;
-// - PACK: dy as the TMA needs it: rows of `pitch` bf16 (a multiple of 8), `tokens` per part (whole
-//   steps), zeros behind the last row and column.  fp32 is cut into three parts of 8 bits each by
-//   truncation, whose sum is the number itself; an infinity or a NaN stays in the first.
-template <typename T, int V, bool PACK>
-__global__ void __launch_bounds__(1024)
-    bias_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
+// dy as the TMA needs it, in one pass that also takes its column sums (partial not null, as below): rows
+// of `pitch` bf16 (a multiple of 8), `tokens` per part (whole steps), zeros behind the last row and
+// column.  fp32 is cut into three parts of 8 bits each by truncation, whose sum is the number itself; an
+// infinity or a NaN stays in the first.  Thread = 8 columns, read by the 16-byte granules that hold them
+// (10,744 x 1,854 bf16 element by element: 33 us); two rows' loads are on their way at a time.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(512, 2)
+    pack_kernel(const T* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
                 float* __restrict__ partial, bf16* __restrict__ out, int64_t pitch, int64_t tokens) {
-    __shared__ float tile[32][32 * V + 1];
-    if constexpr (!PACK) gq::pdl_launch_dependents();  // what follows waits where it reads the sums
+    __shared__ float tile[16][257];
+    gq::pdl_launch_dependents();  // what follows waits before it reads
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * V;
-    float s[V];
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * 8;
+    const int left = c < outs ? static_cast<int>(min(outs - c, int64_t(8))) : 0;
+    float s[8] = {};
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * 16;
+    constexpr int P = sizeof(T) / 2 + (ALIGNED ? 0 : 1), B = 2;
+    for (int64_t t = static_cast<int64_t>(blockIdx.y) * 16 + y; t < tokens; t += B * stride) {
+        uint32_t r[B][4 * P], m[B];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = 0.0f;
-    const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32 + y;
-    if constexpr (PACK) {
-        if (c < pitch) {
-            constexpr int B = V == 1 ? 8 : 2;  // rows whose loads are issued together
-            for (int64_t t = t0; t < tokens; t += B * stride) {
-                float v[B][V];
+        for (int k = 0; k < B; ++k) {
+            const uint8_t* q = reinterpret_cast<const uint8_t*>(dy + (t + k * stride) * ld + c);
+            m[k] = ALIGNED ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 15u;
+            const int bytes =
+                t + k * stride < rows && left > 0 ? static_cast<int>(m[k]) + left * static_cast<int>(sizeof(T)) : 0;
 #pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    if (t + k * stride < rows) {
-                        load<T, V, 16>(dy + (t + k * stride) * ld, c, outs, v[k]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    if (t + k * stride >= tokens) break;
-                    uint32_t top[V];
-#pragma unroll
-                    for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (p == 0) s[i] += v[k][i];
-                            const uint32_t bits = __float_as_uint(v[k][i]);
-                            top[i] = (bits & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FFF0000u : bits & 0xFFFF0000u;
-                            const bool special = (bits & 0x7F800000u) == 0x7F800000u;
-                            v[k][i] = special ? 0.0f : v[k][i] - __uint_as_float(top[i]);
-                        }
-                        bf16* to = out + (p * tokens + t + k * stride) * pitch + c;
-                        if constexpr (V == 8)
-                            *reinterpret_cast<uint4*>(to) =
-                                make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3],
-                                           top[4] >> 16 | top[5], top[6] >> 16 | top[7]);
-                        else
-                            *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(top[0] >> 16);
-                    }
-                }
+            for (int i = 0; i < P; ++i) {
+                const uint4 g = 16 * i < bytes ? __ldg(reinterpret_cast<const uint4*>(q - m[k]) + i)
+                                               : make_uint4(0u, 0u, 0u, 0u);
+                r[k][4 * i] = g.x; r[k][4 * i + 1] = g.y; r[k][4 * i + 2] = g.z; r[k][4 * i + 3] = g.w;
             }
         }
-    } else if (c < outs) {
-        const T* p = dy + t0 * ld;
-        int64_t left = rows - t0;
-        if constexpr (V == 8) {
-            // (the test for the last columns is outside, and rows that are not there are read as the
-            // first and left out, so that the loads are issued together)
-            if (c + V <= outs) {
-                constexpr int B = 8;
-                for (; left > 0; left -= B * stride, p += B * stride * ld) {
-                    Raw8<T> r[B];
 #pragma unroll
-                    for (int k = 0; k < B; ++k) r[k] = raw8(p + (left > k * stride ? k * stride * ld : 0) + c, 0, 8);
+        for (int k = 0; k < B; ++k) {
+            if (t + k * stride >= tokens) break;
+            const Raw8<T> w = shifted<T, ALIGNED>(r[k], m[k], left);
+            F2 h[4];
+            pairs(w, h);
+            float v[8];
 #pragma unroll
-                    for (int k = 0; k < B; ++k) {
-                        F2 v[4];
-                        pairs(r[k], v);
+            for (int i = 0; i < 4; ++i) split(h[i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x, y2;
-                            split(v[i], x, y2);
-                            s[2 * i] += left > k * stride ? x : 0.0f;
-                            s[2 * i + 1] += left > k * stride ? y2 : 0.0f;
-                        }
+            for (int i = 0; i < 8; ++i) s[i] += v[i];
+            if (c >= pitch) continue;
+            bf16* to = out + (t + k * stride) * pitch + c;
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4*>(to) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+            } else {
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    uint32_t top[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t bits = __float_as_uint(v[i]);
+                        top[i] = (bits & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FFF0000u : bits & 0xFFFF0000u;
+                        const bool special = (bits & 0x7F800000u) == 0x7F800000u;
+                        v[i] = special ? 0.0f : v[i] - __uint_as_float(top[i]);
                     }
+                    *reinterpret_cast<uint4*>(to + p * tokens * pitch) =
+                        make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3],
+                                   top[4] >> 16 | top[5], top[6] >> 16 | top[7]);
                 }
             }
-        }
-        for (; left > 0; left -= stride, p += stride * ld) {
-            float v[V];
-            load<T, V, 16>(p, c, outs, v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[i] += v[i];
         }
     }
     if (!partial) return;
 #pragma unroll
-    for (int i = 0; i < V; ++i) tile[y][x * V + i] = s[i];
+    for (int i = 0; i < 8; ++i) tile[y][x * 8 + i] = s[i];
+    __syncthreads();
+    const int64_t to = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (threadIdx.x < 256 && to < outs) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v += tile[k][threadIdx.x];
+        partial[blockIdx.y * outs + to] = v;
+    }
+}
+
+// Column sums of a bf16 dy with aligned rows, 32 rows at a time per block, thread = 8 columns:
+// partial[blockIdx.y][outs], or db itself where one block row does.  Eight rows' loads are on their way
+// at a time (16,384 x 4,096: 32 us with four, 27 with eight, of which the memory needs 20).
+__global__ void __launch_bounds__(1024)
+    bias_kernel(const bf16* __restrict__ dy, int64_t ld, int64_t rows, int64_t outs,
+                float* __restrict__ partial) {
+    __shared__ float tile[32][257];
+    gq::pdl_launch_dependents();  // what follows waits where it reads the sums
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * 8;
+    float s[8] = {};
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * 32;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32 + y;
+    const bf16* p = dy + t0 * ld + c;
+    int64_t left = rows - t0;
+    // (the test for the last columns is outside, and rows that are not there are read as the first and
+    // left out, so that the loads are issued together)
+    if (c + 8 <= outs) {
+        constexpr int B = 8;
+        for (; left > 0; left -= B * stride, p += B * stride * ld) {
+            Raw8<bf16> r[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) r[k] = raw8(p + (left > k * stride ? k * stride * ld : 0), 0, 8);
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                F2 v[4];
+                pairs(r[k], v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    split(v[i], lo, hi);
+                    s[2 * i] += left > k * stride ? lo : 0.0f;
+                    s[2 * i + 1] += left > k * stride ? hi : 0.0f;
+                }
+            }
+        }
+    } else if (c < outs) {
+        for (; left > 0; left -= stride, p += stride * ld) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < outs) s[i] += up(p[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[y][x * 8 + i] = s[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {  // a warp adds up a column
-        const int col = y * V + i;
+    for (int i = 0; i < 8; ++i) {  // a warp adds up a column
+        const int col = y * 8 + i;
         float v = tile[x][col];
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-        const int64_t to = static_cast<int64_t>(blockIdx.x) * 32 * V + col;
+        const int64_t to = static_cast<int64_t>(blockIdx.x) * 256 + col;
         if (x == 0 && to < outs) partial[blockIdx.y * outs + to] = v;
     }
 }
@@ -894,7 +922,7 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
                 consider(tiles * k, static_cast<double>((p.ksteps + k - 1) / k) + 0.15 * k / step, false);
         }
         const double even = static_cast<double>(tiles) * p.ksteps / most;
-        if (even >= 4.0) consider(most, even + 2.0, tiles % most == 0);
+        if (tiles > most || even >= 4.0) consider(most, even + 2.0, tiles % most == 0);
     }
     const int rows_of = p.big ? Large::kRows : Small::kRows, cols_of = p.big ? Large::BN : Small::BN;
     p.tiles_m = (outs + rows_of - 1) / rows_of;
@@ -902,7 +930,7 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.pitch = (outs + 7) / 8 * 8;
     // the pass over dy: up to 512 rows in one go if there are only sums to take, else one wave of blocks
     // (one per SM, two where dy is packed)
-    const int64_t groups = row_align(dy, dtype, rows, ld) ? (outs + 255) / 256 : (outs + 31) / 32;
+    const int64_t groups = (outs + 255) / 256;
     const int64_t wave = p.pack ? 2 * sms : sms;
     int64_t sh = rows <= 512 && !p.pack ? 1 : groups < wave ? wave / groups : 1;
     const int64_t rows_each = p.pack ? 32 : 128;
@@ -929,8 +957,8 @@ bool wgrad_sizes(int64_t rows, int64_t outs, int64_t cols) {
            static_cast<double>(rows) * outs * cols < 1e17;
 }
 
-// early: the launch before this one on the stream is of the sums of dy, which the kernel waits for only
-// where it reads them; what came before those is done when it starts.
+// early: the launch before this one on the stream is of the sums of dy or of its packed form, which the
+// kernel waits for only where it reads them; what came before those is done when it starts.
 template <typename C>
 gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, bool early, cudaStream_t st) {
     auto k = wgrad_kernel<C>;
@@ -950,7 +978,7 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, bool early, cudaS
     cfg.numAttrs = C::CG > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, k, map, a) != cudaSuccess) return GQ_ERR_CUDA;
     if (a.units > 0) {  // tiles that several shares work on
-        const dim3 grid(static_cast<unsigned>(a.units / a.ksteps), C::CG == 2 ? 32 : 8);
+        const dim3 grid(static_cast<unsigned>(a.units / a.ksteps), C::kRows * C::BN / 8 / 256);
         join_kernel<C><<<grid, 256, 0, st>>>(a);
     }
     return gqh::launch_status();
@@ -1001,19 +1029,18 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
         const int64_t tokens = p.ktok * kTok;
         bf16* out = p.pack ? reinterpret_cast<bf16*>(w + p.pack_off) : nullptr;
         const bool vec = row_align(dy, dtype, rows, lddy) != 0;
-        const int64_t cols_of = 32 * (vec ? 8 : 1), across = p.pack ? p.pitch : outs;
-        const dim3 grid(static_cast<unsigned>((across + cols_of - 1) / cols_of), p.bias_shares);
-#define GQA_SUMS(T, V, PACK)                                                                         \
-    bias_kernel<T, V, PACK><<<grid, 1024, 0, st>>>(static_cast<const T*>(dy), lddy, rows, outs, part, out, \
-                                                   p.pitch, tokens)
+        const dim3 grid(static_cast<unsigned>((outs + 255) / 256), p.bias_shares);
+#define GQA_PACK(T, ALIGNED)                                                                             \
+    pack_kernel<T, ALIGNED><<<grid, 512, 0, st>>>(static_cast<const T*>(dy), lddy, rows, outs, part, out, \
+                                                  p.pitch, tokens)
         if (dtype == GQ_F32) {
-            if (vec) GQA_SUMS(float, 8, true); else GQA_SUMS(float, 1, true);
+            if (vec) GQA_PACK(float, true); else GQA_PACK(float, false);
         } else if (p.pack) {
-            GQA_SUMS(bf16, 1, true);
+            GQA_PACK(bf16, false);
         } else {
-            GQA_SUMS(bf16, 8, false);  // aligned: else it would be packed
+            bias_kernel<<<grid, 1024, 0, st>>>(static_cast<const bf16*>(dy), lddy, rows, outs, part);
         }
-#undef GQA_SUMS
+#undef GQA_PACK
         if (sums && p.bias_shares > 1) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>((outs + 31) / 32));
@@ -1069,8 +1096,8 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
         a.ldw = a.cols = p.sums_ld;
         a.out_f32 = a.fast = 1;
     }
-    // a packed dy has to be there before the main kernel starts; sums alone only where it reads them
-    const bool early = sums && !p.pack;
+    a.packed = p.pack;
+    const bool early = sums || p.pack;
     const gq_status r = p.big ? launch_wgrad<Large>(map, a, early, st)
                               : launch_wgrad<Small>(map, a, early, st);
     if (r != GQ_OK || !raw) return r;

@@ -426,6 +426,30 @@ def test_linear_wgrad_pairs(gq, torch, rows, outs, cols, dtype, out, affine_part
     assert torch.equal(dw, again)
 
 
+@pytest.mark.parametrize("rows,outs,cols,dtype", [
+    (1, 100, 26000, "bf16"), (3, 5, 30000, "f32"), (70, 100, 26000, "bf16"), (130, 24000, 130, "f32"),
+    (40, 2100, 9000, "bf16"), (700, 2600, 1300, "f32")])
+def test_linear_wgrad_many_tiles(gq, torch, rows, outs, cols, dtype):
+    """More tiles than blocks, of few steps: whole tiles to each block, then shares of the rest."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((rows, cols), generator=g, device="cuda")
+    dy = (torch.randn((rows, outs), generator=g, device="cuda") * 1e-2).to(types(torch, dtype))
+    shift = torch.randn(cols, generator=g, device="cuda")
+    one = torch.ones_like(shift)
+    act = gq.gq_act_quantize(x)
+    v = gq.gq_act_dequantize(act, out_dtype=torch.float32).double()
+    d = dy.double()
+    dw, db = gq.gq_linear_wgrad(dy, act, scale=one, shift=shift)
+    want = d.t() @ v + torch.outer(d.sum(0), shift.double())
+    bias = d.abs().sum(0)
+    tolb = (rows + 40) * U * bias
+    steps = 3 * rows if dtype == "f32" else rows
+    tol = ((steps / 16 + 32) * 2.0 ** -22 + 4 * U) * (d.abs().t() @ v.abs()) + \
+        torch.outer(tolb + 4 * U * bias, shift.double().abs()) + U * want.abs()
+    assert ((dw.double() - want).abs() <= tol).all()
+    assert ((db.double() - d.sum(0)).abs() <= tolb).all()
+
+
 def test_linear_wgrad_special_values(gq, torch):
     """A NaN block of the checkpoint reaches its columns only; an infinite gradient its row only."""
     x = np.random.default_rng(0).standard_normal((70, 96)).astype(np.float32)
