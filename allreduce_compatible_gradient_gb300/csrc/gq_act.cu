@@ -216,30 +216,92 @@ template <typename T> __device__ __forceinline__ uint32_t top16(const uint32_t (
     }
 }
 
-// Rows that are not 16-byte aligned are written by warps: a piece's 16 values go to shared memory,
-// and 16 lanes each store those of one piece after the other, neighbours to neighbours.
+// Stores a lane's 16 elements of 2 bytes of a row that is not 16-byte aligned, of which `left` lie in the
+// row.  adjoins: the lane before holds what is in front of them.  16-byte granules are put together
+// from two neighbours' words; only where a neighbour is missing, and at the row's end, are elements
+// stored one by one.  The whole warp takes part.
+template <typename T>
+__device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const uint32_t (&w)[8]) {
+    constexpr int NW = 8, N = 16, G = 8;  // words, elements, elements of a granule
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const int full = left >= N;
+    const int before = __shfl_up_sync(kFull, full, 1);
+    const int joined = full && before && adjoins && lane > 0;
+    const int after = __shfl_down_sync(kFull, joined, 1);
+    uint32_t r[NW + 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __shfl_up_sync(kFull, w[NW - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) r[4 + i] = w[i];
+    const uint32_t d = 16u - m;  // the first granule's start in r
+#pragma unroll
+    for (int i = 0; i < NW; ++i) r[i] = (d & 16u) ? r[i + 4] : r[i];
+#pragma unroll
+    for (int i = 0; i < NW + 2; ++i) r[i] = (d & 8u) ? r[i + 2] : r[i];
+#pragma unroll
+    for (int i = 0; i < NW + 1; ++i) r[i] = (d & 4u) ? r[i + 1] : r[i];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], (d & 2u) * 8u);
+    auto one = [&](int i) {
+        reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> i % 2 * 16);
+    };
+    if (full) {
+        uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) - m);
+#pragma unroll
+        for (int j = 0; j < NW / 4; ++j)
+            if (j > 0 || joined || m == 0u)
+                q[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        if (m != 0u && !joined) {  // up to the first granule's end
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (2 * i < static_cast<int>(d)) one(i);
+        }
+        if (m != 0u && (!after || lane == 31)) {  // the next granule's part
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (2 * (G - i) <= static_cast<int>(m)) one(N - G + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) one(i);
+    }
+}
+// fp32 rows that are not 16-byte aligned are written by warps: a piece's 16 values go to shared memory,
+// and 16 lanes each store those of one piece after the other, neighbours to neighbours.  (By granules
+// as above 13,860 x 1,922 are read from codes in 33 us, so in 28; 32,046 x 1,317 bf16 so in 42 us, by
+// granules in 29.)
 struct Stage {
     float v[32][17];
     void* to[32];
     int left[32];
 };
 template <typename T>
-__device__ __forceinline__ void put16(T* p, bool live, int left, int align, Stage* st, const F2 (&v)[8]) {
+__device__ __forceinline__ void put16(T* p, bool live, bool adjoins, int left, int align, Stage* st,
+                                      const F2 (&v)[8]) {
     float o[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
     if (align == 0) {
-        const int lane = threadIdx.x & 31;
-        __syncwarp();
+        if constexpr (sizeof(T) == 2) {
+            uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st->v[lane][i] = o[i];
-        st->to[lane] = p;
-        st->left[lane] = live ? left : 0;
-        __syncwarp();
+            for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i], o[2 * i + 1], T());
+            put_words(p, live ? left : 0, adjoins, w);
+        } else {
+            const int lane = threadIdx.x & 31;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) st->v[lane][i] = o[i];
+            st->to[lane] = p;
+            st->left[lane] = live ? left : 0;
+            __syncwarp();
 #pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int k = 2 * i + (lane >> 4), j = lane & 15;
-            if (j < st->left[k]) down(st->v[k][j], static_cast<T*>(st->to[k])[j]);
+            for (int i = 0; i < 16; ++i) {
+                const int k = 2 * i + (lane >> 4), j = lane & 15;
+                if (j < st->left[k]) static_cast<T*>(st->to[k])[j] = st->v[k][j];
+            }
         }
     } else if (live) {
         if (align == 32) store<T, 16, 32>(p, 0, left, o);
@@ -308,7 +370,7 @@ __global__ void __launch_bounds__(kT, 4)
         if constexpr (OP != kSave) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], cdf<OP, sizeof(T) == 4, false>(v[i], nullptr));
-            put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, left, align, st, v);
+            put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, st, v);
         }
     }
     copy_all();
@@ -362,7 +424,7 @@ __global__ void __launch_bounds__(kT, 4)
         for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
         T* out = du + static_cast<int64_t>(row) * lddu + c;
         if constexpr (OP == kSave) {
-            put16<T>(out, live, left, align, st, v);
+            put16<T>(out, live, piece > 0, left, align, st, v);
         } else {
             uint32_t w[kWords<T>];
             F2 g[8];
@@ -375,8 +437,8 @@ __global__ void __launch_bounds__(kT, 4)
                 g[i] = mul2(g[i], add2(p, u_phi));
                 v[i] = mul2(v[i], p);
             }
-            put16<T>(out, live, left, align, st, g);
-            if (h) put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, left, align, st, v);
+            put16<T>(out, live, piece > 0, left, align, st, g);
+            if (h) put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, st, v);
         }
     }
     copy_all();
@@ -398,7 +460,9 @@ unsigned plan_walk(K kernel, size_t smem, int64_t rows, int64_t cols, Walk& a) {
     a.per_row = make_div(static_cast<uint32_t>(pieces));
     return static_cast<unsigned>((a.lanes * pieces + kT - 1) / kT);
 }
-constexpr size_t stage_bytes(int align) { return align ? 0 : kT / 32 * sizeof(Stage); }
+template <typename T> constexpr size_t stage_bytes(int align) {
+    return align || sizeof(T) == 2 ? 0 : kT / 32 * sizeof(Stage);
+}
 
 // What a call is made of; rows 32-, 16- or 0-byte aligned.
 struct SaveCall {
@@ -415,7 +479,7 @@ struct SaveCall {
 template <typename T, bool ALIGNED, int OP, int RND> gq_status run_save(const SaveCall& s) {
     auto k = save_kernel<T, ALIGNED, OP, RND>;
     const size_t smem = kRing<T, ALIGNED> * kT * 16 * (sizeof(T) + (ALIGNED ? 0 : 1)) +
-                        (OP == kSave ? 0 : stage_bytes(s.out));
+                        (OP == kSave ? 0 : stage_bytes<T>(s.out));
     Walk a;
     const unsigned grid = plan_walk(k, smem, s.rows, s.cols, a);
     k<<<grid, kT, smem, s.st>>>(static_cast<const T*>(s.x), s.ldx, static_cast<T*>(s.h), s.ldh, s.out, a,
@@ -448,7 +512,7 @@ struct ReadCall {
 template <typename T, bool ALIGNED, int OP> gq_status run_read(const ReadCall& s) {
     auto k = read_kernel<T, ALIGNED, OP>;
     const size_t n = OP == kSave ? 0 : sizeof(T) + (ALIGNED ? 0 : 1);
-    const size_t smem = kRing<T, ALIGNED> * (kT * 16 * (n + 1) + kT * 4) + stage_bytes(s.out);
+    const size_t smem = kRing<T, ALIGNED> * (kT * 16 * (n + 1) + kT * 4) + stage_bytes<T>(s.out);
     Walk a;
     const unsigned grid = plan_walk(k, smem, s.rows, s.cols, a);
     k<<<grid, kT, smem, s.st>>>(s.codes, s.exps, a, static_cast<const T*>(s.dy), s.lddy,
