@@ -104,29 +104,16 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
 }
 
 // V consecutive elements starting at column c of the row at p, widened to fp32; columns at and
-// past `cols` read as 0.  V = 1: one element.  V = 8 or 16: p + c is ALIGN-byte aligned.
-template <typename T, int V, int ALIGN>
+// past `cols` read as 0.  V = 1: one element.  V = 8: p + c is 16-byte aligned.
+template <typename T, int V>
 __device__ __forceinline__ void load(const T* p, int64_t c, int64_t cols, float (&v)[V]) {
     if constexpr (V > 1) {
         if (c + V <= cols) {
             if constexpr (sizeof(T) == 4) {
-                if constexpr (V * 4 >= 32) {
-#pragma unroll
-                    for (int k = 0; k < V / 8; ++k) {
-                        uint32_t w[8];
-                        ld32<ALIGN>(p + c + 8 * k, w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[8 * k + i] = __uint_as_float(w[i]);
-                    }
-                }
-            } else if constexpr (V == 16) {
                 uint32_t w[8];
-                ld32<ALIGN>(p + c, w);
+                ld32<16>(p + c, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                }
+                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
             } else {
                 const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + c));
                 const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -143,6 +130,7 @@ __device__ __forceinline__ void load(const T* p, int64_t c, int64_t cols, float 
     for (int i = 0; i < V; ++i) v[i] = c + i < cols ? up(p[c + i]) : 0.0f;
 }
 
+// The same for storing; V = 8 or 16: p + c is ALIGN-byte aligned.
 template <typename T, int V, int ALIGN>
 __device__ __forceinline__ void store(T* p, int64_t c, int64_t cols, const float (&v)[V]) {
     if constexpr (V > 1) {
@@ -395,28 +383,6 @@ __device__ __forceinline__ void values8(uint2 w, uint32_t e, F2 (&v)[4]) {
 template <typename T> struct Raw8 {
     uint32_t w[sizeof(T) * 2];
 };
-template <typename T>
-__device__ __forceinline__ Raw8<T> raw8(const T* p, int64_t c, int64_t cols) {
-    Raw8<T> r;
-    if (c + 8 <= cols) {
-#pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + c) + k);
-            r.w[4 * k] = a.x; r.w[4 * k + 1] = a.y; r.w[4 * k + 2] = a.z; r.w[4 * k + 3] = a.w;
-        }
-    } else {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? up(p[c + i]) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (sizeof(T) == 4) r.w[i] = __float_as_uint(v[i]);
-            else if (i & 1) r.w[i / 2] |= __float_as_uint(v[i]) & 0xFFFF0000u;
-            else r.w[i / 2] = __float_as_uint(v[i]) >> 16;
-        }
-    }
-    return r;
-}
 // 8 elements out of the words of the 16-byte granules that hold them: the first is m bytes behind the
 // first granule's start (0 where ALIGNED); `left` of them are wanted, the others read as 0.
 template <typename T, bool ALIGNED, int N>
@@ -459,11 +425,11 @@ __device__ __forceinline__ void pairs(const Raw8<T>& r, F2 (&v)[4]) {
     }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t c, int64_t cols, const F2 (&v)[4]) {
+__device__ __forceinline__ void store8(T* p, const F2 (&v)[4]) {
     float o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
-    store<T, 8, 16>(p, c, cols, o);
+    store<T, 8, 16>(p, 0, 8, o);
 }
 
 // What V codes stand for.  A code byte plus 128 in the low byte of the fp32 number 2^23 gives

@@ -28,9 +28,9 @@ __device__ __forceinline__ void vec_of(const void* p, int wide, float none, int6
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = none;
     } else if (wide) {
-        load<float, V, 16>(static_cast<const float*>(p), c, cols, v);
+        load<float, V>(static_cast<const float*>(p), c, cols, v);
     } else {
-        load<bf16, V, 16>(static_cast<const bf16*>(p), c, cols, v);
+        load<bf16, V>(static_cast<const bf16*>(p), c, cols, v);
     }
 }
 
@@ -173,7 +173,7 @@ template <typename T, bool ALIGNED>
 __device__ __forceinline__ void put8(T* row, uint32_t col, bool in, uint32_t first, uint32_t cols,
                                      float* square, const F2 (&v)[4]) {
     if constexpr (ALIGNED) {
-        if (in) store8(row + col, 0, 8, v);
+        if (in) store8(row + col, v);
     } else {
         const int lane = threadIdx.x & 31;
         __syncwarp();

@@ -37,7 +37,7 @@ __device__ __forceinline__ void hat_of(const Source<T>& src, const Shape& s, int
             for (int i = 0; i < V; ++i) v[i] = 0.0f;
         }
     } else {
-        load<T, V, 16>(src.x + row * src.ldx, c, s.cols, v);
+        load<T, V>(src.x + row * src.ldx, c, s.cols, v);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = c + i < s.cols ? (v[i] - mean) * rstd : 0.0f;
     }
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(512)
     float g[VPT][V], h[VPT][V];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        load<T, V, 16>(dyr, k * step + t * V, s.cols, g[k]);
+        load<T, V>(dyr, k * step + t * V, s.cols, g[k]);
         hat_of<T, V, CODES>(src, s, row, mean, rstd, k * step + t * V, h[k]);
     }
     float c[2] = {0.0f, 0.0f};
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(512)
     }
     for (int64_t col = beyond + t * V; col < s.cols; col += step) {
         float a[V], b[V], wv[V];
-        load<T, V, 16>(dyr, col, s.cols, a);
+        load<T, V>(dyr, col, s.cols, a);
         hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
         vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
 #pragma unroll
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(512)
     }
     for (int64_t col = beyond + t * V; col < s.cols; col += step) {
         float a[V], b[V], wv[V];
-        load<T, V, 16>(dyr, col, s.cols, a);
+        load<T, V>(dyr, col, s.cols, a);
         hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
         vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
 #pragma unroll

@@ -26,13 +26,13 @@ __global__ void __launch_bounds__(512)
     float sum[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        load<T, V, 16>(xr, k * step + t * V, s.cols, v[k]);
+        load<T, V>(xr, k * step + t * V, s.cols, v[k]);
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[0] += v[k][i];
     }
     for (int64_t c = beyond + t * V; c < s.cols; c += step) {
         float z[V];
-        load<T, V, 16>(xr, c, s.cols, z);
+        load<T, V>(xr, c, s.cols, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[0] += z[i];
     }
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(512)
     }
     for (int64_t c = beyond + t * V; c < s.cols; c += step) {
         float z[V];
-        load<T, V, 16>(xr, c, s.cols, z);
+        load<T, V>(xr, c, s.cols, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float d = c + i < s.cols ? z[i] - mean : 0.0f;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(512)
     for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
         const int64_t c = c0 + t * V;
         float z[V];
-        load<T, V, 16>(xr, c, s.cols, z);
+        load<T, V>(xr, c, s.cols, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = c + i < s.cols ? z[i] - mean : 0.0f;
         finish(c, z);

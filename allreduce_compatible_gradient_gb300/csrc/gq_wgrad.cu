@@ -786,13 +786,14 @@ __global__ void __launch_bounds__(1024)
     if (c + 8 <= outs) {
         constexpr int B = 8;
         for (; left > 0; left -= B * stride, p += B * stride * ld) {
-            Raw8<bf16> r[B];
+            uint4 r[B];
 #pragma unroll
-            for (int k = 0; k < B; ++k) r[k] = raw8(p + (left > k * stride ? k * stride * ld : 0), 0, 8);
+            for (int k = 0; k < B; ++k)
+                r[k] = __ldg(reinterpret_cast<const uint4*>(p + (left > k * stride ? k * stride * ld : 0)));
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 F2 v[4];
-                pairs(r[k], v);
+                pairs(Raw8<bf16>{{r[k].x, r[k].y, r[k].z, r[k].w}}, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float lo, hi;
