@@ -219,7 +219,7 @@ struct Held {
 };
 inline Held held_for(int64_t rows, int64_t cols) {
     Held h;
-    h.vpt = cols <= 256 ? 1 : 2;
+    h.vpt = cols <= 256 || (cols > 512 && cols <= 768) ? 1 : 2;
     h.wpr = static_cast<int>((cols + 256 * h.vpt - 1) / (256 * h.vpt));
     h.groups = h.wpr <= 4 && rows > 2 * gqh::sm_count() ? 8 / h.wpr : 1;
     h.threads = 32 * h.wpr * h.groups;
@@ -242,7 +242,8 @@ inline HeldArgs held_args(const Held& h, int grid, const Shape& s, int64_t in, i
 }
 // run.template operator()<VPT, W, MOST>() for a shape of the held form
 template <typename F> auto held_switch(const Held& h, F run) {
-    if (h.vpt == 1) return run.template operator()<1, kOne, 256>();
+    if (h.vpt == 1 && h.wpr == 1) return run.template operator()<1, kOne, 256>();
+    if (h.vpt == 1) return run.template operator()<1, kFour, 256>();
     if (h.wpr == 1) return run.template operator()<2, kOne, 256>();
     if (h.wpr <= 4) return run.template operator()<2, kFour, 256>();
     if (h.wpr <= 8) return run.template operator()<2, kMany, 256>();
