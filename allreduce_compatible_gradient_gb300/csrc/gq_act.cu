@@ -4,7 +4,9 @@
 // next to that by the instructions it issues (random rounding above all: a Philox call per 8
 // elements).  A thread owns a piece of 16 columns (half a block of the format; the other half is its
 // neighbour's) and walks down the rows, so that the column part of the random words is computed once
-// and the next rows' copies are in flight meanwhile.
+// and the next rows' copies are in flight meanwhile.  At 32,768 x 4,096 bf16 (268 MB) saving takes 64 us
+// rounding to nearest and 77 at random (5.3 TB/s, its issue slots 69 % busy), reading back 62 (6.5 TB/s),
+// GELU forward with the checkpoint 109 (6.2 TB/s), backward with the output 150 (6.3 TB/s).
 #include "gq_act.cuh"
 
 #include <type_traits>
@@ -22,7 +24,7 @@ constexpr int kT = 256;  // threads per block
 // (8 coefficients, fp32 outputs) or 5e-6 (6 coefficients, bf16 outputs, whose own rounding is
 // 2e-3).  One exponential serves the distribution and the density.  Two elements are worked on
 // at a time (pairs of fp32): instructions, not memory, bounded the first form of the backward pass
-// (239 us at 32,768 x 4,096 bf16 with the output, of which the memory needs 139).
+// (32,768 x 4,096 bf16 with the output: 239 us one at a time, 150 so, of which the memory needs 139).
 template <bool WIDE> struct Tail;
 template <> struct Tail<true> {
     static constexpr float p = 0.30f;

@@ -4,9 +4,9 @@
 // Format: a row of `cols` elements is cut into blocks of 32 columns.  A block with largest
 // magnitude a has the exponent byte E = min{ E >= 1 : a <= 127 * 2^(E - 127) }, 255 if it holds
 // a NaN, an infinity or a magnitude above 127 * 2^121 (its codes are then 0 and it reads back as
-// NaN: 0 * 2^128); an element stands for code * 2^(E - 127).  A power-of-two step costs at most one bit against a free step
-// (the code of the block's largest element lies in 64..127) and makes every value, 7 bits times
-// a power of two, exact in bf16: what reads a checkpoint rounds nothing.
+// NaN: 0 * 2^128); an element stands for code * 2^(E - 127).  A power-of-two step costs at most one
+// bit against a free step (the code of the block's largest element lies in 64..127) and makes every
+// value, 7 bits times a power of two, exact in bf16: what reads a checkpoint rounds nothing.
 #pragma once
 #include "gq.h"
 #include "gq_host.cuh"

@@ -6,9 +6,14 @@
 //   backward  dx = rstd (w dy - mean(w dy) - xh mean(w dy xh));  dw = sum_rows dy xh;
 //             db = sum_rows dy
 //
-// Both are bound by memory.  A row stays in registers between its reductions, so it is read
-// once ("rows held by fixed threads"); the generic kernels take rows of more columns than a block holds,
-// and read again what does not fit their registers (from L2, mostly).  All sums are fp32.
+// Both are bound by memory, and next to that by their instructions (65,536 x 1,024 bf16: forward 41 us
+// without a checkpoint, 54 with one rounded to nearest, 71 at random, of which the memory needs 40, 50
+// and 50; backward 59 from x and 61 from codes, of which it needs 59 and 50).  A row stays in
+// registers between its reductions, so it is read once ("rows held by fixed threads"); the generic
+// kernels take rows of more columns than a block holds, and read again what does not fit their registers
+// (from L2, mostly).  That form costs 2 to 3 times as much (4,096 x 8,192 bf16 forward 37 us held, 3,640 x
+// 9,216 as many bytes in 93), and rows of it that are not aligned are read element by element (142 us).
+// All sums are fp32.
 #pragma once
 #include "gq_act.cuh"
 
@@ -65,14 +70,14 @@ inline Shape shape_of(int64_t rows, int64_t cols) {
 
 // ---- rows held by fixed threads ------------------------------------------------------------
 // The form for rows of up to 8,192 columns, with a variant for 16-byte aligned rows of a multiple of 8
-// columns.  A group of 32 wpr
-// threads (whole warps, 16 columns per thread as two pieces of 8; 8 columns up to 256) walks over
+// columns.  A group of 32 wpr threads (whole warps, 16 columns per thread as two pieces of 8) walks over
 // rows; a thread has the same columns of every row, so that weights, the backward sums and the column
 // part of the random words stay in registers, and the next rows are on their way while one is worked
 // on.  What bounds it is the number of instructions per row beside its elements' own: 16 columns per
-// thread instead of 8 took the backward pass at 65,536 x 1,024 bf16 from 75 to 65 us; no branches
-// depend on the thread either: a thread behind the last column works on copies of the first columns
-// with weights and masks of 0, and only its stores are left out.
+// thread instead of 8 took the backward pass at 65,536 x 1,024 bf16 from 75 to 65 us.  No branches
+// depend on the thread either (65 -> 59 us): a thread behind the last column works on copies of the
+// first columns with weights and masks of 0, and only its stores are left out.  The two pieces lie 256
+// columns apart, so that neighbours load neighbours (16 columns side by side: 59 -> 67 us).
 
 // Warps per row, as far as the reductions differ by it.
 enum Wide { kOne = 1, kFour = 4, kMany = 16 };
@@ -211,9 +216,13 @@ inline bool held_ok(int64_t cols, int64_t ld_bytes) {
     return cols <= kHeldCols && ld_bytes < (int64_t(1) << 32);
 }
 
-// Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.  With
-// fewer rows than two per SM a block takes one at a time: there is nothing to share, and the sums
-// need not be put together within the block.
+// Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.  One piece
+// per thread where two would leave a quarter of them idle in whole warps: up to 256 columns, and from
+// 513 to 768 (43,690 x 768 bf16, backward from codes: 50 us with two pieces, 39 with one; at 1,024
+// columns two are faster, see above).  Eight warps a block, two blocks per SM: three, with 84
+// registers a thread, took the forward pass at 65,536 x 1,024 from 72 to 78 us.  With fewer rows than
+// two per SM a block takes one at a time: there is nothing to share, and the sums need not be put
+// together within the block.
 struct Held {
     int vpt, threads, wpr, groups;
 };

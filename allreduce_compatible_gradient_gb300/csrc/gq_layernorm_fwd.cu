@@ -5,8 +5,8 @@ using namespace gqa;
 
 namespace {
 
-// Rows of more columns than the held form takes: a block per row, thread t of its `threads` takes the pieces of V columns t, t + threads, ...: the first VPT
-// of them in registers.  The loops run to the code pitch, and past it to a whole number of pieces
+// Rows of more columns than the held form takes: a block per row, thread t of its `threads` takes the
+// pieces of V columns t, t + threads, ...: the first VPT of them in registers.  The loops run to the code pitch, and past it to a whole number of pieces
 // per warp, so that every lane takes part in the block reductions of the checkpoint.
 template <typename T, int V, int VPT, int RND>
 __global__ void __launch_bounds__(512)

@@ -20,14 +20,24 @@
 //               of a load or of a barrier is that of two steps' time
 // Both operands are contiguous along their outer dimension ("MN-major"), so neither is transposed.
 // Why pairs: shared memory moves 128 bytes per cycle, and one block with a 256 x 256 tile asks for 160
-// (operands 96, dy's arrival 32, the widened codes 32): it ran at 74 % of the MMA rate.  A pair shares
-// the widened codes, and asks for 112.
+// (operands 96, dy's arrival 32, the widened codes 32).  A pair shares the widened codes, and asks for 112.
 //
-// The steps (64 tokens) of all tiles are one list, cut into equal contiguous shares, one per block or
-// pair: a tile that two or more of them work on leaves fp32 partial tiles in the workspace, which
-// join_kernel adds in a fixed order.  The tensor cores' fp32 accumulation rounds each sum of 16 products
-// towards zero or nearly so, an error that grows with the length of the chain (7.8e-6 of the result's
-// norm over 16,384 tokens): a chain ends after kChain steps, and the rest is added to it in fp32 outside.
+// Each block or pair first works on whole tiles of its own, beside the others' in the matrix (so that they
+// read the same rows of dy and the same codes at the same time: 0.76 GB from memory at 4,096 x 4,096 x
+// 16,384 tokens, 1.03 where each began elsewhere); the steps (64 tokens) of the tiles that are left are
+// one list, cut into equal contiguous pieces.  A tile that two or more blocks work on leaves fp32 partial
+// tiles in the workspace, which join_kernel adds in a fixed order.
+//
+// The tensor cores' fp32 accumulation rounds each sum of 16 products towards zero or nearly so, an error
+// that grows with the length of the chain (5.8e-6 of the result's norm over 16,384 tokens): a chain ends
+// after kChain steps, and the rest is added to it in fp32 outside (1.6e-6; an fp32 product by the
+// library has 2.2e-6).
+//
+// What bounds it: the tensor cores, and the ends of the chains, when 256 KB of sums per block leave or
+// cross the L2.  4,096 x 4,096 x 16,384 tokens, bf16: 333 us without db (the library's product of two
+// bf16 matrices 285; chains of 256 steps would take 310), 360 with it.  Tiles side by side, a chain's
+// steps widened ahead, its accumulators finished one after the other, and first chains of different
+// lengths took it there from 352 and 379.
 #include "gq_act.cuh"
 
 #include <cuda.h>
@@ -37,7 +47,7 @@ using namespace gqa;
 namespace {
 
 constexpr int kTok = 64;              // tokens per step
-constexpr int kChain = 96;            // steps of one accumulation
+constexpr int kChain = 96;            // steps of one accumulation (error and time above)
 constexpr int kEarly = 2;             // steps widened for the next chain before one's sums are stored
 constexpr int kTeams = 2;             // teams of widening warps that take turns at the steps
 constexpr int kChunk = kTok * 128;    // bytes of 64 outs (or columns) x 64 tokens in bf16
@@ -899,8 +909,10 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
     p.ksteps = p.ktok * p.parts;
     // Small or large tiles, and how many shares: the smallest of the times that the steps, a launch's
     // ends and the partial tiles take, in microseconds as measured (a step of a 512 x 256 tile 0.55, of
-    // a 128 x 128 tile 0.36; splitting tiles costs 12 or 6 more: 4096 x 4096 x 16384 takes 338 us in
-    // large tiles and 783 in small ones, 768 x 768 x 384 takes 14.5 us in 54 shares, 8.3 in 36 whole tiles).
+    // a 128 x 128 tile 0.36; splitting tiles costs 12 or 6 more).  Both sides, in graphs, outs x columns x
+    // tokens: 2,048 x 2,048 x 8,192 66 us in large tiles and 114 in small ones, 4,096 x 1,024 x 512 23.0 and
+    // 25.5, 768 x 768 x 384 21 and 12, 3,840 x 41 x 15,872 66 and 53; 768 x 768 x 384 in 54 shares of the
+    // small tiles instead of 36 whole ones 14.5 and 10.4.
     double best = 0.0;
     for (int large = 0; large < 2; ++large) {
         const int rows_of = large ? Large::kRows : Small::kRows, cols_of = large ? Large::BN : Small::BN;
