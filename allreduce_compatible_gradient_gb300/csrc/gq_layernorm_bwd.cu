@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
                   float* __restrict__ partial) {
     gq::pdl_launch_dependents();  // sum_kernel, which waits for this one's end before it reads
     __shared__ alignas(16) float buf[2][2 * kSlots];
-    extern __shared__ __align__(16) uint8_t ring[];  // afterwards 2 x cols sums, with several groups
+    extern __shared__ __align__(16) uint8_t ring[];  // afterwards the groups' column sums
     const int warp = threadIdx.x >> 5;
     const int group = W == kMany ? 0 : warp / a.wpr, wr = warp - group * a.wpr;
     const uint32_t t = wr * 32 + (threadIdx.x & 31), apart = a.wpr * 256;
@@ -281,51 +281,37 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
         }
     }
     copy_all();
-    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    float* shared_cols = reinterpret_cast<float*>(ring);
-    float* out = a.groups > 1 ? shared_cols : pw;
-    for (int q = 0; q < a.groups; ++q) {  // the groups add up their columns one after another
-        if (a.groups > 1) __syncthreads();
-        if (group != q) continue;
+    // every group's column sums to shared memory (whole warps' columns, behind the last one too), then
+    // the block's to its partial row
+    float* const sums = reinterpret_cast<float*>(ring);
+    const uint32_t pitch = apart * VPT;
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            if (!in[k]) continue;
-            if constexpr (!ALIGNED) {
+    for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    float u[2], d[2];
-                    split(aw[k][z / 2], u[0], u[1]);
-                    split(ab[k][z / 2], d[0], d[1]);
-                    if (z >= left[k]) continue;
-                    float* at = out + col[k] + z;
-                    at[0] = (q > 0 ? at[0] : 0.0f) + u[z & 1];
-                    at[a.cols] = (q > 0 ? at[a.cols] : 0.0f) + d[z & 1];
-                }
-            } else {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {  // 4 columns of dw, 4 more, the same of db
-                    const F2 lo = z < 2 ? aw[k][2 * z] : ab[k][2 * z - 4];
-                    const F2 hi = z < 2 ? aw[k][2 * z + 1] : ab[k][2 * z - 3];
-                    float4 v;
-                    split(lo, v.x, v.y);
-                    split(hi, v.z, v.w);
-                    float4* at = reinterpret_cast<float4*>(out + (z < 2 ? 0u : a.cols) + col[k] + (z & 1) * 4);
-                    if (q > 0) {
-                        const float4 u = *at;
-                        v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-                    }
-                    *at = v;
-                }
-            }
+        for (int z = 0; z < 4; ++z) {  // 4 columns of dw, 4 more, the same of db
+            const F2* from = z < 2 ? aw[k] : ab[k];
+            float4 v;
+            split(from[z % 2 * 2], v.x, v.y);
+            split(from[z % 2 * 2 + 1], v.z, v.w);
+            *reinterpret_cast<float4*>(sums + (2 * group + z / 2) * pitch + k * apart + t * 8 + z % 2 * 4) = v;
         }
     }
-    if (a.groups > 1) {
-        __syncthreads();
+    __syncthreads();
+    float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    for (uint32_t i = threadIdx.x * (ALIGNED ? 4 : 1); i < 2 * a.cols; i += blockDim.x * (ALIGNED ? 4 : 1)) {
+        const float* at = sums + (i < a.cols ? i : pitch + i - a.cols);
         if constexpr (ALIGNED) {
-            for (uint32_t i = threadIdx.x; i < a.cols / 2; i += blockDim.x)
-                reinterpret_cast<float4*>(pw)[i] = reinterpret_cast<const float4*>(shared_cols)[i];
+            float4 v = *reinterpret_cast<const float4*>(at);
+            for (int q = 1; q < a.groups; ++q) {
+                const float4 u = *reinterpret_cast<const float4*>(at + 2 * q * pitch);
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            *reinterpret_cast<float4*>(pw + i) = v;
         } else {
-            for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) pw[i] = shared_cols[i];
+            float v = *at;
+            for (int q = 1; q < a.groups; ++q) v += at[2 * q * pitch];
+            pw[i] = v;
         }
     }
 }
@@ -355,7 +341,7 @@ template <typename T, bool ALIGNED, bool CODES> struct BackwardHeld {
     const Held& h;
     template <int VPT, int W, int MOST> int operator()() const {
         using R = Ring<T, ALIGNED>;
-        // (also room for 2 x cols sums: 56 bytes per thread and piece at least)
+        // (also room for the column sums, 64 bytes per thread and piece: the slots have 88 at least)
         const size_t smem = static_cast<size_t>(slots_of<T, ALIGNED, MOST>) * h.threads * VPT *
                                 (CODES ? 16 * R::kPieces + 12 : 32 * R::kPieces) +
                             (ALIGNED ? 0 : h.threads / 32 * kSquare * sizeof(float));
