@@ -218,13 +218,12 @@ template <typename T> __device__ __forceinline__ uint32_t top16(const uint32_t (
     }
 }
 
-// Stores a lane's 16 elements of 2 bytes of a row that is not 16-byte aligned, of which `left` lie in the
-// row.  adjoins: the lane before holds what is in front of them.  16-byte granules are put together
+// Stores a lane's 16 elements of a row that is not 16-byte aligned, of which `left` lie in the row.  adjoins: the lane before holds what is in front of them.  16-byte granules are put together
 // from two neighbours' words; only where a neighbour is missing, and at the row's end, are elements
 // stored one by one.  The whole warp takes part.
 template <typename T>
-__device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const uint32_t (&w)[8]) {
-    constexpr int NW = 8, N = 16, G = 8;  // words, elements, elements of a granule
+__device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const uint32_t (&w)[kWords<T>]) {
+    constexpr int E = sizeof(T), NW = kWords<T>, N = 16, G = 16 / E;  // words, elements, those of a granule
     const int lane = threadIdx.x & 31;
     const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
     const int full = left >= N;
@@ -243,10 +242,13 @@ __device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const ui
     for (int i = 0; i < NW + 2; ++i) r[i] = (d & 8u) ? r[i + 2] : r[i];
 #pragma unroll
     for (int i = 0; i < NW + 1; ++i) r[i] = (d & 4u) ? r[i + 1] : r[i];
+    if constexpr (E == 2) {
 #pragma unroll
-    for (int i = 0; i < NW; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], (d & 2u) * 8u);
+        for (int i = 0; i < NW; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], (d & 2u) * 8u);
+    }
     auto one = [&](int i) {
-        reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> i % 2 * 16);
+        if constexpr (E == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> i % 2 * 16);
     };
     if (full) {
         uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) - m);
@@ -257,12 +259,12 @@ __device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const ui
         if (m != 0u && !joined) {  // up to the first granule's end
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (2 * i < static_cast<int>(d)) one(i);
+                if (E * i < static_cast<int>(d)) one(i);
         }
         if (m != 0u && (!after || lane == 31)) {  // the next granule's part
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (2 * (G - i) <= static_cast<int>(m)) one(N - G + i);
+                if (E * (G - i) <= static_cast<int>(m)) one(N - G + i);
         }
     } else {
 #pragma unroll
@@ -270,26 +272,29 @@ __device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const ui
             if (i < left) one(i);
     }
 }
-// fp32 rows that are not 16-byte aligned are written by warps: a piece's 16 values go to shared memory,
-// and 16 lanes each store those of one piece after the other, neighbours to neighbours.  (By granules
-// as above 13,860 x 1,922 are read from codes in 33 us, so in 28; 32,046 x 1,317 bf16 so in 42 us, by
-// granules in 29.)
+// The other way, for fp32 values that were read from codes: a piece's 16 values go to shared memory, and
+// 16 lanes each store those of one piece after the other, neighbours to neighbours.  (13,860 x 1,922
+// fp32: read from codes in 28 us so, in 33 by granules; GELU forward with random codes 55 so, 51 by
+// granules.  32,046 x 1,317 bf16: read from codes in 42 so, in 29 by granules.)
 struct Stage {
     float v[32][17];
     void* to[32];
     int left[32];
 };
-template <typename T>
+template <typename T, bool GRANULES>
 __device__ __forceinline__ void put16(T* p, bool live, bool adjoins, int left, int align, Stage* st,
                                       const F2 (&v)[8]) {
     float o[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
     if (align == 0) {
-        if constexpr (sizeof(T) == 2) {
-            uint32_t w[8];
+        if constexpr (GRANULES) {
+            uint32_t w[kWords<T>];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i], o[2 * i + 1], T());
+            for (int i = 0; i < kWords<T>; ++i) {
+                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(o[i]);
+                else w[i] = pack2(o[2 * i], o[2 * i + 1], T());
+            }
             put_words(p, live ? left : 0, adjoins, w);
         } else {
             const int lane = threadIdx.x & 31;
@@ -323,7 +328,6 @@ __global__ void __launch_bounds__(kT, 4)
     const uint32_t piece = id - first * a.per_row.d, c = piece * 16;
     const int left = static_cast<int>(a.cols) - static_cast<int>(c);
     const bool mine = first < a.lanes;
-    Stage* st = reinterpret_cast<Stage*>(ring + D * slot) + (threadIdx.x >> 5);
     const uint32_t base = gq::smem_u32(ring) + threadIdx.x * 16;
     gq::PhiloxGroup pg[2];
     if constexpr (RND == 1) {
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kT, 4)
         if constexpr (OP != kSave) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], cdf<OP, sizeof(T) == 4, false>(v[i], nullptr));
-            put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, st, v);
+            put16<T, true>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, nullptr, v);
         }
     }
     copy_all();
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(kT, 4)
         for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
         T* out = du + static_cast<int64_t>(row) * lddu + c;
         if constexpr (OP == kSave) {
-            put16<T>(out, live, piece > 0, left, align, st, v);
+            put16<T, sizeof(T) == 2>(out, live, piece > 0, left, align, st, v);
         } else {
             uint32_t w[kWords<T>];
             F2 g[8];
@@ -439,8 +443,8 @@ __global__ void __launch_bounds__(kT, 4)
                 g[i] = mul2(g[i], add2(p, u_phi));
                 v[i] = mul2(v[i], p);
             }
-            put16<T>(out, live, piece > 0, left, align, st, g);
-            if (h) put16<T>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, st, v);
+            put16<T, sizeof(T) == 2>(out, live, piece > 0, left, align, st, g);
+            if (h) put16<T, sizeof(T) == 2>(h + static_cast<int64_t>(row) * ldh + c, live, piece > 0, left, align, st, v);
         }
     }
     copy_all();
@@ -480,8 +484,7 @@ struct SaveCall {
 };
 template <typename T, bool ALIGNED, int OP, int RND> gq_status run_save(const SaveCall& s) {
     auto k = save_kernel<T, ALIGNED, OP, RND>;
-    const size_t smem = kRing<T, ALIGNED> * kT * 16 * (sizeof(T) + (ALIGNED ? 0 : 1)) +
-                        (OP == kSave ? 0 : stage_bytes<T>(s.out));
+    const size_t smem = kRing<T, ALIGNED> * kT * 16 * (sizeof(T) + (ALIGNED ? 0 : 1));
     Walk a;
     const unsigned grid = plan_walk(k, smem, s.rows, s.cols, a);
     k<<<grid, kT, smem, s.st>>>(static_cast<const T*>(s.x), s.ldx, static_cast<T*>(s.h), s.ldh, s.out, a,
