@@ -223,22 +223,6 @@ __device__ __forceinline__ float sum2(F2 a) {
 
 // ---- the 8-bit block format ----------------------------------------------------------------
 
-// Largest magnitude of the 32-column block that 32 / V neighbouring lanes hold, as fp32 bits
-// (which order like the magnitudes, with NaN above infinity).  Every lane of the warp calls it.
-template <int V>
-__device__ __forceinline__ uint32_t block_top(const float (&v)[V]) {
-    uint32_t m = __float_as_uint(v[0]) & 0x7FFFFFFFu;
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    if constexpr (V == 1) {
-        m = __reduce_max_sync(kFull, m);
-    } else {
-#pragma unroll
-        for (int o = 1; o < kBlk / V; o *= 2) m = max(m, __shfl_xor_sync(kFull, m, o));
-    }
-    return m;
-}
-
 // The exponent byte: with a = 1.f * 2^k, a <= 127 * 2^(k - 6) iff 1.f <= 127 / 64, that is iff
 // the fraction field is at most 0x7E0000; adding 0x1FFFF carries into the exponent otherwise.
 __device__ __forceinline__ uint32_t exp_byte(uint32_t top) {
@@ -257,9 +241,10 @@ __device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_
     return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
 }
 
-// The same for 8 columns held as pairs: largest magnitude of the lane's 8 and of the block's 4
-// lanes.  Maxima of floating-point numbers pass over a NaN, so `plain` says that there is none
-// (and no infinity); otherwise the bits are compared.
+// Largest magnitude of the 32-column block that 4 neighbouring lanes hold, 8 columns each as pairs, as fp32
+// bits (which order like the magnitudes, with NaN above infinity).  Every lane of the warp calls it.
+// Maxima of floating-point numbers pass over a NaN, so `plain` says that there is none (and no
+// infinity); otherwise the bits are compared.
 __device__ __forceinline__ uint32_t block_top8(const F2 (&h)[4], bool plain) {
     float v[8];
 #pragma unroll
@@ -279,7 +264,10 @@ __device__ __forceinline__ uint32_t block_top8(const F2 (&h)[4], bool plain) {
     return max(m, __shfl_xor_sync(kFull, m, 2));
 }
 
-// Codes of 8 columns; r: their Philox call (not read when rounding to nearest).
+// Codes of 8 columns; r: their Philox call (not read when rounding to nearest).  Nearest: x / step + 1.5 *
+// 2^23 leaves the integer nearest to x / step, ties to even, in the low byte (one rounding, the product
+// is exact).  Random: x / step * 2^16 + 1.5 * 2^24 keeps 128 + x / step in units of 2^-15 in the
+// fraction; doubled and increased by the 16-bit random number, bits 16..23 hold floor(128 + x / step + u).
 template <bool RANDOM>
 __device__ __forceinline__ uint2 codes8(const F2 (&h)[4], uint32_t e, const uint4& r) {
     const F2 inv = f2(inv_step(e));
@@ -306,67 +294,23 @@ __device__ __forceinline__ uint2 codes8(const F2 (&h)[4], uint32_t e, const uint
     return w;
 }
 
-// Codes of V elements (V = 1: in the low byte).  Nearest: x / step + 1.5 * 2^23 leaves the integer
-// nearest to x / step, ties to even, in the low byte (one rounding, the product is exact).
-// Random: x / step * 2^16 + 1.5 * 2^24 keeps 128 + x / step in units of 2^-15 in the fraction;
-// doubled and increased by the 16-bit random number, bits 16..23 hold floor(128 + x / step + u).
-// c is the element's column (a multiple of V), row its row; pg the part of the random words
-// that depends on the columns (V = 16: of two calls).
-template <int V, bool RANDOM>
-__device__ __forceinline__ void codes_of(const float (&v)[V], uint32_t e, uint32_t row, uint32_t c,
-                                         const Rng& rng, const gq::PhiloxGroup (&pg)[(V + 7) / 8],
-                                         uint32_t (&w)[(V + 3) / 4]) {
-    const float inv = inv_step(e);
-    if constexpr (V == 1) {
-        if constexpr (RANDOM) {
-            const uint4 r = gq::philox_row(pg[0], row, rng.step_lo, rng.rk);
-            const uint32_t q = (c & 4) ? ((c & 2) ? r.w : r.z) : ((c & 2) ? r.y : r.x);
-            const uint32_t t = (__float_as_uint(__fmaf_rn(v[0] * inv, 65536.0f, 25165824.0f)) << 1) +
-                               ((c & 1) ? q >> 16 : q & 0xFFFFu);
-            w[0] = ((t >> 16) ^ 0x80u) & 0xFFu;
-        } else {
-            w[0] = __float_as_uint(__fmaf_rn(v[0], inv, 12582912.0f)) & 0xFFu;
-        }
-        if (e == 255u) w[0] = 0u;
-    } else {
-#pragma unroll
-        for (int g = 0; g < V / 8; ++g) {
-            F2 h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = f2(v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
-            uint4 r = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (RANDOM) r = gq::philox_row(pg[g], row, rng.step_lo, rng.rk);
-            const uint2 q = codes8<RANDOM>(h, e, r);
-            w[2 * g] = q.x;
-            w[2 * g + 1] = q.y;
-        }
-    }
-}
-
-// Quantises the V elements at column c of `row` and writes their codes, and the block's exponent
-// byte from its first lane.  Called by every lane of the warp; lanes with live = false (past the
-// last row) only take part in the reduction.  Columns past cols hold 0 and have code 0.
-template <int V, bool RANDOM>
-__device__ __forceinline__ void save(const float (&v)[V], bool live, uint32_t row, uint32_t c,
-                                     int64_t pitch, int64_t epitch, const Rng& rng,
-                                     const gq::PhiloxGroup (&pg)[(V + 7) / 8], int8_t* codes,
-                                     uint8_t* exps) {
-    const uint32_t e = exp_byte(block_top<V>(v));
-    uint32_t w[(V + 3) / 4];
-    codes_of<V, RANDOM>(v, e, row, c, rng, pg, w);
+// Codes and exponent of 8 columns of a row from column c on; `live`: they are to be stored.
+template <bool RANDOM>
+__device__ __forceinline__ void save8(const F2 (&h)[4], bool live, uint32_t row, uint32_t c, int64_t pitch,
+                                      int64_t epitch, const Rng& rng, int8_t* codes, uint8_t* exps) {
+    const uint32_t e = exp_byte(block_top8(h, false));
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (RANDOM)
+        r = gq::philox_row(gq::philox_group(c >> 3, rng.step_lo, rng.step_hi, rng.rk), row, rng.step_lo, rng.rk);
+    const uint2 q = codes8<RANDOM>(h, e, r);
     if (!live) return;
-    int8_t* p = codes + static_cast<int64_t>(row) * pitch + c;
-    if constexpr (V == 16)
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else if constexpr (V == 8)
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else
-        *p = static_cast<int8_t>(w[0]);
+    *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(row) * pitch + c) = q;
     if ((c & (kBlk - 1)) == 0)
         exps[static_cast<int64_t>(row) * epitch + (c >> 5)] = static_cast<uint8_t>(e);
 }
 
-// The values of 8 codes as pairs.
+// The values of 8 codes as pairs.  A code byte plus 128 in the low byte of the fp32 number 2^23 gives
+// 2^23 + 128 + code without a conversion instruction.
 __device__ __forceinline__ void values8(uint2 w, uint32_t e, F2 (&v)[4]) {
     const F2 s = f2(step_of(e)), off = f2(-8388736.0f);
     const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
@@ -430,43 +374,6 @@ __device__ __forceinline__ void store8(T* p, const F2 (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
     store<T, 8, 16>(p, 0, 8, o);
-}
-
-// What V codes stand for.  A code byte plus 128 in the low byte of the fp32 number 2^23 gives
-// 2^23 + 128 + code without a conversion instruction.
-template <int V>
-__device__ __forceinline__ void values_of(const uint32_t (&w)[(V + 3) / 4], uint32_t e,
-                                          float (&v)[V]) {
-    const float s = step_of(e);
-    if constexpr (V == 1) {
-        v[0] = static_cast<float>(static_cast<int8_t>(w[0])) * s;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const uint32_t u = w[i] ^ 0x80808080u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[4 * i + k] =
-                    (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + k)) - 8388736.0f) * s;
-        }
-    }
-}
-
-// The V saved values at column c of a row whose codes and exponents begin at p and pe.
-template <int V>
-__device__ __forceinline__ void saved(const int8_t* p, const uint8_t* pe, int64_t c,
-                                      float (&v)[V]) {
-    uint32_t w[(V + 3) / 4];
-    if constexpr (V == 16) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p + c));
-        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
-    } else if constexpr (V == 8) {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(p + c));
-        w[0] = t.x; w[1] = t.y;
-    } else {
-        w[0] = static_cast<uint8_t>(p[c]);
-    }
-    values_of<V>(w, pe[c >> 5], v);
 }
 
 // p + row * ld elements, in one multiplication: rows and their distance in bytes fit 32 bits each.

@@ -11,8 +11,8 @@
 // and 50; backward 59 from x and 61 from codes, of which it needs 59 and 50).  A row stays in
 // registers between its reductions, so it is read once ("rows held by fixed threads"); the generic
 // kernels take rows of more columns than a block holds, and read again what does not fit their registers
-// (from L2, mostly).  That form costs 2 to 3 times as much (4,096 x 8,192 bf16 forward 37 us held, 3,640 x
-// 9,216 as many bytes in 93), and rows of it that are not aligned are read element by element (142 us).
+// (from L2, mostly).  That form costs more: as many bytes in 4,096 x 8,192 and 4,092 x 8,200 bf16 take 37
+// and 68 us forward, 44 and 129 backward from codes (whose columns' sums are a second kernel there).
 // All sums are fp32.
 #pragma once
 #include "gq_act.cuh"
@@ -190,6 +190,58 @@ __device__ __forceinline__ void put8(T* row, uint32_t col, bool in, uint32_t fir
             const uint32_t c = i * 32 + lane;
             if (first + c < cols) down(square[(c >> 3) * 9 + (c & 7)], row[first + c]);
         }
+    }
+}
+
+// ---- longer rows: 8 columns straight from memory --------------------------------------------
+// How many of the 8 columns from c on lie in the row.
+__device__ __forceinline__ int left_of(int64_t c, int64_t cols) {
+    return static_cast<int>(min(max(cols - c, int64_t(0)), int64_t(8)));
+}
+// Sets those behind the row's end to 0.
+__device__ __forceinline__ void cut8(F2 (&v)[4], int left) {
+    if (left >= 8) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x, y;
+        split(v[i], x, y);
+        v[i] = f2(2 * i < left ? x : 0.0f, 2 * i + 1 < left ? y : 0.0f);
+    }
+}
+// 8 columns of a row, 0 behind its end; rows that are not aligned by the 16-byte granules that hold them.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t cols, F2 (&v)[4]) {
+    constexpr int P = sizeof(T) / 2 + (ALIGNED ? 0 : 1);
+    const int left = left_of(c, cols);
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(row + c);
+    const uint32_t m = ALIGNED ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 15u;
+    const int bytes = left > 0 ? static_cast<int>(m) + left * static_cast<int>(sizeof(T)) : 0;
+    uint32_t r[4 * P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const uint4 g = 16 * i < bytes ? __ldg(reinterpret_cast<const uint4*>(q - m) + i)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+        r[4 * i] = g.x; r[4 * i + 1] = g.y; r[4 * i + 2] = g.z; r[4 * i + 3] = g.w;
+    }
+    pairs(shifted<T, ALIGNED>(r, m, left), v);
+}
+// Stores them; `first` is the warp's first column, the whole warp takes part.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void put_row(T* row, int64_t c, int64_t first, int64_t cols, float* square,
+                                        const F2 (&v)[4]) {
+    if constexpr (ALIGNED) {
+        if (c + 8 <= cols) {
+            store8(row + c, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float e[2];
+                split(v[i / 2], e[0], e[1]);
+                if (c + i < cols) down(e[i % 2], row[c + i]);
+            }
+        }
+    } else {
+        put8<T, false>(row, 0u, false, static_cast<uint32_t>(first), static_cast<uint32_t>(cols), square, v);
     }
 }
 

@@ -21,116 +21,121 @@ template <typename T> struct Source {
     const float* mean;
 };
 
-template <typename T, int V, bool CODES>
+template <typename T, bool ALIGNED, bool CODES>
 __device__ __forceinline__ void hat_of(const Source<T>& src, const Shape& s, int64_t row, float mean,
-                                       float rstd, int64_t c, float (&v)[V]) {
+                                       float rstd, int64_t c, F2 (&v)[4]) {
     if constexpr (CODES) {
         if (c < s.pitch) {
-            saved<V>(src.codes + row * s.pitch, src.exps + row * s.epitch, c, v);
-            if (c + V > s.cols) {  // a block marked 255 reads as NaN in the padding too
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i >= s.cols) v[i] = 0.0f;
-            }
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(src.codes + row * s.pitch + c));
+            values8(q, src.exps[row * s.epitch + (c >> 5)], v);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 4; ++i) v[i] = f2(0.0f);
         }
     } else {
-        load<T, V>(src.x + row * src.ldx, c, s.cols, v);
+        load8<T, ALIGNED>(src.x + row * src.ldx, c, s.cols, v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = c + i < s.cols ? (v[i] - mean) * rstd : 0.0f;
+        for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-mean)), f2(rstd));
     }
+    cut8(v, left_of(c, s.cols));  // a block marked 255 reads as NaN in the padding too
 }
 
-// dx of rows of more columns than the held form takes: a block per row.
-template <typename T, int V, int VPT, bool CODES>
-__global__ void __launch_bounds__(512)
+// dx of rows of more columns than the held form takes: a block per row, as in the forward pass.  4,092 x
+// 8,200 bf16 from codes with the columns' sums below: 129 us with two blocks per SM, 171 with one (84
+// registers a thread), 144 with three and nothing kept in registers between the two passes.
+template <typename T, bool ALIGNED, int VPT, bool CODES>
+__global__ void __launch_bounds__(512, 2)
     backward_kernel(const T* __restrict__ dy, int64_t lddy, Shape s, const void* w, int wide,
                     const float* __restrict__ rstd_in, Source<T> src, T* __restrict__ dx,
                     int64_t lddx) {
     __shared__ float buf[32][2];
-    const int threads = blockDim.x, t = threadIdx.x;
-    const int64_t step = static_cast<int64_t>(threads) * V;
-    const int64_t beyond = step * VPT, row = blockIdx.x;
+    __shared__ float squares[ALIGNED ? 1 : 16 * kSquare];
+    const int threads = blockDim.x, t = threadIdx.x, lane = t & 31;
+    float* const square = squares + (ALIGNED ? 0 : t / 32 * kSquare);
+    const int64_t step = static_cast<int64_t>(threads) * 8, row = blockIdx.x;
+    const int64_t mine = (t - lane) * 8, beyond = step * VPT + mine;
 
     const T* dyr = dy + row * lddy;
     T* dxr = dx + row * lddx;
     const float rstd = rstd_in[row];
     const float mean = CODES ? 0.0f : src.mean[row];
-    float g[VPT][V], h[VPT][V];
+    F2 c1 = f2(0.0f), c2 = f2(0.0f);
+    auto fetch = [&](int64_t c, F2 (&g)[4], F2 (&h)[4]) {  // w dy and xh
+        load8<T, ALIGNED>(dyr, c, s.cols, g);
+        hat_of<T, ALIGNED, CODES>(src, s, row, mean, rstd, c, h);
+        F2 wv[4];
+        vec8(w, wide & 1, wide >> 1, 1.0f, c, s.cols, wv);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        load<T, V>(dyr, k * step + t * V, s.cols, g[k]);
-        hat_of<T, V, CODES>(src, s, row, mean, rstd, k * step + t * V, h[k]);
-    }
-    float c[2] = {0.0f, 0.0f};
+        for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], wv[i]);
+    };
+    auto add = [&](const F2 (&g)[4], const F2 (&h)[4]) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        float wv[V];
-        vec_of<V>(w, wide & 1, 1.0f, k * step + t * V, s.cols, wv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            g[k][i] *= wv[i];
-            c[0] += g[k][i];
-            c[1] = fmaf(g[k][i], h[k][i], c[1]);
+        for (int i = 0; i < 4; ++i) {
+            c1 = add2(c1, g[i]);
+            c2 = fma2(g[i], h[i], c2);
         }
+    };
+    F2 g[VPT][4], h[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) fetch(k * step + t * 8, g[k], h[k]);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) add(g[k], h[k]);
+    for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
+        F2 a[4], b[4];
+        fetch(c0 + lane * 8, a, b);
+        add(a, b);
     }
-    for (int64_t col = beyond + t * V; col < s.cols; col += step) {
-        float a[V], b[V], wv[V];
-        load<T, V>(dyr, col, s.cols, a);
-        hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
-        vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
+    float m[2] = {sum2(c1), sum2(c2)};
+    row_sum(m, buf, threads);
+    const F2 m1 = f2(-m[0] * s.inv_cols), m2 = f2(-m[1] * s.inv_cols), rs = f2(rstd);
+    auto finish = [&](int64_t first, F2 (&a)[4], const F2 (&b)[4]) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            a[i] *= wv[i];
-            c[0] += a[i];
-            c[1] = fmaf(a[i], b[i], c[1]);
-        }
-    }
-    row_sum(c, buf, threads);
-    const float c1 = c[0] * s.inv_cols, c2 = c[1] * s.inv_cols;
+        for (int i = 0; i < 4; ++i) a[i] = mul2(add2(a[i], fma2(b[i], m2, m1)), rs);
+        put_row<T, ALIGNED>(dxr, first + lane * 8, first, s.cols, square, a);
+    };
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int64_t col = k * step + t * V;
-        if (col < s.cols) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                g[k][i] = (g[k][i] - fmaf(h[k][i], c2, c1)) * rstd;
-            store<T, V, 16>(dxr, col, s.cols, g[k]);
-        }
-    }
-    for (int64_t col = beyond + t * V; col < s.cols; col += step) {
-        float a[V], b[V], wv[V];
-        load<T, V>(dyr, col, s.cols, a);
-        hat_of<T, V, CODES>(src, s, row, mean, rstd, col, b);
-        vec_of<V>(w, wide & 1, 1.0f, col, s.cols, wv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = (a[i] * wv[i] - fmaf(b[i], c2, c1)) * rstd;
-        store<T, V, 16>(dxr, col, s.cols, a);
+    for (int k = 0; k < VPT; ++k)
+        if (k * step + mine < s.cols) finish(k * step + mine, g[k], h[k]);
+    for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
+        F2 a[4], b[4];
+        fetch(c0 + lane * 8, a, b);
+        finish(c0, a, b);
     }
 }
 
-// Column sums for rows that do not fit the registers: thread = column, blockIdx.y = a share of
+// Column sums for rows that do not fit the registers: thread = 8 columns, blockIdx.y = a share of
 // the rows; partial[blockIdx.y][0 and 1][cols].
-template <typename T, bool CODES>
-__global__ void __launch_bounds__(256)
+template <typename T, bool ALIGNED, bool CODES>
+__global__ void __launch_bounds__(128)
     columns_kernel(const T* __restrict__ dy, int64_t lddy, Shape s,
                    const float* __restrict__ rstd_in, Source<T> src, float* __restrict__ partial) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (col >= s.cols) return;
-    float aw = 0.0f, ab = 0.0f;
-#pragma unroll 4
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * 8;
+    if (c >= s.cols) return;
+    F2 aw[4], ab[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) aw[i] = ab[i] = f2(0.0f);
+#pragma unroll 2
     for (int64_t row = blockIdx.y; row < s.rows; row += gridDim.y) {
-        const float g = up(dy[row * lddy + col]);
-        float h[1];
-        hat_of<T, 1, CODES>(src, s, row, CODES ? 0.0f : src.mean[row], rstd_in[row], col, h);
-        aw = fmaf(g, h[0], aw);
-        ab += g;
+        F2 g[4], h[4];
+        load8<T, ALIGNED>(dy + row * lddy, c, s.cols, g);
+        hat_of<T, ALIGNED, CODES>(src, s, row, CODES ? 0.0f : src.mean[row], rstd_in[row], c, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            aw[i] = fma2(g[i], h[i], aw[i]);
+            ab[i] = add2(ab[i], g[i]);
+        }
     }
-    float* p = partial + static_cast<int64_t>(blockIdx.y) * 2 * s.cols + col;
-    p[0] = aw;
-    p[s.cols] = ab;
+    float* p = partial + static_cast<int64_t>(blockIdx.y) * 2 * s.cols + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float u[2], d[2];
+        split(aw[i / 2], u[0], u[1]);
+        split(ab[i / 2], d[0], d[1]);
+        if (c + i < s.cols) {
+            p[i] = u[i % 2];
+            p[s.cols + i] = d[i % 2];
+        }
+    }
 }
 
 // Adds the partial rows: 32 columns x 32 shares of the rows per block.
@@ -354,10 +359,15 @@ template <typename T, bool ALIGNED, bool CODES> struct BackwardHeld {
         return grid;
     }
 };
-template <typename T, int V, int VPT, bool CODES> void backward_generic(const BackwardCall<T>& a) {
-    const int threads = threads_for(a.s.cols, V * VPT, 128, 512);
-    backward_kernel<T, V, VPT, CODES><<<static_cast<unsigned>(a.s.rows), threads, 0, a.st>>>(
+template <typename T, bool ALIGNED, bool CODES>
+void backward_generic(const BackwardCall<T>& a, int parts, bool sums) {
+    constexpr int VPT = 2;
+    const int threads = threads_for(a.s.cols, 8 * VPT, 128, 512);
+    backward_kernel<T, ALIGNED, VPT, CODES><<<static_cast<unsigned>(a.s.rows), threads, 0, a.st>>>(
         a.dy, a.lddy, a.s, a.w, a.wide, a.rstd, a.src, a.dx, a.lddx);
+    const dim3 grid(static_cast<unsigned>((a.s.cols + 1023) / 1024), static_cast<unsigned>(parts));
+    if (sums)
+        columns_kernel<T, ALIGNED, CODES><<<grid, 128, 0, a.st>>>(a.dy, a.lddy, a.s, a.rstd, a.src, a.partial);
 }
 
 template <typename T, bool CODES>
@@ -371,12 +381,9 @@ gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype,
         parts = vec && cols % 8 == 0 ? held_switch(h, BackwardHeld<T, true, CODES>{a, h})
                                      : held_switch(h, BackwardHeld<T, false, CODES>{a, h});
     } else {
-        if (vec) backward_generic<T, 8, 2, CODES>(a);
-        else backward_generic<T, 1, 8, CODES>(a);
-        parts = static_cast<int>((a.s.rows + 7) / 8 < 64 ? (a.s.rows + 7) / 8 : 64);
-        const dim3 grid(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(parts));
-        if (dw || db)
-            columns_kernel<T, CODES><<<grid, 256, 0, a.st>>>(a.dy, a.lddy, a.s, a.rstd, a.src, a.partial);
+        parts = static_cast<int>((a.s.rows + 7) / 8 < 128 ? (a.s.rows + 7) / 8 : 128);
+        if (vec) backward_generic<T, true, CODES>(a, parts, dw || db);
+        else backward_generic<T, false, CODES>(a, parts, dw || db);
     }
     if (cudaPeekAtLastError() == cudaSuccess && (dw || db)) {
         cudaLaunchConfig_t cfg = {};

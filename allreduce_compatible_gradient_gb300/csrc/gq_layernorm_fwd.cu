@@ -6,58 +6,65 @@ using namespace gqa;
 namespace {
 
 // Rows of more columns than the held form takes: a block per row, thread t of its `threads` takes the
-// pieces of V columns t, t + threads, ...: the first VPT of them in registers.  The loops run to the code pitch, and past it to a whole number of pieces
-// per warp, so that every lane takes part in the block reductions of the checkpoint.
-template <typename T, int V, int VPT, int RND>
-__global__ void __launch_bounds__(512)
+// pieces of 8 columns t, t + threads, ...: the first VPT of them in registers.  Warps go on as long as one
+// of their lanes has a column, so that all take part in the checkpoint's reductions.  Rows that are not
+// aligned take the same pieces by granules (2,730 x 12,289 bf16 with random codes: 85 us, element by
+// element 218); two blocks per SM (one, with 84 registers a thread: 111).
+template <typename T, bool ALIGNED, int VPT, int RND>
+__global__ void __launch_bounds__(512, 2)
     forward_kernel(const T* __restrict__ x, int64_t ldx, Shape s, Affine af, float eps,
                    T* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
                    float* __restrict__ rstd_out, int8_t* __restrict__ codes,
                    uint8_t* __restrict__ exps, Rng rng) {
     __shared__ float buf[2][32][1];
-    const int threads = blockDim.x, t = threadIdx.x;
+    __shared__ float squares[ALIGNED ? 1 : 16 * kSquare];
+    const int threads = blockDim.x, t = threadIdx.x, lane = t & 31;
+    float* const square = squares + (ALIGNED ? 0 : t / 32 * kSquare);
     const int64_t row = blockIdx.x;
     const T* xr = x + row * ldx;
     T* yr = y + row * ldy;
-    const int64_t step = static_cast<int64_t>(threads) * V;
-    const int64_t beyond = step * VPT;  // first column that is not in registers
+    const int64_t step = static_cast<int64_t>(threads) * 8;
+    const int64_t mine = (t - lane) * 8;           // the warp's first column
+    const int64_t beyond = step * VPT + mine;  // that of its first piece that is not in registers
 
-    float v[VPT][V];
-    float sum[1] = {0.0f};
+    F2 v[VPT][4];
+    F2 acc = f2(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        load<T, V>(xr, k * step + t * V, s.cols, v[k]);
+        load8<T, ALIGNED>(xr, k * step + t * 8, s.cols, v[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[0] += v[k][i];
+        for (int i = 0; i < 4; ++i) acc = add2(acc, v[k][i]);
     }
-    for (int64_t c = beyond + t * V; c < s.cols; c += step) {
-        float z[V];
-        load<T, V>(xr, c, s.cols, z);
+    for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
+        F2 z[4];
+        load8<T, ALIGNED>(xr, c0 + lane * 8, s.cols, z);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[0] += z[i];
+        for (int i = 0; i < 4; ++i) acc = add2(acc, z[i]);
     }
+    float sum[1] = {sum2(acc)};
     row_sum(sum, buf[0], threads);
     const float mean = sum[0] * s.inv_cols;
 
-    float sq[1] = {0.0f};
+    auto centre = [&](F2 (&z)[4], int64_t c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = add2(z[i], f2(-mean));
+        cut8(z, left_of(c, s.cols));
+    };
+    acc = f2(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int64_t c = k * step + t * V;
+        centre(v[k], k * step + t * 8);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[k][i] = c + i < s.cols ? v[k][i] - mean : 0.0f;
-            sq[0] = fmaf(v[k][i], v[k][i], sq[0]);
-        }
+        for (int i = 0; i < 4; ++i) acc = fma2(v[k][i], v[k][i], acc);
     }
-    for (int64_t c = beyond + t * V; c < s.cols; c += step) {
-        float z[V];
-        load<T, V>(xr, c, s.cols, z);
+    for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
+        F2 z[4];
+        load8<T, ALIGNED>(xr, c0 + lane * 8, s.cols, z);
+        centre(z, c0 + lane * 8);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float d = c + i < s.cols ? z[i] - mean : 0.0f;
-            sq[0] = fmaf(d, d, sq[0]);
-        }
+        for (int i = 0; i < 4; ++i) acc = fma2(z[i], z[i], acc);
     }
+    float sq[1] = {sum2(acc)};
     row_sum(sq, buf[1], threads);
     const float rstd = rsqrtf(__fmul_rn(sq[0], s.inv_cols) + eps);  // within 2 units
     if (t == 0) {
@@ -65,36 +72,28 @@ __global__ void __launch_bounds__(512)
         rstd_out[row] = rstd;
     }
 
-    auto finish = [&](int64_t c, float (&z)[V]) {  // z: x - mean
+    auto finish = [&](int64_t first, F2 (&z)[4]) {  // z: x - mean
+        const int64_t c = first + lane * 8;
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = z[i] * rstd;
+        for (int i = 0; i < 4; ++i) z[i] = mul2(z[i], f2(rstd));
         if constexpr (RND >= 0)
-        {
-            gq::PhiloxGroup pg[1];
-            if constexpr (RND == 1)
-                pg[0] = gq::philox_group(static_cast<uint32_t>(c >> 3), rng.step_lo, rng.step_hi, rng.rk);
-            save<V, RND == 1>(z, c < s.pitch, static_cast<uint32_t>(row), static_cast<uint32_t>(c),
-                              s.pitch, s.epitch, rng, pg, codes, exps);
-        }
-        if (c < s.cols) {
-            float w[V], b[V];
-            vec_of<V>(af.w, af.wide, 1.0f, c, s.cols, w);
-            vec_of<V>(af.b, af.wide, 0.0f, c, s.cols, b);
+            save8<RND == 1>(z, c < s.pitch, static_cast<uint32_t>(row), static_cast<uint32_t>(c), s.pitch,
+                            s.epitch, rng, codes, exps);
+        F2 w[4], b[4];
+        vec8(af.w, af.wide, af.aligned, 1.0f, c, s.cols, w);
+        vec8(af.b, af.wide, af.aligned, 0.0f, c, s.cols, b);
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = fmaf(z[i], w[i], b[i]);
-            store<T, V, 16>(yr, c, s.cols, z);
-        }
+        for (int i = 0; i < 4; ++i) z[i] = fma2(z[i], w[i], b[i]);
+        put_row<T, ALIGNED>(yr, c, first, s.cols, square, z);
     };
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-        if (k * step < s.cols) finish(k * step + t * V, v[k]);
+        if (k * step + mine < s.cols) finish(k * step + mine, v[k]);
     for (int64_t c0 = beyond; c0 < s.cols; c0 += step) {
-        const int64_t c = c0 + t * V;
-        float z[V];
-        load<T, V>(xr, c, s.cols, z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = c + i < s.cols ? z[i] - mean : 0.0f;
-        finish(c, z);
+        F2 z[4];
+        load8<T, ALIGNED>(xr, c0 + lane * 8, s.cols, z);
+        centre(z, c0 + lane * 8);
+        finish(c0, z);
     }
 }
 
@@ -230,10 +229,10 @@ struct ForwardCall {
     cudaStream_t st;
 };
 
-template <typename T, int V, int VPT, int RND>
+template <typename T, bool ALIGNED, int VPT, int RND>
 gq_status forward_generic(const ForwardCall<T>& a) {
-    const int threads = threads_for(a.s.cols, V * VPT, 128, 512);
-    forward_kernel<T, V, VPT, RND><<<static_cast<unsigned>(a.s.rows), threads, 0, a.st>>>(
+    const int threads = threads_for(a.s.cols, 8 * VPT, 128, 512);
+    forward_kernel<T, ALIGNED, VPT, RND><<<static_cast<unsigned>(a.s.rows), threads, 0, a.st>>>(
         a.x, a.ldx, a.s, a.af, a.eps, a.y, a.ldy, a.mean, a.rstd, a.codes, a.exps, a.rng);
     return gqh::launch_status();
 }
@@ -256,7 +255,7 @@ template <typename T, bool ALIGNED, int RND> struct ForwardHeld {
 template <typename T, int RND>
 gq_status forward_any(const ForwardCall<T>& a, bool vec) {
     if (!held_ok(a.s.cols, (a.ldx > a.ldy ? a.ldx : a.ldy) * sizeof(T)))
-        return vec ? forward_generic<T, 8, 4, RND>(a) : forward_generic<T, 1, 8, RND>(a);
+        return vec ? forward_generic<T, true, 4, RND>(a) : forward_generic<T, false, 4, RND>(a);
     const Held h = held_for(a.s.rows, a.s.cols);
     return vec && a.s.cols % 8 == 0 ? held_switch(h, ForwardHeld<T, true, RND>{a, h})
                                     : held_switch(h, ForwardHeld<T, false, RND>{a, h});
