@@ -71,7 +71,7 @@ class Act8:
     exponent byte per 32 columns (rows x round_up(ceil(cols / 32), 16)); `shape` is that of the
     tensor it was made from."""
 
-    __slots__ = ("shape", "_parts", "_data", "_at")
+    __slots__ = ("shape", "_cols", "_codes", "_exps")
 
     def __init__(self, codes: torch.Tensor, exps: torch.Tensor, cols: int, shape=None):
         rows = codes.shape[0] if codes.dim() == 2 else -1
@@ -87,50 +87,49 @@ class Act8:
         if not codes.is_cuda or codes.get_device() != exps.get_device():
             raise ValueError("codes and exponents must be on one CUDA device")
         self.shape = (rows, cols) if shape is None else tuple(shape)
-        self._parts, self._data = (codes, exps), None
-        # addresses of codes and exponents, rows, columns, device: what the calls take
-        self._at = (codes.data_ptr(), exps.data_ptr(), rows, cols, codes.get_device())
+        self._cols, self._codes, self._exps = cols, codes, exps
 
     @classmethod
-    def _made(cls, data, at, shape):
-        """One that a call has written: codes, then exponents, in one allocation."""
+    def _made(cls, data, cols, shape):
+        """One that a call has written: codes, then exponents, in one allocation (bytes, a row each of
+        the codes' and the exponents' pitch)."""
         self = cls.__new__(cls)
-        self.shape, self._parts, self._data, self._at = shape, None, data, at
+        self.shape, self._cols, self._codes, self._exps = shape, cols, data, None
         return self
 
     @property
     def rows(self) -> int:
-        return self._at[2]
+        return self._codes.shape[0]
 
     @property
     def cols(self) -> int:
-        return self._at[3]
+        return self._cols
 
     @property
     def codes(self) -> torch.Tensor:
-        return self._views()[0]
+        if self._exps is not None:
+            return self._codes
+        pitch = _pitches(self._cols)[0]
+        return self._codes.view(-1)[:self.rows * pitch].view(torch.int8).view(self.rows, pitch)
 
     @property
     def exps(self) -> torch.Tensor:
-        return self._views()[1]
-
-    def _views(self):
-        if self._parts is None:
-            pitch, epitch = _pitches(self.cols)
-            n = self.rows * pitch
-            self._parts = (self._data[:n].view(torch.int8).view(self.rows, pitch),
-                           self._data[n:].view(self.rows, epitch))
-        return self._parts
+        if self._exps is not None:
+            return self._exps
+        pitch, epitch = _pitches(self._cols)
+        return self._codes.view(-1)[self.rows * pitch:].view(self.rows, epitch)
 
     @property
     def nbytes(self) -> int:
-        return self.rows * sum(_pitches(self.cols))
+        return self.rows * sum(_pitches(self._cols))
 
 
 def _place_of(act):
+    """What the calls take of a checkpoint: its tensors, whose addresses they read themselves, so that a
+    copy, or new storage, is never read at an old address."""
     if type(act) is not Act8:
         raise TypeError("act must be an Act8")
-    return act._at
+    return act._codes, act._exps, act._cols
 
 
 def _form(approximate: str) -> int:
@@ -156,8 +155,7 @@ def gq_act_quantize(x, seed=None, step=0, stream=None) -> Act8:
     """8-bit checkpoint of x: rounded to nearest (seed None), or at random without bias."""
     if stream is not None:
         return _on(stream, gq_act_quantize, x, seed, step)
-    data, *at = _native.act_quantize(x, seed, step)
-    return Act8._made(data, at, x.shape)
+    return Act8._made(_native.act_quantize(x, seed, step), x.shape[-1], x.shape)
 
 
 def gq_act_dequantize(act, out=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
@@ -173,8 +171,8 @@ def gq_layernorm_forward(x, weight=None, bias=None, eps=1e-5, checkpoint=True, s
     normalised rows (None with checkpoint=False)."""
     if stream is not None:
         return _on(stream, gq_layernorm_forward, x, weight, bias, eps, checkpoint, seed, step)
-    y, mean, rstd, data, *at = _native.layernorm_forward(x, weight, bias, eps, checkpoint, seed, step)
-    return y, mean, rstd, None if data is None else Act8._made(data, at, x.shape)
+    y, mean, rstd, data = _native.layernorm_forward(x, weight, bias, eps, checkpoint, seed, step)
+    return y, mean, rstd, None if data is None else Act8._made(data, x.shape[-1], x.shape)
 
 
 def gq_layernorm_backward(dy, weight, rstd, act=None, x=None, mean=None, grad_dtype=torch.float32,
@@ -183,7 +181,7 @@ def gq_layernorm_backward(dy, weight, rstd, act=None, x=None, mean=None, grad_dt
     dweight and dbias are of grad_dtype (float32 or bfloat16)."""
     if stream is not None:
         return _on(stream, gq_layernorm_backward, dy, weight, rstd, act, x, mean, grad_dtype, ws)
-    at = (None,) * 5 if act is None else _place_of(act)
+    at = (None,) * 3 if act is None else _place_of(act)
     return _native.layernorm_backward(dy, weight, rstd, *at, x, mean, _OUT_TYPES.get(grad_dtype, -1), ws)
 
 
@@ -192,8 +190,8 @@ def gq_gelu_forward(u, approximate="none", checkpoint=True, seed=None, step=0, s
     u (None with checkpoint=False)."""
     if stream is not None:
         return _on(stream, gq_gelu_forward, u, approximate, checkpoint, seed, step)
-    h, data, *at = _native.gelu_forward(u, _form(approximate), checkpoint, seed, step)
-    return h, None if data is None else Act8._made(data, at, u.shape)
+    h, data = _native.gelu_forward(u, _form(approximate), checkpoint, seed, step)
+    return h, None if data is None else Act8._made(data, u.shape[-1], u.shape)
 
 
 def gq_gelu_backward(dh, act, approximate="none", need_output=False, stream=None):

@@ -174,30 +174,51 @@ at::ScalarType scalar_of(int code) {
     return code == GQ_F32 ? at::kFloat : code == GQ_BF16 ? at::kBFloat16 : at::kHalf;
 }
 
-// A checkpoint as the package passes it: (codes address, exponents address, rows, cols, device).
+// A checkpoint as the package passes it: (codes, exponents, columns), or (bytes, None, columns) with the
+// codes and behind them the exponents of all rows in one tensor.  Addresses are taken from the tensors at
+// every call, and what the tensors hold is checked against the size: their storage may have been replaced.
 struct Saved {
     const int8_t* codes = nullptr;
     const uint8_t* exps = nullptr;
     int64_t rows = 0, cols = 0;
     int index = 0;
-    explicit Saved(PyObject* const* a)
-        : codes(static_cast<const int8_t*>(PyLong_AsVoidPtr(a[0]))),
-          exps(static_cast<const uint8_t*>(PyLong_AsVoidPtr(a[1]))), rows(signed64(a[2])),
-          cols(signed64(a[3])), index(static_cast<int>(signed64(a[4]))) {}
+    explicit Saved(PyObject* const* a) : cols(signed64(a[2])) {
+        const at::Tensor& c = tensor(a[0], "the checkpoint");
+        if (cols < 1 || cols >= int64_t(1) << 31) refuse(PyExc_ValueError, "the checkpoint has no columns");
+        const int64_t pitch = (cols + 31) / 32 * 32, epitch = (pitch / 32 + 15) / 16 * 16;
+        const bool apart = a[1] != Py_None;
+        holds(c, apart ? pitch : pitch + epitch);
+        index = c.get_device();
+        rows = c.size(0);
+        codes = static_cast<const int8_t*>(c.data_ptr());
+        exps = reinterpret_cast<const uint8_t*>(codes) + rows * pitch;
+        if (apart) {
+            const at::Tensor& e = tensor(a[1], "the checkpoint's exponents");
+            holds(e, epitch);
+            if (e.get_device() != index || e.size(0) != rows)
+                refuse(PyExc_ValueError, "the checkpoint's exponents are not those of its codes");
+            exps = static_cast<const uint8_t*>(e.data_ptr());
+        }
+    }
+    static void holds(const at::Tensor& t, int64_t pitch) {
+        if (!t.is_cuda() || t.dim() != 2 || t.size(1) != pitch || t.element_size() != 1 || !t.is_contiguous())
+            refuse(PyExc_ValueError, "the checkpoint must be contiguous rows of %lld bytes on a CUDA device",
+                   static_cast<long long>(pitch));
+    }
     void covers(int64_t r, int64_t c, int i) const {
         if (rows != r || (c >= 0 && cols != c) || index != i)
             refuse(PyExc_ValueError, "the checkpoint holds %lld x %lld on cuda:%d",
                    static_cast<long long>(rows), static_cast<long long>(cols), index);
     }
 };
-// A new one: codes, then exponents, in one allocation.
+// A new one.
 struct NewSaved {
     at::Tensor data;
     int8_t* codes = nullptr;
     uint8_t* exps = nullptr;
     void make(int64_t rows, int64_t cols, int index) {
         const int64_t pitch = (cols + 31) / 32 * 32, epitch = (pitch / 32 + 15) / 16 * 16;
-        data = empty({rows * (pitch + epitch)}, at::kByte, index);
+        data = empty({rows, pitch + epitch}, at::kByte, index);
         codes = static_cast<int8_t*>(data.data_ptr());
         exps = reinterpret_cast<uint8_t*>(codes) + rows * pitch;
     }
@@ -230,7 +251,7 @@ void count(Py_ssize_t have, Py_ssize_t want) {
     if (have != want) refuse(PyExc_TypeError, "%zd arguments, %zd expected", have, want);
 }
 
-// (x, seed, step) -> (data, codes, exps, rows, cols, device)
+// (x, seed, step) -> data
 PyObject* act_quantize(PyObject* const* a, Py_ssize_t n) {
     count(n, 3);
     const at::Tensor& x = tensor(a[0], "x");
@@ -242,26 +263,25 @@ PyObject* act_quantize(PyObject* const* a, Py_ssize_t n) {
     check(api.act_quantize(m.p, m.code, m.rows, m.cols, m.ld, r.mode, r.seed, r.step, s.codes, s.exps,
                            at.stream),
           "gq_act_quantize");
-    return Py_BuildValue("NNNLLi", wrap(s.data), PyLong_FromVoidPtr(s.codes), PyLong_FromVoidPtr(s.exps),
-                         static_cast<long long>(m.rows), static_cast<long long>(m.cols), m.index);
+    return wrap(s.data);
 }
 
-// (checkpoint x 5, shape, out or None, type code) -> out
+// (checkpoint x 3, shape, out or None, type code) -> out
 PyObject* act_dequantize(PyObject* const* a, Py_ssize_t n) {
-    count(n, 8);
+    count(n, 6);
     const Saved s(a);
     const Place at(s.index);
     at::Tensor out;
-    if (a[6] == Py_None) {
-        const int64_t c = signed64(a[7]);
+    if (a[4] == Py_None) {
+        const int64_t c = signed64(a[5]);
         if (c != GQ_F32 && c != GQ_BF16 && c != GQ_F16)
             refuse(PyExc_TypeError, "values are float32, bfloat16 or float16");
         c10::SmallVector<int64_t, 8> shape;
-        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[5]); ++i)
-            shape.push_back(signed64(PyTuple_GET_ITEM(a[5], i)));
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[3]); ++i)
+            shape.push_back(signed64(PyTuple_GET_ITEM(a[3], i)));
         out = empty(shape, scalar_of(static_cast<int>(c)), s.index);
     } else {
-        out = tensor(a[6], "out");
+        out = tensor(a[4], "out");
     }
     const Matrix m = matrix(out, "out", true);
     if (m.rows != s.rows || m.cols != s.cols || m.index != s.index)
@@ -273,7 +293,7 @@ PyObject* act_dequantize(PyObject* const* a, Py_ssize_t n) {
 }
 
 // (x, weight, bias, eps, checkpoint, seed, step)
-//   -> (y, mean, rstd, data or None, codes, exps, rows, cols, device)
+//   -> (y, mean, rstd, data or None)
 PyObject* layernorm_forward(PyObject* const* a, Py_ssize_t n) {
     count(n, 7);
     const at::Tensor& x = tensor(a[0], "x");
@@ -295,24 +315,22 @@ PyObject* layernorm_forward(PyObject* const* a, Py_ssize_t n) {
                                 static_cast<float*>(mean.data_ptr()), static_cast<float*>(rstd.data_ptr()),
                                 r.mode, r.seed, r.step, s.codes, s.exps, at.stream),
           "gq_layernorm_forward");
-    return Py_BuildValue("NNNNNNLLi", wrap(y), wrap(mean), wrap(rstd), wrap(s.data),
-                         PyLong_FromVoidPtr(s.codes), PyLong_FromVoidPtr(s.exps),
-                         static_cast<long long>(m.rows), static_cast<long long>(m.cols), m.index);
+    return Py_BuildValue("NNNN", wrap(y), wrap(mean), wrap(rstd), wrap(s.data));
 }
 
-// (dy, weight, rstd, checkpoint x 5 or None x 5, x or None, mean or None, type code, ws or None)
+// (dy, weight, rstd, checkpoint x 3 or None x 3, x or None, mean or None, type code, ws or None)
 //   -> (dx, dweight, dbias)
 PyObject* layernorm_backward(PyObject* const* a, Py_ssize_t n) {
-    count(n, 12);
+    count(n, 10);
     const at::Tensor& dy = tensor(a[0], "dy");
     const Matrix m = matrix(dy, "dy");
     int wcode = -1;
     const void* w = vector(a[1], m.cols, m.index, &wcode, "weight");
     const float* rstd = floats(a[2], m.rows, m.index, "rstd");
     const bool saved = a[3] != Py_None;
-    if (saved == (a[8] != Py_None) || (a[8] == Py_None) != (a[9] == Py_None))
+    if (saved == (a[6] != Py_None) || (a[6] == Py_None) != (a[7] == Py_None))
         refuse(PyExc_ValueError, "give either act, or x and mean");
-    const int gcode = output_code(a[10], "grad_dtype");
+    const int gcode = output_code(a[8], "grad_dtype");
     const int8_t* codes = nullptr;
     const uint8_t* exps = nullptr;
     const void* xp = nullptr;
@@ -324,15 +342,15 @@ PyObject* layernorm_backward(PyObject* const* a, Py_ssize_t n) {
         codes = s.codes;
         exps = s.exps;
     } else {
-        const Matrix x = matrix(tensor(a[8], "x"), "x");
+        const Matrix x = matrix(tensor(a[6], "x"), "x");
         if (x.code != m.code || x.rows != m.rows || x.cols != m.cols || x.index != m.index)
             refuse(PyExc_ValueError, "x must match dy in shape, type and device");
         xp = x.p;
         ldx = x.ld;
-        mean = floats(a[9], m.rows, m.index, "mean");
+        mean = floats(a[7], m.rows, m.index, "mean");
     }
     const Place at(m.index);
-    const Workspace ws(a[11], a[11] == Py_None ? api.layernorm_workspace_bytes(m.rows, m.cols) : 0, m.index);
+    const Workspace ws(a[9], a[9] == Py_None ? api.layernorm_workspace_bytes(m.rows, m.cols) : 0, m.index);
     const at::Tensor dx = empty(dy.sizes(), dy.scalar_type(), m.index);
     const at::Tensor dw = empty({m.cols}, scalar_of(gcode), m.index);
     const at::Tensor db = empty({m.cols}, scalar_of(gcode), m.index);
@@ -343,7 +361,7 @@ PyObject* layernorm_backward(PyObject* const* a, Py_ssize_t n) {
     return Py_BuildValue("NNN", wrap(dx), wrap(dw), wrap(db));
 }
 
-// (u, form, checkpoint, seed, step) -> (h, data or None, codes, exps, rows, cols, device)
+// (u, form, checkpoint, seed, step) -> (h, data or None)
 PyObject* gelu_forward(PyObject* const* a, Py_ssize_t n) {
     count(n, 5);
     const at::Tensor& u = tensor(a[0], "u");
@@ -356,14 +374,12 @@ PyObject* gelu_forward(PyObject* const* a, Py_ssize_t n) {
     check(api.gelu_forward(m.p, m.code, m.rows, m.cols, m.ld, static_cast<int>(signed64(a[1])), h.data_ptr(),
                            m.cols, r.mode, r.seed, r.step, s.codes, s.exps, at.stream),
           "gq_gelu_forward");
-    return Py_BuildValue("NNNNLLi", wrap(h), wrap(s.data), PyLong_FromVoidPtr(s.codes),
-                         PyLong_FromVoidPtr(s.exps), static_cast<long long>(m.rows),
-                         static_cast<long long>(m.cols), m.index);
+    return Py_BuildValue("NN", wrap(h), wrap(s.data));
 }
 
-// (dh, checkpoint x 5, form, output) -> du, or (du, h)
+// (dh, checkpoint x 3, form, output) -> du, or (du, h)
 PyObject* gelu_backward(PyObject* const* a, Py_ssize_t n) {
-    count(n, 8);
+    count(n, 6);
     const at::Tensor& dh = tensor(a[0], "dh");
     const Matrix m = matrix(dh, "dh");
     const Saved s(a + 1);
@@ -371,34 +387,34 @@ PyObject* gelu_backward(PyObject* const* a, Py_ssize_t n) {
     const Place at(m.index);
     const at::Tensor du = empty(dh.sizes(), dh.scalar_type(), m.index);
     at::Tensor h;
-    if (truth(a[7])) h = empty(dh.sizes(), dh.scalar_type(), m.index);
+    if (truth(a[5])) h = empty(dh.sizes(), dh.scalar_type(), m.index);
     check(api.gelu_backward(m.p, m.code, m.rows, m.cols, m.ld, s.codes, s.exps,
-                            static_cast<int>(signed64(a[6])), du.data_ptr(), m.cols,
+                            static_cast<int>(signed64(a[4])), du.data_ptr(), m.cols,
                             h.defined() ? h.data_ptr() : nullptr, m.cols, at.stream),
           "gq_gelu_backward");
     if (!h.defined()) return wrap(du);
     return Py_BuildValue("NN", wrap(du), wrap(h));
 }
 
-// (dy, checkpoint x 5, scale, shift, type code, bias, ws or None) -> (dw, dbias or None)
+// (dy, checkpoint x 3, scale, shift, type code, bias, ws or None) -> (dw, dbias or None)
 PyObject* linear_wgrad(PyObject* const* a, Py_ssize_t n) {
-    count(n, 11);
+    count(n, 9);
     const at::Tensor& dy = tensor(a[0], "dy");
     const Matrix m = matrix(dy, "dy");
     const Saved s(a + 1);
     s.covers(m.rows, -1, m.index);
     int f32 = GQ_F32;
-    const float* scale = static_cast<const float*>(vector(a[6], s.cols, m.index, &f32, "scale"));
-    const float* shift = static_cast<const float*>(vector(a[7], s.cols, m.index, &f32, "shift"));
-    const int code = output_code(a[8], "out_dtype");
+    const float* scale = static_cast<const float*>(vector(a[4], s.cols, m.index, &f32, "scale"));
+    const float* shift = static_cast<const float*>(vector(a[5], s.cols, m.index, &f32, "shift"));
+    const int code = output_code(a[6], "out_dtype");
     const Place at(m.index);
-    const Workspace ws(a[10], a[10] == Py_None ? api.linear_wgrad_workspace_bytes(m.p, m.code, m.rows, m.cols,
-                                                                                 m.ld, s.cols)
-                                               : 0,
+    const Workspace ws(a[8], a[8] == Py_None ? api.linear_wgrad_workspace_bytes(m.p, m.code, m.rows, m.cols,
+                                                                                m.ld, s.cols)
+                                             : 0,
                        m.index);
     const at::Tensor dw = empty({m.cols, s.cols}, scalar_of(code), m.index);
     at::Tensor db;
-    if (truth(a[9])) db = empty({m.cols}, at::kFloat, m.index);
+    if (truth(a[7])) db = empty({m.cols}, at::kFloat, m.index);
     check(api.linear_wgrad(m.p, m.code, m.rows, m.cols, m.ld, s.codes, s.exps, s.cols, scale, shift,
                            dw.data_ptr(), code, s.cols,
                            db.defined() ? static_cast<float*>(db.data_ptr()) : nullptr, ws.p, ws.bytes,

@@ -1,0 +1,73 @@
+"""Checkpoints as Python objects, and the layers over them in the uses of a training program: copies,
+second derivatives, memory, frozen parameters, seeds."""
+import copy
+import pickle
+
+import pytest
+
+from gpu_common import gq_module
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def gq():
+    return gq_module()
+
+
+# ---- a checkpoint follows its tensors --------------------------------------------------------
+
+def everywhere(gq, act, dy):
+    """What every operator that reads a checkpoint makes of it."""
+    rstd = torch.ones(act.rows, device="cuda")
+    return [gq.gq_act_dequantize(act), *gq.gq_layernorm_backward(dy, None, rstd, act=act),
+            *gq.gq_gelu_backward(dy, act, need_output=True), *gq.gq_linear_wgrad(dy, act)]
+
+
+@pytest.mark.parametrize("made", ["by a call", "from tensors"])
+@pytest.mark.parametrize("duplicate", [copy.deepcopy, lambda a: pickle.loads(pickle.dumps(a))],
+                         ids=["deepcopy", "pickle"])
+def test_a_copied_checkpoint_is_read_from_its_own_memory(gq, duplicate, made):
+    """The original is overwritten, not freed: its copy still reads as before."""
+    x = torch.randn((40, 96), device="cuda")
+    dy = torch.randn((40, 96), device="cuda")
+    act = gq.gq_act_quantize(x)
+    if made == "from tensors":
+        act = gq.Act8(act.codes.clone(), act.exps.clone(), 96)
+    want = everywhere(gq, act, dy)
+    other = duplicate(act)
+    act.codes.zero_()
+    act.exps.fill_(1)
+    assert other.shape == act.shape and other.rows == 40 and other.cols == 96
+    for a, b in zip(everywhere(gq, other, dy), want):
+        assert torch.equal(a, b)
+    assert not gq.gq_act_dequantize(act).any()
+
+
+def test_a_checkpoint_follows_new_storage(gq):
+    """codes and exponents given new storage are read from there (the old one stays allocated)."""
+    x = torch.randn((8, 64), device="cuda")
+    a, b = gq.gq_act_quantize(x), gq.gq_act_quantize(2 * x.flip(0))
+    codes, exps = a.codes.clone(), a.exps.clone()
+    old = codes.detach(), exps.detach()
+    act = gq.Act8(codes, exps, 64)
+    codes.data, exps.data = b.codes.clone(), b.exps.clone()
+    assert torch.equal(gq.gq_act_dequantize(act), gq.gq_act_dequantize(b))
+    assert old[0].numel() and old[1].numel()
+
+
+def test_a_checkpoint_whose_tensors_no_longer_hold_it_is_refused(gq):
+    x = torch.randn((8, 64), device="cuda")
+    made = gq.gq_act_quantize(x)
+    for part in (0, 1):
+        parts = [made.codes.clone(), made.exps.clone()]
+        keep = [p.detach() for p in parts]
+        act = gq.Act8(*parts, 64)
+        parts[part].data = parts[part][:7].clone()  # a row short
+        with pytest.raises(ValueError):
+            gq.gq_act_dequantize(act)
+        assert keep[part].numel()
+        parts[part].data = made.codes.cpu() if part == 0 else made.exps.cpu()
+        with pytest.raises(ValueError):
+            gq.gq_act_dequantize(act)
