@@ -7,11 +7,15 @@ checkpoint of the normalised rows serves both the layer norm's backward pass and
 of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.
 Checkpoints are rounded at random without bias, with the random words of (seed, step, row, column)
 that gq_quantize uses for gradients; every layer has a seed of its own.
+
+Gradients are of the first order only: a second derivative (create_graph=True, then a backward pass
+through the result) raises a RuntimeError.
 """
 from __future__ import annotations
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import _activations as ops
 
@@ -27,6 +31,7 @@ class _NormLinear(torch.autograd.Function):
         return out.view(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         norm_weight, norm_bias, weight, rstd = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])
@@ -46,6 +51,7 @@ class _GeluLinear(torch.autograd.Function):
         return out.view(*u.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         weight, = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])

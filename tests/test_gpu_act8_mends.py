@@ -71,3 +71,58 @@ def test_a_checkpoint_whose_tensors_no_longer_hold_it_is_refused(gq):
         parts[part].data = made.codes.cpu() if part == 0 else made.exps.cpu()
         with pytest.raises(ValueError):
             gq.gq_act_dequantize(act)
+
+
+# ---- the layers ------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def layers(gq):
+    from allreduce_compatible_gradient_gb300 import act8_layers
+    return act8_layers
+
+
+def block_of(layers, width=96, hidden=200, **kw):
+    torch.manual_seed(3)
+    block = layers.MlpBlock8(width, hidden, device="cuda", **kw)
+    with torch.no_grad():
+        for p in block.parameters():
+            p += 0.1 * torch.randn_like(p)
+    return block
+
+
+def exact_gradients(block, x, r):
+    """Autograd's, in fp64, of sum(block(x) r)."""
+    p = {k: v.detach().double().requires_grad_() for k, v in block.named_parameters()}
+    x = x.detach().double().requires_grad_()
+    y = torch.nn.functional.layer_norm(x, x.shape[-1:], p["norm_weight"], p["norm_bias"], block.eps)
+    h = torch.nn.functional.gelu(y @ p["w1"].t() + p["b1"], approximate=block.approximate)
+    out = x + h @ p["w2"].t() + p["b2"]
+    return dict(zip(["x", *p], torch.autograd.grad((out * r.double()).sum(), [x, *p.values()])))
+
+
+@pytest.fixture
+def calls(layers, monkeypatch):
+    """(name, arguments, result) of every operator that the layers call."""
+    seen = []
+
+    def record(name):
+        call = getattr(layers.ops, name)
+
+        def recorded(*a, **kw):
+            out = call(*a, **kw)
+            seen.append((name, a, kw, out))
+            return out
+        monkeypatch.setattr(layers.ops, name, recorded)
+    for name in ("gq_layernorm_forward", "gq_layernorm_backward", "gq_gelu_forward", "gq_gelu_backward",
+                 "gq_linear_wgrad"):
+        record(name)
+    return seen
+
+
+def test_a_second_derivative_is_refused(layers):
+    """The operators of the backward pass are not differentiable: a gradient penalty is refused, not
+    computed without their part."""
+    block, x = block_of(layers), torch.randn((10, 96), device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(block(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()
