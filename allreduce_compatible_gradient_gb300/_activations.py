@@ -90,12 +90,19 @@ class Act8:
         self._cols, self._codes, self._exps = cols, codes, exps
 
     @classmethod
-    def _made(cls, data, cols, shape):
-        """One that a call has written: codes, then exponents, in one allocation (bytes, a row each of
-        the codes' and the exponents' pitch)."""
+    def of_data(cls, data: torch.Tensor, cols: int, shape=None) -> "Act8":
+        """The checkpoint whose `data` this is: for code that keeps tensors and not objects, as autograd
+        functions do."""
         self = cls.__new__(cls)
-        self.shape, self._cols, self._codes, self._exps = shape, cols, data, None
+        self.shape = (data.shape[0], cols) if shape is None else shape
+        self._cols, self._codes, self._exps = cols, data, None
         return self
+
+    @property
+    def data(self) -> torch.Tensor:
+        """What a call has written, one tensor of bytes: the codes of all rows, then the exponents (None
+        for a checkpoint made of two tensors)."""
+        return self._codes if self._exps is None else None
 
     @property
     def rows(self) -> int:
@@ -155,7 +162,7 @@ def gq_act_quantize(x, seed=None, step=0, stream=None) -> Act8:
     """8-bit checkpoint of x: rounded to nearest (seed None), or at random without bias."""
     if stream is not None:
         return _on(stream, gq_act_quantize, x, seed, step)
-    return Act8._made(_native.act_quantize(x, seed, step), x.shape[-1], x.shape)
+    return Act8.of_data(_native.act_quantize(x, seed, step), x.shape[-1], x.shape)
 
 
 def gq_act_dequantize(act, out=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
@@ -172,7 +179,7 @@ def gq_layernorm_forward(x, weight=None, bias=None, eps=1e-5, checkpoint=True, s
     if stream is not None:
         return _on(stream, gq_layernorm_forward, x, weight, bias, eps, checkpoint, seed, step)
     y, mean, rstd, data = _native.layernorm_forward(x, weight, bias, eps, checkpoint, seed, step)
-    return y, mean, rstd, None if data is None else Act8._made(data, x.shape[-1], x.shape)
+    return y, mean, rstd, None if data is None else Act8.of_data(data, x.shape[-1], x.shape)
 
 
 def gq_layernorm_backward(dy, weight, rstd, act=None, x=None, mean=None, grad_dtype=torch.float32,
@@ -191,7 +198,7 @@ def gq_gelu_forward(u, approximate="none", checkpoint=True, seed=None, step=0, s
     if stream is not None:
         return _on(stream, gq_gelu_forward, u, approximate, checkpoint, seed, step)
     h, data = _native.gelu_forward(u, _form(approximate), checkpoint, seed, step)
-    return h, None if data is None else Act8._made(data, u.shape[-1], u.shape)
+    return h, None if data is None else Act8.of_data(data, u.shape[-1], u.shape)
 
 
 def gq_gelu_backward(dh, act, approximate="none", need_output=False, stream=None):

@@ -4,7 +4,8 @@ operators): layer norm + linear, GELU + linear, and the pre-norm MLP block made 
 Parameters are fp32; activations and their gradients are bf16 (or fp32).  The forward pass keeps one
 8-bit checkpoint per normalised input and one per GELU input, and nothing else of their size: the
 checkpoint of the normalised rows serves both the layer norm's backward pass and the weight gradient
-of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.
+of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.  They
+are saved tensors like any others: the backward pass frees them, and saved-tensor hooks see them.
 Checkpoints are rounded at random without bias, with the random words of (seed, step, row, column)
 that gq_quantize uses for gradients; every layer has a seed of its own.
 
@@ -25,18 +26,19 @@ class _NormLinear(torch.autograd.Function):
     def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step):
         rows = x.reshape(-1, x.shape[-1])
         y, _, rstd, act = ops.gq_layernorm_forward(rows, norm_weight, norm_bias, eps, seed=seed, step=step)
-        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd)
-        ctx.act, ctx.shape = act, x.shape
+        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act.data)
+        ctx.shape = x.shape
         out = torch.nn.functional.linear(y, weight.to(y.dtype), bias.to(y.dtype))
         return out.view(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        norm_weight, norm_bias, weight, rstd = ctx.saved_tensors
+        norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
+        act = ops.Act8.of_data(data, weight.shape[1])
         d = dout.reshape(-1, dout.shape[-1])
-        dweight, dbias = ops.gq_linear_wgrad(d, ctx.act, scale=norm_weight, shift=norm_bias)
-        dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=ctx.act)
+        dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight, shift=norm_bias)
+        dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
         return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None
 
 
@@ -45,18 +47,18 @@ class _GeluLinear(torch.autograd.Function):
     def forward(ctx, u, weight, bias, approximate, seed, step):
         rows = u.reshape(-1, u.shape[-1])
         h, act = ops.gq_gelu_forward(rows, approximate=approximate, seed=seed, step=step)
-        ctx.save_for_backward(weight)
-        ctx.act, ctx.approximate, ctx.shape = act, approximate, u.shape
+        ctx.save_for_backward(weight, act.data)
+        ctx.approximate, ctx.shape = approximate, u.shape
         out = torch.nn.functional.linear(h, weight.to(h.dtype), bias.to(h.dtype))
         return out.view(*u.shape[:-1], weight.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        weight, = ctx.saved_tensors
+        weight, data = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])
-        du, h = ops.gq_gelu_backward(d @ weight.to(d.dtype), ctx.act, approximate=ctx.approximate,
-                                     need_output=True)
+        du, h = ops.gq_gelu_backward(d @ weight.to(d.dtype), ops.Act8.of_data(data, weight.shape[1]),
+                                     approximate=ctx.approximate, need_output=True)
         dweight = (d.t() @ h).float()
         return du.view(ctx.shape), dweight, d.float().sum(0), None, None, None
 

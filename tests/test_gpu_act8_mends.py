@@ -126,3 +126,50 @@ def test_a_second_derivative_is_refused(layers):
     g, = torch.autograd.grad(block(x).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+def test_checkpoints_are_freed_by_the_backward_pass(layers):
+    """As autograd's saved tensors are: not when the loss goes, which most loops hold into the next step."""
+    block = block_of(layers, 256, 1024)
+    x = torch.randn((4096, 256), device="cuda", dtype=torch.bfloat16)
+    saved = 4096 * (256 + 1024)  # bytes of codes
+
+    def step():
+        loss = block(x).float().sum()
+        loss.backward()
+        return loss
+    step()  # gradients and library workspaces are there from here on
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    loss = step()
+    assert torch.cuda.memory_allocated() - before < saved / 4
+    assert loss.isfinite()
+
+
+def test_saved_tensor_hooks_see_the_checkpoints(layers):
+    """Offloaded to the host and brought back, they give the same gradients."""
+    block = block_of(layers)
+    x = torch.randn((150, 96), device="cuda", dtype=torch.bfloat16)
+    sizes = []
+
+    def gradients():
+        return torch.autograd.grad(block(x).float().square().sum(), list(block.parameters()))
+
+    def pack(t):
+        sizes.append(t.nbytes)
+        return t.cpu()
+    want = gradients()
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+        got = gradients()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    # codes of 96 and of round_up(200, 32) bytes a row, 16 exponent bytes a row each
+    assert sizes.count(150 * (96 + 16)) == 1 and sizes.count(150 * (224 + 16)) == 1
+
+
+def test_a_graph_that_is_kept_gives_the_same_gradients_again(layers):
+    block = block_of(layers)
+    loss = block(torch.randn((20, 96), device="cuda")).square().sum()
+    first = torch.autograd.grad(loss, list(block.parameters()), retain_graph=True)
+    for a, b in zip(first, torch.autograd.grad(loss, list(block.parameters()))):
+        assert torch.equal(a, b)
