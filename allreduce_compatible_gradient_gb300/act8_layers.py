@@ -1,7 +1,8 @@
 """Transformer layers that keep their activations in 8 bits (torch modules over the activation
 operators): layer norm + linear, GELU + linear, and the pre-norm MLP block made of the two.
 
-Parameters are fp32; activations and their gradients are bf16 (or fp32).  The forward pass keeps one
+Parameters are fp32 (or bf16, as their gradients then are); activations and their gradients are bf16 (or
+fp32).  The forward pass keeps one
 8-bit checkpoint per normalised input and one per GELU input, and nothing else of their size: the
 checkpoint of the normalised rows serves both the layer norm's backward pass and the weight gradient
 of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.  They
@@ -37,7 +38,7 @@ class _NormLinear(torch.autograd.Function):
         norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
         act = ops.Act8.of_data(data, weight.shape[1])
         d = dout.reshape(-1, dout.shape[-1])
-        dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight, shift=norm_bias)
+        dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight.float(), shift=norm_bias.float())
         dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
         return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None
 

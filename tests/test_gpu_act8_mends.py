@@ -173,3 +173,16 @@ def test_a_graph_that_is_kept_gives_the_same_gradients_again(layers):
     first = torch.autograd.grad(loss, list(block.parameters()), retain_graph=True)
     for a, b in zip(first, torch.autograd.grad(loss, list(block.parameters()))):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_bf16_parameters(layers, dtype):
+    """Gradients of a block whose parameters are bf16: 2 % of the norm as in the fp32 block's test, and
+    2^-8 for their own rounding."""
+    block = block_of(layers, seed=5).bfloat16()
+    x = torch.randn((2, 75, 96), device="cuda").to(dtype).requires_grad_()
+    r = torch.randn((2, 75, 96), device="cuda")
+    got = torch.autograd.grad((block(x).float() * r).sum(), [x, *block.parameters()])
+    for g, p, (name, w) in zip(got, [x, *block.parameters()], exact_gradients(block, x, r).items()):
+        assert g.dtype == p.dtype and g.shape == p.shape
+        assert (g.double() - w).norm() < (0.02 + 2.0 ** -8) * w.norm(), name
