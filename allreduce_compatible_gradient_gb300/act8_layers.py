@@ -2,11 +2,12 @@
 operators): layer norm + linear, GELU + linear, and the pre-norm MLP block made of the two.
 
 Parameters are fp32 (or bf16, as their gradients then are); activations and their gradients are bf16 (or
-fp32).  The forward pass keeps one
-8-bit checkpoint per normalised input and one per GELU input, and nothing else of their size: the
-checkpoint of the normalised rows serves both the layer norm's backward pass and the weight gradient
-of the linear layer behind it, and GELU's backward pass rebuilds the second linear layer's input.  They
-are saved tensors like any others: the backward pass frees them, and saved-tensor hooks see them.
+fp32).  The forward pass keeps one 8-bit checkpoint per normalised input and one per GELU input, and
+nothing else of their size: the checkpoint of the normalised rows serves both the layer norm's backward
+pass and the weight gradient of the linear layer behind it, and GELU's backward pass rebuilds the second
+linear layer's input.  They are saved tensors like any others: the backward pass frees them, and
+saved-tensor hooks see them.  Where no backward pass will read one (under no_grad, or with nothing before
+it that requires a gradient) it is not made.
 Checkpoints are rounded at random without bias, with the random words of (seed, step, row, column)
 that gq_quantize uses for gradients; every layer has a seed of its own.
 
@@ -24,10 +25,11 @@ from . import _activations as ops
 
 class _NormLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step):
+    def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step, record=True):
         rows = x.reshape(-1, x.shape[-1])
-        y, _, rstd, act = ops.gq_layernorm_forward(rows, norm_weight, norm_bias, eps, seed=seed, step=step)
-        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act.data)
+        y, _, rstd, act = ops.gq_layernorm_forward(rows, norm_weight, norm_bias, eps, seed=seed, step=step,
+                                                   checkpoint=record and any(ctx.needs_input_grad[:4]))
+        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data)
         ctx.shape = x.shape
         out = torch.nn.functional.linear(y, weight.to(y.dtype), bias.to(y.dtype))
         return out.view(*x.shape[:-1], weight.shape[0])
@@ -36,19 +38,22 @@ class _NormLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
-        act = ops.Act8.of_data(data, weight.shape[1])
         d = dout.reshape(-1, dout.shape[-1])
+        if data is None:  # the bias' gradient alone
+            return None, None, None, None, d.sum(0, dtype=torch.float32), None, None, None, None
+        act = ops.Act8.of_data(data, weight.shape[1])
         dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight.float(), shift=norm_bias.float())
         dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
-        return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None
+        return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None, None
 
 
 class _GeluLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, u, weight, bias, approximate, seed, step):
+    def forward(ctx, u, weight, bias, approximate, seed, step, record=True):
         rows = u.reshape(-1, u.shape[-1])
-        h, act = ops.gq_gelu_forward(rows, approximate=approximate, seed=seed, step=step)
-        ctx.save_for_backward(weight, act.data)
+        h, act = ops.gq_gelu_forward(rows, approximate=approximate, seed=seed, step=step,
+                                     checkpoint=record and any(ctx.needs_input_grad[:2]))
+        ctx.save_for_backward(weight, act and act.data)
         ctx.approximate, ctx.shape = approximate, u.shape
         out = torch.nn.functional.linear(h, weight.to(h.dtype), bias.to(h.dtype))
         return out.view(*u.shape[:-1], weight.shape[0])
@@ -58,10 +63,12 @@ class _GeluLinear(torch.autograd.Function):
     def backward(ctx, dout):
         weight, data = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])
+        if data is None:  # the bias' gradient alone
+            return None, None, d.sum(0, dtype=torch.float32), None, None, None, None
         du, h = ops.gq_gelu_backward(d @ weight.to(d.dtype), ops.Act8.of_data(data, weight.shape[1]),
                                      approximate=ctx.approximate, need_output=True)
         dweight = (d.t() @ h).float()
-        return du.view(ctx.shape), dweight, d.float().sum(0), None, None, None
+        return du.view(ctx.shape), dweight, d.float().sum(0), None, None, None, None
 
 
 class MlpBlock8(nn.Module):
@@ -80,6 +87,8 @@ class MlpBlock8(nn.Module):
         self.approximate, self.eps, self.seed, self.step = approximate, eps, seed, 0
 
     def forward(self, x):
+        record = torch.is_grad_enabled()  # not seen within a Function's forward pass
         u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps,
-                              2 * self.seed, self.step)
-        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, 2 * self.seed + 1, self.step)
+                              2 * self.seed, self.step, record)
+        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, 2 * self.seed + 1, self.step,
+                                     record)

@@ -186,3 +186,27 @@ def test_bf16_parameters(layers, dtype):
     for g, p, (name, w) in zip(got, [x, *block.parameters()], exact_gradients(block, x, r).items()):
         assert g.dtype == p.dtype and g.shape == p.shape
         assert (g.double() - w).norm() < (0.02 + 2.0 ** -8) * w.norm(), name
+
+
+def test_no_checkpoints_without_a_backward_pass(layers, calls):
+    """Under no_grad, and where nothing requires a gradient; the outputs are the same."""
+    block, x = block_of(layers), torch.randn((70, 96), device="cuda", dtype=torch.bfloat16)
+
+    def checkpoints():
+        made = [out[-1] is not None for name, _, _, out in calls if name.endswith("forward")]
+        calls.clear()
+        return made
+    want = block(x)
+    assert checkpoints() == [True, True]
+    with torch.no_grad():
+        assert torch.equal(block(x), want)
+    assert checkpoints() == [False, False]
+    block.requires_grad_(False)
+    assert torch.equal(block(x), want)
+    assert checkpoints() == [False, False]
+    block.b2.requires_grad_()  # whose gradient needs no activation
+    assert torch.equal(block(x), want)
+    assert checkpoints() == [False, False]
+    block.w2.requires_grad_()
+    assert torch.equal(block(x), want)
+    assert checkpoints() == [False, True]
