@@ -39,12 +39,18 @@ class _NormLinear(torch.autograd.Function):
     def backward(ctx, dout):
         norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])
-        if data is None:  # the bias' gradient alone
-            return None, None, None, None, d.sum(0, dtype=torch.float32), None, None, None, None
-        act = ops.Act8.of_data(data, weight.shape[1])
-        dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight.float(), shift=norm_bias.float())
-        dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
-        return dx.view(ctx.shape), dnw, dnb, dweight, dbias, None, None, None, None
+        need = ctx.needs_input_grad
+        dx = dnw = dnb = dweight = dbias = None
+        act = None if data is None else ops.Act8.of_data(data, weight.shape[1])
+        if need[3]:
+            dweight, dbias = ops.gq_linear_wgrad(d, act, scale=norm_weight.float(), shift=norm_bias.float(),
+                                                 need_bias=need[4])
+        elif need[4]:
+            dbias = d.sum(0, dtype=torch.float32)
+        if any(need[:3]):
+            dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
+            dx = dx.view(ctx.shape)
+        return dx, dnw, dnb, dweight, dbias, None, None, None, None
 
 
 class _GeluLinear(torch.autograd.Function):
@@ -63,12 +69,16 @@ class _GeluLinear(torch.autograd.Function):
     def backward(ctx, dout):
         weight, data = ctx.saved_tensors
         d = dout.reshape(-1, dout.shape[-1])
-        if data is None:  # the bias' gradient alone
-            return None, None, d.sum(0, dtype=torch.float32), None, None, None, None
-        du, h = ops.gq_gelu_backward(d @ weight.to(d.dtype), ops.Act8.of_data(data, weight.shape[1]),
-                                     approximate=ctx.approximate, need_output=True)
-        dweight = (d.t() @ h).float()
-        return du.view(ctx.shape), dweight, d.float().sum(0), None, None, None, None
+        need = ctx.needs_input_grad
+        du = dweight = None
+        if need[0] or need[1]:
+            got = ops.gq_gelu_backward(d @ weight.to(d.dtype), ops.Act8.of_data(data, weight.shape[1]),
+                                       approximate=ctx.approximate, need_output=need[1])
+            du, h = got if need[1] else (got, None)
+            du = du.view(ctx.shape)
+            if need[1]:
+                dweight = (d.t() @ h).float()
+        return du, dweight, d.float().sum(0) if need[2] else None, None, None, None, None
 
 
 class MlpBlock8(nn.Module):

@@ -210,3 +210,33 @@ def test_no_checkpoints_without_a_backward_pass(layers, calls):
     block.w2.requires_grad_()
     assert torch.equal(block(x), want)
     assert checkpoints() == [False, True]
+
+
+@pytest.mark.parametrize("wanted,called", [
+    (["b2"], []), (["w2"], ["gelu"]), (["b1"], ["gelu"]), (["w1"], ["gelu", "wgrad"]),
+    (["w1", "b1"], ["gelu", "wgrad"]), (["norm_weight"], ["gelu", "norm"]), (["norm_bias", "w2"], ["gelu", "norm"]),
+    (["x"], ["gelu", "norm"]), (["x", "b1", "b2"], ["gelu", "norm"]),
+    (["norm_weight", "norm_bias", "w1", "b1", "w2", "b2"], ["gelu", "wgrad", "norm"])])
+def test_frozen_parameters_cost_no_gradient(layers, calls, wanted, called):
+    """Only what requires a gradient gets one, the same one as when all do, and operators whose results
+    nobody wants are not called."""
+    block = block_of(layers)
+    x = torch.randn((70, 96), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    r = torch.randn((70, 96), device="cuda")
+    leaves = dict(x=x, **dict(block.named_parameters()))
+
+    def gradients():
+        names = [k for k, v in leaves.items() if v.requires_grad]
+        loss = (block(x).float() * r).sum()
+        return dict(zip(names, torch.autograd.grad(loss, [leaves[k] for k in names])))
+    want = gradients()
+    for k, v in leaves.items():
+        v.requires_grad_(k in wanted)
+    calls.clear()
+    got = gradients()
+    assert set(got) == set(wanted)
+    for k, g in got.items():
+        # (a bias' gradient alone is a plain sum, of another order)
+        assert torch.equal(g, want[k]) if k != "b1" or "w1" in wanted else torch.allclose(g, want[k], rtol=1e-3, atol=1e-4)
+    short = {"gq_gelu_backward": "gelu", "gq_linear_wgrad": "wgrad", "gq_layernorm_backward": "norm"}
+    assert [short[n] for n, *_ in calls if n in short] == called
