@@ -23,11 +23,17 @@ from torch.autograd.function import once_differentiable
 from . import _activations as ops
 
 
+def _rows(x):
+    """x as a matrix that the operators take: a copy where its elements do not lie side by side, or where
+    rows share their memory."""
+    m = x.reshape(-1, x.shape[-1])
+    return m if m.stride(1) == 1 and (m.shape[0] < 2 or m.stride(0) >= m.shape[1]) else m.contiguous()
+
+
 class _NormLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step, record=True):
-        rows = x.reshape(-1, x.shape[-1])
-        y, _, rstd, act = ops.gq_layernorm_forward(rows, norm_weight, norm_bias, eps, seed=seed, step=step,
+        y, _, rstd, act = ops.gq_layernorm_forward(_rows(x), norm_weight, norm_bias, eps, seed=seed, step=step,
                                                    checkpoint=record and any(ctx.needs_input_grad[:4]))
         ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data)
         ctx.shape = x.shape
@@ -38,7 +44,7 @@ class _NormLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
-        d = dout.reshape(-1, dout.shape[-1])
+        d = _rows(dout)
         need = ctx.needs_input_grad
         dx = dnw = dnb = dweight = dbias = None
         act = None if data is None else ops.Act8.of_data(data, weight.shape[1])
@@ -56,8 +62,7 @@ class _NormLinear(torch.autograd.Function):
 class _GeluLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, u, weight, bias, approximate, seed, step, record=True):
-        rows = u.reshape(-1, u.shape[-1])
-        h, act = ops.gq_gelu_forward(rows, approximate=approximate, seed=seed, step=step,
+        h, act = ops.gq_gelu_forward(_rows(u), approximate=approximate, seed=seed, step=step,
                                      checkpoint=record and any(ctx.needs_input_grad[:2]))
         ctx.save_for_backward(weight, act and act.data)
         ctx.approximate, ctx.shape = approximate, u.shape
@@ -68,7 +73,7 @@ class _GeluLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         weight, data = ctx.saved_tensors
-        d = dout.reshape(-1, dout.shape[-1])
+        d = _rows(dout)
         need = ctx.needs_input_grad
         du = dweight = None
         if need[0] or need[1]:

@@ -240,3 +240,19 @@ def test_frozen_parameters_cost_no_gradient(layers, calls, wanted, called):
         assert torch.equal(g, want[k]) if k != "b1" or "w1" in wanted else torch.allclose(g, want[k], rtol=1e-3, atol=1e-4)
     short = {"gq_gelu_backward": "gelu", "gq_linear_wgrad": "wgrad", "gq_layernorm_backward": "norm"}
     assert [short[n] for n, *_ in calls if n in short] == called
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_inputs_of_any_strides(layers, dtype):
+    """A transposed matrix, a broadcast row, every second column: as their contiguous copies."""
+    block = block_of(layers)
+    base = torch.randn((96, 40), device="cuda").to(dtype)
+    for x in (base.t(), base.t()[:1].expand(40, 96), torch.randn((40, 192), device="cuda").to(dtype)[:, ::2],
+              base.t().reshape(2, 20, 96).transpose(0, 1)):
+        results = []
+        for v in (x, x.contiguous()):
+            v = v.detach().requires_grad_()
+            out = block(v)
+            results.append([out, *torch.autograd.grad(out.float().square().sum(), [v, *block.parameters()])])
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
