@@ -8,13 +8,19 @@ pass and the weight gradient of the linear layer behind it, and GELU's backward 
 linear layer's input.  They are saved tensors like any others: the backward pass frees them, and
 saved-tensor hooks see them.  Where no backward pass will read one (under no_grad, or with nothing before
 it that requires a gradient) it is not made.
-Checkpoints are rounded at random without bias, with the random words of (seed, step, row, column)
-that gq_quantize uses for gradients; every layer has a seed of its own.
+
+Checkpoints are rounded at random without bias, with random words of (key, step, row, column) as
+gq_quantize draws them for gradients.  An estimate made of several roundings is unbiased only where their
+words are independent, so no two share any: every layer of every block has a key of its own, bit 63 of
+which is set (gradients keep theirs clear by seeds below 2^63), and the rank of a data-parallel job is part
+of the step.
 
 Gradients are of the first order only: a second derivative (create_graph=True, then a backward pass
 through the result) raises a RuntimeError.
 """
 from __future__ import annotations
+
+import itertools
 
 import torch
 from torch import nn
@@ -86,12 +92,20 @@ class _GeluLinear(torch.autograd.Function):
         return du, dweight, d.float().sum(0) if need[2] else None, None, None, None, None
 
 
+_numbers = itertools.count()  # of the blocks of this process
+
+
 class MlpBlock8(nn.Module):
-    """x + W2 gelu(W1 norm(x) + b1) + b2 with 8-bit checkpoints.  `step` numbers the training steps:
-    set it before each forward pass, so that every step rounds with words of its own."""
+    """x + W2 gelu(W1 norm(x) + b1) + b2 with 8-bit checkpoints.
+
+    `step` numbers the training steps: set it before each forward pass (below 2^48; another one each time,
+    where a block is applied more than once), so that every pass rounds with words of its own.  Data-parallel ranks need words of their own too: `rank` (below 2^16)
+    tells them apart, torch.distributed's where it is None and a process group is there, else 0.  Every
+    block has its own words; `seed` names them instead, for words that a later run can draw again, and then
+    blocks of one model need different seeds."""
 
     def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
-                 seed: int = 0, device=None):
+                 seed: int | None = None, device=None, rank: int | None = None):
         super().__init__()
         self.norm_weight = nn.Parameter(torch.ones(width, device=device))
         self.norm_bias = nn.Parameter(torch.zeros(width, device=device))
@@ -99,11 +113,31 @@ class MlpBlock8(nn.Module):
         self.b1 = nn.Parameter(torch.zeros(hidden, device=device))
         self.w2 = nn.Parameter(torch.randn(width, hidden, device=device) * hidden ** -0.5)
         self.b2 = nn.Parameter(torch.zeros(width, device=device))
-        self.approximate, self.eps, self.seed, self.step = approximate, eps, seed, 0
+        self.approximate, self.eps, self.seed, self.rank, self.step = approximate, eps, seed, rank, 0
+        self._number = next(_numbers)
+
+    def __setstate__(self, state):  # a copy, or one read back from a file
+        super().__setstate__(state)
+        self._number = next(_numbers)
+
+    def words(self, layer: int):
+        """(seed, step) of the random words of a layer: 0 the layer norm's checkpoint, 1 GELU's."""
+        if self.seed is None:  # from the top down, where no seed is taken
+            seed = (1 << 62) - 1 - self._number
+        elif 0 <= self.seed < (1 << 62) - (1 << 32):
+            seed = self.seed
+        else:
+            raise ValueError("seed must be a number below 2^62 - 2^32")
+        rank = self.rank
+        if rank is None:
+            there = torch.distributed.is_available() and torch.distributed.is_initialized()
+            rank = torch.distributed.get_rank() if there else 0
+        if not (0 <= rank < 1 << 16 and 0 <= self.step < 1 << 48):
+            raise ValueError("rank must be a number below 2^16 and step one below 2^48")
+        return 1 << 63 | 2 * seed + layer, rank << 48 | self.step
 
     def forward(self, x):
         record = torch.is_grad_enabled()  # not seen within a Function's forward pass
-        u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps,
-                              2 * self.seed, self.step, record)
-        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, 2 * self.seed + 1, self.step,
-                                     record)
+        u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps, *self.words(0),
+                              record)
+        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, *self.words(1), record)

@@ -3,8 +3,9 @@ as unbiased 8-bit checkpoints, gradients of n workers compressed and averaged by
 
     python examples/train_mlp8.py [--workers 4] [--steps 30] [--width 256] [--tokens 512]
 
-Each step, every worker runs its own batch through the same model; the workers' gradients are the rows
-of one matrix, which gq_allreduce_mean turns into the unbiased estimate of their mean.  The task is to
+Each step, every worker runs its own batch through the same model, and rounds its activations with random
+words of its own (block.rank); the workers' gradients are the rows of one matrix, which gq_allreduce_mean
+turns into the unbiased estimate of their mean.  The task is to
 imitate a fixed teacher of the same shape.  Prints the loss and what the checkpoints take.
 """
 import argparse
@@ -22,8 +23,8 @@ from allreduce_compatible_gradient_gb300.act8_layers import MlpBlock8  # noqa: E
 def train(workers=4, steps=30, width=256, hidden=1024, tokens=512, lr=0.5, seed=0):
     """The losses of the steps, averaged over the workers."""
     torch.manual_seed(seed)
-    teacher, model = (torch.nn.Sequential(*[MlpBlock8(width, hidden, seed=i, device="cuda")
-                                            for i in range(2)]) for _ in range(2))
+    teacher, model = (torch.nn.Sequential(*[MlpBlock8(width, hidden, device="cuda") for _ in range(2)])
+                      for _ in range(2))
     params = list(model.parameters())
     d = sum(p.numel() for p in params)
     grads = torch.empty((workers, d), device="cuda")
@@ -33,7 +34,7 @@ def train(workers=4, steps=30, width=256, hidden=1024, tokens=512, lr=0.5, seed=
         total = 0.0
         for w in range(workers):
             for block in model:
-                block.step = step * workers + w
+                block.rank, block.step = w, step
             x = torch.randn((tokens, width), device="cuda").bfloat16()
             with torch.no_grad():
                 want = teacher(x).float()

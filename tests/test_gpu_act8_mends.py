@@ -242,6 +242,42 @@ def test_frozen_parameters_cost_no_gradient(layers, calls, wanted, called):
     assert [short[n] for n, *_ in calls if n in short] == called
 
 
+# ---- random words ------------------------------------------------------------------------------
+
+def errors(calls, gq):
+    """Rounding errors of the checkpoints made since the last time, in steps of their blocks."""
+    out = []
+    for name, a, kw, got in calls:
+        if name == "gq_gelu_forward" and got[1] is not None:
+            act = got[1]
+            step = torch.ldexp(torch.ones((), device="cuda"), act.exps[:, :act.codes.shape[1] // 32].int() - 127)
+            step = step.repeat_interleave(32, dim=1)[:, :act.cols]
+            out.append((gq.gq_act_dequantize(act, out_dtype=torch.float32) - a[0].float()) / step)
+    calls.clear()
+    return out
+
+
+def test_blocks_do_not_share_their_rounding(gq, layers, calls):
+    """Two blocks made alike, ranks and steps of one: errors of 70 x 200 roundings of the same numbers are
+    uncorrelated within 5 / sqrt(14,000), where the same words make them equal."""
+    a, b = (layers.MlpBlock8(96, 200, device="cuda") for _ in range(2))
+    b.load_state_dict(a.state_dict())
+    x = torch.randn((70, 96), device="cuda")
+    a(x), b(x)
+    a.rank = 1
+    a(x)
+    a.step = 1
+    a(x)
+    got = errors(calls, gq)
+    assert len(got) == 4
+    for i in range(4):
+        for j in range(i):
+            e, f = got[i] - got[i].mean(), got[j] - got[j].mean()
+            assert abs((e * f).sum() / (e.norm() * f.norm())) < 5 / 14000 ** 0.5
+    a(x)
+    assert torch.equal(errors(calls, gq)[0], got[3])  # the same words again
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_inputs_of_any_strides(layers, dtype):
     """A transposed matrix, a broadcast row, every second column: as their contiguous copies."""
