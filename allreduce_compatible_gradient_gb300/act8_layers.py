@@ -88,8 +88,10 @@ class _GeluLinear(torch.autograd.Function):
             du, h = got if need[1] else (got, None)
             du = du.view(ctx.shape)
             if need[1]:
-                dweight = (d.t() @ h).float()
-        return du, dweight, d.float().sum(0) if need[2] else None, None, None, None, None
+                # bf16 operands, fp32 sums: the gradient of an fp32 parameter is not rounded to bf16
+                dweight = d.t() @ h if d.dtype == torch.float32 else torch.mm(d.t(), h, out_dtype=torch.float32)
+        dbias = d.sum(0, dtype=torch.float32) if need[2] else None
+        return du, dweight, dbias, None, None, None, None
 
 
 _numbers = itertools.count()  # of the blocks of this process

@@ -292,3 +292,18 @@ def test_inputs_of_any_strides(layers, dtype):
             results.append([out, *torch.autograd.grad(out.float().square().sum(), [v, *block.parameters()])])
         for a, b in zip(*results):
             assert torch.equal(a, b)
+
+
+def test_gradient_of_the_second_weight_is_not_rounded_to_bf16(layers, calls):
+    """An fp32 parameter's gradient from bf16 operands carries the error of their sum alone, which the
+    tensor cores may truncate 2^-22 of the largest partial sum per 16 products; nothing of bf16's 2^-9."""
+    block = block_of(layers)
+    x = torch.randn((150, 96), device="cuda", dtype=torch.bfloat16)
+    r = torch.randn((150, 96), device="cuda").bfloat16()
+    dw2, db2 = torch.autograd.grad((block(x) * r).sum(), [block.w2, block.b2])
+    h, = [out[1] for name, _, _, out in calls if name == "gq_gelu_backward"]
+    d, h = r.double(), h.double()
+    mag = d.abs().t() @ h.abs()
+    assert dw2.dtype == db2.dtype == torch.float32
+    assert ((dw2.double() - d.t() @ h).abs() <= (150 / 16 + 32) * 2.0 ** -22 * mag).all()
+    assert ((db2.double() - d.sum(0)).abs() <= 190 * 2.0 ** -24 * d.abs().sum(0)).all()
