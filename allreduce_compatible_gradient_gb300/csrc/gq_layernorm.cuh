@@ -75,8 +75,8 @@ inline Shape shape_of(int64_t rows, int64_t cols) {
 // part of the random words stay in registers, and the next rows are on their way while one is worked
 // on.  What bounds it is the number of instructions per row beside its elements' own: 16 columns per
 // thread instead of 8 took the backward pass at 65,536 x 1,024 bf16 from 75 to 65 us.  No branches
-// depend on the thread either (65 -> 59 us): a thread behind the last column works on copies of the
-// first columns with weights and masks of 0, and only its stores are left out.  The two pieces lie 256
+// depend on the thread either (65 -> 59 us): a thread behind the last column works on zeros (and on the
+// first columns' codes), and only its stores are left out.  The two pieces lie 256
 // columns apart, so that neighbours load neighbours (16 columns side by side: 59 -> 67 us).
 
 // Warps per row, as far as the reductions differ by it.
@@ -141,7 +141,8 @@ __device__ __forceinline__ void vec8(const void* p, int wide, int aligned, float
 
 // 8 elements of a thread in a slot of copies in flight: planes of 16 bytes per thread.  Rows that are
 // not 16-byte aligned are copied by the 16-byte granules that hold a byte of them, one more at most, and
-// moved into place as they are read; `left` of the elements lie in the row, the others read as 0.
+// moved into place as they are read; `left` of the elements lie in the row, the others read as 0 (an
+// aligned piece lies in the row as a whole, or not at all: left 0).
 template <typename T, bool ALIGNED> struct Ring {
     static constexpr int kSlots = ALIGNED ? kDepth : 2;
     static constexpr int kPieces = sizeof(T) / 2 + (ALIGNED ? 0 : 1);
@@ -149,7 +150,7 @@ template <typename T, bool ALIGNED> struct Ring {
         const uint8_t* q = reinterpret_cast<const uint8_t*>(p);
         if constexpr (ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) copy_async<16>(to + i * plane, q + 16 * i);
+            for (int i = 0; i < kPieces; ++i) copy_part(to + i * plane, q + 16 * i, left > 0 ? 16u : 0u);
         } else {
             const int m = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15u);
             const int bytes = m + min(left, 8) * static_cast<int>(sizeof(T));

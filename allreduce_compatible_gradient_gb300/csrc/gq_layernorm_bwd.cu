@@ -185,19 +185,15 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
     float* const slots = &buf[0][W == kFour ? group * 8 : 0];
     bool in[VPT];
     uint32_t col[VPT];
-    int left[VPT];  // elements of the row from col on
+    int left[VPT];  // elements of the row from col on, 0 behind the last column
     F2 wv[VPT][4], aw[VPT][4], ab[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const uint32_t c = k * apart + t * 8;
         in[k] = c < a.cols;
         col[k] = in[k] ? c : 0u;
-        left[k] = static_cast<int>(a.cols - col[k]);
+        left[k] = in[k] ? static_cast<int>(a.cols - c) : 0;
         vec8(w, wide & 1, wide >> 1, 1.0f, c, a.cols, wv[k]);
-        if (!in[k]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wv[k][i] = f2(0.0f);
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = f2(0.0f);
     }

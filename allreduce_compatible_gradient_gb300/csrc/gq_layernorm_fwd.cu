@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
     float* const slots = &buf[0][W == kFour ? group * 4 : 0];
     bool in[VPT], padded[VPT];  // columns of the matrix; of the codes
     uint32_t col[VPT];
-    int left[VPT];  // elements of the row from col on
+    int left[VPT];  // elements of the row from col on, 0 behind the last column
     F2 w[VPT][4], b[VPT][4], mask[VPT][ALIGNED ? 1 : 4];
     gq::PhiloxGroup pg[VPT];
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
         in[k] = c < a.cols;
         padded[k] = c < a.pitch;
         col[k] = in[k] ? c : 0u;
-        left[k] = static_cast<int>(a.cols - col[k]);
+        left[k] = in[k] ? static_cast<int>(a.cols - c) : 0;
 #pragma unroll
         for (int i = 0; i < (ALIGNED ? 1 : 4); ++i)
             mask[k][i] = f2(c + 2 * i < a.cols ? 1.0f : 0.0f,
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
         for (int k = 0; k < VPT; ++k) {
             R::read(slot + k * P * plane, plane, row_of(x, row, a.in) + col[k], left[k], v[k]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum = fma2(v[k][i], mask[k][ALIGNED ? 0 : i], sum);
+            for (int i = 0; i < 4; ++i) sum = add2(sum, v[k][i]);
         }
         float m[1] = {sum2(sum)};
         group_sum<W>(m, slots, wr, a.wpr, group);

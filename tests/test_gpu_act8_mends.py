@@ -307,3 +307,50 @@ def test_gradient_of_the_second_weight_is_not_rounded_to_bf16(layers, calls):
     assert dw2.dtype == db2.dtype == torch.float32
     assert ((dw2.double() - d.t() @ h).abs() <= (150 / 16 + 32) * 2.0 ** -22 * mag).all()
     assert ((db2.double() - d.sum(0)).abs() <= 190 * 2.0 ** -24 * d.abs().sum(0)).all()
+
+
+# ---- infinities ------------------------------------------------------------------------------
+
+WIDTHS = [1, 8, 40, 96, 200, 256, 264, 512, 520, 768, 1000, 1024, 1030, 2048, 2056, 3000, 4096, 5000, 8192, 8200, 9001]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_layernorm_of_an_infinity(gq, cols, dtype):
+    """The mean of a row that holds an infinity is that infinity, wherever it stands; its rstd and outputs
+    are NaN.  The other rows are as without it."""
+    x = torch.randn((9, cols), device="cuda").to(dtype)
+    y0, mean0, rstd0, _ = gq.gq_layernorm_forward(x)
+    x[2, 0], x[5, cols - 1], x[7, cols // 2] = float("inf"), float("-inf"), float("inf")
+    y, mean, rstd, act = gq.gq_layernorm_forward(x)
+    assert mean[[2, 5, 7]].tolist() == [float("inf"), float("-inf"), float("inf")]
+    rest = [0, 1, 3, 4, 6, 8]
+    assert y[[2, 5, 7]].isnan().all() and rstd[[2, 5, 7]].isnan().all()
+    assert gq.gq_act_dequantize(act)[[2, 5, 7]].isnan().all()
+    assert torch.equal(y[rest], y0[rest]) and torch.equal(mean[rest], mean0[rest])
+    assert torch.equal(rstd[rest], rstd0[rest])
+
+
+@pytest.mark.parametrize("source", ["codes", "input"])
+@pytest.mark.parametrize("cols", WIDTHS[1:])
+def test_layernorm_backward_of_an_infinite_gradient(gq, cols, source):
+    """dx of its row follows the formula's own infinities and NaNs; other rows and columns are finite."""
+    x = torch.randn((9, cols), device="cuda")
+    x[4] = x[4].abs()
+    w = 0.5 + torch.rand(cols, device="cuda")
+    _, mean, rstd, act = gq.gq_layernorm_forward(x, w)
+    dy = torch.randn((9, cols), device="cuda")
+    dy[4, 0] = float("inf")
+    if source == "codes":
+        got = gq.gq_layernorm_backward(dy, w, rstd, act=act)
+        hat = gq.gq_act_dequantize(act, out_dtype=torch.float32).double()
+    else:
+        got = gq.gq_layernorm_backward(dy, w, rstd, x=x, mean=mean)
+        hat = (x - mean[:, None]).double() * rstd.double()[:, None]
+    g = dy.double() * w.double()
+    want = rstd.double()[:, None] * (g - g.mean(1, keepdim=True) - hat * (g * hat).mean(1, keepdim=True))
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(got[0]), kind(want))
+    others = [0, 1, 2, 3, 5, 6, 7, 8]
+    assert got[0][others].isfinite().all()
+    assert got[2][0].isinf() and got[2][1:].isfinite().all() and got[1][1:].isfinite().all()
