@@ -138,11 +138,12 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// Adds the partial rows: 32 columns x 32 shares of the rows per block.
+// Adds the partial rows: 32 columns x 32 shares of the rows per block.  (partial is not __restrict__: the
+// main kernel may still write it when this one starts, so its loads must be ordinary ones, which stay behind
+// the wait.)
 template <typename G>
 __global__ void __launch_bounds__(1024)
-    sum_kernel(const float* __restrict__ partial, int parts, int64_t cols, G* __restrict__ dw,
-               G* __restrict__ db) {
+    sum_kernel(const float* partial, int parts, int64_t cols, G* dw, G* db) {
     __shared__ float tile[kSumRows][33];
     gq::pdl_wait();
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;

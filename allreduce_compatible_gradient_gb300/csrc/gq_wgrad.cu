@@ -293,7 +293,7 @@ __device__ __forceinline__ void finish(const WArgs& a, int64_t o, int64_t i, flo
             }
         }
         if (a.shift) {
-            const float d = __ldg(a.db + o);
+            const float d = a.db[o];  // not __ldg: written while the main kernel already runs
 #pragma unroll
             for (int k = 0; k < N; k += 4) {
                 const float4 f = __ldg(reinterpret_cast<const float4*>(a.shift + i + k));
@@ -833,8 +833,10 @@ __global__ void __launch_bounds__(1024)
         if (x == 0 && to < outs) partial[blockIdx.y * outs + to] = v;
     }
 }
+// (partial is not __restrict__: the launch before may still write it when this one starts, so its loads
+// must be ordinary ones, which stay behind the wait)
 __global__ void __launch_bounds__(256)
-    bias_sum_kernel(const float* __restrict__ partial, int parts, int64_t outs, float* db) {
+    bias_sum_kernel(const float* partial, int parts, int64_t outs, float* db) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
     __shared__ float tile[8][32];
     gq::pdl_launch_dependents();

@@ -354,3 +354,31 @@ def test_layernorm_backward_of_an_infinite_gradient(gq, cols, source):
     others = [0, 1, 2, 3, 5, 6, 7, 8]
     assert got[0][others].isfinite().all()
     assert got[2][0].isinf() and got[2][1:].isfinite().all() and got[1][1:].isfinite().all()
+
+
+# ---- launches that overlap -------------------------------------------------------------------
+
+def test_sums_of_an_overlapping_launch_are_its_own(gq):
+    """Back to back calls in one workspace, whose launches start before those ahead of them have ended:
+    every result is that of the call alone, bit for bit."""
+    shapes = [(600, 384, 256), (5000, 520, 264), (130, 70, 33)]
+    for rows, outs, cols in shapes:
+        x = torch.randn((rows, cols), device="cuda")
+        act, shift = gq.gq_act_quantize(x), torch.randn(cols, device="cuda")
+        rstd = torch.rand(rows, device="cuda")
+        grads = [torch.randn((rows, outs), device="cuda").bfloat16() * 10.0 ** i for i in range(4)]
+        dys = [torch.randn((rows, cols), device="cuda").bfloat16() * 10.0 ** i for i in range(4)]
+        want = []
+        for g, d in zip(grads, dys):
+            one = [*gq.gq_linear_wgrad(g, act, shift=shift), *gq.gq_layernorm_backward(d, None, rstd, act=act)]
+            torch.cuda.synchronize()
+            want.append(one)
+        ws = [torch.empty(gq.gq_linear_wgrad_workspace_bytes(grads[0], cols), dtype=torch.uint8, device="cuda"),
+              torch.empty(gq.gq_layernorm_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")]
+        got = []
+        for i in range(40):
+            got.append([*gq.gq_linear_wgrad(grads[i % 4], act, shift=shift, ws=ws[0]),
+                        *gq.gq_layernorm_backward(dys[i % 4], None, rstd, act=act, ws=ws[1])])
+        for i, one in enumerate(got):
+            for a, b in zip(one, want[i % 4]):
+                assert torch.equal(a, b)
