@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (VPT == 1 ? 3 : 2) : 1)
 
 // Partial rows: at most one per block of the main kernel, or the row shares of the column kernel.
 constexpr int kMostParts = 1024;
+inline int column_parts(int64_t rows) { return static_cast<int>((rows + 7) / 8 < 128 ? (rows + 7) / 8 : 128); }
 
 template <typename T>
 struct BackwardCall {
@@ -378,7 +379,7 @@ gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype,
         parts = vec && cols % 8 == 0 ? held_switch(h, BackwardHeld<T, true, CODES>{a, h})
                                      : held_switch(h, BackwardHeld<T, false, CODES>{a, h});
     } else {
-        parts = static_cast<int>((a.s.rows + 7) / 8 < 128 ? (a.s.rows + 7) / 8 : 128);
+        parts = column_parts(a.s.rows);
         if (vec) backward_generic<T, true, CODES>(a, parts, dw || db);
         else backward_generic<T, false, CODES>(a, parts, dw || db);
     }
@@ -410,8 +411,8 @@ extern "C" {
 size_t gq_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
     if (!size_ok(rows, cols)) return 0;
     if (rows == 0) return 16;
-    return static_cast<size_t>(rows < kMostParts ? rows : kMostParts) * 2 *
-           static_cast<size_t>(cols) * sizeof(float);
+    const int64_t parts = cols > kHeldCols ? column_parts(rows) : rows < kMostParts ? rows : kMostParts;
+    return static_cast<size_t>(parts) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 
 gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t cols, int64_t lddy,

@@ -382,3 +382,18 @@ def test_sums_of_an_overlapping_launch_are_its_own(gq):
         for i, one in enumerate(got):
             for a, b in zip(one, want[i % 4]):
                 assert torch.equal(a, b)
+
+
+# ---- workspaces ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", [(1, 8200), (9, 8193), (1030, 9000), (40, 16384), (300, 8192)])
+def test_layernorm_backward_stays_in_its_workspace(gq, rows, cols):
+    x = torch.randn((rows, cols), device="cuda").bfloat16()
+    _, _, rstd, act = gq.gq_layernorm_forward(x)
+    n = gq.gq_layernorm_workspace_bytes(rows, cols)
+    full = torch.full((n + 8192,), 77, dtype=torch.uint8, device="cuda")
+    want = gq.gq_layernorm_backward(x, None, rstd, act=act)
+    got = gq.gq_layernorm_backward(x, None, rstd, act=act, ws=full[4096:-4096])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert (full[:4096] == 77).all() and (full[-4096:] == 77).all()
