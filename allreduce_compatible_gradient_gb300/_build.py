@@ -11,6 +11,7 @@ units are compiled with contraction, and spell out the roundings that their code
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -93,16 +94,17 @@ def is_stale(lib: str = LIB) -> bool:
 
 def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Build libgq.so (debug: libgq_debug.so, with -DGQ_DEBUG) if missing or older than its
-    sources, and beside it the extension module of the activation operators; return the library's
-    path."""
+    sources, and beside it, where torch is installed, the extension module of the activation
+    operators; return the library's path.  The library itself needs nvcc alone."""
     lib = DEBUG_LIB if debug else LIB
-    native = native_path()
     building = None
-    if not debug and (force or not os.path.exists(native) or any(
-            os.path.getmtime(f) > os.path.getmtime(native)
-            for f in (NATIVE, os.path.join(ROOT, "include", "gq.h")))):
-        made = native + ".tmp.%d" % os.getpid()
-        building = subprocess.Popen(native_command(made))
+    if not debug and importlib.util.find_spec("torch") is not None:
+        native = native_path()
+        if force or not os.path.exists(native) or any(
+                os.path.getmtime(f) > os.path.getmtime(native)
+                for f in (NATIVE, os.path.join(ROOT, "include", "gq.h"))):
+            made = native + ".tmp.%d" % os.getpid()
+            building = subprocess.Popen(native_command(made))
     try:
         _build_cuda(lib, force, verbose, debug)
     finally:
