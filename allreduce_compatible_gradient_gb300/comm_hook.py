@@ -205,8 +205,9 @@ def _exp_ring(codes, state, step):
     return torch.cat([parts[c][:bounds[c][1] - bounds[c][0]] for c in range(n)])
 
 
-def global_qsgd_hook(state: GlobalQSGDState, bucket) -> torch.futures.Future:
-    """DDP communication hook: quantise, allreduce and dequantise one gradient bucket."""
+# (no return annotation: register_comm_hook takes Future[torch.Tensor] there, as an object, or none)
+def global_qsgd_hook(state: GlobalQSGDState, bucket):
+    """DDP communication hook: quantise, allreduce and dequantise one gradient bucket; a Future of it."""
     buf = bucket.buffer()
     if buf.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("Global-QSGD hook: gradients must be float32 or bfloat16, got %s" % buf.dtype)
