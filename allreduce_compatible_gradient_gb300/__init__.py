@@ -22,4 +22,4 @@ from ._activations import (  # noqa: F401
     ACT_NEAREST, ACT_RANDOM, GELU_ERF, GELU_TANH, Act8, gq_act_dequantize, gq_act_exp_pitch,
     gq_act_quantize, gq_gelu_backward, gq_gelu_forward, gq_layernorm_backward,
     gq_layernorm_forward, gq_layernorm_workspace_bytes, gq_linear_wgrad,
-    gq_linear_wgrad_workspace_bytes, load_native)
+    gq_linear_wgrad_plan, gq_linear_wgrad_workspace_bytes, load_native)

@@ -27,7 +27,8 @@ GELU_ERF, GELU_TANH = 0, 1
 _FORMS = {"none": GELU_ERF, "tanh": GELU_TANH}
 _FUNCTIONS = ("gq_act_quantize", "gq_act_dequantize", "gq_layernorm_forward",
               "gq_layernorm_workspace_bytes", "gq_layernorm_backward", "gq_gelu_forward",
-              "gq_gelu_backward", "gq_linear_wgrad_workspace_bytes", "gq_linear_wgrad")
+              "gq_gelu_backward", "gq_linear_wgrad_workspace_bytes", "gq_linear_wgrad_plan",
+              "gq_linear_wgrad")
 
 
 def load_native():
@@ -156,6 +157,14 @@ def gq_layernorm_workspace_bytes(rows: int, cols: int) -> int:
 
 def gq_linear_wgrad_workspace_bytes(dy: torch.Tensor, cols: int) -> int:
     return _native.linear_wgrad_workspace_bytes(dy, cols)
+
+
+_PLAN = ("tile_outs", "tile_cols", "steps", "shares", "own", "left", "longest", "chain")
+
+
+def gq_linear_wgrad_plan(dy: torch.Tensor, cols: int) -> dict:
+    """How gq_linear_wgrad divides its work for this dy and a checkpoint of `cols` columns (include/gq.h)."""
+    return dict(zip(_PLAN, _native.linear_wgrad_plan(dy, cols)))
 
 
 def gq_act_quantize(x, seed=None, step=0, stream=None) -> Act8:

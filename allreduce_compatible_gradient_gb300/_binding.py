@@ -90,6 +90,7 @@ def lib() -> ctypes.CDLL:
         "gq_gelu_forward": (ci, [vp, ci, i64, i64, i64, ci, vp, i64, ci, u64, u64, vp, vp, vp]),
         "gq_gelu_backward": (ci, [vp, ci, i64, i64, i64, vp, vp, ci, vp, i64, vp, i64, vp]),
         "gq_linear_wgrad_workspace_bytes": (sz, [vp, ci, i64, i64, i64, i64]),
+        "gq_linear_wgrad_plan": (ci, [vp, ci, i64, i64, i64, i64, ctypes.POINTER(i64)]),
         "gq_linear_wgrad": (ci, [vp, ci, i64, i64, i64, vp, vp, i64, vp, vp, vp, ci, i64, vp, vp, sz,
                                  vp]),
     }

@@ -29,6 +29,7 @@ struct Api {
     decltype(&gq_gelu_forward) gelu_forward;
     decltype(&gq_gelu_backward) gelu_backward;
     decltype(&gq_linear_wgrad_workspace_bytes) linear_wgrad_workspace_bytes;
+    decltype(&gq_linear_wgrad_plan) linear_wgrad_plan;
     decltype(&gq_linear_wgrad) linear_wgrad;
 };
 constexpr int kFunctions = sizeof(Api) / sizeof(void*);
@@ -431,6 +432,25 @@ PyObject* linear_wgrad_workspace_bytes(PyObject* const* a, Py_ssize_t n) {
         api.linear_wgrad_workspace_bytes(m.p, m.code, m.rows, m.cols, m.ld, signed64(a[1])));
 }
 
+// (dy, cols) -> 8 numbers
+PyObject* linear_wgrad_plan(PyObject* const* a, Py_ssize_t n) {
+    count(n, 2);
+    const Matrix m = matrix(tensor(a[0], "dy"), "dy");
+    const Place at(m.index);
+    int64_t p[8];
+    check(api.linear_wgrad_plan(m.p, m.code, m.rows, m.cols, m.ld, signed64(a[1]), p), "gq_linear_wgrad_plan");
+    PyObject* out = PyTuple_New(8);
+    for (Py_ssize_t i = 0; out && i < 8; ++i) {
+        PyObject* v = PyLong_FromLongLong(p[i]);
+        if (!v) {
+            Py_DECREF(out);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(out, i, v);
+    }
+    return out;
+}
+
 // (the package's GQError, the addresses of Api's functions)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     count(n, 1 + kFunctions);
@@ -466,6 +486,7 @@ PyMethodDef methods[] = {GQ_ENTRY(bind),
                          GQ_ENTRY(gelu_backward),
                          GQ_ENTRY(linear_wgrad),
                          GQ_ENTRY(linear_wgrad_workspace_bytes),
+                         GQ_ENTRY(linear_wgrad_plan),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gq_native", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};

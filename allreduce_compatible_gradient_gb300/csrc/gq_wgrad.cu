@@ -1010,6 +1010,28 @@ size_t gq_linear_wgrad_workspace_bytes(const void *dy, int dtype, int64_t rows, 
     return wgrad_plan(dy, dtype, rows, outs, lddy, cols).bytes;
 }
 
+gq_status gq_linear_wgrad_plan(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
+                               int64_t cols, int64_t *plan) {
+    if (!in_type(dtype) || !wgrad_sizes(rows, outs, cols) || !plan) return GQ_ERR_INVALID;
+    for (int i = 0; i < 8; ++i) plan[i] = 0;
+    if (rows == 0) return GQ_OK;
+    const WPlan p = wgrad_plan(dy, dtype, rows, outs, lddy, cols);
+    const int64_t tiles = p.tiles_m * p.tiles_n, own = tiles / p.shares, left = tiles % p.shares;
+    int64_t longest = own ? p.ksteps : 0, u = 0;
+    for (int64_t b = 0; b < p.shares; ++b) {
+        const int64_t end = u + left * p.ksteps / p.shares + (b < left * p.ksteps % p.shares ? 1 : 0);
+        while (u < end) {  // as far as the tile goes
+            const int64_t stop = (u / p.ksteps + 1) * p.ksteps, n = (stop < end ? stop : end) - u;
+            if (n > longest) longest = n;
+            u += n;
+        }
+    }
+    const int64_t out[8] = {p.big ? Large::kRows : Small::kRows, p.big ? Large::BN : Small::BN,
+                            p.ksteps, p.shares, own, left, longest, kChain};
+    for (int i = 0; i < 8; ++i) plan[i] = out[i];
+    return GQ_OK;
+}
+
 gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
                           const int8_t *codes, const uint8_t *exps, int64_t cols,
                           const float *scale, const float *shift, void *dw, int out_dtype,

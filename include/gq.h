@@ -541,6 +541,12 @@ gq_status gq_gelu_backward(const void *dh, int dtype, int64_t rows, int64_t cols
  */
 size_t gq_linear_wgrad_workspace_bytes(const void *dy, int dtype, int64_t rows, int64_t outs,
                                        int64_t lddy, int64_t cols);
+/* How the call divides its work, 8 numbers to plan (host memory): outs and columns of a tile; a tile's
+ * steps (64 tokens of one bf16 part of dy each); shares (blocks or pairs of blocks); whole tiles of each
+ * share; tiles left, whose steps the shares divide evenly; the longest run of one tile's steps in a share;
+ * the steps of one accumulation on the tensor cores (a longer run takes several, added in fp32). */
+gq_status gq_linear_wgrad_plan(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
+                               int64_t cols, int64_t *plan);
 gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs, int64_t lddy,
                           const int8_t *codes, const uint8_t *exps, int64_t cols,
                           const float *scale, const float *shift, void *dw, int out_dtype,
