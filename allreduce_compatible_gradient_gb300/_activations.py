@@ -95,7 +95,7 @@ class Act8:
         """The checkpoint whose `data` this is: for code that keeps tensors and not objects, as autograd
         functions do."""
         self = cls.__new__(cls)
-        self.shape = (data.shape[0], cols) if shape is None else shape
+        self.shape = (data.shape[0], cols) if shape is None else tuple(shape)
         self._cols, self._codes, self._exps = cols, data, None
         return self
 

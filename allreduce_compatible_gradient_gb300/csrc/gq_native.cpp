@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <memory>
 
 #include "gq.h"
 
@@ -277,9 +278,11 @@ PyObject* act_dequantize(PyObject* const* a, Py_ssize_t n) {
         const int64_t c = signed64(a[5]);
         if (c != GQ_F32 && c != GQ_BF16 && c != GQ_F16)
             refuse(PyExc_TypeError, "values are float32, bfloat16 or float16");
+        const std::unique_ptr<PyObject, void (*)(PyObject*)> sizes(PySequence_Tuple(a[3]), Py_DecRef);
+        if (!sizes) throw Refused{};
         c10::SmallVector<int64_t, 8> shape;
-        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[3]); ++i)
-            shape.push_back(signed64(PyTuple_GET_ITEM(a[3], i)));
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(sizes.get()); ++i)
+            shape.push_back(signed64(PyTuple_GET_ITEM(sizes.get(), i)));
         out = empty(shape, scalar_of(static_cast<int>(c)), s.index);
     } else {
         out = tensor(a[4], "out");

@@ -384,6 +384,19 @@ def test_sums_of_an_overlapping_launch_are_its_own(gq):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("shape,ok", [([2, 20, 96], True), (torch.Size([40, 96]), True), (None, False), (7, False),
+                                      ([40, "96"], False), ([40, 95], False), ([-1, 96], False), ([3840], False)])
+def test_a_checkpoints_shape_may_be_any_sequence(gq, shape, ok):
+    """`shape` is an attribute that a program can set: a list is taken, what is no shape is refused."""
+    act = gq.gq_act_quantize(torch.randn((40, 96), device="cuda"))
+    act.shape = shape
+    if ok:
+        assert gq.gq_act_dequantize(act).shape == torch.Size(shape)
+    else:
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            gq.gq_act_dequantize(act)
+
+
 # ---- workspaces ------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,cols", [(1, 8200), (9, 8193), (1030, 9000), (40, 16384), (300, 8192)])
