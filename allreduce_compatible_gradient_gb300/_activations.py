@@ -4,7 +4,9 @@ section on activations): argument checks and marshalling over libgq.so, like _bi
 Matrices are CUDA tensors of at least two dimensions whose last one is contiguous and whose
 leading ones can be viewed as one (rows may be further apart than their length); float32 or
 bfloat16.  Outputs are new tensors of the same leading shape.  With `stream`, the call runs on that
-stream and its new tensors belong to it.
+stream and its new tensors belong to it.  Like every call of this package they are not recorded by
+autograd: outputs do not require gradients, whatever the inputs do (act8_layers has autograd functions
+over them).
 
 The checks, the allocations and the calls are in csrc/gq_native.cpp: on a small matrix they would take
 longer in Python than the kernels on the GPU.

@@ -4,9 +4,10 @@
 // next to that by the instructions it issues (random rounding above all: a Philox call per 8
 // elements).  A thread owns a piece of 16 columns (half a block of the format; the other half is its
 // neighbour's) and walks down the rows, so that the column part of the random words is computed once
-// and the next rows' copies are in flight meanwhile.  At 32,768 x 4,096 bf16 (268 MB) saving takes 64 us
-// rounding to nearest and 77 at random (5.3 TB/s, its issue slots 69 % busy), reading back 62 (6.5 TB/s),
-// GELU forward with the checkpoint 109 (6.2 TB/s), backward with the output 150 (6.3 TB/s).
+// and the next rows' copies are in flight meanwhile.  At 32,768 x 4,096 bf16 (268 MB), call after call with
+// inputs that change, saving takes 69 us rounding to nearest (5.9 TB/s) and 78 at random (its issue slots
+// 69 % busy), reading back 73 (5.6 TB/s), GELU forward 92 without a checkpoint, 121 with one rounded to
+// nearest (5.6 TB/s) and 137 at random, backward 121 and with the output 155 (6.1 TB/s).
 #include "gq_act.cuh"
 
 #include <type_traits>
@@ -18,11 +19,13 @@ namespace {
 constexpr int kT = 256;  // threads per block
 
 // ---- GELU ----------------------------------------------------------------------------------
-// Normal distribution function at -|u|: q(|u|) = t P(t) exp(-u^2 / 2), t = 1 / (1 + p |u|).  The
-// polynomials are least-maximum fits of erfc(z) exp(z^2) / 2 over 0 <= u <= 14 (computed for this
-// file by iteratively reweighted least squares on Chebyshev nodes); relative error below 1.5e-7
-// (8 coefficients, fp32 outputs) or 5e-6 (6 coefficients, bf16 outputs, whose own rounding is
-// 2e-3).  One exponential serves the distribution and the density.  Two elements are worked on
+// Normal distribution function at -|u|: q(|u|) = t P(t) exp(-u^2 / 2), t = 1 / (1 + p |u|), the form of
+// Hastings' approximations (1955).  The polynomials are least-maximum fits of erfc(z) exp(z^2) / 2, z =
+// u / sqrt 2, over 0 <= u <= 14 (computed for this file by iteratively reweighted least squares on
+// Chebyshev nodes); the fit's relative error is below 1.7e-7 (8 coefficients, fp32 outputs) or 4.7e-6 (6
+// coefficients, bf16 outputs, whose own rounding is 2e-3).  GELU as computed for fp32 outputs is within
+// 2.7e-7 |u| of its value everywhere, and within 5.4e-7 of it for |u| < 1, 2.1e-6 down to u = -6 and 8.1e-6
+// down to -13, where the rounding of u^2 / 2 enters through the exponential.  One exponential serves the distribution and the density.  Two elements are worked on
 // at a time (pairs of fp32): instructions, not memory, bounded the first form of the backward pass
 // (32,768 x 4,096 bf16 with the output: 239 us one at a time, 150 so, of which the memory needs 139).
 template <bool WIDE> struct Tail;

@@ -1,5 +1,5 @@
-// gq_act.cuh -- device and host pieces shared by the activation kernels (gq_act.cu,
-// gq_layernorm.cu, gq_wgrad.cu): element access, the 8-bit block format and its two roundings.
+// gq_act.cuh -- device and host pieces shared by the activation kernels (gq_act.cu, gq_layernorm_fwd.cu,
+// gq_layernorm_bwd.cu, gq_wgrad.cu): element access, the 8-bit block format and its two roundings.
 //
 // Format: a row of `cols` elements is cut into blocks of 32 columns.  A block with largest
 // magnitude a has the exponent byte E = min{ E >= 1 : a <= 127 * 2^(E - 127) }, 255 if it holds

@@ -6,13 +6,14 @@
 //   backward  dx = rstd (w dy - mean(w dy) - xh mean(w dy xh));  dw = sum_rows dy xh;
 //             db = sum_rows dy
 //
-// Both are bound by memory, and next to that by their instructions (65,536 x 1,024 bf16: forward 41 us
-// without a checkpoint, 54 with one rounded to nearest, 71 at random, of which the memory needs 40, 50
-// and 50; backward 59 from x and 61 from codes, of which it needs 59 and 50).  A row stays in
+// Both are bound by memory, and next to that by what a row does one after the other with 16 warps per SM
+// to overlap it (65,536 x 1,024 bf16, inputs changing from call to call: forward 46 us without a
+// checkpoint, 58 with one rounded to nearest, 71 at random, of which the memory needs 40, 50 and 50;
+// backward 70 from x and 64 from codes, of which it needs 59 and 50).  A row stays in
 // registers between its reductions, so it is read once ("rows held by fixed threads"); the generic
 // kernels take rows of more columns than a block holds, and read again what does not fit their registers
 // (from L2, mostly).  That form costs more: as many bytes in 4,096 x 8,192 and 4,092 x 8,200 bf16 take 37
-// and 68 us forward, 44 and 129 backward from codes (whose columns' sums are a second kernel there).
+// and 69 us forward, 45 and 133 backward from codes (whose columns' sums are a second kernel there).
 // All sums are fp32.
 #pragma once
 #include "gq_act.cuh"
@@ -270,9 +271,11 @@ inline bool held_ok(int64_t cols, int64_t ld_bytes) {
 }
 
 // Threads of the held form: pieces of 8 columns per thread, warps per row, rows per block.  One piece
-// per thread where two would leave a quarter of them idle in whole warps: up to 256 columns, and from
-// 513 to 768 (43,690 x 768 bf16, backward from codes: 50 us with two pieces, 39 with one; at 1,024
-// columns two are faster, see above).  Eight warps a block, two blocks per SM: three, with 84
+// per thread up to 256 columns, where one warp holds a row so, and from 513 to 768, where three warps do
+// and two of two pieces would idle for a quarter of the time or more (43,690 x 768 bf16, backward from
+// codes: 50 us with two pieces, 39 with one; at 1,024 columns two are faster, see above).  From 1,025 to
+// 1,152 columns two pieces leave a quarter to a third of three warps idle too; one piece, in five warps
+// with a reduction of more steps and one row per block, was not measured there.  Eight warps a block, two blocks per SM: three, with 84
 // registers a thread, took the forward pass at 65,536 x 1,024 from 72 to 78 us.  With fewer rows than
 // two per SM a block takes one at a time: there is nothing to share, and the sums need not be put
 // together within the block.

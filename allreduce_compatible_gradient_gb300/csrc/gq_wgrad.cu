@@ -29,13 +29,15 @@
 // tiles in the workspace, which join_kernel adds in a fixed order.
 //
 // The tensor cores' fp32 accumulation rounds each sum of 16 products towards zero or nearly so, an error
-// that grows with the length of the chain (5.8e-6 of the result's norm over 16,384 tokens): a chain ends
-// after kChain steps, and the rest is added to it in fp32 outside (1.6e-6; an fp32 product by the
-// library has 2.2e-6).
+// that grows with the length of the chain (5.8e-6 of the result's norm over 16,384 tokens in one): a chain
+// ends after kChain steps, and the rest is added to it in fp32 outside.  Errors against 64 bits, normal
+// numbers: 1.7e-6 at 6,144 and at 16,384 tokens (the library's product of the same bf16 matrices 2.0e-6 and
+// 7.5e-6, its product of fp32 ones 0.3e-6 and 0.5e-6), 4.8e-7 at 2,048 (4.8e-7, 1.3e-7), 7.8e-8 at 384
+// (7.8e-8, 4.9e-8).
 //
 // What bounds it: the tensor cores, and the ends of the chains, when 256 KB of sums per block leave or
-// cross the L2.  4,096 x 4,096 x 16,384 tokens, bf16: 333 us without db (the library's product of two
-// bf16 matrices 285; chains of 256 steps would take 310), 360 with it.  Tiles side by side, a chain's
+// cross the L2.  4,096 x 4,096 x 16,384 tokens, bf16: 335 us without db (the library's product of two
+// bf16 matrices 285; chains of 256 steps would take 310), 383 with it, inputs changing.  Tiles side by side, a chain's
 // steps widened ahead, its accumulators finished one after the other, and first chains of different
 // lengths took it there from 352 and 379.
 #include "gq_act.cuh"
@@ -137,7 +139,10 @@ template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // blocks.  What an arrival announces are operands in shared memory, made visible to the tensor cores
 // by a proxy fence or written by the TMA, and registers read from TMEM, ordered by a tcgen05 fence; no
 // thread of the other block reads them with ordinary loads, so the arrival is not a release at cluster
-// scope (which waits for every store of the thread: 1,600 cycles, most of a step).
+// scope (which waits for every store of the thread: 1,600 cycles, most of a step).  The PTX memory model
+// promises the order of ordinary accesses between two blocks for the cluster's scope alone; what is relied
+// on here instead is that a proxy fence makes the stores before it visible to the async proxy, through which
+// the tensor cores read the shared memory of both blocks, before the arrival behind it is counted.
 template <int CG> __device__ __forceinline__ uint32_t pair_rank() {
     uint32_t r = 0;
     if constexpr (CG == 2) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -931,8 +936,9 @@ WPlan wgrad_plan(const void* dy, int dtype, int64_t rows, int64_t outs, int64_t 
         };
         if (tiles <= most) {
             consider(tiles, static_cast<double>(p.ksteps), true);
-            const int64_t q = most / tiles;  // shares per tile, none of which crosses tiles
-            // (adding the partial tiles takes about 0.15 us for each of a tile's)
+            // k shares for each tile; where k does not divide the steps some lie across two tiles and leave
+            // two partial tiles, which is not counted (adding them takes about 0.15 us for each of a tile's)
+            const int64_t q = most / tiles;
             for (int64_t k = 2; k <= q && p.ksteps >= 2 * k; k = k < 8 ? k + 1 : k * 5 / 4)
                 consider(tiles * k, static_cast<double>((p.ksteps + k - 1) / k) + 0.15 * k / step, false);
         }
