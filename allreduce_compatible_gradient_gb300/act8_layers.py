@@ -101,10 +101,11 @@ class MlpBlock8(nn.Module):
     """x + W2 gelu(W1 norm(x) + b1) + b2 with 8-bit checkpoints.
 
     `step` numbers the training steps: set it before each forward pass (below 2^48; another one each time,
-    where a block is applied more than once), so that every pass rounds with words of its own.  Data-parallel ranks need words of their own too: `rank` (below 2^16)
-    tells them apart, torch.distributed's where it is None and a process group is there, else 0.  Every
-    block has its own words; `seed` names them instead, for words that a later run can draw again, and then
-    blocks of one model need different seeds."""
+    where a block is applied more than once), so that every pass rounds with words of its own.
+    Data-parallel ranks need words of their own too: `rank` (below 2^16) tells them apart,
+    torch.distributed's where it is None and a process group is there, else 0.  Every block has its own
+    words; `seed` names them instead, for words that a later run can draw again, and then blocks of one
+    model need different seeds.  A captured CUDA graph replays the words of its capture."""
 
     def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
                  seed: int | None = None, device=None, rank: int | None = None):

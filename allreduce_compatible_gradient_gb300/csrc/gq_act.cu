@@ -25,9 +25,10 @@ constexpr int kT = 256;  // threads per block
 // Chebyshev nodes); the fit's relative error is below 1.7e-7 (8 coefficients, fp32 outputs) or 4.7e-6 (6
 // coefficients, bf16 outputs, whose own rounding is 2e-3).  GELU as computed for fp32 outputs is within
 // 2.7e-7 |u| of its value everywhere, and within 5.4e-7 of it for |u| < 1, 2.1e-6 down to u = -6 and 8.1e-6
-// down to -13, where the rounding of u^2 / 2 enters through the exponential.  One exponential serves the distribution and the density.  Two elements are worked on
-// at a time (pairs of fp32): instructions, not memory, bounded the first form of the backward pass
-// (32,768 x 4,096 bf16 with the output: 239 us one at a time, 150 so, of which the memory needs 139).
+// down to -13, where the rounding of u^2 / 2 enters through the exponential.  One exponential serves the
+// distribution and the density.  Two elements are worked on at a time (pairs of fp32): instructions, not
+// memory, bounded the first form of the backward pass (32,768 x 4,096 bf16 with the output: 239 us one at a
+// time, 150 so, of which the memory needs 139).
 template <bool WIDE> struct Tail;
 template <> struct Tail<true> {
     static constexpr float p = 0.30f;
@@ -221,8 +222,8 @@ template <typename T> __device__ __forceinline__ uint32_t top16(const uint32_t (
     }
 }
 
-// Stores a lane's 16 elements of a row that is not 16-byte aligned, of which `left` lie in the row.  adjoins: the lane before holds what is in front of them.  16-byte granules are put together
-// from two neighbours' words; only where a neighbour is missing, and at the row's end, are elements
+// Stores a lane's 16 elements of a row that is not 16-byte aligned, of which `left` lie in the row.
+// adjoins: the lane before holds what is in front of them.  16-byte granules are put together from two neighbours' words; only where a neighbour is missing, and at the row's end, are elements
 // stored one by one.  The whole warp takes part.
 template <typename T>
 __device__ __forceinline__ void put_words(T* p, int left, bool adjoins, const uint32_t (&w)[kWords<T>]) {

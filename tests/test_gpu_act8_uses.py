@@ -237,7 +237,8 @@ def test_frozen_parameters_cost_no_gradient(layers, calls, wanted, called):
     assert set(got) == set(wanted)
     for k, g in got.items():
         # (a bias' gradient alone is a plain sum, of another order)
-        assert torch.equal(g, want[k]) if k != "b1" or "w1" in wanted else torch.allclose(g, want[k], rtol=1e-3, atol=1e-4)
+        exact = k != "b1" or "w1" in wanted
+        assert torch.equal(g, want[k]) if exact else torch.allclose(g, want[k], rtol=1e-3, atol=1e-4)
     short = {"gq_gelu_backward": "gelu", "gq_linear_wgrad": "wgrad", "gq_layernorm_backward": "norm"}
     assert [short[n] for n, *_ in calls if n in short] == called
 
@@ -410,3 +411,52 @@ def test_layernorm_backward_stays_in_its_workspace(gq, rows, cols):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert (full[:4096] == 77).all() and (full[-4096:] == 77).all()
+
+
+# ---- other uses ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(0, 96), (2, 0, 96), (96,), (1, 96), (3, 1, 96)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_inputs_without_rows_and_single_rows(layers, shape, dtype):
+    block = block_of(layers)
+    x = torch.randn(shape, device="cuda").to(dtype).requires_grad_()
+    out = block(x)
+    got = torch.autograd.grad(out.float().sum(), [x, *block.parameters()])
+    assert out.shape == x.shape
+    for g, p in zip(got, [x, *block.parameters()]):
+        assert g.shape == p.shape and g.isfinite().all()
+        assert x.numel() or not g.any()
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_recomputed_blocks_give_the_same_gradients(layers, reentrant):
+    """torch.utils.checkpoint over a block: the first pass or the second makes the checkpoints."""
+    from torch.utils.checkpoint import checkpoint
+    block = block_of(layers)
+    x = torch.randn((40, 96), device="cuda", requires_grad=True)
+    want = torch.autograd.grad(block(x).square().sum(), [x, *block.parameters()])
+    checkpoint(block, x, use_reentrant=reentrant).square().sum().backward()
+    for p, w in zip([x, *block.parameters()], want):
+        assert torch.equal(p.grad, w)
+
+
+def test_a_captured_step_replays(layers):
+    block = block_of(layers)
+    x = torch.randn((40, 96), device="cuda", requires_grad=True)
+
+    def step():
+        return torch.autograd.grad(block(x).square().sum(), [x, *block.parameters()])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for g in got:
+        g.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
