@@ -36,7 +36,7 @@ def lib() -> ctypes.CDLL:
                           "g.build()\"` first; there is no fallback path" % _LIB_PATH)
     L = ctypes.CDLL(_LIB_PATH)
     i64, u64, vp, ci = ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int
-    sz = ctypes.c_size_t
+    sz, f64 = ctypes.c_size_t, ctypes.c_double
     sig = {
         "gq_abi_version": (ci, []),
         "gq_workspace_bytes": (sz, [i64, i64]),
@@ -93,6 +93,17 @@ def lib() -> ctypes.CDLL:
         "gq_linear_wgrad_plan": (ci, [vp, ci, i64, i64, i64, i64, ctypes.POINTER(i64)]),
         "gq_linear_wgrad": (ci, [vp, ci, i64, i64, i64, vp, vp, i64, vp, vp, vp, ci, i64, vp, vp, sz,
                                  vp]),
+        "gq_fp8_code_pitch": (i64, [i64]),
+        "gq_fp8_exp_bytes": (sz, [i64, i64]),
+        "gq_fp8_quantize": (ci, [vp, ci, i64, i64, i64, ci, vp, vp, vp, vp]),
+        "gq_fp8_dequantize": (ci, [vp, vp, i64, i64, vp, ci, i64, vp]),
+        "gq_fp8_linear": (ci, [vp, ci, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp, ci, i64, vp]),
+        "gq_fp8_linear_dgrad": (ci, [vp, ci, i64, vp, vp, i64, i64, vp, vp, i64, vp, ci, i64, vp]),
+        "gq_tensors_norm_workspace_bytes": (sz, [i64]),
+        "gq_tensors_norm": (ci, [i64, vp, vp, ci, vp, vp, sz, vp]),
+        "gq_adamw_step": (ci, [i64, vp, ci, vp, ci, vp, vp, vp, vp, i64, vp, f64, f64, f64, f64, f64, vp,
+                               f64, ci, u64, i64, vp]),
+        "gq_adamw_values": (ci, [i64, vp, vp, vp, vp, vp, vp, ci, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

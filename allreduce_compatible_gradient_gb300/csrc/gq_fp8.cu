@@ -1,0 +1,250 @@
+// gq_fp8.cu -- a matrix into 8-bit floating point with a scale for each block of 128, and back (C ABI in
+// include/gq.h; the format is described in gq_fp8.cuh).
+//
+// Both directions are one pass over the data, bound by memory: bytes in flight and few instructions.
+#include "gq_fp8.cuh"
+
+using namespace gqa;
+
+namespace {
+
+// The granules that hold 8 elements at p: nothing is read where left <= 0, and no granule behind the last one
+// with an element that is wanted.
+template <typename T, bool ALIGNED> struct Granules {
+    static constexpr int P = sizeof(T) / 2 + (ALIGNED ? 0 : 1);
+    uint32_t w[4 * P];
+    uint32_t m;
+    __device__ __forceinline__ void fetch(const T* p, int left) {
+        const uint8_t* q = reinterpret_cast<const uint8_t*>(p);
+        m = ALIGNED ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 15u;
+        const int bytes = left > 0 ? static_cast<int>(m) + min(left, 8) * static_cast<int>(sizeof(T)) : 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint4 g = 16 * i < bytes ? __ldg(reinterpret_cast<const uint4*>(q - m) + i)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * i] = g.x; w[4 * i + 1] = g.y; w[4 * i + 2] = g.z; w[4 * i + 3] = g.w;
+        }
+    }
+    __device__ __forceinline__ void values(int left, F2 (&v)[4]) {
+        pairs(shifted<T, ALIGNED>(w, m, min(max(left, 0), 8)), v);
+    }
+};
+
+__device__ __forceinline__ uint32_t top8(const F2 (&h)[4]) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        split(h[i], a, b);
+        m = max(m, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    }
+    return m;
+}
+
+// One exponent per row and 128 columns.  A warp takes rows r, r + 32, r + 64, r + 96 of 128 and 512 columns,
+// 256 at a time: 16 lanes hold a block, and its first lane ends up with the 16 exponents that lie side by
+// side.  Four rows' loads are on their way at a time.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(256)
+    rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, int64_t words,
+                int64_t tasks, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+    gq::pdl_launch_dependents();  // a product that follows waits before it reads
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < tasks;
+         t += static_cast<int64_t>(gridDim.x) * 8) {
+        // neighbouring warps take neighbouring columns of the same rows
+        const int64_t word = t % words, r0 = t / words / 32 * 128 + (t / words & 31);
+        uint32_t e4[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c = word * 512 + h * 256 + lane * 8;
+            const int left = static_cast<int>(min(cols - c, int64_t(8)));
+            Granules<T, ALIGNED> g[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                g[j].fetch(x + (r0 + 32 * j) * ld + c, r0 + 32 * j < rows ? left : 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                F2 v[4];
+                g[j].values(r0 + 32 * j < rows ? left : 0, v);
+                uint32_t m = top8(v);
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+                const uint32_t e = fp8_exp_byte(m);
+                uint2 q = fp8_codes8(v, inv_step(e));
+                if (e == 255u) q = make_uint2(0u, 0u);
+                if (r0 + 32 * j < rows && c < pitch)
+                    *reinterpret_cast<uint2*>(codes + (r0 + 32 * j) * pitch + c) = q;
+                // blocks 2 h and 2 h + 1 of the word
+                e4[j] |= (e | __shfl_down_sync(kFull, e, 16) << 8) << (16 * h);
+            }
+        }
+        if (lane == 0)
+            *reinterpret_cast<uint4*>(exps + (r0 / 128 * words + word) * kExpTile + (r0 & 31) * 16) =
+                make_uint4(e4[0], e4[1], e4[2], e4[3]);
+    }
+}
+
+// One exponent per 128 x 128 elements, written for every row (exps) and every column (exps_t, nullable).
+// Block = one tile, 64 elements per thread.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(256)
+    tiles_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, int64_t across,
+                 uint8_t* __restrict__ codes, uint8_t* __restrict__ exps, uint8_t* __restrict__ exps_t) {
+    gq::pdl_launch_dependents();
+    __shared__ uint32_t most[8];
+    const int64_t tr = blockIdx.x / across, tc = blockIdx.x % across;
+    const int64_t r0 = tr * 128 + (threadIdx.x >> 4), c = tc * 128 + (threadIdx.x & 15) * 8;
+    const int left = static_cast<int>(min(cols - c, int64_t(8)));
+    F2 v[8][4];
+    uint32_t m = 0u;
+    constexpr int B = 4;  // loads on their way
+#pragma unroll
+    for (int i = 0; i < 8; i += B) {
+        Granules<T, ALIGNED> g[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            g[k].fetch(x + (r0 + 16 * (i + k)) * ld + c, r0 + 16 * (i + k) < rows ? left : 0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            g[k].values(r0 + 16 * (i + k) < rows ? left : 0, v[i + k]);
+            m = max(m, top8(v[i + k]));
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, most[i]);
+    const uint32_t e = fp8_exp_byte(m);
+    const float inv = inv_step(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint2 q = fp8_codes8(v[i], inv);
+        if (e == 255u) q = make_uint2(0u, 0u);
+        if (r0 + 16 * i < rows && c < pitch)
+            *reinterpret_cast<uint2*>(codes + (r0 + 16 * i) * pitch + c) = q;
+    }
+    const int k = threadIdx.x & 127;  // 4-byte places of 128 rows, each for 4 blocks
+    if (threadIdx.x < 128)
+        exps[(tr * exp_words(cols) + (tc >> 2)) * kExpTile + k * 4 + (tc & 3)] = static_cast<uint8_t>(e);
+    else if (exps_t)
+        exps_t[(tc * exp_words(rows) + (tr >> 2)) * kExpTile + k * 4 + (tr & 3)] = static_cast<uint8_t>(e);
+}
+
+// 16 columns of a row per thread, which are in one block.
+template <typename O, int ALIGN>
+__global__ void __launch_bounds__(256)
+    values_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t cols,
+                  int64_t pitch, int64_t words, int64_t pieces, int64_t across, O* __restrict__ out, int64_t ld) {
+    constexpr int B = 2;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < pieces; t += B * stride) {
+        uint4 q[B];
+        uint32_t e[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int64_t at = t + k * stride;
+            if (at >= pieces) break;
+            const int64_t row = at / across, c = at % across * 16;
+            q[k] = __ldg(reinterpret_cast<const uint4*>(codes + row * pitch + c));
+            e[k] = __ldg(exps + (row / 128 * words + c / 512) * kExpTile + (row & 31) * 16 + (row >> 5 & 3) * 4 +
+                         (c >> 7 & 3));
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int64_t at = t + k * stride;
+            if (at >= pieces) break;
+            const int64_t row = at / across, c = at % across * 16;
+            const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+            const F2 s = f2(step_of(e[k]));
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const F2 p = mul2(fp8_values2(w[i >> 1] >> (16 * (i & 1))), s);
+                split(p, v[2 * i], v[2 * i + 1]);
+            }
+            O* to = out + row * ld;
+            if constexpr (ALIGN > 0) {
+                store<O, 16, ALIGN>(to, c, cols, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < cols) down(v[i], to[c + i]);
+            }
+        }
+    }
+}
+
+template <typename T>
+gq_status quantize(const T* x, int64_t rows, int64_t cols, int64_t ld, bool tiles, uint8_t* codes,
+                   uint8_t* exps, uint8_t* exps_t, cudaStream_t st) {
+    const int64_t pitch = fp8_pitch(cols), words = exp_words(cols);
+    const bool aligned = row_align(x, sizeof(T) == 4 ? GQ_F32 : GQ_BF16, rows, ld) != 0;
+    if (tiles) {
+        const int64_t across = (cols + 127) / 128, n = (rows + 127) / 128 * across;
+        auto k = aligned ? tiles_kernel<T, true> : tiles_kernel<T, false>;
+        k<<<static_cast<unsigned>(n), 256, 0, st>>>(x, ld, rows, cols, pitch, across, codes, exps, exps_t);
+        return gqh::launch_status();
+    }
+    const int64_t tasks = (rows + 127) / 128 * 32 * words;
+    auto k = aligned ? rows_kernel<T, true> : rows_kernel<T, false>;
+    const int64_t most = resident_blocks(k, 256, 0), need = (tasks + 7) / 8;
+    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(x, ld, rows, cols, pitch, words, tasks,
+                                                                        codes, exps);
+    return gqh::launch_status();
+}
+
+template <typename O>
+gq_status dequantize(const uint8_t* codes, const uint8_t* exps, int64_t rows, int64_t cols, O* out, int dtype,
+                     int64_t ld, cudaStream_t st) {
+    const int64_t across = (cols + 15) / 16, pieces = rows * across;
+    const int a = row_align(out, dtype, rows, ld);
+    auto k = a == 32 ? values_kernel<O, 32> : a == 16 ? values_kernel<O, 16> : values_kernel<O, 0>;
+    const int64_t most = resident_blocks(k, 256, 0), need = (pieces + 255) / 256;
+    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(
+        codes, exps, cols, fp8_pitch(cols), exp_words(cols), pieces, across, out, ld);
+    return gqh::launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gq_fp8_code_pitch(int64_t cols) { return cols < 1 ? 0 : fp8_pitch(cols); }
+
+size_t gq_fp8_exp_bytes(int64_t rows, int64_t cols) {
+    return !size_ok(rows, cols) ? 0 : static_cast<size_t>(exp_bytes(rows, cols));
+}
+
+gq_status gq_fp8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int block_rows,
+                          uint8_t *codes, uint8_t *exps, uint8_t *exps_t, void *stream) {
+    if (!in_type(dtype) || !size_ok(rows, cols) || !matrix_ok(x, dtype, rows, cols, ldx)) return GQ_ERR_INVALID;
+    if ((block_rows != 1 && block_rows != 128) || (block_rows == 1 && exps_t)) return GQ_ERR_INVALID;
+    if ((rows + 127) / 128 * ((cols + 127) / 128) >= (int64_t(1) << 31)) return GQ_ERR_INVALID;
+    if (rows == 0) return GQ_OK;
+    if (!saved_ok(codes, exps) || !mult(exps_t, 16)) return GQ_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == GQ_F32 ? quantize(static_cast<const float*>(x), rows, cols, ldx, block_rows > 1, codes, exps,
+                                      exps_t, st)
+                           : quantize(static_cast<const bf16*>(x), rows, cols, ldx, block_rows > 1, codes, exps,
+                                      exps_t, st);
+}
+
+gq_status gq_fp8_dequantize(const uint8_t *codes, const uint8_t *exps, int64_t rows, int64_t cols, void *out,
+                            int out_dtype, int64_t ldout, void *stream) {
+    if ((!in_type(out_dtype) && out_dtype != GQ_F16) || !size_ok(rows, cols) ||
+        !matrix_ok(out, out_dtype, rows, cols, ldout))
+        return GQ_ERR_INVALID;
+    if (rows == 0) return GQ_OK;
+    if (!saved_ok(codes, exps)) return GQ_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (out_dtype == GQ_F32)
+        return dequantize(codes, exps, rows, cols, static_cast<float*>(out), out_dtype, ldout, st);
+    if (out_dtype == GQ_BF16)
+        return dequantize(codes, exps, rows, cols, static_cast<bf16*>(out), out_dtype, ldout, st);
+    return dequantize(codes, exps, rows, cols, static_cast<__half*>(out), out_dtype, ldout, st);
+}
+
+}  // extern "C"

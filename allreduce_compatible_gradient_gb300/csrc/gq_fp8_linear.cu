@@ -1,0 +1,366 @@
+// gq_fp8_linear.cu -- products of a linear layer on operands in 8-bit floating point (C ABI in
+// include/gq.h; the format is described in gq_fp8.cuh).
+//
+//   forward   y[t, o]  = sum_i X[t, i] W[o, i] + bias[o]
+//   gradient  dx[t, i] = sum_o DY[t, o] W[o, i]
+//
+// Both are D[m, t] = sum_k A[m, k] B[t, k] with A = W or its transposed matrix and B the tokens' operand.
+// The outputs are the tensor cores' rows (128 of them) and the tokens their columns (16 to 128), so that a
+// few tokens leave no tensor core idle rows to work on, and a warp with a lane per output stores 32
+// neighbouring ones.  W is stored once: the gradient's product reads the same bytes with the outer dimension
+// contiguous.  Scales are block scales of tcgen05.mma: the four instructions of a step of 128 take the
+// same byte of each operand's exponents.
+//
+// Small form: a block per tile, and where there are few tiles a cluster of up to 8 blocks per tile, each with
+// a part of the sum; the parts are added through distributed shared memory in the blocks' order.
+//   warp 0   TMA loads of both operands (128 of k per step) and bulk copies of exponents (512 of k each)
+//   warp 1   one thread copies exponents to TMEM and issues tcgen05.mma, accumulators in TMEM
+//   2 to 5   the sums from TMEM to memory
+#include "gq_fp8.cuh"
+#include "gq_tc.cuh"
+
+using namespace gqa;
+
+namespace {
+
+constexpr int kStep = 128;             // of k per step: bytes of a row of an operand's tile
+constexpr int kTile = 128 * kStep;     // bytes of a tile of W
+
+struct LArgs {
+    int rows, m;                 // tokens, outputs
+    int steps;                   // of k
+    int tiles_m;
+    const uint8_t* a_exps;       // of W (or its transposed matrix), of the tokens' operand
+    const uint8_t* b_exps;
+    const float* bias;           // nullable
+    void* y;
+    int64_t ldy;
+    int out_f32;
+};
+
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                        uint32_t sb, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add ? 1u : 0u)
+        : "memory");
+}
+// 32 rows of 16 bytes to 4 columns of TMEM, in each of its four quarters.
+__device__ __forceinline__ void copy_exps(uint32_t tmem, uint64_t smem) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(smem) : "memory");
+}
+// Rows of 128 bytes, 128-byte swizzle, 8 rows every 1,024 bytes: along k (128 of k of a row of the matrix)
+// and along the outer dimension (128 outer elements of a k) alike.
+__device__ __forceinline__ uint64_t operand(uint32_t smem) {
+    return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// Exponents: rows of 16 bytes one after the other, 8 of them every 128 bytes, no swizzle.
+__device__ __forceinline__ uint64_t exp_operand(uint32_t smem) {
+    return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (uint64_t(1) << 46);
+}
+// e4m3 operands, exponent bytes as scales, N columns, M = 128; a_outer: A is contiguous along its outer
+// dimension.  The scales' byte of a word is added per step.
+template <int N, bool A_OUTER> struct Instruction {
+    static constexpr uint32_t value = (A_OUTER ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+                                      (1u << 23) | (128u >> 4 << 24);
+    static __device__ __forceinline__ uint32_t of(uint32_t byte) { return value | byte << 4 | byte << 29; }
+};
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float peer_load(uint32_t smem, uint32_t rank) {
+    uint32_t there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    return v;
+}
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void put(const LArgs& a, int64_t token, int out, float v) {
+    if (a.out_f32) static_cast<float*>(a.y)[token * a.ldy + out] = v;
+    else static_cast<bf16*>(a.y)[token * a.ldy + out] = __float2bfloat16_rn(v);
+}
+
+// BN tokens per tile: fewer than 128 only where one tile holds all of them, so that a tile's exponents begin
+// with its first row.
+template <int BN_> struct Small {
+    static constexpr int BN = BN_;
+    static constexpr int kBytes = kTile + BN * kStep;      // of a step's operands
+    static constexpr int kStages = 6;
+    static constexpr int kCols = BN <= 16 ? 32 : BN <= 32 ? 64 : BN <= 64 ? 128 : 256;  // of TMEM
+    // columns behind the accumulator: two sets of 4 for W's exponents and 4 for the tokens', in turn
+    static constexpr int kExps = BN;
+    static_assert(kExps + 16 <= kCols, "exponents fit behind the accumulator");
+    static constexpr int kSmem = kStages * (kBytes + 2 * kExpTile) + 1024;
+    static_assert(128 * BN * 4 <= kStages * kBytes, "a block's sums fit in its operands' place");
+};
+
+template <typename C, bool A_OUTER>
+__global__ void __launch_bounds__(192, 1)
+    small_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                 const LArgs a) {
+    constexpr int BN = C::BN, S = C::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ alignas(8) uint64_t full[S], empty[S], acc_full, drain;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank(), parts = cluster_size();
+    auto a_stage = [&](int s) { return base + s * C::kBytes; };
+    auto b_stage = [&](int s) { return base + s * C::kBytes + kTile; };
+    auto e_stage = [&](int s) { return base + S * C::kBytes + s * 2 * kExpTile; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            gq::mbar_init(gq::smem_u32(&full[s]), 1u);
+            gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
+        }
+        gq::mbar_init(gq::smem_u32(&acc_full), 1u);
+        gq::mbar_init(gq::smem_u32(&drain), 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<1>(gq::smem_u32(&tmem_slot), C::kCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int tile = blockIdx.x / parts;
+    const int m0 = tile % a.tiles_m * 128, t0 = tile / a.tiles_m * BN;
+    const int words = (a.steps + 3) / 4;
+    const int k0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / parts);
+    const int k1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / parts);
+    // exponents come with the first step of the block's, and with each that begins 512 of k
+    auto with_exps = [&](int k) { return k == k0 || (k & 3) == 0; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            // W's side of a step, then the tokens': the launch before may still write those
+            auto load_a = [&](int k, int s) {
+                const uint32_t bar = gq::smem_u32(&full[s]);
+                gq::mbar_arrive_expect_tx(bar, C::kBytes + (with_exps(k) ? 2 * kExpTile : 0));
+                tma_load(a_stage(s), &a_map, A_OUTER ? m0 : k * kStep, A_OUTER ? k * kStep : m0, bar);
+                if (with_exps(k))
+                    bulk_load(e_stage(s), a.a_exps + (static_cast<int64_t>(m0 / 128) * words + k / 4) * kExpTile,
+                              kExpTile, bar);
+            };
+            auto load_b = [&](int k, int s) {
+                const uint32_t bar = gq::smem_u32(&full[s]);
+                tma_load(b_stage(s), &b_map, k * kStep, t0, bar);
+                if (with_exps(k))
+                    bulk_load(e_stage(s) + kExpTile,
+                              a.b_exps + (static_cast<int64_t>(t0 / 128) * words + k / 4) * kExpTile, kExpTile, bar);
+            };
+            const int first = min(k1 - k0, S);
+            for (int n = 0; n < first; ++n) load_a(k0 + n, n);
+            gq::pdl_wait();
+            for (int n = 0; n < first; ++n) load_b(k0 + n, n);
+            int n = first;
+            for (; n < k1 - k0; ++n) {
+                ok = gq::mbar_wait(gq::smem_u32(&empty[n % S]), ((n / S) - 1) & 1);
+                if (!ok) break;
+                load_a(k0 + n, n % S);
+                load_b(k0 + n, n % S);
+            }
+            // nothing of this block's is in flight when it ends, whatever the others did
+            for (int j = n > S ? n - S : 0; j < n; ++j) gq::mbar_wait(gq::smem_u32(&full[j % S]), (j / S) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t set = 1;  // of exponents' columns
+            for (int n = 0; n < k1 - k0; ++n) {
+                const int k = k0 + n, s = n % S;
+                ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
+                if (!ok) break;
+                fence_after();
+                if (with_exps(k)) {
+                    set ^= 1u;
+                    copy_exps(tmem + C::kExps + 8 * set, exp_operand(e_stage(s)));
+                    copy_exps(tmem + C::kExps + 8 * set + 4, exp_operand(e_stage(s) + kExpTile));
+                }
+#pragma unroll
+                for (int kk = 0; kk < kStep / 32; ++kk)
+                    mma_fp8(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)), operand(b_stage(s) + kk * 32),
+                            Instruction<BN, A_OUTER>::of(k & 3), tmem + C::kExps + 8 * set,
+                            tmem + C::kExps + 8 * set + 4, n > 0 || kk > 0);
+                mma_commit<1>(gq::smem_u32(&empty[s]));
+            }
+            mma_commit<1>(gq::smem_u32(ok ? &acc_full : &drain));
+            if (!ok) gq::mbar_wait(gq::smem_u32(&drain), 0);  // what was issued finishes before TMEM is freed
+        }
+    } else {
+        const int q = warp & 3, m = q * 32 + lane;
+        bool ok = k1 <= k0 || gq::mbar_wait(gq::smem_u32(&acc_full), 0);
+        ok = __all_sync(kFull, ok);
+        fence_after();
+        const float b = a.bias && m0 + m < a.m ? __ldg(a.bias + m0 + m) : 0.0f;
+        float* sums = reinterpret_cast<float*>(raw + (base - gq::smem_u32(raw)));
+        gq::pdl_wait();  // y may be what the launch before still reads
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 16) {
+            if (t0 + c >= a.rows) break;
+            uint32_t v[16];
+            tmem_load16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+            if (!ok) {  // a wait gave up: the tile is marked
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0x7FFFFFFFu;
+            }
+            if (parts > 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + m] = __uint_as_float(v[i]);
+            } else if (m0 + m < a.m) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (t0 + c + i < a.rows) put(a, t0 + c + i, m0 + m, __uint_as_float(v[i]) + b);
+            }
+        }
+    }
+    fence_before();
+    __syncwarp();
+    if (parts > 1) {
+        cluster_sync();
+        if (warp >= 2) {
+            const int m = (warp - 2) * 32 + lane;
+            const float b = a.bias && m0 + m < a.m ? __ldg(a.bias + m0 + m) : 0.0f;
+            for (int c = rank; c < BN && t0 + c < a.rows; c += parts) {
+                float v = 0.0f;
+                for (uint32_t r = 0; r < parts; ++r) v += peer_load(base + (c * 128 + m) * 4, r);
+                if (m0 + m < a.m) put(a, t0 + c, m0 + m, v + b);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no block's sums are read any more
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) tmem_free<1>(tmem, C::kCols);
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+// A matrix of bytes, `rows` of them `pitch` apart with `width` elements each, in boxes of 128 x `box`.
+bool byte_map(CUtensorMap* map, const uint8_t* p, int64_t width, int64_t rows, int64_t pitch, int box) {
+    EncodeFn encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t sizes[2] = {kStep, static_cast<cuuint32_t>(box)}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, sizes, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// early: the launch before this one on the stream wrote the tokens' operand, and let this one start.
+template <typename C, bool A_OUTER>
+gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, int parts, bool early,
+                       cudaStream_t st) {
+    auto k = small_kernel<C, A_OUTER>;
+    gqh::blocks_per_sm(k, C::kSmem, 192);  // raises the shared-memory limit once
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * ((a.rows + C::BN - 1) / C::BN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * parts));
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a) != cudaSuccess) return GQ_ERR_CUDA;
+    return gqh::launch_status();
+}
+
+// D = A B^T as above: `outs` rows of A, sums over `depth`.
+template <bool A_OUTER>
+gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_t* xexps, int64_t rows,
+                  int64_t depth, const uint8_t* wcodes, const uint8_t* wexps, int64_t outs, const float* bias,
+                  void* y, int out_dtype, int64_t ldy, cudaStream_t st) {
+    const int64_t most = int64_t(1) << 30;
+    if (!in_type(out_dtype) || !size_ok(rows, depth) || outs < 1 || rows >= most || depth >= most || outs >= most)
+        return GQ_ERR_INVALID;
+    if (!matrix_ok(y, out_dtype, rows, outs, ldy) || !mult(bias, 4)) return GQ_ERR_INVALID;
+    if (x && (!in_type(dtype) || !matrix_ok(x, dtype, rows, depth, ldx))) return GQ_ERR_INVALID;
+    if (rows == 0) return GQ_OK;
+    if (!saved_ok(xcodes, xexps) || !saved_ok(wcodes, wexps)) return GQ_ERR_INVALID;
+    const int64_t sms = gqh::sm_count(), tiles_m = (outs + 127) / 128, steps = (depth + kStep - 1) / kStep;
+    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    const int64_t tiles = tiles_m * ((rows + bn - 1) / bn);
+    if (tiles * 8 >= int64_t(1) << 31) return GQ_ERR_INVALID;
+    CUtensorMap a_map, b_map;
+    if (!byte_map(&a_map, wcodes, A_OUTER ? outs : depth, A_OUTER ? depth : outs,
+                  fp8_pitch(A_OUTER ? outs : depth), 128) ||
+        !byte_map(&b_map, xcodes, depth, rows, fp8_pitch(depth), bn))
+        return GQ_ERR_CUDA;
+    if (x) {
+        const gq_status r = gq_fp8_quantize(x, dtype, rows, depth, ldx, 1, xcodes, xexps, nullptr, st);
+        if (r != GQ_OK) return r;
+    }
+    LArgs a;
+    a.rows = static_cast<int>(rows); a.m = static_cast<int>(outs);
+    a.steps = static_cast<int>(steps); a.tiles_m = static_cast<int>(tiles_m);
+    a.a_exps = wexps; a.b_exps = xexps; a.bias = bias;
+    a.y = y; a.ldy = ldy; a.out_f32 = out_dtype == GQ_F32;
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= sms && steps >= parts * 2) parts *= 2;
+    switch (bn) {
+        case 16: return launch_small<Small<16>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
+        case 32: return launch_small<Small<32>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
+        case 64: return launch_small<Small<64>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
+        default: return launch_small<Small<128>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+gq_status gq_fp8_linear(const void *x, int dtype, int64_t ldx, uint8_t *xcodes, uint8_t *xexps, int64_t rows,
+                        int64_t cols, const uint8_t *wcodes, const uint8_t *wexps, int64_t outs,
+                        const float *bias, void *y, int out_dtype, int64_t ldy, void *stream) {
+    return product<false>(x, dtype, ldx, xcodes, xexps, rows, cols, wcodes, wexps, outs, bias, y, out_dtype, ldy,
+                          static_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_fp8_linear_dgrad(const void *dy, int dtype, int64_t lddy, uint8_t *dycodes, uint8_t *dyexps,
+                              int64_t rows, int64_t outs, const uint8_t *wcodes, const uint8_t *wexps_t,
+                              int64_t cols, void *dx, int out_dtype, int64_t lddx, void *stream) {
+    return product<true>(dy, dtype, lddy, dycodes, dyexps, rows, outs, wcodes, wexps_t, cols, nullptr, dx,
+                         out_dtype, lddx, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,4 +1,5 @@
-// gq_native.cpp -- Python entry points of the activation operators (include/gq.h) on torch tensors.
+// gq_native.cpp -- Python entry points of the operators around the linear layers of a training step and of
+// the optimizer's step (include/gq.h) on torch tensors.
 //
 // Argument checks, allocation of outputs and the call of libgq.so, in C++: a call on a small matrix
 // takes 3 to 5 us on the GPU, and the same marshalling in Python took 11 to 22 us on the host.  The
@@ -13,8 +14,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <memory>
+#include <vector>
 
 #include "gq.h"
 
@@ -32,6 +35,14 @@ struct Api {
     decltype(&gq_linear_wgrad_workspace_bytes) linear_wgrad_workspace_bytes;
     decltype(&gq_linear_wgrad_plan) linear_wgrad_plan;
     decltype(&gq_linear_wgrad) linear_wgrad;
+    decltype(&gq_fp8_quantize) fp8_quantize;
+    decltype(&gq_fp8_dequantize) fp8_dequantize;
+    decltype(&gq_fp8_linear) fp8_linear;
+    decltype(&gq_fp8_linear_dgrad) fp8_linear_dgrad;
+    decltype(&gq_tensors_norm_workspace_bytes) tensors_norm_workspace_bytes;
+    decltype(&gq_tensors_norm) tensors_norm;
+    decltype(&gq_adamw_step) adamw_step;
+    decltype(&gq_adamw_values) adamw_values;
 };
 constexpr int kFunctions = sizeof(Api) / sizeof(void*);
 Api api;
@@ -454,6 +465,387 @@ PyObject* linear_wgrad_plan(PyObject* const* a, Py_ssize_t n) {
     return out;
 }
 
+// ---- 8-bit floating point ------------------------------------------------------------------
+
+int64_t fp8_exp_bytes(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 511) / 512) * 512; }
+
+// A matrix in 8-bit floating point as the package passes it: (codes, exps, exps_t or None, rows, columns,
+// tiles), or (bytes, None, None, ...) with the codes, the exponents and (tiles) those of the transposed matrix
+// one after the other.  Checked against the size at every call, like Saved.
+struct Fp8 {
+    uint8_t *codes = nullptr, *exps = nullptr, *exps_t = nullptr;
+    int64_t rows = 0, cols = 0;
+    bool tiles = false;
+    int index = 0;
+    explicit Fp8(PyObject* const* a) : rows(signed64(a[3])), cols(signed64(a[4])), tiles(truth(a[5])) {
+        const at::Tensor& c = tensor(a[0], "the matrix's codes");
+        if (rows < 0 || cols < 1 || rows >= int64_t(1) << 31 || cols >= int64_t(1) << 31)
+            refuse(PyExc_ValueError, "the matrix has no such size");
+        const int64_t pitch = (cols + 15) / 16 * 16, e = fp8_exp_bytes(rows, cols), et = fp8_exp_bytes(cols, rows);
+        if (a[1] == Py_None) {
+            codes = bytes(c, rows * pitch + e + (tiles ? et : 0), c);
+            exps = codes + rows * pitch;
+            if (tiles) exps_t = exps + e;
+        } else {
+            codes = bytes(c, rows * pitch, c);
+            exps = bytes(tensor(a[1], "the matrix's exponents"), e, c);
+            if (a[2] != Py_None) exps_t = bytes(tensor(a[2], "the transposed matrix's exponents"), et, c);
+        }
+        index = c.get_device();
+    }
+    static uint8_t* bytes(const at::Tensor& t, int64_t n, const at::Tensor& beside) {
+        if (!t.is_cuda() || t.get_device() != beside.get_device() || t.element_size() != 1 || t.numel() != n ||
+            !t.is_contiguous())
+            refuse(PyExc_ValueError, "the matrix must be contiguous bytes on one CUDA device, %lld in one of its parts",
+                   static_cast<long long>(n));
+        return static_cast<uint8_t*>(t.data_ptr());
+    }
+};
+
+// (x, tiles) -> data
+PyObject* fp8_quantize(PyObject* const* a, Py_ssize_t n) {
+    count(n, 2);
+    const Matrix m = matrix(tensor(a[0], "x"), "x");
+    const bool tiles = truth(a[1]);
+    const Place at(m.index);
+    const int64_t codes = m.rows * ((m.cols + 15) / 16 * 16), e = fp8_exp_bytes(m.rows, m.cols);
+    const at::Tensor data =
+        empty({codes + e + (tiles ? fp8_exp_bytes(m.cols, m.rows) : 0)}, at::kByte, m.index);
+    uint8_t* p = static_cast<uint8_t*>(data.data_ptr());
+    check(api.fp8_quantize(m.p, m.code, m.rows, m.cols, m.ld, tiles ? 128 : 1, p, p + codes,
+                           tiles ? p + codes + e : nullptr, at.stream),
+          "gq_fp8_quantize");
+    return wrap(data);
+}
+
+c10::SmallVector<int64_t, 8> sizes_of(PyObject* o) {
+    const std::unique_ptr<PyObject, void (*)(PyObject*)> sizes(PySequence_Tuple(o), Py_DecRef);
+    if (!sizes) throw Refused{};
+    c10::SmallVector<int64_t, 8> shape;
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(sizes.get()); ++i)
+        shape.push_back(signed64(PyTuple_GET_ITEM(sizes.get(), i)));
+    return shape;
+}
+
+// (matrix x 6, shape, out or None, type code) -> out
+PyObject* fp8_dequantize(PyObject* const* a, Py_ssize_t n) {
+    count(n, 9);
+    const Fp8 s(a);
+    const Place at(s.index);
+    at::Tensor out;
+    if (a[7] == Py_None) {
+        const int64_t c = signed64(a[8]);
+        if (c != GQ_F32 && c != GQ_BF16 && c != GQ_F16)
+            refuse(PyExc_TypeError, "values are float32, bfloat16 or float16");
+        out = empty(sizes_of(a[6]), scalar_of(static_cast<int>(c)), s.index);
+    } else {
+        out = tensor(a[7], "out");
+    }
+    const Matrix m = matrix(out, "out", true);
+    if (m.rows != s.rows || m.cols != s.cols || m.index != s.index)
+        refuse(PyExc_ValueError, "out must hold %lld x %lld on cuda:%d", static_cast<long long>(s.rows),
+               static_cast<long long>(s.cols), s.index);
+    check(api.fp8_dequantize(s.codes, s.exps, s.rows, s.cols, m.p, m.code, m.ld, at.stream), "gq_fp8_dequantize");
+    return wrap(out);
+}
+
+// The tokens' operand of a product: a tensor, whose codes then live in `own` for the call, or a matrix in
+// 8-bit floating point.
+struct Tokens {
+    const void* p = nullptr;
+    int code = GQ_BF16, index = 0;
+    int64_t ld = 0, rows = 0, cols = 0;
+    uint8_t *codes = nullptr, *exps = nullptr;
+    c10::SmallVector<int64_t, 8> shape;  // of the tensor it was made from
+    at::Tensor own;
+    Tokens(PyObject* const* a, const char* what) {  // tensor or None, matrix x 6 or None x 6, shape or None
+        if (a[0] != Py_None) {
+            const at::Tensor& x = tensor(a[0], what);
+            const Matrix m = matrix(x, what);
+            p = m.p; code = m.code; index = m.index; ld = m.ld; rows = m.rows; cols = m.cols;
+            shape.append(x.sizes().begin(), x.sizes().end());
+        } else {
+            const Fp8 s(a + 1);
+            if (s.tiles)
+                refuse(PyExc_ValueError, "%s must have an exponent for each of its rows' blocks (tiles=False)", what);
+            index = s.index; rows = s.rows; cols = s.cols; codes = s.codes; exps = s.exps;
+            shape = sizes_of(a[7]);
+        }
+    }
+    void make() {
+        if (codes || !p) return;
+        const int64_t pitch = (cols + 15) / 16 * 16;
+        own = empty({rows * pitch + fp8_exp_bytes(rows, cols)}, at::kByte, index);
+        codes = static_cast<uint8_t*>(own.data_ptr());
+        exps = codes + rows * pitch;
+    }
+    at::Tensor result(int64_t width, PyObject* type) {
+        c10::SmallVector<int64_t, 8> size(shape);
+        size.back() = width;
+        return empty(size, scalar_of(output_code(type, "out_dtype")), index);
+    }
+};
+
+// (x or None, matrix x 6 or None x 6, shape or None, weight x 6, bias or None, type code) -> y
+PyObject* fp8_linear(PyObject* const* a, Py_ssize_t n) {
+    count(n, 16);
+    Tokens x(a, "x");
+    const Fp8 w(a + 8);
+    if (w.cols != x.cols || w.index != x.index)
+        refuse(PyExc_ValueError, "the weight holds %lld x %lld on cuda:%d", static_cast<long long>(w.rows),
+               static_cast<long long>(w.cols), w.index);
+    if (w.rows < 1) refuse(PyExc_ValueError, "the weight has no rows");
+    int f32 = GQ_F32;
+    const float* bias = static_cast<const float*>(vector(a[14], w.rows, x.index, &f32, "bias"));
+    const Place at(x.index);
+    x.make();
+    const at::Tensor y = x.result(w.rows, a[15]);
+    check(api.fp8_linear(x.p, x.code, x.ld, x.codes, x.exps, x.rows, x.cols, w.codes, w.exps, w.rows, bias,
+                         y.data_ptr(), type_code(y.scalar_type()), w.rows, at.stream),
+          "gq_fp8_linear");
+    return wrap(y);
+}
+
+// (dy or None, matrix x 6 or None x 6, shape or None, weight x 6, type code) -> dx
+PyObject* fp8_linear_dgrad(PyObject* const* a, Py_ssize_t n) {
+    count(n, 15);
+    Tokens dy(a, "dy");
+    const Fp8 w(a + 8);
+    if (w.rows != dy.cols || w.index != dy.index)
+        refuse(PyExc_ValueError, "the weight holds %lld x %lld on cuda:%d", static_cast<long long>(w.rows),
+               static_cast<long long>(w.cols), w.index);
+    if (!w.exps_t) refuse(PyExc_ValueError, "the weight has no exponents of its transposed matrix (tiles=True)");
+    const Place at(dy.index);
+    dy.make();
+    const at::Tensor dx = dy.result(w.cols, a[14]);
+    check(api.fp8_linear_dgrad(dy.p, dy.code, dy.ld, dy.codes, dy.exps, dy.rows, dy.cols, w.codes, w.exps_t,
+                               w.cols, dx.data_ptr(), type_code(dx.scalar_type()), w.cols, at.stream),
+          "gq_fp8_linear_dgrad");
+    return wrap(dx);
+}
+
+// ---- the optimizer's step ------------------------------------------------------------------
+
+// A list or tuple, borrowed for the call.
+struct Items {
+    PyObject* seq;
+    Py_ssize_t n;
+    Items(PyObject* o, const char* what) {
+        if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(PyExc_TypeError, "%s must be a list or a tuple", what);
+        seq = PySequence_Fast(o, what);
+        if (!seq) throw Refused{};
+        n = PySequence_Fast_GET_SIZE(seq);
+    }
+    ~Items() { Py_DECREF(seq); }
+    Items(const Items&) = delete;
+    PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+};
+
+// A contiguous tensor of a list, on the list's device; index < 0 before the first.
+const at::Tensor& part(PyObject* o, int* index, const char* what) {
+    const at::Tensor& t = tensor(o, what);
+    if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous CUDA tensors", what);
+    if (*index < 0) *index = t.get_device();
+    if (t.get_device() != *index) refuse(PyExc_ValueError, "%s must be on cuda:%d like the others", what, *index);
+    return t;
+}
+void same_type(int* code, const at::Tensor& t, const char* what) {
+    const int c = type_code(t.scalar_type());
+    if (c != GQ_F32 && c != GQ_BF16) refuse(PyExc_TypeError, "%s must be float32 or bfloat16", what);
+    if (*code >= 0 && *code != c) refuse(PyExc_TypeError, "%s must be of one type", what);
+    *code = c;
+}
+// Autograd's count of in-place changes: a backward pass that saved the old values refuses the new ones.
+void changed(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+struct State {
+    void *m, *v;
+    uint8_t* e = nullptr;
+};
+// (m, v) fp32, or (m, v, exps) bytes of a tensor of n elements.
+State state(PyObject* o, int64_t n, int* index, bool eight, bool written) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != (eight ? 3 : 2))
+        refuse(PyExc_TypeError, "states must be Adam8, or pairs of float32 tensors, all of one kind");
+    const at::Tensor &m = part(PyTuple_GET_ITEM(o, 0), index, "states"),
+                     &v = part(PyTuple_GET_ITEM(o, 1), index, "states");
+    State s;
+    if (eight) {
+        const at::Tensor& e = part(PyTuple_GET_ITEM(o, 2), index, "states");
+        const int64_t room = (n + 31) / 32 * 32;
+        if (m.scalar_type() != at::kByte || v.scalar_type() != at::kByte || e.scalar_type() != at::kByte)
+            refuse(PyExc_TypeError, "8-bit states must be uint8 tensors");
+        if (m.numel() != room || v.numel() != room || e.numel() != room / 16)
+            refuse(PyExc_ValueError, "an 8-bit state of %lld elements has %lld, %lld and %lld bytes",
+                   static_cast<long long>(n), static_cast<long long>(room), static_cast<long long>(room),
+                   static_cast<long long>(room / 16));
+        s.e = static_cast<uint8_t*>(e.data_ptr());
+        if (written) changed(e);
+    } else {
+        if (m.scalar_type() != at::kFloat || v.scalar_type() != at::kFloat)
+            refuse(PyExc_TypeError, "states must be Adam8, or pairs of float32 tensors, all of one kind");
+        if (m.numel() != n || v.numel() != n)
+            refuse(PyExc_ValueError, "a state must have its parameter's %lld elements", static_cast<long long>(n));
+    }
+    s.m = m.data_ptr();
+    s.v = v.data_ptr();
+    if (written) {
+        changed(m);
+        changed(v);
+    }
+    return s;
+}
+bool in_8_bits(const Items& states) {
+    return states.n > 0 && PyTuple_Check(states[0]) && PyTuple_GET_SIZE(states[0]) == 3;
+}
+double number(PyObject* o, const char* what) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(PyExc_TypeError, "%s must be a number", what);
+    }
+    return v;
+}
+const float* scalar(PyObject* o, int index, const char* what) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, what);
+    if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != at::kFloat || t.numel() != 1)
+        refuse(PyExc_ValueError, "%s must be one float32 number on cuda:%d", what, index);
+    return static_cast<const float*>(t.data_ptr());
+}
+
+// (tensors, ws or None) -> norm
+PyObject* tensors_norm(PyObject* const* a, Py_ssize_t n) {
+    count(n, 2);
+    const Items list(a[0], "tensors");
+    if (list.n == 0) refuse(PyExc_ValueError, "there are no tensors");
+    std::vector<const void*> p(list.n);
+    std::vector<int64_t> numel(list.n);
+    int index = -1, code = -1;
+    for (Py_ssize_t i = 0; i < list.n; ++i) {
+        const at::Tensor& t = part(list[i], &index, "tensors");
+        same_type(&code, t, "tensors");
+        p[i] = t.data_ptr();
+        numel[i] = t.numel();
+    }
+    const Place at(index);
+    const Workspace ws(a[1], a[1] == Py_None ? api.tensors_norm_workspace_bytes(list.n) : 0, index);
+    const at::Tensor norm = empty({1}, at::kFloat, index);
+    check(api.tensors_norm(list.n, p.data(), numel.data(), code, static_cast<float*>(norm.data_ptr()), ws.p, ws.bytes,
+                           at.stream),
+          "gq_tensors_norm");
+    return wrap(norm);
+}
+
+// (params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm or None, max_norm or None, seed or
+// None, first) -> None
+PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
+    count(n, 13);
+    const Items params(a[0], "params"), grads(a[1], "grads"), states(a[2], "states");
+    if (grads.n != params.n || states.n != params.n)
+        refuse(PyExc_ValueError, "%zd parameters, %zd gradients and %zd states", params.n, grads.n, states.n);
+    if (params.n == 0) return Py_NewRef(Py_None);
+    const bool eight = in_8_bits(states);
+    std::vector<void*> p(params.n), m(params.n), v(params.n);
+    std::vector<const void*> g(params.n);
+    std::vector<uint8_t*> e(eight ? params.n : 0);
+    std::vector<int64_t> numel(params.n);
+    int index = -1, pcode = -1, gcode = -1;
+    for (Py_ssize_t i = 0; i < params.n; ++i) {
+        const at::Tensor &t = part(params[i], &index, "params"), &d = part(grads[i], &index, "grads");
+        same_type(&pcode, t, "params");
+        same_type(&gcode, d, "grads");
+        numel[i] = t.numel();
+        if (d.numel() != numel[i])
+            refuse(PyExc_ValueError, "gradient %zd has %lld elements, its parameter %lld", i,
+                   static_cast<long long>(d.numel()), static_cast<long long>(numel[i]));
+        p[i] = t.data_ptr();
+        g[i] = d.data_ptr();
+        const State s = state(states[i], numel[i], &index, eight, false);
+        m[i] = s.m;
+        v[i] = s.v;
+        if (eight) e[i] = s.e;
+    }
+    std::vector<void*> once;
+    once.reserve(3 * params.n);
+    for (Py_ssize_t i = 0; i < params.n; ++i)
+        if (numel[i] > 0) once.insert(once.end(), {p[i], m[i], v[i]});
+    std::sort(once.begin(), once.end());
+    if (std::adjacent_find(once.begin(), once.end()) != once.end())
+        refuse(PyExc_ValueError, "a parameter or a state is there twice");
+    const int64_t* counter = nullptr;
+    int64_t step = 1;
+    if (THPVariable_Check(a[3])) {
+        const at::Tensor& t = THPVariable_Unpack(a[3]);
+        if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != at::kLong || t.numel() != 1)
+            refuse(PyExc_ValueError, "step must be a number, or one int64 number on cuda:%d", index);
+        counter = static_cast<const int64_t*>(t.data_ptr());
+    } else {
+        step = signed64(a[3]);
+        if (step < 1) refuse(PyExc_ValueError, "step must be at least 1");
+    }
+    const double lr = number(a[4], "lr"), beta1 = number(a[5], "betas"), beta2 = number(a[6], "betas"),
+                 eps = number(a[7], "eps"), decay = number(a[8], "weight_decay");
+    if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0))
+        refuse(PyExc_ValueError, "betas must be at least 0 and below 1");
+    if (!(eps >= 0.0)) refuse(PyExc_ValueError, "eps must not be negative");
+    const float* norm = scalar(a[9], index, "norm");
+    double most = -1.0;
+    if (a[10] != Py_None) {
+        most = number(a[10], "max_norm");
+        if (!(most >= 0.0)) refuse(PyExc_ValueError, "max_norm must not be negative");
+        if (!norm) refuse(PyExc_ValueError, "max_norm needs the norm");
+    }
+    const uint64_t seed = a[11] == Py_None ? 0 : unsigned64(a[11], "seed");
+    const int64_t first = signed64(a[12]);
+    if (first < 0 || first + params.n > int64_t(1) << 30) refuse(PyExc_ValueError, "first is out of range");
+    const Place at(index);
+    check(api.adamw_step(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(), eight ? e.data() : nullptr,
+                         numel.data(), step, counter, lr, beta1, beta2, eps, decay, norm, most,
+                         a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first, at.stream),
+          "gq_adamw_step");
+    for (Py_ssize_t i = 0; i < params.n; ++i) {
+        changed(THPVariable_Unpack(params[i]));
+        state(states[i], numel[i], &index, eight, true);
+    }
+    return Py_NewRef(Py_None);
+}
+
+// (states, moments, roots: lists of tensors, of which the first give the elements) -> None
+PyObject* adamw_values(PyObject* const* a, Py_ssize_t n) {
+    count(n, 3);
+    const Items states(a[0], "states"), moments(a[1], "out"), roots(a[2], "out");
+    if (moments.n != states.n || roots.n != states.n)
+        refuse(PyExc_ValueError, "%zd states, %zd and %zd outputs", states.n, moments.n, roots.n);
+    if (states.n == 0) return Py_NewRef(Py_None);
+    std::vector<const uint8_t*> m(states.n), v(states.n), e(states.n);
+    std::vector<void*> x(states.n), r(states.n);
+    std::vector<int64_t> numel(states.n);
+    int index = -1, code = -1;
+    for (Py_ssize_t i = 0; i < states.n; ++i) {
+        const at::Tensor &t = part(moments[i], &index, "out"), &u = part(roots[i], &index, "out");
+        same_type(&code, t, "out");
+        same_type(&code, u, "out");
+        numel[i] = t.numel();
+        if (u.numel() != numel[i]) refuse(PyExc_ValueError, "the outputs of state %zd differ in size", i);
+        const State s = state(states[i], numel[i], &index, true, false);
+        m[i] = static_cast<const uint8_t*>(s.m);
+        v[i] = static_cast<const uint8_t*>(s.v);
+        e[i] = s.e;
+        x[i] = t.data_ptr();
+        r[i] = u.data_ptr();
+    }
+    const Place at(index);
+    check(api.adamw_values(states.n, m.data(), v.data(), e.data(), numel.data(), x.data(), r.data(), code, at.stream),
+          "gq_adamw_values");
+    for (Py_ssize_t i = 0; i < states.n; ++i) {
+        changed(THPVariable_Unpack(moments[i]));
+        changed(THPVariable_Unpack(roots[i]));
+    }
+    return Py_NewRef(Py_None);
+}
+
 // (the package's GQError, the addresses of Api's functions)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     count(n, 1 + kFunctions);
@@ -490,6 +882,13 @@ PyMethodDef methods[] = {GQ_ENTRY(bind),
                          GQ_ENTRY(linear_wgrad),
                          GQ_ENTRY(linear_wgrad_workspace_bytes),
                          GQ_ENTRY(linear_wgrad_plan),
+                         GQ_ENTRY(fp8_quantize),
+                         GQ_ENTRY(fp8_dequantize),
+                         GQ_ENTRY(fp8_linear),
+                         GQ_ENTRY(fp8_linear_dgrad),
+                         GQ_ENTRY(tensors_norm),
+                         GQ_ENTRY(adamw_step),
+                         GQ_ENTRY(adamw_values),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gq_native", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};

@@ -41,8 +41,7 @@
 // steps widened ahead, its accumulators finished one after the other, and first chains of different
 // lengths took it there from 352 and 379.
 #include "gq_act.cuh"
-
-#include <cuda.h>
+#include "gq_tc.cuh"
 
 using namespace gqa;
 
@@ -97,22 +96,6 @@ struct WArgs {
 };
 
 // ---- tcgen05 -------------------------------------------------------------------------------
-#define GQA_CG(CG, one, two, ...)                     \
-    do {                                              \
-        if constexpr ((CG) == 1) asm volatile(one __VA_ARGS__); \
-        else asm volatile(two __VA_ARGS__);           \
-    } while (0)
-template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t cols) {
-    GQA_CG(CG, "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;",
-           "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;",
-           ::"r"(smem), "r"(cols) : "memory");
-    GQA_CG(CG, "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;",
-           "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;", ::);
-}
-template <int CG> __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    GQA_CG(CG, "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;",
-           "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;", ::"r"(addr), "r"(cols));
-}
 template <int CG>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          bool add) {
@@ -123,68 +106,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}",
            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
-// Arrives on this barrier of every block of the tile when the MMAs issued so far are done.
-template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-            "[%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
-            : "memory");
-}
-// The pair: this block's rank, an arrival on the same barrier in the first block, and a barrier of both
-// blocks.  What an arrival announces are operands in shared memory, made visible to the tensor cores
-// by a proxy fence or written by the TMA, and registers read from TMEM, ordered by a tcgen05 fence; no
-// thread of the other block reads them with ordinary loads, so the arrival is not a release at cluster
-// scope (which waits for every store of the thread: 1,600 cycles, most of a step).  The PTX memory model
-// promises the order of ordinary accesses between two blocks for the cluster's scope alone; what is relied
-// on here instead is that a proxy fence makes the stores before it visible to the async proxy, through which
-// the tensor cores read the shared memory of both blocks, before the arrival behind it is counted.
-template <int CG> __device__ __forceinline__ uint32_t pair_rank() {
-    uint32_t r = 0;
-    if constexpr (CG == 2) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-template <int CG> __device__ __forceinline__ void arrive_first(uint32_t bar) {
-    if constexpr (CG == 1) {
-        gq::mbar_arrive(bar);
-    } else {
-        uint32_t there;
-        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(bar));
-        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
-    }
-}
-template <int CG> __device__ __forceinline__ void pair_sync() {
-    if constexpr (CG == 2) {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    } else {
-        __syncthreads();
-    }
-}
-__device__ __forceinline__ void fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 // Shared-memory descriptor of an operand that is contiguous along its outer dimension, 128-byte
 // swizzle: rows of 64 elements (one token each, 128 bytes), 8 tokens every 1,024 bytes (stride
 // offset), the next 64 outer elements kChunk bytes on (leading offset).
@@ -198,15 +119,6 @@ template <int CG, int BN> struct Instruction {
     static constexpr uint32_t value = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                       (static_cast<uint32_t>(BN >> 3) << 17) | ((128u * CG) >> 4 << 24);
 };
-
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
 
 // Two codes (the low bytes of the halves of p, 0x43 above them) times a power of two.  0x43cc is
 // 128 + (c & 127) if c's sign bit is taken out, and 0x4300 or 0x4380, 128 or 256, from the sign
@@ -879,23 +791,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- host ----------------------------------------------------------------------------------
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                             CUtensorMapFloatOOBfill);
-EncodeFn encode_fn() {
-    static EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
 
 struct WPlan {
     bool big;            // pairs of blocks on 512 x 256 tiles, else 128 x 128

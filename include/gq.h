@@ -552,6 +552,117 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
                           const float *scale, const float *shift, void *dw, int out_dtype,
                           int64_t lddw, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---- Linear layers in 8-bit floating point ---------------------------------------------------
+ *
+ * Products of a training step on operands of 8 bits, for activations and weights next to the 8-bit
+ * checkpoints above (whose weight gradient is gq_linear_wgrad).  No counterpart in the paper.
+ *
+ * A rows x cols matrix in 8-bit floating point is two arrays in device memory, 16-byte aligned:
+ *   codes  e4m3 bytes, rows of gq_fp8_code_pitch(cols) = round_up(cols, 16); padding codes are 0;
+ *   exps   gq_fp8_exp_bytes(rows, cols) = ceil(rows / 128) ceil(cols / 512) 512 bytes as the tensor
+ *          cores read them, uint8 [ceil(rows / 128)][ceil(cols / 512)][32][4][4]: the byte at
+ *          [t][w][r][j][b] is that of row 128 t + 32 j + r in block 4 w + b, the columns from
+ *          128 (4 w + b) on.
+ * Element (i, j) stands for code * 2^(E - 127), E its block's byte: the smallest value >= 1 with
+ * 448 * 2^(E - 127) >= the largest magnitude in the block, 255 for a block that holds a NaN or an
+ * infinity, whose codes are 0 and which reads back as NaN.  A block is 128 columns of one row
+ * (block_rows = 1: activations) or of 128 rows (block_rows = 128: weights, whose transposed matrix
+ * then has the same blocks).  Codes are rounded to nearest even; bytes of blocks that do not exist
+ * are not to be relied on.
+ *
+ * Matrices: as for the 8-bit checkpoints (GQ_F32 or GQ_BF16, any row distance, element-aligned).
+ */
+int64_t gq_fp8_code_pitch(int64_t cols);                 /* 0 if cols < 1 */
+size_t gq_fp8_exp_bytes(int64_t rows, int64_t cols);     /* 0 for invalid sizes and for no rows */
+
+/* exps_t (nullable, block_rows = 128 only): the exponents of the transposed matrix,
+ * gq_fp8_exp_bytes(cols, rows) bytes, which gq_fp8_linear_dgrad reads. */
+gq_status gq_fp8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                          int block_rows, uint8_t *codes, uint8_t *exps, uint8_t *exps_t,
+                          void *stream);
+
+/* The values as out_dtype (exact in GQ_F32, and in GQ_BF16 where a value is not below 2^-126; GQ_F16
+ * rounds to nearest even and overflows to infinity). */
+gq_status gq_fp8_dequantize(const uint8_t *codes, const uint8_t *exps, int64_t rows, int64_t cols,
+                            void *out, int out_dtype, int64_t ldout, void *stream);
+
+/*
+ * y[t][o] = sum over i of X[t][i] W[o][i] + bias[o]  (rows x outs, out_dtype GQ_F32 or GQ_BF16, rows
+ * ldy apart; bias nullable, fp32) with X (rows x cols, block_rows = 1) and W (outs x cols, either
+ * block_rows) in 8-bit floating point.  Where x is not null, X is made from it first (gq_fp8_quantize
+ * into xcodes and xexps, which keep it).  The tensor cores multiply codes and apply the scales; sums
+ * are fp32 and in a fixed order, rounded once.  A bounded wait that gives up (about a second; a broken
+ * kernel only) leaves NaN in the tiles concerned.  rows, outs and cols < 2^30.
+ */
+gq_status gq_fp8_linear(const void *x, int dtype, int64_t ldx, uint8_t *xcodes, uint8_t *xexps,
+                        int64_t rows, int64_t cols, const uint8_t *wcodes, const uint8_t *wexps,
+                        int64_t outs, const float *bias, void *y, int out_dtype, int64_t ldy,
+                        void *stream);
+
+/* The input's gradient: dx[t][i] = sum over o of DY[t][o] W[o][i]  (rows x cols), with DY (rows x outs,
+ * block_rows = 1) made from dy where that is not null, and W as above (block_rows = 128), with the
+ * exponents of its transposed matrix. */
+gq_status gq_fp8_linear_dgrad(const void *dy, int dtype, int64_t lddy, uint8_t *dycodes, uint8_t *dyexps,
+                              int64_t rows, int64_t outs, const uint8_t *wcodes, const uint8_t *wexps_t,
+                              int64_t cols, void *dx, int out_dtype, int64_t lddx, void *stream);
+
+/*
+ * ---- The optimizer's step --------------------------------------------------------------------
+ *
+ * What follows the gradients' mean: AdamW over all parameters in one call, with its two moments in
+ * fp32 or in 8 bits, and the norm over all gradients that clipping needs.  No counterpart in the
+ * paper.  Lists of tensors are HOST arrays of `count` device pointers and element counts (each below
+ * 2^34; 0 <= count < 2^30; tensors without elements are passed over).  Tensors are contiguous and
+ * element-aligned (32-byte aligned ones take the wide accesses), may lie anywhere and do not overlap.
+ * Addresses are arguments of the kernels: nothing is copied to the device, and a captured call keeps
+ * its own.
+ *
+ * gq_tensors_norm: *norm_dev = the square root of the sum of all squares (fp32 over 64 elements, fp64
+ * over those, in a fixed order; magnitudes above 1.8e19 make it infinite).  dtype GQ_F32 or GQ_BF16.
+ * ws: gq_tensors_norm_workspace_bytes(count) bytes, 16-byte aligned, contents irrelevant.
+ */
+size_t gq_tensors_norm_workspace_bytes(int64_t count);
+gq_status gq_tensors_norm(int64_t count, const void *const *tensors, const int64_t *numel, int dtype,
+                          float *norm_dev, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gq_adamw_step, in place, for every element of every tensor:
+ *   g' = g min(1, max_norm / (*norm_dev + 1e-6))    (g where norm_dev is null or max_norm < 0)
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * computed in fp32.  Where *norm_dev is a NaN or infinite, everything stays as it was.  t: step, at
+ * least 1, or *step_dev where that is not null (for captured graphs; t >= 1 there is the caller's
+ * affair).  0 <= beta < 1, eps >= 0.
+ * States: m and v fp32 (exps null), or in 8 bits: for every 32 elements of a tensor of n, and
+ * N = round_up(n, 32),
+ *   m     N e4m3 bytes (16-byte aligned), times 2^(E - 127), E the smallest value >= 1 with
+ *         448 * 2^(E - 127) >= the largest magnitude of the 32;
+ *   v     N bytes (16-byte aligned) that stand for the root of v: c for c < 16, else
+ *         (16 + c % 16) 2^(c / 16 - 1), times 2^(F - 127), F the smallest value >= 1 with
+ *         31 * 2^14 * 2^(F - 127) >= the largest root; a root that is not 0 keeps a code that is not 0;
+ *   exps  N / 32 pairs of bytes E, F (2-byte aligned); 255 where a block is not finite: it reads as NaN.
+ * All bytes 0 is a state of zeros.  Padding codes are 0.  The update uses the moments before they are
+ * rounded.
+ * Rounding of 8-bit states, and of bf16 parameters: GQ_ACT_NEAREST (ties to even), or GQ_ACT_RANDOM,
+ * floor(x + (H + 1/2) / 2^16) in units of the last place (floor(x + H / 2^16) for parameters) with H as
+ * for the 8-bit checkpoints, element i in column i of row 3 (first + k) + j, step t: k the tensor's place
+ * in the list, j = 0 for m, 1 for the root, 2 for the parameter.  An average over many steps changes by
+ * less than half of a code's step at a time: rounded to nearest it
+ * would stay where it is.
+ */
+gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, const void *const *grads,
+                        int grad_dtype, void *const *m, void *const *v, uint8_t *const *exps,
+                        const int64_t *numel, int64_t step, const int64_t *step_dev, double lr, double beta1,
+                        double beta2, double eps, double weight_decay, const float *norm_dev, double max_norm,
+                        int rounding, uint64_t seed, int64_t first, void *stream);
+
+/* The values of 8-bit states: first moments and roots of the second, each as out_dtype (GQ_F32 or GQ_BF16;
+ * exact in both down to 2^-126). */
+gq_status gq_adamw_values(int64_t count, const uint8_t *const *m, const uint8_t *const *v,
+                          const uint8_t *const *exps, const int64_t *numel, void *const *moments,
+                          void *const *roots, int out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
