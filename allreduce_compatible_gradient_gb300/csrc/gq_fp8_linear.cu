@@ -38,17 +38,21 @@ struct LArgs {
     int out_f32;
 };
 
+template <int CG>
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
                                         uint32_t sb, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add ? 1u : 0u)
-        : "memory");
+    GQA_CG(CG,
+           "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+           "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
+           "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+           "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
+           ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add ? 1u : 0u) : "memory");
 }
-// 32 rows of 16 bytes to 4 columns of TMEM, in each of its four quarters.
-__device__ __forceinline__ void copy_exps(uint32_t tmem, uint64_t smem) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(smem) : "memory");
+// 32 rows of 16 bytes to 4 columns of TMEM, in each of its four quarters (of both blocks of a pair, from the
+// same place in each one's shared memory).
+template <int CG> __device__ __forceinline__ void copy_exps(uint32_t tmem, uint64_t smem) {
+    GQA_CG(CG, "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;", "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;",
+           ::"r"(tmem), "l"(smem) : "memory");
 }
 // Rows of 128 bytes, 128-byte swizzle, 8 rows every 1,024 bytes: along k (128 of k of a row of the matrix)
 // and along the outer dimension (128 outer elements of a k) alike.
@@ -61,11 +65,11 @@ __device__ __forceinline__ uint64_t exp_operand(uint32_t smem) {
     return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
            (uint64_t(1) << 46);
 }
-// e4m3 operands, exponent bytes as scales, N columns, M = 128; a_outer: A is contiguous along its outer
-// dimension.  The scales' byte of a word is added per step.
-template <int N, bool A_OUTER> struct Instruction {
+// e4m3 operands, exponent bytes as scales, N columns, M = 128 per block; A_OUTER: A is contiguous along its
+// outer dimension.  The scales' byte of a word is added per step.
+template <int CG, int N, bool A_OUTER> struct Instruction {
     static constexpr uint32_t value = (A_OUTER ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
-                                      (1u << 23) | (128u >> 4 << 24);
+                                      (1u << 23) | (128u * CG >> 4 << 24);
     static __device__ __forceinline__ uint32_t of(uint32_t byte) { return value | byte << 4 | byte << 29; }
 };
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -94,17 +98,6 @@ __device__ __forceinline__ float peer_load(uint32_t smem, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
     return v;
-}
-// 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void put(const LArgs& a, int64_t token, int out, float v) {
     if (a.out_f32) static_cast<float*>(a.y)[token * a.ldy + out] = v;
@@ -206,13 +199,13 @@ __global__ void __launch_bounds__(192, 1)
                 fence_after();
                 if (with_exps(k)) {
                     set ^= 1u;
-                    copy_exps(tmem + C::kExps + 8 * set, exp_operand(e_stage(s)));
-                    copy_exps(tmem + C::kExps + 8 * set + 4, exp_operand(e_stage(s) + kExpTile));
+                    copy_exps<1>(tmem + C::kExps + 8 * set, exp_operand(e_stage(s)));
+                    copy_exps<1>(tmem + C::kExps + 8 * set + 4, exp_operand(e_stage(s) + kExpTile));
                 }
 #pragma unroll
                 for (int kk = 0; kk < kStep / 32; ++kk)
-                    mma_fp8(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)), operand(b_stage(s) + kk * 32),
-                            Instruction<BN, A_OUTER>::of(k & 3), tmem + C::kExps + 8 * set,
+                    mma_fp8<1>(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)), operand(b_stage(s) + kk * 32),
+                            Instruction<1, BN, A_OUTER>::of(k & 3), tmem + C::kExps + 8 * set,
                             tmem + C::kExps + 8 * set + 4, n > 0 || kk > 0);
                 mma_commit<1>(gq::smem_u32(&empty[s]));
             }
@@ -231,7 +224,7 @@ __global__ void __launch_bounds__(192, 1)
         for (int c = 0; c < BN; c += 16) {
             if (t0 + c >= a.rows) break;
             uint32_t v[16];
-            tmem_load16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+            tmem_load(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
             if (!ok) {  // a wait gave up: the tile is marked
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = 0x7FFFFFFFu;
@@ -265,6 +258,171 @@ __global__ void __launch_bounds__(192, 1)
         __syncthreads();
     }
     if (warp == 1) tmem_free<1>(tmem, C::kCols);
+}
+
+// ---- the large form ------------------------------------------------------------------------
+//
+// A pair of blocks works on 256 outputs x 256 tokens: each block loads 128 of the outputs and 128 of the
+// tokens, and one tcgen05.mma of both tensor cores reads both blocks' shared memory (a step of 128 x 256 in
+// one block would ask for 48 KB of operands in the time of 32).  Pairs stay and take tile after tile; the
+// sums leave TMEM for registers at once, so that the next tile's products go on while they are stored.
+struct Large {
+    static constexpr int BN = 256, kStages = 6, kWarps = 8;         // warps that take the sums
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr int kBytes = 2 * kTile;                        // of a step's operands, per block
+    static constexpr int kExps = BN;                                // columns of exponents: two sets, in turn,
+    static constexpr int kSet = 12;                                 // of 4 for the outputs and 8 for the tokens
+    static constexpr int kCols = 512;
+    static constexpr int kSmem = kStages * (kBytes + 3 * kExpTile) + 1024;
+};
+
+template <bool A_OUTER>
+__global__ void __launch_bounds__(Large::kThreads, 1)
+    large_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                 const LArgs a) {
+    using C = Large;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t raw[];
+    // full: a step's operands are there (in the pair's first block); full_b: the second block's
+    __shared__ alignas(8) uint64_t full[S], full_b[S], empty[S], acc_full, acc_empty, drain;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = pair_rank<2>();
+    auto a_stage = [&](int s) { return base + s * C::kBytes; };
+    auto b_stage = [&](int s) { return base + s * C::kBytes + kTile; };
+    auto e_stage = [&](int s) { return base + S * C::kBytes + s * 3 * kExpTile; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            gq::mbar_init(gq::smem_u32(&full[s]), 2u);
+            gq::mbar_init(gq::smem_u32(&full_b[s]), 1u);
+            gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
+        }
+        gq::mbar_init(gq::smem_u32(&acc_full), 1u);
+        gq::mbar_init(gq::smem_u32(&acc_empty), 2 * C::kWarps);
+        gq::mbar_init(gq::smem_u32(&drain), 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<2>(gq::smem_u32(&tmem_slot), C::kCols);
+    fence_before();
+    __syncthreads();
+    pair_sync<2>();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int pairs = gridDim.x / 2, tiles = a.tiles_m * ((a.rows + C::BN - 1) / C::BN);
+    const int words = (a.steps + 3) / 4;
+    const int last_a = (a.m - 1) / 128, last_b = (a.rows - 1) / 128;  // 128 rows of exponents that exist
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int n = 0;
+            bool ok = true;
+            gq::pdl_wait();  // the tokens' operand may be the launch before's work
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs) {
+                const int am = tile % a.tiles_m * 2 + static_cast<int>(rank);  // in 128 rows
+                const int bt = tile / a.tiles_m * 2;
+                const uint8_t* ea = a.a_exps + static_cast<int64_t>(min(am, last_a)) * words * kExpTile;
+                const uint8_t* eb0 = a.b_exps + static_cast<int64_t>(bt) * words * kExpTile;
+                const uint8_t* eb1 = a.b_exps + static_cast<int64_t>(min(bt + 1, last_b)) * words * kExpTile;
+                for (int k = 0; k < a.steps; ++k, ++n) {
+                    const int s = n % S;
+                    if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                    if (!ok) break;
+                    const uint32_t bar = gq::smem_u32(rank == 0 ? &full[s] : &full_b[s]);
+                    const bool exps = (k & 3) == 0;
+                    gq::mbar_arrive_expect_tx(bar, C::kBytes + (exps ? 3 * kExpTile : 0));
+                    tma_load(a_stage(s), &a_map, A_OUTER ? am * 128 : k * kStep, A_OUTER ? k * kStep : am * 128, bar);
+                    tma_load(b_stage(s), &b_map, k * kStep, (bt + static_cast<int>(rank)) * 128, bar);
+                    if (exps) {
+                        bulk_load(e_stage(s), ea + (k / 4) * kExpTile, kExpTile, bar);
+                        bulk_load(e_stage(s) + kExpTile, eb0 + (k / 4) * kExpTile, kExpTile, bar);
+                        bulk_load(e_stage(s) + 2 * kExpTile, eb1 + (k / 4) * kExpTile, kExpTile, bar);
+                    }
+                }
+            }
+            // nothing of this block's is in flight when it ends, whatever the others did
+            for (int j = n > S ? n - S : 0; j < n; ++j)
+                gq::mbar_wait(gq::smem_u32(rank == 0 ? &full[j % S] : &full_b[j % S]), (j / S) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int n = 0, done = 0;
+            bool ok = true;
+            uint32_t set = 1;  // of exponents' columns
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs, ++done) {
+                if (done > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (done - 1) & 1);
+                fence_after();
+                for (int k = 0; k < a.steps && ok; ++k, ++n) {
+                    const int s = n % S;
+                    ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
+                    if (!ok) break;
+                    fence_after();
+                    if ((k & 3) == 0) {
+                        set ^= 1u;
+#pragma unroll
+                        for (int j = 0; j < 3; ++j)
+                            copy_exps<2>(tmem + C::kExps + C::kSet * set + 4 * j, exp_operand(e_stage(s) + j * kExpTile));
+                    }
+                    const uint32_t sa = tmem + C::kExps + C::kSet * set;
+#pragma unroll
+                    for (int kk = 0; kk < kStep / 32; ++kk)
+                        mma_fp8<2>(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)),
+                                   operand(b_stage(s) + kk * 32), Instruction<2, C::BN, A_OUTER>::of(k & 3), sa, sa + 4,
+                                   k > 0 || kk > 0);
+                    mma_commit<2>(gq::smem_u32(&empty[s]));
+                }
+                if (ok) mma_commit<2>(gq::smem_u32(&acc_full));
+            }
+            if (!ok) {  // let what was issued finish before TMEM is given back
+                mma_commit<2>(gq::smem_u32(&drain));
+                gq::mbar_wait(gq::smem_u32(&drain), 0);
+            }
+        } else if (lane == 0) {  // the second block: tells the first that its operands have arrived
+            int n = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs)
+                for (int k = 0; k < a.steps && ok; ++k, ++n) {
+                    ok = gq::mbar_wait(gq::smem_u32(&full_b[n % S]), (n / S) & 1);
+                    if (ok) arrive_first<2>(gq::smem_u32(&full[n % S]));
+                }
+        }
+    } else {
+        const int quad = warp & 3, group = (warp - 2) >> 2;
+        int done = 0;
+        bool ok = true;
+        gq::pdl_wait();  // y may be what the launch before still reads
+        for (int tile = blockIdx.x / 2; tile < tiles; tile += pairs, ++done) {
+            const int m = (tile % a.tiles_m * 2 + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+            const int t0 = tile / a.tiles_m * C::BN + group * 128;
+            const float b = a.bias && m < a.m ? __ldg(a.bias + m) : 0.0f;
+            if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), done & 1);
+            ok = __all_sync(kFull, ok);
+            fence_after();
+            uint32_t v[4][32];
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * 128 + j * 32, v[j]);
+            } else {  // a wait gave up: the tile is marked
+#pragma unroll
+                for (int j = 0; j < 128; ++j) v[j >> 5][j & 31] = 0x7FFFFFFFu;
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_first<2>(gq::smem_u32(&acc_empty));
+            if (m >= a.m) continue;
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+                if (t0 + j < a.rows) put(a, t0 + j, m, __uint_as_float(v[j >> 5][j & 31]) + b);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    pair_sync<2>();  // neither block's memory is in use any more
+    if (warp == 1) tmem_free<2>(tmem, C::kCols);
+    pair_sync<2>();
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -305,6 +463,30 @@ gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const
     return gqh::launch_status();
 }
 
+template <bool A_OUTER>
+gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs a, bool early, cudaStream_t st) {
+    auto k = large_kernel<A_OUTER>;
+    gqh::blocks_per_sm(k, Large::kSmem, Large::kThreads);  // raises the shared-memory limit once
+    a.tiles_m = (a.m + 255) / 256;
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * ((a.rows + Large::BN - 1) / Large::BN);
+    const int64_t pairs = gqh::sm_count() / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(Large::kThreads);
+    cfg.dynamicSmemBytes = Large::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a) != cudaSuccess) return GQ_ERR_CUDA;
+    return gqh::launch_status();
+}
+
 // D = A B^T as above: `outs` rows of A, sums over `depth`.
 template <bool A_OUTER>
 gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_t* xexps, int64_t rows,
@@ -335,6 +517,8 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     a.steps = static_cast<int>(steps); a.tiles_m = static_cast<int>(tiles_m);
     a.a_exps = wexps; a.b_exps = xexps; a.bias = bias;
     a.y = y; a.ldy = ldy; a.out_f32 = out_dtype == GQ_F32;
+    if (((outs + 255) / 256) * ((rows + 255) / 256) >= 64)
+        return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
     int parts = 1;
     while (parts < 8 && tiles * parts * 2 <= sms && steps >= parts * 2) parts *= 2;
     switch (bn) {
