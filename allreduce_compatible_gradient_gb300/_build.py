@@ -3,10 +3,10 @@ extension module through which Python calls its operators on tensors (csrc/gq_na
 
 Twelve translation units (the C ABI and the other kernels in gq.cu; the quantise launchers, one per
 gradient type and scheme; the kernels of activations, 8-bit floating point and the optimizer) compiled in
-parallel with one -gencode (sm_103a), then linked with the static CUDA runtime: the library depends on nothing but the driver
-at load time.  -fmad=false keeps every fp32 operation of the gradient path a separately rounded
-IEEE operation (its rounding decisions must be bit-identical to their definition); the other
-units are compiled with contraction, and spell out the roundings that their codes depend on.
+parallel with one -gencode (sm_103a), then linked with the static CUDA runtime: the library depends on
+nothing but the driver at load time.  -fmad=false keeps every fp32 operation of the gradient path and of the
+optimizer a separately rounded IEEE operation (rounding decisions must be bit-identical to their definition);
+the other units are compiled with contraction, and spell out the roundings that their codes depend on.
 """
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ UNITS = ["gq.cu", "gq_quant_f32_l.cu", "gq_quant_f32_e.cu", "gq_quant_bf16_l.cu"
          "gq_quant_bf16_e.cu", "gq_act.cu", "gq_layernorm_fwd.cu", "gq_layernorm_bwd.cu",
          "gq_wgrad.cu", "gq_fp8.cu", "gq_fp8_linear.cu", "gq_adamw.cu"]
 CONTRACTED = {"gq_act.cu", "gq_layernorm_fwd.cu", "gq_layernorm_bwd.cu", "gq_wgrad.cu", "gq_fp8.cu",
-              "gq_fp8_linear.cu", "gq_adamw.cu"}
+              "gq_fp8_linear.cu"}
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgq.so")
 # the same library with the kernels' bounds checks compiled in (-DGQ_DEBUG)

@@ -10,9 +10,9 @@
 // byte of its own: c < 16 stands for c, others for (16 + c % 16) 2^(c / 16 - 1), times 2^(E - 127).  The root
 // halves the range, and what a code rounds is then the step's denominator itself.  A root that is not zero
 // keeps a code that is not zero: a moment that survives its rounding where the root does not would be divided
-// by eps.  Products and sums of the moments are rounded one by one, so that codes are those of the
-// formulas in fp32 on any compiler; the update, which no code depends on, is contracted and divides by a
-// reciprocal (2 units in the last place of the update).
+// by eps.  Products and sums of the moments are rounded one by one, so that codes are those of
+// the formulas in fp32, whatever computes them; the update, where nothing is rounded at random behind it, takes
+// a reciprocal (2 units in the last place of the update).
 //
 // Random rounding (seed): an average of 1,000 steps moves by less than half of a code's step at a time, and
 // rounding to nearest would leave it where it is.  16-bit numbers of the library's Philox stream.
@@ -29,8 +29,7 @@ using namespace gqa;
 namespace {
 
 constexpr int kThreadsA = 256;
-constexpr int kRounds = 4;                          // of 8 elements per thread and block
-constexpr int kChunk = kThreadsA * 8 * kRounds;     // elements of a block
+constexpr int kRound = kThreadsA * 8;   // elements of a block's round, 8 per thread
 
 struct Slot {
     void* p;
@@ -64,41 +63,44 @@ struct Step {
     const int64_t* step;         // nullable
     const float* norm;           // nullable
     float max_norm;              // negative: no limit
-    int random;
+    int rounds;                  // of a block
     Rng rng;
 };
 
-// 8 elements at p + i; `left` of them exist.  Ordinary loads: most of it is written again.
+// 8 elements at p + i as they lie; `left` of them exist.  Ordinary loads: most of it is written again.
 template <typename T>
-__device__ __forceinline__ void get8(const void* p, int64_t i, int64_t left, uint32_t wide, F2 (&v)[4]) {
+__device__ __forceinline__ Raw8<T> raw8(const void* p, int64_t i, int64_t left, uint32_t wide) {
     const T* q = static_cast<const T*>(p) + i;
+    Raw8<T> r;
     if (wide && left >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            uint32_t w[8];
-            if (wide == 32u) {
-                asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
-                               "=r"(w[7])
-                             : "l"(q));
-            } else {
-                const uint4 a = reinterpret_cast<const uint4*>(q)[0], b = reinterpret_cast<const uint4*>(q)[1];
-                w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-                w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = f2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        if (sizeof(T) == 4 && wide == 32u) {
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[sizeof(T) == 4 ? 4 : 0]),
+                           "=r"(r.w[sizeof(T) == 4 ? 5 : 1]), "=r"(r.w[sizeof(T) == 4 ? 6 : 2]),
+                           "=r"(r.w[sizeof(T) == 4 ? 7 : 3])
+                         : "l"(q));
         } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(q);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = f2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) {
+                const uint4 a = reinterpret_cast<const uint4*>(q)[k];
+                r.w[4 * k] = a.x; r.w[4 * k + 1] = a.y; r.w[4 * k + 2] = a.z; r.w[4 * k + 3] = a.w;
+            }
         }
-        return;
+        return r;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        v[k] = f2(2 * k < left ? up(q[2 * k]) : 0.0f, 2 * k + 1 < left ? up(q[2 * k + 1]) : 0.0f);
+    for (int k = 0; k < static_cast<int>(sizeof(T)) * 2; ++k) r.w[k] = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left) {
+            if constexpr (sizeof(T) == 4) r.w[k] = __float_as_uint(q[k]);
+            else r.w[k >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(q[k])) << (16 * (k & 1));
+        }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void get8(const void* p, int64_t i, int64_t left, uint32_t wide, F2 (&v)[4]) {
+    pairs(raw8<T>(p, i, left, wide), v);
 }
 template <typename T>
 __device__ __forceinline__ void put8(void* p, int64_t i, int64_t left, uint32_t wide, const float (&v)[8]) {
@@ -113,20 +115,18 @@ __device__ __forceinline__ void put8(void* p, int64_t i, int64_t left, uint32_t 
         if (k < left) down(v[k], q[k]);
 }
 
-// The maximum of 8 fp32 bit patterns over the 4 lanes of a block of 32.
-__device__ __forceinline__ uint32_t top32(uint32_t m) {
+// The largest magnitude of 8 numbers as fp32 bits, above infinity's where one is a NaN; over the 4 lanes of a
+// block of 32.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t top32(const float (&v)[8]) {
+    const float a = max3(max3(v[0], v[1], v[2]), v[3], v[4]);
+    uint32_t m = __float_as_uint(max3(a, max3(v[5], v[6], v[7]), 0.0f));
     m = max(m, __shfl_xor_sync(kFull, m, 1));
     return max(m, __shfl_xor_sync(kFull, m, 2));
-}
-// bits >> drop, to nearest even or with a 16-bit number.
-template <int DROP> __device__ __forceinline__ uint32_t cut(uint32_t bits, bool random, uint32_t h) {
-    const uint32_t by = random ? h << (DROP - 16) | 1u << (DROP - 17)
-                               : (1u << (DROP - 1)) - 1u + (bits >> DROP & 1u);
-    return (bits + by) >> DROP;
-}
-__device__ __forceinline__ uint32_t half_of(const uint4& w, int k) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    return u[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
 }
 // 31 * 2^14 * 2^(E - 127) >= a: with a = 1.f * 2^k iff 1.f <= 31 / 16, a fraction field of at most 0x780000.
 __device__ __forceinline__ uint32_t root_exp_byte(uint32_t top) {
@@ -138,38 +138,155 @@ __device__ __forceinline__ uint32_t root_exp_byte(uint32_t top) {
 __device__ __forceinline__ float root_scale(uint32_t e) {
     return e == 255u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((e + 66u) << 23);
 }
-
-struct Words {
-    uint4 m, r, p;
-};
-
-// 8 elements of a step.  first moments, roots (EIGHT) or second moments, in and out.
-template <bool EIGHT>
-__device__ __forceinline__ void step8(const Step& a, float clip, float size, float fix, const F2 (&g)[4],
-                                      F2 (&m)[4], F2 (&v)[4], float (&p)[8]) {
-    const F2 b1 = f2(a.beta1), r1 = f2(a.rest1), b2 = f2(a.beta2), r2 = f2(a.rest2);
+// The values of 8 codes of either kind, as pairs.
+__device__ __forceinline__ void moments8(uint2 c, uint32_t e, F2 (&m)[4]) {
+    const uint32_t w[2] = {c.x, c.y};
+    const F2 s = f2(step_of(e));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const F2 c = mul2(g[i], f2(clip));
-        m[i] = add2(mul2(m[i], b1), mul2(c, r1));
-        if constexpr (EIGHT) v[i] = mul2(v[i], v[i]);
-        v[i] = add2(mul2(v[i], b2), mul2(mul2(c, c), r2));
-        float x, y, mx, my;
-        split(v[i], x, y);
-        x = __fsqrt_rn(x);
-        y = __fsqrt_rn(y);
-        if constexpr (EIGHT) v[i] = f2(x, y);
-        split(m[i], mx, my);
-        p[2 * i] = fmaf(p[2 * i], a.keep, -size * __fdividef(mx, fmaf(x, fix, a.eps)));
-        p[2 * i + 1] = fmaf(p[2 * i + 1], a.keep, -size * __fdividef(my, fmaf(y, fix, a.eps)));
+    for (int j = 0; j < 4; ++j) m[j] = mul2(fp8_values2(w[j >> 1] >> (16 * (j & 1))), s);
+}
+__device__ __forceinline__ void roots8(uint2 c, uint32_t e, F2 (&r)[4]) {
+    const uint32_t w[2] = {c.x, c.y};
+    const F2 s = f2(root_scale(e)), up64 = f2(0x1p64f);
+    constexpr uint32_t mask = 0xFFu << 19;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        r[2 * j] = f2(__uint_as_float(w[j] << 19 & mask), __uint_as_float(w[j] << 11 & mask));
+        r[2 * j + 1] = f2(__uint_as_float(w[j] << 3 & mask), __uint_as_float(w[j] >> 5 & mask));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = mul2(mul2(r[j], up64), s);
+}
+
+// Codes of 8 numbers y whose exponent field has been made the code's own (y is below 2^-111): the code ends at
+// bit 27 - LEFT of the number and at bit 32 after a shift by LEFT, where what is behind it is rounded off: to
+// nearest even, or by the 16-bit numbers of a Philox call, each with a half behind it, H 256 + 128 of 2^24.
+template <int LEFT, bool RANDOM>
+__device__ __forceinline__ uint2 codes_of(const uint32_t (&y)[8], const uint4& words) {
+    const uint32_t h[4] = {words.x, words.y, words.z, words.w};
+    uint32_t t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t by = RANDOM ? __byte_perm(h[j >> 1], 0x80u, j & 1 ? 0x5324 : 0x5104)
+                                   : 0x7FFFFFu + (y[j] >> (24 - LEFT) & 1u);
+        t[j] = (y[j] << LEFT) + by;
+    }
+    return make_uint2(gather_bytes<3>(t[0], t[1], t[2], t[3]), gather_bytes<3>(t[4], t[5], t[6], t[7]));
+}
+
+__device__ __forceinline__ float rsqrt_fast(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Roots of 8 numbers >= 0: a reciprocal root y (an approximation), s = v y, and one of Newton's steps for the
+// root, s + (v - s^2) y / 2, whose error is a rounding's.  Numbers below fp32's normal ones, which the
+// approximation takes for 0, go the long way.
+__device__ __forceinline__ void roots(const F2 (&v)[4], F2 (&r)[4]) {
+    uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        split(v[j], a, b);
+        low = min(low, min(__float_as_uint(a) - 1u, __float_as_uint(b) - 1u));  // 0 is the largest
+        const F2 y = f2(rsqrt_fast(fmaxf(a, 0x1p-126f)), rsqrt_fast(fmaxf(b, 0x1p-126f)));
+        const F2 s = mul2(v[j], y), half = mul2(y, f2(0.5f));
+        r[j] = fma2(fma2(mul2(s, f2(-1.0f)), s, v[j]), half, s);
+    }
+    // (infinities and NaN too: s would be NaN for the former)
+    uint32_t high = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        split(v[j], a, b);
+        high = max(high, max(__float_as_uint(a), __float_as_uint(b)));
+    }
+    if (low < 0x7FFFFFu || high >= 0x7F800000u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(v[j], a, b);
+            r[j] = f2(__fsqrt_rn(a), __fsqrt_rn(b));
+        }
     }
 }
 
-template <typename P, typename G, bool EIGHT, int N>
+// a + b, each rounded by itself: sums of pairs would be contracted with the products that they add, whatever
+// the compiler is told.
+__device__ __forceinline__ F2 sum_of(F2 a, F2 b) {
+    float ax, ay, bx, by;
+    split(a, ax, ay);
+    split(b, bx, by);
+    return f2(__fadd_rn(ax, bx), __fadd_rn(ay, by));
+}
+
+// 8 elements of a step: gradients, first moments, second moments and parameters; the roots come back in r.
+// EXACT: the update's operations are rounded one by one like the moments', for a parameter that is rounded at
+// random behind them.
+template <bool EXACT>
+__device__ __forceinline__ void step8(const Step& a, float clip, float size, float fix, const F2 (&g)[4],
+                                      F2 (&m)[4], F2 (&v)[4], F2 (&p)[4], F2 (&r)[4]) {
+    const F2 b1 = f2(a.beta1), r1 = f2(a.rest1), b2 = f2(a.beta2), r2 = f2(a.rest2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const F2 c = mul2(g[j], f2(clip));
+        m[j] = sum_of(mul2(m[j], b1), mul2(c, r1));
+        v[j] = sum_of(mul2(v[j], b2), mul2(mul2(c, c), r2));
+    }
+    roots(v, r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x, y;
+        if constexpr (EXACT) {
+            float mx, my;
+            split(sum_of(mul2(r[j], f2(fix)), f2(a.eps)), x, y);
+            split(m[j], mx, my);
+            p[j] = sum_of(mul2(p[j], f2(a.keep)), mul2(f2(__fdiv_rn(mx, x), __fdiv_rn(my, y)), f2(-size)));
+        } else {
+            split(fma2(r[j], f2(fix), f2(a.eps)), x, y);
+            const F2 u = mul2(m[j], f2(rcp_fast(x), rcp_fast(y)));
+            p[j] = fma2(p[j], f2(a.keep), mul2(u, f2(-size)));
+        }
+    }
+}
+__device__ __forceinline__ void apart(const F2 (&v)[4], float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(v[j], x[2 * j], x[2 * j + 1]);
+}
+
+// What a thread reads of 8 elements with 8-bit states.
+template <typename P, typename G> struct Load {
+    Raw8<P> p;
+    Raw8<G> g;
+    uint2 m, v;
+    uint32_t e;
+    __device__ __forceinline__ void fetch(const Slot& s, int64_t i) {
+        const int64_t left = s.n - i;
+        g = raw8<G>(s.g, i, left, s.wg);
+        p = raw8<P>(s.p, i, left, s.wp);
+        m = v = make_uint2(0u, 0u);
+        e = 0x0101u;
+        if (left > 0) {
+            m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + i);
+            v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + i);
+            e = reinterpret_cast<const uint16_t*>(s.e)[i >> 5];
+        }
+    }
+};
+
+template <typename P, typename G, bool EIGHT, bool RANDOM, int N>
 __global__ void __launch_bounds__(kThreadsA)
     adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step a) {
-    const Slot& s = t.s[t.of(blockIdx.x)];
+    // from the end: the last gradients are what the norm's pass has left in the L2
+    const uint32_t block = gridDim.x - 1 - blockIdx.x;
+    const Slot& s = t.s[t.of(block)];
     float clip = 1.0f, size = a.size, fix = a.fix;
+    gq::pdl_wait();
     if (a.norm) {
         const float norm = *a.norm;
         if (!(norm < INFINITY)) return;  // not a number, or infinite: the step is left out
@@ -184,178 +301,179 @@ __global__ void __launch_bounds__(kThreadsA)
         size = __fdiv_rn(a.lr, -expm1f(f * a.log1));
         fix = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f(f * a.log2)));
     }
-    const int64_t begin = static_cast<int64_t>(blockIdx.x - s.first) * kChunk + threadIdx.x * 8;
+    const int64_t begin = static_cast<int64_t>(block - s.first) * (a.rounds * kRound);
+    // 8-bit states: the next round is on its way while one is computed (the instructions of a round take as
+    // long as its bytes)
+    Load<P, G> next;
+    if constexpr (EIGHT) next.fetch(s, begin + threadIdx.x * 8);
 #pragma unroll 1
-    for (int k = 0; k < kRounds; ++k) {
-        const int64_t i = begin + k * (kThreadsA * 8);
-        if (i - threadIdx.x * 8 >= s.n) break;  // of the whole block
-        const int64_t left = s.n - i;           // may be 0 or less: then only for the others' sake
-        F2 g[4], m[4], v[4], q[4];
-        float p[8];
-        get8<G>(s.g, i, left, s.wg, g);
-        get8<P>(s.p, i, left, s.wp, q);
-        uint32_t em = 1u, ev = 1u;
+    for (int k = 0; k < a.rounds; ++k) {
+        const int64_t i0 = begin + k * kRound, i = i0 + threadIdx.x * 8;
+        if (i0 >= s.n) break;          // of the whole block
+        const int64_t left = s.n - i;  // may be 0 or less: then only for the others' sake
+        F2 g[4], m[4], v[4], p[4], r[4];
         if constexpr (EIGHT) {
-            uint2 cm = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
-            if (left > 0) {
-                cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + i);
-                cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + i);
-                const uint32_t e = reinterpret_cast<const uint16_t*>(s.e)[i >> 5];
-                em = e & 255u;
-                ev = e >> 8;
-            }
-            const uint32_t wm[2] = {cm.x, cm.y}, wv[2] = {cv.x, cv.y};
+            const Load<P, G> now = next;
+            if (k + 1 < a.rounds && i0 + kRound < s.n) next.fetch(s, i + kRound);
+            pairs(now.g, g);
+            pairs(now.p, p);
+            moments8(now.m, now.e & 255u, m);
+            roots8(now.v, now.e >> 8, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[j] = mul2(fp8_values2(wm[j >> 1] >> (16 * (j & 1))), f2(step_of(em)));
-                const uint32_t c = wv[j >> 1] >> (16 * (j & 1));
-                v[j] = mul2(mul2(f2(__uint_as_float((c & 255u) << 19), __uint_as_float((c >> 8 & 255u) << 19)),
-                                 f2(0x1p64f)), f2(root_scale(ev)));
-            }
+            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
         } else {
+            get8<G>(s.g, i, left, s.wg, g);
+            get8<P>(s.p, i, left, s.wp, p);
             get8<float>(s.m, i, left, s.wm, m);
             get8<float>(s.v, i, left, s.wv, v);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split(q[j], p[2 * j], p[2 * j + 1]);
-        step8<EIGHT>(a, clip, size, fix, g, m, v, p);
+        step8<RANDOM && sizeof(P) == 2>(a, clip, size, fix, g, m, v, p, r);
 
-        Words w;
-        if (a.random) {
+        uint4 wm = make_uint4(0u, 0u, 0u, 0u), wr = wm, wp = wm;
+        if constexpr (RANDOM) {
             const gq::PhiloxGroup pg = gq::philox_group(static_cast<uint32_t>(i >> 3), step_lo, step_hi, a.rng.rk);
             if constexpr (EIGHT) {
-                w.m = gq::philox_row(pg, s.row, step_lo, a.rng.rk);
-                w.r = gq::philox_row(pg, s.row + 1, step_lo, a.rng.rk);
+                wm = gq::philox_row(pg, s.row, step_lo, a.rng.rk);
+                wr = gq::philox_row(pg, s.row + 1, step_lo, a.rng.rk);
             }
-            if constexpr (sizeof(P) == 2) w.p = gq::philox_row(pg, s.row + 2, step_lo, a.rng.rk);
+            if constexpr (sizeof(P) == 2) wp = gq::philox_row(pg, s.row + 2, step_lo, a.rng.rk);
         }
-        if constexpr (sizeof(P) == 2) {
-            if (a.random) {
+        float x[8];
+        apart(p, x);
+        if constexpr (RANDOM && sizeof(P) == 2) {
+            const uint32_t h[4] = {wp.x, wp.y, wp.z, wp.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t b = __float_as_uint(p[j]);
-                    if ((b & 0x7F800000u) != 0x7F800000u) p[j] = __uint_as_float((b + half_of(w.p, j)) & 0xFFFF0000u);
-                }
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = __float_as_uint(x[j]);
+                if ((b & 0x7F800000u) != 0x7F800000u)
+                    x[j] = __uint_as_float((b + (h[j >> 1] >> (16 * (j & 1)) & 0xFFFFu)) & 0xFFFF0000u);
             }
         }
-        put8<P>(s.p, i, left, s.wp, p);
+        put8<P>(s.p, i, left, s.wp, x);
         if constexpr (EIGHT) {
-            float x[8], r[8];
-            uint32_t tm = 0u, tr = 0u;
+            uint32_t y[8];
+            apart(m, x);
+            const uint32_t em = fp8_exp_byte(top32(x));
+            uint32_t sign[2] = {gather_bytes<3>(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                                __float_as_uint(x[3])),
+                                gather_bytes<3>(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
+                                                __float_as_uint(x[7]))};
+            F2 im = f2(inv_step(em));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                split(m[j], x[2 * j], x[2 * j + 1]);
-                split(v[j], r[2 * j], r[2 * j + 1]);
-            }
+            for (int j = 0; j < 4; ++j) m[j] = mul2(mul2(m[j], im), f2(0x1p-120f));  // e4m3's exponent field
+            apart(m, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                tm = max(tm, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-                tr = max(tr, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-            }
-            em = fp8_exp_byte(top32(tm));
-            ev = root_exp_byte(top32(tr));
-            const float im = inv_step(em), ir = __uint_as_float((188u - min(ev, 187u)) << 23);
-            uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
+            for (int j = 0; j < 8; ++j) y[j] = __float_as_uint(x[j]);
+            uint2 cm = codes_of<4, RANDOM>(y, wm);  // (the sign is shifted out)
+            cm.x = (cm.x & 0x7F7F7F7Fu) | (sign[0] & 0x80808080u);
+            cm.y = (cm.y & 0x7F7F7F7Fu) | (sign[1] & 0x80808080u);
+            if (em == 255u) cm = make_uint2(0u, 0u);
+
+            apart(r, x);
+            const uint32_t er = root_exp_byte(top32(x));
+            im = f2(__uint_as_float((188u - min(er, 187u)) << 23));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // e4m3's exponent field becomes fp32's
-                const uint32_t b = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x[j]), im), 0x1p-120f));
-                uint32_t c = cut<20>(b, a.random != 0, half_of(w.m, j)) | (x[j] < 0.0f ? 128u : 0u);
-                cm[j >> 2] |= (em == 255u ? 0u : c) << (8 * (j & 3));
-                const uint32_t d = __float_as_uint(__fmul_rn(__fmul_rn(r[j], ir), 0x1p-64f));
-                c = max(cut<19>(d, a.random != 0, half_of(w.r, j)), r[j] > 0.0f ? 1u : 0u);
-                cv[j >> 2] |= (ev == 255u ? 0u : c) << (8 * (j & 3));
-            }
-            if (left > 0) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + i) = make_uint2(cm[0], cm[1]);
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + i) = make_uint2(cv[0], cv[1]);
-            }
-            // a block of 32 belongs to 4 lanes; the first of them has an element of it, or none has
-            if ((threadIdx.x & 3) == 0 && left > 0)
-                reinterpret_cast<uint16_t*>(s.e)[i >> 5] = static_cast<uint16_t>(em | ev << 8);
-            // codes of the block's other lanes, where the tensor ends inside it, are zeros
-            if (left <= 0 && (i & ~int64_t(31)) < s.n) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + i) = make_uint2(0u, 0u);
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + i) = make_uint2(0u, 0u);
+            for (int j = 0; j < 8; ++j) y[j] = min(__float_as_uint(x[j]), 1u << 19);  // the least code, or 0
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = mul2(mul2(r[j], im), f2(0x1p-64f));
+            apart(r, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = max(__float_as_uint(x[j]), y[j]);
+            uint2 cr = codes_of<5, RANDOM>(y, wr);
+            if (er == 255u) cr = make_uint2(0u, 0u);
+            // where the tensor ends inside a block of 32, its other lanes' codes are zeros
+            if ((i & ~int64_t(31)) < s.n) {
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + i) = cm;
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + i) = cr;
+                if ((threadIdx.x & 3) == 0) reinterpret_cast<uint16_t*>(s.e)[i >> 5] = static_cast<uint16_t>(em | er << 8);
             }
         } else {
-            float x[8], y[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                split(m[j], x[2 * j], x[2 * j + 1]);
-                split(v[j], y[2 * j], y[2 * j + 1]);
-            }
+            apart(m, x);
             put8<float>(s.m, i, left, s.wm, x);
-            put8<float>(s.v, i, left, s.wv, y);
+            apart(v, x);
+            put8<float>(s.v, i, left, s.wv, x);
         }
     }
 }
 
 // The values of 8-bit states: first moments to p, roots to g (the slot's places for two outputs).
 template <typename O, int N>
-__global__ void __launch_bounds__(kThreadsA) values_kernel(const __grid_constant__ Table<N> t) {
+__global__ void __launch_bounds__(kThreadsA) values_kernel(const __grid_constant__ Table<N> t, int rounds) {
     const Slot& s = t.s[t.of(blockIdx.x)];
-    const int64_t begin = static_cast<int64_t>(blockIdx.x - s.first) * kChunk + threadIdx.x * 8;
-#pragma unroll
-    for (int k = 0; k < kRounds; ++k) {
-        const int64_t i = begin + k * (kThreadsA * 8), left = s.n - i;
+    const int64_t begin = static_cast<int64_t>(blockIdx.x - s.first) * (rounds * kRound) + threadIdx.x * 8;
+#pragma unroll 2
+    for (int k = 0; k < rounds; ++k) {
+        const int64_t i = begin + k * kRound, left = s.n - i;
         if (left <= 0) break;
         const uint2 cm = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + i));
         const uint2 cv = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + i));
         const uint32_t e = __ldg(reinterpret_cast<const uint16_t*>(s.e) + (i >> 5));
-        const uint32_t wm[2] = {cm.x, cm.y}, wv[2] = {cv.x, cv.y};
-        float x[8], r[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            split(mul2(fp8_values2(wm[j >> 1] >> (16 * (j & 1))), f2(step_of(e & 255u))), x[2 * j], x[2 * j + 1]);
-            const uint32_t c = wv[j >> 1] >> (16 * (j & 1));
-            split(mul2(mul2(f2(__uint_as_float((c & 255u) << 19), __uint_as_float((c >> 8 & 255u) << 19)),
-                            f2(0x1p64f)), f2(root_scale(e >> 8))), r[2 * j], r[2 * j + 1]);
-        }
+        F2 v[4];
+        float x[8];
+        moments8(cm, e & 255u, v);
+        apart(v, x);
         put8<O>(s.p, i, left, s.wp, x);
-        put8<O>(const_cast<void*>(s.g), i, left, s.wg, r);
+        roots8(cv, e >> 8, v);
+        apart(v, x);
+        put8<O>(const_cast<void*>(s.g), i, left, s.wg, x);
     }
 }
 
 // ---- the norm ------------------------------------------------------------------------------
 
-constexpr int kNormBlocks = 608;   // partial sums per launch: at most
-constexpr int kNormChunk = 16384;  // elements
+constexpr int kNormBlocks = 1216;  // partial sums per launch: at most
 
-// Sums of squares of the chunks blockIdx.x, blockIdx.x + gridDim.x, ...: fp32 over a thread's 64 elements of
-// a chunk, fp64 over chunks and threads.
+// Sums of squares of the chunks blockIdx.x, blockIdx.x + gridDim.x, ...: fp32 over a thread's elements of a
+// chunk (64 at most) and over a warp, with what chunks' sums lose carried along; fp64 over warps and blocks
+// (over threads, its few units took 3 us of a pass).
 template <typename G, int N>
 __global__ void __launch_bounds__(256)
-    squares_kernel(const __grid_constant__ Table<N> t, uint32_t chunks, double* partial) {
-    double sum = 0.0;
+    squares_kernel(const __grid_constant__ Table<N> t, uint32_t chunks, int rounds, double* partial) {
+    gq::pdl_launch_dependents();  // the sum of the sums waits before it reads
+    float sum = 0.0f, carry = 0.0f;
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         const Slot& s = t.s[t.of(c)];
-        const int64_t begin = static_cast<int64_t>(c - s.first) * kNormChunk + threadIdx.x * 8;
-        F2 part = f2(0.0f);
+        int64_t i = static_cast<int64_t>(c - s.first) * (rounds * kRound) + threadIdx.x * 8;
+        F2 part[2] = {f2(0.0f), f2(0.0f)};
+        for (int k = 0; k < rounds; k += 4) {
+            Raw8<G> w[4];
 #pragma unroll
-        for (int k = 0; k < kNormChunk / 2048; ++k) {
-            const int64_t i = begin + k * 2048;
-            F2 g[4];
-            if (i < s.n) get8<G>(s.g, i, s.n - i, s.wg, g);
-            else g[0] = g[1] = g[2] = g[3] = f2(0.0f);
+            for (int j = 0; j < 4; ++j, i += kRound) {
+                if (k + j < rounds && i < s.n) {
+                    w[j] = raw8<G>(s.g, i, s.n - i, s.wg);
+                } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part = fma2(g[j], g[j], part);
+                    for (int q = 0; q < static_cast<int>(sizeof(G)) * 2; ++q) w[j].w[q] = 0u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                F2 g[4];
+                pairs(w[j], g);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) part[q & 1] = fma2(g[q], g[q], part[q & 1]);
+            }
         }
-        sum += static_cast<double>(sum2(part));
+        const float more = sum2(add2(part[0], part[1])) - carry, all = sum + more;
+        carry = (all - sum) - more;
+        sum = all;
     }
-    __shared__ double warps[8];
+    // an infinite or overflowing sum leaves a NaN behind: its norm is not finite either way
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    __shared__ float warps[8];
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         double all = 0.0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) all += warps[i];
+        for (int i = 0; i < 8; ++i) all += static_cast<double>(warps[i]);
         partial[blockIdx.x] = all;
     }
 }
 __global__ void __launch_bounds__(256) root_kernel(const double* partial, int64_t n, float* norm) {
+    gq::pdl_launch_dependents();
+    gq::pdl_wait();
     double sum = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += 256) sum += partial[i];
     __shared__ double warps[8];
@@ -409,24 +527,48 @@ gq_status in_runs(int64_t count, const int64_t* numel, int chunk, Fill fill, Lau
     return GQ_OK;
 }
 
+// Rounds of a block, of `most`: fewer where the tensors would not give every SM several blocks.
+int rounds_for(int64_t count, const int64_t* numel, int most) {
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) total += numel[i];
+    const int64_t each = total / (8 * gqh::sm_count()) / kRound;
+    return each < 1 ? 1 : each < most ? static_cast<int>(each) : most;
+}
+
+// A launch that may begin while the one before it on the stream ends.
+template <typename... Params, typename... Args>
+void launch_early(void (*k)(Params...), uint32_t blocks, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreadsA);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 // Widest access to 8 elements at a time.
 uint8_t wide(const void* p) { return mult(p, 32) ? 32 : mult(p, 16) ? 16 : 0; }
 
-template <typename P, typename G, bool EIGHT>
+template <typename P, typename G, bool EIGHT, bool RANDOM>
 gq_status adamw(int64_t count, void* const* params, const void* const* grads, void* const* m, void* const* v,
-                uint8_t* const* exps, const int64_t* numel, int64_t first, const Step& a, cudaStream_t st) {
+                uint8_t* const* exps, const int64_t* numel, int64_t first, Step a, cudaStream_t st) {
     auto fill = [&](Slot& s, int64_t i) {
         s.p = params[i]; s.g = grads[i]; s.m = m[i]; s.v = v[i];
         s.e = EIGHT ? exps[i] : nullptr;
         s.row = static_cast<uint32_t>(3 * (first + i));
         s.wp = wide(s.p); s.wg = wide(s.g); s.wm = wide(s.m); s.wv = wide(s.v);
     };
+    a.rounds = rounds_for(count, numel, EIGHT ? 16 : 4);
     if (count <= kFew)
-        return in_runs<kFew>(count, numel, kChunk, fill, [&](const Table<kFew>& t, uint32_t blocks) {
-            adamw_kernel<P, G, EIGHT, kFew><<<blocks, kThreadsA, 0, st>>>(t, a);
+        return in_runs<kFew>(count, numel, a.rounds * kRound, fill, [&](const Table<kFew>& t, uint32_t blocks) {
+            launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kFew>, blocks, st, t, a);
         });
-    return in_runs<kMany>(count, numel, kChunk, fill, [&](const Table<kMany>& t, uint32_t blocks) {
-        adamw_kernel<P, G, EIGHT, kMany><<<blocks, kThreadsA, 0, st>>>(t, a);
+    return in_runs<kMany>(count, numel, a.rounds * kRound, fill, [&](const Table<kMany>& t, uint32_t blocks) {
+        launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kMany>, blocks, st, t, a);
     });
 }
 
@@ -453,18 +595,19 @@ gq_status gq_tensors_norm(int64_t count, const void *const *tensors, const int64
         s.g = tensors[i];
         s.wg = wide(s.g);
     };
-    const uint32_t most = static_cast<uint32_t>(4 * gqh::sm_count() < kNormBlocks ? 4 * gqh::sm_count() : kNormBlocks);
+    const uint32_t most = static_cast<uint32_t>(8 * gqh::sm_count() < kNormBlocks ? 8 * gqh::sm_count() : kNormBlocks);
+    const int rounds = rounds_for(count, numel, 8);
     auto run = [&](const auto& t, uint32_t chunks) {
         constexpr int N = sizeof(t.s) / sizeof(Slot);
         const uint32_t blocks = chunks < most ? chunks : most;
-        if (dtype == GQ_F32) squares_kernel<float, N><<<blocks, 256, 0, st>>>(t, chunks, partial + parts);
-        else squares_kernel<bf16, N><<<blocks, 256, 0, st>>>(t, chunks, partial + parts);
+        if (dtype == GQ_F32) squares_kernel<float, N><<<blocks, 256, 0, st>>>(t, chunks, rounds, partial + parts);
+        else squares_kernel<bf16, N><<<blocks, 256, 0, st>>>(t, chunks, rounds, partial + parts);
         parts += blocks;
     };
-    const gq_status r = count <= kFew ? in_runs<kFew>(count, numel, kNormChunk, fill, run)
-                                      : in_runs<kMany>(count, numel, kNormChunk, fill, run);
+    const gq_status r = count <= kFew ? in_runs<kFew>(count, numel, rounds * kRound, fill, run)
+                                      : in_runs<kMany>(count, numel, rounds * kRound, fill, run);
     if (r != GQ_OK) return r;
-    root_kernel<<<1, 256, 0, st>>>(partial, parts, norm_dev);
+    launch_early(root_kernel, 1, st, static_cast<const double*>(partial), parts, norm_dev);
     return gqh::launch_status();
 }
 
@@ -502,14 +645,17 @@ gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, con
     a.step = step_dev;
     a.norm = norm_dev;
     a.max_norm = max_norm >= 0.0 ? static_cast<float>(max_norm) : -1.0f;
-    a.random = rounding == GQ_ACT_RANDOM;
     a.rng = make_rng(seed, static_cast<uint64_t>(step));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define GQA_ADAMW(P, G)                                                                                       \
-    (exps ? adamw<P, G, true>(count, params, grads, m, v, exps, numel, first, a, st)                            \
-          : adamw<P, G, false>(count, params, grads, m, v, exps, numel, first, a, st))
-    if (param_dtype == GQ_F32) return grad_dtype == GQ_F32 ? GQA_ADAMW(float, float) : GQA_ADAMW(float, bf16);
-    return grad_dtype == GQ_F32 ? GQA_ADAMW(bf16, float) : GQA_ADAMW(bf16, bf16);
+    const bool random = rounding == GQ_ACT_RANDOM;
+#define GQA_ADAMW(P, G, EIGHT, RANDOM) \
+    adamw<P, G, EIGHT, RANDOM>(count, params, grads, m, v, exps, numel, first, a, st)
+#define GQA_STATE(P, G)                                                                     \
+    (exps ? random ? GQA_ADAMW(P, G, true, true) : GQA_ADAMW(P, G, true, false)              \
+          : random && sizeof(P) == 2 ? GQA_ADAMW(P, G, false, (sizeof(P) == 2)) : GQA_ADAMW(P, G, false, false))
+    if (param_dtype == GQ_F32) return grad_dtype == GQ_F32 ? GQA_STATE(float, float) : GQA_STATE(float, bf16);
+    return grad_dtype == GQ_F32 ? GQA_STATE(bf16, float) : GQA_STATE(bf16, bf16);
+#undef GQA_STATE
 #undef GQA_ADAMW
 }
 
@@ -526,6 +672,7 @@ gq_status gq_adamw_values(int64_t count, const uint8_t *const *m, const uint8_t 
             return GQ_ERR_INVALID;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int rounds = rounds_for(count, numel, 4);
     auto fill = [&](Slot& s, int64_t i) {
         s.p = moments[i]; s.g = roots[i];
         s.m = const_cast<uint8_t*>(m[i]); s.v = const_cast<uint8_t*>(v[i]);
@@ -534,11 +681,11 @@ gq_status gq_adamw_values(int64_t count, const uint8_t *const *m, const uint8_t 
     };
     auto run = [&](const auto& t, uint32_t blocks) {
         constexpr int N = sizeof(t.s) / sizeof(Slot);
-        if (out_dtype == GQ_F32) values_kernel<float, N><<<blocks, kThreadsA, 0, st>>>(t);
-        else values_kernel<bf16, N><<<blocks, kThreadsA, 0, st>>>(t);
+        if (out_dtype == GQ_F32) values_kernel<float, N><<<blocks, kThreadsA, 0, st>>>(t, rounds);
+        else values_kernel<bf16, N><<<blocks, kThreadsA, 0, st>>>(t, rounds);
     };
-    return count <= kFew ? in_runs<kFew>(count, numel, kChunk, fill, run)
-                         : in_runs<kMany>(count, numel, kChunk, fill, run);
+    return count <= kFew ? in_runs<kFew>(count, numel, rounds * kRound, fill, run)
+                         : in_runs<kMany>(count, numel, rounds * kRound, fill, run);
 }
 
 }  // extern "C"
