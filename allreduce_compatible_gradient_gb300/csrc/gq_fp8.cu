@@ -25,138 +25,181 @@ template <typename T, bool ALIGNED> struct Granules {
             w[4 * i] = g.x; w[4 * i + 1] = g.y; w[4 * i + 2] = g.z; w[4 * i + 3] = g.w;
         }
     }
-    __device__ __forceinline__ void values(int left, F2 (&v)[4]) {
-        pairs(shifted<T, ALIGNED>(w, m, min(max(left, 0), 8)), v);
+    __device__ __forceinline__ Raw8<T> wanted(int left) {
+        return shifted<T, ALIGNED>(w, m, min(max(left, 0), 8));
     }
 };
 
-__device__ __forceinline__ uint32_t top8(const F2 (&h)[4]) {
-    uint32_t m = 0u;
+// Largest magnitude of 8 elements as fp32 bits, above infinity's where one is a NaN.
+__device__ __forceinline__ uint32_t top8(const Raw8<float>& r) {
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        split(h[i], a, b);
-        m = max(m, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    for (int i = 0; i < 8; i += 2)
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(__uint_as_float(r.w[i])), "f"(__uint_as_float(r.w[i + 1])));
+    return __float_as_uint(a);
+}
+// (bf16 magnitudes order like their bits)
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t top8(const Raw8<bf16>& r) {
+    uint32_t m = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max16x2(m, r.w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFF0000u, m << 16);
+}
+// The same over the 16 lanes of a block, for four rows.
+__device__ __forceinline__ void tops(const Raw8<float> (&r)[4], uint32_t (&top)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        top[j] = top8(r[j]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top[j] = max(top[j], __shfl_xor_sync(kFull, top[j], o));
     }
-    return m;
+}
+__device__ __forceinline__ void tops(const Raw8<bf16> (&r)[4], uint32_t (&top)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {  // two rows in a register
+        uint32_t m = top8(r[j]) >> 16 | top8(r[j + 1]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max16x2(m, __shfl_xor_sync(kFull, m, o));
+        top[j] = m << 16;
+        top[j + 1] = m & 0xFFFF0000u;
+    }
 }
 
-// One exponent per row and 128 columns.  A warp takes rows r, r + 32, r + 64, r + 96 of 128 and 512 columns,
-// 256 at a time: 16 lanes hold a block, and its first lane ends up with the 16 exponents that lie side by
-// side.  Four rows' loads are on their way at a time.
+// One exponent per row and 128 columns.  A warp's task is rows r, r + 32, r + 64, r + 96 of 128 and 256 columns:
+// 16 lanes hold a block, and the 8 exponents lie in 16 bytes.  The next task's loads are on their way while
+// one is computed.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(256)
-    rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, int64_t words,
-                int64_t tasks, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+    rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
+                Div by, uint32_t tasks, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
     gq::pdl_launch_dependents();  // a product that follows waits before it reads
     const int lane = threadIdx.x & 31;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < tasks;
-         t += static_cast<int64_t>(gridDim.x) * 8) {
-        // neighbouring warps take neighbouring columns of the same rows
-        const int64_t word = t % words, r0 = t / words / 32 * 128 + (t / words & 31);
-        uint32_t e4[4] = {0u, 0u, 0u, 0u};
+    const uint32_t stride = gridDim.x * 8;
+    Granules<T, ALIGNED> g[4];
+    // neighbouring warps take neighbouring columns of the same rows
+    auto fetch = [&](uint32_t t) {
+        const uint32_t q = across > 1 ? quot(t, by) : t;
+        const int64_t r = static_cast<int64_t>(q >> 5) * 128 + (q & 31);
+        const int64_t c = static_cast<int64_t>(t - q * across) * 256 + lane * 8;
+        const int left = static_cast<int>(min(cols - c, int64_t(8)));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t c = word * 512 + h * 256 + lane * 8;
-            const int left = static_cast<int>(min(cols - c, int64_t(8)));
-            Granules<T, ALIGNED> g[4];
+        for (int j = 0; j < 4; ++j) g[j].fetch(x + (r + 32 * j) * ld + c, r + 32 * j < rows ? left : 0);
+    };
+    uint32_t t = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t < tasks) fetch(t);
+    for (; t < tasks; t += stride) {
+        const uint32_t q = across > 1 ? quot(t, by) : t;
+        const int64_t r = static_cast<int64_t>(q >> 5) * 128 + (q & 31);
+        const uint32_t piece = t - q * across;
+        const int64_t c = static_cast<int64_t>(piece) * 256 + lane * 8;
+        const int left = static_cast<int>(min(cols - c, int64_t(8)));
+        Raw8<T> now[4];
+        uint32_t top[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                g[j].fetch(x + (r0 + 32 * j) * ld + c, r0 + 32 * j < rows ? left : 0);
+        for (int j = 0; j < 4; ++j) now[j] = g[j].wanted(r + 32 * j < rows ? left : 0);
+        if (t < tasks - min(stride, tasks)) fetch(t + stride);
+        tops(now, top);
+        uint32_t e4 = 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                F2 v[4];
-                g[j].values(r0 + 32 * j < rows ? left : 0, v);
-                uint32_t m = top8(v);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-                const uint32_t e = fp8_exp_byte(m);
-                uint2 q = fp8_codes8(v, inv_step(e));
-                if (e == 255u) q = make_uint2(0u, 0u);
-                if (r0 + 32 * j < rows && c < pitch)
-                    *reinterpret_cast<uint2*>(codes + (r0 + 32 * j) * pitch + c) = q;
-                // blocks 2 h and 2 h + 1 of the word
-                e4[j] |= (e | __shfl_down_sync(kFull, e, 16) << 8) << (16 * h);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t e = fp8_exp_byte(top[j]);
+            F2 v[4];
+            pairs(now[j], v);
+            uint2 w = fp8_codes8(v, inv_step(e));
+            if (e == 255u) w = make_uint2(0u, 0u);
+            if (r + 32 * j < rows && c < pitch) *reinterpret_cast<uint2*>(codes + (r + 32 * j) * pitch + c) = w;
+            e4 |= e << (8 * j);
         }
-        if (lane == 0)
-            *reinterpret_cast<uint4*>(exps + (r0 / 128 * words + word) * kExpTile + (r0 & 31) * 16) =
-                make_uint4(e4[0], e4[1], e4[2], e4[3]);
+        // lane j < 4: row j's two blocks
+        const uint32_t other = __shfl_xor_sync(kFull, e4, 16);
+        if (lane < 4)
+            *reinterpret_cast<uint16_t*>(exps + (static_cast<int64_t>(q >> 5) * ((across + 1) / 2) + piece / 2) * kExpTile +
+                                         (q & 31) * 16 + lane * 4 + (piece & 1) * 2) =
+                static_cast<uint16_t>(__byte_perm(e4, other, lane | (4 + lane) << 4));
     }
 }
 
 // One exponent per 128 x 128 elements, written for every row (exps) and every column (exps_t, nullable).
-// Block = one tile, 64 elements per thread.
+// Block = one tile, 32 elements per thread.
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(256)
-    tiles_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, int64_t across,
+__global__ void __launch_bounds__(512)
+    tiles_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
                  uint8_t* __restrict__ codes, uint8_t* __restrict__ exps, uint8_t* __restrict__ exps_t) {
     gq::pdl_launch_dependents();
-    __shared__ uint32_t most[8];
+    __shared__ uint32_t most[16];
     const int64_t tr = blockIdx.x / across, tc = blockIdx.x % across;
     const int64_t r0 = tr * 128 + (threadIdx.x >> 4), c = tc * 128 + (threadIdx.x & 15) * 8;
     const int left = static_cast<int>(min(cols - c, int64_t(8)));
-    F2 v[8][4];
+    Granules<T, ALIGNED> g[4];
+    Raw8<T> now[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i].fetch(x + (r0 + 32 * i) * ld + c, r0 + 32 * i < rows ? left : 0);
     uint32_t m = 0u;
-    constexpr int B = 4;  // loads on their way
 #pragma unroll
-    for (int i = 0; i < 8; i += B) {
-        Granules<T, ALIGNED> g[B];
-#pragma unroll
-        for (int k = 0; k < B; ++k)
-            g[k].fetch(x + (r0 + 16 * (i + k)) * ld + c, r0 + 16 * (i + k) < rows ? left : 0);
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            g[k].values(r0 + 16 * (i + k) < rows ? left : 0, v[i + k]);
-            m = max(m, top8(v[i + k]));
-        }
+    for (int i = 0; i < 4; ++i) {
+        now[i] = g[i].wanted(r0 + 32 * i < rows ? left : 0);
+        m = max(m, top8(now[i]));
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
     if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, most[i]);
+    for (int i = 0; i < 16; ++i) m = max(m, most[i]);
     const uint32_t e = fp8_exp_byte(m);
     const float inv = inv_step(e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint2 q = fp8_codes8(v[i], inv);
+    for (int i = 0; i < 4; ++i) {
+        F2 v[4];
+        pairs(now[i], v);
+        uint2 q = fp8_codes8(v, inv);
         if (e == 255u) q = make_uint2(0u, 0u);
-        if (r0 + 16 * i < rows && c < pitch)
-            *reinterpret_cast<uint2*>(codes + (r0 + 16 * i) * pitch + c) = q;
+        if (r0 + 32 * i < rows && c < pitch)
+            *reinterpret_cast<uint2*>(codes + (r0 + 32 * i) * pitch + c) = q;
     }
     const int k = threadIdx.x & 127;  // 4-byte places of 128 rows, each for 4 blocks
     if (threadIdx.x < 128)
         exps[(tr * exp_words(cols) + (tc >> 2)) * kExpTile + k * 4 + (tc & 3)] = static_cast<uint8_t>(e);
-    else if (exps_t)
+    else if (threadIdx.x < 256 && exps_t)
         exps_t[(tc * exp_words(rows) + (tr >> 2)) * kExpTile + k * 4 + (tr & 3)] = static_cast<uint8_t>(e);
 }
 
 // 16 columns of a row per thread, which are in one block.
 template <typename O, int ALIGN>
 __global__ void __launch_bounds__(256)
-    values_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t cols,
-                  int64_t pitch, int64_t words, int64_t pieces, int64_t across, O* __restrict__ out, int64_t ld) {
+    values_kernel(const uint8_t* codes, const uint8_t* exps, int64_t cols, int64_t pitch, int64_t words,
+                  int64_t pieces, uint32_t across, Div by, O* out, int64_t ld) {
     constexpr int B = 2;
+    gq::pdl_wait();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < pieces; t += B * stride) {
         uint4 q[B];
         uint32_t e[B];
+        int64_t row[B], c[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             const int64_t at = t + k * stride;
             if (at >= pieces) break;
-            const int64_t row = at / across, c = at % across * 16;
-            q[k] = __ldg(reinterpret_cast<const uint4*>(codes + row * pitch + c));
-            e[k] = __ldg(exps + (row / 128 * words + c / 512) * kExpTile + (row & 31) * 16 + (row >> 5 & 3) * 4 +
-                         (c >> 7 & 3));
+            if (pieces <= INT32_MAX) {
+                const uint32_t n = across > 1 ? quot(static_cast<uint32_t>(at), by) : static_cast<uint32_t>(at);
+                row[k] = n;
+                c[k] = static_cast<int64_t>(static_cast<uint32_t>(at) - n * across) * 16;
+            } else {
+                row[k] = at / across;
+                c[k] = at % across * 16;
+            }
+            q[k] = *reinterpret_cast<const uint4*>(codes + row[k] * pitch + c[k]);
+            e[k] = exps[((row[k] >> 7) * words + (c[k] >> 9)) * kExpTile + (row[k] & 31) * 16 + (row[k] >> 5 & 3) * 4 +
+                        (c[k] >> 7 & 3)];
         }
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const int64_t at = t + k * stride;
-            if (at >= pieces) break;
-            const int64_t row = at / across, c = at % across * 16;
+            if (t + k * stride >= pieces) break;
             const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
             const F2 s = f2(step_of(e[k]));
             float v[16];
@@ -165,34 +208,39 @@ __global__ void __launch_bounds__(256)
                 const F2 p = mul2(fp8_values2(w[i >> 1] >> (16 * (i & 1))), s);
                 split(p, v[2 * i], v[2 * i + 1]);
             }
-            O* to = out + row * ld;
+            O* to = out + row[k] * ld;
             if constexpr (ALIGN > 0) {
-                store<O, 16, ALIGN>(to, c, cols, v);
+                store<O, 16, ALIGN>(to, c[k], cols, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (c + i < cols) down(v[i], to[c + i]);
+                    if (c[k] + i < cols) down(v[i], to[c[k] + i]);
             }
         }
     }
 }
 
+Div div_by(int64_t d) { return d > 1 ? make_div(static_cast<uint32_t>(d)) : Div{1, 0, 0}; }
+
 template <typename T>
 gq_status quantize(const T* x, int64_t rows, int64_t cols, int64_t ld, bool tiles, uint8_t* codes,
                    uint8_t* exps, uint8_t* exps_t, cudaStream_t st) {
-    const int64_t pitch = fp8_pitch(cols), words = exp_words(cols);
+    const int64_t pitch = fp8_pitch(cols);
     const bool aligned = row_align(x, sizeof(T) == 4 ? GQ_F32 : GQ_BF16, rows, ld) != 0;
     if (tiles) {
         const int64_t across = (cols + 127) / 128, n = (rows + 127) / 128 * across;
         auto k = aligned ? tiles_kernel<T, true> : tiles_kernel<T, false>;
-        k<<<static_cast<unsigned>(n), 256, 0, st>>>(x, ld, rows, cols, pitch, across, codes, exps, exps_t);
+        k<<<static_cast<unsigned>(n), 512, 0, st>>>(x, ld, rows, cols, pitch, static_cast<uint32_t>(across), codes,
+                                                    exps, exps_t);
         return gqh::launch_status();
     }
-    const int64_t tasks = (rows + 127) / 128 * 32 * words;
+    const int64_t across = (cols + 255) / 256, tasks = (rows + 127) / 128 * 32 * across;
+    if (tasks >= int64_t(1) << 31) return GQ_ERR_INVALID;
     auto k = aligned ? rows_kernel<T, true> : rows_kernel<T, false>;
     const int64_t most = resident_blocks(k, 256, 0), need = (tasks + 7) / 8;
-    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(x, ld, rows, cols, pitch, words, tasks,
-                                                                        codes, exps);
+    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(
+        x, ld, rows, cols, pitch, static_cast<uint32_t>(across), div_by(across), static_cast<uint32_t>(tasks), codes,
+        exps);
     return gqh::launch_status();
 }
 
@@ -203,8 +251,17 @@ gq_status dequantize(const uint8_t* codes, const uint8_t* exps, int64_t rows, in
     const int a = row_align(out, dtype, rows, ld);
     auto k = a == 32 ? values_kernel<O, 32> : a == 16 ? values_kernel<O, 16> : values_kernel<O, 0>;
     const int64_t most = resident_blocks(k, 256, 0), need = (pieces + 255) / 256;
-    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(
-        codes, exps, cols, fp8_pitch(cols), exp_words(cols), pieces, across, out, ld);
+    cudaLaunchConfig_t cfg = {};  // it may begin while what wrote the codes ends
+    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, k, codes, exps, cols, fp8_pitch(cols), exp_words(cols), pieces,
+                       static_cast<uint32_t>(across), div_by(across), out, ld);
     return gqh::launch_status();
 }
 
