@@ -15,9 +15,12 @@
 // a part of the sum; the parts are added through distributed shared memory in the blocks' order.
 //   warp 0   TMA loads of both operands (128 of k per step) and bulk copies of exponents (512 of k each)
 //   warp 1   one thread copies exponents to TMEM and issues tcgen05.mma, accumulators in TMEM
-//   2 to 5   the sums from TMEM to memory
+//   2 to 5   the sums from TMEM to memory; where x is given and one tile holds all tokens, they also put x
+//            into 8 bits on its way to shared memory, so that a call of few tokens is one launch
 #include "gq_fp8.cuh"
 #include "gq_tc.cuh"
+
+#include <type_traits>
 
 using namespace gqa;
 
@@ -35,7 +38,9 @@ struct LArgs {
     const float* bias;           // nullable
     void* y;
     int64_t ldy;
-    int out_f32;
+    int out_f32, wide;           // wide: four neighbouring outputs of a row can be stored at once
+    const void* x;               // of a fused call
+    int64_t ldx;
 };
 
 template <int CG>
@@ -92,11 +97,14 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float peer_load(uint32_t smem, uint32_t rank) {
+__device__ __forceinline__ float4 peer_load(uint32_t smem, uint32_t rank) {
     uint32_t there;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(there)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void put(const LArgs& a, int64_t token, int out, float v) {
@@ -104,24 +112,137 @@ __device__ __forceinline__ void put(const LArgs& a, int64_t token, int out, floa
     else static_cast<bf16*>(a.y)[token * a.ldy + out] = __float2bfloat16_rn(v);
 }
 
-// BN tokens per tile: fewer than 128 only where one tile holds all of them, so that a tile's exponents begin
-// with its first row.
+// Four neighbouring outputs of a token.
+__device__ __forceinline__ void put4(const LArgs& a, int64_t token, int out, float4 v) {
+    if (a.wide && out + 4 <= a.m) {
+        if (a.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + token * a.ldy + out) = v;
+        else
+            *reinterpret_cast<uint2*>(static_cast<bf16*>(a.y) + token * a.ldy + out) =
+                make_uint2(pack2(v.x, v.y, bf16()), pack2(v.z, v.w, bf16()));
+        return;
+    }
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (out + i < a.m) put(a, token, out + i, w[i]);
+}
+
+// BN tokens per tile: fewer than 128 only where one tile holds all of them.  A tile's exponents then begin with
+// its first row, at an address in TMEM that is a multiple of 4 columns, as the scales of an instruction have to.
 template <int BN_> struct Small {
     static constexpr int BN = BN_;
     static constexpr int kBytes = kTile + BN * kStep;      // of a step's operands
-    static constexpr int kStages = 6;
+    static constexpr int kStages = BN <= 32 ? 8 : 6;
     static constexpr int kCols = BN <= 16 ? 32 : BN <= 32 ? 64 : BN <= 64 ? 128 : 256;  // of TMEM
-    // columns behind the accumulator: two sets of 4 for W's exponents and 4 for the tokens', in turn
+    // columns behind the accumulator: two sets of 4 for W's exponents, two of 4 for the tokens'
     static constexpr int kExps = BN;
     static_assert(kExps + 16 <= kCols, "exponents fit behind the accumulator");
     static constexpr int kSmem = kStages * (kBytes + 2 * kExpTile) + 1024;
     static_assert(128 * BN * 4 <= kStages * kBytes, "a block's sums fit in its operands' place");
 };
 
-template <typename C, bool A_OUTER>
+// The tokens' side of a step, 128 columns of BN tokens, from x: 16 lanes hold a row's block, 8 rows at a time
+// by four warps.  Behind the last row and column stand zeros.
+template <typename T, int BN> struct Squeeze {
+    static constexpr int R = BN / 8;
+    Raw8<T> w[R];
+    __device__ __forceinline__ void fetch(const LArgs& a, int k, int depth, int thread, bool wide) {
+        const int c = k * kStep + (thread & 15) * 8;
+        const int left = depth - c;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = (thread >> 4) + 8 * i;
+            const T* p = static_cast<const T*>(a.x) + row * a.ldx + c;
+#pragma unroll
+            for (int j = 0; j < static_cast<int>(sizeof(T)) * 2; ++j) w[i].w[j] = 0u;
+            if (row >= a.rows || left <= 0) continue;
+            if (wide && left >= 8) {
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) {
+                    const uint4 g = reinterpret_cast<const uint4*>(p)[j];
+                    w[i].w[4 * j] = g.x; w[i].w[4 * j + 1] = g.y; w[i].w[4 * j + 2] = g.z; w[i].w[4 * j + 3] = g.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < left) {
+                        if constexpr (sizeof(T) == 4) w[i].w[j] = __float_as_uint(p[j]);
+                        else w[i].w[j >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[j])) << (16 * (j & 1));
+                    }
+            }
+        }
+    }
+    // codes in the layout of a swizzled box, exponents at the step's byte of each row's word
+    __device__ __forceinline__ void store(uint32_t codes, uint32_t exps, int k, int thread) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = (thread >> 4) + 8 * i, unit = (thread & 15) >> 1;
+            F2 v[4];
+            pairs(w[i], v);
+            uint32_t m = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x, y;
+                split(v[j], x, y);
+                m = max(m, max(__float_as_uint(x) & 0x7FFFFFFFu, __float_as_uint(y) & 0x7FFFFFFFu));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+            const uint32_t e = fp8_exp_byte(m);
+            uint2 q = fp8_codes8(v, inv_step(e));
+            if (e == 255u) q = make_uint2(0u, 0u);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(codes + row * 128 + ((unit ^ (row & 7)) << 4) +
+                                                                  (thread & 1) * 8),
+                         "r"(q.x), "r"(q.y)
+                         : "memory");
+            if ((thread & 15) == 0)
+                asm volatile("st.shared.b8 [%0], %1;" ::"r"(exps + (row & 31) * 16 + (row >> 5) * 4 + (k & 3)), "r"(e)
+                             : "memory");
+        }
+    }
+};
+
+// Adds the parts of tokens c, c + 4 PARTS, ... below `end` (four warps, each block a PARTS-th) and stores them;
+// eight loads are on their way at a time (one by one, 128 tokens took 4 us).
+template <int PARTS>
+__device__ __forceinline__ void join(const LArgs& a, uint32_t from, int c, int end, int t0, int out, float4 b) {
+    constexpr int B = 8 / PARTS;
+    for (; c < end; c += B * 4 * PARTS) {
+        float4 p[B][PARTS];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int r = 0; r < PARTS; ++r) {
+                // (tokens behind the last are read as the last, and left out)
+                const uint32_t at = from + min(c + j * 4 * PARTS, end - 1) * 512;
+                if constexpr (PARTS == 1)
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(p[j][r].x), "=f"(p[j][r].y), "=f"(p[j][r].z), "=f"(p[j][r].w)
+                                 : "r"(at)
+                                 : "memory");
+                else
+                    p[j][r] = peer_load(at, r);
+            }
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            float4 v = p[j][0];
+#pragma unroll
+            for (int r = 1; r < PARTS; ++r) {
+                v.x += p[j][r].x; v.y += p[j][r].y; v.z += p[j][r].z; v.w += p[j][r].w;
+            }
+            v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+            if (c + j * 4 * PARTS < end) put4(a, t0 + c + j * 4 * PARTS, out, v);
+        }
+    }
+}
+
+// T: the type of x in a fused call (one tile of tokens), else void.
+template <typename C, bool A_OUTER, typename T>
 __global__ void __launch_bounds__(192, 1)
     small_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-                 const LArgs a) {
+                 const LArgs a, const int depth) {
+    constexpr bool FUSED = !std::is_void<T>::value;
     constexpr int BN = C::BN, S = C::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ alignas(8) uint64_t full[S], empty[S], acc_full, drain;
@@ -135,7 +256,7 @@ __global__ void __launch_bounds__(192, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            gq::mbar_init(gq::smem_u32(&full[s]), 1u);
+            gq::mbar_init(gq::smem_u32(&full[s]), FUSED ? 5u : 1u);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
@@ -161,65 +282,89 @@ __global__ void __launch_bounds__(192, 1)
             // W's side of a step, then the tokens': the launch before may still write those
             auto load_a = [&](int k, int s) {
                 const uint32_t bar = gq::smem_u32(&full[s]);
-                gq::mbar_arrive_expect_tx(bar, C::kBytes + (with_exps(k) ? 2 * kExpTile : 0));
+                gq::mbar_arrive_expect_tx(bar, (FUSED ? kTile : C::kBytes) +
+                                                   (with_exps(k) ? (FUSED ? 1 : 2) * kExpTile : 0));
                 tma_load(a_stage(s), &a_map, A_OUTER ? m0 : k * kStep, A_OUTER ? k * kStep : m0, bar);
                 if (with_exps(k))
                     bulk_load(e_stage(s), a.a_exps + (static_cast<int64_t>(m0 / 128) * words + k / 4) * kExpTile,
                               kExpTile, bar);
             };
             auto load_b = [&](int k, int s) {
-                const uint32_t bar = gq::smem_u32(&full[s]);
-                tma_load(b_stage(s), &b_map, k * kStep, t0, bar);
-                if (with_exps(k))
-                    bulk_load(e_stage(s) + kExpTile,
-                              a.b_exps + (static_cast<int64_t>(t0 / 128) * words + k / 4) * kExpTile, kExpTile, bar);
+                if constexpr (!FUSED) {
+                    const uint32_t bar = gq::smem_u32(&full[s]);
+                    tma_load(b_stage(s), &b_map, k * kStep, t0, bar);
+                    if (with_exps(k))
+                        bulk_load(e_stage(s) + kExpTile,
+                                  a.b_exps + (static_cast<int64_t>(t0 / 128) * words + k / 4) * kExpTile, kExpTile, bar);
+                }
             };
             const int first = min(k1 - k0, S);
             for (int n = 0; n < first; ++n) load_a(k0 + n, n);
-            gq::pdl_wait();
+            if constexpr (!FUSED) gq::pdl_wait();
             for (int n = 0; n < first; ++n) load_b(k0 + n, n);
             int n = first;
             for (; n < k1 - k0; ++n) {
-                ok = gq::mbar_wait(gq::smem_u32(&empty[n % S]), ((n / S) - 1) & 1);
+                ok = mbar_rest(gq::smem_u32(&empty[n % S]), ((n / S) - 1) & 1);
                 if (!ok) break;
                 load_a(k0 + n, n % S);
                 load_b(k0 + n, n % S);
             }
             // nothing of this block's is in flight when it ends, whatever the others did
-            for (int j = n > S ? n - S : 0; j < n; ++j) gq::mbar_wait(gq::smem_u32(&full[j % S]), (j / S) & 1);
+            for (int j = n > S ? n - S : 0; j < n; ++j) mbar_rest(gq::smem_u32(&full[j % S]), (j / S) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0) {
             bool ok = true;
-            uint32_t set = 1;  // of exponents' columns
+            uint32_t set = 1, set_b = 1;  // of exponents' columns
             for (int n = 0; n < k1 - k0; ++n) {
                 const int k = k0 + n, s = n % S;
-                ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
+                ok = mbar_rest(gq::smem_u32(&full[s]), (n / S) & 1);
                 if (!ok) break;
                 fence_after();
                 if (with_exps(k)) {
                     set ^= 1u;
-                    copy_exps<1>(tmem + C::kExps + 8 * set, exp_operand(e_stage(s)));
-                    copy_exps<1>(tmem + C::kExps + 8 * set + 4, exp_operand(e_stage(s) + kExpTile));
+                    copy_exps<1>(tmem + C::kExps + 4 * set, exp_operand(e_stage(s)));
                 }
+                if (FUSED || with_exps(k)) {  // (a fused call has a step's bytes with the step)
+                    set_b ^= 1u;
+                    copy_exps<1>(tmem + C::kExps + 8 + 4 * set_b, exp_operand(e_stage(s) + kExpTile));
+                }
+                const uint32_t sa = tmem + C::kExps + 4 * set, sb = tmem + C::kExps + 8 + 4 * set_b;
 #pragma unroll
                 for (int kk = 0; kk < kStep / 32; ++kk)
                     mma_fp8<1>(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)), operand(b_stage(s) + kk * 32),
-                            Instruction<1, BN, A_OUTER>::of(k & 3), tmem + C::kExps + 8 * set,
-                            tmem + C::kExps + 8 * set + 4, n > 0 || kk > 0);
+                               Instruction<1, BN, A_OUTER>::of(k & 3), sa, sb, n > 0 || kk > 0);
                 mma_commit<1>(gq::smem_u32(&empty[s]));
             }
             mma_commit<1>(gq::smem_u32(ok ? &acc_full : &drain));
-            if (!ok) gq::mbar_wait(gq::smem_u32(&drain), 0);  // what was issued finishes before TMEM is freed
+            if (!ok) mbar_rest(gq::smem_u32(&drain), 0);  // what was issued finishes before TMEM is freed
         }
     } else {
         const int q = warp & 3, m = q * 32 + lane;
-        bool ok = k1 <= k0 || gq::mbar_wait(gq::smem_u32(&acc_full), 0);
+        bool ok = true;
+        if constexpr (FUSED) {
+            const int thread = threadIdx.x - 64;
+            const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(a.ldx * sizeof(T))) & 15u) == 0;
+            Squeeze<T, BN> now, next;
+            next.fetch(a, k0, depth, thread, wide);
+            for (int n = 0; n < k1 - k0; ++n) {
+                const int s = n % S;
+                now = next;
+                if (n + 1 < k1 - k0) next.fetch(a, k0 + n + 1, depth, thread, wide);
+                if (n >= S && ok) ok = mbar_rest(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                now.store(b_stage(s), e_stage(s) + kExpTile, k0 + n, thread);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full[s]));
+            }
+        }
+        if (ok) ok = mbar_rest(gq::smem_u32(&acc_full), 0);
         ok = __all_sync(kFull, ok);
         fence_after();
-        const float b = a.bias && m0 + m < a.m ? __ldg(a.bias + m0 + m) : 0.0f;
         float* sums = reinterpret_cast<float*>(raw + (base - gq::smem_u32(raw)));
-        gq::pdl_wait();  // y may be what the launch before still reads
+        if constexpr (!FUSED) gq::pdl_wait();  // y may be what the launch before still reads
 #pragma unroll 1
         for (int c = 0; c < BN; c += 16) {
             if (t0 + c >= a.rows) break;
@@ -229,34 +374,34 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = 0x7FFFFFFFu;
             }
-            if (parts > 1) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + m] = __uint_as_float(v[i]);
-            } else if (m0 + m < a.m) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (t0 + c + i < a.rows) put(a, t0 + c + i, m0 + m, __uint_as_float(v[i]) + b);
-            }
+            for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + m] = __uint_as_float(v[i]);
         }
     }
     fence_before();
     __syncwarp();
-    if (parts > 1) {
-        cluster_sync();
-        if (warp >= 2) {
-            const int m = (warp - 2) * 32 + lane;
-            const float b = a.bias && m0 + m < a.m ? __ldg(a.bias + m0 + m) : 0.0f;
-            for (int c = rank; c < BN && t0 + c < a.rows; c += parts) {
-                float v = 0.0f;
-                for (uint32_t r = 0; r < parts; ++r) v += peer_load(base + (c * 128 + m) * 4, r);
-                if (m0 + m < a.m) put(a, t0 + c, m0 + m, v + b);
-            }
+    if (parts > 1) cluster_sync();
+    else __syncthreads();
+    if (warp >= 2) {  // every parts-th token, four outputs a lane, and of those every fourth a warp
+        const int m = lane * 4;
+        float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.bias) {
+            float* w = reinterpret_cast<float*>(&b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (m0 + m + i < a.m) w[i] = __ldg(a.bias + m0 + m + i);
         }
-        __syncwarp();
-        cluster_sync();  // no block's sums are read any more
-    } else {
-        __syncthreads();
+        const uint32_t from = base + m * 4;
+        const int c = static_cast<int>(rank) + (warp - 2) * static_cast<int>(parts), end = min(BN, a.rows - t0);
+        switch (parts) {
+            case 1: join<1>(a, from, c, end, t0, m0 + m, b); break;
+            case 2: join<2>(a, from, c, end, t0, m0 + m, b); break;
+            case 4: join<4>(a, from, c, end, t0, m0 + m, b); break;
+            default: join<8>(a, from, c, end, t0, m0 + m, b); break;
+        }
     }
+    __syncwarp();
+    if (parts > 1) cluster_sync();  // no block's sums are read any more
     if (warp == 1) tmem_free<1>(tmem, C::kCols);
 }
 
@@ -266,6 +411,9 @@ __global__ void __launch_bounds__(192, 1)
 // tokens, and one tcgen05.mma of both tensor cores reads both blocks' shared memory (a step of 128 x 256 in
 // one block would ask for 48 KB of operands in the time of 32).  Pairs stay and take tile after tile; the
 // sums leave TMEM for registers at once, so that the next tile's products go on while they are stored.
+// What bounds it is the time from a step's last product to the arrival of the operands six steps on, in which
+// the other five run: copies of both blocks count on the first one's barrier, which its issuing thread waits
+// for, and waiting threads sleep.
 struct Large {
     static constexpr int BN = 256, kStages = 6, kWarps = 8;         // warps that take the sums
     static constexpr int kThreads = 64 + 32 * kWarps;
@@ -276,15 +424,50 @@ struct Large {
     static constexpr int kSmem = kStages * (kBytes + 3 * kExpTile) + 1024;
 };
 
+// 64 tokens' sums of this lane's output, from token t on.  bf16 (even rows of y at 4 bytes): neighbouring lanes
+// change halves, so that each stores two outputs of every other token.
+__device__ __forceinline__ void put_column(const LArgs& a, int t, int m, float b, const uint32_t (&v)[64]) {
+    if (!a.out_f32 && a.wide) {
+        const int odd = threadIdx.x & 1;
+        bf16* p = static_cast<bf16*>(a.y) + static_cast<int64_t>(t + odd) * a.ldy + (m & ~1);
+        const bool both = (m | 1) < a.m;
+        const int left = a.rows - t - odd;
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+            const uint32_t own = pack2(__uint_as_float(v[j]) + b, __uint_as_float(v[j + 1]) + b, bf16());
+            const uint32_t other = __shfl_xor_sync(kFull, own, 1);
+            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            if (j < left) {
+                if (both) *reinterpret_cast<uint32_t*>(p) = w;
+                else if ((m & ~1) < a.m) *p = __ushort_as_bfloat16(static_cast<uint16_t>(w));
+            }
+            p += 2 * a.ldy;
+        }
+        return;
+    }
+    if (m >= a.m) return;
+    if (a.out_f32) {
+        float* p = static_cast<float*>(a.y) + static_cast<int64_t>(t) * a.ldy + m;
+#pragma unroll
+        for (int j = 0; j < 64; ++j, p += a.ldy)
+            if (t + j < a.rows) *p = __uint_as_float(v[j]) + b;
+    } else {
+        bf16* p = static_cast<bf16*>(a.y) + static_cast<int64_t>(t) * a.ldy + m;
+#pragma unroll
+        for (int j = 0; j < 64; ++j, p += a.ldy)
+            if (t + j < a.rows) *p = __float2bfloat16_rn(__uint_as_float(v[j]) + b);
+    }
+}
+
 template <bool A_OUTER>
 __global__ void __launch_bounds__(Large::kThreads, 1)
     large_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                 const __grid_constant__ CUtensorMap a_exps, const __grid_constant__ CUtensorMap b_exps,
                  const LArgs a) {
     using C = Large;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t raw[];
-    // full: a step's operands are there (in the pair's first block); full_b: the second block's
-    __shared__ alignas(8) uint64_t full[S], full_b[S], empty[S], acc_full, acc_empty, drain;
+    __shared__ alignas(8) uint64_t full[S], empty[S], acc_full, acc_empty, drain;  // full: in the first block
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (gq::smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -295,8 +478,7 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            gq::mbar_init(gq::smem_u32(&full[s]), 2u);
-            gq::mbar_init(gq::smem_u32(&full_b[s]), 1u);
+            gq::mbar_init(gq::smem_u32(&full[s]), 1u);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
@@ -310,7 +492,8 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
     pair_sync<2>();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const int pairs = gridDim.x / 2, tiles = a.tiles_m * ((a.rows + C::BN - 1) / C::BN);
+    const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    const int across = (a.m + 255) / 256, tiles = across * ((a.rows + C::BN - 1) / C::BN);
     const int words = (a.steps + 3) / 4;
     const int last_a = (a.m - 1) / 128, last_b = (a.rows - 1) / 128;  // 128 rows of exponents that exist
 
@@ -319,43 +502,43 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
             int n = 0;
             bool ok = true;
             gq::pdl_wait();  // the tokens' operand may be the launch before's work
-            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs) {
-                const int am = tile % a.tiles_m * 2 + static_cast<int>(rank);  // in 128 rows
-                const int bt = tile / a.tiles_m * 2;
-                const uint8_t* ea = a.a_exps + static_cast<int64_t>(min(am, last_a)) * words * kExpTile;
-                const uint8_t* eb0 = a.b_exps + static_cast<int64_t>(bt) * words * kExpTile;
-                const uint8_t* eb1 = a.b_exps + static_cast<int64_t>(min(bt + 1, last_b)) * words * kExpTile;
+            for (int tile = first; tile < tiles && ok; tile += pairs) {
+                const int am = tile % across * 2 + static_cast<int>(rank);  // in 128 rows
+                const int bt = tile / across * 2;
+                const int ea = min(am, last_a) * words, eb0 = bt * words, eb1 = min(bt + 1, last_b) * words;
                 for (int k = 0; k < a.steps; ++k, ++n) {
                     const int s = n % S;
-                    if (n >= S) ok = gq::mbar_wait(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                    if (n >= S) ok = mbar_rest(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
                     if (!ok) break;
-                    const uint32_t bar = gq::smem_u32(rank == 0 ? &full[s] : &full_b[s]);
+                    const uint32_t bar = place_in(gq::smem_u32(&full[s]), 0);
                     const bool exps = (k & 3) == 0;
-                    gq::mbar_arrive_expect_tx(bar, C::kBytes + (exps ? 3 * kExpTile : 0));
-                    tma_load(a_stage(s), &a_map, A_OUTER ? am * 128 : k * kStep, A_OUTER ? k * kStep : am * 128, bar);
-                    tma_load(b_stage(s), &b_map, k * kStep, (bt + static_cast<int>(rank)) * 128, bar);
+                    if (rank == 0)  // what both blocks will load
+                        gq::mbar_arrive_expect_tx(gq::smem_u32(&full[s]), 2 * (C::kBytes + (exps ? 3 * kExpTile : 0)));
+                    tma_load_pair(a_stage(s), &a_map, A_OUTER ? am * 128 : k * kStep, A_OUTER ? k * kStep : am * 128,
+                                  bar);
+                    tma_load_pair(b_stage(s), &b_map, k * kStep, (bt + static_cast<int>(rank)) * 128, bar);
                     if (exps) {
-                        bulk_load(e_stage(s), ea + (k / 4) * kExpTile, kExpTile, bar);
-                        bulk_load(e_stage(s) + kExpTile, eb0 + (k / 4) * kExpTile, kExpTile, bar);
-                        bulk_load(e_stage(s) + 2 * kExpTile, eb1 + (k / 4) * kExpTile, kExpTile, bar);
+                        tma_load_pair(e_stage(s), &a_exps, 0, ea + k / 4, bar);
+                        tma_load_pair(e_stage(s) + kExpTile, &b_exps, 0, eb0 + k / 4, bar);
+                        tma_load_pair(e_stage(s) + 2 * kExpTile, &b_exps, 0, eb1 + k / 4, bar);
                     }
                 }
             }
-            // nothing of this block's is in flight when it ends, whatever the others did
-            for (int j = n > S ? n - S : 0; j < n; ++j)
-                gq::mbar_wait(gq::smem_u32(rank == 0 ? &full[j % S] : &full_b[j % S]), (j / S) & 1);
+            // nothing that comes to this block is in flight when it ends: what was loaded has been read, and
+            // the word of that has come
+            for (int j = n > S ? n - S : 0; j < n; ++j) mbar_rest(gq::smem_u32(&empty[j % S]), (j / S) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             int n = 0, done = 0;
             bool ok = true;
             uint32_t set = 1;  // of exponents' columns
-            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs, ++done) {
-                if (done > 0) ok = gq::mbar_wait(gq::smem_u32(&acc_empty), (done - 1) & 1);
+            for (int tile = first; tile < tiles && ok; tile += pairs, ++done) {
+                if (done > 0) ok = mbar_rest(gq::smem_u32(&acc_empty), (done - 1) & 1);
                 fence_after();
                 for (int k = 0; k < a.steps && ok; ++k, ++n) {
                     const int s = n % S;
-                    ok = gq::mbar_wait(gq::smem_u32(&full[s]), (n / S) & 1);
+                    ok = mbar_rest(gq::smem_u32(&full[s]), (n / S) & 1);
                     if (!ok) break;
                     fence_after();
                     if ((k & 3) == 0) {
@@ -376,45 +559,35 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
             }
             if (!ok) {  // let what was issued finish before TMEM is given back
                 mma_commit<2>(gq::smem_u32(&drain));
-                gq::mbar_wait(gq::smem_u32(&drain), 0);
+                mbar_rest(gq::smem_u32(&drain), 0);
             }
-        } else if (lane == 0) {  // the second block: tells the first that its operands have arrived
-            int n = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs)
-                for (int k = 0; k < a.steps && ok; ++k, ++n) {
-                    ok = gq::mbar_wait(gq::smem_u32(&full_b[n % S]), (n / S) & 1);
-                    if (ok) arrive_first<2>(gq::smem_u32(&full[n % S]));
-                }
         }
     } else {
         const int quad = warp & 3, group = (warp - 2) >> 2;
         int done = 0;
         bool ok = true;
         gq::pdl_wait();  // y may be what the launch before still reads
-        for (int tile = blockIdx.x / 2; tile < tiles; tile += pairs, ++done) {
-            const int m = (tile % a.tiles_m * 2 + static_cast<int>(rank)) * 128 + quad * 32 + lane;
-            const int t0 = tile / a.tiles_m * C::BN + group * 128;
+        for (int tile = first; tile < tiles; tile += pairs, ++done) {
+            const int m = (tile % across * 2 + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+            const int t0 = tile / across * C::BN + group * 128;
             const float b = a.bias && m < a.m ? __ldg(a.bias + m) : 0.0f;
-            if (ok) ok = gq::mbar_wait(gq::smem_u32(&acc_full), done & 1);
+            if (ok) ok = mbar_rest(gq::smem_u32(&acc_full), done & 1);
             ok = __all_sync(kFull, ok);
             fence_after();
-            uint32_t v[4][32];
+            uint32_t v[2][64];
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * 128 + j * 32, v[j]);
+                for (int j = 0; j < 2; ++j)
+                    tmem_load(tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * 128 + j * 64, v[j]);
             } else {  // a wait gave up: the tile is marked
 #pragma unroll
-                for (int j = 0; j < 128; ++j) v[j >> 5][j & 31] = 0x7FFFFFFFu;
+                for (int j = 0; j < 128; ++j) v[j >> 6][j & 63] = 0x7FFFFFFFu;
             }
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_first<2>(gq::smem_u32(&acc_empty));
-            if (m >= a.m) continue;
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-                if (t0 + j < a.rows) put(a, t0 + j, m, __uint_as_float(v[j >> 5][j & 31]) + b);
+            put_column(a, t0, m, b, v[0]);
+            put_column(a, t0 + 64, m, b, v[1]);
         }
     }
     __syncwarp();
@@ -439,11 +612,23 @@ bool byte_map(CUtensorMap* map, const uint8_t* p, int64_t width, int64_t rows, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Exponents of a matrix of `rows` rows as rows of 512 bytes, one of them per box.
+bool exp_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t steps) {
+    EncodeFn encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {kExpTile / 4, static_cast<cuuint64_t>((rows + 127) / 128 * ((steps + 3) / 4))};
+    const cuuint64_t strides[1] = {kExpTile};
+    const cuuint32_t sizes[2] = {kExpTile / 4, 1}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, sizes, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // early: the launch before this one on the stream wrote the tokens' operand, and let this one start.
-template <typename C, bool A_OUTER>
-gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, int parts, bool early,
-                       cudaStream_t st) {
-    auto k = small_kernel<C, A_OUTER>;
+template <typename C, bool A_OUTER, typename T>
+gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, int64_t depth, int parts,
+                       bool early, cudaStream_t st) {
+    auto k = small_kernel<C, A_OUTER, T>;
     gqh::blocks_per_sm(k, C::kSmem, 192);  // raises the shared-memory limit once
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * ((a.rows + C::BN - 1) / C::BN);
     cudaLaunchConfig_t cfg = {};
@@ -452,24 +637,32 @@ gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    int n = 0;
+    if (parts > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(parts);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = early ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a) != cudaSuccess) return GQ_ERR_CUDA;
+    cfg.numAttrs = n;
+    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a, static_cast<int>(depth)) != cudaSuccess) return GQ_ERR_CUDA;
     return gqh::launch_status();
 }
 
 template <bool A_OUTER>
-gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs a, bool early, cudaStream_t st) {
+gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, bool early, cudaStream_t st) {
     auto k = large_kernel<A_OUTER>;
     gqh::blocks_per_sm(k, Large::kSmem, Large::kThreads);  // raises the shared-memory limit once
-    a.tiles_m = (a.m + 255) / 256;
-    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * ((a.rows + Large::BN - 1) / Large::BN);
+    const int64_t tiles = (static_cast<int64_t>(a.m) + 255) / 256 * ((static_cast<int64_t>(a.rows) + Large::BN - 1) / Large::BN);
     const int64_t pairs = gqh::sm_count() / 2;
+    CUtensorMap a_exps, b_exps;
+    if (!exp_map(&a_exps, a.a_exps, a.m, a.steps) || !exp_map(&b_exps, a.b_exps, a.rows, a.steps)) return GQ_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(Large::kThreads);
@@ -483,8 +676,22 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a_exps, b_exps, a) != cudaSuccess) return GQ_ERR_CUDA;
     return gqh::launch_status();
+}
+
+// The form that a call takes: bn tokens per tile and parts of the sums, Large::BN for the large form.
+struct Choice {
+    int bn, parts;
+    bool fused;
+};
+Choice choose(int64_t rows, int64_t tiles_m, int64_t steps, int64_t sms, bool from_x) {
+    if ((tiles_m + 1) / 2 * ((rows + 255) / 256) >= 64) return {Large::BN, 1, false};
+    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    const int64_t tiles = tiles_m * ((rows + bn - 1) / bn);
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= sms && steps >= parts * 2) parts *= 2;
+    return {bn, parts, from_x && bn <= 32};
 }
 
 // D = A B^T as above: `outs` rows of A, sums over `depth`.
@@ -500,33 +707,42 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     if (rows == 0) return GQ_OK;
     if (!saved_ok(xcodes, xexps) || !saved_ok(wcodes, wexps)) return GQ_ERR_INVALID;
     const int64_t sms = gqh::sm_count(), tiles_m = (outs + 127) / 128, steps = (depth + kStep - 1) / kStep;
-    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int64_t tiles = tiles_m * ((rows + bn - 1) / bn);
-    if (tiles * 8 >= int64_t(1) << 31) return GQ_ERR_INVALID;
-    CUtensorMap a_map, b_map;
-    if (!byte_map(&a_map, wcodes, A_OUTER ? outs : depth, A_OUTER ? depth : outs,
-                  fp8_pitch(A_OUTER ? outs : depth), 128) ||
-        !byte_map(&b_map, xcodes, depth, rows, fp8_pitch(depth), bn))
-        return GQ_ERR_CUDA;
-    if (x) {
-        const gq_status r = gq_fp8_quantize(x, dtype, rows, depth, ldx, 1, xcodes, xexps, nullptr, st);
-        if (r != GQ_OK) return r;
-    }
+    if (tiles_m * ((rows + 15) / 16) * 8 >= int64_t(1) << 31) return GQ_ERR_INVALID;
     LArgs a;
     a.rows = static_cast<int>(rows); a.m = static_cast<int>(outs);
     a.steps = static_cast<int>(steps); a.tiles_m = static_cast<int>(tiles_m);
     a.a_exps = wexps; a.b_exps = xexps; a.bias = bias;
     a.y = y; a.ldy = ldy; a.out_f32 = out_dtype == GQ_F32;
-    if (((outs + 255) / 256) * ((rows + 255) / 256) >= 64)
-        return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
-    int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= sms && steps >= parts * 2) parts *= 2;
-    switch (bn) {
-        case 16: return launch_small<Small<16>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
-        case 32: return launch_small<Small<32>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
-        case 64: return launch_small<Small<64>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
-        default: return launch_small<Small<128>, A_OUTER>(a_map, b_map, a, parts, x != nullptr, st);
+    a.wide = mult(y, a.out_f32 ? 16 : 8) && (ldy % 4 == 0 || rows == 1);
+    a.x = x; a.ldx = ldx;
+    const Choice c = choose(rows, tiles_m, steps, sms, x != nullptr);
+    if (c.bn < 128 && rows > c.bn) return GQ_ERR_INVALID;  // see Small
+    CUtensorMap a_map, b_map;
+    if (!byte_map(&a_map, wcodes, A_OUTER ? outs : depth, A_OUTER ? depth : outs,
+                  fp8_pitch(A_OUTER ? outs : depth), 128))
+        return GQ_ERR_CUDA;
+    if (c.fused) {
+        b_map = a_map;  // not used
+    } else {
+        if (!byte_map(&b_map, xcodes, depth, rows, fp8_pitch(depth), c.bn < 128 ? c.bn : 128)) return GQ_ERR_CUDA;
+        if (x) {
+            const gq_status r = gq_fp8_quantize(x, dtype, rows, depth, ldx, 1, xcodes, xexps, nullptr, st);
+            if (r != GQ_OK) return r;
+        }
     }
+    if (c.bn == Large::BN) return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
+#define GQA_SMALL(BN, T) launch_small<Small<BN>, A_OUTER, T>(a_map, b_map, a, depth, c.parts, x && !c.fused, st)
+    if (c.fused && dtype == GQ_F32)
+        return c.bn == 16 ? GQA_SMALL(16, float) : GQA_SMALL(32, float);
+    if (c.fused)
+        return c.bn == 16 ? GQA_SMALL(16, bf16) : GQA_SMALL(32, bf16);
+    switch (c.bn) {
+        case 16: return GQA_SMALL(16, void);
+        case 32: return GQA_SMALL(32, void);
+        case 64: return GQA_SMALL(64, void);
+        default: return GQA_SMALL(128, void);
+    }
+#undef GQA_SMALL
 }
 
 }  // namespace

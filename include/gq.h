@@ -590,10 +590,11 @@ gq_status gq_fp8_dequantize(const uint8_t *codes, const uint8_t *exps, int64_t r
 /*
  * y[t][o] = sum over i of X[t][i] W[o][i] + bias[o]  (rows x outs, out_dtype GQ_F32 or GQ_BF16, rows
  * ldy apart; bias nullable, fp32) with X (rows x cols, block_rows = 1) and W (outs x cols, either
- * block_rows) in 8-bit floating point.  Where x is not null, X is made from it first (gq_fp8_quantize
- * into xcodes and xexps, which keep it).  The tensor cores multiply codes and apply the scales; sums
- * are fp32 and in a fixed order, rounded once.  A bounded wait that gives up (about a second; a broken
- * kernel only) leaves NaN in the tiles concerned.  rows, outs and cols < 2^30.
+ * block_rows) in 8-bit floating point.  Where x is not null, X is made from it (as by gq_fp8_quantize), and
+ * xcodes and xexps are room for it, whose contents afterwards are not to be relied on.  The tensor cores
+ * multiply codes and apply the scales; sums are fp32 and in a fixed order, rounded once.  A bounded wait that
+ * gives up (about a second; a broken kernel only) leaves NaN in the tiles concerned.  rows, outs and
+ * cols < 2^30.
  */
 gq_status gq_fp8_linear(const void *x, int dtype, int64_t ldx, uint8_t *xcodes, uint8_t *xexps,
                         int64_t rows, int64_t cols, const uint8_t *wcodes, const uint8_t *wexps,

@@ -156,7 +156,7 @@ def forward(gq, rows, cols, outs, dtype, out, tiles=True, bias=True, seed=0, ext
 PRODUCTS = [(1, 1, 1), (1, 128, 128), (1, 4096, 512), (2, 130, 100), (5, 640, 129), (16, 512, 256), (17, 1000, 40),
             (33, 2048, 300), (64, 96, 1000), (65, 1300, 700), (100, 256, 1024), (128, 768, 768), (200, 513, 127),
             (384, 768, 768), (1021, 1001, 2050), (2000, 700, 900), (3000, 2560, 1024), (2100, 1300, 2100),
-            (4000, 260, 1100), (300, 520, 12000), (9000, 2100, 700), (2500, 4096, 2304)]
+            (4000, 260, 1100), (300, 520, 12000), (9000, 2100, 700), (2500, 4096, 2304), (17000, 200, 250)]
 
 
 @pytest.mark.parametrize("rows,cols,outs", PRODUCTS)
