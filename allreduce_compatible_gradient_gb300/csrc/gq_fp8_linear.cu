@@ -313,31 +313,35 @@ __global__ void __launch_bounds__(192, 1)
             for (int j = n > S ? n - S : 0; j < n; ++j) mbar_rest(gq::smem_u32(&full[j % S]), (j / S) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t set = 1, set_b = 1;  // of exponents' columns
-            for (int n = 0; n < k1 - k0; ++n) {
-                const int k = k0 + n, s = n % S;
-                ok = mbar_rest(gq::smem_u32(&full[s]), (n / S) & 1);
-                if (!ok) break;
-                fence_after();
-                if (with_exps(k)) {
-                    set ^= 1u;
-                    copy_exps<1>(tmem + C::kExps + 4 * set, exp_operand(e_stage(s)));
-                }
-                if (FUSED || with_exps(k)) {  // (a fused call has a step's bytes with the step)
-                    set_b ^= 1u;
-                    copy_exps<1>(tmem + C::kExps + 8 + 4 * set_b, exp_operand(e_stage(s) + kExpTile));
-                }
-                const uint32_t sa = tmem + C::kExps + 4 * set, sb = tmem + C::kExps + 8 + 4 * set_b;
+        bool ok = true;
+        uint32_t set = 1, set_b = 1;  // of exponents' columns
+        for (int n = 0; n < k1 - k0; ++n) {
+            const int k = k0 + n, s = n % S;
+            ok = __all_sync(kFull, mbar_rest(gq::smem_u32(&full[s]), (n / S) & 1));
+            if (!ok) break;
+            fence_after();
+            const bool exps = with_exps(k), exps_b = FUSED || exps;  // (a fused call has a step's bytes with the step)
+            if (exps) set ^= 1u;
+            if (exps_b) set_b ^= 1u;
+            const uint32_t sa = tmem + C::kExps + 4 * set, sb = tmem + C::kExps + 8 + 4 * set_b;
+            const uint64_t da = operand(a_stage(s)), db = operand(b_stage(s));
+            const uint32_t idesc = Instruction<1, BN, A_OUTER>::of(k & 3);
+            if (elect_one()) {
+                if (exps) copy_exps<1>(sa, exp_operand(e_stage(s)));
+                if (exps_b) copy_exps<1>(sb, exp_operand(e_stage(s) + kExpTile));
 #pragma unroll
                 for (int kk = 0; kk < kStep / 32; ++kk)
-                    mma_fp8<1>(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)), operand(b_stage(s) + kk * 32),
-                               Instruction<1, BN, A_OUTER>::of(k & 3), sa, sb, n > 0 || kk > 0);
+                    mma_fp8<1>(tmem, da + kk * ((A_OUTER ? 32 * 128 : 32) >> 4), db + kk * (32 >> 4), idesc, sa, sb,
+                               n > 0 || kk > 0);
                 mma_commit<1>(gq::smem_u32(&empty[s]));
+                if (n + 1 == k1 - k0) mma_commit<1>(gq::smem_u32(&acc_full));
             }
-            mma_commit<1>(gq::smem_u32(ok ? &acc_full : &drain));
-            if (!ok) mbar_rest(gq::smem_u32(&drain), 0);  // what was issued finishes before TMEM is freed
+            __syncwarp();
+        }
+        if (!ok) {  // what was issued finishes before TMEM is freed
+            if (elect_one()) mma_commit<1>(gq::smem_u32(&drain));
+            __syncwarp();
+            mbar_rest(gq::smem_u32(&drain), 0);
         }
     } else {
         const int q = warp & 3, m = q * 32 + lane;
@@ -529,36 +533,44 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
             for (int j = n > S ? n - S : 0; j < n; ++j) mbar_rest(gq::smem_u32(&empty[j % S]), (j / S) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int n = 0, done = 0;
             bool ok = true;
             uint32_t set = 1;  // of exponents' columns
-            for (int tile = first; tile < tiles && ok; tile += pairs, ++done) {
-                if (done > 0) ok = mbar_rest(gq::smem_u32(&acc_empty), (done - 1) & 1);
+            auto wait = [&](uint64_t* bar, int phase) {
+                ok = __all_sync(kFull, mbar_rest(gq::smem_u32(bar), phase & 1));
                 fence_after();
+            };
+            for (int tile = first; tile < tiles && ok; tile += pairs, ++done) {
+                if (done > 0) wait(&acc_empty, done - 1);
                 for (int k = 0; k < a.steps && ok; ++k, ++n) {
                     const int s = n % S;
-                    ok = mbar_rest(gq::smem_u32(&full[s]), (n / S) & 1);
+                    wait(&full[s], n / S);
                     if (!ok) break;
-                    fence_after();
-                    if ((k & 3) == 0) {
-                        set ^= 1u;
-#pragma unroll
-                        for (int j = 0; j < 3; ++j)
-                            copy_exps<2>(tmem + C::kExps + C::kSet * set + 4 * j, exp_operand(e_stage(s) + j * kExpTile));
-                    }
+                    const bool exps = (k & 3) == 0;
+                    if (exps) set ^= 1u;
                     const uint32_t sa = tmem + C::kExps + C::kSet * set;
+                    const uint64_t da = operand(a_stage(s)), db = operand(b_stage(s));
+                    const uint32_t idesc = Instruction<2, C::BN, A_OUTER>::of(k & 3);
+                    if (elect_one()) {
+                        if (exps) {
 #pragma unroll
-                    for (int kk = 0; kk < kStep / 32; ++kk)
-                        mma_fp8<2>(tmem, operand(a_stage(s) + kk * (A_OUTER ? 32 * 128 : 32)),
-                                   operand(b_stage(s) + kk * 32), Instruction<2, C::BN, A_OUTER>::of(k & 3), sa, sa + 4,
-                                   k > 0 || kk > 0);
-                    mma_commit<2>(gq::smem_u32(&empty[s]));
+                            for (int j = 0; j < 3; ++j)
+                                copy_exps<2>(sa + 4 * j, exp_operand(e_stage(s) + j * kExpTile));
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < kStep / 32; ++kk)
+                            mma_fp8<2>(tmem, da + kk * ((A_OUTER ? 32 * 128 : 32) >> 4), db + kk * (32 >> 4), idesc, sa,
+                                       sa + 4, k > 0 || kk > 0);
+                        mma_commit<2>(gq::smem_u32(&empty[s]));
+                        if (k + 1 == a.steps) mma_commit<2>(gq::smem_u32(&acc_full));
+                    }
+                    __syncwarp();
                 }
-                if (ok) mma_commit<2>(gq::smem_u32(&acc_full));
             }
             if (!ok) {  // let what was issued finish before TMEM is given back
-                mma_commit<2>(gq::smem_u32(&drain));
+                if (elect_one()) mma_commit<2>(gq::smem_u32(&drain));
+                __syncwarp();
                 mbar_rest(gq::smem_u32(&drain), 0);
             }
         }

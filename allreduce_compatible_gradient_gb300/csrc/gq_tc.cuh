@@ -69,6 +69,18 @@ template <int CG> __device__ __forceinline__ void pair_sync() {
         __syncthreads();
     }
 }
+// One thread of a warp that is here as a whole.  Instructions of the tensor cores that it issues take their
+// operands from registers of the warp; behind a branch on the lane's number each one waited for its operands to
+// be moved there (4 tcgen05.mma and a commit 406 cycles, longer than their products take).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
