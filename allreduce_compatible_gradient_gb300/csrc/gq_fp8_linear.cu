@@ -425,30 +425,15 @@ struct Large {
     static constexpr int kExps = BN;                                // columns of exponents: two sets, in turn,
     static constexpr int kSet = 12;                                 // of 4 for the outputs and 8 for the tokens
     static constexpr int kCols = 512;
-    static constexpr int kSmem = kStages * (kBytes + 3 * kExpTile) + 1024;
+    // rows of y on their way out: two groups of warps, three buffers of 16 tokens each
+    static constexpr int kOut = 16, kRing = 3, kOutBytes = kOut * 256;
+    static constexpr int kOperands = kStages * (kBytes + 3 * kExpTile);
+    static constexpr int kSmem = kOperands + 2 * kRing * kOutBytes + 1024;
 };
 
-// 64 tokens' sums of this lane's output, from token t on.  bf16 (even rows of y at 4 bytes): neighbouring lanes
-// change halves, so that each stores two outputs of every other token.
+// 64 tokens' sums of this lane's output, from token t on, element by element: fp32, and rows of y that the TMA
+// cannot write.
 __device__ __forceinline__ void put_column(const LArgs& a, int t, int m, float b, const uint32_t (&v)[64]) {
-    if (!a.out_f32 && a.wide) {
-        const int odd = threadIdx.x & 1;
-        bf16* p = static_cast<bf16*>(a.y) + static_cast<int64_t>(t + odd) * a.ldy + (m & ~1);
-        const bool both = (m | 1) < a.m;
-        const int left = a.rows - t - odd;
-#pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-            const uint32_t own = pack2(__uint_as_float(v[j]) + b, __uint_as_float(v[j + 1]) + b, bf16());
-            const uint32_t other = __shfl_xor_sync(kFull, own, 1);
-            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-            if (j < left) {
-                if (both) *reinterpret_cast<uint32_t*>(p) = w;
-                else if ((m & ~1) < a.m) *p = __ushort_as_bfloat16(static_cast<uint16_t>(w));
-            }
-            p += 2 * a.ldy;
-        }
-        return;
-    }
     if (m >= a.m) return;
     if (a.out_f32) {
         float* p = static_cast<float*>(a.y) + static_cast<int64_t>(t) * a.ldy + m;
@@ -462,12 +447,45 @@ __device__ __forceinline__ void put_column(const LArgs& a, int t, int m, float b
             if (t + j < a.rows) *p = __float2bfloat16_rn(__uint_as_float(v[j]) + b);
     }
 }
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+
+// The same through shared memory, in bf16: four warps fill 16 tokens' rows of 128 outputs, which the TMA takes
+// to y while they fill the next (two stores of 64 bytes in every instruction, straight from registers, took
+// 4 us a tile).  next: the ring's place, the same for the group.
+__device__ __forceinline__ void put_rows(const CUtensorMap* y_map, uint32_t ring, int group, int warp, int lane, int t,
+                                         int m0, int rows, float b, const uint32_t (&v)[64],
+                                         int& next) {
+    using C = Large;
+    const bool leads = warp == 0 && lane == 0;
+#pragma unroll
+    for (int c = 0; c < 64; c += C::kOut) {
+        const uint32_t at = ring + next * C::kOutBytes;
+        if (leads) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::kRing - 1) : "memory");
+        group_sync(group);
+#pragma unroll
+        for (int j = 0; j < C::kOut; j += 2) {
+            const uint32_t w = pack2(__uint_as_float(v[c + j]) + b, __uint_as_float(v[c + j + 1]) + b, bf16());
+            const uint32_t to = at + j * 256 + (warp * 32 + lane) * 2;
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(static_cast<uint16_t>(w)) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + 256), "h"(static_cast<uint16_t>(w >> 16)) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        group_sync(group);
+        if (leads && t + c < rows) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(y_map),
+                         "r"(m0), "r"(t + c), "r"(at)
+                         : "memory");
+        }
+        if (leads) asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // (the ring counts empty ones too)
+        next = next + 1 == C::kRing ? 0 : next + 1;
+    }
+}
 
 template <bool A_OUTER>
 __global__ void __launch_bounds__(Large::kThreads, 1)
     large_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                  const __grid_constant__ CUtensorMap a_exps, const __grid_constant__ CUtensorMap b_exps,
-                 const LArgs a) {
+                 const __grid_constant__ CUtensorMap y_map, const LArgs a) {
     using C = Large;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t raw[];
@@ -576,11 +594,12 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
         }
     } else {
         const int quad = warp & 3, group = (warp - 2) >> 2;
-        int done = 0;
+        const uint32_t ring = base + C::kOperands + group * (C::kRing * C::kOutBytes);
+        int done = 0, next = 0;
         bool ok = true;
         gq::pdl_wait();  // y may be what the launch before still reads
         for (int tile = first; tile < tiles; tile += pairs, ++done) {
-            const int m = (tile % across * 2 + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+            const int m0 = (tile % across * 2 + static_cast<int>(rank)) * 128, m = m0 + quad * 32 + lane;
             const int t0 = tile / across * C::BN + group * 128;
             const float b = a.bias && m < a.m ? __ldg(a.bias + m) : 0.0f;
             if (ok) ok = mbar_rest(gq::smem_u32(&acc_full), done & 1);
@@ -598,9 +617,20 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_first<2>(gq::smem_u32(&acc_empty));
-            put_column(a, t0, m, b, v[0]);
-            put_column(a, t0 + 64, m, b, v[1]);
+            if (a.wide) {
+                if (m0 >= a.m) continue;  // (the whole group)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (t0 + 64 * j < a.rows)
+                        put_rows(&y_map, ring, group, quad, lane, t0 + 64 * j, m0, a.rows, b, v[j],
+                                 next);
+            } else {
+                put_column(a, t0, m, b, v[0]);
+                put_column(a, t0 + 64, m, b, v[1]);
+            }
         }
+        // nothing leaves shared memory any more when the block ends
+        if (quad == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     fence_before();
@@ -632,6 +662,20 @@ bool exp_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t steps) {
     const cuuint64_t strides[1] = {kExpTile};
     const cuuint32_t sizes[2] = {kExpTile / 4, 1}, one[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, sizes, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y in bf16, in boxes of 128 outputs x 16 tokens; false where its rows do not suit the TMA.
+bool out_map(CUtensorMap* map, const LArgs& a) {
+    EncodeFn encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.m), static_cast<cuuint64_t>(a.rows)};
+    const cuuint64_t strides[1] = {a.rows > 1 ? static_cast<cuuint64_t>(a.ldy) * 2
+                                              : (static_cast<cuuint64_t>(a.m) * 2 + 15) / 16 * 16};
+    const cuuint32_t sizes[2] = {128, Large::kOut}, one[2] = {1, 1};
+    return strides[0] < (cuuint64_t(1) << 40) &&
+           encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y, dims, strides, sizes, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -668,13 +712,15 @@ gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const
 }
 
 template <bool A_OUTER>
-gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, bool early, cudaStream_t st) {
+gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs a, bool early, cudaStream_t st) {
     auto k = large_kernel<A_OUTER>;
     gqh::blocks_per_sm(k, Large::kSmem, Large::kThreads);  // raises the shared-memory limit once
     const int64_t tiles = (static_cast<int64_t>(a.m) + 255) / 256 * ((static_cast<int64_t>(a.rows) + Large::BN - 1) / Large::BN);
     const int64_t pairs = gqh::sm_count() / 2;
     CUtensorMap a_exps, b_exps;
     if (!exp_map(&a_exps, a.a_exps, a.m, a.steps) || !exp_map(&b_exps, a.b_exps, a.rows, a.steps)) return GQ_ERR_CUDA;
+    CUtensorMap y_map = a_map;  // not used where it cannot be made
+    a.wide = !a.out_f32 && mult(a.y, 16) && (a.ldy % 8 == 0 || a.rows == 1) && out_map(&y_map, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(Large::kThreads);
@@ -688,7 +734,7 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, const
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a_exps, b_exps, a) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a_exps, b_exps, y_map, a) != cudaSuccess) return GQ_ERR_CUDA;
     return gqh::launch_status();
 }
 
