@@ -133,8 +133,8 @@ __device__ __forceinline__ void put4(const LArgs& a, int64_t token, int out, flo
 template <int BN_> struct Small {
     static constexpr int BN = BN_;
     static constexpr int kBytes = kTile + BN * kStep;      // of a step's operands
-    static constexpr int kStages = BN <= 32 ? 8 : 6;
-    static constexpr int kCols = BN <= 16 ? 32 : BN <= 32 ? 64 : BN <= 64 ? 128 : 256;  // of TMEM
+    static constexpr int kStages = BN <= 16 ? 8 : 6;
+    static constexpr int kCols = BN <= 16 ? 32 : BN <= 64 ? 128 : 256;  // of TMEM
     // columns behind the accumulator: two sets of 4 for W's exponents, two of 4 for the tokens'
     static constexpr int kExps = BN;
     static_assert(kExps + 16 <= kCols, "exponents fit behind the accumulator");
@@ -349,19 +349,31 @@ __global__ void __launch_bounds__(192, 1)
         if constexpr (FUSED) {
             const int thread = threadIdx.x - 64;
             const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(a.ldx * sizeof(T))) & 15u) == 0;
-            Squeeze<T, BN> now, next;
-            next.fetch(a, k0, depth, thread, wide);
-            for (int n = 0; n < k1 - k0; ++n) {
-                const int s = n % S;
-                now = next;
-                if (n + 1 < k1 - k0) next.fetch(a, k0 + n + 1, depth, thread, wide);
-                if (n >= S && ok) ok = mbar_rest(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                now.store(b_stage(s), e_stage(s) + kExpTile, k0 + n, thread);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full[s]));
+            // steps' loads on their way while as many are put into 8 bits
+            constexpr int B = sizeof(T) == 4 ? 2 : 4;
+            Squeeze<T, BN> now[B], next[B];
+            auto fetch = [&](int n) {
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if (n + j < k1 - k0) next[j].fetch(a, k0 + n + j, depth, thread, wide);
+            };
+            fetch(0);
+            for (int n0 = 0; n0 < k1 - k0 && ok; n0 += B) {
+#pragma unroll
+                for (int j = 0; j < B; ++j) now[j] = next[j];
+                fetch(n0 + B);
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    const int n = n0 + j, s = n % S;
+                    if (n >= k1 - k0 || !ok) break;
+                    if (n >= S) ok = mbar_rest(gq::smem_u32(&empty[s]), ((n / S) - 1) & 1);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    now[j].store(b_stage(s), e_stage(s) + kExpTile, k0 + n, thread);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) gq::mbar_arrive(gq::smem_u32(&full[s]));
+                }
             }
         }
         if (ok) ok = mbar_rest(gq::smem_u32(&acc_full), 0);
@@ -738,18 +750,32 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
     return gqh::launch_status();
 }
 
-// The form that a call takes: bn tokens per tile and parts of the sums, Large::BN for the large form.
+// The form that a call takes: bn tokens per tile and parts of the sums, Large::BN for the large form; fused: one
+// launch, which puts x into 8 bits itself.  The smallest of the times that the waves of blocks take, in
+// microseconds as measured in graphs: 5 for a launch's ends, and for each wave 2 and 0.28 a step (0.7 more for a
+// join); 6 and 1 in the large form, whose pairs stay.  Both sides, depth x outputs for so many tokens: 768 x
+// 768 for 384 in four parts 6.3 and in one 7.1, 4,096 x 4,096 for 256 in two parts 11.9, in one 15.6, large
+// 15.6; for 1,024 tokens of 1,024 x 4,096 large 8.9 and small 15.4, 256 x 256 for 4,096 large 6.9 and small
+// 5.7.  Fused or not, 4,096 x 4,096: 1 token 6.6 and 7.8, 16 tokens 7.8 and 8.4, 32 tokens 8.9 and 8.1.
 struct Choice {
     int bn, parts;
     bool fused;
 };
-Choice choose(int64_t rows, int64_t tiles_m, int64_t steps, int64_t sms, bool from_x) {
-    if ((tiles_m + 1) / 2 * ((rows + 255) / 256) >= 64) return {Large::BN, 1, false};
-    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int64_t tiles = tiles_m * ((rows + bn - 1) / bn);
-    int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= sms && steps >= parts * 2) parts *= 2;
-    return {bn, parts, from_x && bn <= 32};
+Choice choose(int64_t rows, int64_t outs, int64_t steps, int64_t sms, bool from_x) {
+    const int bn = rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+    const int64_t tiles = (outs + 127) / 128 * ((rows + bn - 1) / bn);
+    const int64_t large = (outs + 255) / 256 * ((rows + Large::BN - 1) / Large::BN), pairs = sms / 2;
+    double best = 6.0 + static_cast<double>((large + pairs - 1) / pairs) * (1.0 + 0.28 * steps);
+    Choice c{Large::BN, 1, false};
+    for (int parts = 1; parts <= 8 && parts <= steps; parts *= 2) {
+        const double waves = static_cast<double>((tiles * parts + sms - 1) / sms);
+        const double t = 5.0 + waves * (2.0 + 0.28 * ((steps + parts - 1) / parts)) + (parts > 1 ? 0.7 : 0.0);
+        if (t <= best) {
+            best = t;
+            c = {bn, parts, from_x && bn == 16};
+        }
+    }
+    return c;
 }
 
 // D = A B^T as above: `outs` rows of A, sums over `depth`.
@@ -773,7 +799,7 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     a.y = y; a.ldy = ldy; a.out_f32 = out_dtype == GQ_F32;
     a.wide = mult(y, a.out_f32 ? 16 : 8) && (ldy % 4 == 0 || rows == 1);
     a.x = x; a.ldx = ldx;
-    const Choice c = choose(rows, tiles_m, steps, sms, x != nullptr);
+    const Choice c = choose(rows, outs, steps, sms, x != nullptr);
     if (c.bn < 128 && rows > c.bn) return GQ_ERR_INVALID;  // see Small
     CUtensorMap a_map, b_map;
     if (!byte_map(&a_map, wcodes, A_OUTER ? outs : depth, A_OUTER ? depth : outs,
@@ -790,13 +816,9 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     }
     if (c.bn == Large::BN) return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
 #define GQA_SMALL(BN, T) launch_small<Small<BN>, A_OUTER, T>(a_map, b_map, a, depth, c.parts, x && !c.fused, st)
-    if (c.fused && dtype == GQ_F32)
-        return c.bn == 16 ? GQA_SMALL(16, float) : GQA_SMALL(32, float);
-    if (c.fused)
-        return c.bn == 16 ? GQA_SMALL(16, bf16) : GQA_SMALL(32, bf16);
+    if (c.fused) return dtype == GQ_F32 ? GQA_SMALL(16, float) : GQA_SMALL(16, bf16);
     switch (c.bn) {
         case 16: return GQA_SMALL(16, void);
-        case 32: return GQA_SMALL(32, void);
         case 64: return GQA_SMALL(64, void);
         default: return GQA_SMALL(128, void);
     }
