@@ -4,6 +4,8 @@ rules for matrices, streams and autograd.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _activations as _acts
@@ -24,7 +26,7 @@ def _up(v, m):
 
 
 def _exp_shape(rows, cols):
-    return _up(rows, 128) // 128, _up(cols, 512) // 512, 32, 4, 4
+    return (rows + 127) // 128, (cols + 511) // 512, 32, 4, 4
 
 
 class Fp8:
@@ -37,20 +39,18 @@ class Fp8:
 
     def __init__(self, codes: torch.Tensor, exps: torch.Tensor, cols: int, exps_t: torch.Tensor | None = None,
                  shape=None):
-        rows = codes.shape[0] if codes.dim() == 2 else -1
-        if cols < 1 or rows < 0 or codes.shape[1] != _up(cols, 16) or exps.shape != _exp_shape(rows, cols):
+        rows, pitch = codes.shape if codes.dim() == 2 else (-1, 0)
+        if cols < 1 or rows < 0 or pitch != (cols + 15) // 16 * 16 or exps.shape != _exp_shape(rows, cols):
             raise ValueError("a matrix of %d columns has codes of rows x %d and exponents %s, got %s and %s"
                              % (cols, _up(cols, 16), _exp_shape(max(rows, 0), cols), tuple(codes.shape),
                                 tuple(exps.shape)))
         if exps_t is not None and exps_t.shape != _exp_shape(cols, rows):
             raise ValueError("the transposed matrix has exponents %s, got %s"
                              % (_exp_shape(cols, rows), tuple(exps_t.shape)))
-        if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or any(
-                e is not None and e.dtype != torch.uint8 for e in (exps, exps_t)):
+        if (codes.dtype is not torch.uint8 and codes.dtype is not torch.float8_e4m3fn
+                or exps.dtype is not torch.uint8 or exps_t is not None and exps_t.dtype is not torch.uint8):
             raise TypeError("codes must be uint8 or float8_e4m3fn and exponents uint8")
-        for t in (codes, exps, exps_t):
-            if t is not None and (not t.is_contiguous() or not t.is_cuda or t.get_device() != codes.get_device()):
-                raise ValueError("codes and exponents must be contiguous and on one CUDA device")
+        # (that all of it is contiguous, and on one device, is checked by every call)
         self.shape = (rows, cols) if shape is None else tuple(shape)
         self._rows, self._cols, self._tiles = rows, cols, exps_t is not None
         self._codes, self._exps, self._exps_t = codes, exps, exps_t
@@ -92,14 +92,9 @@ class Fp8:
         shapes = ((self._rows, pitch), _exp_shape(self._rows, self._cols), _exp_shape(self._cols, self._rows))
         if k == 2 and not self._tiles:
             return None
-        at, view = 0, None
-        for shape in shapes[:k + 1]:
-            n = 1
-            for v in shape:
-                n *= v
-            view = self._codes[at:at + n].view(shape)
-            at += n
-        return view
+        sizes = [math.prod(v) for v in shapes]
+        at = sum(sizes[:k])
+        return self._codes[at:at + sizes[k]].view(shapes[k])
 
     @property
     def codes(self) -> torch.Tensor:

@@ -15,6 +15,11 @@ words are independent, so no two share any: every layer of every block has a key
 which is set (gradients keep theirs clear by seeds below 2^63), and the rank of a data-parallel job is part
 of the step.
 
+With products="e4m3" the linear layers' products run in 8-bit floating point: inputs and gradients with an
+exponent per 128 columns of a row, weights with one per 128 x 128 elements, put into it in every forward pass
+and kept (1 byte an element) for the input's gradient.  Weight gradients stay bf16 products on the checkpoints.
+Gradients are those of the products as if nothing were rounded (straight through).
+
 Gradients are of the first order only: a second derivative (create_graph=True, then a backward pass
 through the result) raises a RuntimeError.
 """
@@ -27,6 +32,7 @@ from torch import nn
 from torch.autograd.function import once_differentiable
 
 from . import _activations as ops
+from . import _fp8 as fp8
 
 
 def _rows(x):
@@ -36,20 +42,34 @@ def _rows(x):
     return m if m.stride(1) == 1 and (m.shape[0] < 2 or m.stride(0) >= m.shape[1]) else m.contiguous()
 
 
+def _product(y, weight, bias, e4m3):
+    """y weight^T + bias, and what its backward pass reads of the weight in 8 bits."""
+    if not e4m3:
+        return torch.nn.functional.linear(y, weight.to(y.dtype), bias.to(y.dtype)), None
+    w8 = fp8.gq_fp8_quantize(_rows(weight), tiles=True)
+    return fp8.gq_fp8_linear(y, w8, bias=bias.float()), w8.data
+
+
+def _input_gradient(d, weight, data):
+    if data is None:
+        return d @ weight.to(d.dtype)
+    return fp8.gq_fp8_linear_dgrad(d, fp8.Fp8.of_data(data, *weight.shape, tiles=True))
+
+
 class _NormLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step, record=True):
+    def forward(ctx, x, norm_weight, norm_bias, weight, bias, eps, seed, step, record=True, e4m3=False):
         y, _, rstd, act = ops.gq_layernorm_forward(_rows(x), norm_weight, norm_bias, eps, seed=seed, step=step,
                                                    checkpoint=record and any(ctx.needs_input_grad[:4]))
-        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data)
+        out, w8 = _product(y, weight, bias, e4m3)
+        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data, w8)
         ctx.shape = x.shape
-        out = torch.nn.functional.linear(y, weight.to(y.dtype), bias.to(y.dtype))
         return out.view(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        norm_weight, norm_bias, weight, rstd, data = ctx.saved_tensors
+        norm_weight, norm_bias, weight, rstd, data, w8 = ctx.saved_tensors
         d = _rows(dout)
         need = ctx.needs_input_grad
         dx = dnw = dnb = dweight = dbias = None
@@ -60,30 +80,30 @@ class _NormLinear(torch.autograd.Function):
         elif need[4]:
             dbias = d.sum(0, dtype=torch.float32)
         if any(need[:3]):
-            dx, dnw, dnb = ops.gq_layernorm_backward(d @ weight.to(d.dtype), norm_weight, rstd, act=act)
+            dx, dnw, dnb = ops.gq_layernorm_backward(_input_gradient(d, weight, w8), norm_weight, rstd, act=act)
             dx = dx.view(ctx.shape)
-        return dx, dnw, dnb, dweight, dbias, None, None, None, None
+        return dx, dnw, dnb, dweight, dbias, None, None, None, None, None
 
 
 class _GeluLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, u, weight, bias, approximate, seed, step, record=True):
+    def forward(ctx, u, weight, bias, approximate, seed, step, record=True, e4m3=False):
         h, act = ops.gq_gelu_forward(_rows(u), approximate=approximate, seed=seed, step=step,
                                      checkpoint=record and any(ctx.needs_input_grad[:2]))
-        ctx.save_for_backward(weight, act and act.data)
+        out, w8 = _product(h, weight, bias, e4m3)
+        ctx.save_for_backward(weight, act and act.data, w8)
         ctx.approximate, ctx.shape = approximate, u.shape
-        out = torch.nn.functional.linear(h, weight.to(h.dtype), bias.to(h.dtype))
         return out.view(*u.shape[:-1], weight.shape[0])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        weight, data = ctx.saved_tensors
+        weight, data, w8 = ctx.saved_tensors
         d = _rows(dout)
         need = ctx.needs_input_grad
         du = dweight = None
         if need[0] or need[1]:
-            got = ops.gq_gelu_backward(d @ weight.to(d.dtype), ops.Act8.of_data(data, weight.shape[1]),
+            got = ops.gq_gelu_backward(_input_gradient(d, weight, w8), ops.Act8.of_data(data, weight.shape[1]),
                                        approximate=ctx.approximate, need_output=need[1])
             du, h = got if need[1] else (got, None)
             du = du.view(ctx.shape)
@@ -91,7 +111,7 @@ class _GeluLinear(torch.autograd.Function):
                 # bf16 operands, fp32 sums: the gradient of an fp32 parameter is not rounded to bf16
                 dweight = d.t() @ h if d.dtype == torch.float32 else torch.mm(d.t(), h, out_dtype=torch.float32)
         dbias = d.sum(0, dtype=torch.float32) if need[2] else None
-        return du, dweight, dbias, None, None, None, None
+        return du, dweight, dbias, None, None, None, None, None
 
 
 _numbers = itertools.count()  # of the blocks of this process
@@ -105,11 +125,15 @@ class MlpBlock8(nn.Module):
     Data-parallel ranks need words of their own too: `rank` (below 2^16) tells them apart,
     torch.distributed's where it is None and a process group is there, else 0.  Every block has its own
     words; `seed` names them instead, for words that a later run can draw again, and then blocks of one
-    model need different seeds.  A captured CUDA graph replays the words of its capture."""
+    model need different seeds.  A captured CUDA graph replays the words of its capture.
+
+    `products`: "bf16" for the library's products in the activations' type, "e4m3" for 8-bit floating point."""
 
     def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
-                 seed: int | None = None, device=None, rank: int | None = None):
+                 seed: int | None = None, device=None, rank: int | None = None, products: str = "bf16"):
         super().__init__()
+        if products not in ("bf16", "e4m3"):
+            raise ValueError("products must be 'bf16' or 'e4m3'")
         self.norm_weight = nn.Parameter(torch.ones(width, device=device))
         self.norm_bias = nn.Parameter(torch.zeros(width, device=device))
         self.w1 = nn.Parameter(torch.randn(hidden, width, device=device) * width ** -0.5)
@@ -117,10 +141,12 @@ class MlpBlock8(nn.Module):
         self.w2 = nn.Parameter(torch.randn(width, hidden, device=device) * hidden ** -0.5)
         self.b2 = nn.Parameter(torch.zeros(width, device=device))
         self.approximate, self.eps, self.seed, self.rank, self.step = approximate, eps, seed, rank, 0
+        self.products = products
         self._number = next(_numbers)
 
     def __setstate__(self, state):  # a copy, or one read back from a file
         super().__setstate__(state)
+        self.__dict__.setdefault("products", "bf16")  # of a file from before it
         self._number = next(_numbers)
 
     def words(self, layer: int):
@@ -141,6 +167,7 @@ class MlpBlock8(nn.Module):
 
     def forward(self, x):
         record = torch.is_grad_enabled()  # not seen within a Function's forward pass
+        e4m3 = self.products == "e4m3"
         u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps, *self.words(0),
-                              record)
-        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, *self.words(1), record)
+                              record, e4m3)
+        return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, *self.words(1), record, e4m3)
