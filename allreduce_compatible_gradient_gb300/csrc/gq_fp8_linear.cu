@@ -299,6 +299,9 @@ __global__ void __launch_bounds__(192, 1)
                 }
             };
             const int first = min(k1 - k0, S);
+            // W may be the work of the launch before too, but not where that one puts x into 8 bits: it began
+            // when all before it had ended
+            if constexpr (FUSED) gq::pdl_wait();
             for (int n = 0; n < first; ++n) load_a(k0 + n, n);
             if constexpr (!FUSED) gq::pdl_wait();
             for (int n = 0; n < first; ++n) load_b(k0 + n, n);
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(192, 1)
                 for (int j = 0; j < B; ++j)
                     if (n + j < k1 - k0) next[j].fetch(a, k0 + n + j, depth, thread, wide);
             };
+            gq::pdl_wait();
             fetch(0);
             for (int n0 = 0; n0 < k1 - k0 && ok; n0 += B) {
 #pragma unroll
@@ -692,7 +696,8 @@ bool out_map(CUtensorMap* map, const LArgs& a) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// early: the launch before this one on the stream wrote the tokens' operand, and let this one start.
+// early: this launch may begin while the one before it on the stream ends (and waits for that before it reads
+// what may be its work).
 template <typename C, bool A_OUTER, typename T>
 gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, int64_t depth, int parts,
                        bool early, cudaStream_t st) {
@@ -815,7 +820,7 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
         }
     }
     if (c.bn == Large::BN) return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
-#define GQA_SMALL(BN, T) launch_small<Small<BN>, A_OUTER, T>(a_map, b_map, a, depth, c.parts, x && !c.fused, st)
+#define GQA_SMALL(BN, T) launch_small<Small<BN>, A_OUTER, T>(a_map, b_map, a, depth, c.parts, x != nullptr, st)
     if (c.fused) return dtype == GQ_F32 ? GQA_SMALL(16, float) : GQA_SMALL(16, bf16);
     switch (c.bn) {
         case 16: return GQA_SMALL(16, void);
