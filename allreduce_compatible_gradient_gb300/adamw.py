@@ -19,7 +19,7 @@ class AdamW(torch.optim.Optimizer):
     states: "8bit" or "f32".  max_norm: gradients are clipped to this norm over all of them, and a step whose
     gradients hold a NaN or an infinity changes nothing (it still counts).  capturable: the number of the step
     is kept on the device, so that step() can be captured into a graph and replayed (the states have to be
-    there: make one step, or call make_states(), before).  Parameters are float32 or bfloat16; those without a
+    there: make a step, or call make_states(), before).  Parameters are float32 or bfloat16; those without a
     gradient are passed over."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="8bit",
@@ -41,15 +41,36 @@ class AdamW(torch.optim.Optimizer):
         """The key of the random words: between those of MlpBlock8's seeds and of its unnamed blocks."""
         return (1 << 64) - (1 << 33) + self.seed
 
+    def __getstate__(self):
+        own = ("max_norm", "random", "seed", "capturable")
+        return {**super().__getstate__(), **{k: self.__dict__[k] for k in own}}
+
     def make_states(self) -> None:
-        """States of zeros for the parameters that have none."""
+        """States of zeros for the parameters that have none, and with `capturable` the steps' numbers on the
+        device."""
         for group in self.param_groups:
             for p in group["params"]:
                 self._state(p, group)
+            if self.capturable and group["params"]:
+                self._number(group, group["params"][0].device)
+
+    def _number(self, group, device):
+        """The group's count of steps as a tensor on the device."""
+        if not torch.is_tensor(group["step"]) or group["step"].device != device:
+            self._not_captured()
+            group["step"] = torch.full((1,), int(group["step"]), dtype=torch.int64, device=device)
+        return group["step"]
+
+    @staticmethod
+    def _not_captured():
+        # a graph would make them again, as zeros, at every replay
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("states are made before a step is captured: make a step, or call make_states()")
 
     def _state(self, p, group):
         s = self.state[p]
         if not s:
+            self._not_captured()
             if group["states"] == "8bit":
                 s.update(zip(("m", "v", "exps"), ops.gq_adamw_state(p.numel(), p.device)))
             else:
@@ -90,9 +111,7 @@ class AdamW(torch.optim.Optimizer):
         first = 0
         for group, lists in calls:
             if self.capturable:
-                if not torch.is_tensor(group["step"]):
-                    group["step"] = torch.full((1,), group["step"], dtype=torch.int64, device=grads[0].device)
-                group["step"].add_(1)
+                self._number(group, grads[0].device).add_(1)
             else:
                 group["step"] = int(group["step"]) + 1
             for params, gradients, states in lists.values():

@@ -682,7 +682,8 @@ bool exp_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t steps) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y in bf16, in boxes of 128 outputs x 16 tokens; false where its rows do not suit the TMA.
+// y in bf16, in boxes of 128 outputs x 16 tokens; false where its rows do not suit the TMA, which writes whole
+// 16-byte pieces also where a row ends inside one.
 bool out_map(CUtensorMap* map, const LArgs& a) {
     EncodeFn encode = encode_fn();
     if (!encode) return false;
@@ -737,7 +738,7 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
     CUtensorMap a_exps, b_exps;
     if (!exp_map(&a_exps, a.a_exps, a.m, a.steps) || !exp_map(&b_exps, a.b_exps, a.rows, a.steps)) return GQ_ERR_CUDA;
     CUtensorMap y_map = a_map;  // not used where it cannot be made
-    a.wide = !a.out_f32 && mult(a.y, 16) && (a.ldy % 8 == 0 || a.rows == 1) && out_map(&y_map, a);
+    a.wide = !a.out_f32 && mult(a.y, 16) && a.m % 8 == 0 && (a.ldy % 8 == 0 || a.rows == 1) && out_map(&y_map, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(Large::kThreads);

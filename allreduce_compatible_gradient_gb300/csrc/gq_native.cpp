@@ -581,6 +581,9 @@ struct Tokens {
     }
     at::Tensor result(int64_t width, PyObject* type) {
         c10::SmallVector<int64_t, 8> size(shape);
+        int64_t n = size.empty() ? -1 : 1;
+        for (size_t i = 0; i + 1 < size.size(); ++i) n *= size[i];
+        if (n != rows) refuse(PyExc_ValueError, "the matrix's shape is not that of its %lld rows", static_cast<long long>(rows));
         size.back() = width;
         return empty(size, scalar_of(output_code(type, "out_dtype")), index);
     }

@@ -217,6 +217,38 @@ def test_linear_not_finite(gq):
     assert y[:, 140].isnan().all() and y.isnan().sum() == 200
 
 
+@pytest.mark.parametrize("rows", [1, 16, 40])
+def test_linear_not_finite_few_tokens(gq, rows):
+    x, w = torch.randn((rows, 700), device="cuda"), torch.randn((300, 700), device="cuda")
+    x[rows - 1, 600] = -float("inf")
+    y = gq.gq_fp8_linear(x, gq.gq_fp8_quantize(w, tiles=True))
+    assert y[rows - 1].isnan().all() and y[:rows - 1].isfinite().all()
+
+
+@pytest.mark.parametrize("rows,outs", [(1, 200), (9, 131), (50, 200), (300, 131), (4200, 1030), (4200, 1032)])
+@pytest.mark.parametrize("ldy,shift", [(0, 0), (8, 0), (2, 0), (1, 0), (8, 8), (8, 1)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_outputs_of_any_place(gq, rows, outs, ldy, shift, out):
+    """The C entry: rows of y further apart than their length and at any element; what lies between them stays."""
+    cols, ld = 260, outs + ldy
+    x, w = matrix(rows, cols, "bf16", 1), gq.gq_fp8_quantize(matrix(outs, cols, "f32", 2), tiles=True)
+    want = gq.gq_fp8_linear(x, w, out_dtype=TYPES[out])
+    f = gq.gq_fp8_quantize(x)
+    for given in (None, x):
+        room = torch.full((rows * ld + shift + 8,), 7.0, dtype=TYPES[out], device="cuda")
+        y = room[shift:]
+        codes, exps = f.codes.clone(), f.exps.clone()
+        status = gq.lib().gq_fp8_linear(None if given is None else given.data_ptr(), gq.BF16, cols, codes.data_ptr(),
+                                        exps.data_ptr(), rows, cols, w.codes.data_ptr(), w.exps.data_ptr(), outs, None,
+                                        y.data_ptr(), gq.BF16 if out == "bf16" else gq.F32, ld,
+                                        torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        torch.cuda.synchronize()
+        body = y[:rows * ld].view(rows, ld)
+        assert torch.equal(body[:, :outs], want)
+        assert (body[:, outs:] == 7).all() and (room[:shift] == 7).all() and (room[shift + rows * ld:] == 7).all()
+
+
 def test_linear_extreme_scales(gq):
     """Blocks whose scales differ by 2^60 within a sum, and sums near the ends of fp32's range."""
     g = torch.Generator(device="cuda").manual_seed(5)

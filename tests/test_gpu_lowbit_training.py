@@ -196,6 +196,25 @@ def test_products_captured_in_graphs(gq, rows, cols, outs):
         assert torch.equal(y, want) and torch.equal(d, gq.gq_fp8_linear_dgrad(want, w))
 
 
+def test_overlapping_calls_keep_their_inputs(gq):
+    """Weights written by the launch right before a product, in a loop that nothing waits in: each product sees
+    the weight of its turn, in every form."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for rows, cols, outs in ((1, 1024, 512), (200, 1024, 512), (4200, 512, 1100)):
+        x = torch.randn((rows, cols), generator=g, device="cuda").bfloat16()
+        fx = gq.gq_fp8_quantize(x)
+        ws = [torch.randn((outs, cols), generator=g, device="cuda") for _ in range(8)]
+        want = []
+        for w in ws:
+            f = gq.gq_fp8_quantize(w, tiles=True)
+            torch.cuda.synchronize()
+            want.append(gq.gq_fp8_linear(x, f))
+            torch.cuda.synchronize()
+        for source in (x, fx):
+            got = [gq.gq_fp8_linear(source, gq.gq_fp8_quantize(w, tiles=True)) for w in ws]
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ---- the optimizer ---------------------------------------------------------------------------
 
 def parameters(dtype=torch.float32, seed=1):
@@ -329,6 +348,37 @@ def test_optimizer_captured_in_a_graph(adamw):
     assert all(torch.equal(x, y) for p, q in zip(ours, theirs) for x, y in zip(a.state[p].values(), b.state[q].values()))
 
 
+def test_optimizer_captured_from_made_states(adamw):
+    """Captured before any step: refused without states, and with them the replays count from 1."""
+    ours, theirs = with_gradients(parameters(), 1), with_gradients(parameters(), 1)
+    a, b = (adamw.AdamW(p, capturable=True) for p in (ours, theirs))
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before a step is captured"):
+        with torch.cuda.graph(graph):
+            a.step()
+    a.make_states()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+    for _ in range(3):
+        graph.replay()
+        b.step()
+    assert a.param_groups[0]["step"].item() == 3
+    assert all(torch.equal(p, q) for p, q in zip(ours, theirs))
+
+
+def test_optimizer_copies(adamw):
+    """A deep copy goes on like the original, clipping and words included."""
+    ours = with_gradients(parameters(torch.bfloat16), 1)
+    a = adamw.AdamW(ours, max_norm=0.1, seed=3)
+    a.step()
+    b = copy.deepcopy(a)
+    twins = with_gradients([p for g in b.param_groups for p in g["params"]], 1)
+    a.step()
+    b.step()
+    assert all(p is not q and torch.equal(p, q) for p, q in zip(ours, twins))
+
+
 def test_optimizer_refuses(adamw):
     for bad in (dict(states="4bit"), dict(betas=(1.0, 0.9)), dict(betas=(0.9, -0.1)), dict(eps=-1.0),
                 dict(max_norm=-1.0), dict(seed=-1), dict(seed=1 << 31)):
@@ -391,6 +441,10 @@ def test_refusals(gq):
         gq.gq_fp8_linear(x, f, bias=torch.zeros(71, device="cuda"))
     with pytest.raises(ValueError):
         gq.gq_fp8_linear(x.cpu(), f)
+    for shape in ((1, 300), (40, 2, 300), ()):               # not that of its rows
+        q = gq.gq_fp8_quantize(x)
+        with pytest.raises(ValueError):
+            gq.gq_fp8_linear(gq.Fp8(q.codes, q.exps, 300, shape=shape), f)
     with pytest.raises(ValueError):
         gq.gq_fp8_quantize(x.t()[::2])
     with pytest.raises(ValueError):
