@@ -177,6 +177,33 @@ def test_linear_dgrad(gq, rows, cols, outs, dtype, out):
     assert torch.equal(got, gq.gq_fp8_linear_dgrad(gq.gq_fp8_quantize(dy), f, out_dtype=TYPES[out]))
 
 
+@pytest.mark.parametrize("rows,cols,outs,dtype", [(16300, 2048, 1024, "bf16"), (16384, 4096, 4096, "bf16"),
+                                                  (9800, 2100, 1000, "f32")])
+def test_many_waves_of_tiles(gq, rows, cols, outs, dtype):
+    """Long x: bit for bit the result of the same matrix put into 8 bits before, over and over with nothing waiting in
+    between, and replayed from a graph; some rows against 64 bits."""
+    w = matrix(outs, cols, "f32", 2)
+    f = gq.gq_fp8_quantize(w, tiles=True)
+    xs = [matrix(rows, cols, dtype, k) for k in range(2)]
+    want = [gq.gq_fp8_linear(gq.gq_fp8_quantize(x), f, out_dtype=torch.bfloat16) for x in xs]
+    some = torch.randint(0, rows, (200,), device="cuda")
+    xv, wv = ref.values(*ref.fp8(xs[0][some], 1), 1), ref.values(*ref.fp8(w, 128), 128)
+    near(want[0][some], xv @ wv.t(), xv.abs() @ wv.abs().t(), cols)
+    for _ in range(4):
+        got = [gq.gq_fp8_linear(x, f, out_dtype=torch.bfloat16) for x in xs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    x = xs[0].clone()
+    with torch.cuda.graph(graph):
+        y = gq.gq_fp8_linear(x, f, out_dtype=torch.bfloat16)
+        z = y.sum()
+    for k in (0, 1, 0):
+        x.copy_(xs[k])
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, want[k]) and torch.equal(z, want[k].sum())
+
+
 def test_linear_weights_by_rows(gq):
     """A weight with an exponent per row's block, and no bias."""
     forward(gq, 77, 1500, 333, "bf16", "bf16", tiles=False, bias=False)
