@@ -30,7 +30,8 @@ _FORMS = {"none": GELU_ERF, "tanh": GELU_TANH}
 _FUNCTIONS = ("gq_act_quantize", "gq_act_dequantize", "gq_layernorm_forward",
               "gq_layernorm_workspace_bytes", "gq_layernorm_backward", "gq_gelu_forward",
               "gq_gelu_backward", "gq_linear_wgrad_workspace_bytes", "gq_linear_wgrad_plan",
-              "gq_linear_wgrad", "gq_fp8_quantize", "gq_fp8_dequantize", "gq_fp8_linear", "gq_fp8_linear_dgrad",
+              "gq_linear_wgrad", "gq_fp8_quantize", "gq_fp8_dequantize",
+              "gq_fp8_linear_workspace_bytes", "gq_fp8_linear", "gq_fp8_linear_dgrad",
               "gq_tensors_norm_workspace_bytes", "gq_tensors_norm", "gq_adamw_step", "gq_adamw_values")
 
 

@@ -97,6 +97,7 @@ def lib() -> ctypes.CDLL:
         "gq_fp8_exp_bytes": (sz, [i64, i64]),
         "gq_fp8_quantize": (ci, [vp, ci, i64, i64, i64, ci, vp, vp, vp, vp]),
         "gq_fp8_dequantize": (ci, [vp, vp, i64, i64, vp, ci, i64, vp]),
+        "gq_fp8_linear_workspace_bytes": (sz, [i64, i64, i64]),
         "gq_fp8_linear": (ci, [vp, ci, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp, ci, i64, vp]),
         "gq_fp8_linear_dgrad": (ci, [vp, ci, i64, vp, vp, i64, i64, vp, vp, i64, vp, ci, i64, vp]),
         "gq_tensors_norm_workspace_bytes": (sz, [i64]),

@@ -21,6 +21,10 @@ def gq_fp8_exp_bytes(rows: int, cols: int) -> int:
     return lib().gq_fp8_exp_bytes(rows, cols)
 
 
+def gq_fp8_linear_workspace_bytes(rows: int, depth: int, outs: int) -> int:
+    return lib().gq_fp8_linear_workspace_bytes(rows, depth, outs)
+
+
 def _up(v, m):
     return (v + m - 1) // m * m
 

@@ -31,46 +31,6 @@ template <typename T, bool ALIGNED> struct Granules {
     }
 };
 
-// Largest magnitude of 8 elements as fp32 bits, above infinity's where one is a NaN.
-__device__ __forceinline__ uint32_t top8(const Raw8<float>& r) {
-    float a = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2)
-        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(__uint_as_float(r.w[i])), "f"(__uint_as_float(r.w[i + 1])));
-    return __float_as_uint(a);
-}
-// (bf16 magnitudes order like their bits)
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t top8(const Raw8<bf16>& r) {
-    uint32_t m = r.w[0] & 0x7FFF7FFFu;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) m = max16x2(m, r.w[i] & 0x7FFF7FFFu);
-    return max(m & 0xFFFF0000u, m << 16);
-}
-// The same over the 16 lanes of a block, for four rows.
-__device__ __forceinline__ void tops(const Raw8<float> (&r)[4], uint32_t (&top)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        top[j] = top8(r[j]);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top[j] = max(top[j], __shfl_xor_sync(kFull, top[j], o));
-    }
-}
-__device__ __forceinline__ void tops(const Raw8<bf16> (&r)[4], uint32_t (&top)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {  // two rows in a register
-        uint32_t m = top8(r[j]) >> 16 | top8(r[j + 1]);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max16x2(m, __shfl_xor_sync(kFull, m, o));
-        top[j] = m << 16;
-        top[j + 1] = m & 0xFFFF0000u;
-    }
-}
-
 // One exponent per row and 128 columns.  A warp's task is rows r, r + 32, r + 64, r + 96 of 128 and 256 columns:
 // 16 lanes hold a block, and the 8 exponents lie in 16 bytes.  The next task's loads are on their way while
 // one is computed.
@@ -104,7 +64,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < 4; ++j) now[j] = g[j].wanted(r + 32 * j < rows ? left : 0);
         if (t < tasks - min(stride, tasks)) fetch(t + stride);
-        tops(now, top);
+        tops<4>(now, top);
         uint32_t e4 = 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

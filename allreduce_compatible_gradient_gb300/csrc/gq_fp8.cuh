@@ -29,6 +29,47 @@ __device__ __forceinline__ uint32_t fp8_exp_byte(uint32_t top) {
     const int e = static_cast<int>((top + 0x1FFFFFu) >> 23) - 8;
     return top >= 0x7F800000u ? 255u : static_cast<uint32_t>(max(e, 1));
 }
+// Largest magnitude of 8 elements as fp32 bits, above infinity's where one is a NaN.
+__device__ __forceinline__ uint32_t top8(const Raw8<float>& r) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;"
+            : "=f"(a)
+            : "f"(a), "f"(__uint_as_float(r.w[i])), "f"(__uint_as_float(r.w[i + 1])));
+    return __float_as_uint(a);
+}
+// (bf16 magnitudes order like their bits)
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t top8(const Raw8<bf16>& r) {
+    uint32_t m = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max16x2(m, r.w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFF0000u, m << 16);
+}
+// The same over the 16 lanes of a block, for R rows.
+template <int R> __device__ __forceinline__ void tops(const Raw8<float> (&r)[R], uint32_t (&top)[R]) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        top[j] = top8(r[j]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top[j] = max(top[j], __shfl_xor_sync(kFull, top[j], o));
+    }
+}
+template <int R> __device__ __forceinline__ void tops(const Raw8<bf16> (&r)[R], uint32_t (&top)[R]) {
+#pragma unroll
+    for (int j = 0; j < R; j += 2) {  // two rows in a register
+        uint32_t m = top8(r[j]) >> 16 | top8(r[j + 1]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max16x2(m, __shfl_xor_sync(kFull, m, o));
+        top[j] = m << 16;
+        top[j + 1] = m & 0xFFFF0000u;
+    }
+}
 // Codes of 8 elements times inv, the reciprocal of their block's step (products of at most 448, so nothing
 // saturates): rounded to nearest even.
 __device__ __forceinline__ uint2 fp8_codes8(const F2 (&h)[4], float inv) {

@@ -15,8 +15,8 @@
 // a part of the sum; the parts are added through distributed shared memory in the blocks' order.
 //   warp 0   TMA loads of both operands (128 of k per step) and bulk copies of exponents (512 of k each)
 //   warp 1   one thread copies exponents to TMEM and issues tcgen05.mma, accumulators in TMEM
-//   2 to 5   the sums from TMEM to memory; where x is given and 16 tokens or fewer, they also put x into 8 bits
-//            on its way to shared memory, so that a call of few tokens is one launch
+//   2 to 5   the sums from TMEM to memory; in calls of few steps a block, and of up to 16 tokens, they also put x
+//            into 8 bits on its way to shared memory, so that the call is one launch
 // What bounds it: latency.  One token through 4,096 x 4,096 weights takes 6.6 us in a graph with the weights in the
 // L2 (their 16.8 MB would take 2.5 from memory), 384 tokens through 768 x 768 6.3 us: a launch's ends, an
 // operand's way, a chain of four steps or so, a join.
@@ -149,21 +149,20 @@ template <int BN_> struct Small {
     static_assert(128 * BN * 4 <= kStages * kBytes, "a block's sums fit in its operands' place");
 };
 
-// The tokens' side of a step, 128 columns of BN tokens, from x: 16 lanes hold a row's block, 8 rows at a time
-// by four warps.  Behind the last row and column stand zeros.
+// The tokens' side of a step, 128 columns of BN tokens from token t0 on, from x: 16 lanes hold a row's block, 8
+// rows at a time by four warps.  Behind the last row and column stand zeros.
 template <typename T, int BN> struct Squeeze {
     static constexpr int R = BN / 8;
     Raw8<T> w[R];
-    __device__ __forceinline__ void fetch(const LArgs& a, int k, int depth, int thread, bool wide) {
+    __device__ __forceinline__ void fetch(const LArgs& a, int t0, int k, int depth, int thread, bool wide) {
         const int c = k * kStep + (thread & 15) * 8;
-        const int left = depth - c;
+        const int left = depth - c, rows = a.rows - t0;
+        const T* p = static_cast<const T*>(a.x) + (t0 + (thread >> 4)) * a.ldx + c;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = (thread >> 4) + 8 * i;
-            const T* p = static_cast<const T*>(a.x) + row * a.ldx + c;
+        for (int i = 0; i < R; ++i, p += 8 * a.ldx) {
 #pragma unroll
             for (int j = 0; j < static_cast<int>(sizeof(T)) * 2; ++j) w[i].w[j] = 0u;
-            if (row >= a.rows || left <= 0) continue;
+            if ((thread >> 4) + 8 * i >= rows || left <= 0) continue;
             if (wide && left >= 8) {
 #pragma unroll
                 for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) {
@@ -182,21 +181,14 @@ template <typename T, int BN> struct Squeeze {
     }
     // codes in the layout of a swizzled box, exponents at the step's byte of each row's word
     __device__ __forceinline__ void store(uint32_t codes, uint32_t exps, int k, int thread) {
+        uint32_t top[R];
+        tops<R>(w, top);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int row = (thread >> 4) + 8 * i, unit = (thread & 15) >> 1;
+            const uint32_t e = fp8_exp_byte(top[i]);
             F2 v[4];
             pairs(w[i], v);
-            uint32_t m = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float x, y;
-                split(v[j], x, y);
-                m = max(m, max(__float_as_uint(x) & 0x7FFFFFFFu, __float_as_uint(y) & 0x7FFFFFFFu));
-            }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-            const uint32_t e = fp8_exp_byte(m);
             uint2 q = fp8_codes8(v, inv_step(e));
             if (e == 255u) q = make_uint2(0u, 0u);
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(codes + row * 128 + ((unit ^ (row & 7)) << 4) +
@@ -244,7 +236,7 @@ __device__ __forceinline__ void join(const LArgs& a, uint32_t from, int c, int e
     }
 }
 
-// T: the type of x in a fused call (one tile of tokens), else void.
+// T: the type of x in a fused call, else void.
 template <typename C, bool A_OUTER, typename T>
 __global__ void __launch_bounds__(192, 1)
     small_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
@@ -359,20 +351,22 @@ __global__ void __launch_bounds__(192, 1)
         if constexpr (FUSED) {
             const int thread = threadIdx.x - 64;
             const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(a.ldx * sizeof(T))) & 15u) == 0;
-            // steps' loads on their way while as many are put into 8 bits
-            constexpr int B = sizeof(T) == 4 ? 2 : 4;
+            // steps' loads on their way while as many are put into 8 bits, as far as registers go
+            constexpr int kRegs = BN / 8 * 2 * sizeof(T), B = BN == 16 ? 32 / kRegs : 1;
+            constexpr bool AHEAD = kRegs <= 64;
             Squeeze<T, BN> now[B], next[B];
             auto fetch = [&](int n) {
 #pragma unroll
                 for (int j = 0; j < B; ++j)
-                    if (n + j < k1 - k0) next[j].fetch(a, k0 + n + j, depth, thread, wide);
+                    if (n + j < k1 - k0) next[j].fetch(a, t0, k0 + n + j, depth, thread, wide);
             };
             gq::pdl_wait();
-            fetch(0);
+            if (AHEAD) fetch(0);
             for (int n0 = 0; n0 < k1 - k0 && ok; n0 += B) {
+                if (!AHEAD) fetch(n0);
 #pragma unroll
                 for (int j = 0; j < B; ++j) now[j] = next[j];
-                fetch(n0 + B);
+                if (AHEAD) fetch(n0 + B);
 #pragma unroll
                 for (int j = 0; j < B; ++j) {
                     const int n = n0 + j, s = n % S;
@@ -770,7 +764,8 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
 // join); 6 and 1 in the large form, whose pairs stay.  Both sides, depth x outputs for so many tokens: 768 x
 // 768 for 384 in four parts 6.3 and in one 7.1, 4,096 x 4,096 for 256 in two parts 11.9, in one 15.6, large
 // 15.6; for 1,024 tokens of 1,024 x 4,096 large 8.9 and small 15.4, 256 x 256 for 4,096 large 6.9 and small
-// 5.7.  Fused or not, 4,096 x 4,096: 1 token 6.6 and 7.8, 16 tokens 7.8 and 8.4, 32 tokens 8.9 and 8.1.
+// 5.7.  Fused or not, 4,096 x 4,096: 1 token 6.6 and 7.8, 16 tokens 7.8 and 8.4, 32 tokens 8.9 and 8.1; a step of
+// 64 or 128 tokens takes four warps 0.5 or 1 us, and what is saved is a launch of 3.
 struct Choice {
     int bn, parts;
     bool fused;
@@ -786,7 +781,8 @@ Choice choose(int64_t rows, int64_t outs, int64_t steps, int64_t sms, bool from_
         const double t = 5.0 + waves * (2.0 + 0.28 * ((steps + parts - 1) / parts)) + (parts > 1 ? 0.7 : 0.0);
         if (t <= best) {
             best = t;
-            c = {bn, parts, from_x && bn == 16};
+            const double squeeze = (bn == 16 ? 0.0 : bn / 128.0) * ((steps + parts - 1) / parts) * waves;
+            c = {bn, parts, from_x && squeeze <= 3.0};
         }
     }
     return c;
@@ -803,7 +799,7 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     if (!matrix_ok(y, out_dtype, rows, outs, ldy) || !mult(bias, 4)) return GQ_ERR_INVALID;
     if (x && (!in_type(dtype) || !matrix_ok(x, dtype, rows, depth, ldx))) return GQ_ERR_INVALID;
     if (rows == 0) return GQ_OK;
-    if (!saved_ok(xcodes, xexps) || !saved_ok(wcodes, wexps)) return GQ_ERR_INVALID;
+    if (!saved_ok(wcodes, wexps)) return GQ_ERR_INVALID;
     const int64_t sms = gqh::sm_count(), tiles_m = (outs + 127) / 128, steps = (depth + kStep - 1) / kStep;
     if (tiles_m * ((rows + 15) / 16) * 8 >= int64_t(1) << 31) return GQ_ERR_INVALID;
     LArgs a;
@@ -815,6 +811,7 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     a.x = x; a.ldx = ldx;
     const Choice c = choose(rows, outs, steps, sms, x != nullptr);
     if (c.bn < 128 && rows > c.bn) return GQ_ERR_INVALID;  // see Small
+    if (!c.fused && !saved_ok(xcodes, xexps)) return GQ_ERR_INVALID;
     CUtensorMap a_map, b_map;
     if (!byte_map(&a_map, wcodes, A_OUTER ? outs : depth, A_OUTER ? depth : outs,
                   fp8_pitch(A_OUTER ? outs : depth), 128))
@@ -830,18 +827,23 @@ gq_status product(const void* x, int dtype, int64_t ldx, uint8_t* xcodes, uint8_
     }
     if (c.bn == Large::BN) return launch_large<A_OUTER>(a_map, b_map, a, x != nullptr, st);
 #define GQA_SMALL(BN, T) launch_small<Small<BN>, A_OUTER, T>(a_map, b_map, a, depth, c.parts, x != nullptr, st)
-    if (c.fused) return dtype == GQ_F32 ? GQA_SMALL(16, float) : GQA_SMALL(16, bf16);
-    switch (c.bn) {
-        case 16: return GQA_SMALL(16, void);
-        case 64: return GQA_SMALL(64, void);
-        default: return GQA_SMALL(128, void);
-    }
+#define GQA_TOKENS(T) \
+    (c.bn == 16 ? GQA_SMALL(16, T) : c.bn == 64 ? GQA_SMALL(64, T) : GQA_SMALL(128, T))
+    if (!c.fused) return GQA_TOKENS(void);
+    return dtype == GQ_F32 ? GQA_TOKENS(float) : GQA_TOKENS(bf16);
+#undef GQA_TOKENS
 #undef GQA_SMALL
 }
 
 }  // namespace
 
 extern "C" {
+
+size_t gq_fp8_linear_workspace_bytes(int64_t rows, int64_t depth, int64_t outs) {
+    if (!size_ok(rows, depth) || rows < 1 || outs < 1) return 0;
+    if (choose(rows, outs, (depth + kStep - 1) / kStep, gqh::sm_count(), true).fused) return 0;
+    return static_cast<size_t>(rows * fp8_pitch(depth) + exp_bytes(rows, depth));
+}
 
 gq_status gq_fp8_linear(const void *x, int dtype, int64_t ldx, uint8_t *xcodes, uint8_t *xexps, int64_t rows,
                         int64_t cols, const uint8_t *wcodes, const uint8_t *wexps, int64_t outs,

@@ -37,6 +37,7 @@ struct Api {
     decltype(&gq_linear_wgrad) linear_wgrad;
     decltype(&gq_fp8_quantize) fp8_quantize;
     decltype(&gq_fp8_dequantize) fp8_dequantize;
+    decltype(&gq_fp8_linear_workspace_bytes) fp8_linear_workspace_bytes;
     decltype(&gq_fp8_linear) fp8_linear;
     decltype(&gq_fp8_linear_dgrad) fp8_linear_dgrad;
     decltype(&gq_tensors_norm_workspace_bytes) tensors_norm_workspace_bytes;
@@ -572,12 +573,12 @@ struct Tokens {
             shape = sizes_of(a[7]);
         }
     }
-    void make() {
-        if (codes || !p) return;
-        const int64_t pitch = (cols + 15) / 16 * 16;
-        own = empty({rows * pitch + fp8_exp_bytes(rows, cols)}, at::kByte, index);
+    void make(int64_t outs) {
+        const size_t need = codes || !p ? 0 : api.fp8_linear_workspace_bytes(rows, cols, outs);
+        if (need == 0) return;
+        own = empty({static_cast<int64_t>(need)}, at::kByte, index);
         codes = static_cast<uint8_t*>(own.data_ptr());
-        exps = codes + rows * pitch;
+        exps = codes + rows * ((cols + 15) / 16 * 16);
     }
     at::Tensor result(int64_t width, PyObject* type) {
         c10::SmallVector<int64_t, 8> size(shape);
@@ -601,7 +602,7 @@ PyObject* fp8_linear(PyObject* const* a, Py_ssize_t n) {
     int f32 = GQ_F32;
     const float* bias = static_cast<const float*>(vector(a[14], w.rows, x.index, &f32, "bias"));
     const Place at(x.index);
-    x.make();
+    x.make(w.rows);
     const at::Tensor y = x.result(w.rows, a[15]);
     check(api.fp8_linear(x.p, x.code, x.ld, x.codes, x.exps, x.rows, x.cols, w.codes, w.exps, w.rows, bias,
                          y.data_ptr(), type_code(y.scalar_type()), w.rows, at.stream),
@@ -619,7 +620,7 @@ PyObject* fp8_linear_dgrad(PyObject* const* a, Py_ssize_t n) {
                static_cast<long long>(w.cols), w.index);
     if (!w.exps_t) refuse(PyExc_ValueError, "the weight has no exponents of its transposed matrix (tiles=True)");
     const Place at(dy.index);
-    dy.make();
+    dy.make(w.cols);
     const at::Tensor dx = dy.result(w.cols, a[14]);
     check(api.fp8_linear_dgrad(dy.p, dy.code, dy.ld, dy.codes, dy.exps, dy.rows, dy.cols, w.codes, w.exps_t,
                                w.cols, dx.data_ptr(), type_code(dx.scalar_type()), w.cols, at.stream),

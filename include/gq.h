@@ -591,11 +591,15 @@ gq_status gq_fp8_dequantize(const uint8_t *codes, const uint8_t *exps, int64_t r
  * y[t][o] = sum over i of X[t][i] W[o][i] + bias[o]  (rows x outs, out_dtype GQ_F32 or GQ_BF16, rows
  * ldy apart; bias nullable, fp32) with X (rows x cols, block_rows = 1) and W (outs x cols, either
  * block_rows) in 8-bit floating point.  Where x is not null, X is made from it (as by gq_fp8_quantize), and
- * xcodes and xexps are room for it, whose contents afterwards are not to be relied on.  The tensor cores
+ * xcodes and xexps are room for it, whose contents afterwards are not to be relied on (null where
+ * gq_fp8_linear_workspace_bytes is 0: such a call needs none).  The tensor cores
  * multiply codes and apply the scales; sums are fp32 and in a fixed order, rounded once.  A bounded wait that
  * gives up (about a second; a broken kernel only) leaves NaN in the tiles concerned.  rows, outs and
  * cols < 2^30.
  */
+/* Bytes of both, the codes' gq_fp8_code_pitch(depth) rows first, for a call with x (or dy) of rows x depth and
+ * outs outputs on the current device. */
+size_t gq_fp8_linear_workspace_bytes(int64_t rows, int64_t depth, int64_t outs);
 gq_status gq_fp8_linear(const void *x, int dtype, int64_t ldx, uint8_t *xcodes, uint8_t *xexps,
                         int64_t rows, int64_t cols, const uint8_t *wcodes, const uint8_t *wexps,
                         int64_t outs, const float *bias, void *y, int out_dtype, int64_t ldy,

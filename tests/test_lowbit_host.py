@@ -25,6 +25,9 @@ def test_sizes(L):
     assert [gq.gq_fp8_code_pitch(c) for c in (0, 1, 16, 17, 4096)] == [0, 16, 16, 32, 4096]
     assert gq.gq_fp8_exp_bytes(1, 1) == 512 and gq.gq_fp8_exp_bytes(129, 513) == 4 * 512
     assert gq.gq_fp8_exp_bytes(0, 5) == 0 and gq.gq_fp8_exp_bytes(-1, 5) == 0 and gq.gq_fp8_exp_bytes(5, 0) == 0
+    # rows of codes, and exponents behind them; none where x is put into 8 bits on its way
+    assert gq.gq_fp8_linear_workspace_bytes(5000, 700, 4096) == 5000 * 704 + 40 * 2 * 512
+    assert gq.gq_fp8_linear_workspace_bytes(1, 4096, 4096) == 0 == gq.gq_fp8_linear_workspace_bytes(0, 64, 64)
     one = gq.gq_tensors_norm_workspace_bytes(1)
     assert one > 0 and gq.gq_tensors_norm_workspace_bytes(257) == 2 * one
     assert gq.gq_tensors_norm_workspace_bytes(-1) == 0
