@@ -15,7 +15,7 @@
 // a part of the sum; the parts are added through distributed shared memory in the blocks' order.
 //   warp 0   TMA loads of both operands (128 of k per step) and bulk copies of exponents (512 of k each)
 //   warp 1   one thread copies exponents to TMEM and issues tcgen05.mma, accumulators in TMEM
-//   2 to 5   the sums from TMEM to memory; in calls of few steps a block, and of up to 16 tokens, they also put x
+//   2 on     (4 or 8) the sums from TMEM to memory; in calls of few steps a block, and of up to 16 tokens, they also put x
 //            into 8 bits on its way to shared memory, so that the call is one launch
 // What bounds it: latency.  One token through 4,096 x 4,096 weights takes 6.6 us in a graph with the weights in the
 // L2 (their 16.8 MB would take 2.5 from memory), 384 tokens through 768 x 768 6.3 us: a launch's ends, an
@@ -149,20 +149,24 @@ template <int BN_> struct Small {
     static_assert(128 * BN * 4 <= kStages * kBytes, "a block's sums fit in its operands' place");
 };
 
-// The tokens' side of a step, 128 columns of BN tokens from token t0 on, from x: 16 lanes hold a row's block, 8
-// rows at a time by four warps.  Behind the last row and column stand zeros.
-template <typename T, int BN> struct Squeeze {
-    static constexpr int R = BN / 8;
+// Warps that take the sums, and x in a fused call (8 where a step has much of it: 384 x 768 x 768 in two steps a
+// block 9.2 us with four).
+template <int BN, typename T> constexpr int kWarpsOf = !std::is_void<T>::value && BN > 16 ? 8 : 4;
+
+// The tokens' side of a step, 128 columns of BN tokens from token t0 on, from x: 16 lanes hold a row's block, 2 W
+// rows at a time by W warps.  Behind the last row and column stand zeros.
+template <typename T, int BN, int W> struct Squeeze {
+    static constexpr int S = 2 * W, R = BN / S;
     Raw8<T> w[R];
     __device__ __forceinline__ void fetch(const LArgs& a, int t0, int k, int depth, int thread, bool wide) {
         const int c = k * kStep + (thread & 15) * 8;
         const int left = depth - c, rows = a.rows - t0;
         const T* p = static_cast<const T*>(a.x) + (t0 + (thread >> 4)) * a.ldx + c;
 #pragma unroll
-        for (int i = 0; i < R; ++i, p += 8 * a.ldx) {
+        for (int i = 0; i < R; ++i, p += S * a.ldx) {
 #pragma unroll
             for (int j = 0; j < static_cast<int>(sizeof(T)) * 2; ++j) w[i].w[j] = 0u;
-            if ((thread >> 4) + 8 * i >= rows || left <= 0) continue;
+            if ((thread >> 4) + S * i >= rows || left <= 0) continue;
             if (wide && left >= 8) {
 #pragma unroll
                 for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) {
@@ -185,7 +189,7 @@ template <typename T, int BN> struct Squeeze {
         tops<R>(w, top);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int row = (thread >> 4) + 8 * i, unit = (thread & 15) >> 1;
+            const int row = (thread >> 4) + S * i, unit = (thread & 15) >> 1;
             const uint32_t e = fp8_exp_byte(top[i]);
             F2 v[4];
             pairs(w[i], v);
@@ -202,19 +206,19 @@ template <typename T, int BN> struct Squeeze {
     }
 };
 
-// Adds the parts of tokens c, c + 4 PARTS, ... below `end` (four warps, each block a PARTS-th) and stores them;
+// Adds the parts of tokens c, c + W PARTS, ... below `end` (W warps, each block a PARTS-th) and stores them;
 // eight loads are on their way at a time (one by one, 128 tokens took 4 us).
-template <int PARTS>
+template <int PARTS, int W>
 __device__ __forceinline__ void join(const LArgs& a, uint32_t from, int c, int end, int t0, int out, float4 b) {
     constexpr int B = 8 / PARTS;
-    for (; c < end; c += B * 4 * PARTS) {
+    for (; c < end; c += B * W * PARTS) {
         float4 p[B][PARTS];
 #pragma unroll
         for (int j = 0; j < B; ++j)
 #pragma unroll
             for (int r = 0; r < PARTS; ++r) {
                 // (tokens behind the last are read as the last, and left out)
-                const uint32_t at = from + min(c + j * 4 * PARTS, end - 1) * 512;
+                const uint32_t at = from + min(c + j * W * PARTS, end - 1) * 512;
                 if constexpr (PARTS == 1)
                     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                  : "=f"(p[j][r].x), "=f"(p[j][r].y), "=f"(p[j][r].z), "=f"(p[j][r].w)
@@ -231,18 +235,18 @@ __device__ __forceinline__ void join(const LArgs& a, uint32_t from, int c, int e
                 v.x += p[j][r].x; v.y += p[j][r].y; v.z += p[j][r].z; v.w += p[j][r].w;
             }
             v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
-            if (c + j * 4 * PARTS < end) put4(a, t0 + c + j * 4 * PARTS, out, v);
+            if (c + j * W * PARTS < end) put4(a, t0 + c + j * W * PARTS, out, v);
         }
     }
 }
 
 // T: the type of x in a fused call, else void.
 template <typename C, bool A_OUTER, typename T>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(64 + 32 * kWarpsOf<C::BN, T>, 1)
     small_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                  const LArgs a, const int depth) {
     constexpr bool FUSED = !std::is_void<T>::value;
-    constexpr int BN = C::BN, S = C::kStages;
+    constexpr int BN = C::BN, S = C::kStages, W = kWarpsOf<BN, T>;
     extern __shared__ uint8_t raw[];
     __shared__ alignas(8) uint64_t full[S], empty[S], acc_full, drain;
     __shared__ uint32_t tmem_slot;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(192, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            gq::mbar_init(gq::smem_u32(&full[s]), FUSED ? 5u : 1u);
+            gq::mbar_init(gq::smem_u32(&full[s]), FUSED ? 1u + W : 1u);
             gq::mbar_init(gq::smem_u32(&empty[s]), 1u);
         }
         gq::mbar_init(gq::smem_u32(&acc_full), 1u);
@@ -351,22 +355,20 @@ __global__ void __launch_bounds__(192, 1)
         if constexpr (FUSED) {
             const int thread = threadIdx.x - 64;
             const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(a.ldx * sizeof(T))) & 15u) == 0;
-            // steps' loads on their way while as many are put into 8 bits, as far as registers go
-            constexpr int kRegs = BN / 8 * 2 * sizeof(T), B = BN == 16 ? 32 / kRegs : 1;
-            constexpr bool AHEAD = kRegs <= 64;
-            Squeeze<T, BN> now[B], next[B];
+            // steps' loads on their way while as many are put into 8 bits
+            constexpr int B = BN == 16 ? 8 / static_cast<int>(sizeof(T)) : 1;
+            Squeeze<T, BN, W> now[B], next[B];
             auto fetch = [&](int n) {
 #pragma unroll
                 for (int j = 0; j < B; ++j)
                     if (n + j < k1 - k0) next[j].fetch(a, t0, k0 + n + j, depth, thread, wide);
             };
             gq::pdl_wait();
-            if (AHEAD) fetch(0);
+            fetch(0);
             for (int n0 = 0; n0 < k1 - k0 && ok; n0 += B) {
-                if (!AHEAD) fetch(n0);
 #pragma unroll
                 for (int j = 0; j < B; ++j) now[j] = next[j];
-                if (AHEAD) fetch(n0 + B);
+                fetch(n0 + B);
 #pragma unroll
                 for (int j = 0; j < B; ++j) {
                     const int n = n0 + j, s = n % S;
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(192, 1)
         float* sums = reinterpret_cast<float*>(raw + (base - gq::smem_u32(raw)));
         if constexpr (!FUSED) gq::pdl_wait();  // y may be what the launch before still reads
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
+        for (int c = (warp - 2) / 4 * 16; c < BN; c += W * 4) {
             if (t0 + c >= a.rows) break;
             uint32_t v[16];
             tmem_load(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
@@ -415,10 +417,10 @@ __global__ void __launch_bounds__(192, 1)
         const uint32_t from = base + m * 4;
         const int c = static_cast<int>(rank) + (warp - 2) * static_cast<int>(parts), end = min(BN, a.rows - t0);
         switch (parts) {
-            case 1: join<1>(a, from, c, end, t0, m0 + m, b); break;
-            case 2: join<2>(a, from, c, end, t0, m0 + m, b); break;
-            case 4: join<4>(a, from, c, end, t0, m0 + m, b); break;
-            default: join<8>(a, from, c, end, t0, m0 + m, b); break;
+            case 1: join<1, W>(a, from, c, end, t0, m0 + m, b); break;
+            case 2: join<2, W>(a, from, c, end, t0, m0 + m, b); break;
+            case 4: join<4, W>(a, from, c, end, t0, m0 + m, b); break;
+            default: join<8, W>(a, from, c, end, t0, m0 + m, b); break;
         }
     }
     __syncwarp();
@@ -705,11 +707,12 @@ template <typename C, bool A_OUTER, typename T>
 gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const LArgs& a, int64_t depth, int parts,
                        bool early, cudaStream_t st) {
     auto k = small_kernel<C, A_OUTER, T>;
-    gqh::blocks_per_sm(k, C::kSmem, 192);  // raises the shared-memory limit once
+    constexpr int kThreadsS = 64 + 32 * kWarpsOf<C::BN, T>;
+    gqh::blocks_per_sm(k, C::kSmem, kThreadsS);  // raises the shared-memory limit once
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * ((a.rows + C::BN - 1) / C::BN);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * parts));
-    cfg.blockDim = dim3(192);
+    cfg.blockDim = dim3(kThreadsS);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -765,7 +768,9 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
 // 768 for 384 in four parts 6.3 and in one 7.1, 4,096 x 4,096 for 256 in two parts 11.9, in one 15.6, large
 // 15.6; for 1,024 tokens of 1,024 x 4,096 large 8.9 and small 15.4, 256 x 256 for 4,096 large 6.9 and small
 // 5.7.  Fused or not, 4,096 x 4,096: 1 token 6.6 and 7.8, 16 tokens 7.8 and 8.4, 32 tokens 8.9 and 8.1; a step of
-// 64 or 128 tokens takes four warps 0.5 or 1 us, and what is saved is a launch of 3.
+// 64 or 128 tokens takes the warps 0.3 or 0.6 us more, and what is saved is a launch: 64 tokens x 1,024 x 1,024 5.3 for
+// 5.8 in one step a block, 384 x 768 x 768 7.8 for 7.4 in two, 200 x 2,048 x 1,024 9.9 for 7.9 in four, and 2.7 us
+// of the host in each.
 struct Choice {
     int bn, parts;
     bool fused;
@@ -781,8 +786,8 @@ Choice choose(int64_t rows, int64_t outs, int64_t steps, int64_t sms, bool from_
         const double t = 5.0 + waves * (2.0 + 0.28 * ((steps + parts - 1) / parts)) + (parts > 1 ? 0.7 : 0.0);
         if (t <= best) {
             best = t;
-            const double squeeze = (bn == 16 ? 0.0 : bn / 128.0) * ((steps + parts - 1) / parts) * waves;
-            c = {bn, parts, from_x && squeeze <= 3.0};
+            const double squeeze = (bn == 16 ? 0.0 : 0.6 * bn / 128.0) * ((steps + parts - 1) / parts) * waves;
+            c = {bn, parts, from_x && squeeze <= 1.5};
         }
     }
     return c;
