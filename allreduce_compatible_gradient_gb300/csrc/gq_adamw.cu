@@ -20,8 +20,8 @@
 // What bounds it: memory, one pass over everything; 28 bytes an element with fp32 states, 14.1 with 8-bit ones
 // and bf16 gradients, where the issue slots are 70 % busy beside it (67 instructions an element; 94 took 650 us
 // for 201 M elements).  201 M elements: 796 us with fp32 states and gradients (7.1 TB/s), 455 with 8-bit ones
-// (6.2); the norm of their gradients 133 in fp32, 72 in bf16.  The tensors' addresses are an argument of the kernel (constant memory), so that nothing
-// is copied to the device and a captured step keeps its own.
+// (6.2); the norm of their gradients 133 in fp32, 72 in bf16.  The tensors' addresses are an argument of the
+// kernel (constant memory), so that nothing is copied to the device and a captured step keeps its own.
 #include "gq_fp8.cuh"
 
 #include <cmath>

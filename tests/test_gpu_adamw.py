@@ -233,6 +233,8 @@ def test_norm(gq):
             assert got.shape == (1,) and got.dtype == torch.float32
             assert abs(got.double() - want) <= 80 * U * want
             assert torch.equal(got, gq.gq_tensors_norm(t))
+            ws = torch.full((gq.gq_tensors_norm_workspace_bytes(len(t)),), 255, dtype=torch.uint8, device="cuda")
+            assert torch.equal(got, gq.gq_tensors_norm(t, ws=ws))
     assert gq.gq_tensors_norm([torch.empty(0, device="cuda")]).item() == 0.0
     x = torch.ones(100, device="cuda")
     for bad in (float("nan"), float("inf"), -float("inf"), 1e30):
