@@ -431,6 +431,7 @@ constexpr int kNormBlocks = 1216;  // partial sums per launch: at most
 template <typename G, int N>
 __global__ void __launch_bounds__(256)
     squares_kernel(const __grid_constant__ Table<N> t, uint32_t chunks, int rounds, double* partial) {
+    gq::pdl_wait();
     gq::pdl_launch_dependents();  // the sum of the sums waits before it reads
     float sum = 0.0f, carry = 0.0f;
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -537,21 +538,6 @@ int rounds_for(int64_t count, const int64_t* numel, int most) {
     return each < 1 ? 1 : each < most ? static_cast<int>(each) : most;
 }
 
-// A launch that may begin while the one before it on the stream ends.
-template <typename... Params, typename... Args>
-void launch_early(void (*k)(Params...), uint32_t blocks, cudaStream_t st, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreadsA);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 // Widest access to 8 elements at a time.
 uint8_t wide(const void* p) { return mult(p, 32) ? 32 : mult(p, 16) ? 16 : 0; }
 
@@ -567,10 +553,10 @@ gq_status adamw(int64_t count, void* const* params, const void* const* grads, vo
     a.rounds = rounds_for(count, numel, EIGHT ? 16 : 4);
     if (count <= kFew)
         return in_runs<kFew>(count, numel, a.rounds * kRound, fill, [&](const Table<kFew>& t, uint32_t blocks) {
-            launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kFew>, blocks, st, t, a);
+            launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kFew>, blocks, kThreadsA, st, t, a);
         });
     return in_runs<kMany>(count, numel, a.rounds * kRound, fill, [&](const Table<kMany>& t, uint32_t blocks) {
-        launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kMany>, blocks, st, t, a);
+        launch_early(adamw_kernel<P, G, EIGHT, RANDOM, kMany>, blocks, kThreadsA, st, t, a);
     });
 }
 
@@ -602,14 +588,14 @@ gq_status gq_tensors_norm(int64_t count, const void *const *tensors, const int64
     auto run = [&](const auto& t, uint32_t chunks) {
         constexpr int N = sizeof(t.s) / sizeof(Slot);
         const uint32_t blocks = chunks < most ? chunks : most;
-        if (dtype == GQ_F32) squares_kernel<float, N><<<blocks, 256, 0, st>>>(t, chunks, rounds, partial + parts);
-        else squares_kernel<bf16, N><<<blocks, 256, 0, st>>>(t, chunks, rounds, partial + parts);
+        if (dtype == GQ_F32) launch_early(squares_kernel<float, N>, blocks, 256, st, t, chunks, rounds, partial + parts);
+        else launch_early(squares_kernel<bf16, N>, blocks, 256, st, t, chunks, rounds, partial + parts);
         parts += blocks;
     };
     const gq_status r = count <= kFew ? in_runs<kFew>(count, numel, rounds * kRound, fill, run)
                                       : in_runs<kMany>(count, numel, rounds * kRound, fill, run);
     if (r != GQ_OK) return r;
-    launch_early(root_kernel, 1, st, static_cast<const double*>(partial), parts, norm_dev);
+    launch_early(root_kernel, 1, kThreadsA, st, static_cast<const double*>(partial), parts, norm_dev);
     return gqh::launch_status();
 }
 

@@ -21,8 +21,8 @@ template <typename T, bool ALIGNED> struct Granules {
         const int bytes = left > 0 ? static_cast<int>(m) + min(left, 8) * static_cast<int>(sizeof(T)) : 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const uint4 g = 16 * i < bytes ? __ldg(reinterpret_cast<const uint4*>(q - m) + i)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+            // an ordinary load: a read-only one may pass the wait for the launch before, whose work x may be
+            const uint4 g = 16 * i < bytes ? reinterpret_cast<const uint4*>(q - m)[i] : make_uint4(0u, 0u, 0u, 0u);
             w[4 * i] = g.x; w[4 * i + 1] = g.y; w[4 * i + 2] = g.z; w[4 * i + 3] = g.w;
         }
     }
@@ -36,9 +36,10 @@ template <typename T, bool ALIGNED> struct Granules {
 // one is computed.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(256)
-    rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
-                Div by, uint32_t tasks, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
-    gq::pdl_launch_dependents();  // a product that follows waits before it reads
+    rows_kernel(const T* x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
+                Div by, uint32_t tasks, uint8_t* codes, uint8_t* exps) {
+    gq::pdl_wait();
+    gq::pdl_launch_dependents();  // a product that follows waits before it reads the codes; all before has ended
     const int lane = threadIdx.x & 31;
     const uint32_t stride = gridDim.x * 8;
     Granules<T, ALIGNED> g[4];
@@ -89,8 +90,9 @@ __global__ void __launch_bounds__(256)
 // Block = one tile, 32 elements per thread.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(512)
-    tiles_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
-                 uint8_t* __restrict__ codes, uint8_t* __restrict__ exps, uint8_t* __restrict__ exps_t) {
+    tiles_kernel(const T* x, int64_t ld, int64_t rows, int64_t cols, int64_t pitch, uint32_t across,
+                 uint8_t* codes, uint8_t* exps, uint8_t* exps_t) {
+    gq::pdl_wait();
     gq::pdl_launch_dependents();
     __shared__ uint32_t most[16];
     const int64_t tr = blockIdx.x / across, tc = blockIdx.x % across;
@@ -191,17 +193,15 @@ gq_status quantize(const T* x, int64_t rows, int64_t cols, int64_t ld, bool tile
     if (tiles) {
         const int64_t across = (cols + 127) / 128, n = (rows + 127) / 128 * across;
         auto k = aligned ? tiles_kernel<T, true> : tiles_kernel<T, false>;
-        k<<<static_cast<unsigned>(n), 512, 0, st>>>(x, ld, rows, cols, pitch, static_cast<uint32_t>(across), codes,
-                                                    exps, exps_t);
+        launch_early(k, n, 512, st, x, ld, rows, cols, pitch, static_cast<uint32_t>(across), codes, exps, exps_t);
         return gqh::launch_status();
     }
     const int64_t across = (cols + 255) / 256, tasks = (rows + 127) / 128 * 32 * across;
     if (tasks >= int64_t(1) << 31) return GQ_ERR_INVALID;
     auto k = aligned ? rows_kernel<T, true> : rows_kernel<T, false>;
     const int64_t most = resident_blocks(k, 256, 0), need = (tasks + 7) / 8;
-    k<<<static_cast<unsigned>(need < most ? need : most), 256, 0, st>>>(
-        x, ld, rows, cols, pitch, static_cast<uint32_t>(across), div_by(across), static_cast<uint32_t>(tasks), codes,
-        exps);
+    launch_early(k, need < most ? need : most, 256, st, x, ld, rows, cols, pitch, static_cast<uint32_t>(across),
+                 div_by(across), static_cast<uint32_t>(tasks), codes, exps);
     return gqh::launch_status();
 }
 
@@ -212,17 +212,8 @@ gq_status dequantize(const uint8_t* codes, const uint8_t* exps, int64_t rows, in
     const int a = row_align(out, dtype, rows, ld);
     auto k = a == 32 ? values_kernel<O, 32> : a == 16 ? values_kernel<O, 16> : values_kernel<O, 0>;
     const int64_t most = resident_blocks(k, 256, 0), need = (pieces + 255) / 256;
-    cudaLaunchConfig_t cfg = {};  // it may begin while what wrote the codes ends
-    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, k, codes, exps, cols, fp8_pitch(cols), exp_words(cols), pieces,
-                       static_cast<uint32_t>(across), div_by(across), out, ld);
+    launch_early(k, need < most ? need : most, 256, st, codes, exps, cols, fp8_pitch(cols), exp_words(cols), pieces,
+                 static_cast<uint32_t>(across), div_by(across), out, ld);
     return gqh::launch_status();
 }
 

@@ -92,4 +92,20 @@ __device__ __forceinline__ F2 fp8_values2(uint32_t w) {
     return f2(v.x, v.y);
 }
 
+// A launch that may begin while the one before it on the stream ends.  Its kernel waits for that one
+// (gq::pdl_wait) before it reads or writes memory, and lets a launch behind it begin only after.
+template <typename... Params, typename... Args>
+void launch_early(void (*k)(Params...), int64_t blocks, int threads, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 }  // namespace gqa

@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(64 + 32 * kWarpsOf<C::BN, T>, 1)
                 }
             };
             const int first = min(k1 - k0, S);
-            // W may be the work of the launch before too, but not where that one puts x into 8 bits: it began
-            // when all before it had ended
+            // W may be the work of the launch before too, but not where that one puts x into 8 bits: it let this
+            // one begin when all before it had ended
             if constexpr (FUSED) gq::pdl_wait();
             for (int n = 0; n < first; ++n) load_a(k0 + n, n);
             if constexpr (!FUSED) gq::pdl_wait();
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(64 + 32 * kWarpsOf<C::BN, T>, 1)
             float* w = reinterpret_cast<float*>(&b);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (m0 + m + i < a.m) w[i] = __ldg(a.bias + m0 + m + i);
+                if (m0 + m + i < a.m) w[i] = a.bias[m0 + m + i];
         }
         const uint32_t from = base + m * 4;
         const int c = static_cast<int>(rank) + (warp - 2) * static_cast<int>(parts), end = min(BN, a.rows - t0);
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(Large::kThreads, 1)
         for (int tile = first; tile < tiles; tile += pairs, ++done) {
             const int m0 = (tile % across * 2 + static_cast<int>(rank)) * 128, m = m0 + quad * 32 + lane;
             const int t0 = tile / across * C::BN + group * 128;
-            const float b = a.bias && m < a.m ? __ldg(a.bias + m) : 0.0f;
+            const float b = a.bias && m < a.m ? a.bias[m] : 0.0f;
             if (ok) ok = mbar_rest(gq::smem_u32(&acc_full), done & 1);
             ok = __all_sync(kFull, ok);
             fence_after();
