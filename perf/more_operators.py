@@ -367,6 +367,13 @@ def _plain(s):
 
 # ---- the library ---------------------------------------------------------------------------
 
+def _cut(x, s):
+    """The tensors' elements of a buffer, without what lies behind them in their room."""
+    sizes = [v for n, room in zip(s["numel"], s["room"]) for v in ((n, room - n) if n < room else (n,))]
+    gap = [k for n, room in zip(s["numel"], s["room"]) for k in ((False, True) if n < room else (False,))]
+    return [t for t, k in zip(x.split(sizes), gap) if not k]
+
+
 def _library(s):
     import allreduce_compatible_gradient_gb300 as gq
 
@@ -384,8 +391,7 @@ def _library(s):
         # the states' values, in one buffer like the parameters
         new = torch.empty if s["numel"] == s["room"] else torch.zeros
         m, r = (new(sum(s["room"]), dtype=torch.bfloat16, device="cuda") for _ in range(2))
-        gq.gq_adamw_values(states, out=([t[:n] for t, n in zip(m.split(s["room"]), s["numel"])],
-                                        [t[:n] for t, n in zip(r.split(s["room"]), s["numel"])]))
+        gq.gq_adamw_values(states, out=(_cut(m, s), _cut(r, s)))
         return [norm, s["p"], m, r]
     if op == "fp8":
         return gq.gq_fp8_dequantize(gq.gq_fp8_quantize(s["x"], tiles=case["tiles"]),
