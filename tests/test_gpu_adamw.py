@@ -225,7 +225,8 @@ def test_small_roots_are_kept(gq):
 
 def test_norm(gq):
     g = torch.Generator(device="cuda").manual_seed(2)
-    for sizes in ([1], [0, 3], [7, 16384, 16385, 1], [3] * 600, [1 << 22, 5]):
+    for sizes in ([1], [0, 3], [7, 16384, 16385, 1], [3] * 600, [1 << 22, 5], [1 << 20], [(1 << 20) + 1], [1 << 21],
+                  [4097] * 200, [4096] * 256, [100, 0, 900000, 4095]):
         for dtype in TYPES.values():
             t = [flat(n, g, 3.0, dtype, shift=i % 3) for i, n in enumerate(sizes)]
             want = torch.stack([x.double().square().sum() for x in t]).sum().sqrt()
