@@ -27,5 +27,5 @@ from ._fp8 import (  # noqa: F401
     Fp8, gq_fp8_code_pitch, gq_fp8_dequantize, gq_fp8_exp_bytes, gq_fp8_linear, gq_fp8_linear_dgrad,
     gq_fp8_linear_workspace_bytes, gq_fp8_quantize)
 from ._optimizer import (  # noqa: F401
-    Adam8, gq_adamw_state, gq_adamw_step, gq_adamw_values, gq_tensors_norm,
+    Adam8, gq_adamw_state, gq_adamw_step, gq_adamw_step_places, gq_adamw_values, gq_tensors_norm,
     gq_tensors_norm_workspace_bytes)

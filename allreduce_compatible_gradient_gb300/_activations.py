@@ -32,7 +32,7 @@ _FUNCTIONS = ("gq_act_quantize", "gq_act_dequantize", "gq_layernorm_forward",
               "gq_gelu_backward", "gq_linear_wgrad_workspace_bytes", "gq_linear_wgrad_plan",
               "gq_linear_wgrad", "gq_fp8_quantize", "gq_fp8_dequantize",
               "gq_fp8_linear_workspace_bytes", "gq_fp8_linear", "gq_fp8_linear_dgrad",
-              "gq_tensors_norm_workspace_bytes", "gq_tensors_norm", "gq_adamw_step", "gq_adamw_values")
+              "gq_tensors_norm_workspace_bytes", "gq_tensors_norm", "gq_adamw_step_places", "gq_adamw_values")
 
 
 def load_native():

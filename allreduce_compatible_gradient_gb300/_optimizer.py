@@ -60,7 +60,21 @@ def gq_adamw_step(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=
                    max_norm, seed, first)
     beta1, beta2 = betas
     return _acts._native.adamw_step(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm,
-                                    max_norm, seed, first)
+                                    max_norm, seed, first, None)
+
+
+def gq_adamw_step_places(params, grads, states, step, places, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                         weight_decay=1e-2, norm=None, max_norm=None, seed=None, first=0, stream=None) -> None:
+    """gq_adamw_step for lists that leave out some of a program's tensors.  places: a number for each tensor, in
+    ascending order, counted from `first`: its random words are those of its number, whichever others are there."""
+    if stream is not None:
+        return _on(stream, gq_adamw_step_places, params, grads, states, step, places, lr, betas, eps,
+                   weight_decay, norm, max_norm, seed, first)
+    if places is None:
+        raise TypeError("places must be a list or a tuple")
+    beta1, beta2 = betas
+    return _acts._native.adamw_step(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm,
+                                    max_norm, seed, first, places)
 
 
 def gq_adamw_values(states, out=None, out_dtype=torch.bfloat16, stream=None):

@@ -2,7 +2,8 @@
 
 8-bit states take 2.1 bytes a parameter instead of 8.  They, and bf16 parameters, are rounded at random
 without bias by default (random=False: to nearest).  The words are those of (key, step, tensor, element) with a
-key of the optimizer's own that no gradient and no MlpBlock8 draws from.  They do not depend on the rank:
+key of the optimizer's own that no gradient and no MlpBlock8 draws from.  A tensor's number is given to it in its
+first step and kept with its state, whichever others have a gradient later.  Words do not depend on the rank:
 data-parallel replicas that make the same steps stay equal bit for bit.  `seed` (below 2^31) tells the
 optimizers of one program apart, where it has several.
 """
@@ -37,6 +38,7 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, step=0,
                                       states=states))
         self.max_norm, self.random, self.seed, self.capturable = max_norm, random, seed, capturable
+        self._forget()
 
     @property
     def key(self) -> int:
@@ -46,6 +48,27 @@ class AdamW(torch.optim.Optimizer):
     def __getstate__(self):
         own = ("max_norm", "random", "seed", "capturable")
         return {**super().__getstate__(), **{k: self.__dict__[k] for k in own}}
+
+    def __setstate__(self, state):  # also of a load_state_dict()
+        super().__setstate__(state)
+        self._forget()
+
+    def _forget(self):
+        """Of the states, what is read from them once."""
+        self._places, self._next = {}, None
+
+    def _place(self, p):
+        """The parameter's number."""
+        place = self._places.get(p)
+        if place is None:
+            s = self.state[p]
+            if "place" not in s:
+                if self._next is None:
+                    self._next = 1 + max((int(v["place"]) for v in self.state.values() if "place" in v), default=-1)
+                s["place"] = torch.tensor(self._next, device="cpu")
+                self._next += 1
+            place = self._places[p] = int(s["place"])
+        return place
 
     def make_states(self) -> None:
         """States of zeros for the parameters that have none, and with `capturable` the steps' numbers on the
@@ -73,6 +96,7 @@ class AdamW(torch.optim.Optimizer):
         s = self.state[p]
         if not s:
             self._not_captured()
+            self._places.pop(p, None)
             if group["states"] == "8bit":
                 s.update(zip(("m", "v", "exps"), ops.gq_adamw_state(p.numel(), p.device)))
             else:
@@ -103,24 +127,26 @@ class AdamW(torch.optim.Optimizer):
                 grads.append(g)
                 state = self._state(p, group)
                 # a call's tensors are of one type, and their states of one kind
-                for v, x in zip(lists.setdefault((p.dtype, g.dtype, len(state)), ([], [], [])), (p, g, state)):
-                    v.append(x)
+                lists.setdefault((p.dtype, g.dtype, len(state)), []).append((p, g, state))
+            # (parameters that are new get their numbers call by call, so that those of a call follow one another)
+            lists = [sorted(((self._place(p), p, g, s) for p, g, s in entries), key=lambda entry: entry[0])
+                     for entries in lists.values()]
             if lists:
                 calls.append((group, lists))
         if not calls:
             return loss
         norm = None if self.max_norm is None else self._norm(grads)
-        first = 0
         for group, lists in calls:
             if self.capturable:
                 self._number(group, grads[0].device).add_(1)
             else:
                 group["step"] = int(group["step"]) + 1
-            for params, gradients, states in lists.values():
-                ops.gq_adamw_step(params, gradients, states, group["step"], lr=group["lr"], betas=group["betas"],
-                                  eps=group["eps"], weight_decay=group["weight_decay"], norm=norm,
-                                  max_norm=self.max_norm, seed=self.key if self.random else None, first=first)
-                first += len(params)
+            for entries in lists:
+                places, params, gradients, states = map(list, zip(*entries))
+                ops.gq_adamw_step_places(params, gradients, states, group["step"], places, lr=group["lr"],
+                                         betas=group["betas"], eps=group["eps"],
+                                         weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
+                                         seed=self.key if self.random else None)
         return loss
 
     def load_state_dict(self, state_dict) -> None:
@@ -131,4 +157,6 @@ class AdamW(torch.optim.Optimizer):
         new = [p for group in self.param_groups for p in group["params"]]
         for i, p in zip(old, new):
             if i in state_dict["state"]:
-                self.state[p] = {k: v.detach().to(p.device, copy=True) for k, v in state_dict["state"][i].items()}
+                self.state[p] = {k: v.detach().to("cpu" if k == "place" else p.device, copy=True)
+                                 for k, v in state_dict["state"][i].items()}
+        self._forget()

@@ -543,11 +543,11 @@ uint8_t wide(const void* p) { return mult(p, 32) ? 32 : mult(p, 16) ? 16 : 0; }
 
 template <typename P, typename G, bool EIGHT, bool RANDOM>
 gq_status adamw(int64_t count, void* const* params, const void* const* grads, void* const* m, void* const* v,
-                uint8_t* const* exps, const int64_t* numel, int64_t first, Step a, cudaStream_t st) {
+                uint8_t* const* exps, const int64_t* numel, int64_t first, const int64_t* places, Step a, cudaStream_t st) {
     auto fill = [&](Slot& s, int64_t i) {
         s.p = params[i]; s.g = grads[i]; s.m = m[i]; s.v = v[i];
         s.e = EIGHT ? exps[i] : nullptr;
-        s.row = static_cast<uint32_t>(3 * (first + i));
+        s.row = static_cast<uint32_t>(3 * (first + (places ? places[i] : i)));
         s.wp = wide(s.p); s.wg = wide(s.g); s.wm = wide(s.m); s.wv = wide(s.v);
     };
     a.rounds = rounds_for(count, numel, EIGHT ? 16 : 4);
@@ -604,13 +604,25 @@ gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, con
                         const int64_t *numel, int64_t step, const int64_t *step_dev, double lr, double beta1,
                         double beta2, double eps, double weight_decay, const float *norm_dev, double max_norm,
                         int rounding, uint64_t seed, int64_t first, void *stream) {
+    return gq_adamw_step_places(count, params, param_dtype, grads, grad_dtype, m, v, exps, numel, step, step_dev, lr,
+                                beta1, beta2, eps, weight_decay, norm_dev, max_norm, rounding, seed, first, nullptr,
+                                stream);
+}
+
+gq_status gq_adamw_step_places(int64_t count, void *const *params, int param_dtype, const void *const *grads,
+                               int grad_dtype, void *const *m, void *const *v, uint8_t *const *exps,
+                               const int64_t *numel, int64_t step, const int64_t *step_dev, double lr, double beta1,
+                               double beta2, double eps, double weight_decay, const float *norm_dev, double max_norm,
+                               int rounding, uint64_t seed, int64_t first, const int64_t *places, void *stream) {
     if (!in_type(param_dtype) || !in_type(grad_dtype) || !sizes_ok(count, numel)) return GQ_ERR_INVALID;
     if (count > 0 && (!params || !grads || !m || !v)) return GQ_ERR_INVALID;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(lr) ||
         !std::isfinite(weight_decay) || (!step_dev && step < 1) || !mult(step_dev, 8) || !mult(norm_dev, 4))
         return GQ_ERR_INVALID;
-    if ((rounding != GQ_ACT_NEAREST && rounding != GQ_ACT_RANDOM) || first < 0 || first + count > int64_t(1) << 30)
+    if ((rounding != GQ_ACT_NEAREST && rounding != GQ_ACT_RANDOM) || first < 0 || first > (int64_t(1) << 30) - count)
         return GQ_ERR_INVALID;
+    for (int64_t i = 0; places && i < count; ++i)
+        if (places[i] < (i > 0 ? places[i - 1] + 1 : 0) || places[i] >= (int64_t(1) << 30) - first) return GQ_ERR_INVALID;
     for (int64_t i = 0; i < count; ++i) {
         if (numel[i] == 0) continue;
         if (!params[i] || !grads[i] || !m[i] || !v[i] || (exps && !exps[i])) return GQ_ERR_INVALID;
@@ -637,7 +649,7 @@ gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool random = rounding == GQ_ACT_RANDOM;
 #define GQA_ADAMW(P, G, EIGHT, RANDOM) \
-    adamw<P, G, EIGHT, RANDOM>(count, params, grads, m, v, exps, numel, first, a, st)
+    adamw<P, G, EIGHT, RANDOM>(count, params, grads, m, v, exps, numel, first, places, a, st)
 #define GQA_STATE(P, G)                                                                     \
     (exps ? random ? GQA_ADAMW(P, G, true, true) : GQA_ADAMW(P, G, true, false)              \
           : random && sizeof(P) == 2 ? GQA_ADAMW(P, G, false, (sizeof(P) == 2)) : GQA_ADAMW(P, G, false, false))

@@ -42,7 +42,7 @@ struct Api {
     decltype(&gq_fp8_linear_dgrad) fp8_linear_dgrad;
     decltype(&gq_tensors_norm_workspace_bytes) tensors_norm_workspace_bytes;
     decltype(&gq_tensors_norm) tensors_norm;
-    decltype(&gq_adamw_step) adamw_step;
+    decltype(&gq_adamw_step_places) adamw_step_places;
     decltype(&gq_adamw_values) adamw_values;
 };
 constexpr int kFunctions = sizeof(Api) / sizeof(void*);
@@ -753,9 +753,9 @@ PyObject* tensors_norm(PyObject* const* a, Py_ssize_t n) {
 }
 
 // (params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm or None, max_norm or None, seed or
-// None, first) -> None
+// None, first, places or None) -> None
 PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
-    count(n, 13);
+    count(n, 14);
     const Items params(a[0], "params"), grads(a[1], "grads"), states(a[2], "states");
     if (grads.n != params.n || states.n != params.n)
         refuse(PyExc_ValueError, "%zd parameters, %zd gradients and %zd states", params.n, grads.n, states.n);
@@ -813,11 +813,24 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
     }
     const uint64_t seed = a[11] == Py_None ? 0 : unsigned64(a[11], "seed");
     const int64_t first = signed64(a[12]);
-    if (first < 0 || first + params.n > int64_t(1) << 30) refuse(PyExc_ValueError, "first is out of range");
+    if (first < 0 || first > (int64_t(1) << 30) - params.n) refuse(PyExc_ValueError, "first is out of range");
+    std::vector<int64_t> places;
+    if (a[13] != Py_None) {
+        const Items list(a[13], "places");
+        if (list.n != params.n) refuse(PyExc_ValueError, "%zd parameters and %zd places", params.n, list.n);
+        places.reserve(list.n);
+        for (Py_ssize_t i = 0; i < list.n; ++i) {
+            const int64_t k = signed64(list[i]);
+            if (k < (i > 0 ? places.back() + 1 : 0) || k >= (int64_t(1) << 30) - first)
+                refuse(PyExc_ValueError, "places must ascend from 0, and stay below 2^30 with first");
+            places.push_back(k);
+        }
+    }
     const Place at(index);
-    check(api.adamw_step(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(), eight ? e.data() : nullptr,
+    check(api.adamw_step_places(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(), eight ? e.data() : nullptr,
                          numel.data(), step, counter, lr, beta1, beta2, eps, decay, norm, most,
-                         a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first, at.stream),
+                         a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first,
+                         places.empty() ? nullptr : places.data(), at.stream),
           "gq_adamw_step");
     for (Py_ssize_t i = 0; i < params.n; ++i) {
         changed(THPVariable_Unpack(params[i]));
