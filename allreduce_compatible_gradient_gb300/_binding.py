@@ -105,7 +105,7 @@ def lib() -> ctypes.CDLL:
         "gq_adamw_step": (ci, [i64, vp, ci, vp, ci, vp, vp, vp, vp, i64, vp, f64, f64, f64, f64, f64, vp,
                                f64, ci, u64, i64, vp]),
         "gq_adamw_step_places": (ci, [i64, vp, ci, vp, ci, vp, vp, vp, vp, i64, vp, f64, f64, f64, f64, f64,
-                                      vp, f64, ci, u64, i64, vp, vp]),
+                                      vp, f64, ci, u64, i64, vp, vp, vp]),
         "gq_adamw_values": (ci, [i64, vp, vp, vp, vp, vp, vp, ci, vp]),
     }
     for name, (res, args) in sig.items():

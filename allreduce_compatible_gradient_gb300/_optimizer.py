@@ -60,21 +60,23 @@ def gq_adamw_step(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=
                    max_norm, seed, first)
     beta1, beta2 = betas
     return _acts._native.adamw_step(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm,
-                                    max_norm, seed, first, None)
+                                    max_norm, seed, first, None, None)
 
 
 def gq_adamw_step_places(params, grads, states, step, places, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
-                         weight_decay=1e-2, norm=None, max_norm=None, seed=None, first=0, stream=None) -> None:
+                         weight_decay=1e-2, norm=None, max_norm=None, seed=None, first=0, step_places=None,
+                         stream=None) -> None:
     """gq_adamw_step for lists that leave out some of a program's tensors.  places: a number for each tensor, in
-    ascending order, counted from `first`: its random words are those of its number, whichever others are there."""
+    ascending order, counted from `first`: its random words are those of its number, whichever others are there.
+    step_places: for a `step` on the device that holds several numbers, the place of each tensor's."""
     if stream is not None:
         return _on(stream, gq_adamw_step_places, params, grads, states, step, places, lr, betas, eps,
-                   weight_decay, norm, max_norm, seed, first)
+                   weight_decay, norm, max_norm, seed, first, step_places)
     if places is None:
         raise TypeError("places must be a list or a tuple")
     beta1, beta2 = betas
     return _acts._native.adamw_step(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm,
-                                    max_norm, seed, first, places)
+                                    max_norm, seed, first, places, step_places)
 
 
 def gq_adamw_values(states, out=None, out_dtype=torch.bfloat16, stream=None):

@@ -2,28 +2,40 @@
 
 8-bit states take 2.1 bytes a parameter instead of 8.  They, and bf16 parameters, are rounded at random
 without bias by default (random=False: to nearest).  The words are those of (key, step, tensor, element) with a
-key of the optimizer's own that no gradient and no MlpBlock8 draws from.  A tensor's number is given to it in its
-first step and kept with its state, whichever others have a gradient later.  Words do not depend on the rank:
-data-parallel replicas that make the same steps stay equal bit for bit.  `seed` (below 2^31) tells the
-optimizers of one program apart, where it has several.
+key of the optimizer's own that no gradient and no MlpBlock8 draws from.  The step is the number of the tensor's
+own steps; the tensor's number is given to it in its first one and kept with its state, whichever others have a
+gradient later.  Words do not depend on the rank: data-parallel replicas that make the same steps stay equal bit
+for bit.  `seed` (below 2^31) tells the optimizers of one program apart, where it has several.
 """
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 
 from . import _optimizer as ops
 
 
+class _Counts(NamedTuple):
+    """The numbers of steps that a group and, behind its own, each of its parameters have made: one tensor, on the
+    device for captured steps, with its views, of which the states hold theirs; and the parameters' numbers."""
+
+    counts: torch.Tensor
+    own: torch.Tensor
+    steps: list
+    places: list
+
+
 class AdamW(torch.optim.Optimizer):
-    """Decoupled weight decay (Loshchilov, Hutter, arXiv 1711.05101), as torch.optim.AdamW.
+    """Decoupled weight decay (Loshchilov, Hutter, arXiv 1711.05101), as torch.optim.AdamW: a parameter's bias is
+    corrected by the number of its own steps, those in which it had a gradient.
 
     states: "8bit" or "f32".  max_norm: gradients are clipped to this norm over all of them, and a step whose
-    gradients hold a NaN or an infinity changes nothing (it still counts).  capturable: the number of the step
-    is kept on the device, so that step() can be captured into a graph and replayed (the states have to be
+    gradients hold a NaN or an infinity changes nothing (it still counts).  capturable: the numbers of steps
+    are kept on the device, so that step() can be captured into a graph and replayed (the states have to be
     there: make a step, or call make_states(), before).  A captured step keeps the learning rate and the other
     settings of its capture, and works on the states that were there: capture again after changing a setting or
-    load_state_dict().  Parameters are float32 or bfloat16; those without a
-    gradient are passed over."""
+    load_state_dict().  Parameters are float32 or bfloat16; those without a gradient are passed over."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="8bit",
                  max_norm=None, random=True, seed=0, capturable=False):
@@ -54,37 +66,65 @@ class AdamW(torch.optim.Optimizer):
         self._forget()
 
     def _forget(self):
-        """Of the states, what is read from them once."""
-        self._places, self._next = {}, None
-
-    def _place(self, p):
-        """The parameter's number."""
-        place = self._places.get(p)
-        if place is None:
-            s = self.state[p]
-            if "place" not in s:
-                if self._next is None:
-                    self._next = 1 + max((int(v["place"]) for v in self.state.values() if "place" in v), default=-1)
-                s["place"] = torch.tensor(self._next, device="cpu")
-                self._next += 1
-            place = self._places[p] = int(s["place"])
-        return place
+        """What is kept beside the states is made anew from them."""
+        self._kept, self._next = {}, None
+        for index, group in enumerate(self.param_groups):
+            states = [self.state[p] for p in group["params"] if self.state.get(p)]
+            for s in states:  # of a file from before parameters counted
+                s.setdefault("step", torch.tensor(int(group["step"]), device="cpu"))
+            if states:
+                self._counts(index, group)
 
     def make_states(self) -> None:
         """States of zeros for the parameters that have none, and with `capturable` the steps' numbers on the
         device."""
-        for group in self.param_groups:
+        for index, group in enumerate(self.param_groups):
             for p in group["params"]:
                 self._state(p, group)
-            if self.capturable and group["params"]:
-                self._number(group, group["params"][0].device)
+            if group["params"]:
+                self._counts(index, group)
 
-    def _number(self, group, device):
-        """The group's count of steps as a tensor on the device."""
-        if not torch.is_tensor(group["step"]) or group["step"].device != device:
+    def _counts(self, index, group):
+        """A group's _Counts, as its states have them."""
+        params, kept = group["params"], self._kept.get(index)
+        device = params[0].device if self.capturable else torch.device("cpu")
+        states = [self.state.get(p) for p in params]
+        if (kept is None or kept.counts.device != device or len(kept.steps) != 1 + len(params)
+                or self.capturable and group["step"] is not kept.own
+                or any(s and s.get("step", v) is not v for s, v in zip(states, kept.steps[1:]))):
             self._not_captured()
-            group["step"] = torch.full((1,), int(group["step"]), dtype=torch.int64, device=device)
-        return group["step"]
+            numbers = [int(group["step"]), *(int(s["step"]) if s and "step" in s else 0 for s in states)]
+            counts = torch.tensor(numbers, dtype=torch.int64, device=device)
+            kept = self._kept[index] = _Counts(counts, counts[:1], list(counts), [None] * len(numbers))
+            if self.capturable:
+                group["step"] = kept.own
+            for s, v in zip(states, kept.steps[1:]):
+                if s and "step" in s:
+                    s["step"] = v
+        for k, s in enumerate(states, 1):
+            if s and "step" not in s:  # a new state, perhaps in the place of a dropped one
+                kept.steps[k].zero_()
+                kept.places[k] = None
+                s["step"] = kept.steps[k]
+        return kept
+
+    def _place(self, s):
+        """The number of the parameter of a state."""
+        if "place" not in s:
+            if self._next is None:
+                self._next = 1 + max((int(v["place"]) for v in self.state.values() if "place" in v), default=-1)
+            s["place"] = torch.tensor(self._next, device="cpu")
+            self._next += 1
+        return int(s["place"])
+
+    @staticmethod
+    def _add(counts, at, by):
+        """counts[at] += by (at ascends), in as many launches as there are runs."""
+        begin = 0
+        for i in range(1, len(at) + 1):
+            if i == len(at) or at[i] != at[i - 1] + 1:
+                (counts if i - begin == len(counts) else counts[at[begin]:at[i - 1] + 1]).add_(by)
+                begin = i
 
     @staticmethod
     def _not_captured():
@@ -96,12 +136,11 @@ class AdamW(torch.optim.Optimizer):
         s = self.state[p]
         if not s:
             self._not_captured()
-            self._places.pop(p, None)
             if group["states"] == "8bit":
                 s.update(zip(("m", "v", "exps"), ops.gq_adamw_state(p.numel(), p.device)))
             else:
                 s.update((k, torch.zeros(p.shape, dtype=torch.float32, device=p.device)) for k in ("m", "v"))
-        return ops.Adam8(s["m"], s["v"], s["exps"]) if "exps" in s else (s["m"], s["v"])
+        return s
 
     def _norm(self, grads):
         """Over gradients of either type."""
@@ -116,37 +155,51 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         calls, grads = [], []
-        for group in self.param_groups:
-            lists = {}
-            for p in group["params"]:
-                if p.grad is None:
+        for index, group in enumerate(self.param_groups):
+            some, lists = [], {}
+            for k, p in enumerate(group["params"], 1):
+                g = p.grad
+                if g is None:
                     continue
-                if p.grad.is_sparse:
+                if g.is_sparse:
                     raise RuntimeError("sparse gradients are not supported")
-                g = p.grad.contiguous()
+                g = g.contiguous()
+                s = self._state(p, group)
                 grads.append(g)
-                state = self._state(p, group)
-                # a call's tensors are of one type, and their states of one kind
-                lists.setdefault((p.dtype, g.dtype, len(state)), []).append((p, g, state))
+                some.append((k, p, g, s))
+            if not some:
+                continue
+            kept = self._counts(index, group)
+            steps = None if self.capturable else kept.counts.tolist()
+            for entry in some:
+                k, p, g, s = entry
+                # a call's tensors are of one type, their states of one kind, and the host counts for all of them
+                kind = p.dtype, g.dtype, "exps" in s, steps and steps[k] + 1
+                lists.setdefault(kind, []).append(entry)
             # (parameters that are new get their numbers call by call, so that those of a call follow one another)
-            lists = [sorted(((self._place(p), p, g, s) for p, g, s in entries), key=lambda entry: entry[0])
-                     for entries in lists.values()]
-            if lists:
-                calls.append((group, lists))
+            for entries in lists.values():
+                for k, _, _, s in entries:
+                    if kept.places[k] is None:
+                        kept.places[k] = self._place(s)
+                entries.sort(key=lambda entry: kept.places[entry[0]])
+            calls.append((group, kept, lists))
         if not calls:
             return loss
         norm = None if self.max_norm is None else self._norm(grads)
-        for group, lists in calls:
-            if self.capturable:
-                self._number(group, grads[0].device).add_(1)
-            else:
+        for group, kept, lists in calls:
+            own = [0]
+            for (_, _, eight, step), entries in lists.items():
+                at, params, gradients, states = zip(*entries)
+                self._add(kept.counts, sorted((*own, *at)), 1)
+                own = []
+                ops.gq_adamw_step_places(
+                    params, gradients,
+                    [(s["m"], s["v"], s["exps"]) if eight else (s["m"], s["v"]) for s in states],
+                    step or kept.counts, [kept.places[k] for k in at], lr=group["lr"], betas=group["betas"],
+                    eps=group["eps"], weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
+                    seed=self.key if self.random else None, step_places=None if step else at)
+            if not self.capturable:
                 group["step"] = int(group["step"]) + 1
-            for entries in lists:
-                places, params, gradients, states = map(list, zip(*entries))
-                ops.gq_adamw_step_places(params, gradients, states, group["step"], places, lr=group["lr"],
-                                         betas=group["betas"], eps=group["eps"],
-                                         weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
-                                         seed=self.key if self.random else None)
         return loss
 
     def load_state_dict(self, state_dict) -> None:
@@ -157,6 +210,6 @@ class AdamW(torch.optim.Optimizer):
         new = [p for group in self.param_groups for p in group["params"]]
         for i, p in zip(old, new):
             if i in state_dict["state"]:
-                self.state[p] = {k: v.detach().to("cpu" if k == "place" else p.device, copy=True)
+                self.state[p] = {k: v.detach().to("cpu" if k in ("place", "step") else p.device, copy=True)
                                  for k, v in state_dict["state"][i].items()}
         self._forget()

@@ -42,6 +42,7 @@ struct Slot {
     int64_t n;
     uint32_t first;     // block of the launch
     uint32_t row;       // the first of the tensor's three rows of random words
+    uint32_t at;        // of the tensor's number of steps, where the device counts them
     uint8_t wp, wg, wm, wv;  // widest access that each takes: 32 or 16 bytes, else element by element
 };
 template <int N> struct Table {
@@ -62,7 +63,7 @@ template <int N> struct Table {
 struct Step {
     float beta1, rest1, beta2, rest2, keep, size, fix, eps;  // keep = 1 - lr decay; size, fix: host's step
     float lr, log1, log2;        // for a step that the device counts
-    const int64_t* step;         // nullable
+    const int64_t* step;         // nullable: the device counts, per tensor where slots say so
     const float* norm;           // nullable
     float max_norm;              // negative: no limit
     int rounds;                  // of a block
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreadsA)
     }
     uint32_t step_lo = a.rng.step_lo, step_hi = a.rng.step_hi;
     if (a.step) {
-        const int64_t n = *a.step;
+        const int64_t n = a.step[s.at];
         step_lo = static_cast<uint32_t>(n);
         step_hi = static_cast<uint32_t>(n >> 32);
         const float f = static_cast<float>(n);
@@ -543,11 +544,13 @@ uint8_t wide(const void* p) { return mult(p, 32) ? 32 : mult(p, 16) ? 16 : 0; }
 
 template <typename P, typename G, bool EIGHT, bool RANDOM>
 gq_status adamw(int64_t count, void* const* params, const void* const* grads, void* const* m, void* const* v,
-                uint8_t* const* exps, const int64_t* numel, int64_t first, const int64_t* places, Step a, cudaStream_t st) {
+                uint8_t* const* exps, const int64_t* numel, int64_t first, const int64_t* places,
+                const int64_t* step_places, Step a, cudaStream_t st) {
     auto fill = [&](Slot& s, int64_t i) {
         s.p = params[i]; s.g = grads[i]; s.m = m[i]; s.v = v[i];
         s.e = EIGHT ? exps[i] : nullptr;
         s.row = static_cast<uint32_t>(3 * (first + (places ? places[i] : i)));
+        s.at = step_places ? static_cast<uint32_t>(step_places[i]) : 0u;
         s.wp = wide(s.p); s.wg = wide(s.g); s.wm = wide(s.m); s.wv = wide(s.v);
     };
     a.rounds = rounds_for(count, numel, EIGHT ? 16 : 4);
@@ -606,14 +609,15 @@ gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, con
                         int rounding, uint64_t seed, int64_t first, void *stream) {
     return gq_adamw_step_places(count, params, param_dtype, grads, grad_dtype, m, v, exps, numel, step, step_dev, lr,
                                 beta1, beta2, eps, weight_decay, norm_dev, max_norm, rounding, seed, first, nullptr,
-                                stream);
+                                nullptr, stream);
 }
 
 gq_status gq_adamw_step_places(int64_t count, void *const *params, int param_dtype, const void *const *grads,
                                int grad_dtype, void *const *m, void *const *v, uint8_t *const *exps,
                                const int64_t *numel, int64_t step, const int64_t *step_dev, double lr, double beta1,
                                double beta2, double eps, double weight_decay, const float *norm_dev, double max_norm,
-                               int rounding, uint64_t seed, int64_t first, const int64_t *places, void *stream) {
+                               int rounding, uint64_t seed, int64_t first, const int64_t *places,
+                               const int64_t *step_places, void *stream) {
     if (!in_type(param_dtype) || !in_type(grad_dtype) || !sizes_ok(count, numel)) return GQ_ERR_INVALID;
     if (count > 0 && (!params || !grads || !m || !v)) return GQ_ERR_INVALID;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(lr) ||
@@ -623,6 +627,9 @@ gq_status gq_adamw_step_places(int64_t count, void *const *params, int param_dty
         return GQ_ERR_INVALID;
     for (int64_t i = 0; places && i < count; ++i)
         if (places[i] < (i > 0 ? places[i - 1] + 1 : 0) || places[i] >= (int64_t(1) << 30) - first) return GQ_ERR_INVALID;
+    if (step_places && !step_dev) return GQ_ERR_INVALID;
+    for (int64_t i = 0; step_places && i < count; ++i)
+        if (step_places[i] < 0 || step_places[i] >= int64_t(1) << 31) return GQ_ERR_INVALID;
     for (int64_t i = 0; i < count; ++i) {
         if (numel[i] == 0) continue;
         if (!params[i] || !grads[i] || !m[i] || !v[i] || (exps && !exps[i])) return GQ_ERR_INVALID;
@@ -649,7 +656,7 @@ gq_status gq_adamw_step_places(int64_t count, void *const *params, int param_dty
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool random = rounding == GQ_ACT_RANDOM;
 #define GQA_ADAMW(P, G, EIGHT, RANDOM) \
-    adamw<P, G, EIGHT, RANDOM>(count, params, grads, m, v, exps, numel, first, places, a, st)
+    adamw<P, G, EIGHT, RANDOM>(count, params, grads, m, v, exps, numel, first, places, step_places, a, st)
 #define GQA_STATE(P, G)                                                                     \
     (exps ? random ? GQA_ADAMW(P, G, true, true) : GQA_ADAMW(P, G, true, false)              \
           : random && sizeof(P) == 2 ? GQA_ADAMW(P, G, false, (sizeof(P) == 2)) : GQA_ADAMW(P, G, false, false))

@@ -753,9 +753,9 @@ PyObject* tensors_norm(PyObject* const* a, Py_ssize_t n) {
 }
 
 // (params, grads, states, step, lr, beta1, beta2, eps, weight_decay, norm or None, max_norm or None, seed or
-// None, first, places or None) -> None
+// None, first, places or None, step's places or None) -> None
 PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
-    count(n, 14);
+    count(n, 15);
     const Items params(a[0], "params"), grads(a[1], "grads"), states(a[2], "states");
     if (grads.n != params.n || states.n != params.n)
         refuse(PyExc_ValueError, "%zd parameters, %zd gradients and %zd states", params.n, grads.n, states.n);
@@ -789,12 +789,14 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
     if (std::adjacent_find(once.begin(), once.end()) != once.end())
         refuse(PyExc_ValueError, "a parameter or a state is there twice");
     const int64_t* counter = nullptr;
-    int64_t step = 1;
+    int64_t step = 1, counters = 0;
     if (THPVariable_Check(a[3])) {
         const at::Tensor& t = THPVariable_Unpack(a[3]);
-        if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != at::kLong || t.numel() != 1)
+        if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != at::kLong || !t.is_contiguous() ||
+            (t.numel() != 1 && a[14] == Py_None))
             refuse(PyExc_ValueError, "step must be a number, or one int64 number on cuda:%d", index);
         counter = static_cast<const int64_t*>(t.data_ptr());
+        counters = t.numel();
     } else {
         step = signed64(a[3]);
         if (step < 1) refuse(PyExc_ValueError, "step must be at least 1");
@@ -826,11 +828,23 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
             places.push_back(k);
         }
     }
+    std::vector<int64_t> step_places;
+    if (a[14] != Py_None) {
+        const Items list(a[14], "step_places");
+        if (list.n != params.n) refuse(PyExc_ValueError, "%zd parameters and %zd places of steps", params.n, list.n);
+        step_places.reserve(list.n);
+        for (Py_ssize_t i = 0; i < list.n; ++i) {
+            const int64_t k = signed64(list[i]);
+            if (k < 0 || k >= counters) refuse(PyExc_ValueError, "step_places must be places in a tensor of steps");
+            step_places.push_back(k);
+        }
+    }
     const Place at(index);
     check(api.adamw_step_places(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(), eight ? e.data() : nullptr,
                          numel.data(), step, counter, lr, beta1, beta2, eps, decay, norm, most,
                          a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first,
-                         places.empty() ? nullptr : places.data(), at.stream),
+                         places.empty() ? nullptr : places.data(),
+                         step_places.empty() ? nullptr : step_places.data(), at.stream),
           "gq_adamw_step");
     for (Py_ssize_t i = 0; i < params.n; ++i) {
         changed(THPVariable_Unpack(params[i]));

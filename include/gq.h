@@ -662,15 +662,18 @@ gq_status gq_adamw_step(int64_t count, void *const *params, int param_dtype, con
                         double beta2, double eps, double weight_decay, const float *norm_dev, double max_norm,
                         int rounding, uint64_t seed, int64_t first, void *stream);
 
-/* The same for a list that leaves out some of a program's tensors: places (HOST, nullable: 0, 1, ...) are
- * count numbers in ascending order, none twice, below 2^30 - first, and tensor i draws the words of rows
- * 3 (first + places[i]) + j, whichever others are in the list. */
+/* The same for a list that leaves out some of a program's tensors.  places (HOST, nullable: 0, 1, ...): count
+ * numbers in ascending order, none twice, below 2^30 - first; tensor i draws the words of rows
+ * 3 (first + places[i]) + j, whichever others are in the list.  step_places (HOST, nullable, with step_dev
+ * only): count numbers from 0 to 2^31 - 1; tensor i's t is step_dev[step_places[i]], so that tensors which
+ * have not made the same number of steps share a call. */
 gq_status gq_adamw_step_places(int64_t count, void *const *params, int param_dtype, const void *const *grads,
                                int grad_dtype, void *const *m, void *const *v, uint8_t *const *exps,
                                const int64_t *numel, int64_t step, const int64_t *step_dev, double lr,
                                double beta1, double beta2, double eps, double weight_decay,
                                const float *norm_dev, double max_norm, int rounding, uint64_t seed,
-                               int64_t first, const int64_t *places, void *stream);
+                               int64_t first, const int64_t *places, const int64_t *step_places,
+                               void *stream);
 
 /* The values of 8-bit states: first moments and roots of the second, each as out_dtype (GQ_F32 or GQ_BF16;
  * exact in both down to 2^-126). */

@@ -140,7 +140,7 @@ def test_places_refused_by_the_library():
 
     def step(places, first=0):
         return L.gq_adamw_step_places(2, t, 0, t, 0, t, t, None, n, 1, None, 1e-3, 0.9, 0.999, 1e-8, 0.1, None, -1.0, 0,
-                                      0, first, places, None)
+                                      0, first, places, None, None)
     top = (1 << 30) - 1
     for good, first in ((None, 0), (N(0, 1), 0), (N(5, top), 0), (N(0, top - 7), 7), (None, top - 1)):
         assert step(good, first) == 0
