@@ -190,14 +190,19 @@ class AdamW(torch.optim.Optimizer):
             own = [0]
             for (_, _, eight, step), entries in lists.items():
                 at, params, gradients, states = zip(*entries)
-                self._add(kept.counts, sorted((*own, *at)), 1)
+                counted = sorted((*own, *at))
+                self._add(kept.counts, counted, 1)
+                try:
+                    ops.gq_adamw_step_places(
+                        params, gradients,
+                        [(s["m"], s["v"], s["exps"]) if eight else (s["m"], s["v"]) for s in states],
+                        step or kept.counts, [kept.places[k] for k in at], lr=group["lr"], betas=group["betas"],
+                        eps=group["eps"], weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
+                        seed=self.key if self.random else None, step_places=None if step else at)
+                except Exception:  # refused: these have made no step
+                    self._add(kept.counts, counted, -1)
+                    raise
                 own = []
-                ops.gq_adamw_step_places(
-                    params, gradients,
-                    [(s["m"], s["v"], s["exps"]) if eight else (s["m"], s["v"]) for s in states],
-                    step or kept.counts, [kept.places[k] for k in at], lr=group["lr"], betas=group["betas"],
-                    eps=group["eps"], weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
-                    seed=self.key if self.random else None, step_places=None if step else at)
             if not self.capturable:
                 group["step"] = int(group["step"]) + 1
         return loss
