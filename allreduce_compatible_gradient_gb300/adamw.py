@@ -33,9 +33,10 @@ class AdamW(torch.optim.Optimizer):
     states: "8bit" or "f32".  max_norm: gradients are clipped to this norm over all of them, and a step whose
     gradients hold a NaN or an infinity changes nothing (it still counts).  capturable: the numbers of steps
     are kept on the device, so that step() can be captured into a graph and replayed (the states have to be
-    there: make a step, or call make_states(), before).  A captured step keeps the learning rate and the other
-    settings of its capture, and works on the states that were there: capture again after changing a setting or
-    load_state_dict().  Parameters are float32 or bfloat16; those without a gradient are passed over."""
+    there: make a step, or call make_states(), before); without it a capture is refused.  A captured step keeps
+    the learning rate and the other settings of its capture, and works on the states that were there: capture
+    again after changing a setting or load_state_dict().  Parameters are float32 or bfloat16; those without a
+    gradient are passed over."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="8bit",
                  max_norm=None, random=True, seed=0, capturable=False):
@@ -127,9 +128,12 @@ class AdamW(torch.optim.Optimizer):
                 begin = i
 
     @staticmethod
-    def _not_captured():
+    def _captured():
+        return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+
+    def _not_captured(self):
         # a graph would make them again, as zeros, at every replay
-        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        if self._captured():
             raise RuntimeError("states are made before a step is captured: make a step, or call make_states()")
 
     def _state(self, p, group):
@@ -154,6 +158,8 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if not self.capturable and self._captured():
+            raise RuntimeError("a captured step would repeat its number at every replay: it needs capturable=True")
         calls, grads = [], []
         for index, group in enumerate(self.param_groups):
             some, lists = [], {}
