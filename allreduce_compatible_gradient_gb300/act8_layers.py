@@ -132,8 +132,8 @@ class MlpBlock8(nn.Module):
     def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
                  seed: int | None = None, device=None, rank: int | None = None, products: str = "bf16"):
         super().__init__()
-        if products not in ("bf16", "e4m3"):
-            raise ValueError("products must be 'bf16' or 'e4m3'")
+        self.products = products
+        self._e4m3()
         self.norm_weight = nn.Parameter(torch.ones(width, device=device))
         self.norm_bias = nn.Parameter(torch.zeros(width, device=device))
         self.w1 = nn.Parameter(torch.randn(hidden, width, device=device) * width ** -0.5)
@@ -141,13 +141,18 @@ class MlpBlock8(nn.Module):
         self.w2 = nn.Parameter(torch.randn(width, hidden, device=device) * hidden ** -0.5)
         self.b2 = nn.Parameter(torch.zeros(width, device=device))
         self.approximate, self.eps, self.seed, self.rank, self.step = approximate, eps, seed, rank, 0
-        self.products = products
         self._number = next(_numbers)
 
     def __setstate__(self, state):  # a copy, or one read back from a file
         super().__setstate__(state)
         self.__dict__.setdefault("products", "bf16")  # of a file from before it
         self._number = next(_numbers)
+
+    def _e4m3(self):
+        """Whether products are in 8-bit floating point."""
+        if self.products not in ("bf16", "e4m3"):
+            raise ValueError("products must be 'bf16' or 'e4m3'")
+        return self.products == "e4m3"
 
     def words(self, layer: int):
         """(seed, step) of the random words of a layer: 0 the layer norm's checkpoint, 1 GELU's."""
@@ -167,7 +172,7 @@ class MlpBlock8(nn.Module):
 
     def forward(self, x):
         record = torch.is_grad_enabled()  # not seen within a Function's forward pass
-        e4m3 = self.products == "e4m3"
+        e4m3 = self._e4m3()
         u = _NormLinear.apply(x, self.norm_weight, self.norm_bias, self.w1, self.b1, self.eps, *self.words(0),
                               record, e4m3)
         return x + _GeluLinear.apply(u, self.w2, self.b2, self.approximate, *self.words(1), record, e4m3)
