@@ -428,7 +428,8 @@ constexpr int kNormBlocks = 1216;  // partial sums per launch: at most
 
 // Sums of squares of the chunks blockIdx.x, blockIdx.x + gridDim.x, ...: fp32 over a thread's elements of a
 // chunk (64 at most) and over a warp, with what chunks' sums lose carried along; fp64 over warps and blocks
-// (over threads, its few units took 3 us of a pass).
+// (over threads, its few units took 3 us of a pass).  A block whose sums leave fp32's range reads its chunks once
+// more and adds in fp64 from the first square on: the norm is no number only where a square is none.
 template <typename G, int N>
 __global__ void __launch_bounds__(256)
     squares_kernel(const __grid_constant__ Table<N> t, uint32_t chunks, int rounds, double* partial) {
@@ -462,12 +463,42 @@ __global__ void __launch_bounds__(256)
         carry = (all - sum) - more;
         sum = all;
     }
-    // an infinite or overflowing sum leaves a NaN behind: its norm is not finite either way
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     __shared__ float warps[8];
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
-    __syncthreads();
+    // (an infinity or a NaN among the gradients, or sums above 3.4e38, which leave an infinity or a NaN behind)
+    if (__syncthreads_or(!(sum < INFINITY))) {
+        double wide = 0.0;
+        for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+            const Slot& s = t.s[t.of(c)];
+            int64_t i = static_cast<int64_t>(c - s.first) * (rounds * kRound) + threadIdx.x * 8;
+#pragma unroll 1
+            for (int k = 0; k < rounds && i < s.n; ++k, i += kRound) {
+                F2 g[4];
+                pairs(raw8<G>(s.g, i, s.n - i, s.wg), g);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x, y;
+                    split(mul2(g[q], g[q]), x, y);
+                    wide += static_cast<double>(x);
+                    wide += static_cast<double>(y);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) wide += __shfl_xor_sync(kFull, wide, o);
+        __shared__ double wides[8];
+        if ((threadIdx.x & 31) == 0) wides[threadIdx.x >> 5] = wide;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double all = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) all += wides[i];
+            partial[blockIdx.x] = all;
+        }
+        return;
+    }
     if (threadIdx.x == 0) {
         double all = 0.0;
 #pragma unroll

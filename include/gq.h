@@ -623,8 +623,12 @@ gq_status gq_fp8_linear_dgrad(const void *dy, int dtype, int64_t lddy, uint8_t *
  * Addresses are arguments of the kernels: nothing is copied to the device, and a captured call keeps
  * its own.
  *
- * gq_tensors_norm: *norm_dev = the square root of the sum of all squares (fp32 over 64 elements, fp64
- * over those, in a fixed order; magnitudes above 1.8e19 make it infinite).  dtype GQ_F32 or GQ_BF16.
+ * gq_tensors_norm: *norm_dev = the square root of the sum of all squares, in a fixed order: squares in fp32, their
+ * sums in fp32 over 64 elements, over a thread's such sums (with what they lose carried along) and over 32 threads,
+ * in fp64 over those, and in fp64 altogether where fp32's range does not do.  It is infinite or a NaN where a
+ * magnitude is above 1.8e19 (whose square is no fp32 number) or not finite, and where the root itself is above
+ * fp32's range.  Magnitudes below 1.1e-19 lose digits of their squares, and those below 2.6e-23 count as 0.
+ * dtype GQ_F32 or GQ_BF16.
  * ws: gq_tensors_norm_workspace_bytes(count) bytes, 16-byte aligned, contents irrelevant.
  */
 size_t gq_tensors_norm_workspace_bytes(int64_t count);
