@@ -148,9 +148,11 @@ class AdamW(torch.optim.Optimizer):
 
     def _norm(self, grads):
         """Over gradients of either type."""
-        norms = [ops.gq_tensors_norm(v) for v in ([g for g in grads if g.dtype == t]
-                                                  for t in (torch.float32, torch.bfloat16)) if v]
-        return norms[0] if len(norms) == 1 else torch.stack(norms).norm(dim=0)
+        kinds = {}
+        for g in grads:
+            kinds.setdefault(g.dtype, []).append(g)
+        first, *others = [ops.gq_tensors_norm(v) for v in kinds.values()]
+        return torch.hypot(first, *others) if others else first
 
     @torch.no_grad()
     def step(self, closure=None):
