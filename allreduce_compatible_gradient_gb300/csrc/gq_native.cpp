@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -734,21 +735,20 @@ PyObject* tensors_norm(PyObject* const* a, Py_ssize_t n) {
         numel[i] = t.numel();
     }
     const Place at(index);
-    // without a workspace of the caller's one lies behind the norm, in its storage (10 KB for 256 tensors; an
-    // allocation of its own took 1.6 of a call's 6 us)
-    constexpr int64_t kHead = 4;  // floats: the workspace is 16-byte aligned
-    const int64_t need = a[1] == Py_None ? static_cast<int64_t>(api.tensors_norm_workspace_bytes(list.n)) : 0;
-    const at::Tensor norm = empty({kHead + need / 4}, at::kFloat, index);
+    // (a norm that is kept holds no more than its four bytes; the workspace goes back to the allocator, in the
+    // stream's order, without having been a tensor)
+    const at::Tensor norm = empty({1}, at::kFloat, index);
     float* const out = static_cast<float*>(norm.data_ptr());
     if (a[1] == Py_None) {
-        check(api.tensors_norm(list.n, p.data(), numel.data(), code, out, out + kHead, need, at.stream),
+        const size_t need = api.tensors_norm_workspace_bytes(list.n);
+        const c10::DataPtr own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+        check(api.tensors_norm(list.n, p.data(), numel.data(), code, out, own.get(), need, at.stream),
               "gq_tensors_norm");
     } else {
         const Workspace ws(a[1], 0, index);
         check(api.tensors_norm(list.n, p.data(), numel.data(), code, out, ws.p, ws.bytes, at.stream),
               "gq_tensors_norm");
     }
-    norm.unsafeGetTensorImpl()->set_sizes_contiguous({1});
     return wrap(norm);
 }
 
