@@ -260,6 +260,11 @@ struct Workspace {
     }
 };
 
+// Autograd's count of in-place changes: a backward pass that saved the old values refuses the new ones.
+void changed(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // ---- the entry points: positional arguments, all of them given ---------------------------------
 
 void count(Py_ssize_t have, Py_ssize_t want) {
@@ -306,6 +311,7 @@ PyObject* act_dequantize(PyObject* const* a, Py_ssize_t n) {
                static_cast<long long>(s.cols), s.index);
     check(api.act_dequantize(s.codes, s.exps, s.rows, s.cols, m.p, m.code, m.ld, at.stream),
           "gq_act_dequantize");
+    if (a[4] != Py_None) changed(out);
     return wrap(out);
 }
 
@@ -548,6 +554,7 @@ PyObject* fp8_dequantize(PyObject* const* a, Py_ssize_t n) {
         refuse(PyExc_ValueError, "out must hold %lld x %lld on cuda:%d", static_cast<long long>(s.rows),
                static_cast<long long>(s.cols), s.index);
     check(api.fp8_dequantize(s.codes, s.exps, s.rows, s.cols, m.p, m.code, m.ld, at.stream), "gq_fp8_dequantize");
+    if (a[7] != Py_None) changed(out);
     return wrap(out);
 }
 
@@ -659,10 +666,6 @@ void same_type(int* code, const at::Tensor& t, const char* what) {
     if (c != GQ_F32 && c != GQ_BF16) refuse(PyExc_TypeError, "%s must be float32 or bfloat16", what);
     if (*code >= 0 && *code != c) refuse(PyExc_TypeError, "%s must be of one type", what);
     *code = c;
-}
-// Autograd's count of in-place changes: a backward pass that saved the old values refuses the new ones.
-void changed(const at::Tensor& t) {
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 struct State {
