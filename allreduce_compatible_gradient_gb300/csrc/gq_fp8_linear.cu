@@ -21,9 +21,11 @@
 // L2 (their 16.8 MB would take 2.5 from memory), 384 tokens through 768 x 768 6.3 us: a launch's ends, an
 // operand's way, a chain of four steps or so, a join.
 //
-// The sums of the tensor cores: of normal numbers within 4.1e-8 of the result's norm at a depth of 1,024 (a
-// product of the same values in fp32 4.1e-8), 1.1e-7 at 4,096 (8.4e-8) and 4.9e-7 at 8,192 in one chain
-// (1.3e-7): 32 products are added at a time, half as many roundings as bf16 products have, so chains are not cut.
+// The sums of the tensor cores: 32 products are added at a time, and the sum is cut each time, so the error of a chain
+// grows with its length.  Of normal numbers, in one chain: 5.9e-8 of the result's norm at a depth of 1,024 (a
+// product of the same values in fp32 4.1e-8), 2.2e-7 at 4,096 (8.4e-8) and 5.0e-7 at 8,192 (1.3e-7); where a
+// cluster shares a sum (100 tokens, 1,280 outputs) 3.5e-8, 6.2e-8 and 8.1e-8.  Beside operands of 4 bits chains of the
+// large form are not shortened for it: a second accumulator does not fit.
 #include "gq_fp8.cuh"
 #include "gq_tc.cuh"
 

@@ -593,7 +593,10 @@ gq_status gq_fp8_dequantize(const uint8_t *codes, const uint8_t *exps, int64_t r
  * block_rows) in 8-bit floating point.  Where x is not null, X is made from it (as by gq_fp8_quantize), and
  * xcodes and xexps are room for it, whose contents afterwards are not to be relied on (null where
  * gq_fp8_linear_workspace_bytes is 0: such a call needs none).  The tensor cores
- * multiply codes and apply the scales; sums are fp32 and in a fixed order, rounded once.  A bounded wait that
+ * multiply codes and apply the scales; sums are fp32 and in a fixed order, rounded once at the end.  The tensor cores
+ * cut a sum with every 32 products that they add to it, so its error grows with the depth: of normal numbers,
+ * 5.9e-8 of the result's norm at a depth of 1,024 and 5.0e-7 at 8,192, in proportion beyond (a third to a sixth
+ * of it from 4,096 on where rows and outs are few and up to 8 blocks share a sum).  A bounded wait that
  * gives up (about a second; a broken kernel only) leaves NaN in the tiles concerned.  rows, outs and
  * cols < 2^30.
  */
