@@ -46,7 +46,7 @@ def gq_tensors_norm(tensors, ws=None, stream=None) -> torch.Tensor:
 
 def gq_adamw_step(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                   norm=None, max_norm=None, seed=None, first=0, stream=None) -> None:
-    """One AdamW step, in place, on lists of contiguous tensors.
+    """One AdamW step, in place, on lists of contiguous tensors, of which parameters and states share no memory.
 
     params and grads: float32 or bfloat16 (all of a list of one type); states: an Adam8 or a pair of float32
     tensors (first and second moment) for each, all of one kind.  step: the step's number from 1 on, or an

@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <memory>
+#include <utility>
 #include <vector>
 
 #include "gq.h"
@@ -668,12 +669,27 @@ void same_type(int* code, const at::Tensor& t, const char* what) {
     *code = c;
 }
 
+// Ranges of memory that a call writes, each element by a thread of its own: none twice.
+struct Apart {
+    std::vector<std::pair<uintptr_t, int64_t>> ranges;
+    explicit Apart(Py_ssize_t n) { ranges.reserve(n); }
+    void add(const void* p, int64_t bytes) {
+        if (bytes > 0) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), bytes);
+    }
+    void check(const char* what) {
+        std::sort(ranges.begin(), ranges.end());
+        for (size_t i = 1; i < ranges.size(); ++i)
+            if (ranges[i].first - ranges[i - 1].first < static_cast<uintptr_t>(ranges[i - 1].second))
+                refuse(PyExc_ValueError, "%s is there twice, or a part of it", what);
+    }
+};
+
 struct State {
     void *m, *v;
     uint8_t* e = nullptr;
 };
 // (m, v) fp32, or (m, v, exps) bytes of a tensor of n elements.
-State state(PyObject* o, int64_t n, int* index, bool eight, bool written) {
+State state(PyObject* o, int64_t n, int* index, bool eight) {
     if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != (eight ? 3 : 2))
         refuse(PyExc_TypeError, "states must be Adam8, or pairs of float32 tensors, all of one kind");
     const at::Tensor &m = part(PyTuple_GET_ITEM(o, 0), index, "states"),
@@ -689,7 +705,6 @@ State state(PyObject* o, int64_t n, int* index, bool eight, bool written) {
                    static_cast<long long>(n), static_cast<long long>(room), static_cast<long long>(room),
                    static_cast<long long>(room / 16));
         s.e = static_cast<uint8_t*>(e.data_ptr());
-        if (written) changed(e);
     } else {
         if (m.scalar_type() != at::kFloat || v.scalar_type() != at::kFloat)
             refuse(PyExc_TypeError, "states must be Adam8, or pairs of float32 tensors, all of one kind");
@@ -698,10 +713,6 @@ State state(PyObject* o, int64_t n, int* index, bool eight, bool written) {
     }
     s.m = m.data_ptr();
     s.v = v.data_ptr();
-    if (written) {
-        changed(m);
-        changed(v);
-    }
     return s;
 }
 bool in_8_bits(const Items& states) {
@@ -779,18 +790,20 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
                    static_cast<long long>(d.numel()), static_cast<long long>(numel[i]));
         p[i] = t.data_ptr();
         g[i] = d.data_ptr();
-        const State s = state(states[i], numel[i], &index, eight, false);
+        const State s = state(states[i], numel[i], &index, eight);
         m[i] = s.m;
         v[i] = s.v;
         if (eight) e[i] = s.e;
     }
-    std::vector<void*> once;
-    once.reserve(3 * params.n);
-    for (Py_ssize_t i = 0; i < params.n; ++i)
-        if (numel[i] > 0) once.insert(once.end(), {p[i], m[i], v[i]});
-    std::sort(once.begin(), once.end());
-    if (std::adjacent_find(once.begin(), once.end()) != once.end())
-        refuse(PyExc_ValueError, "a parameter or a state is there twice");
+    Apart written(4 * params.n);
+    for (Py_ssize_t i = 0; i < params.n; ++i) {
+        const int64_t room = eight ? (numel[i] + 31) / 32 * 32 : 4 * numel[i];
+        written.add(p[i], (pcode == GQ_F32 ? 4 : 2) * numel[i]);
+        written.add(m[i], room);
+        written.add(v[i], room);
+        if (eight) written.add(e[i], room / 16);
+    }
+    written.check("a parameter or a state");
     const int64_t* counter = nullptr;
     int64_t step = 1, counters = 0;
     if (THPVariable_Check(a[3])) {
@@ -851,7 +864,7 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
           "gq_adamw_step");
     for (Py_ssize_t i = 0; i < params.n; ++i) {
         changed(THPVariable_Unpack(params[i]));
-        state(states[i], numel[i], &index, eight, true);
+        for (Py_ssize_t k = 0; k < (eight ? 3 : 2); ++k) changed(THPVariable_Unpack(PyTuple_GET_ITEM(states[i], k)));
     }
     return Py_NewRef(Py_None);
 }
@@ -873,13 +886,17 @@ PyObject* adamw_values(PyObject* const* a, Py_ssize_t n) {
         same_type(&code, u, "out");
         numel[i] = t.numel();
         if (u.numel() != numel[i]) refuse(PyExc_ValueError, "the outputs of state %zd differ in size", i);
-        const State s = state(states[i], numel[i], &index, true, false);
+        const State s = state(states[i], numel[i], &index, true);
         m[i] = static_cast<const uint8_t*>(s.m);
         v[i] = static_cast<const uint8_t*>(s.v);
         e[i] = s.e;
         x[i] = t.data_ptr();
         r[i] = u.data_ptr();
     }
+    Apart written(2 * states.n);
+    for (Py_ssize_t i = 0; i < states.n; ++i)
+        for (void* q : {x[i], r[i]}) written.add(q, (code == GQ_F32 ? 4 : 2) * numel[i]);
+    written.check("an output");
     const Place at(index);
     check(api.adamw_values(states.n, m.data(), v.data(), e.data(), numel.data(), x.data(), r.data(), code, at.stream),
           "gq_adamw_values");
