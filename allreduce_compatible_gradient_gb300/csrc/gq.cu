@@ -180,9 +180,7 @@ int gq_fused_launches(int dtype, int64_t n, int64_t d, int with_codes) {
 gq_status gq_workspace_init(void* ws, size_t ws_bytes, void* stream) {
     if (!ws || !aligned16(ws) || ws_bytes < gq_workspace_bytes(1, 1))
         return GQ_ERR_WORKSPACE;
-    if (cudaMemsetAsync(ws, 0, gq_workspace_bytes(1, 1), static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return GQ_ERR_CUDA;
-    return GQ_OK;
+    return status_of(cudaMemsetAsync(ws, 0, gq_workspace_bytes(1, 1), static_cast<cudaStream_t>(stream)));
 }
 
 int gq_code_bits(int scheme, int s) {
@@ -378,21 +376,21 @@ gq_status gq_philox4x32_10(const uint32_t* ctr_key_dev, uint32_t* out_dev, int64
 gq_status gq_get_status(void* ws, void* stream) {
     if (!ws) return GQ_ERR_WORKSPACE;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(cs) != cudaSuccess) return GQ_ERR_CUDA;
+    gq_status st = status_of(cudaStreamSynchronize(cs));
     unsigned int v = 0;
     gq::WsHeader* hdr = static_cast<gq::WsHeader*>(ws);
-    if (cudaMemcpy(&v, &hdr->status, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess)
-        return GQ_ERR_CUDA;
+    if (st == GQ_OK) st = status_of(cudaMemcpy(&v, &hdr->status, sizeof v, cudaMemcpyDeviceToHost));
+    if (st != GQ_OK) return st;
     if (v != 0) {
         const unsigned int zero = 0;
-        if (cudaMemcpy(&hdr->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
-            return GQ_ERR_CUDA;
+        st = status_of(cudaMemcpy(&hdr->status, &zero, sizeof zero, cudaMemcpyHostToDevice));
         // a wait that gave up may have left a completion ticket or the grid barrier's arrival
         // counts short of a full set: start them again from zero
-        if (v == GQ_ERR_TIMEOUT &&
-            (cudaMemcpy(&hdr->ticket, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess ||
-             cudaMemcpy(&hdr->bar, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess))
-            return GQ_ERR_CUDA;
+        if (v == GQ_ERR_TIMEOUT) {
+            if (st == GQ_OK) st = status_of(cudaMemcpy(&hdr->ticket, &zero, sizeof zero, cudaMemcpyHostToDevice));
+            if (st == GQ_OK) st = status_of(cudaMemcpy(&hdr->bar, &zero, sizeof zero, cudaMemcpyHostToDevice));
+        }
+        if (st != GQ_OK) return st;
     }
     return static_cast<gq_status>(v);
 }
@@ -452,7 +450,7 @@ gq_status noalloc_scratch(unsigned char** out) {
     std::lock_guard<std::mutex> lock(mu);
     if (addr[dev] == nullptr) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr)
+        if (status_of(cudaGetSymbolAddress(&p, g_noalloc_scratch)) != GQ_OK || p == nullptr)
             return GQ_ERR_CUDA;
         addr[dev] = p;
     }
@@ -507,7 +505,7 @@ extern "C" gq_status gq_allreduce_mean_noalloc(const void* grads, int dtype, int
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // the array keeps the previous call's contents: the status word, the completion ticket and
     // the single launch's barrier word must start at zero
-    if (cudaMemsetAsync(ws, 0, gq::kHeaderBytes, cs) != cudaSuccess) return GQ_ERR_CUDA;
+    if ((st = status_of(cudaMemsetAsync(ws, 0, gq::kHeaderBytes, cs))) != GQ_OK) return st;
     const float* ws_norm = &reinterpret_cast<const gq::WsHeader*>(ws)->norm;
     gq::QuantArgs a = make_args(ws_norm, dtype, n, d, s, seed, step, scheme);
     a.compact = mode == gq::kL2L2 || mode == gq::kMaxL2;  // as gq_allreduce_mean chooses

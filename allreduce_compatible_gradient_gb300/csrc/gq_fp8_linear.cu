@@ -732,8 +732,7 @@ gq_status launch_small(const CUtensorMap& a_map, const CUtensorMap& b_map, const
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a, static_cast<int>(depth)) != cudaSuccess) return GQ_ERR_CUDA;
-    return gqh::launch_status();
+    return gqh::status_of(cudaLaunchKernelEx(&cfg, k, a_map, b_map, a, static_cast<int>(depth)));
 }
 
 template <bool A_OUTER>
@@ -759,8 +758,7 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k, a_map, b_map, a_exps, b_exps, y_map, a) != cudaSuccess) return GQ_ERR_CUDA;
-    return gqh::launch_status();
+    return gqh::status_of(cudaLaunchKernelEx(&cfg, k, a_map, b_map, a_exps, b_exps, y_map, a));
 }
 
 // The form that a call takes: bn tokens per tile and parts of the sums, Large::BN for the large form; fused: one

@@ -75,6 +75,14 @@ unsigned grid_for(K kernel, int64_t work, int64_t cap = INT32_MAX, int smem = 0)
     return static_cast<unsigned>(g);
 }
 
+// The status of a call of the runtime.  A refused call leaves its error behind, which the next launch_status(),
+// of some later call that is right, would take for its own.
+inline gq_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return GQ_OK;
+    cudaGetLastError();
+    return GQ_ERR_CUDA;
+}
+
 inline gq_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
 }

@@ -399,7 +399,7 @@ gq_status backward_any(const BackwardCall<T>& a, void* dw, void* db, int gdtype,
                                                   static_cast<float*>(dw), static_cast<float*>(db))
                              : cudaLaunchKernelEx(&cfg, sum_kernel<bf16>, partial, parts, cols,
                                                   static_cast<bf16*>(dw), static_cast<bf16*>(db));
-        if (e != cudaSuccess) return GQ_ERR_CUDA;
+        if (e != cudaSuccess) return gqh::status_of(e);
     }
     return gqh::launch_status();
 }
@@ -430,9 +430,9 @@ gq_status gq_layernorm_backward(const void *dy, int dtype, int64_t rows, int64_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (rows == 0) {  // sums over no rows
         const size_t n = static_cast<size_t>(cols) * elt_bytes(gdtype);
-        if (dweight && cudaMemsetAsync(dweight, 0, n, st) != cudaSuccess) return GQ_ERR_CUDA;
-        if (dbias && cudaMemsetAsync(dbias, 0, n, st) != cudaSuccess) return GQ_ERR_CUDA;
-        return GQ_OK;
+        gq_status r = dweight ? gqh::status_of(cudaMemsetAsync(dweight, 0, n, st)) : GQ_OK;
+        if (r == GQ_OK && dbias) r = gqh::status_of(cudaMemsetAsync(dbias, 0, n, st));
+        return r;
     }
     if (!rstd || !mult(rstd, 4)) return GQ_ERR_INVALID;
     // exactly one source of the normalised rows

@@ -25,7 +25,7 @@ gq_status launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t sme
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return status_of(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // ---- quantize (+ sum + dequantize) ----------------------------------------------------------
@@ -138,8 +138,7 @@ gq_status launch_resident(const T* x, const gq::QuantArgs& a, int64_t gpb, unsig
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, x, a, gpb, out, norm_user, ws) == cudaSuccess ? GQ_OK
-                                                                                     : GQ_ERR_CUDA;
+    return status_of(cudaLaunchKernelEx(&cfg, k, x, a, gpb, out, norm_user, ws));
 }
 
 // The fused call in one launch when the problem fits (aligned rows, no codes requested):

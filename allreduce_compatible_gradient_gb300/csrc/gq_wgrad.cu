@@ -892,7 +892,8 @@ gq_status launch_wgrad(const CUtensorMap& map, const WArgs& a, bool early, cudaS
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C::CG > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k, map, a) != cudaSuccess) return GQ_ERR_CUDA;
+    const gq_status r = gqh::status_of(cudaLaunchKernelEx(&cfg, k, map, a));
+    if (r != GQ_OK) return r;
     if (a.units > 0) {  // tiles that several shares work on
         const dim3 grid(static_cast<unsigned>(a.units / a.ksteps), C::kRows * C::BN / 8 / 256);
         join_kernel<C><<<grid, 256, 0, st>>>(a);
@@ -945,11 +946,9 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (rows == 0) {  // sums over no tokens
         const size_t elt = elt_bytes(out_dtype);
-        if (cudaMemset2DAsync(dw, lddw * elt, 0, cols * elt, outs, st) != cudaSuccess)
-            return GQ_ERR_CUDA;
-        if (dbias && cudaMemsetAsync(dbias, 0, outs * sizeof(float), st) != cudaSuccess)
-            return GQ_ERR_CUDA;
-        return GQ_OK;
+        gq_status r = gqh::status_of(cudaMemset2DAsync(dw, lddw * elt, 0, cols * elt, outs, st));
+        if (r == GQ_OK && dbias) r = gqh::status_of(cudaMemsetAsync(dbias, 0, outs * sizeof(float), st));
+        return r;
     }
     if (!saved_ok(codes, exps)) return GQ_ERR_INVALID;
     const WPlan p = wgrad_plan(dy, dtype, rows, outs, lddy, cols);
@@ -989,9 +988,9 @@ gq_status gq_linear_wgrad(const void *dy, int dtype, int64_t rows, int64_t outs,
             attr.val.programmaticStreamSerializationAllowed = 1;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            if (cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(part), p.bias_shares,
-                                   outs, db) != cudaSuccess)
-                return GQ_ERR_CUDA;
+            const gq_status r = gqh::status_of(cudaLaunchKernelEx(
+                &cfg, bias_sum_kernel, static_cast<const float*>(part), p.bias_shares, outs, db));
+            if (r != GQ_OK) return r;
         }
         if (p.pack) {
             src = out;
