@@ -62,7 +62,8 @@ class _NormLinear(torch.autograd.Function):
         y, _, rstd, act = ops.gq_layernorm_forward(_rows(x), norm_weight, norm_bias, eps, seed=seed, step=step,
                                                    checkpoint=record and any(ctx.needs_input_grad[:4]))
         out, w8 = _product(y, weight, bias, e4m3)
-        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data, w8)
+        ctx.save_for_backward(norm_weight, norm_bias, weight, rstd, act and act.data,
+                              w8 if any(ctx.needs_input_grad[:3]) else None)
         ctx.shape = x.shape
         return out.view(*x.shape[:-1], weight.shape[0])
 
@@ -91,7 +92,7 @@ class _GeluLinear(torch.autograd.Function):
         h, act = ops.gq_gelu_forward(_rows(u), approximate=approximate, seed=seed, step=step,
                                      checkpoint=record and any(ctx.needs_input_grad[:2]))
         out, w8 = _product(h, weight, bias, e4m3)
-        ctx.save_for_backward(weight, act and act.data, w8)
+        ctx.save_for_backward(weight, act and act.data, w8 if any(ctx.needs_input_grad[:2]) else None)
         ctx.approximate, ctx.shape = approximate, u.shape
         return out.view(*u.shape[:-1], weight.shape[0])
 
