@@ -9,6 +9,7 @@ for bit.  `seed` (below 2^31) tells the optimizers of one program apart, where i
 """
 from __future__ import annotations
 
+from array import array
 from typing import NamedTuple
 
 import torch
@@ -18,9 +19,11 @@ from . import _optimizer as ops
 
 class _Counts(NamedTuple):
     """The numbers of steps that a group and, behind its own, each of its parameters have made: one tensor, on the
-    device for captured steps, with its views, of which the states hold theirs; and the parameters' numbers."""
+    device for captured steps, else over `host`'s memory, with its views, of which the states hold theirs; and the
+    parameters' numbers."""
 
     counts: torch.Tensor
+    host: array | None
     own: torch.Tensor
     steps: list
     places: list
@@ -95,8 +98,10 @@ class AdamW(torch.optim.Optimizer):
                 or any(s and s.get("step", v) is not v for s, v in zip(states, kept.steps[1:]))):
             self._not_captured()
             numbers = [int(group["step"]), *(int(s["step"]) if s and "step" in s else 0 for s in states)]
-            counts = torch.tensor(numbers, dtype=torch.int64, device=device)
-            kept = self._kept[index] = _Counts(counts, counts[:1], list(counts), [None] * len(numbers))
+            host = None if self.capturable else array("q", numbers)
+            counts = (torch.tensor(numbers, dtype=torch.int64, device=device) if host is None
+                      else torch.frombuffer(host, dtype=torch.int64))
+            kept = self._kept[index] = _Counts(counts, host, counts[:1], list(counts), [None] * len(numbers))
             if self.capturable:
                 group["step"] = kept.own
             for s, v in zip(states, kept.steps[1:]):
@@ -119,17 +124,25 @@ class AdamW(torch.optim.Optimizer):
         return int(s["place"])
 
     @staticmethod
-    def _add(counts, at, by):
-        """counts[at] += by (at ascends), in as many launches as there are runs."""
+    def _add(kept, at, by):
+        """counts[at] += by, on the device in as many launches as there are runs."""
+        if kept.host is not None:
+            for k in at:
+                kept.host[k] += by
+            return
+        if len(at) == len(kept.steps):
+            kept.counts.add_(by)
+            return
+        at = sorted(at)
         begin = 0
         for i in range(1, len(at) + 1):
             if i == len(at) or at[i] != at[i - 1] + 1:
-                (counts if i - begin == len(counts) else counts[at[begin]:at[i - 1] + 1]).add_(by)
+                kept.counts[at[begin]:at[i - 1] + 1].add_(by)
                 begin = i
 
     @staticmethod
     def _captured():
-        return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+        return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
 
     def _not_captured(self):
         # a graph would make them again, as zeros, at every replay
@@ -164,8 +177,9 @@ class AdamW(torch.optim.Optimizer):
             raise RuntimeError("a captured step would repeat its number at every replay: it needs capturable=True")
         calls, grads = [], []
         for index, group in enumerate(self.param_groups):
-            some, lists = [], {}
-            for k, p in enumerate(group["params"], 1):
+            some, lists, params, kept = [], {}, group["params"], self._kept.get(index)
+            fits = kept is not None and len(kept.steps) == 1 + len(params)
+            for k, p in enumerate(params, 1):
                 g = p.grad
                 if g is None:
                     continue
@@ -173,33 +187,37 @@ class AdamW(torch.optim.Optimizer):
                     raise RuntimeError("sparse gradients are not supported")
                 g = g.contiguous()
                 s = self._state(p, group)
+                fits = fits and s.get("step") is kept.steps[k]
                 grads.append(g)
                 some.append((k, p, g, s))
             if not some:
                 continue
-            kept = self._counts(index, group)
-            steps = None if self.capturable else kept.counts.tolist()
+            if not fits or self.capturable and (group["step"] is not kept.own or kept.own.device != grads[-1].device):
+                kept = self._counts(index, group)
+            steps = kept.host
             for entry in some:
                 k, p, g, s = entry
                 # a call's tensors are of one type, their states of one kind, and the host counts for all of them
-                kind = p.dtype, g.dtype, "exps" in s, steps and steps[k] + 1
+                kind = p.dtype, g.dtype, "exps" in s, None if steps is None else steps[k] + 1
                 lists.setdefault(kind, []).append(entry)
             # (parameters that are new get their numbers call by call, so that those of a call follow one another)
             for entries in lists.values():
                 for k, _, _, s in entries:
                     if kept.places[k] is None:
                         kept.places[k] = self._place(s)
-                entries.sort(key=lambda entry: kept.places[entry[0]])
+                places = [kept.places[entry[0]] for entry in entries]
+                if places != sorted(places):
+                    entries.sort(key=lambda entry: kept.places[entry[0]])
             calls.append((group, kept, lists))
         if not calls:
             return loss
         norm = None if self.max_norm is None else self._norm(grads)
         for group, kept, lists in calls:
-            own = [0]
+            own = (0,)
             for (_, _, eight, step), entries in lists.items():
                 at, params, gradients, states = zip(*entries)
-                counted = sorted((*own, *at))
-                self._add(kept.counts, counted, 1)
+                counted = own + at
+                self._add(kept, counted, 1)
                 try:
                     ops.gq_adamw_step_places(
                         params, gradients,
@@ -208,9 +226,9 @@ class AdamW(torch.optim.Optimizer):
                         eps=group["eps"], weight_decay=group["weight_decay"], norm=norm, max_norm=self.max_norm,
                         seed=self.key if self.random else None, step_places=None if step else at)
                 except Exception:  # refused: these have made no step
-                    self._add(kept.counts, counted, -1)
+                    self._add(kept, counted, -1)
                     raise
-                own = []
+                own = ()
             if not self.capturable:
                 group["step"] = int(group["step"]) + 1
         return loss

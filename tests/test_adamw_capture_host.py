@@ -22,7 +22,7 @@ def test_numbers_of_the_host_are_not_captured(monkeypatch):
     p.grad = torch.ones(4)
     opt = AdamW([p])
     opt.step()
-    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
     with pytest.raises(RuntimeError, match="capturable"):
         opt.step()
