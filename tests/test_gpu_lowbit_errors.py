@@ -1,4 +1,8 @@
 """A launch that the driver refuses is an error of its call, and of no other."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 from gpu_common import gq_module
@@ -36,7 +40,7 @@ def calls(gq):
     return made
 
 
-def test_the_call_after_a_refused_launch():
+def refuse_and_go_on():
     """Launches into a capture that has ended early (a synchronisation inside it) are refused on the host: each by
     itself, and a right call behind it is right."""
     gq = gq_module()
@@ -60,3 +64,16 @@ def test_the_call_after_a_refused_launch():
                 wrong.append((name, other, str(e)))
     torch.cuda.synchronize()
     assert not wrong, wrong
+
+
+def test_the_call_after_a_refused_launch():
+    """In a process of its own: torch's random numbers stay in a capture that has not ended well."""
+    gq_module()
+    done = subprocess.run([sys.executable, os.path.abspath(__file__)], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "all right" in done.stdout, done.stdout + done.stderr
+
+
+if __name__ == "__main__":
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    refuse_and_go_on()
+    print("all right")
