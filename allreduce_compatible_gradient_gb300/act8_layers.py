@@ -128,7 +128,10 @@ class MlpBlock8(nn.Module):
     words; `seed` names them instead, for words that a later run can draw again, and then blocks of one
     model need different seeds.  A captured CUDA graph replays the words of its capture.
 
-    `products`: "bf16" for the library's products in the activations' type, "e4m3" for 8-bit floating point."""
+    `products`: "bf16" for the library's products in the activations' type, "e4m3" for 8-bit floating point, which takes
+    less time in large blocks, and in small ones where steps are not captured (forward and backward pass of 768 x
+    3,088 over 384 tokens 79 and 99 us in a graph, 843 and 600 call after call; 4,096 x 16,384 over 8,192 tokens
+    4.2 and 3.4 ms in a graph)."""
 
     def __init__(self, width: int, hidden: int, approximate: str = "none", eps: float = 1e-5,
                  seed: int | None = None, device=None, rank: int | None = None, products: str = "bf16"):

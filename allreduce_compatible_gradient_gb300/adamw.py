@@ -34,12 +34,13 @@ class AdamW(torch.optim.Optimizer):
     corrected by the number of its own steps, those in which it had a gradient.
 
     states: "8bit" or "f32".  max_norm: gradients are clipped to this norm over all of them, and a step whose
-    gradients hold a NaN or an infinity changes nothing (it still counts).  capturable: the numbers of steps
-    are kept on the device, so that step() can be captured into a graph and replayed (the states have to be
-    there: make a step, or call make_states(), before); without it a capture is refused.  A captured step keeps
-    the learning rate and the other settings of its capture, and works on the states that were there: capture
-    again after changing a setting or load_state_dict().  Parameters are float32 or bfloat16; those without a
-    gradient are passed over."""
+    gradients hold a NaN, an infinity or a magnitude above 1.8e19 changes nothing (it still counts).
+    capturable: the numbers of steps are kept on the device, so that step() can be captured into a graph and
+    replayed (the states have to be there: make a step, or call make_states(), before); without it a capture is
+    refused.  A captured step keeps the learning rate and the other settings of its capture, and works on the
+    states that were there: capture again after changing a setting or load_state_dict().  Parameters are float32
+    or bfloat16; those without a gradient are passed over.  A group's parameters lie on one GPU, with max_norm
+    those of all groups."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="8bit",
                  max_norm=None, random=True, seed=0, capturable=False):

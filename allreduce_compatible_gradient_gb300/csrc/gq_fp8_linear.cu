@@ -17,9 +17,9 @@
 //   warp 1   one thread copies exponents to TMEM and issues tcgen05.mma, accumulators in TMEM
 //   2 on     (4 or 8) the sums from TMEM to memory; in calls of few steps a block, and of up to 16 tokens, they also put x
 //            into 8 bits on its way to shared memory, so that the call is one launch
-// What bounds it: latency.  One token through 4,096 x 4,096 weights takes 6.6 us in a graph with the weights in the
-// L2 (their 16.8 MB would take 2.5 from memory), 384 tokens through 768 x 768 6.3 us: a launch's ends, an
-// operand's way, a chain of four steps or so, a join.
+// What bounds it: latency.  With bf16 tokens, in a graph, the weights in the L2: one token through 4,096 x 4,096
+// weights 6.6 to 8.0 us (their 16.8 MB would take 2.5 from memory), 384 tokens through 768 x 768 7.8 to 9.2; of
+// tokens in 8 bits already 7.5 and 6.3 to 7.4.  A launch's ends, an operand's way, a chain of four steps or so, a join.
 //
 // The sums of the tensor cores: 32 products are added at a time, and the sum is cut each time, so the error of a chain
 // grows with its length.  Of normal numbers, in one chain: 5.9e-8 of the result's norm at a depth of 1,024 (a
@@ -770,7 +770,8 @@ gq_status launch_large(const CUtensorMap& a_map, const CUtensorMap& b_map, LArgs
 // 5.7.  Fused or not, 4,096 x 4,096: 1 token 6.6 and 7.8, 16 tokens 7.8 and 8.4, 32 tokens 8.9 and 8.1; a step of
 // 64 or 128 tokens takes the warps 0.3 or 0.6 us more, and what is saved is a launch: 64 tokens x 1,024 x 1,024 5.3 for
 // 5.8 in one step a block, 384 x 768 x 768 7.8 for 7.4 in two, 200 x 2,048 x 1,024 9.9 for 7.9 in four, and 2.7 us
-// of the host in each.
+// of the host in each.  So up to 1.5 us of the GPU are given for the host's 2.7: a call is faster, its replay in a graph
+// up to 0.5 us slower (384 x 768 x 768; 128 x 1,024 x 4,096 8.1 for 7.6; 512 x 1,024 x 1,024 8.1 for 7.8).
 struct Choice {
     int bn, parts;
     bool fused;

@@ -632,7 +632,8 @@ gq_status gq_fp8_linear_dgrad(const void *dy, int dtype, int64_t lddy, uint8_t *
  * magnitude is above 1.8e19 (whose square is no fp32 number) or not finite, and where the root itself is above
  * fp32's range.  Magnitudes below 1.1e-19 lose digits of their squares, and those below 2.6e-23 count as 0.
  * dtype GQ_F32 or GQ_BF16.
- * ws: gq_tensors_norm_workspace_bytes(count) bytes, 16-byte aligned, contents irrelevant.
+ * ws: gq_tensors_norm_workspace_bytes(count) bytes, 16-byte aligned, contents irrelevant, used by no other
+ * call (or replay of a captured one) at the same time.
  */
 size_t gq_tensors_norm_workspace_bytes(int64_t count);
 gq_status gq_tensors_norm(int64_t count, const void *const *tensors, const int64_t *numel, int dtype,
