@@ -856,9 +856,9 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
         }
     }
     const Place at(index);
-    check(api.adamw_step_places(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(), eight ? e.data() : nullptr,
-                         numel.data(), step, counter, lr, beta1, beta2, eps, decay, norm, most,
-                         a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first,
+    check(api.adamw_step_places(params.n, p.data(), pcode, g.data(), gcode, m.data(), v.data(),
+                         eight ? e.data() : nullptr, numel.data(), step, counter, lr, beta1, beta2, eps, decay, norm,
+                         most, a[11] == Py_None ? GQ_ACT_NEAREST : GQ_ACT_RANDOM, seed, first,
                          places.empty() ? nullptr : places.data(),
                          step_places.empty() ? nullptr : step_places.data(), at.stream),
           "gq_adamw_step");

@@ -10,8 +10,8 @@ torch = pytest.importorskip("torch")
 @pytest.mark.parametrize("a,b", [(1e18, 1e18), (1e18, 1.0), (3.0, 4.0), (0.0, 2.0), (1e-18, 1e-18)])
 @pytest.mark.parametrize("dtypes", [(torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)])
 def test_norm_of_both_types(a, b, dtypes):
-    """Two norms joined: within 82 units (80 a norm, 2 of the join) of the root of the sum of their squares, also where those are no
-    fp32 numbers."""
+    """Two norms joined: within 82 units of fp32 (80 a norm, 2 of the join) of the root of the sum of their squares,
+    also where those are no fp32 numbers."""
     gq_module()
     from allreduce_compatible_gradient_gb300.adamw import AdamW
     params = [torch.nn.Parameter(torch.zeros(1024, device="cuda", dtype=t)) for t in dtypes]

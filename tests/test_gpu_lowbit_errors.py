@@ -1,4 +1,4 @@
-"""A launch that the driver refuses is an error of its call, and of no other."""
+"""A launch that CUDA refuses is an error of its call, and of no other."""
 import os
 import subprocess
 import sys
